@@ -7,7 +7,7 @@ router    logits -> the K experts of each token and their weights; with
 int8      rows of bf16 -> 8-bit rows with a scale each -> the product with
           8-bit weights that have a scale for each channel.  ``gate_up``: the
           experts' gate and up products with SwiGLU, on the tokens of each
-          expert (the permute's gather included).  ``down``: the experts'
+          expert (their copy into expert-major order included).  ``down``: the experts'
           down product on expert-major rows.  ``dense``: one matrix.
 few       the whole expert layer for T <= 64 tokens, weights in bf16 or in 8
           bits.
@@ -95,13 +95,15 @@ def _ids(g, T, K, E):
 
 
 def _routing(ids, E):
-    """Expert-major order of the slots and the experts' row offsets."""
+    """The slots in expert-major order, each slot's row there, and the experts' row offsets."""
     flat = ids.reshape(-1).long()
-    order = torch.sort(flat, stable=True).indices.to(torch.int32)
+    order = torch.sort(flat, stable=True).indices
+    row_map = torch.empty_like(order)
+    row_map[order] = torch.arange(order.numel(), device=DEV)
     counts = torch.bincount(flat, minlength=E)
     offsets = torch.zeros(E + 1, dtype=torch.int32, device=DEV)
     offsets[1:] = counts.cumsum(0).to(torch.int32)
-    return order, offsets, int(counts.max())
+    return order.to(torch.int32), row_map.to(torch.int32), offsets, int(counts.max())
 
 
 def prepare(case, seed):
@@ -121,7 +123,7 @@ def prepare(case, seed):
             s["offsets"], s["rows"] = None, T
             s["w"], s["cs"] = _eight_bit(g, (1, I, H))
             return s
-        s["order"], s["offsets"], s["rows"] = _routing(_ids(g, T, K, E), E)
+        s["order"], s["row_map"], s["offsets"], s["rows"] = _routing(_ids(g, T, K, E), E)
         if form == "gate_up":
             s["x"] = _normal(g, (T, H))
             s["wg"], s["gs"] = _eight_bit(g, (E, I, H))
@@ -163,7 +165,7 @@ def _run_own(s):
         return [lib.moe_layer_few_tokens(s["x"], s["ids"], s["probs"], s["wg"], s["wu"], s["wd"],
                                          scales=s["scales"], shared_x=s["shared"])]
     if c["form"] == "gate_up":
-        q, rs = lib.moe_quantize_rows(s["x"], sorted_indices=s["order"], K=c["K"])
+        q, rs = lib.moe_quantize_rows(s["x"], row_map=s["row_map"], K=c["K"])
         return [lib.moe_gate_up_swiglu_int8(q, rs, s["offsets"], s["wg"], s["gs"], s["wu"], s["us"])]
     q, rs = lib.moe_quantize_rows(s["x"])
     return [lib.moe_down_proj_int8(q, rs, s["offsets"], s["w"], s["cs"])]

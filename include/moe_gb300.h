@@ -13,6 +13,14 @@
  *   backward     moe_unpermute_grad, moe_expert_mlp_grad, moe_permute_grad
  *   indices      rank-major -> expert-major permute indices from per-(rank,
  *                expert) counts (moe_permute_indices)
+ *   router       the K experts of each token and their weights from the
+ *                router's logits, and its gradient (moe_router_topk,
+ *                moe_router_topk_grad)
+ *   8-bit        rows in 8-bit integers with a scale each
+ *                (moe_quantize_rows) and the grouped products with 8-bit
+ *                weights (moe_gate_up_swiglu_int8, moe_down_proj_int8)
+ *   few tokens   the whole layer for T <= 64 tokens in one launch
+ *                (moe_layer_few_tokens)
  *
  * Notation: T tokens, H hidden size, K experts per token (top-K), E routed
  * experts, I expert intermediate size, f = t*K + k the flat slot index.
@@ -73,6 +81,7 @@ extern "C" {
 /* ---- dtypes ------------------------------------------------------------ */
 #define MOE_F32 0
 #define MOE_BF16 1
+#define MOE_INT8 2 /* weights of moe_layer_few_tokens only */
 
 /* Human-readable name of a status code (static string, never NULL). */
 const char* moe_status_string(int status);
@@ -411,6 +420,120 @@ int moe_down_wgrad(const void* grad_expanded, const void* act, int dtype,
 int moe_gate_up_wgrad(const void* dgu, const void* permuted, int dtype,
                       const int32_t* expert_offsets, int N, int H, int I, int E, void* dW_gate,
                       void* dW_up, int32_t* dev_status, cudaStream_t stream);
+
+/* ---- router -------------------------------------------------------------
+ *
+ * The K experts of each token from its logits l = logits[t, :], and their
+ * weights:
+ *   expert_ids[t]  = the indices of the K largest logits in descending order
+ *                    of the logit, ties to the lowest index
+ *   MOE_SCORE_SOFTMAX  p_j = e^(l_j - m) / sum_i e^(l_i - m),  m = max l
+ *   MOE_SCORE_SIGMOID  p_j = 1 / (1 + e^(-l_j))
+ *   probs[t, k]    = scale * p_id(k),                    renormalize == 0
+ *                  = scale * p_id(k) / sum_k' p_id(k'),  renormalize != 0
+ * in fp32 whatever the logits' dtype (both scores grow with the logit, so
+ * the selection compares the logits themselves, without rounding).
+ *   -inf masks an expert: its weight is 0 (it is selected, lowest index
+ *   first, only when fewer than K logits are above -inf; a row of -inf alone
+ *   gets ids 0..K-1 and weights 0).  +inf counts as the largest finite
+ *   float.  A NaN counts as -inf and sets MOE_ERR_INVALID_ARG in dev_status.
+ * logits [T, E] MOE_F32 or MOE_BF16, expert_ids [T, K] int32, probs [T, K]
+ * float32; 1 <= K <= 16, K <= E <= 1024.
+ *
+ * moe_router_topk_grad: grad_logits [T, E] (the logits' dtype) from
+ * grad_probs [T, K] and the forward's logits and expert_ids.  The selection
+ * itself has no gradient.  Every element is written; masked logits get 0.
+ * With g_k = scale * grad_probs[k], q_k = probs[k] / scale and
+ * D = sum_k g_k q_k:
+ *   softmax, not renormalised   d_j = p_j ([j selected] g_j - D)
+ *   softmax, renormalised       d_j = [j selected] q_j (g_j - D)
+ *   sigmoid, not renormalised   d_j = [j selected] g_j p_j (1 - p_j)
+ *   sigmoid, renormalised       d_j = [j selected] q_j (g_j - D) (1 - p_j)
+ * An id outside [0, E) sets MOE_ERR_BAD_ID and takes no part. */
+#define MOE_SCORE_SOFTMAX 0
+#define MOE_SCORE_SIGMOID 1
+int moe_router_topk(const void* logits, int dtype, int T, int E, int K, int scoring,
+                    int renormalize, float scale, int32_t* expert_ids, float* probs,
+                    int32_t* dev_status, cudaStream_t stream);
+int moe_router_topk_grad(const float* grad_probs, const void* logits, int dtype,
+                         const int32_t* expert_ids, int T, int E, int K, int scoring,
+                         int renormalize, float scale, void* grad_logits, int32_t* dev_status,
+                         cudaStream_t stream);
+
+/* ---- 8-bit rows and products ----------------------------------------------
+ *
+ * moe_quantize_rows: each row in 8-bit integers with one float32 scale,
+ *   top = max_h |x[t, h]|,  scale = top / 127,
+ *   q[h] = round-to-nearest-even(127 x[t, h] / top)      in [-127, 127]
+ * (a row of zeros: q = 0, scale = 0; a row that holds a NaN or an infinity:
+ * scale = NaN, q = 0, so that every product with it is NaN).
+ *   row_map NULL      row t of x becomes row t of q and scale (N >= T rows)
+ *   row_map [T*K]     row t becomes the rows row_map[t*K + k], k < K: the row
+ *                     copy of moe_permute_rows with the rounding fused in.
+ *                     Entries outside [0, N) are skipped; rows that no entry
+ *                     names are not written.
+ * x [T, H] MOE_F32 or MOE_BF16, q [N, H] int8, scale [N]; H % 16 == 0.  For
+ * weights, call it on [E * rows, H]: the scale of a row is then the scale of
+ * an output channel.
+ *
+ * The products, for the rows of expert e (expert_offsets as above;
+ * expert_offsets NULL with E = 1: one matrix for all N rows):
+ *   y[i, n] = row_scale[i] * channel_scale[e, n] * sum_k x_q[i, k] W_q[e, n, k]
+ * moe_gate_up_swiglu_int8: act = silu(g) * u with g, u such products,
+ *   W_gate_q and W_up_q [E, I, H], gate_scale and up_scale [E, I],
+ *   permuted_q [N, H], act [N, I] bf16 (what moe_quantize_rows reads next).
+ * moe_down_proj_int8: W_down_q [E, H, I], down_scale [E, H], act_q [N, I],
+ *   expanded [N, H] MOE_BF16 or MOE_F32 (out_dtype).
+ * The integers are multiplied exactly and summed in 32 bits (fp32: exact
+ * while the partial sums stay under 2^24, else each addition rounds to 24
+ * bits); one rounding to the output's dtype.  H and I multiples of 16, at
+ * most 131072; rows >= expert_offsets[E] are not touched. */
+int moe_quantize_rows(const void* x, int dtype, const int32_t* row_map, int T, int H, int K, int N,
+                      int8_t* q, float* scale, cudaStream_t stream);
+int moe_gate_up_swiglu_int8(const int8_t* permuted_q, const float* row_scale,
+                            const int32_t* expert_offsets, int N, int H, int I, int E,
+                            const int8_t* W_gate_q, const float* gate_scale,
+                            const int8_t* W_up_q, const float* up_scale, void* act,
+                            int32_t* dev_status, cudaStream_t stream);
+int moe_down_proj_int8(const int8_t* act_q, const float* row_scale, const int32_t* expert_offsets,
+                       int N, int H, int I, int E, const int8_t* W_down_q,
+                       const float* down_scale, void* expanded, int out_dtype,
+                       int32_t* dev_status, cudaStream_t stream);
+
+/* ---- the whole layer for a few tokens --------------------------------------
+ *
+ *   act[t, k] = silu(W_gate[e] x_t) * (W_up[e] x_t),       e = expert_ids[t, k]
+ *   out[t]    = shared_x[t] + sum_k probs[t, k] W_down[e] act[t, k]
+ * for 0 <= T <= MOE_FEW_TOKENS tokens in bf16: what moe_permute, moe_expert_mlp
+ * and moe_combine give, without their buffers, reading each weight of an
+ * expert that some token chose once.
+ *   tokens, out     [T, H] bf16; shared_x [T, H] bf16 or NULL
+ *   weight_dtype    MOE_BF16: W_gate, W_up [E, I, H], W_down [E, H, I] bf16
+ *                   (the scale pointers are NULL); MOE_INT8: the same in int8
+ *                   with gate_scale, up_scale [E, I] and down_scale [E, H]
+ *                   float32 (moe_quantize_rows of the weights' rows).  The
+ *                   tokens stay in bf16 with 8-bit weights.
+ *   expert_ids      [T, K]; ids in [E, E + num_special) and slots whose
+ *                   active_mask byte is zero (mask_dims as in
+ *                   moe_permute_masked) add nothing.  An id outside
+ *                   [0, E + num_special) or repeated within a row sets
+ *                   MOE_ERR_BAD_ID and adds nothing.
+ *   workspace       moe_layer_few_tokens_workspace_size(T, K, H, I, E) bytes,
+ *                   16-byte aligned, needs no clearing; calls that can
+ *                   overlap on the GPU need one each
+ * A token without an active slot gets shared_x[t], or zeros.  H and I are
+ * multiples of 64.  Sums are fp32 in an order that depends on the sizes and
+ * the ids alone; act is rounded to bf16 once.  A token's result depends on
+ * its own row and its own experts' weights only. */
+#define MOE_FEW_TOKENS 64
+size_t moe_layer_few_tokens_workspace_size(int T, int K, int H, int I, int E);
+int moe_layer_few_tokens(const void* tokens, const int32_t* expert_ids, const float* probs, int T,
+                         int H, int K, int I, int E, int num_special, const uint8_t* active_mask,
+                         int mask_dims, int weight_dtype, const void* W_gate, const void* W_up,
+                         const void* W_down, const float* gate_scale, const float* up_scale,
+                         const float* down_scale, const void* shared_x, void* out,
+                         void* workspace, size_t workspace_bytes, int32_t* dev_status,
+                         cudaStream_t stream);
 
 #ifdef __cplusplus
 }

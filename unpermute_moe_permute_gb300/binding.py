@@ -32,6 +32,11 @@ MOE_ERR_BAD_ID = 7
 
 MOE_F32 = 0
 MOE_BF16 = 1
+MOE_INT8 = 2
+
+MOE_SCORE_SOFTMAX = 0
+MOE_SCORE_SIGMOID = 1
+MOE_FEW_TOKENS = 64
 
 _DTYPES = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16}
 
@@ -46,6 +51,7 @@ _lib = None
 
 _P = ctypes.c_void_p
 _I = ctypes.c_int
+_F = ctypes.c_float
 _SZ = ctypes.c_size_t
 
 _SIGNATURES = {
@@ -83,6 +89,14 @@ _SIGNATURES = {
     "moe_shared_expert_mlp": ([_P, _I, _I, _I, _P, _P, _P, _P, _P, _P, _P], _I),
     "moe_gate_up_swiglu_gather": ([_P, _I, _P, _I, _P, _I, _I, _I, _I, _P, _P, _P, _P, _P, _P], _I),
     "moe_gate_up_wgrad_gather": ([_P, _P, _I, _P, _I, _P, _I, _I, _I, _I, _P, _P, _P, _P], _I),
+    "moe_router_topk": ([_P, _I, _I, _I, _I, _I, _I, _F, _P, _P, _P, _P], _I),
+    "moe_router_topk_grad": ([_P, _P, _I, _P, _I, _I, _I, _I, _I, _F, _P, _P, _P], _I),
+    "moe_quantize_rows": ([_P, _I, _P, _I, _I, _I, _I, _P, _P, _P], _I),
+    "moe_gate_up_swiglu_int8": ([_P, _P, _P, _I, _I, _I, _I, _P, _P, _P, _P, _P, _P, _P], _I),
+    "moe_down_proj_int8": ([_P, _P, _P, _I, _I, _I, _I, _P, _P, _P, _I, _P, _P], _I),
+    "moe_layer_few_tokens_workspace_size": ([_I, _I, _I, _I, _I], _SZ),
+    "moe_layer_few_tokens": ([_P, _P, _P, _I, _I, _I, _I, _I, _I, _P, _I, _I, _P, _P, _P, _P, _P,
+                              _P, _P, _P, _P, _SZ, _P, _P], _I),
 }
 
 
@@ -532,3 +546,178 @@ def moe_permute_indices_window(counts, R: int, E_all: int, col_start: int, col_c
           _ptr(indices), capacity, _ptr(tokens_per_column), _ptr(total), _ptr(dev_status),
           _stream())
     return indices, tokens_per_column, total
+
+
+# ---------------------------------------------------------------- router
+
+_SCORING = {"softmax": MOE_SCORE_SOFTMAX, "sigmoid": MOE_SCORE_SIGMOID}
+
+
+def _scoring(name: str) -> int:
+    try:
+        return _SCORING[name]
+    except KeyError:
+        raise ValueError(f"scoring must be 'softmax' or 'sigmoid', got {name!r}") from None
+
+
+def _shape(t: Optional[torch.Tensor], shape: tuple, name: str):
+    if t is not None and tuple(t.shape) != shape:
+        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+
+
+def moe_router_topk(logits, K: int, *, scoring: str = "softmax", renormalize: bool = True,
+                    scale: float = 1.0, expert_ids=None, probs=None, dev_status=None):
+    """The K experts of each token and their weights from logits [T, E]
+    (float32 or bfloat16): (expert_ids [T, K] int32, probs [T, K] float32)."""
+    T, E = logits.shape
+    if expert_ids is None:
+        expert_ids = torch.empty((T, K), dtype=torch.int32, device=logits.device)
+    if probs is None:
+        probs = torch.empty((T, K), dtype=torch.float32, device=logits.device)
+    _check(expert_ids, torch.int32, "expert_ids")
+    _check(probs, torch.float32, "probs")
+    _shape(expert_ids, (T, K), "expert_ids")
+    _shape(probs, (T, K), "probs")
+    _call("moe_router_topk", _ptr(logits), _dtype(logits), T, E, K, _scoring(scoring),
+          int(renormalize), scale, _ptr(expert_ids), _ptr(probs), _ptr(dev_status), _stream())
+    return expert_ids, probs
+
+
+def moe_router_topk_grad(grad_probs, logits, expert_ids, *, scoring: str = "softmax",
+                         renormalize: bool = True, scale: float = 1.0, grad_logits=None,
+                         dev_status=None):
+    """grad_logits [T, E] (the logits' dtype) of moe_router_topk."""
+    T, E = logits.shape
+    K = expert_ids.shape[1]
+    if grad_logits is None:
+        grad_logits = torch.empty_like(logits)
+    _check(grad_probs, torch.float32, "grad_probs")
+    _check(expert_ids, torch.int32, "expert_ids")
+    _check(grad_logits, logits.dtype, "grad_logits")
+    _shape(grad_probs, (T, K), "grad_probs")
+    _shape(expert_ids, (T, K), "expert_ids")
+    _shape(grad_logits, (T, E), "grad_logits")
+    _call("moe_router_topk_grad", _ptr(grad_probs), _ptr(logits), _dtype(logits),
+          _ptr(expert_ids), T, E, K, _scoring(scoring), int(renormalize), scale,
+          _ptr(grad_logits), _ptr(dev_status), _stream())
+    return grad_logits
+
+
+# ---------------------------------------------------------------- 8-bit rows and products
+
+def moe_quantize_rows(x, *, row_map=None, K: int = 1, N: Optional[int] = None, q=None, scale=None):
+    """Rows of x [T, H] in int8 with a float32 scale each: (q [N, H], scale
+    [N]).  With row_map [T*K] (a PermuteResult's) row t goes to the rows
+    row_map[t*K + k], the expert-major copy of the permute."""
+    T, H = x.shape
+    if row_map is not None:
+        _check(row_map, torch.int32, "row_map")
+        if row_map.numel() != T * K:
+            raise ValueError(f"row_map must have T*K = {T * K} entries, got {row_map.numel()}")
+    if N is None:
+        N = T * K if row_map is not None else T
+    if q is None:
+        q = torch.empty((N, H), dtype=torch.int8, device=x.device)
+    if scale is None:
+        scale = torch.empty(N, dtype=torch.float32, device=x.device)
+    _check(q, torch.int8, "q")
+    _check(scale, torch.float32, "scale")
+    _shape(q, (N, H), "q")
+    _shape(scale, (N,), "scale")
+    _call("moe_quantize_rows", _ptr(x), _dtype(x), _ptr(row_map), T, H, K, N, _ptr(q),
+          _ptr(scale), _stream())
+    return q, scale
+
+
+def moe_gate_up_swiglu_int8(permuted_q, row_scale, expert_offsets, W_gate_q, gate_scale, W_up_q,
+                            up_scale, *, act=None, dev_status=None):
+    """act [N, I] bf16 = silu(g) * u, g and u the 8-bit products of the
+    expert-major rows permuted_q [N, H] (int8, row_scale [N])."""
+    N, H = permuted_q.shape
+    E, I, _ = W_gate_q.shape
+    if act is None:
+        act = torch.empty((N, I), dtype=torch.bfloat16, device=permuted_q.device)
+    for t, n in ((permuted_q, "permuted_q"), (W_gate_q, "W_gate_q"), (W_up_q, "W_up_q")):
+        _check(t, torch.int8, n)
+    for t, n in ((row_scale, "row_scale"), (gate_scale, "gate_scale"), (up_scale, "up_scale")):
+        _check(t, torch.float32, n)
+    _check(expert_offsets, torch.int32, "expert_offsets")
+    _check(act, torch.bfloat16, "act")
+    _shape(row_scale, (N,), "row_scale")
+    _shape(W_gate_q, (E, I, H), "W_gate_q")
+    _shape(W_up_q, (E, I, H), "W_up_q")
+    _shape(gate_scale, (E, I), "gate_scale")
+    _shape(up_scale, (E, I), "up_scale")
+    _shape(act, (N, I), "act")
+    _call("moe_gate_up_swiglu_int8", _ptr(permuted_q), _ptr(row_scale), _ptr(expert_offsets), N,
+          H, I, E, _ptr(W_gate_q), _ptr(gate_scale), _ptr(W_up_q), _ptr(up_scale), _ptr(act),
+          _ptr(dev_status), _stream())
+    return act
+
+
+def moe_down_proj_int8(act_q, row_scale, expert_offsets, W_down_q, down_scale, *, expanded=None,
+                       out_dtype=torch.bfloat16, dev_status=None):
+    """expanded [N, H] (bfloat16 or float32) = the 8-bit product of act_q
+    [N, I] (int8, row_scale [N]) with each expert's W_down_q [E, H, I].
+    expert_offsets None: one matrix (E = 1) for all rows."""
+    N, I = act_q.shape
+    E, H, _ = W_down_q.shape
+    if expanded is None:
+        expanded = torch.empty((N, H), dtype=out_dtype, device=act_q.device)
+    for t, n in ((act_q, "act_q"), (W_down_q, "W_down_q")):
+        _check(t, torch.int8, n)
+    for t, n in ((row_scale, "row_scale"), (down_scale, "down_scale")):
+        _check(t, torch.float32, n)
+    _check(expert_offsets, torch.int32, "expert_offsets")
+    _shape(row_scale, (N,), "row_scale")
+    _shape(W_down_q, (E, H, I), "W_down_q")
+    _shape(down_scale, (E, H), "down_scale")
+    _shape(expanded, (N, H), "expanded")
+    _call("moe_down_proj_int8", _ptr(act_q), _ptr(row_scale), _ptr(expert_offsets), N, H, I, E,
+          _ptr(W_down_q), _ptr(down_scale), _ptr(expanded), _dtype(expanded), _ptr(dev_status),
+          _stream())
+    return expanded
+
+
+# ---------------------------------------------------------------- the layer for a few tokens
+
+def moe_layer_few_tokens_workspace_size(T: int, K: int, H: int, I: int, E: int) -> int:
+    return int(load_library().moe_layer_few_tokens_workspace_size(T, K, H, I, E))
+
+
+def moe_layer_few_tokens(tokens, expert_ids, probs, W_gate, W_up, W_down, *, scales=None,
+                         num_special: int = 0, active_mask=None, shared_x=None, out=None,
+                         workspace=None, dev_status=None):
+    """The whole expert layer for T <= MOE_FEW_TOKENS tokens [T, H] (bf16):
+    out[t] = shared_x[t] + sum_k probs[t, k] expert_{ids[t, k]}(tokens[t]).
+    Weights in bf16, or in int8 with scales = (gate [E, I], up [E, I],
+    down [E, H]) float32."""
+    T, H = tokens.shape
+    K = expert_ids.shape[1]
+    E, I, _ = W_gate.shape
+    wdt = torch.bfloat16 if scales is None else torch.int8
+    gs, us, ds = scales if scales is not None else (None, None, None)
+    if out is None:
+        out = torch.empty((T, H), dtype=torch.bfloat16, device=tokens.device)
+    if workspace is None:
+        ws = moe_layer_few_tokens_workspace_size(T, K, H, I, E)
+        workspace = torch.empty(max(ws, 16), dtype=torch.uint8, device=tokens.device)
+    for t, dt, shape, n in ((tokens, torch.bfloat16, (T, H), "tokens"),
+                            (expert_ids, torch.int32, (T, K), "expert_ids"),
+                            (probs, torch.float32, (T, K), "probs"),
+                            (W_gate, wdt, (E, I, H), "W_gate"), (W_up, wdt, (E, I, H), "W_up"),
+                            (W_down, wdt, (E, H, I), "W_down"),
+                            (gs, torch.float32, (E, I), "gate scale"),
+                            (us, torch.float32, (E, I), "up scale"),
+                            (ds, torch.float32, (E, H), "down scale"),
+                            (shared_x, torch.bfloat16, (T, H), "shared_x"),
+                            (out, torch.bfloat16, (T, H), "out")):
+        _check(t, dt, n)
+        _shape(t, shape, n)
+    mask = _mask(active_mask, T, K) if active_mask is not None else None
+    _call("moe_layer_few_tokens", _ptr(tokens), _ptr(expert_ids), _ptr(probs), T, H, K, I, E,
+          num_special, _ptr(mask), mask.dim() if mask is not None else 0,
+          MOE_BF16 if scales is None else MOE_INT8, _ptr(W_gate), _ptr(W_up), _ptr(W_down),
+          _ptr(gs), _ptr(us), _ptr(ds), _ptr(shared_x), _ptr(out), _ptr(workspace),
+          workspace.numel() * workspace.element_size(), _ptr(dev_status), _stream())
+    return out

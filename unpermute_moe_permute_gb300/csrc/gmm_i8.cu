@@ -1,85 +1,382 @@
 // Grouped products of 8-bit rows and 8-bit expert weights with a scale for
-// each row and each channel, on the 4-way integer dot product (exact int32
-// sums).  Tiles of 64 x 64 outputs, 256 threads, 4 x 4 outputs per thread, a
-// 64-deep k slice staged in shared memory as 16 words.
+// each row and each channel, on tcgen05 tensor cores (sm_103a).
+//
+//   y[i, n] = rs[i] cs[e, n] sum_k q[i, k] w[e, n, k]
+//
+// sm_103a has no 8-bit integer MMA with tensor-memory accumulators, so both
+// operands are expanded on chip to fp16, which holds every byte exactly, and
+// multiplied by kind::f16 with fp32 sums (exact while they stay under 2^24).
+// DRAM and L2 see bytes only.  What bounds it is the tensor pipe at its fp16
+// rate when experts have rows enough, else the stream of weights; next to
+// either stands shared memory, which the expansion crosses twice, so:
+//
+//   * the weights are the A operand (M = channels): they go from the 8-bit
+//     tile through registers into tensor memory, never back to shared memory;
+//   * the rows are the B operand (N = rows), so a tile takes as many rows as
+//     an expert has, in steps of 16 up to 192: 25 rows cost 32 columns, not
+//     128 rows;
+//   * CTA pairs (cta_group::2): 256 channels per MMA, each CTA expands its
+//     own 128 channels and half of the rows.  Per 64-deep step a CTA moves
+//     14 KB (TMA) + 14 KB (read) + 12 KB (fp16 rows) + 12 KB (MMA reads) in
+//     the 384 cycles of its MMAs at 192 rows.
+//
+// Warps: 4 epilogue (one per tensor-memory lane quarter), 8 expand A (two
+// groups of 4, one per 64-byte half of the 128-byte stage rows), 4 expand B,
+// 1 TMA producer, 1 MMA issuer (in the leading CTA; in the other it forwards
+// "operands expanded" to the leader).  Tensor memory: two 192-column
+// accumulators and four 32-column A buffers.
 #include <math.h>
+
+#include <mutex>
 
 #include "common.cuh"
 #include "sched.cuh"
+#include "tc_ptx.cuh"
+#include "tma_host.cuh"
 
 namespace moe {
+namespace tc {
 namespace {
 
-constexpr int BM = 64, BN = 64, BKW = 16, kThreads = 256;
+constexpr int kRowTile = 192;                  // B rows (N) of a tile, at most
+constexpr int kStages = 5;                     // 8-bit stages, 128 deep
+constexpr int kBufs = 4;                       // expanded steps, 64 deep
+constexpr uint32_t kA8 = 128 * 128;            // 8-bit A bytes of a stage
+constexpr uint32_t kB8 = kRowTile / 2 * 128;   // 8-bit B bytes of a stage
+constexpr uint32_t kB16 = kRowTile / 2 * 128;  // fp16 B bytes of a step
+constexpr uint32_t kAccCols = kRowTile, kACol = 2 * kAccCols;
+constexpr int kEpiWarp = 0, kAWarp = 4, kBWarp = 12, kTmaWarp = 16, kMmaWarp = 17;
+constexpr int kThreadsI8 = 18 * 32;
+constexpr int kBars = 2 * kStages + 3 * kBufs + 4 + 1;
+constexpr uint32_t kCtrl = kStages * (kA8 + kB8) + kBufs * kB16;
+constexpr uint32_t kHolder = kCtrl + 8 * kBars;
+constexpr uint32_t kTable = kHolder + 8;       // prefix, offsets, scan scratch
+constexpr uint32_t kSmem = kTable + 2 * (kMaxExperts + 1) * 4 + 32 * 4 + 1024;
+static_assert(kSmem <= 232448, "more shared memory than one CTA may use");
+static_assert(kACol + kBufs * 32 <= 512, "more tensor memory than there is");
+
+struct I8Params {
+  const int32_t* off;
+  const float *rs, *s0, *s1;
+  void* out;
+  int32_t* status;
+  int N, E, Kd, Nout;
+  int ch_tiles;  // channel tiles per expert: of 256 (128 for gate/up)
+  int row_tile;  // rows of a tile, at most
+};
+
+struct I8Tile {
+  int e, row0, hi;  // expert, first row, end of the expert's rows
+  int n;            // MMA N: rows of the tile, a multiple of 16, at least 32
+  int ch0;          // first channel of this CTA
+};
+
+// Tile t is channel tile (t mod ch_tiles) of row tile t / ch_tiles; the rows
+// of an expert are split evenly over its ceil(rows / row_tile) row tiles.
+template <bool kSwiglu>
+__device__ __forceinline__ I8Tile i8_tile(int t, const I8Params& p, const int32_t* prefix,
+                                          const int32_t* offs, int rank) {
+  I8Tile x;
+  const int g = t / p.ch_tiles;
+  x.e = find_expert(prefix, p.E, g);
+  const ExpertRows r = expert_rows(offs, x.e, p.N);
+  const int parts = prefix[x.e + 1] - prefix[x.e], i = g - prefix[x.e];
+  const int per = ((r.hi - r.lo + parts - 1) / parts + 15) & ~15;
+  x.row0 = r.lo + i * per;
+  x.hi = min(r.hi, x.row0 + per);
+  x.n = max(32, per);
+  x.ch0 = (t - g * p.ch_tiles) * (kSwiglu ? 128 : 256) + rank * (kSwiglu ? 64 : 128);
+  return x;
+}
+
+// Four signed bytes as fp16: 0x64uu is 1024 + u, u = byte + 128.
+__device__ __forceinline__ void expand4(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  const uint32_t u = w ^ 0x80808080u;
+  const __half2 bias = __halves2half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480));  // 1152
+  uint32_t a = __byte_perm(u, 0x64646464u, 0x4140), b = __byte_perm(u, 0x64646464u, 0x4342);
+  __half2 x = __hsub2(*reinterpret_cast<__half2*>(&a), bias);
+  __half2 y = __hsub2(*reinterpret_cast<__half2*>(&b), bias);
+  lo = *reinterpret_cast<uint32_t*>(&x);
+  hi = *reinterpret_cast<uint32_t*>(&y);
+}
+
+__device__ __forceinline__ void expand16(uint4 v, uint32_t* r) {
+  expand4(v.x, r[0], r[1]);
+  expand4(v.y, r[2], r[3]);
+  expand4(v.z, r[4], r[5]);
+  expand4(v.w, r[6], r[7]);
+}
+
+__device__ __forceinline__ void store1(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
+__device__ __forceinline__ void store1(float* p, float v) { *p = v; }
 
 template <bool kSwiglu, typename O>
-__global__ void __launch_bounds__(kThreads)
-gmm_i8_kernel(const int8_t* __restrict__ A, const float* __restrict__ rs,
-              const int8_t* __restrict__ B0, const float* __restrict__ s0,
-              const int8_t* __restrict__ B1, const float* __restrict__ s1,
-              const int32_t* __restrict__ off, int N, int Kd, int Nout, int E,
-              O* __restrict__ out) {
-  __shared__ int32_t prefix[kMaxExperts + 1];
-  __shared__ int32_t offs[kMaxExperts + 1];
-  __shared__ int32_t scratch[32];
-  __shared__ int As[BKW][BM + 1];
-  __shared__ int Bs0[BKW][BN + 1];
-  __shared__ int Bs1[kSwiglu ? BKW : 1][BN + 1];
-  stage_offsets(off, E, N, offs, scratch);
-  build_tile_prefix(offs, E, N, BM, prefix, scratch);
-  const int tile = blockIdx.x;
-  if (tile >= prefix[E]) return;  // uniform across the CTA
-  const int e = find_expert(prefix, E, tile);
-  const ExpertRows rows = expert_rows(offs, e, N);
-  const int row0 = rows.lo + (tile - prefix[e]) * BM;
-  const int n0 = blockIdx.y * BN;
-  const int8_t* b0 = B0 + (size_t)e * Nout * Kd;
-  const int8_t* b1 = kSwiglu ? B1 + (size_t)e * Nout * Kd : nullptr;
-  const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
-  int acc0[4][4] = {}, acc1[4][4] = {};
-  const int lr = tid >> 2, lw = (tid & 3) * 4;
-  for (int k0 = 0; k0 < Kd; k0 += BKW * 4) {
-    const int c = k0 + lw * 4;
-    const int r = row0 + lr, n = n0 + lr;
-    const uint4 z = make_uint4(0u, 0u, 0u, 0u);
-    const uint4 a = (r < rows.hi && c < Kd) ? ld_v4(A + (size_t)r * Kd + c) : z;
-    const uint4 w = (n < Nout && c < Kd) ? ld_v4(b0 + (size_t)n * Kd + c) : z;
-    As[lw][lr] = a.x, As[lw + 1][lr] = a.y, As[lw + 2][lr] = a.z, As[lw + 3][lr] = a.w;
-    Bs0[lw][lr] = w.x, Bs0[lw + 1][lr] = w.y, Bs0[lw + 2][lr] = w.z, Bs0[lw + 3][lr] = w.w;
-    if constexpr (kSwiglu) {
-      const uint4 v = (n < Nout && c < Kd) ? ld_v4(b1 + (size_t)n * Kd + c) : z;
-      Bs1[lw][lr] = v.x, Bs1[lw + 1][lr] = v.y, Bs1[lw + 2][lr] = v.z, Bs1[lw + 3][lr] = v.w;
+__global__ void __launch_bounds__(kThreadsI8, 1)
+gmm_i8_kernel(const __grid_constant__ CUtensorMap mapW0, const __grid_constant__ CUtensorMap mapW1,
+              const __grid_constant__ CUtensorMap mapX32, const __grid_constant__ CUtensorMap mapX8,
+              const I8Params p) {
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  uint8_t* g = smem_raw + (base - raw);
+  const uint32_t sA8 = base, sB8 = base + kStages * kA8, sB16 = sB8 + kStages * kB8;
+  const uint32_t bars = base + kCtrl;
+  auto q_full = [&](int s) { return bars + 8u * s; };
+  auto q_empty = [&](int s) { return bars + 8u * (kStages + s); };
+  auto c_full = [&](int b) { return bars + 8u * (2 * kStages + b); };
+  auto p_full = [&](int b) { return bars + 8u * (2 * kStages + kBufs + b); };
+  auto c_empty = [&](int b) { return bars + 8u * (2 * kStages + 2 * kBufs + b); };
+  auto t_full = [&](int a) { return bars + 8u * (2 * kStages + 3 * kBufs + a); };
+  auto t_empty = [&](int a) { return bars + 8u * (2 * kStages + 3 * kBufs + 2 + a); };
+  const uint32_t drain = bars + 8u * (2 * kStages + 3 * kBufs + 4);
+  uint32_t* holder = reinterpret_cast<uint32_t*>(g + kHolder);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(g + kHolder + 4);
+  int32_t* prefix = reinterpret_cast<int32_t*>(g + kTable);
+  int32_t* offs = prefix + (kMaxExperts + 1);
+  int32_t* scratch = offs + (kMaxExperts + 1);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(q_full(s), 1);
+      mbar_init(q_empty(s), 12);  // the expanding warps
     }
-    __syncthreads();
-#pragma unroll
-    for (int kk = 0; kk < BKW; ++kk) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int av = As[kk][ty * 4 + i];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          acc0[i][j] = __dp4a(av, Bs0[kk][tx * 4 + j], acc0[i][j]);
-          if constexpr (kSwiglu) acc1[i][j] = __dp4a(av, Bs1[kk][tx * 4 + j], acc1[i][j]);
+    for (int b = 0; b < kBufs; ++b) {
+      mbar_init(c_full(b), 8);  // one A group and the B warps
+      mbar_init(p_full(b), 1);
+      mbar_init(c_empty(b), 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(t_full(a), 1);
+      mbar_init(t_empty(a), 8);  // 4 epilogue warps of both CTAs
+    }
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    mbar_fence_init();
+  }
+  if (warp == kTmaWarp && lane == 0) {
+    tma_prefetch_desc(&mapW0);
+    if constexpr (kSwiglu) tma_prefetch_desc(&mapW1);
+    tma_prefetch_desc(&mapX32);
+    tma_prefetch_desc(&mapX8);
+  }
+  if (warp == kMmaWarp) {
+    tmem_alloc_pair(smem_u32(holder), 512);
+    tmem_relinquish_pair();
+  }
+  stage_offsets(p.off, p.E, p.N, offs, scratch);
+  build_tile_prefix(offs, p.E, p.N, p.row_tile, prefix, scratch);  // ends with __syncthreads
+  const int total = prefix[p.E] * p.ch_tiles;
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *holder;
+  cluster_sync_all();  // both CTAs' barriers are initialised
+  const int rank = (int)cluster_ctarank();
+  const int t0 = (int)cluster_id_x(), dt = (int)cluster_count_x();
+  const int stages = (p.Kd + 127) / 128, steps = (p.Kd + 63) / 64;
+
+  if (warp == kTmaWarp) {
+    if (lane == 0) {
+      int s = 0, n = 0;
+      uint32_t ph = 0;
+      bool run = true;
+      for (int t = t0; run && t < total; t += dt) {
+        const I8Tile x = i8_tile<kSwiglu>(t, p, prefix, offs, rank);
+        const int nb = x.n / 2, r0 = x.row0 + rank * nb;
+        const uint32_t tx = kA8 + (uint32_t)nb * 128u;
+        for (int k = 0; k < stages; ++k) {
+          if (!mbar_wait(q_empty(s), ph ^ 1u, abort_flag, p.status)) {
+            run = false;
+            break;
+          }
+          mbar_arrive_expect_tx(q_full(s), tx);
+          const uint32_t a = sA8 + s * kA8, b = sB8 + s * kB8;
+          tma_load_3d(a, &mapW0, q_full(s), k * 128, x.ch0, x.e);
+          if constexpr (kSwiglu) tma_load_3d(a + kA8 / 2, &mapW1, q_full(s), k * 128, x.ch0, x.e);
+          int r = 0;
+          for (; r + 32 <= nb; r += 32) tma_load_2d(b + r * 128, &mapX32, q_full(s), k * 128, r0 + r);
+          for (; r < nb; r += 8) tma_load_2d(b + r * 128, &mapX8, q_full(s), k * 128, r0 + r);
+          ++n;
+          if (++s == kStages) s = 0, ph ^= 1u;
         }
       }
-    }
-    __syncthreads();
-  }
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int r = row0 + ty * 4 + i;
-    if (r >= rows.hi) continue;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int n = n0 + tx * 4 + j;
-      if (n >= Nout) continue;
-      float y = (float)acc0[i][j] * rs[r] * s0[(size_t)e * Nout + n];
-      if constexpr (kSwiglu) {
-        const float u = (float)acc1[i][j] * rs[r] * s1[(size_t)e * Nout + n];
-        y = y / (1.f + expf(-y)) * u;
+      // every copy has landed before the CTA may exit
+      for (int st = 0; st < kStages && st < n; ++st) {
+        const int last = st + (n - 1 - st) / kStages * kStages;
+        mbar_wait(q_full(st), (uint32_t)(last / kStages) & 1u, abort_flag, p.status, false);
       }
-      out[(size_t)r * Nout + n] = (O)y;
     }
+  } else if (warp == kMmaWarp) {
+    if (lane == 0 && rank == 0) {
+      const uint64_t bdesc0 = desc_sw128(sB16, 16, 1024);
+      int b = 0, it = 0;
+      uint32_t ph = 0;
+      bool run = true;
+      for (int t = t0; run && t < total; t += dt, ++it) {
+        const I8Tile x = i8_tile<kSwiglu>(t, p, prefix, offs, rank);
+        const uint32_t idesc = idesc_f16_f32(256, x.n);
+        const int acc = it & 1;
+        if (!mbar_wait<true>(t_empty(acc), ((it >> 1) & 1) ^ 1u, abort_flag, p.status)) break;
+        tc_fence_after();
+        const uint32_t d = tmem + acc * kAccCols;
+        uint32_t accum = 0u;
+        for (int k = 0; k < steps; ++k) {
+          if (!mbar_wait(c_full(b), ph, abort_flag, p.status) ||
+              !mbar_wait<true>(p_full(b), ph, abort_flag, p.status)) {
+            run = false;
+            break;
+          }
+          tc_fence_after();
+          const uint64_t bd = bdesc0 + (uint64_t)b * (kB16 >> 4);
+          const uint32_t a = tmem + kACol + b * 32;
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk) {
+            umma_f16_pair_ta(d, a + kk * 8, bd + kk * 2, idesc, accum);
+            accum = 1u;
+          }
+          umma_commit_pair(c_empty(b), 3);
+          if (++b == kBufs) b = 0, ph ^= 1u;
+        }
+        if (!run) break;
+        umma_commit_pair(t_full(acc), 3);
+      }
+      umma_commit_pair(drain, 1);
+      mbar_wait(drain, 0, abort_flag, p.status, false);
+    } else if (lane == 0) {
+      // The other CTA: its expanded operands, made known to the leader.  One
+      // thread takes the cluster-scope release, not the expanding warps.
+      int b = 0;
+      uint32_t ph = 0;
+      bool run = true;
+      for (int t = t0; run && t < total; t += dt)
+        for (int k = 0; k < steps; ++k) {
+          if (!mbar_wait(c_full(b), ph, abort_flag, p.status)) {
+            run = false;
+            break;
+          }
+          tc_fence_after();
+          tc_fence_before();
+          mbar_arrive_release_cluster(mapa_shared(p_full(b), 0));
+          if (++b == kBufs) b = 0, ph ^= 1u;
+        }
+    }
+  } else if (warp >= kAWarp) {
+    // ---- expand: one 64-deep step at a time ----
+    const bool is_a = warp < kBWarp;
+    const int half = is_a ? (warp - kAWarp) >> 2 : 0;  // A group: which 64 bytes of the stage
+    const int quarter = warp & 3;
+    // A: the weight row of this lane.  Gate/up stages hold 64 gate rows, then
+    // 64 up rows; a warp takes 16 of each, so that gate and up of a channel
+    // meet in lanes i and i + 16 of one epilogue warp.
+    const int arow = kSwiglu ? (lane < 16 ? quarter * 16 + lane : 48 + quarter * 16 + lane)
+                             : quarter * 32 + lane;
+    int s = 0, c = 0;  // stage; steps before this stage
+    uint32_t ph = 0;
+    bool run = true;
+    for (int t = t0; run && t < total; t += dt) {
+      const int nb = is_a ? 0 : i8_tile<kSwiglu>(t, p, prefix, offs, rank).n / 2;
+      for (int k = 0; k < stages; ++k) {
+        if (!__all_sync(0xffffffffu, mbar_wait(q_full(s), ph, abort_flag, p.status))) {
+          run = false;
+          break;
+        }
+        const int here = min(2, steps - 2 * k);  // steps in this stage
+        for (int h = is_a ? half : 0; h < (is_a ? min(half + 1, here) : here); ++h) {
+          const int b = (c + h) % kBufs;
+          const uint32_t bph = ((c + h) / kBufs) & 1;
+          if (is_a) {
+            uint32_t r[32];
+            const uint32_t row = sA8 + s * kA8 + arow * 128;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              expand16(ld_shared_v4(row + (((h * 4 + j) ^ (arow & 7)) << 4)), r + 8 * j);
+            run = __all_sync(0xffffffffu, mbar_wait(c_empty(b), bph ^ 1u, abort_flag, p.status));
+            if (!run) break;
+            tc_fence_after();
+            tmem_st_32x32b_x32(tmem + kACol + b * 32 + ((uint32_t)(quarter * 32) << 16), r);
+            tmem_st_wait();
+            tc_fence_before();
+          } else {
+            run = __all_sync(0xffffffffu, mbar_wait(c_empty(b), bph ^ 1u, abort_flag, p.status));
+            if (!run) break;
+#pragma unroll
+            for (int i = 0; i < kRowTile / 64; ++i) {
+              const int r = lane + 32 * i;
+              if (r >= nb) break;
+              uint32_t f[8];
+              expand16(ld_shared_v4(sB8 + s * kB8 + r * 128 + (((h * 4 + quarter) ^ (r & 7)) << 4)), f);
+              const uint32_t dst = sB16 + b * kB16 + r * 128;
+              st_shared_v4(dst + (((2 * quarter) ^ (r & 7)) << 4), f[0], f[1], f[2], f[3]);
+              st_shared_v4(dst + (((2 * quarter + 1) ^ (r & 7)) << 4), f[4], f[5], f[6], f[7]);
+            }
+            fence_proxy_async_smem();
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(c_full(b));
+        }
+        if (!run) break;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(q_empty(s));
+        c += here;
+        if (++s == kStages) s = 0, ph ^= 1u;
+      }
+    }
+  } else {
+    // ---- epilogue: lanes are channels, accumulator columns are rows ----
+    const int quarter = warp;
+    O* out = static_cast<O*>(p.out);
+    int it = 0;
+    for (int t = t0; t < total; t += dt, ++it) {
+      const I8Tile x = i8_tile<kSwiglu>(t, p, prefix, offs, rank);
+      const int acc = it & 1;
+      const int ch = x.ch0 + (kSwiglu ? quarter * 16 + (lane & 15) : quarter * 32 + lane);
+      const bool in = ch < p.Nout;
+      const float cs = !in ? 0.f
+                           : ((kSwiglu && lane >= 16) ? p.s1 : p.s0)[(size_t)x.e * p.Nout + ch];
+      if (!__all_sync(0xffffffffu, mbar_wait(t_full(acc), (it >> 1) & 1, abort_flag, p.status))) break;
+      tc_fence_after();
+      const uint32_t d = tmem + acc * kAccCols + ((uint32_t)(quarter * 32) << 16);
+      const int rows = x.hi - x.row0;
+      for (int c0 = 0; c0 < rows; c0 += 32) {
+        uint32_t v[32];
+        tmem_ld_32x32b_x32(d + c0, v);
+        const float rs_l = c0 + lane < rows ? p.rs[x.row0 + c0 + lane] : 0.f;
+        tmem_ld_wait();
+        if constexpr (kSwiglu) {
+          // lanes 0-15 hold gate, 16-31 up of the same channels: the lower
+          // half takes the even rows, the upper half the odd ones
+          const bool up = lane >= 16;
+#pragma unroll
+          for (int j = 0; j < 32; j += 2) {
+            const float r0 = __shfl_sync(0xffffffffu, rs_l, j), r1 = __shfl_sync(0xffffffffu, rs_l, j + 1);
+            const float y0 = __uint_as_float(v[j]) * cs * r0, y1 = __uint_as_float(v[j + 1]) * cs * r1;
+            const float got = __shfl_xor_sync(0xffffffffu, up ? y0 : y1, 16);
+            const float gate = up ? got : y0, u = up ? y1 : got;
+            const int row = c0 + j + (up ? 1 : 0);
+            if (in && row < rows)
+              store1(out + (size_t)(x.row0 + row) * p.Nout + ch, gate / (1.f + expf(-gate)) * u);
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < 32; ++j) {
+            const float r = __shfl_sync(0xffffffffu, rs_l, j);
+            if (in && c0 + j < rows)
+              store1(out + (size_t)(x.row0 + c0 + j) * p.Nout + ch, __uint_as_float(v[j]) * cs * r);
+          }
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(mapa_shared(t_empty(acc), 0));
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync_all();  // no CTA leaves while its peer may still signal its barriers
+  if (warp == kMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem, 512);
   }
 }
 
@@ -95,19 +392,61 @@ int check_i8(const void* A, const float* rs, const int32_t* off, int N, int H, i
 template <bool kSwiglu, typename O>
 int launch_i8(const int8_t* A, const float* rs, const int8_t* B0, const float* s0, const int8_t* B1,
               const float* s1, const int32_t* off, int N, int Kd, int Nout, int E, O* out,
-              cudaStream_t s) {
-  const long long tiles = (long long)(N + BM - 1) / BM + (E < N ? E : N);  // at most
-  const dim3 grid((unsigned)tiles, (Nout + BN - 1) / BN);
-  gmm_i8_kernel<kSwiglu, O><<<grid, kThreads, 0, s>>>(A, rs, B0, s0, B1, s1, off, N, Kd, Nout, E, out);
-  MOE_LAUNCH_CHECK();
+              int32_t* status, cudaStream_t s) {
+  if (int rc = device_ok()) return rc;
+  CUtensorMap w0, w1, x32, x8;
+  const uint64_t dw[3] = {(uint64_t)Kd, (uint64_t)Nout, (uint64_t)E};
+  const uint32_t bw[3] = {128, kSwiglu ? 64u : 128u, 1};
+  const uint64_t dx[2] = {(uint64_t)Kd, (uint64_t)N};
+  const uint32_t b32[2] = {128, 32}, b8[2] = {128, 8};
+  if (!make_map_sw128(&w0, B0, 1, 3, dw, bw) || !make_map_sw128(&w1, B1 ? B1 : B0, 1, 3, dw, bw) ||
+      !make_map_sw128(&x32, A, 1, 2, dx, b32) || !make_map_sw128(&x8, A, 1, 2, dx, b8))
+    return MOE_ERR_CUDA;
+  static std::once_flag once;
+  static cudaError_t attr = cudaSuccess;
+  std::call_once(once, [] {
+    attr = cudaFuncSetAttribute(gmm_i8_kernel<kSwiglu, O>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                (int)kSmem);
+  });
+  if (attr != cudaSuccess) return MOE_ERR_CUDA;
+  const int per = kSwiglu ? 128 : 256;
+  const I8Params p{off, rs, s0, s1, out, status, N, E, Kd, Nout, (Nout + per - 1) / per, kRowTile};
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = 2;
+  at[0].val.clusterDim.y = 1;
+  at[0].val.clusterDim.z = 1;
+  // one persistent CTA per SM, as many whole pairs as can be resident
+  cfg.gridDim = dim3(sm_count() / 2 * 2, 1, 1);
+  cfg.blockDim = dim3(kThreadsI8, 1, 1);
+  cfg.dynamicSmemBytes = kSmem;
+  cfg.stream = s;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  static int resident = -1;
+  if (resident < 0) {
+    int n = 0;
+    resident = (cudaOccupancyMaxActiveClusters(&n, gmm_i8_kernel<kSwiglu, O>, &cfg) == cudaSuccess && n > 0)
+                   ? n
+                   : 0;
+    (void)cudaGetLastError();
+  }
+  if (resident > 0 && 2 * resident < (int)cfg.gridDim.x) cfg.gridDim.x = 2 * resident;
+  if (cudaLaunchKernelEx(&cfg, gmm_i8_kernel<kSwiglu, O>, w0, w1, x32, x8, p) != cudaSuccess) {
+    (void)cudaGetLastError();
+    return MOE_ERR_CUDA;
+  }
   count_launches(1);
   return MOE_OK;
 }
 
 }  // namespace
+}  // namespace tc
 }  // namespace moe
 
 using namespace moe;
+using namespace moe::tc;
 
 extern "C" int moe_gate_up_swiglu_int8(const int8_t* permuted_q, const float* row_scale,
                                        const int32_t* expert_offsets, int N, int H, int I, int E,
@@ -118,9 +457,9 @@ extern "C" int moe_gate_up_swiglu_int8(const int8_t* permuted_q, const float* ro
   if (N == 0) return MOE_OK;
   if (!W_gate_q || !W_up_q || !gate_scale || !up_scale || !act) return MOE_ERR_INVALID_ARG;
   if (!aligned16(W_gate_q) || !aligned16(W_up_q) || !aligned16(act)) return MOE_ERR_INVALID_ARG;
-  (void)dev_status;
   return launch_i8<true>(permuted_q, row_scale, W_gate_q, gate_scale, W_up_q, up_scale,
-                         expert_offsets, N, H, I, E, static_cast<__nv_bfloat16*>(act), stream);
+                         expert_offsets, N, H, I, E, static_cast<__nv_bfloat16*>(act), dev_status,
+                         stream);
 }
 
 extern "C" int moe_down_proj_int8(const int8_t* act_q, const float* row_scale,
@@ -132,10 +471,9 @@ extern "C" int moe_down_proj_int8(const int8_t* act_q, const float* row_scale,
   if (N == 0) return MOE_OK;
   if (!W_down_q || !down_scale || !expanded) return MOE_ERR_INVALID_ARG;
   if (!aligned16(W_down_q) || !aligned16(expanded)) return MOE_ERR_INVALID_ARG;
-  (void)dev_status;
   if (out_dtype == MOE_F32)
     return launch_i8<false>(act_q, row_scale, W_down_q, down_scale, nullptr, nullptr, expert_offsets,
-                            N, I, H, E, static_cast<float*>(expanded), stream);
+                            N, I, H, E, static_cast<float*>(expanded), dev_status, stream);
   return launch_i8<false>(act_q, row_scale, W_down_q, down_scale, nullptr, nullptr, expert_offsets, N,
-                          I, H, E, static_cast<__nv_bfloat16*>(expanded), stream);
+                          I, H, E, static_cast<__nv_bfloat16*>(expanded), dev_status, stream);
 }

@@ -20,11 +20,17 @@
 //     14 KB (TMA) + 14 KB (read) + 12 KB (fp16 rows) + 12 KB (MMA reads) in
 //     the 384 cycles of its MMAs at 192 rows.
 //
-// Warps: 4 epilogue (one per tensor-memory lane quarter), 8 expand A (two
-// groups of 4, one per 64-byte half of the 128-byte stage rows), 4 expand B,
-// 1 TMA producer, 1 MMA issuer (in the leading CTA; in the other it forwards
-// "operands expanded" to the leader).  Tensor memory: two 192-column
-// accumulators and four 32-column A buffers.
+// Warps: 4 epilogue (one per tensor-memory lane quarter), 8 expand A and 8
+// expand B (each two groups of 4, one per 64-byte half of the 128-byte stage
+// rows), 1 TMA producer, 1 MMA issuer (in the leading CTA).  Tensor memory:
+// two 192-column accumulators and four 32-column A buffers.
+//
+// The expanding warps of both CTAs arrive on the leader's barrier with the
+// default (CTA-scope) release: what they wrote, tensor memory and shared
+// memory of their own SM, is read by that SM's tensor core alone, and is
+// ordered by tcgen05.wait::st and the async-proxy fence before the arrival.
+// A cluster-scope release there, by one forwarding thread, cost 1100 cycles a
+// step (398 us instead of LATER us for 8192 x 4096 x 4096).
 #include <math.h>
 
 #include <mutex>
@@ -40,20 +46,22 @@ namespace {
 
 constexpr int kRowTile = 192;                  // B rows (N) of a tile, at most
 constexpr int kStages = 5;                     // 8-bit stages, 128 deep
-constexpr int kBufs = 4;                       // expanded steps, 64 deep
+constexpr int kBufs = 2;                       // expanded stages
 constexpr uint32_t kA8 = 128 * 128;            // 8-bit A bytes of a stage
 constexpr uint32_t kB8 = kRowTile / 2 * 128;   // 8-bit B bytes of a stage
-constexpr uint32_t kB16 = kRowTile / 2 * 128;  // fp16 B bytes of a step
+constexpr uint32_t kB16 = kRowTile / 2 * 256;  // fp16 B bytes of a stage, two 64-deep halves
 constexpr uint32_t kAccCols = kRowTile, kACol = 2 * kAccCols;
-constexpr int kEpiWarp = 0, kAWarp = 4, kBWarp = 12, kTmaWarp = 16, kMmaWarp = 17;
-constexpr int kThreadsI8 = 18 * 32;
-constexpr int kBars = 2 * kStages + 3 * kBufs + 4 + 1;
-constexpr uint32_t kCtrl = kStages * (kA8 + kB8) + kBufs * kB16;
+constexpr int kTmaWarp = 0, kMmaWarp = 1, kAWarp = 6, kBWarp = 14;  // 2-5: epilogue
+constexpr int kThreadsI8 = 22 * 32;
+constexpr int kBars = 2 * kStages + 2 * kBufs + 4 + 1;
+constexpr uint32_t kStageWarp = 32 * 128 + kRowTile * 4;  // epilogue staging of a warp
+constexpr uint32_t kStage = kStages * (kA8 + kB8) + kBufs * kB16;
+constexpr uint32_t kCtrl = kStage + 4 * kStageWarp;
 constexpr uint32_t kHolder = kCtrl + 8 * kBars;
 constexpr uint32_t kTable = kHolder + 8;       // prefix, offsets, scan scratch
 constexpr uint32_t kSmem = kTable + 2 * (kMaxExperts + 1) * 4 + 32 * 4 + 1024;
 static_assert(kSmem <= 232448, "more shared memory than one CTA may use");
-static_assert(kACol + kBufs * 32 <= 512, "more tensor memory than there is");
+static_assert(kACol + kBufs * 64 <= 512, "more tensor memory than there is");
 
 struct I8Params {
   const int32_t* off;
@@ -107,8 +115,14 @@ __device__ __forceinline__ void expand16(uint4 v, uint32_t* r) {
   expand4(v.w, r[6], r[7]);
 }
 
-__device__ __forceinline__ void store1(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
-__device__ __forceinline__ void store1(float* p, float v) { *p = v; }
+__device__ __forceinline__ void st_shared_b16(uint32_t addr, float v) {
+  const __nv_bfloat16 h = __float2bfloat16_rn(v);
+  asm volatile("st.shared.u16 [%0], %1;" ::"r"(addr), "h"(*reinterpret_cast<const unsigned short*>(&h))
+               : "memory");
+}
+__device__ __forceinline__ void st_shared_f32(uint32_t addr, float v) {
+  asm volatile("st.shared.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+}
 
 template <bool kSwiglu, typename O>
 __global__ void __launch_bounds__(kThreadsI8, 1)
@@ -124,11 +138,10 @@ gmm_i8_kernel(const __grid_constant__ CUtensorMap mapW0, const __grid_constant__
   auto q_full = [&](int s) { return bars + 8u * s; };
   auto q_empty = [&](int s) { return bars + 8u * (kStages + s); };
   auto c_full = [&](int b) { return bars + 8u * (2 * kStages + b); };
-  auto p_full = [&](int b) { return bars + 8u * (2 * kStages + kBufs + b); };
-  auto c_empty = [&](int b) { return bars + 8u * (2 * kStages + 2 * kBufs + b); };
-  auto t_full = [&](int a) { return bars + 8u * (2 * kStages + 3 * kBufs + a); };
-  auto t_empty = [&](int a) { return bars + 8u * (2 * kStages + 3 * kBufs + 2 + a); };
-  const uint32_t drain = bars + 8u * (2 * kStages + 3 * kBufs + 4);
+  auto c_empty = [&](int b) { return bars + 8u * (2 * kStages + kBufs + b); };
+  auto t_full = [&](int a) { return bars + 8u * (2 * kStages + 2 * kBufs + a); };
+  auto t_empty = [&](int a) { return bars + 8u * (2 * kStages + 2 * kBufs + 2 + a); };
+  const uint32_t drain = bars + 8u * (2 * kStages + 2 * kBufs + 4);
   uint32_t* holder = reinterpret_cast<uint32_t*>(g + kHolder);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(g + kHolder + 4);
   int32_t* prefix = reinterpret_cast<int32_t*>(g + kTable);
@@ -139,11 +152,10 @@ gmm_i8_kernel(const __grid_constant__ CUtensorMap mapW0, const __grid_constant__
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
       mbar_init(q_full(s), 1);
-      mbar_init(q_empty(s), 12);  // the expanding warps
+      mbar_init(q_empty(s), 8);  // the expanding warps of one group
     }
     for (int b = 0; b < kBufs; ++b) {
-      mbar_init(c_full(b), 8);  // one A group and the B warps
-      mbar_init(p_full(b), 1);
+      mbar_init(c_full(b), 16);  // the leader's: an A and a B group of both CTAs
       mbar_init(c_empty(b), 1);
     }
     for (int a = 0; a < 2; ++a) {
@@ -174,7 +186,7 @@ gmm_i8_kernel(const __grid_constant__ CUtensorMap mapW0, const __grid_constant__
   cluster_sync_all();  // both CTAs' barriers are initialised
   const int rank = (int)cluster_ctarank();
   const int t0 = (int)cluster_id_x(), dt = (int)cluster_count_x();
-  const int stages = (p.Kd + 127) / 128, steps = (p.Kd + 63) / 64;
+  const int stages = (p.Kd + 127) / 128;
 
   if (warp == kTmaWarp) {
     if (lane == 0) {
@@ -186,7 +198,7 @@ gmm_i8_kernel(const __grid_constant__ CUtensorMap mapW0, const __grid_constant__
         const int nb = x.n / 2, r0 = x.row0 + rank * nb;
         const uint32_t tx = kA8 + (uint32_t)nb * 128u;
         for (int k = 0; k < stages; ++k) {
-          if (!mbar_wait(q_empty(s), ph ^ 1u, abort_flag, p.status)) {
+          if (!mbar_wait_quiet(q_empty(s), ph ^ 1u, abort_flag, p.status)) {
             run = false;
             break;
           }
@@ -204,7 +216,7 @@ gmm_i8_kernel(const __grid_constant__ CUtensorMap mapW0, const __grid_constant__
       // every copy has landed before the CTA may exit
       for (int st = 0; st < kStages && st < n; ++st) {
         const int last = st + (n - 1 - st) / kStages * kStages;
-        mbar_wait(q_full(st), (uint32_t)(last / kStages) & 1u, abort_flag, p.status, false);
+        mbar_wait_quiet(q_full(st), (uint32_t)(last / kStages) & 1u, abort_flag, p.status, false);
       }
     }
   } else if (warp == kMmaWarp) {
@@ -221,150 +233,185 @@ gmm_i8_kernel(const __grid_constant__ CUtensorMap mapW0, const __grid_constant__
         tc_fence_after();
         const uint32_t d = tmem + acc * kAccCols;
         uint32_t accum = 0u;
-        for (int k = 0; k < steps; ++k) {
-          if (!mbar_wait(c_full(b), ph, abort_flag, p.status) ||
-              !mbar_wait<true>(p_full(b), ph, abort_flag, p.status)) {
+        for (int k = 0; k < stages; ++k) {
+          if (!mbar_wait_quiet(c_full(b), ph, abort_flag, p.status)) {
             run = false;
             break;
           }
           tc_fence_after();
           const uint64_t bd = bdesc0 + (uint64_t)b * (kB16 >> 4);
-          const uint32_t a = tmem + kACol + b * 32;
+          const uint32_t a = tmem + kACol + b * 64;
+          // (past the end of Kd both operands are zeros)
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk) {
-            umma_f16_pair_ta(d, a + kk * 8, bd + kk * 2, idesc, accum);
+          for (int kk = 0; kk < 8; ++kk) {
+            umma_f16_pair_ta(d, a + kk * 8, bd + (kk >> 2) * (kB16 >> 5) + (kk & 3) * 2, idesc, accum);
             accum = 1u;
           }
           umma_commit_pair(c_empty(b), 3);
-          if (++b == kBufs) b = 0, ph ^= 1u;
+          b ^= 1;
+          if (b == 0) ph ^= 1u;
         }
         if (!run) break;
         umma_commit_pair(t_full(acc), 3);
       }
       umma_commit_pair(drain, 1);
-      mbar_wait(drain, 0, abort_flag, p.status, false);
-    } else if (lane == 0) {
-      // The other CTA: its expanded operands, made known to the leader.  One
-      // thread takes the cluster-scope release, not the expanding warps.
-      int b = 0;
-      uint32_t ph = 0;
-      bool run = true;
-      for (int t = t0; run && t < total; t += dt)
-        for (int k = 0; k < steps; ++k) {
-          if (!mbar_wait(c_full(b), ph, abort_flag, p.status)) {
-            run = false;
-            break;
-          }
-          tc_fence_after();
-          tc_fence_before();
-          mbar_arrive_release_cluster(mapa_shared(p_full(b), 0));
-          if (++b == kBufs) b = 0, ph ^= 1u;
-        }
+      mbar_wait_quiet(drain, 0, abort_flag, p.status, false);
     }
   } else if (warp >= kAWarp) {
-    // ---- expand: one 64-deep step at a time ----
+    // ---- expand: the two groups take alternate stages, one buffer each ----
     const bool is_a = warp < kBWarp;
-    const int half = is_a ? (warp - kAWarp) >> 2 : 0;  // A group: which 64 bytes of the stage
+    const int grp = ((warp - kAWarp) >> 2) & 1;
     const int quarter = warp & 3;
     // A: the weight row of this lane.  Gate/up stages hold 64 gate rows, then
     // 64 up rows; a warp takes 16 of each, so that gate and up of a channel
     // meet in lanes i and i + 16 of one epilogue warp.
+    // B: the rows lane, lane + 32, ...; two of the eight 16-byte chunks of a
+    // row per warp.  Chunk c of row r sits at chunk c ^ (r & 7) (128-byte
+    // swizzle) in the 8-bit and the fp16 rows.
     const int arow = kSwiglu ? (lane < 16 ? quarter * 16 + lane : 48 + quarter * 16 + lane)
                              : quarter * 32 + lane;
-    int s = 0, c = 0;  // stage; steps before this stage
-    uint32_t ph = 0;
+    const uint32_t a_src = sA8 + arow * 128 + ((arow & 7) << 4);
+    const uint32_t a_dst = tmem + kACol + grp * 64 + ((uint32_t)(quarter * 32) << 16);
+    const uint32_t b_src = sB8 + lane * 128 + ((lane & 7) << 4);
+    const uint32_t b_dst = sB16 + grp * kB16 + (quarter >> 1) * (kB16 / 2) + lane * 128 + ((lane & 7) << 4);
+    const uint32_t full_of_leader = mapa_shared(c_full(grp), 0);
+    int s = grp, n0 = 0;  // ring stage; stages before this tile
+    uint32_t ph = 0, bph = 0;
     bool run = true;
     for (int t = t0; run && t < total; t += dt) {
       const int nb = is_a ? 0 : i8_tile<kSwiglu>(t, p, prefix, offs, rank).n / 2;
-      for (int k = 0; k < stages; ++k) {
-        if (!__all_sync(0xffffffffu, mbar_wait(q_full(s), ph, abort_flag, p.status))) {
-          run = false;
-          break;
-        }
-        const int here = min(2, steps - 2 * k);  // steps in this stage
-        for (int h = is_a ? half : 0; h < (is_a ? min(half + 1, here) : here); ++h) {
-          const int b = (c + h) % kBufs;
-          const uint32_t bph = ((c + h) / kBufs) & 1;
-          if (is_a) {
-            uint32_t r[32];
-            const uint32_t row = sA8 + s * kA8 + arow * 128;
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-              expand16(ld_shared_v4(row + (((h * 4 + j) ^ (arow & 7)) << 4)), r + 8 * j);
-            run = __all_sync(0xffffffffu, mbar_wait(c_empty(b), bph ^ 1u, abort_flag, p.status));
-            if (!run) break;
-            tc_fence_after();
-            tmem_st_32x32b_x32(tmem + kACol + b * 32 + ((uint32_t)(quarter * 32) << 16), r);
-            tmem_st_wait();
-            tc_fence_before();
-          } else {
-            run = __all_sync(0xffffffffu, mbar_wait(c_empty(b), bph ^ 1u, abort_flag, p.status));
-            if (!run) break;
-#pragma unroll
-            for (int i = 0; i < kRowTile / 64; ++i) {
-              const int r = lane + 32 * i;
-              if (r >= nb) break;
-              uint32_t f[8];
-              expand16(ld_shared_v4(sB8 + s * kB8 + r * 128 + (((h * 4 + quarter) ^ (r & 7)) << 4)), f);
-              const uint32_t dst = sB16 + b * kB16 + r * 128;
-              st_shared_v4(dst + (((2 * quarter) ^ (r & 7)) << 4), f[0], f[1], f[2], f[3]);
-              st_shared_v4(dst + (((2 * quarter + 1) ^ (r & 7)) << 4), f[4], f[5], f[6], f[7]);
-            }
-            fence_proxy_async_smem();
-          }
-          __syncwarp();
-          if (lane == 0) mbar_arrive(c_full(b));
-        }
+      for (int k = (n0 ^ grp) & 1; k < stages; k += 2) {
+        run = __all_sync(0xffffffffu, mbar_wait_quiet(q_full(s), ph, abort_flag, p.status));
         if (!run) break;
+        if (is_a) {
+          uint4 v[4];
+          uint32_t r[32];
+          const uint32_t src = a_src + s * kA8;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) v[j] = ld_shared_v4(src ^ (j << 4));
+#pragma unroll
+          for (int j = 0; j < 4; ++j) expand16(v[j], r + 8 * j);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) v[j] = ld_shared_v4(src ^ ((j + 4) << 4));
+          run = __all_sync(0xffffffffu, mbar_wait_quiet(c_empty(grp), bph ^ 1u, abort_flag, p.status));
+          if (!run) break;
+          tc_fence_after();
+          tmem_st_32x32b_x32(a_dst, r);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) expand16(v[j], r + 8 * j);
+          tmem_st_32x32b_x32(a_dst + 32, r);
+          tmem_st_wait();
+          tc_fence_before();
+        } else {
+          uint4 v[kRowTile / 64][2];
+          const uint32_t src = b_src + s * kB8;
+#pragma unroll
+          for (int i = 0; i < kRowTile / 64; ++i) {
+            if (lane + 32 * i < nb) {
+              v[i][0] = ld_shared_v4((src ^ (2 * quarter << 4)) + i * 4096);
+              v[i][1] = ld_shared_v4((src ^ ((2 * quarter + 1) << 4)) + i * 4096);
+            }
+          }
+          run = __all_sync(0xffffffffu, mbar_wait_quiet(c_empty(grp), bph ^ 1u, abort_flag, p.status));
+          if (!run) break;
+          // 16 bytes become two chunks; this warp's two make four
+          const uint32_t dst = b_dst ^ ((quarter & 1) << 6);
+#pragma unroll
+          for (int i = 0; i < kRowTile / 64; ++i) {
+            if (lane + 32 * i < nb) {
+              uint32_t f[16];
+              expand16(v[i][0], f);
+              expand16(v[i][1], f + 8);
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                st_shared_v4((dst ^ (j << 4)) + i * 4096, f[4 * j], f[4 * j + 1], f[4 * j + 2], f[4 * j + 3]);
+            }
+          }
+          fence_proxy_async_smem();
+        }
         __syncwarp();
-        if (lane == 0) mbar_arrive(q_empty(s));
-        c += here;
-        if (++s == kStages) s = 0, ph ^= 1u;
+        if (lane == 0) {
+          mbar_arrive_cluster(full_of_leader);
+          mbar_arrive(q_empty(s));
+        }
+        bph ^= 1u;
+        s += 2;
+        if (s >= kStages) s -= kStages, ph ^= 1u;
       }
+      n0 += stages;
     }
   } else {
     // ---- epilogue: lanes are channels, accumulator columns are rows ----
-    const int quarter = warp;
-    O* out = static_cast<O*>(p.out);
+    // Pieces of 32 columns are scaled, turned through this warp's staging
+    // rows (one row of 32 channels, or 16 for gate/up, per column) and
+    // written in 16-byte chunks.
+    const int quarter = warp & 3;
+    constexpr int kCh = kSwiglu ? 16 : 32;                      // channels per warp
+    constexpr int kRowB = kCh * (int)sizeof(O), kV = kRowB / 16;  // staging row, its chunks
+    const uint32_t stage_u = base + kStage + (uint32_t)quarter * kStageWarp;
+    uint8_t* stage = g + kStage + quarter * kStageWarp;
+    float* scale = reinterpret_cast<float*>(stage + 32 * 128);  // the tile's row scales
+    const int ch_l = kSwiglu ? quarter * 16 + (lane & 15) : quarter * 32 + lane;
     int it = 0;
     for (int t = t0; t < total; t += dt, ++it) {
       const I8Tile x = i8_tile<kSwiglu>(t, p, prefix, offs, rank);
       const int acc = it & 1;
-      const int ch = x.ch0 + (kSwiglu ? quarter * 16 + (lane & 15) : quarter * 32 + lane);
+      const int ch = x.ch0 + ch_l;
       const bool in = ch < p.Nout;
       const float cs = !in ? 0.f
                            : ((kSwiglu && lane >= 16) ? p.s1 : p.s0)[(size_t)x.e * p.Nout + ch];
-      if (!__all_sync(0xffffffffu, mbar_wait(t_full(acc), (it >> 1) & 1, abort_flag, p.status))) break;
+      const int rows = x.hi - x.row0;
+      for (int c = lane; c < kRowTile; c += 32) scale[c] = c < rows ? p.rs[x.row0 + c] : 0.f;
+      __syncwarp();
+      if (!__all_sync(0xffffffffu, mbar_wait_quiet(t_full(acc), (it >> 1) & 1, abort_flag, p.status))) break;
       tc_fence_after();
       const uint32_t d = tmem + acc * kAccCols + ((uint32_t)(quarter * 32) << 16);
-      const int rows = x.hi - x.row0;
+      // 16-byte chunk of the staging rows that this lane copies out, and the
+      // channels it holds; Nout is a multiple of 16, so a chunk is whole
+      const int wr = lane / kV, wc = lane % kV;
+      const int wch = x.ch0 + quarter * kCh + wc * (16 / (int)sizeof(O));
+      uint8_t* dst = static_cast<uint8_t*>(p.out) + ((size_t)(x.row0 + wr) * p.Nout + wch) * sizeof(O);
+      const size_t dst_step = (size_t)(32 / kV) * p.Nout * sizeof(O);
       for (int c0 = 0; c0 < rows; c0 += 32) {
         uint32_t v[32];
         tmem_ld_32x32b_x32(d + c0, v);
-        const float rs_l = c0 + lane < rows ? p.rs[x.row0 + c0 + lane] : 0.f;
         tmem_ld_wait();
         if constexpr (kSwiglu) {
           // lanes 0-15 hold gate, 16-31 up of the same channels: the lower
           // half takes the even rows, the upper half the odd ones
           const bool up = lane >= 16;
+          const uint32_t st = stage_u + (lane & 15) * 2 + (up ? kRowB : 0);
 #pragma unroll
           for (int j = 0; j < 32; j += 2) {
-            const float r0 = __shfl_sync(0xffffffffu, rs_l, j), r1 = __shfl_sync(0xffffffffu, rs_l, j + 1);
-            const float y0 = __uint_as_float(v[j]) * cs * r0, y1 = __uint_as_float(v[j + 1]) * cs * r1;
+            const float2 r = *reinterpret_cast<const float2*>(scale + c0 + j);
+            const float y0 = __uint_as_float(v[j]) * cs * r.x, y1 = __uint_as_float(v[j + 1]) * cs * r.y;
             const float got = __shfl_xor_sync(0xffffffffu, up ? y0 : y1, 16);
             const float gate = up ? got : y0, u = up ? y1 : got;
-            const int row = c0 + j + (up ? 1 : 0);
-            if (in && row < rows)
-              store1(out + (size_t)(x.row0 + row) * p.Nout + ch, gate / (1.f + expf(-gate)) * u);
+            st_shared_b16(st + j * kRowB, gate / (1.f + expf(-gate)) * u);
           }
         } else {
+          const uint32_t st = stage_u + lane * (uint32_t)sizeof(O);
 #pragma unroll
-          for (int j = 0; j < 32; ++j) {
-            const float r = __shfl_sync(0xffffffffu, rs_l, j);
-            if (in && c0 + j < rows)
-              store1(out + (size_t)(x.row0 + c0 + j) * p.Nout + ch, __uint_as_float(v[j]) * cs * r);
+          for (int j = 0; j < 32; j += 4) {
+            const float4 r = *reinterpret_cast<const float4*>(scale + c0 + j);
+            const float f[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const float y = __uint_as_float(v[j + q]) * cs * f[q];
+              if constexpr (sizeof(O) == 2) st_shared_b16(st + (j + q) * kRowB, y);
+              else st_shared_f32(st + (j + q) * kRowB, y);
+            }
           }
         }
+        __syncwarp();
+        if (wch < p.Nout) {
+#pragma unroll
+          for (int i = 0; i < kV; ++i)
+            if (c0 + wr + i * (32 / kV) < rows)
+              st_v4(dst + i * dst_step, ld_shared_v4(stage_u + lane * 16 + i * 512));
+        }
+        dst += kV * dst_step;
+        __syncwarp();
       }
       tc_fence_before();
       __syncwarp();

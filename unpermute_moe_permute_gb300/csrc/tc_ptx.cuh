@@ -94,6 +94,40 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatil
   }
 }
 
+// The same wait, each attempt suspended by the hardware for up to kSuspendNs:
+// for kernels whose waiting warps share their schedulers with busy ones (an
+// attempt without the hint comes back after a few hundred cycles, and its
+// retry costs issue slots).
+constexpr uint32_t kSuspendNs = 20000;
+
+__device__ __forceinline__ bool mbar_wait_quiet(uint32_t bar, uint32_t parity,
+                                                volatile int* abort_flag, int32_t* status,
+                                                bool honor_abort = true) {
+  unsigned long long t0 = 0;
+  for (uint32_t i = 0;; ++i) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity), "r"(kSuspendNs)
+        : "memory");
+    if (ok) return true;
+    if ((i & 15u) == 15u) {
+      if (honor_abort && *abort_flag) return false;
+      const unsigned long long now = globaltimer();
+      if (t0 == 0) {
+        t0 = now;
+      } else if (now - t0 > kWaitTimeoutNs) {
+        *abort_flag = 1;
+        set_status(status, MOE_ERR_TIMEOUT);
+        return false;
+      }
+    }
+  }
+}
+
 // ---- TMA --------------------------------------------------------------------
 
 __device__ __forceinline__ void tma_prefetch_desc(const CUtensorMap* map) {
@@ -323,14 +357,6 @@ __device__ __forceinline__ uint32_t mapa_shared(uint32_t addr, uint32_t rank) {
 // wgrad took 267 instead of 193 us).
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
-}
-
-// The same with release at cluster scope: what this thread has seen written
-// in its own CTA (other warps' operand rows, through a CTA-scope barrier) is
-// visible to the acquiring CTA.
-__device__ __forceinline__ void mbar_arrive_release_cluster(uint32_t cluster_addr) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
-               : "memory");
 }
 
 // TMA loads into this CTA's shared memory whose byte count goes to an

@@ -20,10 +20,10 @@
 //     14 KB (TMA) + 14 KB (read) + 12 KB (fp16 rows) + 12 KB (MMA reads) in
 //     the 384 cycles of its MMAs at 192 rows.
 //
-// Warps: 4 epilogue (one per tensor-memory lane quarter), 8 expand A and 8
-// expand B (each two groups of 4, one per 64-byte half of the 128-byte stage
-// rows), 1 TMA producer, 1 MMA issuer (in the leading CTA).  Tensor memory:
-// two 192-column accumulators and four 32-column A buffers.
+// Warps: 1 TMA producer, 1 MMA issuer (in the leading CTA), 4 epilogue (one
+// per tensor-memory lane quarter), 8 expand A (two groups of 4 that take
+// alternate 128-deep stages, each with an A buffer of its own), 4 expand B.
+// Tensor memory: two 192-column accumulators and two 64-column A buffers.
 //
 // The expanding warps of both CTAs arrive on the leader's barrier with the
 // default (CTA-scope) release: what they wrote, tensor memory and shared
@@ -52,7 +52,7 @@ constexpr uint32_t kB8 = kRowTile / 2 * 128;   // 8-bit B bytes of a stage
 constexpr uint32_t kB16 = kRowTile / 2 * 256;  // fp16 B bytes of a stage, two 64-deep halves
 constexpr uint32_t kAccCols = kRowTile, kACol = 2 * kAccCols;
 constexpr int kTmaWarp = 0, kMmaWarp = 1, kAWarp = 6, kBWarp = 14;  // 2-5: epilogue
-constexpr int kThreadsI8 = 22 * 32;
+constexpr int kThreadsI8 = 18 * 32;
 constexpr int kBars = 2 * kStages + 2 * kBufs + 4 + 1;
 constexpr uint32_t kStageWarp = 32 * 128 + kRowTile * 4;  // epilogue staging of a warp
 constexpr uint32_t kStage = kStages * (kA8 + kB8) + kBufs * kB16;
@@ -97,15 +97,16 @@ __device__ __forceinline__ I8Tile i8_tile(int t, const I8Params& p, const int32_
   return x;
 }
 
-// Four signed bytes as fp16: 0x64uu is 1024 + u, u = byte + 128.
-__device__ __forceinline__ void expand4(uint32_t w, uint32_t& lo, uint32_t& hi) {
-  const uint32_t u = w ^ 0x80808080u;
+// Four signed bytes as fp16: 0x64uu is 1024 + u with u = byte + 128, less
+// 1152.  The pairs are bytes (0, 2) and (1, 3): both operands are expanded
+// alike, so the sum over k only changes its order.
+__device__ __forceinline__ void expand4(uint32_t w, uint32_t& even, uint32_t& odd) {
   const __half2 bias = __halves2half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480));  // 1152
-  uint32_t a = __byte_perm(u, 0x64646464u, 0x4140), b = __byte_perm(u, 0x64646464u, 0x4342);
+  uint32_t a = (w & 0x00ff00ffu) ^ 0x64806480u, b = ((w >> 8) & 0x00ff00ffu) ^ 0x64806480u;
   __half2 x = __hsub2(*reinterpret_cast<__half2*>(&a), bias);
   __half2 y = __hsub2(*reinterpret_cast<__half2*>(&b), bias);
-  lo = *reinterpret_cast<uint32_t*>(&x);
-  hi = *reinterpret_cast<uint32_t*>(&y);
+  even = *reinterpret_cast<uint32_t*>(&x);
+  odd = *reinterpret_cast<uint32_t*>(&y);
 }
 
 __device__ __forceinline__ void expand16(uint4 v, uint32_t* r) {
@@ -152,10 +153,10 @@ gmm_i8_kernel(const __grid_constant__ CUtensorMap mapW0, const __grid_constant__
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
       mbar_init(q_full(s), 1);
-      mbar_init(q_empty(s), 8);  // the expanding warps of one group
+      mbar_init(q_empty(s), 8);  // an A group and the B warps
     }
     for (int b = 0; b < kBufs; ++b) {
-      mbar_init(c_full(b), 16);  // the leader's: an A and a B group of both CTAs
+      mbar_init(c_full(b), 16);  // the leader's: an A group and the B warps of both CTAs
       mbar_init(c_empty(b), 1);
     }
     for (int a = 0; a < 2; ++a) {
@@ -257,78 +258,94 @@ gmm_i8_kernel(const __grid_constant__ CUtensorMap mapW0, const __grid_constant__
       umma_commit_pair(drain, 1);
       mbar_wait_quiet(drain, 0, abort_flag, p.status, false);
     }
-  } else if (warp >= kAWarp) {
-    // ---- expand: the two groups take alternate stages, one buffer each ----
-    const bool is_a = warp < kBWarp;
-    const int grp = ((warp - kAWarp) >> 2) & 1;
+  } else if (warp >= kBWarp) {
+    // ---- expand B: the rows lane, lane + 32, ...; two of the eight 16-byte
+    // chunks of a row per warp.  Chunk c of row r sits at chunk c ^ (r & 7)
+    // (128-byte swizzle) in the 8-bit and the fp16 rows. ----
     const int quarter = warp & 3;
-    // A: the weight row of this lane.  Gate/up stages hold 64 gate rows, then
-    // 64 up rows; a warp takes 16 of each, so that gate and up of a channel
-    // meet in lanes i and i + 16 of one epilogue warp.
-    // B: the rows lane, lane + 32, ...; two of the eight 16-byte chunks of a
-    // row per warp.  Chunk c of row r sits at chunk c ^ (r & 7) (128-byte
-    // swizzle) in the 8-bit and the fp16 rows.
+    const uint32_t src0 = (sB8 + lane * 128 + ((lane & 7) << 4)) ^ (quarter << 5);
+    const uint32_t dst0 = (sB16 + (quarter >> 1) * (kB16 / 2) + lane * 128 + ((lane & 7) << 4)) ^
+                          ((quarter & 1) << 6);
+    int s = 0, b = 0;
+    uint32_t ph = 0, bph = 0;
+    bool run = true;
+    for (int t = t0; run && t < total; t += dt) {
+      const int nb = i8_tile<kSwiglu>(t, p, prefix, offs, rank).n / 2;
+      for (int k = 0; k < stages; ++k) {
+        run = __all_sync(0xffffffffu, mbar_wait_quiet(q_full(s), ph, abort_flag, p.status));
+        if (!run) break;
+        uint4 v[kRowTile / 64][2];
+        const uint32_t src = src0 + s * kB8;
+#pragma unroll
+        for (int i = 0; i < kRowTile / 64; ++i) {
+          if (lane + 32 * i < nb) {
+            v[i][0] = ld_shared_v4(src + i * 4096);
+            v[i][1] = ld_shared_v4((src ^ 16u) + i * 4096);
+          }
+        }
+        run = __all_sync(0xffffffffu, mbar_wait_quiet(c_empty(b), bph ^ 1u, abort_flag, p.status));
+        if (!run) break;
+        // 16 bytes become two chunks; this warp's two make four
+        const uint32_t dst = dst0 + b * kB16;
+#pragma unroll
+        for (int i = 0; i < kRowTile / 64; ++i) {
+          if (lane + 32 * i < nb) {
+            uint32_t f[16];
+            expand16(v[i][0], f);
+            expand16(v[i][1], f + 8);
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              st_shared_v4((dst ^ (j << 4)) + i * 4096, f[4 * j], f[4 * j + 1], f[4 * j + 2], f[4 * j + 3]);
+          }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive_cluster(mapa_shared(c_full(b), 0));
+          mbar_arrive(q_empty(s));
+        }
+        b ^= 1;
+        if (b == 0) bph ^= 1u;
+        if (++s == kStages) s = 0, ph ^= 1u;
+      }
+    }
+  } else if (warp >= kAWarp) {
+    // ---- expand A: the two groups take alternate stages ----
+    const int grp = (warp - kAWarp) >> 2;
+    const int quarter = warp & 3;
+    // The weight row of this lane.  Gate/up stages hold 64 gate rows, then 64
+    // up rows; a warp takes 16 of each, so that gate and up of a channel meet
+    // in lanes i and i + 16 of one epilogue warp.
     const int arow = kSwiglu ? (lane < 16 ? quarter * 16 + lane : 48 + quarter * 16 + lane)
                              : quarter * 32 + lane;
     const uint32_t a_src = sA8 + arow * 128 + ((arow & 7) << 4);
     const uint32_t a_dst = tmem + kACol + grp * 64 + ((uint32_t)(quarter * 32) << 16);
-    const uint32_t b_src = sB8 + lane * 128 + ((lane & 7) << 4);
-    const uint32_t b_dst = sB16 + grp * kB16 + (quarter >> 1) * (kB16 / 2) + lane * 128 + ((lane & 7) << 4);
     const uint32_t full_of_leader = mapa_shared(c_full(grp), 0);
     int s = grp, n0 = 0;  // ring stage; stages before this tile
     uint32_t ph = 0, bph = 0;
     bool run = true;
     for (int t = t0; run && t < total; t += dt) {
-      const int nb = is_a ? 0 : i8_tile<kSwiglu>(t, p, prefix, offs, rank).n / 2;
       for (int k = (n0 ^ grp) & 1; k < stages; k += 2) {
         run = __all_sync(0xffffffffu, mbar_wait_quiet(q_full(s), ph, abort_flag, p.status));
         if (!run) break;
-        if (is_a) {
-          uint4 v[4];
-          uint32_t r[32];
-          const uint32_t src = a_src + s * kA8;
+        uint4 v[4];
+        uint32_t r[32];
+        const uint32_t src = a_src + s * kA8;
 #pragma unroll
-          for (int j = 0; j < 4; ++j) v[j] = ld_shared_v4(src ^ (j << 4));
+        for (int j = 0; j < 4; ++j) v[j] = ld_shared_v4(src ^ (j << 4));
 #pragma unroll
-          for (int j = 0; j < 4; ++j) expand16(v[j], r + 8 * j);
+        for (int j = 0; j < 4; ++j) expand16(v[j], r + 8 * j);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) v[j] = ld_shared_v4(src ^ ((j + 4) << 4));
-          run = __all_sync(0xffffffffu, mbar_wait_quiet(c_empty(grp), bph ^ 1u, abort_flag, p.status));
-          if (!run) break;
-          tc_fence_after();
-          tmem_st_32x32b_x32(a_dst, r);
+        for (int j = 0; j < 4; ++j) v[j] = ld_shared_v4(src ^ ((j + 4) << 4));
+        run = __all_sync(0xffffffffu, mbar_wait_quiet(c_empty(grp), bph ^ 1u, abort_flag, p.status));
+        if (!run) break;
+        tc_fence_after();
+        tmem_st_32x32b_x32(a_dst, r);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) expand16(v[j], r + 8 * j);
-          tmem_st_32x32b_x32(a_dst + 32, r);
-          tmem_st_wait();
-          tc_fence_before();
-        } else {
-          uint4 v[kRowTile / 64][2];
-          const uint32_t src = b_src + s * kB8;
-#pragma unroll
-          for (int i = 0; i < kRowTile / 64; ++i) {
-            if (lane + 32 * i < nb) {
-              v[i][0] = ld_shared_v4((src ^ (2 * quarter << 4)) + i * 4096);
-              v[i][1] = ld_shared_v4((src ^ ((2 * quarter + 1) << 4)) + i * 4096);
-            }
-          }
-          run = __all_sync(0xffffffffu, mbar_wait_quiet(c_empty(grp), bph ^ 1u, abort_flag, p.status));
-          if (!run) break;
-          // 16 bytes become two chunks; this warp's two make four
-          const uint32_t dst = b_dst ^ ((quarter & 1) << 6);
-#pragma unroll
-          for (int i = 0; i < kRowTile / 64; ++i) {
-            if (lane + 32 * i < nb) {
-              uint32_t f[16];
-              expand16(v[i][0], f);
-              expand16(v[i][1], f + 8);
-#pragma unroll
-              for (int j = 0; j < 4; ++j)
-                st_shared_v4((dst ^ (j << 4)) + i * 4096, f[4 * j], f[4 * j + 1], f[4 * j + 2], f[4 * j + 3]);
-            }
-          }
-          fence_proxy_async_smem();
-        }
+        for (int j = 0; j < 4; ++j) expand16(v[j], r + 8 * j);
+        tmem_st_32x32b_x32(a_dst + 32, r);
+        tmem_st_wait();
+        tc_fence_before();
         __syncwarp();
         if (lane == 0) {
           mbar_arrive_cluster(full_of_leader);

@@ -22,7 +22,7 @@
 //
 // Warps: 1 TMA producer, 1 MMA issuer (in the leading CTA), 4 epilogue (one
 // per tensor-memory lane quarter), 8 expand A (two groups of 4 that take
-// alternate 128-deep stages, each with an A buffer of its own), 4 expand B.
+// alternate 128-deep stages, each with an A buffer of its own), 8 expand B.
 // Tensor memory: two 192-column accumulators and two 64-column A buffers.
 //
 // The expanding warps of both CTAs arrive on the leader's barrier with the
@@ -52,7 +52,7 @@ constexpr uint32_t kB8 = kRowTile / 2 * 128;   // 8-bit B bytes of a stage
 constexpr uint32_t kB16 = kRowTile / 2 * 256;  // fp16 B bytes of a stage, two 64-deep halves
 constexpr uint32_t kAccCols = kRowTile, kACol = 2 * kAccCols;
 constexpr int kTmaWarp = 0, kMmaWarp = 1, kAWarp = 6, kBWarp = 14;  // 2-5: epilogue
-constexpr int kThreadsI8 = 18 * 32;
+constexpr int kThreadsI8 = 22 * 32;
 constexpr int kBars = 2 * kStages + 2 * kBufs + 4 + 1;
 constexpr uint32_t kStageWarp = 32 * 128 + kRowTile * 4;  // epilogue staging of a warp
 constexpr uint32_t kStage = kStages * (kA8 + kB8) + kBufs * kB16;
@@ -148,15 +148,15 @@ gmm_i8_kernel(const __grid_constant__ CUtensorMap mapW0, const __grid_constant__
   int32_t* prefix = reinterpret_cast<int32_t*>(g + kTable);
   int32_t* offs = prefix + (kMaxExperts + 1);
   int32_t* scratch = offs + (kMaxExperts + 1);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = (int)uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
       mbar_init(q_full(s), 1);
-      mbar_init(q_empty(s), 8);  // an A group and the B warps
+      mbar_init(q_empty(s), 12);  // an A group and the B warps
     }
     for (int b = 0; b < kBufs; ++b) {
-      mbar_init(c_full(b), 16);  // the leader's: an A group and the B warps of both CTAs
+      mbar_init(c_full(b), 24);  // the leader's: an A group and the B warps of both CTAs
       mbar_init(c_empty(b), 1);
     }
     for (int a = 0; a < 2; ++a) {
@@ -221,51 +221,50 @@ gmm_i8_kernel(const __grid_constant__ CUtensorMap mapW0, const __grid_constant__
       }
     }
   } else if (warp == kMmaWarp) {
-    if (lane == 0 && rank == 0) {
-      const uint64_t bdesc0 = desc_sw128(sB16, 16, 1024);
+    if (rank == 0) {  // the whole warp, one lane elected for each MMA
+      const uint64_t bdesc0 = desc_sw128(uniform(sB16), 16, 1024);
+      const uint32_t tm = uniform(tmem);
       int b = 0, it = 0;
       uint32_t ph = 0;
       bool run = true;
       for (int t = t0; run && t < total; t += dt, ++it) {
-        const I8Tile x = i8_tile<kSwiglu>(t, p, prefix, offs, rank);
-        const uint32_t idesc = idesc_f16_f32(256, x.n);
+        const uint32_t idesc = uniform(idesc_f16_f32(256, i8_tile<kSwiglu>(t, p, prefix, offs, rank).n));
         const int acc = it & 1;
-        if (!mbar_wait<true>(t_empty(acc), ((it >> 1) & 1) ^ 1u, abort_flag, p.status)) break;
+        run = __all_sync(0xffffffffu, mbar_wait<true>(t_empty(acc), ((it >> 1) & 1) ^ 1u, abort_flag, p.status));
+        if (!run) break;
         tc_fence_after();
-        const uint32_t d = tmem + acc * kAccCols;
+        const uint32_t d = tm + acc * kAccCols;
         uint32_t accum = 0u;
         for (int k = 0; k < stages; ++k) {
-          if (!mbar_wait_quiet(c_full(b), ph, abort_flag, p.status)) {
-            run = false;
-            break;
-          }
+          run = __all_sync(0xffffffffu, mbar_wait_quiet(c_full(b), ph, abort_flag, p.status));
+          if (!run) break;
           tc_fence_after();
           const uint64_t bd = bdesc0 + (uint64_t)b * (kB16 >> 4);
-          const uint32_t a = tmem + kACol + b * 64;
+          const uint32_t a = tm + kACol + b * 64;
           // (past the end of Kd both operands are zeros)
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk) {
-            umma_f16_pair_ta(d, a + kk * 8, bd + (kk >> 2) * (kB16 >> 5) + (kk & 3) * 2, idesc, accum);
+            umma_f16_ta_warp<true>(d, a + kk * 8, bd + (kk >> 2) * (kB16 >> 5) + (kk & 3) * 2, idesc, accum);
             accum = 1u;
           }
-          umma_commit_pair(c_empty(b), 3);
+          umma_commit_pair_warp(c_empty(b), 3);
           b ^= 1;
           if (b == 0) ph ^= 1u;
         }
         if (!run) break;
-        umma_commit_pair(t_full(acc), 3);
+        umma_commit_pair_warp(t_full(acc), 3);
       }
-      umma_commit_pair(drain, 1);
+      umma_commit_pair_warp(drain, 1);
       mbar_wait_quiet(drain, 0, abort_flag, p.status, false);
+      __syncwarp();
     }
   } else if (warp >= kBWarp) {
-    // ---- expand B: the rows lane, lane + 32, ...; two of the eight 16-byte
+    // ---- expand B: the rows lane, lane + 32, ...; one of the eight 16-byte
     // chunks of a row per warp.  Chunk c of row r sits at chunk c ^ (r & 7)
     // (128-byte swizzle) in the 8-bit and the fp16 rows. ----
-    const int quarter = warp & 3;
-    const uint32_t src0 = (sB8 + lane * 128 + ((lane & 7) << 4)) ^ (quarter << 5);
-    const uint32_t dst0 = (sB16 + (quarter >> 1) * (kB16 / 2) + lane * 128 + ((lane & 7) << 4)) ^
-                          ((quarter & 1) << 6);
+    const int bw = warp - kBWarp;
+    const uint32_t src0 = (sB8 + lane * 128 + ((lane & 7) << 4)) ^ (bw << 4);
+    const uint32_t dst0 = (sB16 + (bw >> 2) * (kB16 / 2) + lane * 128 + ((lane & 7) << 4)) ^ ((bw & 3) << 5);
     int s = 0, b = 0;
     uint32_t ph = 0, bph = 0;
     bool run = true;
@@ -274,28 +273,21 @@ gmm_i8_kernel(const __grid_constant__ CUtensorMap mapW0, const __grid_constant__
       for (int k = 0; k < stages; ++k) {
         run = __all_sync(0xffffffffu, mbar_wait_quiet(q_full(s), ph, abort_flag, p.status));
         if (!run) break;
-        uint4 v[kRowTile / 64][2];
+        uint4 v[kRowTile / 64];
         const uint32_t src = src0 + s * kB8;
 #pragma unroll
-        for (int i = 0; i < kRowTile / 64; ++i) {
-          if (lane + 32 * i < nb) {
-            v[i][0] = ld_shared_v4(src + i * 4096);
-            v[i][1] = ld_shared_v4((src ^ 16u) + i * 4096);
-          }
-        }
+        for (int i = 0; i < kRowTile / 64; ++i)
+          if (lane + 32 * i < nb) v[i] = ld_shared_v4(src + i * 4096);
         run = __all_sync(0xffffffffu, mbar_wait_quiet(c_empty(b), bph ^ 1u, abort_flag, p.status));
         if (!run) break;
-        // 16 bytes become two chunks; this warp's two make four
-        const uint32_t dst = dst0 + b * kB16;
+        const uint32_t dst = dst0 + b * kB16;  // 16 bytes become two chunks
 #pragma unroll
         for (int i = 0; i < kRowTile / 64; ++i) {
           if (lane + 32 * i < nb) {
-            uint32_t f[16];
-            expand16(v[i][0], f);
-            expand16(v[i][1], f + 8);
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-              st_shared_v4((dst ^ (j << 4)) + i * 4096, f[4 * j], f[4 * j + 1], f[4 * j + 2], f[4 * j + 3]);
+            uint32_t f[8];
+            expand16(v[i], f);
+            st_shared_v4(dst + i * 4096, f[0], f[1], f[2], f[3]);
+            st_shared_v4((dst ^ 16u) + i * 4096, f[4], f[5], f[6], f[7]);
           }
         }
         fence_proxy_async_smem();

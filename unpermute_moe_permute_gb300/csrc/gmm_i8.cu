@@ -21,9 +21,9 @@
 //     the 384 cycles of its MMAs at 192 rows.
 //
 // Warps: 1 TMA producer, 1 MMA issuer (in the leading CTA), 4 epilogue (one
-// per tensor-memory lane quarter), 8 expand A (two groups of 4 that take
-// alternate 128-deep stages, each with an A buffer of its own), 8 expand B.
-// Tensor memory: two 192-column accumulators and two 64-column A buffers.
+// per tensor-memory lane quarter), two groups of 4 + 3 that expand A and B of
+// alternate 128-deep stages, 32 operand rows a warp.  Tensor memory: two
+// 192-column accumulators and two 64-column A buffers.
 //
 // The expanding warps of both CTAs arrive on the leader's barrier with the
 // default (CTA-scope) release: what they wrote, tensor memory and shared
@@ -52,7 +52,7 @@ constexpr uint32_t kB8 = kRowTile / 2 * 128;   // 8-bit B bytes of a stage
 constexpr uint32_t kB16 = kRowTile / 2 * 256;  // fp16 B bytes of a stage, two 64-deep halves
 constexpr uint32_t kAccCols = kRowTile, kACol = 2 * kAccCols;
 constexpr int kTmaWarp = 0, kMmaWarp = 1, kAWarp = 6, kBWarp = 14;  // 2-5: epilogue
-constexpr int kThreadsI8 = 22 * 32;
+constexpr int kThreadsI8 = 20 * 32;
 constexpr int kBars = 2 * kStages + 2 * kBufs + 4 + 1;
 constexpr uint32_t kStageWarp = 32 * 128 + kRowTile * 4;  // epilogue staging of a warp
 constexpr uint32_t kStage = kStages * (kA8 + kB8) + kBufs * kB16;
@@ -153,10 +153,10 @@ gmm_i8_kernel(const __grid_constant__ CUtensorMap mapW0, const __grid_constant__
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
       mbar_init(q_full(s), 1);
-      mbar_init(q_empty(s), 12);  // an A group and the B warps
+      mbar_init(q_empty(s), 7);  // an expanding group
     }
     for (int b = 0; b < kBufs; ++b) {
-      mbar_init(c_full(b), 24);  // the leader's: an A group and the B warps of both CTAs
+      mbar_init(c_full(b), 14);  // the leader's: an expanding group of both CTAs
       mbar_init(c_empty(b), 1);
     }
     for (int a = 0; a < 2; ++a) {
@@ -199,7 +199,7 @@ gmm_i8_kernel(const __grid_constant__ CUtensorMap mapW0, const __grid_constant__
         const int nb = x.n / 2, r0 = x.row0 + rank * nb;
         const uint32_t tx = kA8 + (uint32_t)nb * 128u;
         for (int k = 0; k < stages; ++k) {
-          if (!mbar_wait_quiet(q_empty(s), ph ^ 1u, abort_flag, p.status)) {
+          if (!mbar_wait(q_empty(s), ph ^ 1u, abort_flag, p.status)) {
             run = false;
             break;
           }
@@ -217,7 +217,7 @@ gmm_i8_kernel(const __grid_constant__ CUtensorMap mapW0, const __grid_constant__
       // every copy has landed before the CTA may exit
       for (int st = 0; st < kStages && st < n; ++st) {
         const int last = st + (n - 1 - st) / kStages * kStages;
-        mbar_wait_quiet(q_full(st), (uint32_t)(last / kStages) & 1u, abort_flag, p.status, false);
+        mbar_wait(q_full(st), (uint32_t)(last / kStages) & 1u, abort_flag, p.status, false);
       }
     }
   } else if (warp == kMmaWarp) {
@@ -236,7 +236,7 @@ gmm_i8_kernel(const __grid_constant__ CUtensorMap mapW0, const __grid_constant__
         const uint32_t d = tm + acc * kAccCols;
         uint32_t accum = 0u;
         for (int k = 0; k < stages; ++k) {
-          run = __all_sync(0xffffffffu, mbar_wait_quiet(c_full(b), ph, abort_flag, p.status));
+          run = mbar_wait_warp(c_full(b), ph, abort_flag, p.status);
           if (!run) break;
           tc_fence_after();
           const uint64_t bd = bdesc0 + (uint64_t)b * (kB16 >> 4);
@@ -255,94 +255,71 @@ gmm_i8_kernel(const __grid_constant__ CUtensorMap mapW0, const __grid_constant__
         umma_commit_pair_warp(t_full(acc), 3);
       }
       umma_commit_pair_warp(drain, 1);
-      mbar_wait_quiet(drain, 0, abort_flag, p.status, false);
-      __syncwarp();
-    }
-  } else if (warp >= kBWarp) {
-    // ---- expand B: the rows lane, lane + 32, ...; one of the eight 16-byte
-    // chunks of a row per warp.  Chunk c of row r sits at chunk c ^ (r & 7)
-    // (128-byte swizzle) in the 8-bit and the fp16 rows. ----
-    const int bw = warp - kBWarp;
-    const uint32_t src0 = (sB8 + lane * 128 + ((lane & 7) << 4)) ^ (bw << 4);
-    const uint32_t dst0 = (sB16 + (bw >> 2) * (kB16 / 2) + lane * 128 + ((lane & 7) << 4)) ^ ((bw & 3) << 5);
-    int s = 0, b = 0;
-    uint32_t ph = 0, bph = 0;
-    bool run = true;
-    for (int t = t0; run && t < total; t += dt) {
-      const int nb = i8_tile<kSwiglu>(t, p, prefix, offs, rank).n / 2;
-      for (int k = 0; k < stages; ++k) {
-        run = __all_sync(0xffffffffu, mbar_wait_quiet(q_full(s), ph, abort_flag, p.status));
-        if (!run) break;
-        uint4 v[kRowTile / 64];
-        const uint32_t src = src0 + s * kB8;
-#pragma unroll
-        for (int i = 0; i < kRowTile / 64; ++i)
-          if (lane + 32 * i < nb) v[i] = ld_shared_v4(src + i * 4096);
-        run = __all_sync(0xffffffffu, mbar_wait_quiet(c_empty(b), bph ^ 1u, abort_flag, p.status));
-        if (!run) break;
-        const uint32_t dst = dst0 + b * kB16;  // 16 bytes become two chunks
-#pragma unroll
-        for (int i = 0; i < kRowTile / 64; ++i) {
-          if (lane + 32 * i < nb) {
-            uint32_t f[8];
-            expand16(v[i], f);
-            st_shared_v4(dst + i * 4096, f[0], f[1], f[2], f[3]);
-            st_shared_v4((dst ^ 16u) + i * 4096, f[4], f[5], f[6], f[7]);
-          }
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive_cluster(mapa_shared(c_full(b), 0));
-          mbar_arrive(q_empty(s));
-        }
-        b ^= 1;
-        if (b == 0) bph ^= 1u;
-        if (++s == kStages) s = 0, ph ^= 1u;
-      }
+      mbar_wait_warp(drain, 0, abort_flag, p.status, false);
     }
   } else if (warp >= kAWarp) {
-    // ---- expand A: the two groups take alternate stages ----
-    const int grp = (warp - kAWarp) >> 2;
-    const int quarter = warp & 3;
-    // The weight row of this lane.  Gate/up stages hold 64 gate rows, then 64
-    // up rows; a warp takes 16 of each, so that gate and up of a channel meet
-    // in lanes i and i + 16 of one epilogue warp.
-    const int arow = kSwiglu ? (lane < 16 ? quarter * 16 + lane : 48 + quarter * 16 + lane)
-                             : quarter * 32 + lane;
-    const uint32_t a_src = sA8 + arow * 128 + ((arow & 7) << 4);
+    // ---- expand: a lane takes one 128-byte row of the stage ----
+    const bool is_a = warp < kBWarp;
+    const int grp = is_a ? (warp - kAWarp) >> 2 : (warp - kBWarp) / 3;
+    const int quarter = warp & 3;                              // A: tensor-memory lanes
+    const int rg = is_a ? 0 : (warp - kBWarp) - 3 * grp;        // B: rows 32 rg + lane
+    // A row of this lane: gate/up stages hold 64 gate rows, then 64 up rows; a
+    // warp takes 16 of each, so that gate and up of a channel meet in lanes i
+    // and i + 16 of one epilogue warp.
+    const int row = is_a ? (kSwiglu ? (lane < 16 ? quarter * 16 + lane : 48 + quarter * 16 + lane)
+                                    : quarter * 32 + lane)
+                         : rg * 32 + lane;
+    // Chunk c of row r sits at chunk c ^ (r & 7) (128-byte swizzle), in the
+    // 8-bit rows and in the fp16 rows, where it has become chunks 2c, 2c + 1
+    // of two 64-deep halves.
+    const uint32_t src0 = (is_a ? sA8 : sB8) + row * 128 + ((row & 7) << 4);
     const uint32_t a_dst = tmem + kACol + grp * 64 + ((uint32_t)(quarter * 32) << 16);
+    const uint32_t b_dst = sB16 + grp * kB16 + row * 128 + ((row & 7) << 4);
+    const uint32_t step = is_a ? kA8 : kB8;
     const uint32_t full_of_leader = mapa_shared(c_full(grp), 0);
     int s = grp, n0 = 0;  // ring stage; stages before this tile
     uint32_t ph = 0, bph = 0;
     bool run = true;
     for (int t = t0; run && t < total; t += dt) {
+      // B rows past the tile's own are not expanded (the MMA does not read them)
+      const bool any = is_a || rg * 32 < i8_tile<kSwiglu>(t, p, prefix, offs, rank).n / 2;
       for (int k = (n0 ^ grp) & 1; k < stages; k += 2) {
-        run = __all_sync(0xffffffffu, mbar_wait_quiet(q_full(s), ph, abort_flag, p.status));
+        run = mbar_wait_warp(q_full(s), ph, abort_flag, p.status);
         if (!run) break;
         uint4 v[4];
         uint32_t r[32];
-        const uint32_t src = a_src + s * kA8;
+        const uint32_t src = src0 + s * step;
+        if (any) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) v[j] = ld_shared_v4(src ^ (j << 4));
+          for (int j = 0; j < 4; ++j) v[j] = ld_shared_v4(src ^ (j << 4));
 #pragma unroll
-        for (int j = 0; j < 4; ++j) expand16(v[j], r + 8 * j);
+          for (int j = 0; j < 4; ++j) expand16(v[j], r + 8 * j);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) v[j] = ld_shared_v4(src ^ ((j + 4) << 4));
-        run = __all_sync(0xffffffffu, mbar_wait_quiet(c_empty(grp), bph ^ 1u, abort_flag, p.status));
-        if (!run) break;
-        tc_fence_after();
-        tmem_st_32x32b_x32(a_dst, r);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) expand16(v[j], r + 8 * j);
-        tmem_st_32x32b_x32(a_dst + 32, r);
-        tmem_st_wait();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive_cluster(full_of_leader);
-          mbar_arrive(q_empty(s));
+          for (int j = 0; j < 4; ++j) v[j] = ld_shared_v4(src ^ ((j + 4) << 4));
         }
+        run = mbar_wait_warp(c_empty(grp), bph ^ 1u, abort_flag, p.status);
+        if (!run) break;
+        if (is_a) {
+          tc_fence_after();
+          tmem_st_32x32b_x32(a_dst, r);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) expand16(v[j], r + 8 * j);
+          tmem_st_32x32b_x32(a_dst + 32, r);
+          tmem_st_wait();
+          tc_fence_before();
+        } else if (any) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            st_shared_v4(b_dst ^ (j << 4), r[4 * j], r[4 * j + 1], r[4 * j + 2], r[4 * j + 3]);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) expand16(v[j], r + 8 * j);
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            st_shared_v4((b_dst ^ (j << 4)) + kB16 / 2, r[4 * j], r[4 * j + 1], r[4 * j + 2], r[4 * j + 3]);
+          fence_proxy_async_smem();
+        }
+        mbar_arrive_cluster_warp(full_of_leader);
+        mbar_arrive_warp(q_empty(s));
         bph ^= 1u;
         s += 2;
         if (s >= kStages) s -= kStages, ph ^= 1u;
@@ -372,7 +349,7 @@ gmm_i8_kernel(const __grid_constant__ CUtensorMap mapW0, const __grid_constant__
       const int rows = x.hi - x.row0;
       for (int c = lane; c < kRowTile; c += 32) scale[c] = c < rows ? p.rs[x.row0 + c] : 0.f;
       __syncwarp();
-      if (!__all_sync(0xffffffffu, mbar_wait_quiet(t_full(acc), (it >> 1) & 1, abort_flag, p.status))) break;
+      if (!mbar_wait_warp(t_full(acc), (it >> 1) & 1, abort_flag, p.status)) break;
       tc_fence_after();
       const uint32_t d = tmem + acc * kAccCols + ((uint32_t)(quarter * 32) << 16);
       // 16-byte chunk of the staging rows that this lane copies out, and the
@@ -396,7 +373,7 @@ gmm_i8_kernel(const __grid_constant__ CUtensorMap mapW0, const __grid_constant__
             const float y0 = __uint_as_float(v[j]) * cs * r.x, y1 = __uint_as_float(v[j + 1]) * cs * r.y;
             const float got = __shfl_xor_sync(0xffffffffu, up ? y0 : y1, 16);
             const float gate = up ? got : y0, u = up ? y1 : got;
-            st_shared_b16(st + j * kRowB, gate / (1.f + expf(-gate)) * u);
+            st_shared_b16(st + j * kRowB, __fdividef(gate, 1.f + __expf(-gate)) * u);
           }
         } else {
           const uint32_t st = stage_u + lane * (uint32_t)sizeof(O);
@@ -423,8 +400,7 @@ gmm_i8_kernel(const __grid_constant__ CUtensorMap mapW0, const __grid_constant__
         __syncwarp();
       }
       tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(mapa_shared(t_empty(acc), 0));
+      mbar_arrive_cluster_warp(mapa_shared(t_empty(acc), 0));
     }
   }
   tc_fence_before();

@@ -94,15 +94,15 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatil
   }
 }
 
-// The same wait, each attempt suspended by the hardware for up to kSuspendNs:
-// for kernels whose waiting warps share their schedulers with busy ones (an
-// attempt without the hint comes back after a few hundred cycles, and its
-// retry costs issue slots).
+// The same wait by a whole warp (uniform result), each attempt suspended by
+// the hardware for up to kSuspendNs: for kernels whose waiting warps share
+// their schedulers with busy ones.  Few instructions when the phase is
+// already complete.
 constexpr uint32_t kSuspendNs = 20000;
 
-__device__ __forceinline__ bool mbar_wait_quiet(uint32_t bar, uint32_t parity,
-                                                volatile int* abort_flag, int32_t* status,
-                                                bool honor_abort = true) {
+__device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity,
+                                               volatile int* abort_flag, int32_t* status,
+                                               bool honor_abort = true) {
   unsigned long long t0 = 0;
   for (uint32_t i = 0;; ++i) {
     uint32_t ok;
@@ -113,19 +113,34 @@ __device__ __forceinline__ bool mbar_wait_quiet(uint32_t bar, uint32_t parity,
         : "=r"(ok)
         : "r"(bar), "r"(parity), "r"(kSuspendNs)
         : "memory");
-    if (ok) return true;
+    if (__all_sync(0xffffffffu, ok != 0)) return true;
     if ((i & 15u) == 15u) {
-      if (honor_abort && *abort_flag) return false;
+      if (__any_sync(0xffffffffu, honor_abort && *abort_flag)) return false;
       const unsigned long long now = globaltimer();
-      if (t0 == 0) {
-        t0 = now;
-      } else if (now - t0 > kWaitTimeoutNs) {
+      if (t0 == 0) t0 = now;
+      if (__any_sync(0xffffffffu, now - t0 > kWaitTimeoutNs)) {
         *abort_flag = 1;
         set_status(status, MOE_ERR_TIMEOUT);
         return false;
       }
     }
   }
+}
+
+// One arrival of the warp, after all its lanes' work so far.
+__device__ __forceinline__ void mbar_arrive_warp(uint32_t bar) {
+  __syncwarp();
+  asm volatile(
+      "{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\t"
+      "@q mbarrier.arrive.shared::cta.b64 _, [%0];\n\t}" ::"r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void mbar_arrive_cluster_warp(uint32_t cluster_addr) {
+  __syncwarp();
+  asm volatile(
+      "{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\t"
+      "@q mbarrier.arrive.shared::cluster.b64 _, [%0];\n\t}" ::"r"(cluster_addr)
+      : "memory");
 }
 
 // ---- TMA --------------------------------------------------------------------

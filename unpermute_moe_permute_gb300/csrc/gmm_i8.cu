@@ -20,7 +20,7 @@
 //     14 KB (TMA) + 14 KB (read) + 12 KB (fp16 rows) + 12 KB (MMA reads) in
 //     the 384 cycles of its MMAs at 192 rows.
 //
-// Warps: 1 TMA producer, 1 MMA issuer (in the leading CTA), 4 epilogue (one
+// Warps: 1 TMA producer, 1 MMA issuer (in the leading CTA), 8 epilogue (two
 // per tensor-memory lane quarter), two groups of 4 + 3 that expand A and B of
 // alternate 128-deep stages, 32 operand rows a warp.  Tensor memory: two
 // 192-column accumulators and two 64-column A buffers.
@@ -51,12 +51,12 @@ constexpr uint32_t kA8 = 128 * 128;            // 8-bit A bytes of a stage
 constexpr uint32_t kB8 = kRowTile / 2 * 128;   // 8-bit B bytes of a stage
 constexpr uint32_t kB16 = kRowTile / 2 * 256;  // fp16 B bytes of a stage, two 64-deep halves
 constexpr uint32_t kAccCols = kRowTile, kACol = 2 * kAccCols;
-constexpr int kTmaWarp = 0, kMmaWarp = 1, kAWarp = 6, kBWarp = 14;  // 2-5: epilogue
-constexpr int kThreadsI8 = 20 * 32;
+constexpr int kTmaWarp = 0, kMmaWarp = 1, kEpiWarp = 2, kAWarp = 10, kBWarp = 18;
+constexpr int kThreadsI8 = 24 * 32;
 constexpr int kBars = 2 * kStages + 2 * kBufs + 4 + 1;
-constexpr uint32_t kStageWarp = 32 * 128 + kRowTile * 4;  // epilogue staging of a warp
+constexpr uint32_t kStageWarp = 2048 + 128;  // epilogue staging of a warp: rows, then row scales
 constexpr uint32_t kStage = kStages * (kA8 + kB8) + kBufs * kB16;
-constexpr uint32_t kCtrl = kStage + 4 * kStageWarp;
+constexpr uint32_t kCtrl = kStage + 8 * kStageWarp;
 constexpr uint32_t kHolder = kCtrl + 8 * kBars;
 constexpr uint32_t kTable = kHolder + 8;       // prefix, offsets, scan scratch
 constexpr uint32_t kSmem = kTable + 2 * (kMaxExperts + 1) * 4 + 32 * 4 + 1024;
@@ -161,7 +161,7 @@ gmm_i8_kernel(const __grid_constant__ CUtensorMap mapW0, const __grid_constant__
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(t_full(a), 1);
-      mbar_init(t_empty(a), 8);  // 4 epilogue warps of both CTAs
+      mbar_init(t_empty(a), 16);  // 8 epilogue warps of both CTAs
     }
     mbar_init(drain, 1);
     *abort_flag = 0;
@@ -328,27 +328,25 @@ gmm_i8_kernel(const __grid_constant__ CUtensorMap mapW0, const __grid_constant__
     }
   } else {
     // ---- epilogue: lanes are channels, accumulator columns are rows ----
-    // Pieces of 32 columns are scaled, turned through this warp's staging
-    // rows (one row of 32 channels, or 16 for gate/up, per column) and
-    // written in 16-byte chunks.
-    const int quarter = warp & 3;
-    constexpr int kCh = kSwiglu ? 16 : 32;                      // channels per warp
+    // The two warps of a quarter take alternate pieces of 32 columns.  A piece
+    // is scaled, turned through the warp's staging rows (one row of 32
+    // channels, or 16 for gate/up, per column) and written in 16-byte chunks.
+    const int quarter = warp & 3, part = (warp - kEpiWarp) >> 2;
+    constexpr int kCh = kSwiglu ? 16 : 32;                        // channels per warp
     constexpr int kRowB = kCh * (int)sizeof(O), kV = kRowB / 16;  // staging row, its chunks
-    const uint32_t stage_u = base + kStage + (uint32_t)quarter * kStageWarp;
-    uint8_t* stage = g + kStage + quarter * kStageWarp;
-    float* scale = reinterpret_cast<float*>(stage + 32 * 128);  // the tile's row scales
+    constexpr int kPass = kRowB > 64 ? 16 : 32;                   // columns staged at a time
+    const uint32_t stage_u = base + kStage + (uint32_t)(warp - kEpiWarp) * kStageWarp;
+    float* scale = reinterpret_cast<float*>(g + kStage + (warp - kEpiWarp) * kStageWarp + 2048);
     const int ch_l = kSwiglu ? quarter * 16 + (lane & 15) : quarter * 32 + lane;
     int it = 0;
     for (int t = t0; t < total; t += dt, ++it) {
       const I8Tile x = i8_tile<kSwiglu>(t, p, prefix, offs, rank);
       const int acc = it & 1;
       const int ch = x.ch0 + ch_l;
-      const bool in = ch < p.Nout;
-      const float cs = !in ? 0.f
-                           : ((kSwiglu && lane >= 16) ? p.s1 : p.s0)[(size_t)x.e * p.Nout + ch];
+      const float cs = ch >= p.Nout ? 0.f
+                                    : ((kSwiglu && lane >= 16) ? p.s1 : p.s0)[(size_t)x.e * p.Nout + ch];
       const int rows = x.hi - x.row0;
-      for (int c = lane; c < kRowTile; c += 32) scale[c] = c < rows ? p.rs[x.row0 + c] : 0.f;
-      __syncwarp();
+      float rs = part * 32 + lane < rows ? p.rs[x.row0 + part * 32 + lane] : 0.f;
       if (!mbar_wait_warp(t_full(acc), (it >> 1) & 1, abort_flag, p.status)) break;
       tc_fence_after();
       const uint32_t d = tmem + acc * kAccCols + ((uint32_t)(quarter * 32) << 16);
@@ -356,48 +354,54 @@ gmm_i8_kernel(const __grid_constant__ CUtensorMap mapW0, const __grid_constant__
       // channels it holds; Nout is a multiple of 16, so a chunk is whole
       const int wr = lane / kV, wc = lane % kV;
       const int wch = x.ch0 + quarter * kCh + wc * (16 / (int)sizeof(O));
-      uint8_t* dst = static_cast<uint8_t*>(p.out) + ((size_t)(x.row0 + wr) * p.Nout + wch) * sizeof(O);
-      const size_t dst_step = (size_t)(32 / kV) * p.Nout * sizeof(O);
-      for (int c0 = 0; c0 < rows; c0 += 32) {
+      const size_t ld = (size_t)p.Nout * sizeof(O);
+      uint8_t* dst = static_cast<uint8_t*>(p.out) + (size_t)(x.row0 + wr) * ld + (size_t)wch * sizeof(O);
+      for (int c0 = part * 32; c0 < rows; c0 += 64) {
         uint32_t v[32];
         tmem_ld_32x32b_x32(d + c0, v);
+        scale[lane] = rs;
+        rs = c0 + 64 + lane < rows ? p.rs[x.row0 + c0 + 64 + lane] : 0.f;
+        __syncwarp();
         tmem_ld_wait();
-        if constexpr (kSwiglu) {
-          // lanes 0-15 hold gate, 16-31 up of the same channels: the lower
-          // half takes the even rows, the upper half the odd ones
-          const bool up = lane >= 16;
-          const uint32_t st = stage_u + (lane & 15) * 2 + (up ? kRowB : 0);
 #pragma unroll
-          for (int j = 0; j < 32; j += 2) {
-            const float2 r = *reinterpret_cast<const float2*>(scale + c0 + j);
-            const float y0 = __uint_as_float(v[j]) * cs * r.x, y1 = __uint_as_float(v[j + 1]) * cs * r.y;
-            const float got = __shfl_xor_sync(0xffffffffu, up ? y0 : y1, 16);
-            const float gate = up ? got : y0, u = up ? y1 : got;
-            st_shared_b16(st + j * kRowB, __fdividef(gate, 1.f + __expf(-gate)) * u);
-          }
-        } else {
-          const uint32_t st = stage_u + lane * (uint32_t)sizeof(O);
+        for (int p0 = 0; p0 < 32; p0 += kPass) {
+          if constexpr (kSwiglu) {
+            // lanes 0-15 hold gate, 16-31 up of the same channels: the lower
+            // half takes the even rows, the upper half the odd ones
+            const bool up = lane >= 16;
+            const uint32_t st = stage_u + (lane & 15) * 2 + (up ? kRowB : 0);
 #pragma unroll
-          for (int j = 0; j < 32; j += 4) {
-            const float4 r = *reinterpret_cast<const float4*>(scale + c0 + j);
-            const float f[4] = {r.x, r.y, r.z, r.w};
+            for (int j = 0; j < 32; j += 2) {
+              const float2 r = *reinterpret_cast<const float2*>(scale + j);
+              const float y0 = __uint_as_float(v[j]) * cs * r.x, y1 = __uint_as_float(v[j + 1]) * cs * r.y;
+              const float got = __shfl_xor_sync(0xffffffffu, up ? y0 : y1, 16);
+              const float gate = up ? got : y0, u = up ? y1 : got;
+              st_shared_b16(st + j * kRowB, __fdividef(gate, 1.f + __expf(-gate)) * u);
+            }
+          } else {
+            const uint32_t st = stage_u + lane * (uint32_t)sizeof(O);
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              const float y = __uint_as_float(v[j + q]) * cs * f[q];
-              if constexpr (sizeof(O) == 2) st_shared_b16(st + (j + q) * kRowB, y);
-              else st_shared_f32(st + (j + q) * kRowB, y);
+            for (int j = 0; j < kPass; j += 4) {
+              const float4 r = *reinterpret_cast<const float4*>(scale + p0 + j);
+              const float f[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+              for (int q = 0; q < 4; ++q) {
+                const float y = __uint_as_float(v[p0 + j + q]) * cs * f[q];
+                if constexpr (sizeof(O) == 2) st_shared_b16(st + (j + q) * kRowB, y);
+                else st_shared_f32(st + (j + q) * kRowB, y);
+              }
             }
           }
-        }
-        __syncwarp();
-        if (wch < p.Nout) {
+          __syncwarp();
+          if (wch < p.Nout) {
 #pragma unroll
-          for (int i = 0; i < kV; ++i)
-            if (c0 + wr + i * (32 / kV) < rows)
-              st_v4(dst + i * dst_step, ld_shared_v4(stage_u + lane * 16 + i * 512));
+            for (int i = 0; i < kPass * kRowB / 512; ++i) {
+              const int r = c0 + p0 + wr + i * (32 / kV);
+              if (r < rows) st_v4(dst + (size_t)(r - wr) * ld, ld_shared_v4(stage_u + lane * 16 + i * 512));
+            }
+          }
+          __syncwarp();
         }
-        dst += kV * dst_step;
-        __syncwarp();
       }
       tc_fence_before();
       mbar_arrive_cluster_warp(mapa_shared(t_empty(acc), 0));

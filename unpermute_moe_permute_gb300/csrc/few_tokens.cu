@@ -1,15 +1,54 @@
-// The whole expert layer for a few tokens.
+// The whole expert layer for T <= 64 tokens, in one kernel.
 //
-// Two kernels: a warp per (slot, intermediate column) for silu(g) * u, and a
-// warp per (token, output column) for the weighted sum of the K down rows.
+//   act[a, t, :] = silu(Wg[e_a] x_t) * (Wu[e_a] x_t)      (phase 1)
+//   out[t]       = shared[t] + sum_a p(t, a) Wd[e_a] act[a, t, :]   (phase 2)
+//
+// over the experts e_a that some token chose.  The floor is one read of those
+// experts' weights, so the kernel is a stream of weights that does not pause:
+//
+//   * one CTA per SM, and each phase's weights cut into equal runs of 32 KB
+//     units (128 rows x 128 bytes of two matrices or of two k blocks): CTA c
+//     takes units [U c / G, U (c + 1) / G), whatever tiles they fall in, so all
+//     SMs read the same amount.  A tile that several CTAs share is summed from
+//     their fp32 partials, in the order of the CTAs, by the one that finishes
+//     last;
+//   * the weights are the A operand (M = 128 of their rows), the tokens the B
+//     operand (N = 16, 32 or 64): every active expert is multiplied with all
+//     tokens, which the tensor cores have time for (at N = 64 under a fifth of
+//     the stream's time), and a (token, expert) pair that was not chosen is
+//     left out when the result is read;
+//   * one warp streams weights through a ring of 4 or 5 stages (TMA) without
+//     ever waiting for results: at the turn from phase 1 to phase 2 it fills
+//     the ring with down weights while the last activations are still being
+//     made.  Another warp loads the tokens' and activations' tiles and alone
+//     waits for an expert's activations to be complete.
+//   * 8-bit weights go from the ring through registers to tensor memory as
+//     bf16 (exact) and are the A operand there; the scale of a channel is a
+//     lane's own factor in the epilogue.
+//
+// CTAs wait for one another, so the launch is cooperative (all of it
+// resident); every wait is bounded.  The counters are zeroed by the kernel
+// itself: each CTA clears its share and then sets its flag to a tag made from
+// the workspace's epoch word; a CTA counts only after it has seen all flags,
+// and CTA 0 then opens the next epoch.  So nothing has to be cleared, neither
+// before the first call nor between the replays of a graph.  (Counters that
+// carried the tag themselves, changed by compare-and-swap, need no flags, but
+// 152 CTAs retrying on one word cost 75 us.)
 #include <math.h>
 
+#include <mutex>
+
 #include "common.cuh"
+#include "tc_ptx.cuh"
+#include "tma_host.cuh"
 
 namespace moe {
+namespace tc {
 namespace {
 
-constexpr int kWarps = 8;
+constexpr int kMaxCtas = 160;
+constexpr int kMaxSlots = MOE_FEW_TOKENS * kMaxK;
+constexpr uint32_t kBox16 = 128 * 128;  // bytes of a weight box: 128 rows of 128 bytes
 
 // Expert of slot (t, k), or -1 for a slot that adds nothing (inactive,
 // special, out of range or repeated).
@@ -26,103 +65,689 @@ __device__ __forceinline__ int slot_expert(const int32_t* ids, const uint8_t* ma
   return e < E ? e : -1;
 }
 
-__device__ __forceinline__ float warp_sum(float v) {
-#pragma unroll
-  for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+struct FewParams {
+  const int32_t* ids;
+  const float* probs;
+  const uint8_t* mask;
+  const float *gs, *us, *ds;
+  const __nv_bfloat16* shared_x;
+  __nv_bfloat16* out;
+  __nv_bfloat16* act;          // [A, T, I]
+  float *part1, *part2;        // [CTA][2][T][2][128], [CTA][2][T][128]
+  unsigned long long* epoch;   // epoch, flag of each CTA
+  uint32_t* count;             // ready[A], tiles of phase 1, tiles of phase 2
+  int32_t* status;
+  int mask_dims, T, H, K, I, E, E_all, A_max;
+};
+
+template <int NP, bool I8>
+struct FewTraits {
+  static constexpr uint32_t b_box = NP * 128;            // 64 k of the tokens
+  static constexpr uint32_t stage = 2 * kBox16 + 2 * b_box;
+  static constexpr int stages = NP == 64 ? 4 : 5;
+  static constexpr int threads = (I8 ? 16 : 7) * 32;
+  static constexpr int k1 = I8 ? 128 : 64;               // k of a phase-1 unit
+  static constexpr int bars = 2 * stages + 4 + 4 + 1;
+  static constexpr uint32_t ctrl = stages * stage;
+  static constexpr uint32_t holder = ctrl + 8 * bars;     // tensor memory, abort, flag, A
+  static constexpr uint32_t bitmap = holder + 16;          // 32 words, then 32 prefixes
+  static constexpr uint32_t list = bitmap + 256;           // active experts
+  static constexpr uint32_t slot = list + 2 * kMaxSlots;   // expert of each slot
+  static constexpr uint32_t prob = slot + 2 * kMaxSlots;
+  static constexpr uint32_t smem = prob + 4 * kMaxSlots + 1024;
+  static_assert(smem <= 232448, "more shared memory than one CTA may use");
+};
+
+// First unit of CTA c of G, of U units.
+__device__ __forceinline__ int first_unit(int U, int c, int G) { return (int)((long long)U * c / G); }
+
+// CTA whose run holds unit u.
+__device__ __forceinline__ int cta_of(int U, int u, int G) {
+  int c = (int)((long long)u * G / U);
+  while (c + 1 < G && first_unit(U, c + 1, G) <= u) ++c;
+  while (first_unit(U, c, G) > u) --c;
+  return c;
+}
+
+// CTAs that hold units of the tile [u0, u0 + n): lo..hi, those with a run.
+__device__ __forceinline__ int pieces_of(int U, int u0, int n, int G, int& lo, int& hi) {
+  lo = cta_of(U, u0, G), hi = cta_of(U, u0 + n - 1, G);
+  int k = 0;
+  for (int c = lo; c <= hi; ++c) k += first_unit(U, c, G) < first_unit(U, c + 1, G);
+  return k;
+}
+
+// Tag of an epoch (a mixing function, so that a workspace filled with one
+// byte does not look like its own tag).
+__device__ __forceinline__ unsigned long long tag_of(unsigned long long e) {
+  e += 0x9e3779b97f4a7c15ull;
+  e = (e ^ (e >> 30)) * 0xbf58476d1ce4e5b9ull;
+  e = (e ^ (e >> 27)) * 0x94d049bb133111ebull;
+  return e ^ (e >> 31);
+}
+
+// Wait by a whole warp until ok() holds in every lane; false when the limit
+// ran out or the CTA is giving up.
+template <typename F>
+__device__ __forceinline__ bool poll_warp(F&& ok, volatile int* abort_flag, int32_t* status) {
+  unsigned long long t0 = 0;
+  for (uint32_t i = 0;; ++i) {
+    if (__all_sync(0xffffffffu, ok())) return true;
+    if ((i & 31u) == 31u) {
+      const unsigned long long now = globaltimer();
+      if (t0 == 0) t0 = now;
+      if (__any_sync(0xffffffffu, *abort_flag || now - t0 > kWaitTimeoutNs)) {
+        *abort_flag = 1;
+        set_status(status, MOE_ERR_TIMEOUT);
+        return false;
+      }
+    }
+  }
+}
+
+__device__ __forceinline__ unsigned long long ld_acquire(const unsigned long long* p) {
+  unsigned long long v;
+  asm volatile("ld.acquire.gpu.global.u64 %0, [%1];" : "=l"(v) : "l"(p) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint32_t ld_acquire(const uint32_t* p) {
+  uint32_t v;
+  asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+  return v;
+}
+// Release of what this thread has seen, acquire of what earlier adders released.
+__device__ __forceinline__ uint32_t add_acq_rel(uint32_t* p) {
+  uint32_t v;
+  asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;" : "=r"(v) : "l"(p) : "memory");
   return v;
 }
 
-// 8 weights as floats
-__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&f)[8]) {
-  VecTraits<__nv_bfloat16>::unpack(ld_v4(p), f);
+__device__ __forceinline__ void epi_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+
+// The epilogue warps' common decision to go on: a warp whose wait ran out
+// must not leave the others in a barrier.
+__device__ __forceinline__ bool epi_all(bool ok) {
+  uint32_t all;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 q, %1, 0;\n\tbar.red.and.pred p, 1, 128, q;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(all)
+      : "r"((uint32_t)ok)
+      : "memory");
+  return all != 0;
 }
-__device__ __forceinline__ void load8(const int8_t* p, float (&f)[8]) {
-  const int2 v = *reinterpret_cast<const int2*>(p);
+
+// Two signed bytes of w (selected by sel) as bf16, exactly: 0x43bb is 128 + m
+// or 256 + 2m for a byte of sign s and low bits m; clearing the sign bit
+// leaves 128 + m, and keeping only it leaves 128 or 256.
+__device__ __forceinline__ uint32_t bytes_to_bf16(uint32_t w, uint32_t sel) {
+  const uint32_t t = __byte_perm(w, 0x43434343u, sel);
+  const uint32_t lo = t & 0xff7fff7fu, hi = t & 0xff80ff80u;
+  __nv_bfloat162 r = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&lo),
+                             *reinterpret_cast<const __nv_bfloat162*>(&hi));
+  return *reinterpret_cast<uint32_t*>(&r);
+}
+
+__device__ __forceinline__ void expand16_bf16(uint4 v, uint32_t* r) {
+  r[0] = bytes_to_bf16(v.x, 0x4140), r[1] = bytes_to_bf16(v.x, 0x4342);
+  r[2] = bytes_to_bf16(v.y, 0x4140), r[3] = bytes_to_bf16(v.y, 0x4342);
+  r[4] = bytes_to_bf16(v.z, 0x4140), r[5] = bytes_to_bf16(v.z, 0x4342);
+  r[6] = bytes_to_bf16(v.w, 0x4140), r[7] = bytes_to_bf16(v.w, 0x4342);
+}
+
+__device__ __forceinline__ float swiglu(float g, float u) { return __fdividef(g, 1.f + __expf(-g)) * u; }
+
+template <int NP, bool I8>
+__global__ void __launch_bounds__(FewTraits<NP, I8>::threads, 1)
+few_tokens_kernel(const __grid_constant__ CUtensorMap mapG, const __grid_constant__ CUtensorMap mapU,
+                  const __grid_constant__ CUtensorMap mapD, const __grid_constant__ CUtensorMap mapX,
+                  const __grid_constant__ CUtensorMap mapAct, const FewParams p) {
+  using TR = FewTraits<NP, I8>;
+  constexpr int S = TR::stages;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t base = uniform((raw + 1023u) & ~1023u);
+  uint8_t* g = smem_raw + (base - raw);
+  const uint32_t bars = base + TR::ctrl;
+  auto full = [&](int s) { return bars + 8u * s; };
+  auto empty = [&](int s) { return bars + 8u * (S + s); };
+  auto t_full = [&](int a) { return bars + 8u * (2 * S + a); };
+  auto t_empty = [&](int a) { return bars + 8u * (2 * S + 2 + a); };
+  auto c_full = [&](int b) { return bars + 8u * (2 * S + 4 + b); };
+  auto c_empty = [&](int b) { return bars + 8u * (2 * S + 6 + b); };
+  const uint32_t drain = bars + 8u * (2 * S + 8);
+  uint32_t* holder = reinterpret_cast<uint32_t*>(g + TR::holder);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(holder + 1);
+  volatile int* flag = reinterpret_cast<volatile int*>(holder + 2);
+  uint32_t* bitmap = reinterpret_cast<uint32_t*>(g + TR::bitmap);
+  int16_t* list = reinterpret_cast<int16_t*>(g + TR::list);
+  int16_t* slot = reinterpret_cast<int16_t*>(g + TR::slot);
+  float* prob = reinterpret_cast<float*>(g + TR::prob);
+  const int warp = (int)uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
+  const int TK = p.T * p.K, G = (int)gridDim.x, cta = (int)blockIdx.x;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S; ++s) {
+      mbar_init(full(s), 2);               // weights, tokens
+      mbar_init(empty(s), I8 ? 9 : 1);     // MMAs (and the expanding warps)
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(t_full(a), 1);
+      mbar_init(t_empty(a), 4);
+      mbar_init(c_full(a), 8);
+      mbar_init(c_empty(a), 1);
+    }
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    mbar_fence_init();
+    tma_prefetch_desc(&mapG);
+    tma_prefetch_desc(&mapU);
+    tma_prefetch_desc(&mapD);
+    tma_prefetch_desc(&mapX);
+    tma_prefetch_desc(&mapAct);
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(holder), 512);
+    tmem_relinquish();
+  }
+  // this CTA's share of the counters, then its flag
+  const int n_count = p.A_max + p.A_max * ((p.I + 127) / 128) + (p.H + 127) / 128;
+  for (int i = cta * TR::threads + threadIdx.x; i < n_count; i += G * TR::threads) p.count[i] = 0u;
+  const unsigned long long epoch = *p.epoch, tag = tag_of(epoch);
+  // the slots' experts, and the experts that some slot chose, in order
+  if (threadIdx.x < 32) bitmap[threadIdx.x] = 0u;
+  __syncthreads();
+  for (int f = threadIdx.x; f < TK; f += TR::threads) {
+    const int t = f / p.K;
+    const int e = slot_expert(p.ids, p.mask, p.mask_dims, t, f - t * p.K, p.K, p.E, p.E_all,
+                              cta == 0 ? p.status : nullptr);
+    slot[f] = (int16_t)e;
+    prob[f] = p.probs[f];
+    if (e >= 0) atomicOr(&bitmap[e >> 5], 1u << (e & 31));
+  }
+  __syncthreads();
+  if (threadIdx.x == 32)
+    asm volatile("st.release.gpu.global.u64 [%0], %1;" ::"l"(p.epoch + 1 + cta), "l"(tag) : "memory");
+  if (warp == 0) {
+    const int n = __popc(bitmap[lane]);
+    int incl = n;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    f[i] = (float)(int8_t)(v.x >> (8 * i));
-    f[4 + i] = (float)(int8_t)(v.y >> (8 * i));
+    for (int d = 1; d < 32; d <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, incl, d);
+      if (lane >= d) incl += v;
+    }
+    int a = incl - n;
+    for (uint32_t w = bitmap[lane]; w != 0u; w &= w - 1) list[a++] = (int16_t)(lane * 32 + __ffs(w) - 1);
+    if (lane == 31) holder[3] = (uint32_t)incl;
   }
-}
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = uniform(holder[0]);
+  const int A = (int)uniform(holder[3]);
+  const int nt1 = (p.I + 127) / 128, nt2 = (p.H + 127) / 128;
+  const int KB1 = (p.H + TR::k1 - 1) / TR::k1, KB2 = (p.I + 127) / 128;
+  const int U1 = A * nt1 * KB1, U2 = nt2 * A * KB2;
+  const int lo1 = first_unit(U1, cta, G), hi1 = first_unit(U1, cta + 1, G);
+  const int lo2 = first_unit(U2, cta, G), hi2 = first_unit(U2, cta + 1, G);
+  uint32_t* ready = p.count;
+  uint32_t* cnt1 = ready + p.A_max;
+  uint32_t* cnt2 = cnt1 + (size_t)p.A_max * nt1;
+  unsigned long long* flags = p.epoch + 1;
 
-template <typename A, typename W>
-__device__ __forceinline__ float dot_row(const A* a, const W* w, int n, int lane) {
-  float s = 0.f;
-  for (int c = lane * 8; c < n; c += 256) {
-    float x[8], y[8];
-    load8(a + c, x);
-    load8(w + c, y);
+  // every CTA's counters are clear (and every CTA has read the epoch)
+  auto all_clear = [&]() {
+    return poll_warp([&]() {
+      bool ok = true;
+      for (int c = lane; c < G; c += 32) ok &= ld_acquire(flags + c) == tag;
+      return ok;
+    }, abort_flag, p.status);
+  };
+
+  if (A == 0) {
+    for (int i = cta * TR::threads + threadIdx.x; i < p.T * p.H; i += G * TR::threads)
+      p.out[i] = p.shared_x ? p.shared_x[i] : __float2bfloat16_rn(0.f);
+  }
+
+  if (warp == 0) {
+    // ---------------- weights ----------------
+    if (lane == 0) {
+      int s = 0, n = 0;
+      uint32_t ph = 0;
+      auto slot_free = [&]() { return mbar_wait(empty(s), ph ^ 1u, abort_flag, p.status); };
+      auto next = [&]() {
+        ++n;
+        if (++s == S) s = 0, ph ^= 1u;
+      };
+      bool run = true;
+      for (int u = lo1; run && u < hi1;) {
+        const int tile = u / KB1, kb = u - tile * KB1, len = min(KB1 - kb, hi1 - u);
+        const int e = list[tile / nt1], i0 = (tile % nt1) * 128;
+        for (int k = kb; k < kb + len; ++k) {
+          if (!(run = slot_free())) break;
+          const uint32_t a = base + s * TR::stage;
+          mbar_arrive_expect_tx(full(s), 2 * kBox16);
+          tma_load_3d(a, &mapG, full(s), k * TR::k1, i0, e);
+          tma_load_3d(a + kBox16, &mapU, full(s), k * TR::k1, i0, e);
+          next();
+        }
+        u += len;
+      }
+      for (int u = lo2; run && u < hi2;) {
+        const int ta = u / KB2, kb = u - ta * KB2, len = min(KB2 - kb, hi2 - u);
+        const int e = list[ta % A], h0 = (ta / A) * 128;
+        for (int k = kb; k < kb + len; ++k) {
+          if (!(run = slot_free())) break;
+          const uint32_t a = base + s * TR::stage;
+          mbar_arrive_expect_tx(full(s), I8 ? kBox16 : 2 * kBox16);
+          tma_load_3d(a, &mapD, full(s), k * 128, h0, e);
+          if constexpr (!I8) tma_load_3d(a + kBox16, &mapD, full(s), k * 128 + 64, h0, e);
+          next();
+        }
+        u += len;
+      }
+      // every copy has landed before the CTA may exit
+      for (int st = 0; st < S && st < n; ++st) {
+        const int last = st + (n - 1 - st) / S * S;
+        mbar_wait(full(st), (uint32_t)(last / S) & 1u, abort_flag, p.status, false);
+      }
+    }
+  } else if (warp == 6) {
+    // ---------------- tokens, activations ----------------
+    int s = 0;
+    uint32_t ph = 0;
+    bool run = true;
+    for (int u = lo1; run && u < hi1; ++u) {
+      const int k = u % KB1;
+      if (!(run = mbar_wait_warp(empty(s), ph ^ 1u, abort_flag, p.status))) break;
+      if (lane == 0) {
+        const uint32_t b = base + s * TR::stage + 2 * kBox16;
+        mbar_arrive_expect_tx(full(s), I8 ? 2 * TR::b_box : TR::b_box);
+        tma_load_2d(b, &mapX, full(s), k * TR::k1, 0);
+        if constexpr (I8) tma_load_2d(b + TR::b_box, &mapX, full(s), k * TR::k1 + 64, 0);
+      }
+      __syncwarp();
+      if (++s == S) s = 0, ph ^= 1u;
+    }
+    if (run) run = all_clear();
+    if (run && cta == 0 && lane == 0) *p.epoch = epoch + 1;
+    int seen = -1, checked = 0;  // last expert; experts known to be complete
+    for (int u = lo2; run && u < hi2; ++u) {
+      const int ta = u / KB2, k = u - ta * KB2, a = ta % A;
+      if (a != seen && checked < A) {  // (the experts come round in order)
+        run = poll_warp([&]() { return ld_acquire(ready + a) == (uint32_t)nt1; }, abort_flag, p.status);
+        if (!run) break;
+        seen = a;
+        ++checked;
+      }
+      if (!(run = mbar_wait_warp(empty(s), ph ^ 1u, abort_flag, p.status))) break;
+      if (lane == 0) {
+        asm volatile("fence.proxy.async.global;" ::: "memory");
+        const uint32_t b = base + s * TR::stage + 2 * kBox16;
+        mbar_arrive_expect_tx(full(s), 2 * TR::b_box);
+        tma_load_3d(b, &mapAct, full(s), k * 128, 0, a);
+        tma_load_3d(b + TR::b_box, &mapAct, full(s), k * 128 + 64, 0, a);
+      }
+      __syncwarp();
+      if (++s == S) s = 0, ph ^= 1u;
+    }
+  } else if (warp == 1) {
+    // ---------------- MMA: the whole warp, one lane elected for each ----------------
+    constexpr uint32_t idesc = idesc_bf16_f32(128, NP, false, false);
+    const uint64_t d0 = desc_sw128(base, 16, 1024);
+    int s = 0, c = 0, it = 0;
+    uint32_t ph = 0, cph = 0;
+    bool run = true;
+    // one segment: len units of one tile (phase 1) or one tile and expert (phase 2)
+    auto segment = [&](int len, bool up) {
+      const int acc = it & 1;
+      run = mbar_wait_warp(t_empty(acc), ((it >> 1) & 1) ^ 1u, abort_flag, p.status);
+      if (!run) return;
+      tc_fence_after();
+      const uint32_t d = tmem + acc * 2 * NP;
+      uint32_t accum = 0u;
+      for (int k = 0; k < len; ++k) {
+        run = mbar_wait_warp(full(s), ph, abort_flag, p.status);
+        if (!run) return;
+        if constexpr (I8) {
+          run = mbar_wait_warp(c_full(c), cph, abort_flag, p.status);
+          if (!run) return;
+        }
+        tc_fence_after();
+        const uint64_t ad = d0 + (uint64_t)s * (TR::stage >> 4);
+        const uint64_t bd = ad + (2 * kBox16 >> 4);
+        if constexpr (I8) {
+          const uint32_t a = tmem + 256 + c * 128;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) s = fmaf(x[i], y[i], s);
+          for (int kk = 0; kk < 8; ++kk) {
+            const uint64_t b = bd + (kk >> 2) * (TR::b_box >> 4) + (kk & 3) * 2;
+            umma_f16_ta_warp<false>(d, a + kk * 8, b, idesc, accum);
+            if (up) umma_f16_ta_warp<false>(d + NP, a + 64 + kk * 8, b, idesc, accum);
+            accum = 1u;
+          }
+          umma_commit_warp(c_empty(c));
+          c ^= 1;
+          if (c == 0) cph ^= 1u;
+        } else {
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk) {
+            umma_f16_warp<false>(d, ad + kk * 2, bd + kk * 2, idesc, accum);
+            if (up) umma_f16_warp<false>(d + NP, ad + (kBox16 >> 4) + kk * 2, bd + kk * 2, idesc, accum);
+            accum = 1u;
+          }
+          if (!up) {
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              umma_f16_warp<false>(d, ad + (kBox16 >> 4) + kk * 2, bd + (TR::b_box >> 4) + kk * 2, idesc, 1u);
+          }
+        }
+        umma_commit_warp(empty(s));
+        if (++s == S) s = 0, ph ^= 1u;
+      }
+      umma_commit_warp(t_full(acc));
+      ++it;
+    };
+    for (int u = lo1; run && u < hi1;) {
+      const int len = min(KB1 - u % KB1, hi1 - u);
+      segment(len, true);
+      u += len;
+    }
+    for (int u = lo2; run && u < hi2;) {
+      const int len = min(KB2 - u % KB2, hi2 - u);
+      segment(len, false);
+      u += len;
+    }
+    umma_commit_warp(drain);
+    mbar_wait_warp(drain, 0, abort_flag, p.status, false);
+  } else if (warp < 6) {
+    // ---------------- epilogue: lanes are weight rows, columns are tokens ----------------
+    const int quarter = warp & 3, r = quarter * 32 + lane;
+    const bool lead = threadIdx.x == 64;
+    const uint32_t tq = tmem + ((uint32_t)(quarter * 32) << 16);
+    int it = 0;
+    bool run = epi_all(all_clear());  // (while the first weights are under way)
+    auto arrive_last = [&](uint32_t* w, int pieces) {
+      __threadfence();
+      epi_sync();  // every thread's partials are written
+      if (lead) *flag = add_acq_rel(w) == (uint32_t)pieces - 1;
+      epi_sync();
+      const bool last = *flag != 0;
+      epi_sync();  // read by all before the next use
+      return last;
+    };
+    for (int u = lo1; run && u < hi1; ++it) {
+      const int tile = u / KB1, kb = u - tile * KB1, len = min(KB1 - kb, hi1 - u);
+      const int a = tile / nt1, e = list[a], i = (tile % nt1) * 128 + r;
+      const bool in = i < p.I;
+      const int acc = it & 1;
+      run = epi_all(mbar_wait_warp(t_full(acc), (it >> 1) & 1, abort_flag, p.status));
+      if (!run) break;
+      tc_fence_after();
+      const uint32_t d = tq + acc * 2 * NP;
+      const bool whole = len == KB1;
+      float gsc = 1.f, usc = 1.f;
+      if (I8 && in) gsc = p.gs[(size_t)e * p.I + i], usc = p.us[(size_t)e * p.I + i];
+      __nv_bfloat16* act = p.act + (size_t)a * p.T * p.I + i;
+      const size_t pstride = (size_t)p.T * 256;  // floats of a partial
+      float* mine = p.part1 + ((size_t)cta * 2 + (u == lo1 ? 0 : 1)) * pstride + r;
+#pragma unroll
+      for (int c0 = 0; c0 < NP; c0 += 16) {
+        if (c0 >= p.T) break;
+        uint32_t gv[16], uv[16];
+        tmem_ld_32x32b_x16(d + c0, gv);
+        tmem_ld_32x32b_x16(d + NP + c0, uv);
+        tmem_ld_wait();
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          const int t = c0 + j;
+          if (t < p.T) {
+            const float gg = __uint_as_float(gv[j]) * gsc, uu = __uint_as_float(uv[j]) * usc;
+            if (whole) {
+              if (in) act[(size_t)t * p.I] = __float2bfloat16_rn(swiglu(gg, uu));
+            } else {
+              mine[t * 256] = gg;
+              mine[t * 256 + 128] = uu;
+            }
+          }
+        }
+      }
+      tc_fence_before();
+      mbar_arrive_warp(t_empty(acc));
+      bool done = whole;
+      if (!whole) {
+        int c_lo, c_hi;
+        const int t0 = tile * KB1, pieces = pieces_of(U1, t0, KB1, G, c_lo, c_hi);
+        done = arrive_last(cnt1 + tile, pieces);
+        if (done && in) {
+          // 16 tokens at a time: their loads are in flight together
+          for (int t = 0; t < p.T; t += 16) {
+            float gg[16], uu[16];
+#pragma unroll
+            for (int j = 0; j < 16; ++j) gg[j] = uu[j] = 0.f;
+            for (int c = c_lo; c <= c_hi; ++c) {
+              const int f = first_unit(U1, c, G);
+              if (f == first_unit(U1, c + 1, G)) continue;
+              const float* q = p.part1 + ((size_t)c * 2 + (f >= t0 ? 0 : 1)) * pstride + r + t * 256;
+#pragma unroll
+              for (int j = 0; j < 16; ++j) {
+                if (t + j < p.T) {
+                  gg[j] += __ldcg(q + j * 256);
+                  uu[j] += __ldcg(q + j * 256 + 128);
+                }
+              }
+            }
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+              if (t + j < p.T) act[(size_t)(t + j) * p.I] = __float2bfloat16_rn(swiglu(gg[j], uu[j]));
+          }
+        }
+      }
+      if (done) {
+        asm volatile("fence.proxy.async.global;" ::: "memory");
+        __threadfence();
+        epi_sync();
+        if (lead) (void)add_acq_rel(ready + a);
+      }
+      u += len;
+    }
+    float sum[NP];
+#pragma unroll
+    for (int t = 0; t < NP; ++t) sum[t] = 0.f;
+    for (int u = lo2; run && u < hi2; ++it) {
+      const int ta = u / KB2, kb = u - ta * KB2, len = min(KB2 - kb, hi2 - u);
+      const int tile = ta / A, a = ta - tile * A, e = list[a], h = tile * 128 + r;
+      const bool in = h < p.H;
+      // the tokens that chose this expert, and their weights: lane, lane + 32
+      float w0 = 0.f, w1 = 0.f;
+      bool m0 = false, m1 = false;
+      for (int k = 0; k < p.K; ++k) {
+        if (lane < p.T && slot[lane * p.K + k] == e) m0 = true, w0 = prob[lane * p.K + k];
+        if (NP > 32 && lane + 32 < p.T && slot[(lane + 32) * p.K + k] == e)
+          m1 = true, w1 = prob[(lane + 32) * p.K + k];
+      }
+      const uint32_t b0 = __ballot_sync(0xffffffffu, m0), b1 = NP > 32 ? __ballot_sync(0xffffffffu, m1) : 0u;
+      const float dsc = I8 && in ? p.ds[(size_t)e * p.H + h] : 1.f;
+      const int acc = it & 1;
+      run = epi_all(mbar_wait_warp(t_full(acc), (it >> 1) & 1, abort_flag, p.status));
+      if (!run) break;
+      tc_fence_after();
+      const uint32_t d = tq + acc * 2 * NP;
+#pragma unroll
+      for (int c0 = 0; c0 < NP; c0 += 16) {
+        const uint32_t bits = ((c0 < 32 ? b0 : b1) >> (c0 & 31)) & 0xffffu;
+        if (bits == 0u) continue;
+        uint32_t v[16];
+        tmem_ld_32x32b_x16(d + c0, v);
+        tmem_ld_wait();
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          const float w = __shfl_sync(0xffffffffu, c0 < 32 ? w0 : w1, (c0 + j) & 31);
+          if ((bits >> j) & 1u) sum[c0 + j] = fmaf(w, __uint_as_float(v[j]) * dsc, sum[c0 + j]);
+        }
+      }
+      tc_fence_before();
+      mbar_arrive_warp(t_empty(acc));
+      u += len;
+      const int t0 = tile * A * KB2, t1 = t0 + A * KB2;  // units of the tile
+      if (u == t1 || u == hi2) {
+        const bool whole = lo2 <= t0 && u == t1;
+        const size_t pstride = (size_t)p.T * 128;
+        auto put = [&](int t, float y) {
+          if (p.shared_x) y += __bfloat162float(p.shared_x[(size_t)t * p.H + h]);
+          p.out[(size_t)t * p.H + h] = __float2bfloat16_rn(y);
+        };
+        float* mine = p.part2 + ((size_t)cta * 2 + (lo2 >= t0 ? 0 : 1)) * pstride + r;
+#pragma unroll
+        for (int t = 0; t < NP; ++t) {
+          if (t < p.T) {
+            if (!whole) mine[t * 128] = sum[t];
+            else if (in) put(t, sum[t]);
+          }
+          sum[t] = 0.f;
+        }
+        if (!whole) {
+          int c_lo, c_hi;
+          const int pieces = pieces_of(U2, t0, A * KB2, G, c_lo, c_hi);
+          if (arrive_last(cnt2 + tile, pieces) && in) {
+            for (int t = 0; t < p.T; t += 16) {
+              float y[16];
+#pragma unroll
+              for (int j = 0; j < 16; ++j) y[j] = 0.f;
+              for (int c = c_lo; c <= c_hi; ++c) {
+                const int f = first_unit(U2, c, G);
+                if (f == first_unit(U2, c + 1, G)) continue;
+                const float* q = p.part2 + ((size_t)c * 2 + (f >= t0 ? 0 : 1)) * pstride + r + t * 128;
+#pragma unroll
+                for (int j = 0; j < 16; ++j)
+                  if (t + j < p.T) y[j] += __ldcg(q + j * 128);
+              }
+#pragma unroll
+              for (int j = 0; j < 16; ++j)
+                if (t + j < p.T) put(t + j, y[j]);
+            }
+          }
+        }
+      }
+    }
+  } else if (I8 && warp >= 8) {
+    // ---------------- expand: 8-bit rows to bf16 in tensor memory ----------------
+    // Phase 1: one warp of a quarter takes the gate rows, the other the up
+    // rows.  Phase 2: one k half each.
+    const int quarter = warp & 3, j = (warp - 8) >> 2, r = quarter * 32 + lane;
+    const uint32_t row = base + r * 128 + ((r & 7) << 4);
+    const uint32_t dst = tmem + 256 + ((uint32_t)(quarter * 32) << 16);
+    const int n1 = hi1 - lo1, n = n1 + hi2 - lo2;
+    int s = 0, c = 0;
+    uint32_t ph = 0, cph = 0;
+    for (int i = 0; i < n; ++i) {
+      if (!mbar_wait_warp(full(s), ph, abort_flag, p.status)) break;
+      const bool one = i < n1;  // phase 1
+      const uint32_t src = row + s * TR::stage + (one ? j * kBox16 : 0);
+      const int c0 = one ? 0 : 4 * j;  // first 16-byte chunk
+      uint4 v[4];
+      uint32_t f[32];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) v[q] = ld_shared_v4(src ^ ((c0 + q) << 4));
+#pragma unroll
+      for (int q = 0; q < 4; ++q) expand16_bf16(v[q], f + 8 * q);
+      if (one) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) v[q] = ld_shared_v4(src ^ ((4 + q) << 4));
+      }
+      if (!mbar_wait_warp(c_empty(c), cph ^ 1u, abort_flag, p.status)) break;
+      tc_fence_after();
+      const uint32_t a = dst + c * 128 + (one ? j * 64 : j * 32);
+      tmem_st_32x32b_x32(a, f);
+      if (one) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) expand16_bf16(v[q], f + 8 * q);
+        tmem_st_32x32b_x32(a + 32, f);
+      }
+      tmem_st_wait();
+      tc_fence_before();
+      mbar_arrive_warp(c_full(c));
+      mbar_arrive_warp(empty(s));
+      c ^= 1;
+      if (c == 0) cph ^= 1u;
+      if (++s == S) s = 0, ph ^= 1u;
+    }
   }
-  return warp_sum(s);
-}
-
-template <typename W>
-__global__ void __launch_bounds__(kWarps * 32)
-few_gate_up_kernel(const __nv_bfloat16* __restrict__ x, const int32_t* __restrict__ ids,
-                   const uint8_t* __restrict__ mask, int mask_dims, int H, int K, int I, int E,
-                   int E_all, const W* __restrict__ Wg, const W* __restrict__ Wu,
-                   const float* __restrict__ gs, const float* __restrict__ us,
-                   __nv_bfloat16* __restrict__ act, int32_t* status) {
-  const int lane = threadIdx.x & 31, i = blockIdx.x * kWarps + (threadIdx.x >> 5);
-  const int f = blockIdx.y, t = f / K;
-  const int e = slot_expert(ids, mask, mask_dims, t, f % K, K, E, E_all, status);
-  if (i >= I || e < 0) return;
-  const size_t r = (size_t)e * I + i;
-  float g = dot_row(x + (size_t)t * H, Wg + r * H, H, lane);
-  float u = dot_row(x + (size_t)t * H, Wu + r * H, H, lane);
-  if (gs != nullptr) g *= gs[r], u *= us[r];
-  if (lane == 0) act[(size_t)f * I + i] = __float2bfloat16_rn(g / (1.f + expf(-g)) * u);
-}
-
-template <typename W>
-__global__ void __launch_bounds__(kWarps * 32)
-few_down_kernel(const __nv_bfloat16* __restrict__ act, const int32_t* __restrict__ ids,
-                const uint8_t* __restrict__ mask, int mask_dims, const float* __restrict__ probs,
-                int H, int K, int I, int E, int E_all, const W* __restrict__ Wd,
-                const float* __restrict__ ds, const __nv_bfloat16* __restrict__ shared_x,
-                __nv_bfloat16* __restrict__ out, int32_t* status) {
-  const int lane = threadIdx.x & 31, h = blockIdx.x * kWarps + (threadIdx.x >> 5), t = blockIdx.y;
-  if (h >= H) return;
-  float y = 0.f;
-  for (int k = 0; k < K; ++k) {
-    const int e = slot_expert(ids, mask, mask_dims, t, k, K, E, E_all, status);
-    if (e < 0) continue;
-    const size_t r = (size_t)e * H + h;
-    float d = dot_row(act + (size_t)(t * K + k) * I, Wd + r * I, I, lane);
-    if (ds != nullptr) d *= ds[r];
-    y = fmaf(probs[t * K + k], d, y);
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
   }
-  if (shared_x != nullptr) y += __bfloat162float(shared_x[(size_t)t * H + h]);
-  if (lane == 0) out[(size_t)t * H + h] = __float2bfloat16_rn(y);
 }
 
-template <typename W>
-int launch_few(const __nv_bfloat16* x, const int32_t* ids, const float* probs, int T, int H, int K,
-               int I, int E, int E_all, const uint8_t* mask, int mask_dims, const void* Wg,
-               const void* Wu, const void* Wd, const float* gs, const float* us, const float* ds,
-               const __nv_bfloat16* shared_x, __nv_bfloat16* out, __nv_bfloat16* act,
-               int32_t* status, cudaStream_t s) {
-  few_gate_up_kernel<W><<<dim3((I + kWarps - 1) / kWarps, T * K), kWarps * 32, 0, s>>>(
-      x, ids, mask, mask_dims, H, K, I, E, E_all, static_cast<const W*>(Wg),
-      static_cast<const W*>(Wu), gs, us, act, status);
-  few_down_kernel<W><<<dim3((H + kWarps - 1) / kWarps, T), kWarps * 32, 0, s>>>(
-      act, ids, mask, mask_dims, probs, H, K, I, E, E_all, static_cast<const W*>(Wd), ds, shared_x,
-      out, status);
-  MOE_LAUNCH_CHECK();
-  count_launches(2);
+struct FewLayout {
+  size_t words, counts, part1, part2, act, total;
+};
+
+FewLayout few_layout(int T, int K, int H, int I, int E) {
+  const size_t A = (size_t)(T * K < E ? T * K : E);
+  auto up = [](size_t v) { return (v + 255) & ~(size_t)255; };
+  FewLayout l;
+  l.words = up(8 * (1 + kMaxCtas));
+  l.counts = up(4 * (A + A * ((I + 127) / 128) + (H + 127) / 128));
+  l.part1 = (size_t)kMaxCtas * 2 * T * 256 * 4;
+  l.part2 = (size_t)kMaxCtas * 2 * T * 128 * 4;
+  l.act = up(A * T * I * 2);
+  l.total = l.words + l.counts + l.part1 + l.part2 + l.act;
+  return l;
+}
+
+template <int NP, bool I8>
+int launch_few(FewParams p, const void* x, const void* Wg, const void* Wu, const void* Wd,
+               cudaStream_t s) {
+  using TR = FewTraits<NP, I8>;
+  constexpr int esz = I8 ? 1 : 2;
+  CUtensorMap mg, mu, md, mx, ma;
+  const uint64_t d1[3] = {(uint64_t)p.H, (uint64_t)p.I, (uint64_t)p.E};
+  const uint64_t d2[3] = {(uint64_t)p.I, (uint64_t)p.H, (uint64_t)p.E};
+  const uint32_t bw[3] = {128 / esz, 128, 1};
+  const uint64_t dx[2] = {(uint64_t)p.H, (uint64_t)p.T};
+  const uint64_t da[3] = {(uint64_t)p.I, (uint64_t)p.T, (uint64_t)p.A_max};
+  const uint32_t bx[3] = {64, NP, 1};
+  if (!make_map_sw128(&mg, Wg, esz, 3, d1, bw) || !make_map_sw128(&mu, Wu, esz, 3, d1, bw) ||
+      !make_map_sw128(&md, Wd, esz, 3, d2, bw) || !make_map_sw128(&mx, x, 2, 2, dx, bx) ||
+      !make_map_sw128(&ma, p.act, 2, 3, da, bx))
+    return MOE_ERR_CUDA;
+  static std::once_flag once;
+  static cudaError_t attr = cudaSuccess;
+  std::call_once(once, [] {
+    attr = cudaFuncSetAttribute(few_tokens_kernel<NP, I8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                (int)TR::smem);
+  });
+  if (attr != cudaSuccess) return MOE_ERR_CUDA;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeCooperative;
+  at[0].val.cooperative = 1;
+  cfg.gridDim = dim3(sm_count() < kMaxCtas ? sm_count() : kMaxCtas, 1, 1);
+  cfg.blockDim = dim3(TR::threads, 1, 1);
+  cfg.dynamicSmemBytes = TR::smem;
+  cfg.stream = s;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, few_tokens_kernel<NP, I8>, mg, mu, md, mx, ma, p) != cudaSuccess) {
+    (void)cudaGetLastError();
+    return MOE_ERR_CUDA;
+  }
+  count_launches(1);
   return MOE_OK;
 }
 
 }  // namespace
+}  // namespace tc
 }  // namespace moe
 
 using namespace moe;
+using namespace moe::tc;
 
 extern "C" size_t moe_layer_few_tokens_workspace_size(int T, int K, int H, int I, int E) {
-  if (T <= 0 || K <= 0 || H <= 0 || I <= 0 || E <= 0) return 0;
-  return (size_t)T * K * I * 2;
+  if (T <= 0 || K <= 0 || H <= 0 || I <= 0 || E <= 0 || T > MOE_FEW_TOKENS || K > kMaxK) return 0;
+  return few_layout(T, K, H, I, E).total;
 }
 
 extern "C" int moe_layer_few_tokens(const void* tokens, const int32_t* expert_ids,
@@ -152,12 +777,37 @@ extern "C" int moe_layer_few_tokens(const void* tokens, const int32_t* expert_id
     if (p && !aligned16(p)) return MOE_ERR_INVALID_ARG;
   if (workspace_bytes < moe_layer_few_tokens_workspace_size(T, K, H, I, E))
     return MOE_ERR_INVALID_ARG;
-  auto go = [&](auto w) {
-    return launch_few<decltype(w)>(
-        static_cast<const __nv_bfloat16*>(tokens), expert_ids, probs, T, H, K, I, E, E + num_special,
-        active_mask, mask_dims, W_gate, W_up, W_down, gate_scale, up_scale, down_scale,
-        static_cast<const __nv_bfloat16*>(shared_x), static_cast<__nv_bfloat16*>(out),
-        static_cast<__nv_bfloat16*>(workspace), dev_status, stream);
+  if (int rc = device_ok()) return rc;
+  const FewLayout l = few_layout(T, K, H, I, E);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  FewParams p{};
+  p.ids = expert_ids;
+  p.probs = probs;
+  p.mask = active_mask;
+  p.gs = gate_scale;
+  p.us = up_scale;
+  p.ds = down_scale;
+  p.shared_x = static_cast<const __nv_bfloat16*>(shared_x);
+  p.out = static_cast<__nv_bfloat16*>(out);
+  p.epoch = reinterpret_cast<unsigned long long*>(ws);
+  p.count = reinterpret_cast<uint32_t*>(ws += l.words);
+  p.part1 = reinterpret_cast<float*>(ws += l.counts);
+  p.part2 = reinterpret_cast<float*>(ws += l.part1);
+  p.act = reinterpret_cast<__nv_bfloat16*>(ws += l.part2);
+  p.status = dev_status;
+  p.mask_dims = mask_dims;
+  p.T = T;
+  p.H = H;
+  p.K = K;
+  p.I = I;
+  p.E = E;
+  p.E_all = E + num_special;
+  p.A_max = T * K < E ? T * K : E;
+  auto go = [&](auto i8) {
+    constexpr bool I8 = decltype(i8)::value;
+    if (T <= 16) return launch_few<16, I8>(p, tokens, W_gate, W_up, W_down, stream);
+    if (T <= 32) return launch_few<32, I8>(p, tokens, W_gate, W_up, W_down, stream);
+    return launch_few<64, I8>(p, tokens, W_gate, W_up, W_down, stream);
   };
-  return i8 ? go(int8_t{}) : go(__nv_bfloat16{});
+  return weight_dtype == MOE_INT8 ? go(std::true_type{}) : go(std::false_type{});
 }

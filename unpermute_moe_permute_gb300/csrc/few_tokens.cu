@@ -85,7 +85,7 @@ struct FewTraits {
   static constexpr uint32_t b_box = NP * 128;            // 64 k of the tokens
   static constexpr uint32_t stage = 2 * kBox16 + 2 * b_box;
   static constexpr int stages = NP == 64 ? 4 : 5;
-  static constexpr int threads = (I8 ? 16 : 7) * 32;
+  static constexpr int threads = (I8 ? 20 : 11) * 32;
   static constexpr int k1 = I8 ? 128 : 64;               // k of a phase-1 unit
   static constexpr int bars = 2 * stages + 4 + 4 + 1;
   static constexpr uint32_t ctrl = stages * stage;
@@ -98,7 +98,8 @@ struct FewTraits {
   static_assert(smem <= 232448, "more shared memory than one CTA may use");
 };
 
-// First unit of CTA c of G, of U units.
+// The U units of a phase are shared by G = min(CTAs, U) CTAs, so that each of
+// those has one at least.  First unit of CTA c:
 __device__ __forceinline__ int first_unit(int U, int c, int G) { return (int)((long long)U * c / G); }
 
 // CTA whose run holds unit u.
@@ -107,14 +108,6 @@ __device__ __forceinline__ int cta_of(int U, int u, int G) {
   while (c + 1 < G && first_unit(U, c + 1, G) <= u) ++c;
   while (first_unit(U, c, G) > u) --c;
   return c;
-}
-
-// CTAs that hold units of the tile [u0, u0 + n): lo..hi, those with a run.
-__device__ __forceinline__ int pieces_of(int U, int u0, int n, int G, int& lo, int& hi) {
-  lo = cta_of(U, u0, G), hi = cta_of(U, u0 + n - 1, G);
-  int k = 0;
-  for (int c = lo; c <= hi; ++c) k += first_unit(U, c, G) < first_unit(U, c + 1, G);
-  return k;
 }
 
 // Tag of an epoch (a mixing function, so that a workspace filled with one
@@ -132,7 +125,10 @@ template <typename F>
 __device__ __forceinline__ bool poll_warp(F&& ok, volatile int* abort_flag, int32_t* status) {
   unsigned long long t0 = 0;
   for (uint32_t i = 0;; ++i) {
-    if (__all_sync(0xffffffffu, ok())) return true;
+    if (__all_sync(0xffffffffu, ok())) {
+      __threadfence();
+      return true;
+    }
     if ((i & 31u) == 31u) {
       const unsigned long long now = globaltimer();
       if (t0 == 0) t0 = now;
@@ -145,14 +141,16 @@ __device__ __forceinline__ bool poll_warp(F&& ok, volatile int* abort_flag, int3
   }
 }
 
-__device__ __forceinline__ unsigned long long ld_acquire(const unsigned long long* p) {
+// Relaxed loads for polling (an acquire load waits for the one before it); a
+// fence follows the poll.
+__device__ __forceinline__ unsigned long long ld_relaxed(const unsigned long long* p) {
   unsigned long long v;
-  asm volatile("ld.acquire.gpu.global.u64 %0, [%1];" : "=l"(v) : "l"(p) : "memory");
+  asm volatile("ld.relaxed.gpu.global.u64 %0, [%1];" : "=l"(v) : "l"(p) : "memory");
   return v;
 }
-__device__ __forceinline__ uint32_t ld_acquire(const uint32_t* p) {
+__device__ __forceinline__ uint32_t ld_relaxed(const uint32_t* p) {
   uint32_t v;
-  asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+  asm volatile("ld.relaxed.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
   return v;
 }
 // Release of what this thread has seen, acquire of what earlier adders released.
@@ -162,14 +160,14 @@ __device__ __forceinline__ uint32_t add_acq_rel(uint32_t* p) {
   return v;
 }
 
-__device__ __forceinline__ void epi_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+__device__ __forceinline__ void epi_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 
 // The epilogue warps' common decision to go on: a warp whose wait ran out
 // must not leave the others in a barrier.
 __device__ __forceinline__ bool epi_all(bool ok) {
   uint32_t all;
   asm volatile(
-      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 q, %1, 0;\n\tbar.red.and.pred p, 1, 128, q;\n\t"
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 q, %1, 0;\n\tbar.red.and.pred p, 1, 256, q;\n\t"
       "selp.u32 %0, 1, 0, p;\n\t}"
       : "=r"(all)
       : "r"((uint32_t)ok)
@@ -233,7 +231,7 @@ few_tokens_kernel(const __grid_constant__ CUtensorMap mapG, const __grid_constan
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(t_full(a), 1);
-      mbar_init(t_empty(a), 4);
+      mbar_init(t_empty(a), 8);  // the epilogue warps
       mbar_init(c_full(a), 8);
       mbar_init(c_empty(a), 1);
     }
@@ -288,8 +286,9 @@ few_tokens_kernel(const __grid_constant__ CUtensorMap mapG, const __grid_constan
   const int nt1 = (p.I + 127) / 128, nt2 = (p.H + 127) / 128;
   const int KB1 = (p.H + TR::k1 - 1) / TR::k1, KB2 = (p.I + 127) / 128;
   const int U1 = A * nt1 * KB1, U2 = nt2 * A * KB2;
-  const int lo1 = first_unit(U1, cta, G), hi1 = first_unit(U1, cta + 1, G);
-  const int lo2 = first_unit(U2, cta, G), hi2 = first_unit(U2, cta + 1, G);
+  const int G1 = min(G, U1), G2 = min(G, U2);
+  const int lo1 = cta < G1 ? first_unit(U1, cta, G1) : 0, hi1 = cta < G1 ? first_unit(U1, cta + 1, G1) : 0;
+  const int lo2 = cta < G2 ? first_unit(U2, cta, G2) : 0, hi2 = cta < G2 ? first_unit(U2, cta + 1, G2) : 0;
   uint32_t* ready = p.count;
   uint32_t* cnt1 = ready + p.A_max;
   uint32_t* cnt2 = cnt1 + (size_t)p.A_max * nt1;
@@ -298,8 +297,13 @@ few_tokens_kernel(const __grid_constant__ CUtensorMap mapG, const __grid_constan
   // every CTA's counters are clear (and every CTA has read the epoch)
   auto all_clear = [&]() {
     return poll_warp([&]() {
+      unsigned long long w[(kMaxCtas + 31) / 32];
+#pragma unroll
+      for (int i = 0; i < (kMaxCtas + 31) / 32; ++i)
+        w[i] = lane + 32 * i < G ? ld_relaxed(flags + lane + 32 * i) : tag;
       bool ok = true;
-      for (int c = lane; c < G; c += 32) ok &= ld_acquire(flags + c) == tag;
+#pragma unroll
+      for (int i = 0; i < (kMaxCtas + 31) / 32; ++i) ok &= w[i] == tag;
       return ok;
     }, abort_flag, p.status);
   };
@@ -352,7 +356,7 @@ few_tokens_kernel(const __grid_constant__ CUtensorMap mapG, const __grid_constan
         mbar_wait(full(st), (uint32_t)(last / S) & 1u, abort_flag, p.status, false);
       }
     }
-  } else if (warp == 6) {
+  } else if (warp == 10) {
     // ---------------- tokens, activations ----------------
     int s = 0;
     uint32_t ph = 0;
@@ -375,7 +379,7 @@ few_tokens_kernel(const __grid_constant__ CUtensorMap mapG, const __grid_constan
     for (int u = lo2; run && u < hi2; ++u) {
       const int ta = u / KB2, k = u - ta * KB2, a = ta % A;
       if (a != seen && checked < A) {  // (the experts come round in order)
-        run = poll_warp([&]() { return ld_acquire(ready + a) == (uint32_t)nt1; }, abort_flag, p.status);
+        run = poll_warp([&]() { return ld_relaxed(ready + a) == (uint32_t)nt1; }, abort_flag, p.status);
         if (!run) break;
         seen = a;
         ++checked;
@@ -459,48 +463,58 @@ few_tokens_kernel(const __grid_constant__ CUtensorMap mapG, const __grid_constan
     }
     umma_commit_warp(drain);
     mbar_wait_warp(drain, 0, abort_flag, p.status, false);
-  } else if (warp < 6) {
+  } else if (warp < 10) {
     // ---------------- epilogue: lanes are weight rows, columns are tokens ----------------
+    // Two warps of a lane quarter, half of the columns each.
+    constexpr int NC = NP / 2;           // columns of this warp
+    constexpr int CH = NC < 16 ? NC : 16;  // read at a time
     const int quarter = warp & 3, r = quarter * 32 + lane;
+    const int col0 = ((warp - 2) >> 2) * NC;
+    const int T = min(p.T - col0, NC);   // tokens of this warp (none: <= 0)
     const bool lead = threadIdx.x == 64;
-    const uint32_t tq = tmem + ((uint32_t)(quarter * 32) << 16);
+    const uint32_t tq = tmem + ((uint32_t)(quarter * 32) << 16) + col0;
     int it = 0;
     bool run = epi_all(all_clear());  // (while the first weights are under way)
+    // Counts this CTA's part of a tile; whether it was the last one.  The
+    // barrier orders every thread's partials before the one release.
     auto arrive_last = [&](uint32_t* w, int pieces) {
-      __threadfence();
-      epi_sync();  // every thread's partials are written
+      epi_sync();
       if (lead) *flag = add_acq_rel(w) == (uint32_t)pieces - 1;
       epi_sync();
-      const bool last = *flag != 0;
-      epi_sync();  // read by all before the next use
-      return last;
+      return *flag != 0;
     };
     for (int u = lo1; run && u < hi1; ++it) {
       const int tile = u / KB1, kb = u - tile * KB1, len = min(KB1 - kb, hi1 - u);
       const int a = tile / nt1, e = list[a], i = (tile % nt1) * 128 + r;
       const bool in = i < p.I;
       const int acc = it & 1;
+      float gsc = 1.f, usc = 1.f;
+      if (I8 && in) gsc = p.gs[(size_t)e * p.I + i], usc = p.us[(size_t)e * p.I + i];
       run = epi_all(mbar_wait_warp(t_full(acc), (it >> 1) & 1, abort_flag, p.status));
       if (!run) break;
       tc_fence_after();
       const uint32_t d = tq + acc * 2 * NP;
       const bool whole = len == KB1;
-      float gsc = 1.f, usc = 1.f;
-      if (I8 && in) gsc = p.gs[(size_t)e * p.I + i], usc = p.us[(size_t)e * p.I + i];
-      __nv_bfloat16* act = p.act + (size_t)a * p.T * p.I + i;
+      __nv_bfloat16* act = p.act + ((size_t)a * p.T + col0) * p.I + i;
       const size_t pstride = (size_t)p.T * 256;  // floats of a partial
-      float* mine = p.part1 + ((size_t)cta * 2 + (u == lo1 ? 0 : 1)) * pstride + r;
+      float* part = p.part1 + (size_t)col0 * 256 + r;
+      float* mine = part + ((size_t)cta * 2 + (u == lo1 ? 0 : 1)) * pstride;
 #pragma unroll
-      for (int c0 = 0; c0 < NP; c0 += 16) {
-        if (c0 >= p.T) break;
-        uint32_t gv[16], uv[16];
-        tmem_ld_32x32b_x16(d + c0, gv);
-        tmem_ld_32x32b_x16(d + NP + c0, uv);
+      for (int c0 = 0; c0 < NC; c0 += CH) {
+        if (c0 >= T) break;
+        uint32_t gv[CH], uv[CH];
+        if constexpr (CH == 16) {
+          tmem_ld_32x32b_x16(d + c0, gv);
+          tmem_ld_32x32b_x16(d + NP + c0, uv);
+        } else {
+          tmem_ld_32x32b_x8(d + c0, gv);
+          tmem_ld_32x32b_x8(d + NP + c0, uv);
+        }
         tmem_ld_wait();
 #pragma unroll
-        for (int j = 0; j < 16; ++j) {
+        for (int j = 0; j < CH; ++j) {
           const int t = c0 + j;
-          if (t < p.T) {
+          if (t < T) {
             const float gg = __uint_as_float(gv[j]) * gsc, uu = __uint_as_float(uv[j]) * usc;
             if (whole) {
               if (in) act[(size_t)t * p.I] = __float2bfloat16_rn(swiglu(gg, uu));
@@ -515,57 +529,68 @@ few_tokens_kernel(const __grid_constant__ CUtensorMap mapG, const __grid_constan
       mbar_arrive_warp(t_empty(acc));
       bool done = whole;
       if (!whole) {
-        int c_lo, c_hi;
-        const int t0 = tile * KB1, pieces = pieces_of(U1, t0, KB1, G, c_lo, c_hi);
-        done = arrive_last(cnt1 + tile, pieces);
+        // the CTAs with a part of this tile; only the first can have begun
+        // before it (its second partial then)
+        const int t0 = tile * KB1, c_lo = cta_of(U1, t0, G1), c_hi = cta_of(U1, t0 + KB1 - 1, G1);
+        done = arrive_last(cnt1 + tile, c_hi - c_lo + 1);
         if (done && in) {
-          // 16 tokens at a time: their loads are in flight together
-          for (int t = 0; t < p.T; t += 16) {
-            float gg[16], uu[16];
+          const float* q0 = part + ((size_t)c_lo * 2 + (first_unit(U1, c_lo, G1) < t0 ? 1 : 0)) * pstride;
+          const float* q1 = part + (size_t)(c_lo + 1) * 2 * pstride;
+          const int more = c_hi - c_lo;
+          // 8 tokens of 2 parts at a time: their loads are in flight together
+          for (int t = 0; t < T; t += 8) {
+            float gg[8], uu[8];
 #pragma unroll
-            for (int j = 0; j < 16; ++j) gg[j] = uu[j] = 0.f;
-            for (int c = c_lo; c <= c_hi; ++c) {
-              const int f = first_unit(U1, c, G);
-              if (f == first_unit(U1, c + 1, G)) continue;
-              const float* q = p.part1 + ((size_t)c * 2 + (f >= t0 ? 0 : 1)) * pstride + r + t * 256;
+            for (int j = 0; j < 8; ++j) {
+              gg[j] = t + j < T ? __ldcg(q0 + (t + j) * 256) : 0.f;
+              uu[j] = t + j < T ? __ldcg(q0 + (t + j) * 256 + 128) : 0.f;
+            }
+            for (int c = 0; c < more; c += 2) {
+              float g2[2][8], u2[2][8];
 #pragma unroll
-              for (int j = 0; j < 16; ++j) {
-                if (t + j < p.T) {
-                  gg[j] += __ldcg(q + j * 256);
-                  uu[j] += __ldcg(q + j * 256 + 128);
+              for (int k = 0; k < 2; ++k) {
+                const float* q = q1 + (size_t)(c + k) * 2 * pstride + t * 256;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                  const bool on = c + k < more && t + j < T;
+                  g2[k][j] = on ? __ldcg(q + j * 256) : 0.f;
+                  u2[k][j] = on ? __ldcg(q + j * 256 + 128) : 0.f;
                 }
               }
+#pragma unroll
+              for (int k = 0; k < 2; ++k)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) gg[j] += g2[k][j], uu[j] += u2[k][j];
             }
 #pragma unroll
-            for (int j = 0; j < 16; ++j)
-              if (t + j < p.T) act[(size_t)(t + j) * p.I] = __float2bfloat16_rn(swiglu(gg[j], uu[j]));
+            for (int j = 0; j < 8; ++j)
+              if (t + j < T) act[(size_t)(t + j) * p.I] = __float2bfloat16_rn(swiglu(gg[j], uu[j]));
           }
         }
       }
       if (done) {
         asm volatile("fence.proxy.async.global;" ::: "memory");
-        __threadfence();
         epi_sync();
         if (lead) (void)add_acq_rel(ready + a);
       }
       u += len;
     }
-    float sum[NP];
+    float sum[NC];
 #pragma unroll
-    for (int t = 0; t < NP; ++t) sum[t] = 0.f;
+    for (int t = 0; t < NC; ++t) sum[t] = 0.f;
     for (int u = lo2; run && u < hi2; ++it) {
       const int ta = u / KB2, kb = u - ta * KB2, len = min(KB2 - kb, hi2 - u);
       const int tile = ta / A, a = ta - tile * A, e = list[a], h = tile * 128 + r;
       const bool in = h < p.H;
-      // the tokens that chose this expert, and their weights: lane, lane + 32
-      float w0 = 0.f, w1 = 0.f;
-      bool m0 = false, m1 = false;
-      for (int k = 0; k < p.K; ++k) {
-        if (lane < p.T && slot[lane * p.K + k] == e) m0 = true, w0 = prob[lane * p.K + k];
-        if (NP > 32 && lane + 32 < p.T && slot[(lane + 32) * p.K + k] == e)
-          m1 = true, w1 = prob[(lane + 32) * p.K + k];
+      // the tokens of this warp that chose the expert, and their weights
+      float w = 0.f;
+      bool m = false;
+      if (lane < T) {
+        const int f = (col0 + lane) * p.K;
+        for (int k = 0; k < p.K; ++k)
+          if (slot[f + k] == e) m = true, w = prob[f + k];
       }
-      const uint32_t b0 = __ballot_sync(0xffffffffu, m0), b1 = NP > 32 ? __ballot_sync(0xffffffffu, m1) : 0u;
+      const uint32_t mask = __ballot_sync(0xffffffffu, m);
       const float dsc = I8 && in ? p.ds[(size_t)e * p.H + h] : 1.f;
       const int acc = it & 1;
       run = epi_all(mbar_wait_warp(t_full(acc), (it >> 1) & 1, abort_flag, p.status));
@@ -573,67 +598,77 @@ few_tokens_kernel(const __grid_constant__ CUtensorMap mapG, const __grid_constan
       tc_fence_after();
       const uint32_t d = tq + acc * 2 * NP;
 #pragma unroll
-      for (int c0 = 0; c0 < NP; c0 += 16) {
-        const uint32_t bits = ((c0 < 32 ? b0 : b1) >> (c0 & 31)) & 0xffffu;
+      for (int c0 = 0; c0 < NC; c0 += CH) {
+        const uint32_t bits = (mask >> c0) & ((1u << CH) - 1u);
         if (bits == 0u) continue;
-        uint32_t v[16];
-        tmem_ld_32x32b_x16(d + c0, v);
+        uint32_t v[CH];
+        if constexpr (CH == 16) tmem_ld_32x32b_x16(d + c0, v);
+        else tmem_ld_32x32b_x8(d + c0, v);
         tmem_ld_wait();
 #pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          const float w = __shfl_sync(0xffffffffu, c0 < 32 ? w0 : w1, (c0 + j) & 31);
-          if ((bits >> j) & 1u) sum[c0 + j] = fmaf(w, __uint_as_float(v[j]) * dsc, sum[c0 + j]);
+        for (int j = 0; j < CH; ++j) {
+          const float wj = __shfl_sync(0xffffffffu, w, c0 + j);
+          if ((bits >> j) & 1u) sum[c0 + j] = fmaf(wj, __uint_as_float(v[j]) * dsc, sum[c0 + j]);
         }
       }
       tc_fence_before();
       mbar_arrive_warp(t_empty(acc));
       u += len;
-      const int t0 = tile * A * KB2, t1 = t0 + A * KB2;  // units of the tile
-      if (u == t1 || u == hi2) {
-        const bool whole = lo2 <= t0 && u == t1;
+      const int n = A * KB2, t0 = tile * n;  // units of the tile
+      if (u == t0 + n || u == hi2) {
+        const bool whole = lo2 <= t0 && u == t0 + n;
         const size_t pstride = (size_t)p.T * 128;
+        float* part = p.part2 + (size_t)col0 * 128 + r;
         auto put = [&](int t, float y) {
-          if (p.shared_x) y += __bfloat162float(p.shared_x[(size_t)t * p.H + h]);
-          p.out[(size_t)t * p.H + h] = __float2bfloat16_rn(y);
+          const size_t at = (size_t)(col0 + t) * p.H + h;
+          if (p.shared_x) y += __bfloat162float(p.shared_x[at]);
+          p.out[at] = __float2bfloat16_rn(y);
         };
-        float* mine = p.part2 + ((size_t)cta * 2 + (lo2 >= t0 ? 0 : 1)) * pstride + r;
+        float* mine = part + ((size_t)cta * 2 + (lo2 >= t0 ? 0 : 1)) * pstride;
 #pragma unroll
-        for (int t = 0; t < NP; ++t) {
-          if (t < p.T) {
+        for (int t = 0; t < NC; ++t) {
+          if (t < T) {
             if (!whole) mine[t * 128] = sum[t];
             else if (in) put(t, sum[t]);
           }
           sum[t] = 0.f;
         }
         if (!whole) {
-          int c_lo, c_hi;
-          const int pieces = pieces_of(U2, t0, A * KB2, G, c_lo, c_hi);
-          if (arrive_last(cnt2 + tile, pieces) && in) {
-            for (int t = 0; t < p.T; t += 16) {
-              float y[16];
+          const int c_lo = cta_of(U2, t0, G2), c_hi = cta_of(U2, t0 + n - 1, G2);
+          if (arrive_last(cnt2 + tile, c_hi - c_lo + 1) && in) {
+            const float* q0 = part + ((size_t)c_lo * 2 + (first_unit(U2, c_lo, G2) < t0 ? 1 : 0)) * pstride;
+            const float* q1 = part + (size_t)(c_lo + 1) * 2 * pstride;
+            const int more = c_hi - c_lo;
+            for (int t = 0; t < T; t += 8) {
+              float y[8];
 #pragma unroll
-              for (int j = 0; j < 16; ++j) y[j] = 0.f;
-              for (int c = c_lo; c <= c_hi; ++c) {
-                const int f = first_unit(U2, c, G);
-                if (f == first_unit(U2, c + 1, G)) continue;
-                const float* q = p.part2 + ((size_t)c * 2 + (f >= t0 ? 0 : 1)) * pstride + r + t * 128;
+              for (int j = 0; j < 8; ++j) y[j] = t + j < T ? __ldcg(q0 + (t + j) * 128) : 0.f;
+              for (int c = 0; c < more; c += 4) {
+                float y2[4][8];
 #pragma unroll
-                for (int j = 0; j < 16; ++j)
-                  if (t + j < p.T) y[j] += __ldcg(q + j * 128);
+                for (int k = 0; k < 4; ++k) {
+                  const float* q = q1 + (size_t)(c + k) * 2 * pstride + t * 128;
+#pragma unroll
+                  for (int j = 0; j < 8; ++j) y2[k][j] = c + k < more && t + j < T ? __ldcg(q + j * 128) : 0.f;
+                }
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+#pragma unroll
+                  for (int j = 0; j < 8; ++j) y[j] += y2[k][j];
               }
 #pragma unroll
-              for (int j = 0; j < 16; ++j)
-                if (t + j < p.T) put(t + j, y[j]);
+              for (int j = 0; j < 8; ++j)
+                if (t + j < T) put(t + j, y[j]);
             }
           }
         }
       }
     }
-  } else if (I8 && warp >= 8) {
+  } else if (I8 && warp >= 12) {
     // ---------------- expand: 8-bit rows to bf16 in tensor memory ----------------
     // Phase 1: one warp of a quarter takes the gate rows, the other the up
     // rows.  Phase 2: one k half each.
-    const int quarter = warp & 3, j = (warp - 8) >> 2, r = quarter * 32 + lane;
+    const int quarter = warp & 3, j = (warp - 12) >> 2, r = quarter * 32 + lane;
     const uint32_t row = base + r * 128 + ((r & 7) << 4);
     const uint32_t dst = tmem + 256 + ((uint32_t)(quarter * 32) << 16);
     const int n1 = hi1 - lo1, n = n1 + hi2 - lo2;

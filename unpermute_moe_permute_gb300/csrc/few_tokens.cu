@@ -46,24 +46,12 @@ namespace moe {
 namespace tc {
 namespace {
 
+#ifndef FEW_STAGES
+#define FEW_STAGES 4
+#endif
 constexpr int kMaxCtas = 160;
 constexpr int kMaxSlots = MOE_FEW_TOKENS * kMaxK;
 constexpr uint32_t kBox16 = 128 * 128;  // bytes of a weight box: 128 rows of 128 bytes
-
-// Expert of slot (t, k), or -1 for a slot that adds nothing (inactive,
-// special, out of range or repeated).
-__device__ __forceinline__ int slot_expert(const int32_t* ids, const uint8_t* mask, int mask_dims,
-                                           int t, int k, int K, int E, int E_all, int32_t* status) {
-  const int e = ids[t * K + k];
-  bool bad = e < 0 || e >= E_all;
-  for (int j = 0; j < k; ++j) bad |= ids[t * K + j] == e;
-  if (bad) {
-    set_status(status, MOE_ERR_BAD_ID);
-    return -1;
-  }
-  if (mask != nullptr && mask[mask_dims == 1 ? t : t * K + k] == 0) return -1;
-  return e < E ? e : -1;
-}
 
 struct FewParams {
   const int32_t* ids;
@@ -84,10 +72,10 @@ template <int NP, bool I8>
 struct FewTraits {
   static constexpr uint32_t b_box = NP * 128;            // 64 k of the tokens
   static constexpr uint32_t stage = 2 * kBox16 + 2 * b_box;
-  static constexpr int stages = NP == 64 ? 4 : 5;
-  static constexpr int threads = (I8 ? 20 : 11) * 32;
+  static constexpr int stages = FEW_STAGES;
+  static constexpr int threads = (I8 ? 20 : 12) * 32;
   static constexpr int k1 = I8 ? 128 : 64;               // k of a phase-1 unit
-  static constexpr int bars = 2 * stages + 4 + 4 + 1;
+  static constexpr int bars = 2 * stages + 4 + 4 + 2;
   static constexpr uint32_t ctrl = stages * stage;
   static constexpr uint32_t holder = ctrl + 8 * bars;     // tensor memory, abort, flag, A
   static constexpr uint32_t bitmap = holder + 16;          // 32 words, then 32 prefixes
@@ -213,7 +201,7 @@ few_tokens_kernel(const __grid_constant__ CUtensorMap mapG, const __grid_constan
   auto t_empty = [&](int a) { return bars + 8u * (2 * S + 2 + a); };
   auto c_full = [&](int b) { return bars + 8u * (2 * S + 4 + b); };
   auto c_empty = [&](int b) { return bars + 8u * (2 * S + 6 + b); };
-  const uint32_t drain = bars + 8u * (2 * S + 8);
+  const uint32_t drain = bars + 8u * (2 * S + 8), clear = bars + 8u * (2 * S + 9);
   uint32_t* holder = reinterpret_cast<uint32_t*>(g + TR::holder);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(holder + 1);
   volatile int* flag = reinterpret_cast<volatile int*>(holder + 2);
@@ -236,6 +224,7 @@ few_tokens_kernel(const __grid_constant__ CUtensorMap mapG, const __grid_constan
       mbar_init(c_empty(a), 1);
     }
     mbar_init(drain, 1);
+    mbar_init(clear, 1);
     *abort_flag = 0;
     mbar_fence_init();
     tma_prefetch_desc(&mapG);
@@ -249,20 +238,31 @@ few_tokens_kernel(const __grid_constant__ CUtensorMap mapG, const __grid_constan
     tmem_relinquish();
   }
   // this CTA's share of the counters, then its flag
+  const unsigned long long epoch = *p.epoch, tag = tag_of(epoch);
   const int n_count = p.A_max + p.A_max * ((p.I + 127) / 128) + (p.H + 127) / 128;
   for (int i = cta * TR::threads + threadIdx.x; i < n_count; i += G * TR::threads) p.count[i] = 0u;
-  const unsigned long long epoch = *p.epoch, tag = tag_of(epoch);
   // the slots' experts, and the experts that some slot chose, in order
   if (threadIdx.x < 32) bitmap[threadIdx.x] = 0u;
   __syncthreads();
+  int32_t* ids = reinterpret_cast<int32_t*>(g);  // (in the ring, which is not in use yet)
   for (int f = threadIdx.x; f < TK; f += TR::threads) {
-    const int t = f / p.K;
-    const int e = slot_expert(p.ids, p.mask, p.mask_dims, t, f - t * p.K, p.K, p.E, p.E_all,
-                              cta == 0 ? p.status : nullptr);
-    slot[f] = (int16_t)e;
+    ids[f] = p.ids[f];
     prob[f] = p.probs[f];
+    slot[f] = p.mask == nullptr ? 1 : p.mask[p.mask_dims == 1 ? f / p.K : f];
+  }
+  __syncthreads();
+  for (int f = threadIdx.x; f < TK; f += TR::threads) {
+    // -1: a slot that adds nothing (inactive, special, out of range or repeated)
+    const int k = f % p.K;
+    int e = ids[f];
+    bool bad = e < 0 || e >= p.E_all;
+    for (int j = 1; j <= k; ++j) bad |= ids[f - j] == e;
+    if (bad && cta == 0) set_status(p.status, MOE_ERR_BAD_ID);
+    if (bad || slot[f] == 0 || e >= p.E) e = -1;
+    slot[f] = (int16_t)e;
     if (e >= 0) atomicOr(&bitmap[e >> 5], 1u << (e & 31));
   }
+  fence_proxy_async_smem();  // (before TMA writes where the ids were)
   __syncthreads();
   if (threadIdx.x == 32)
     asm volatile("st.release.gpu.global.u64 [%0], %1;" ::"l"(p.epoch + 1 + cta), "l"(tag) : "memory");
@@ -294,19 +294,24 @@ few_tokens_kernel(const __grid_constant__ CUtensorMap mapG, const __grid_constan
   uint32_t* cnt2 = cnt1 + (size_t)p.A_max * nt1;
   unsigned long long* flags = p.epoch + 1;
 
-  // every CTA's counters are clear (and every CTA has read the epoch)
-  auto all_clear = [&]() {
-    return poll_warp([&]() {
+  // One warp waits until every CTA's counters are clear (and every CTA has read
+  // the epoch), while the first weights are under way.
+  if (warp == 11) {
+    const bool ok = poll_warp([&]() {
       unsigned long long w[(kMaxCtas + 31) / 32];
 #pragma unroll
       for (int i = 0; i < (kMaxCtas + 31) / 32; ++i)
         w[i] = lane + 32 * i < G ? ld_relaxed(flags + lane + 32 * i) : tag;
-      bool ok = true;
+      bool all = true;
 #pragma unroll
-      for (int i = 0; i < (kMaxCtas + 31) / 32; ++i) ok &= w[i] == tag;
-      return ok;
+      for (int i = 0; i < (kMaxCtas + 31) / 32; ++i) all &= w[i] == tag;
+      return all;
     }, abort_flag, p.status);
-  };
+    if (ok) {
+      if (cta == 0 && lane == 0) *p.epoch = epoch + 1;
+      mbar_arrive_warp(clear);
+    }
+  }
 
   if (A == 0) {
     for (int i = cta * TR::threads + threadIdx.x; i < p.T * p.H; i += G * TR::threads)
@@ -373,8 +378,7 @@ few_tokens_kernel(const __grid_constant__ CUtensorMap mapG, const __grid_constan
       __syncwarp();
       if (++s == S) s = 0, ph ^= 1u;
     }
-    if (run) run = all_clear();
-    if (run && cta == 0 && lane == 0) *p.epoch = epoch + 1;
+    if (run) run = mbar_wait_warp(clear, 0, abort_flag, p.status);
     int seen = -1, checked = 0;  // last expert; experts known to be complete
     for (int u = lo2; run && u < hi2; ++u) {
       const int ta = u / KB2, k = u - ta * KB2, a = ta % A;
@@ -474,9 +478,10 @@ few_tokens_kernel(const __grid_constant__ CUtensorMap mapG, const __grid_constan
     const bool lead = threadIdx.x == 64;
     const uint32_t tq = tmem + ((uint32_t)(quarter * 32) << 16) + col0;
     int it = 0;
-    bool run = epi_all(all_clear());  // (while the first weights are under way)
+    bool run = true;
     // Counts this CTA's part of a tile; whether it was the last one.  The
     // barrier orders every thread's partials before the one release.
+    run = epi_all(mbar_wait_warp(clear, 0, abort_flag, p.status));
     auto arrive_last = [&](uint32_t* w, int pieces) {
       epi_sync();
       if (lead) *flag = add_acq_rel(w) == (uint32_t)pieces - 1;
@@ -578,7 +583,7 @@ few_tokens_kernel(const __grid_constant__ CUtensorMap mapG, const __grid_constan
     float sum[NC];
 #pragma unroll
     for (int t = 0; t < NC; ++t) sum[t] = 0.f;
-    for (int u = lo2; run && u < hi2; ++it) {
+    for (int u = run ? lo2 : hi2; u < hi2; ++it) {
       const int ta = u / KB2, kb = u - ta * KB2, len = min(KB2 - kb, hi2 - u);
       const int tile = ta / A, a = ta - tile * A, e = list[a], h = tile * 128 + r;
       const bool in = h < p.H;
@@ -593,8 +598,8 @@ few_tokens_kernel(const __grid_constant__ CUtensorMap mapG, const __grid_constan
       const uint32_t mask = __ballot_sync(0xffffffffu, m);
       const float dsc = I8 && in ? p.ds[(size_t)e * p.H + h] : 1.f;
       const int acc = it & 1;
-      run = epi_all(mbar_wait_warp(t_full(acc), (it >> 1) & 1, abort_flag, p.status));
-      if (!run) break;
+      // (a warp whose wait ran out still comes to the tile's barrier)
+      run = run && mbar_wait_warp(t_full(acc), (it >> 1) & 1, abort_flag, p.status);
       tc_fence_after();
       const uint32_t d = tq + acc * 2 * NP;
 #pragma unroll
@@ -616,6 +621,8 @@ few_tokens_kernel(const __grid_constant__ CUtensorMap mapG, const __grid_constan
       u += len;
       const int n = A * KB2, t0 = tile * n;  // units of the tile
       if (u == t0 + n || u == hi2) {
+        run = epi_all(run);
+        if (!run) break;
         const bool whole = lo2 <= t0 && u == t0 + n;
         const size_t pstride = (size_t)p.T * 128;
         float* part = p.part2 + (size_t)col0 * 128 + r;
@@ -667,7 +674,8 @@ few_tokens_kernel(const __grid_constant__ CUtensorMap mapG, const __grid_constan
   } else if (I8 && warp >= 12) {
     // ---------------- expand: 8-bit rows to bf16 in tensor memory ----------------
     // Phase 1: one warp of a quarter takes the gate rows, the other the up
-    // rows.  Phase 2: one k half each.
+    // rows.  Phase 2: the two take alternate units (and arrive twice, the
+    // barriers count 8 warps).
     const int quarter = warp & 3, j = (warp - 12) >> 2, r = quarter * 32 + lane;
     const uint32_t row = base + r * 128 + ((r & 7) << 4);
     const uint32_t dst = tmem + 256 + ((uint32_t)(quarter * 32) << 16);
@@ -675,33 +683,34 @@ few_tokens_kernel(const __grid_constant__ CUtensorMap mapG, const __grid_constan
     int s = 0, c = 0;
     uint32_t ph = 0, cph = 0;
     for (int i = 0; i < n; ++i) {
-      if (!mbar_wait_warp(full(s), ph, abort_flag, p.status)) break;
       const bool one = i < n1;  // phase 1
-      const uint32_t src = row + s * TR::stage + (one ? j * kBox16 : 0);
-      const int c0 = one ? 0 : 4 * j;  // first 16-byte chunk
-      uint4 v[4];
-      uint32_t f[32];
+      if (one || c == j) {
+        if (!mbar_wait_warp(full(s), ph, abort_flag, p.status)) break;
+        const uint32_t src = row + s * TR::stage + (one ? j * kBox16 : 0);
+        uint4 v[4];
+        uint32_t f[32];
 #pragma unroll
-      for (int q = 0; q < 4; ++q) v[q] = ld_shared_v4(src ^ ((c0 + q) << 4));
+        for (int q = 0; q < 4; ++q) v[q] = ld_shared_v4(src ^ (q << 4));
 #pragma unroll
-      for (int q = 0; q < 4; ++q) expand16_bf16(v[q], f + 8 * q);
-      if (one) {
+        for (int q = 0; q < 4; ++q) expand16_bf16(v[q], f + 8 * q);
 #pragma unroll
         for (int q = 0; q < 4; ++q) v[q] = ld_shared_v4(src ^ ((4 + q) << 4));
-      }
-      if (!mbar_wait_warp(c_empty(c), cph ^ 1u, abort_flag, p.status)) break;
-      tc_fence_after();
-      const uint32_t a = dst + c * 128 + (one ? j * 64 : j * 32);
-      tmem_st_32x32b_x32(a, f);
-      if (one) {
+        if (!mbar_wait_warp(c_empty(c), cph ^ 1u, abort_flag, p.status)) break;
+        tc_fence_after();
+        const uint32_t a = dst + c * 128 + (one ? j * 64 : 0);
+        tmem_st_32x32b_x32(a, f);
 #pragma unroll
         for (int q = 0; q < 4; ++q) expand16_bf16(v[q], f + 8 * q);
         tmem_st_32x32b_x32(a + 32, f);
+        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive_warp(c_full(c));
+        mbar_arrive_warp(empty(s));
+        if (!one) {
+          mbar_arrive_warp(c_full(c));
+          mbar_arrive_warp(empty(s));
+        }
       }
-      tmem_st_wait();
-      tc_fence_before();
-      mbar_arrive_warp(c_full(c));
-      mbar_arrive_warp(empty(s));
       c ^= 1;
       if (c == 0) cph ^= 1u;
       if (++s == S) s = 0, ph ^= 1u;

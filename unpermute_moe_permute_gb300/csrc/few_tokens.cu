@@ -7,17 +7,18 @@
 // experts' weights, so the kernel is a stream of weights that does not pause:
 //
 //   * one CTA per SM, and each phase's weights cut into equal runs of 32 KB
-//     units (128 rows x 128 bytes of two matrices or of two k blocks): CTA c
-//     takes units [U c / G, U (c + 1) / G), whatever tiles they fall in, so all
-//     SMs read the same amount.  A tile that several CTAs share is summed from
-//     their fp32 partials, in the order of the CTAs, by the one that finishes
-//     last;
+//     units (128 bytes of k of 128 gate and 128 up rows, or of 256 down rows):
+//     CTA c takes units [U c / G, U (c + 1) / G), whatever tiles they fall in,
+//     so all SMs read the same amount.  A tile that several CTAs share is
+//     summed from their fp32 partials in the order of the CTAs: in phase 1 by
+//     the one that finishes last, in phase 2 each of them sums a share of the
+//     tile when all have finished;
 //   * the weights are the A operand (M = 128 of their rows), the tokens the B
 //     operand (N = 16, 32 or 64): every active expert is multiplied with all
 //     tokens, which the tensor cores have time for (at N = 64 under a fifth of
 //     the stream's time), and a (token, expert) pair that was not chosen is
 //     left out when the result is read;
-//   * one warp streams weights through a ring of 4 or 5 stages (TMA) without
+//   * one warp streams weights through a ring of 4 to 6 stages (TMA) without
 //     ever waiting for results: at the turn from phase 1 to phase 2 it fills
 //     the ring with down weights while the last activations are still being
 //     made.  Another warp loads the tokens' and activations' tiles and alone
@@ -46,9 +47,6 @@ namespace moe {
 namespace tc {
 namespace {
 
-#ifndef FEW_STAGES
-#define FEW_STAGES 4
-#endif
 constexpr int kMaxCtas = 160;
 constexpr int kMaxSlots = MOE_FEW_TOKENS * kMaxK;
 constexpr uint32_t kBox16 = 128 * 128;  // bytes of a weight box: 128 rows of 128 bytes
@@ -61,7 +59,7 @@ struct FewParams {
   const __nv_bfloat16* shared_x;
   __nv_bfloat16* out;
   __nv_bfloat16* act;          // [A, T, I]
-  float *part1, *part2;        // [CTA][2][T][2][128], [CTA][2][T][128]
+  float *part1, *part2;        // [CTA][2][T][2][128], [CTA][2][T][256]
   unsigned long long* epoch;   // epoch, flag of each CTA
   uint32_t* count;             // ready[A], tiles of phase 1, tiles of phase 2
   int32_t* status;
@@ -70,11 +68,11 @@ struct FewParams {
 
 template <int NP, bool I8>
 struct FewTraits {
+  static constexpr int k = I8 ? 128 : 64;                // k of a unit
   static constexpr uint32_t b_box = NP * 128;            // 64 k of the tokens
-  static constexpr uint32_t stage = 2 * kBox16 + 2 * b_box;
-  static constexpr int stages = FEW_STAGES;
-  static constexpr int threads = (I8 ? 20 : 12) * 32;
-  static constexpr int k1 = I8 ? 128 : 64;               // k of a phase-1 unit
+  static constexpr uint32_t stage = 2 * kBox16 + (I8 ? 2 : 1) * b_box;
+  static constexpr int stages = (int)(212992 / stage) < 6 ? (int)(212992 / stage) : 6;
+  static constexpr int threads = (I8 ? 16 : 12) * 32;
   static constexpr int bars = 2 * stages + 4 + 4 + 2;
   static constexpr uint32_t ctrl = stages * stage;
   static constexpr uint32_t holder = ctrl + 8 * bars;     // tensor memory, abort, flag, A
@@ -215,12 +213,12 @@ few_tokens_kernel(const __grid_constant__ CUtensorMap mapG, const __grid_constan
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
       mbar_init(full(s), 2);               // weights, tokens
-      mbar_init(empty(s), I8 ? 9 : 1);     // MMAs (and the expanding warps)
+      mbar_init(empty(s), I8 ? 5 : 1);     // MMAs (and the expanding warps)
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(t_full(a), 1);
       mbar_init(t_empty(a), 8);  // the epilogue warps
-      mbar_init(c_full(a), 8);
+      mbar_init(c_full(a), 4);
       mbar_init(c_empty(a), 1);
     }
     mbar_init(drain, 1);
@@ -239,7 +237,7 @@ few_tokens_kernel(const __grid_constant__ CUtensorMap mapG, const __grid_constan
   }
   // this CTA's share of the counters, then its flag
   const unsigned long long epoch = *p.epoch, tag = tag_of(epoch);
-  const int n_count = p.A_max + p.A_max * ((p.I + 127) / 128) + (p.H + 127) / 128;
+  const int n_count = p.A_max + p.A_max * ((p.I + 127) / 128) + (p.H + 255) / 256;
   for (int i = cta * TR::threads + threadIdx.x; i < n_count; i += G * TR::threads) p.count[i] = 0u;
   // the slots' experts, and the experts that some slot chose, in order
   if (threadIdx.x < 32) bitmap[threadIdx.x] = 0u;
@@ -283,8 +281,8 @@ few_tokens_kernel(const __grid_constant__ CUtensorMap mapG, const __grid_constan
   tc_fence_after();
   const uint32_t tmem = uniform(holder[0]);
   const int A = (int)uniform(holder[3]);
-  const int nt1 = (p.I + 127) / 128, nt2 = (p.H + 127) / 128;
-  const int KB1 = (p.H + TR::k1 - 1) / TR::k1, KB2 = (p.I + 127) / 128;
+  const int nt1 = (p.I + 127) / 128, nt2 = (p.H + 255) / 256;
+  const int KB1 = (p.H + TR::k - 1) / TR::k, KB2 = (p.I + TR::k - 1) / TR::k;
   const int U1 = A * nt1 * KB1, U2 = nt2 * A * KB2;
   const int G1 = min(G, U1), G2 = min(G, U2);
   const int lo1 = cta < G1 ? first_unit(U1, cta, G1) : 0, hi1 = cta < G1 ? first_unit(U1, cta + 1, G1) : 0;
@@ -336,21 +334,21 @@ few_tokens_kernel(const __grid_constant__ CUtensorMap mapG, const __grid_constan
           if (!(run = slot_free())) break;
           const uint32_t a = base + s * TR::stage;
           mbar_arrive_expect_tx(full(s), 2 * kBox16);
-          tma_load_3d(a, &mapG, full(s), k * TR::k1, i0, e);
-          tma_load_3d(a + kBox16, &mapU, full(s), k * TR::k1, i0, e);
+          tma_load_3d(a, &mapG, full(s), k * TR::k, i0, e);
+          tma_load_3d(a + kBox16, &mapU, full(s), k * TR::k, i0, e);
           next();
         }
         u += len;
       }
       for (int u = lo2; run && u < hi2;) {
         const int ta = u / KB2, kb = u - ta * KB2, len = min(KB2 - kb, hi2 - u);
-        const int e = list[ta % A], h0 = (ta / A) * 128;
+        const int e = list[ta % A], h0 = (ta / A) * 256;
         for (int k = kb; k < kb + len; ++k) {
           if (!(run = slot_free())) break;
           const uint32_t a = base + s * TR::stage;
-          mbar_arrive_expect_tx(full(s), I8 ? kBox16 : 2 * kBox16);
-          tma_load_3d(a, &mapD, full(s), k * 128, h0, e);
-          if constexpr (!I8) tma_load_3d(a + kBox16, &mapD, full(s), k * 128 + 64, h0, e);
+          mbar_arrive_expect_tx(full(s), 2 * kBox16);
+          tma_load_3d(a, &mapD, full(s), k * TR::k, h0, e);
+          tma_load_3d(a + kBox16, &mapD, full(s), k * TR::k, h0 + 128, e);
           next();
         }
         u += len;
@@ -372,8 +370,8 @@ few_tokens_kernel(const __grid_constant__ CUtensorMap mapG, const __grid_constan
       if (lane == 0) {
         const uint32_t b = base + s * TR::stage + 2 * kBox16;
         mbar_arrive_expect_tx(full(s), I8 ? 2 * TR::b_box : TR::b_box);
-        tma_load_2d(b, &mapX, full(s), k * TR::k1, 0);
-        if constexpr (I8) tma_load_2d(b + TR::b_box, &mapX, full(s), k * TR::k1 + 64, 0);
+        tma_load_2d(b, &mapX, full(s), k * TR::k, 0);
+        if constexpr (I8) tma_load_2d(b + TR::b_box, &mapX, full(s), k * TR::k + 64, 0);
       }
       __syncwarp();
       if (++s == S) s = 0, ph ^= 1u;
@@ -392,9 +390,9 @@ few_tokens_kernel(const __grid_constant__ CUtensorMap mapG, const __grid_constan
       if (lane == 0) {
         asm volatile("fence.proxy.async.global;" ::: "memory");
         const uint32_t b = base + s * TR::stage + 2 * kBox16;
-        mbar_arrive_expect_tx(full(s), 2 * TR::b_box);
-        tma_load_3d(b, &mapAct, full(s), k * 128, 0, a);
-        tma_load_3d(b + TR::b_box, &mapAct, full(s), k * 128 + 64, 0, a);
+        mbar_arrive_expect_tx(full(s), I8 ? 2 * TR::b_box : TR::b_box);
+        tma_load_3d(b, &mapAct, full(s), k * TR::k, 0, a);
+        if constexpr (I8) tma_load_3d(b + TR::b_box, &mapAct, full(s), k * TR::k + 64, 0, a);
       }
       __syncwarp();
       if (++s == S) s = 0, ph ^= 1u;
@@ -407,7 +405,7 @@ few_tokens_kernel(const __grid_constant__ CUtensorMap mapG, const __grid_constan
     uint32_t ph = 0, cph = 0;
     bool run = true;
     // one segment: len units of one tile (phase 1) or one tile and expert (phase 2)
-    auto segment = [&](int len, bool up) {
+    auto segment = [&](int len) {
       const int acc = it & 1;
       run = mbar_wait_warp(t_empty(acc), ((it >> 1) & 1) ^ 1u, abort_flag, p.status);
       if (!run) return;
@@ -430,7 +428,7 @@ few_tokens_kernel(const __grid_constant__ CUtensorMap mapG, const __grid_constan
           for (int kk = 0; kk < 8; ++kk) {
             const uint64_t b = bd + (kk >> 2) * (TR::b_box >> 4) + (kk & 3) * 2;
             umma_f16_ta_warp<false>(d, a + kk * 8, b, idesc, accum);
-            if (up) umma_f16_ta_warp<false>(d + NP, a + 64 + kk * 8, b, idesc, accum);
+            umma_f16_ta_warp<false>(d + NP, a + 64 + kk * 8, b, idesc, accum);
             accum = 1u;
           }
           umma_commit_warp(c_empty(c));
@@ -440,13 +438,8 @@ few_tokens_kernel(const __grid_constant__ CUtensorMap mapG, const __grid_constan
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk) {
             umma_f16_warp<false>(d, ad + kk * 2, bd + kk * 2, idesc, accum);
-            if (up) umma_f16_warp<false>(d + NP, ad + (kBox16 >> 4) + kk * 2, bd + kk * 2, idesc, accum);
+            umma_f16_warp<false>(d + NP, ad + (kBox16 >> 4) + kk * 2, bd + kk * 2, idesc, accum);
             accum = 1u;
-          }
-          if (!up) {
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              umma_f16_warp<false>(d, ad + (kBox16 >> 4) + kk * 2, bd + (TR::b_box >> 4) + kk * 2, idesc, 1u);
           }
         }
         umma_commit_warp(empty(s));
@@ -457,12 +450,12 @@ few_tokens_kernel(const __grid_constant__ CUtensorMap mapG, const __grid_constan
     };
     for (int u = lo1; run && u < hi1;) {
       const int len = min(KB1 - u % KB1, hi1 - u);
-      segment(len, true);
+      segment(len);
       u += len;
     }
     for (int u = lo2; run && u < hi2;) {
       const int len = min(KB2 - u % KB2, hi2 - u);
-      segment(len, false);
+      segment(len);
       u += len;
     }
     umma_commit_warp(drain);
@@ -580,137 +573,140 @@ few_tokens_kernel(const __grid_constant__ CUtensorMap mapG, const __grid_constan
       }
       u += len;
     }
-    float sum[NC];
+    // Phase 2: the two warps of a quarter take 128 of the tile's 256 rows each,
+    // and all columns.
+    constexpr int CP = 16;  // columns read at a time
+    const int rset = (warp - 2) >> 2, r2 = rset * 128 + r;
+    const uint32_t tq2 = tmem + ((uint32_t)(quarter * 32) << 16) + rset * NP;
+    const size_t pstride = (size_t)p.T * 256;  // floats of a partial
+    const int n = A * KB2;                      // units of a tile
+    auto put = [&](int t, int h, float y) {
+      const size_t at = (size_t)t * p.H + h;
+      if (p.shared_x) y += __bfloat162float(p.shared_x[at]);
+      p.out[at] = __float2bfloat16_rn(y);
+    };
+    float sum[NP];
 #pragma unroll
-    for (int t = 0; t < NC; ++t) sum[t] = 0.f;
+    for (int t = 0; t < NP; ++t) sum[t] = 0.f;
     for (int u = run ? lo2 : hi2; u < hi2; ++it) {
       const int ta = u / KB2, kb = u - ta * KB2, len = min(KB2 - kb, hi2 - u);
-      const int tile = ta / A, a = ta - tile * A, e = list[a], h = tile * 128 + r;
+      const int tile = ta / A, a = ta - tile * A, e = list[a], h = tile * 256 + r2;
       const bool in = h < p.H;
-      // the tokens of this warp that chose the expert, and their weights
-      float w = 0.f;
-      bool m = false;
-      if (lane < T) {
-        const int f = (col0 + lane) * p.K;
-        for (int k = 0; k < p.K; ++k)
-          if (slot[f + k] == e) m = true, w = prob[f + k];
+      // the tokens that chose the expert, and their weights: lane, lane + 32
+      float w0 = 0.f, w1 = 0.f;
+      bool m0 = false, m1 = false;
+      for (int k = 0; k < p.K; ++k) {
+        if (lane < p.T && slot[lane * p.K + k] == e) m0 = true, w0 = prob[lane * p.K + k];
+        if (NP > 32 && lane + 32 < p.T && slot[(lane + 32) * p.K + k] == e)
+          m1 = true, w1 = prob[(lane + 32) * p.K + k];
       }
-      const uint32_t mask = __ballot_sync(0xffffffffu, m);
+      const uint32_t b0 = __ballot_sync(0xffffffffu, m0), b1 = NP > 32 ? __ballot_sync(0xffffffffu, m1) : 0u;
       const float dsc = I8 && in ? p.ds[(size_t)e * p.H + h] : 1.f;
       const int acc = it & 1;
       // (a warp whose wait ran out still comes to the tile's barrier)
       run = run && mbar_wait_warp(t_full(acc), (it >> 1) & 1, abort_flag, p.status);
       tc_fence_after();
-      const uint32_t d = tq + acc * 2 * NP;
+      const uint32_t d = tq2 + acc * 2 * NP;
 #pragma unroll
-      for (int c0 = 0; c0 < NC; c0 += CH) {
-        const uint32_t bits = (mask >> c0) & ((1u << CH) - 1u);
+      for (int c0 = 0; c0 < NP; c0 += CP) {
+        const uint32_t bits = ((c0 < 32 ? b0 : b1) >> (c0 & 31)) & ((1u << CP) - 1u);
         if (bits == 0u) continue;
-        uint32_t v[CH];
-        if constexpr (CH == 16) tmem_ld_32x32b_x16(d + c0, v);
-        else tmem_ld_32x32b_x8(d + c0, v);
+        uint32_t v[CP];
+        tmem_ld_32x32b_x16(d + c0, v);
         tmem_ld_wait();
 #pragma unroll
-        for (int j = 0; j < CH; ++j) {
-          const float wj = __shfl_sync(0xffffffffu, w, c0 + j);
-          if ((bits >> j) & 1u) sum[c0 + j] = fmaf(wj, __uint_as_float(v[j]) * dsc, sum[c0 + j]);
+        for (int j = 0; j < CP; ++j) {
+          const float w = __shfl_sync(0xffffffffu, c0 < 32 ? w0 : w1, (c0 + j) & 31);
+          if ((bits >> j) & 1u) sum[c0 + j] = fmaf(w, __uint_as_float(v[j]) * dsc, sum[c0 + j]);
         }
       }
       tc_fence_before();
       mbar_arrive_warp(t_empty(acc));
       u += len;
-      const int n = A * KB2, t0 = tile * n;  // units of the tile
+      const int t0 = tile * n;
       if (u == t0 + n || u == hi2) {
         run = epi_all(run);
         if (!run) break;
         const bool whole = lo2 <= t0 && u == t0 + n;
-        const size_t pstride = (size_t)p.T * 128;
-        float* part = p.part2 + (size_t)col0 * 128 + r;
-        auto put = [&](int t, float y) {
-          const size_t at = (size_t)(col0 + t) * p.H + h;
-          if (p.shared_x) y += __bfloat162float(p.shared_x[at]);
-          p.out[at] = __float2bfloat16_rn(y);
-        };
-        float* mine = part + ((size_t)cta * 2 + (lo2 >= t0 ? 0 : 1)) * pstride;
+        float* mine = p.part2 + ((size_t)cta * 2 + (lo2 >= t0 ? 0 : 1)) * pstride + r2;
 #pragma unroll
-        for (int t = 0; t < NC; ++t) {
-          if (t < T) {
-            if (!whole) mine[t * 128] = sum[t];
-            else if (in) put(t, sum[t]);
+        for (int t = 0; t < NP; ++t) {
+          if (t < p.T) {
+            if (!whole) mine[t * 256] = sum[t];
+            else if (in) put(t, h, sum[t]);
           }
           sum[t] = 0.f;
         }
         if (!whole) {
-          const int c_lo = cta_of(U2, t0, G2), c_hi = cta_of(U2, t0 + n - 1, G2);
-          if (arrive_last(cnt2 + tile, c_hi - c_lo + 1) && in) {
-            const float* q0 = part + ((size_t)c_lo * 2 + (first_unit(U2, c_lo, G2) < t0 ? 1 : 0)) * pstride;
-            const float* q1 = part + (size_t)(c_lo + 1) * 2 * pstride;
-            const int more = c_hi - c_lo;
-            for (int t = 0; t < T; t += 8) {
-              float y[8];
-#pragma unroll
-              for (int j = 0; j < 8; ++j) y[j] = t + j < T ? __ldcg(q0 + (t + j) * 128) : 0.f;
-              for (int c = 0; c < more; c += 4) {
-                float y2[4][8];
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                  const float* q = q1 + (size_t)(c + k) * 2 * pstride + t * 128;
-#pragma unroll
-                  for (int j = 0; j < 8; ++j) y2[k][j] = c + k < more && t + j < T ? __ldcg(q + j * 128) : 0.f;
-                }
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-#pragma unroll
-                  for (int j = 0; j < 8; ++j) y[j] += y2[k][j];
-              }
-#pragma unroll
-              for (int j = 0; j < 8; ++j)
-                if (t + j < T) put(t + j, y[j]);
-            }
-          }
+          epi_sync();
+          if (lead) (void)add_acq_rel(cnt2 + tile);
         }
+      }
+    }
+    // Tiles that this CTA shared: its share of their sums, once all parts are
+    // there.  (At most two: the first and the last of its run.)
+    for (int k = 0; run && lo2 < hi2 && k < 2; ++k) {
+      const int tile = k == 0 ? lo2 / n : (hi2 - 1) / n, t0 = tile * n;
+      if ((k == 1 && tile == lo2 / n) || (lo2 <= t0 && hi2 >= t0 + n)) continue;
+      const int c_lo = cta_of(U2, t0, G2), c_hi = cta_of(U2, t0 + n - 1, G2), parts = c_hi - c_lo + 1;
+      run = epi_all(poll_warp([&]() { return ld_relaxed(cnt2 + tile) == (uint32_t)parts; }, abort_flag, p.status));
+      if (!run) break;
+      const float* q0 = p.part2 + ((size_t)c_lo * 2 + (first_unit(U2, c_lo, G2) < t0 ? 1 : 0)) * pstride;
+      const float* q1 = p.part2 + (size_t)(c_lo + 1) * 2 * pstride;
+      const int total = 256 * p.T, end = (int)((long long)total * (cta - c_lo + 1) / parts);
+      for (int i = (int)((long long)total * (cta - c_lo) / parts) + (int)threadIdx.x - 64; i < end; i += 256) {
+        float y = __ldcg(q0 + i);
+        for (int c = 0; c < parts - 1; c += 8) {
+          float v[8];
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            v[j] = c + j < parts - 1 ? __ldcg(q1 + (size_t)(c + j) * 2 * pstride + i) : 0.f;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) y += v[j];
+        }
+        const int t = i >> 8, h = tile * 256 + (i & 255);
+        if (h < p.H) put(t, h, y);
       }
     }
   } else if (I8 && warp >= 12) {
     // ---------------- expand: 8-bit rows to bf16 in tensor memory ----------------
-    // Phase 1: one warp of a quarter takes the gate rows, the other the up
-    // rows.  Phase 2: the two take alternate units (and arrive twice, the
-    // barriers count 8 warps).
-    const int quarter = warp & 3, j = (warp - 12) >> 2, r = quarter * 32 + lane;
+    // A lane takes one row of each of the unit's two boxes.
+    const int quarter = warp & 3, r = quarter * 32 + lane;
     const uint32_t row = base + r * 128 + ((r & 7) << 4);
     const uint32_t dst = tmem + 256 + ((uint32_t)(quarter * 32) << 16);
-    const int n1 = hi1 - lo1, n = n1 + hi2 - lo2;
+    const int n = hi1 - lo1 + hi2 - lo2;
     int s = 0, c = 0;
     uint32_t ph = 0, cph = 0;
     for (int i = 0; i < n; ++i) {
-      const bool one = i < n1;  // phase 1
-      if (one || c == j) {
-        if (!mbar_wait_warp(full(s), ph, abort_flag, p.status)) break;
-        const uint32_t src = row + s * TR::stage + (one ? j * kBox16 : 0);
-        uint4 v[4];
-        uint32_t f[32];
+      if (!mbar_wait_warp(full(s), ph, abort_flag, p.status)) break;
+      const uint32_t src = row + s * TR::stage, a = dst + c * 128;
+      uint4 v[4];
+      uint32_t f[32];
+      auto load = [&](int half) {  // 64 bytes: half & 1 of box half >> 1
 #pragma unroll
-        for (int q = 0; q < 4; ++q) v[q] = ld_shared_v4(src ^ (q << 4));
-#pragma unroll
-        for (int q = 0; q < 4; ++q) expand16_bf16(v[q], f + 8 * q);
-#pragma unroll
-        for (int q = 0; q < 4; ++q) v[q] = ld_shared_v4(src ^ ((4 + q) << 4));
-        if (!mbar_wait_warp(c_empty(c), cph ^ 1u, abort_flag, p.status)) break;
-        tc_fence_after();
-        const uint32_t a = dst + c * 128 + (one ? j * 64 : 0);
-        tmem_st_32x32b_x32(a, f);
+        for (int q = 0; q < 4; ++q)
+          v[q] = ld_shared_v4((src + (half >> 1) * kBox16) ^ ((4 * (half & 1) + q) << 4));
+      };
+      auto expand = [&]() {
 #pragma unroll
         for (int q = 0; q < 4; ++q) expand16_bf16(v[q], f + 8 * q);
-        tmem_st_32x32b_x32(a + 32, f);
-        tmem_st_wait();
-        tc_fence_before();
-        mbar_arrive_warp(c_full(c));
-        mbar_arrive_warp(empty(s));
-        if (!one) {
-          mbar_arrive_warp(c_full(c));
-          mbar_arrive_warp(empty(s));
-        }
+      };
+      load(0);
+      expand();
+      load(1);
+      if (!mbar_wait_warp(c_empty(c), cph ^ 1u, abort_flag, p.status)) break;
+      tc_fence_after();
+      tmem_st_32x32b_x32(a, f);
+#pragma unroll
+      for (int half = 1; half < 4; ++half) {
+        expand();
+        if (half < 3) load(half + 1);
+        tmem_st_32x32b_x32(a + 32 * half, f);
       }
+      tmem_st_wait();
+      tc_fence_before();
+      mbar_arrive_warp(c_full(c));
+      mbar_arrive_warp(empty(s));
       c ^= 1;
       if (c == 0) cph ^= 1u;
       if (++s == S) s = 0, ph ^= 1u;
@@ -733,9 +729,9 @@ FewLayout few_layout(int T, int K, int H, int I, int E) {
   auto up = [](size_t v) { return (v + 255) & ~(size_t)255; };
   FewLayout l;
   l.words = up(8 * (1 + kMaxCtas));
-  l.counts = up(4 * (A + A * ((I + 127) / 128) + (H + 127) / 128));
+  l.counts = up(4 * (A + A * ((I + 127) / 128) + (H + 255) / 256));
   l.part1 = (size_t)kMaxCtas * 2 * T * 256 * 4;
-  l.part2 = (size_t)kMaxCtas * 2 * T * 128 * 4;
+  l.part2 = (size_t)kMaxCtas * 2 * T * 256 * 4;
   l.act = up(A * T * I * 2);
   l.total = l.words + l.counts + l.part1 + l.part2 + l.act;
   return l;

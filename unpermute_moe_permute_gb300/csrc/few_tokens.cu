@@ -96,6 +96,21 @@ __device__ __forceinline__ int cta_of(int U, int u, int G) {
   return c;
 }
 
+// Tile segments of a run [lo, hi) in the order they are taken: the first and
+// the last, which other CTAs may share, before the whole tiles between them,
+// so that shared tiles are put together while there is other work.
+struct Segments {
+  int lo, hi, KB, first, count;
+  __device__ __forceinline__ Segments(int lo_, int hi_, int KB_)
+      : lo(lo_), hi(hi_), KB(KB_), first(hi_ > lo_ ? lo_ / KB_ : 0),
+        count(hi_ > lo_ ? (hi_ - 1) / KB_ - lo_ / KB_ + 1 : 0) {}
+  __device__ __forceinline__ void get(int i, int& tile, int& u, int& len) const {
+    tile = first + (i == 0 ? 0 : i == 1 ? count - 1 : i - 1);
+    u = max(lo, tile * KB);
+    len = min(hi, (tile + 1) * KB) - u;
+  }
+};
+
 // Tag of an epoch (a mixing function, so that a workspace filled with one
 // byte does not look like its own tag).
 __device__ __forceinline__ unsigned long long tag_of(unsigned long long e) {
@@ -287,6 +302,7 @@ few_tokens_kernel(const __grid_constant__ CUtensorMap mapG, const __grid_constan
   const int G1 = min(G, U1), G2 = min(G, U2);
   const int lo1 = cta < G1 ? first_unit(U1, cta, G1) : 0, hi1 = cta < G1 ? first_unit(U1, cta + 1, G1) : 0;
   const int lo2 = cta < G2 ? first_unit(U2, cta, G2) : 0, hi2 = cta < G2 ? first_unit(U2, cta + 1, G2) : 0;
+  const Segments seg1(lo1, hi1, KB1);
   uint32_t* ready = p.count;
   uint32_t* cnt1 = ready + p.A_max;
   uint32_t* cnt2 = cnt1 + (size_t)p.A_max * nt1;
@@ -327,9 +343,10 @@ few_tokens_kernel(const __grid_constant__ CUtensorMap mapG, const __grid_constan
         if (++s == S) s = 0, ph ^= 1u;
       };
       bool run = true;
-      for (int u = lo1; run && u < hi1;) {
-        const int tile = u / KB1, kb = u - tile * KB1, len = min(KB1 - kb, hi1 - u);
-        const int e = list[tile / nt1], i0 = (tile % nt1) * 128;
+      for (int i = 0; run && i < seg1.count; ++i) {
+        int tile, u, len;
+        seg1.get(i, tile, u, len);
+        const int kb = u - tile * KB1, e = list[tile / nt1], i0 = (tile % nt1) * 128;
         for (int k = kb; k < kb + len; ++k) {
           if (!(run = slot_free())) break;
           const uint32_t a = base + s * TR::stage;
@@ -338,7 +355,6 @@ few_tokens_kernel(const __grid_constant__ CUtensorMap mapG, const __grid_constan
           tma_load_3d(a + kBox16, &mapU, full(s), k * TR::k, i0, e);
           next();
         }
-        u += len;
       }
       for (int u = lo2; run && u < hi2;) {
         const int ta = u / KB2, kb = u - ta * KB2, len = min(KB2 - kb, hi2 - u);
@@ -364,8 +380,10 @@ few_tokens_kernel(const __grid_constant__ CUtensorMap mapG, const __grid_constan
     int s = 0;
     uint32_t ph = 0;
     bool run = true;
-    for (int u = lo1; run && u < hi1; ++u) {
-      const int k = u % KB1;
+    for (int i = 0; run && i < seg1.count; ++i) {
+     int tile, u, len;
+     seg1.get(i, tile, u, len);
+     for (int k = u - tile * KB1; len > 0; ++k, --len) {
       if (!(run = mbar_wait_warp(empty(s), ph ^ 1u, abort_flag, p.status))) break;
       if (lane == 0) {
         const uint32_t b = base + s * TR::stage + 2 * kBox16;
@@ -375,6 +393,7 @@ few_tokens_kernel(const __grid_constant__ CUtensorMap mapG, const __grid_constan
       }
       __syncwarp();
       if (++s == S) s = 0, ph ^= 1u;
+     }
     }
     if (run) run = mbar_wait_warp(clear, 0, abort_flag, p.status);
     int seen = -1, checked = 0;  // last expert; experts known to be complete
@@ -448,10 +467,10 @@ few_tokens_kernel(const __grid_constant__ CUtensorMap mapG, const __grid_constan
       umma_commit_warp(t_full(acc));
       ++it;
     };
-    for (int u = lo1; run && u < hi1;) {
-      const int len = min(KB1 - u % KB1, hi1 - u);
+    for (int i = 0; run && i < seg1.count; ++i) {
+      int tile, u, len;
+      seg1.get(i, tile, u, len);
       segment(len);
-      u += len;
     }
     for (int u = lo2; run && u < hi2;) {
       const int len = min(KB2 - u % KB2, hi2 - u);
@@ -481,8 +500,9 @@ few_tokens_kernel(const __grid_constant__ CUtensorMap mapG, const __grid_constan
       epi_sync();
       return *flag != 0;
     };
-    for (int u = lo1; run && u < hi1; ++it) {
-      const int tile = u / KB1, kb = u - tile * KB1, len = min(KB1 - kb, hi1 - u);
+    for (; run && it < seg1.count; ++it) {
+      int tile, u, len;
+      seg1.get(it, tile, u, len);
       const int a = tile / nt1, e = list[a], i = (tile % nt1) * 128 + r;
       const bool in = i < p.I;
       const int acc = it & 1;
@@ -571,7 +591,6 @@ few_tokens_kernel(const __grid_constant__ CUtensorMap mapG, const __grid_constan
         epi_sync();
         if (lead) (void)add_acq_rel(ready + a);
       }
-      u += len;
     }
     // Phase 2: the two warps of a quarter take 128 of the tile's 256 rows each,
     // and all columns.
@@ -651,21 +670,34 @@ few_tokens_kernel(const __grid_constant__ CUtensorMap mapG, const __grid_constan
       const int c_lo = cta_of(U2, t0, G2), c_hi = cta_of(U2, t0 + n - 1, G2), parts = c_hi - c_lo + 1;
       run = epi_all(poll_warp([&]() { return ld_relaxed(cnt2 + tile) == (uint32_t)parts; }, abort_flag, p.status));
       if (!run) break;
-      const float* q0 = p.part2 + ((size_t)c_lo * 2 + (first_unit(U2, c_lo, G2) < t0 ? 1 : 0)) * pstride;
-      const float* q1 = p.part2 + (size_t)(c_lo + 1) * 2 * pstride;
-      const int total = 256 * p.T, end = (int)((long long)total * (cta - c_lo + 1) / parts);
+      const float4* q0 = reinterpret_cast<const float4*>(
+          p.part2 + ((size_t)c_lo * 2 + (first_unit(U2, c_lo, G2) < t0 ? 1 : 0)) * pstride);
+      const float4* q1 = reinterpret_cast<const float4*>(p.part2 + (size_t)(c_lo + 1) * 2 * pstride);
+      const int total = 64 * p.T, end = (int)((long long)total * (cta - c_lo + 1) / parts);
       for (int i = (int)((long long)total * (cta - c_lo) / parts) + (int)threadIdx.x - 64; i < end; i += 256) {
-        float y = __ldcg(q0 + i);
-        for (int c = 0; c < parts - 1; c += 8) {
-          float v[8];
+        float4 y = __ldcg(q0 + i);
+        for (int c = 0; c < parts - 1; c += 10) {  // loads of ten parts in flight
+          float4 v[10];
 #pragma unroll
-          for (int j = 0; j < 8; ++j)
-            v[j] = c + j < parts - 1 ? __ldcg(q1 + (size_t)(c + j) * 2 * pstride + i) : 0.f;
+          for (int j = 0; j < 10; ++j)
+            v[j] = c + j < parts - 1 ? __ldcg(q1 + (size_t)(c + j) * (pstride / 2) + i)
+                                     : make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) y += v[j];
+          for (int j = 0; j < 10; ++j) y.x += v[j].x, y.y += v[j].y, y.z += v[j].z, y.w += v[j].w;
         }
-        const int t = i >> 8, h = tile * 256 + (i & 255);
-        if (h < p.H) put(t, h, y);
+        const int t = i >> 6, h = tile * 256 + (i & 63) * 4;  // (H is a multiple of 64)
+        if (h < p.H) {
+          const size_t at = (size_t)t * p.H + h;
+          if (p.shared_x) {
+            const uint2 x = *reinterpret_cast<const uint2*>(p.shared_x + at);
+            float f[4];
+            VecTraits<__nv_bfloat16>::unpack2(x.x, f);
+            VecTraits<__nv_bfloat16>::unpack2(x.y, f + 2);
+            y.x += f[0], y.y += f[1], y.z += f[2], y.w += f[3];
+          }
+          *reinterpret_cast<uint2*>(p.out + at) = make_uint2(VecTraits<__nv_bfloat16>::pack2(y.x, y.y),
+                                                             VecTraits<__nv_bfloat16>::pack2(y.z, y.w));
+        }
       }
     }
   } else if (I8 && warp >= 12) {

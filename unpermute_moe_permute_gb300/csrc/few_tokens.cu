@@ -72,7 +72,7 @@ struct FewTraits {
   static constexpr uint32_t b_box = NP * 128;            // 64 k of the tokens
   static constexpr uint32_t stage = 2 * kBox16 + (I8 ? 2 : 1) * b_box;
   static constexpr int stages = (int)(212992 / stage) < 6 ? (int)(212992 / stage) : 6;
-  static constexpr int threads = (I8 ? 16 : 12) * 32;
+  static constexpr int threads = (I8 ? 20 : 12) * 32;
   static constexpr int bars = 2 * stages + 4 + 4 + 2;
   static constexpr uint32_t ctrl = stages * stage;
   static constexpr uint32_t holder = ctrl + 8 * bars;     // tensor memory, abort, flag, A
@@ -228,12 +228,12 @@ few_tokens_kernel(const __grid_constant__ CUtensorMap mapG, const __grid_constan
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
       mbar_init(full(s), 2);               // weights, tokens
-      mbar_init(empty(s), I8 ? 5 : 1);     // MMAs (and the expanding warps)
+      mbar_init(empty(s), I8 ? 9 : 1);     // MMAs (and the expanding warps)
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(t_full(a), 1);
       mbar_init(t_empty(a), 8);  // the epilogue warps
-      mbar_init(c_full(a), 4);
+      mbar_init(c_full(a), 8);
       mbar_init(c_empty(a), 1);
     }
     mbar_init(drain, 1);
@@ -676,14 +676,14 @@ few_tokens_kernel(const __grid_constant__ CUtensorMap mapG, const __grid_constan
       const int total = 64 * p.T, end = (int)((long long)total * (cta - c_lo + 1) / parts);
       for (int i = (int)((long long)total * (cta - c_lo) / parts) + (int)threadIdx.x - 64; i < end; i += 256) {
         float4 y = __ldcg(q0 + i);
-        for (int c = 0; c < parts - 1; c += 10) {  // loads of ten parts in flight
-          float4 v[10];
+        for (int c = 0; c < parts - 1; c += 6) {  // loads of six parts in flight
+          float4 v[6];
 #pragma unroll
-          for (int j = 0; j < 10; ++j)
+          for (int j = 0; j < 6; ++j)
             v[j] = c + j < parts - 1 ? __ldcg(q1 + (size_t)(c + j) * (pstride / 2) + i)
                                      : make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-          for (int j = 0; j < 10; ++j) y.x += v[j].x, y.y += v[j].y, y.z += v[j].z, y.w += v[j].w;
+          for (int j = 0; j < 6; ++j) y.x += v[j].x, y.y += v[j].y, y.z += v[j].z, y.w += v[j].w;
         }
         const int t = i >> 6, h = tile * 256 + (i & 63) * 4;  // (H is a multiple of 64)
         if (h < p.H) {
@@ -702,10 +702,10 @@ few_tokens_kernel(const __grid_constant__ CUtensorMap mapG, const __grid_constan
     }
   } else if (I8 && warp >= 12) {
     // ---------------- expand: 8-bit rows to bf16 in tensor memory ----------------
-    // A lane takes one row of each of the unit's two boxes.
-    const int quarter = warp & 3, r = quarter * 32 + lane;
-    const uint32_t row = base + r * 128 + ((r & 7) << 4);
-    const uint32_t dst = tmem + 256 + ((uint32_t)(quarter * 32) << 16);
+    // A lane takes one row of one of the unit's two boxes.
+    const int quarter = warp & 3, j = (warp - 12) >> 2, r = quarter * 32 + lane;
+    const uint32_t row = base + j * kBox16 + r * 128 + ((r & 7) << 4);
+    const uint32_t dst = tmem + 256 + j * 64 + ((uint32_t)(quarter * 32) << 16);
     const int n = hi1 - lo1 + hi2 - lo2;
     int s = 0, c = 0;
     uint32_t ph = 0, cph = 0;
@@ -714,27 +714,18 @@ few_tokens_kernel(const __grid_constant__ CUtensorMap mapG, const __grid_constan
       const uint32_t src = row + s * TR::stage, a = dst + c * 128;
       uint4 v[4];
       uint32_t f[32];
-      auto load = [&](int half) {  // 64 bytes: half & 1 of box half >> 1
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
-          v[q] = ld_shared_v4((src + (half >> 1) * kBox16) ^ ((4 * (half & 1) + q) << 4));
-      };
-      auto expand = [&]() {
+      for (int q = 0; q < 4; ++q) v[q] = ld_shared_v4(src ^ (q << 4));
 #pragma unroll
-        for (int q = 0; q < 4; ++q) expand16_bf16(v[q], f + 8 * q);
-      };
-      load(0);
-      expand();
-      load(1);
+      for (int q = 0; q < 4; ++q) expand16_bf16(v[q], f + 8 * q);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) v[q] = ld_shared_v4(src ^ ((4 + q) << 4));
       if (!mbar_wait_warp(c_empty(c), cph ^ 1u, abort_flag, p.status)) break;
       tc_fence_after();
       tmem_st_32x32b_x32(a, f);
 #pragma unroll
-      for (int half = 1; half < 4; ++half) {
-        expand();
-        if (half < 3) load(half + 1);
-        tmem_st_32x32b_x32(a + 32 * half, f);
-      }
+      for (int q = 0; q < 4; ++q) expand16_bf16(v[q], f + 8 * q);
+      tmem_st_32x32b_x32(a + 32, f);
       tmem_st_wait();
       tc_fence_before();
       mbar_arrive_warp(c_full(c));

@@ -1,12 +1,22 @@
 // Router: the K largest logits of each token and their weights, and the
 // gradient of the logits.
 //
-// One warp per token; lane i holds the logits i, i + 32, ... of the row in
-// registers (E <= 1024: at most 32 each).  Selection compares 32-bit keys
-// whose unsigned order is the order of the floats: K rounds of a warp-wide
-// maximum (redux), the lowest index among equals, and the winner taken out.
-// Both scores grow with the logit, so no rounded score enters the selection.
+// One warp per token, the row in registers (E <= 1024: at most 32 logits a
+// lane).  Both scores grow with the logit, so no rounded score enters the
+// selection.  Memory asks for 5 us at 16384 x 256 forward and backward
+// together; what bounds the kernels is the instructions of the selection:
+//   * a logit is packed into 32 bits as the upper 22 bits of a key that orders
+//     like the float, and its index counted down: one warp-wide maximum
+//     (redux) gives the largest and, among equals, the lowest index.  bf16
+//     logits fit the 22 bits;
+//   * each lane sorts its packed logits once (a merging network of min / max
+//     pairs) and gives up its head when it wins;
+//   * for fp32 logits, rows where two of the first K + 1 share their 22 bits
+//     without being equal are done again with full keys (two reductions and a
+//     scan a round): about one row in a hundred for normal logits.
 #include <math.h>
+
+#include <type_traits>
 
 #include "common.cuh"
 
@@ -71,15 +81,60 @@ __device__ __forceinline__ float selected_weight(float sel, int lane, int K, int
   return on ? w / s : 0.f;
 }
 
+// Element i of a lane: 16-byte vectors when kVec (16-byte rows, and a lane
+// holds whole vectors), else every 32nd.
+template <typename T, int NPL, bool kVec>
+__device__ __forceinline__ int index_of(int i, int lane) {
+  constexpr int V = VecTraits<T>::kElems;
+  return kVec ? (i / V) * 32 * V + lane * V + i % V : lane + 32 * i;
+}
+
+// The row's logits as the definition takes them, -inf past its end; nan: one
+// of them was a NaN.
+template <typename T, int NPL, bool kVec>
+__device__ __forceinline__ void load_row(const T* row, int E, int lane, float (&v)[NPL], bool& nan) {
+  constexpr int V = VecTraits<T>::kElems;
+  if constexpr (kVec) {
+#pragma unroll
+    for (int i = 0; i < NPL; i += V) {
+      const int j = index_of<T, NPL, kVec>(i, lane);
+      if (j < E) VecTraits<T>::unpack(ld_v4(row + j), v + i);
+      else
+#pragma unroll
+        for (int k = 0; k < V; ++k) v[i + k] = -INFINITY;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < NPL; ++i) v[i] = lane + 32 * i < E ? to_f32(row[lane + 32 * i]) : -INFINITY;
+  }
+#pragma unroll
+  for (int i = 0; i < NPL; ++i) {
+    nan |= v[i] != v[i];
+    v[i] = fminf(fmaxf(v[i], -INFINITY), 3.402823466e+38f) + 0.f;  // NaN: -inf; -0: +0
+  }
+}
+
+// Descending order by a merging network (Batcher's odd-even merge sort).
+template <int N>
+__device__ __forceinline__ void sort_desc(uint32_t (&a)[N]) {
+#pragma unroll
+  for (int p = 1; p < N; p <<= 1)
+#pragma unroll
+    for (int k = p; k >= 1; k >>= 1)
+#pragma unroll
+      for (int j = k % p; j + k < N; j += 2 * k)
+#pragma unroll
+        for (int i = 0; i < k; ++i)
+          if (i + j + k < N && (i + j) / (2 * p) == (i + j + k) / (2 * p)) {
+            const uint32_t x = a[i + j], y = a[i + j + k];
+            a[i + j] = max(x, y);
+            a[i + j + k] = min(x, y);
+          }
+}
+
+// The selection by full keys; lane k < K gets the k-th id.
 template <int NPL, typename T>
-__global__ void __launch_bounds__(kWarps * 32)
-router_topk_kernel(const T* __restrict__ logits, int n_tok, int E, int K, int scoring,
-                   int renormalize, float scale, int32_t* __restrict__ expert_ids,
-                   float* __restrict__ probs, int32_t* status) {
-  const int lane = threadIdx.x & 31;
-  const int t = blockIdx.x * kWarps + (threadIdx.x >> 5);
-  if (t >= n_tok) return;
-  const T* row = logits + (size_t)t * E;
+__device__ __noinline__ int select_exact(const T* row, int E, int K, int lane) {
   uint32_t key[NPL];
   bool nan = false;
 #pragma unroll
@@ -87,21 +142,6 @@ router_topk_kernel(const T* __restrict__ logits, int n_tok, int E, int K, int sc
     const int j = lane + 32 * i;
     key[i] = j < E ? key_of(clean_logit(to_f32(row[j]), nan)) : 0u;
   }
-  if (nan) set_status(status, MOE_ERR_INVALID_ARG);
-  float row_sum = 0.f;
-  if (scoring == MOE_SCORE_SOFTMAX && !renormalize) {
-    uint32_t top = 0;
-#pragma unroll
-    for (int i = 0; i < NPL; ++i) top = max(top, key[i]);
-    const float m = value_of(__reduce_max_sync(kAll, top));
-#pragma unroll
-    for (int i = 0; i < NPL; ++i) {
-      const float v = value_of(key[i]);
-      if (key[i] != 0u && v > -INFINITY) row_sum += expf(v - m);
-    }
-    row_sum = warp_sum(row_sum);
-  }
-  float sel = -INFINITY;
   int sel_id = 0;
   for (int k = 0; k < K; ++k) {
     uint32_t top = 0;
@@ -116,9 +156,68 @@ router_topk_kernel(const T* __restrict__ logits, int n_tok, int E, int K, int sc
 #pragma unroll
     for (int i = 0; i < NPL; ++i)
       if (id == (uint32_t)(lane + 32 * i)) key[i] = 0u;
-    if (lane == k) {
-      sel = value_of(best);
-      sel_id = (int)id;
+    if (lane == k) sel_id = (int)id;
+  }
+  return sel_id;
+}
+
+template <int NPL, bool kVec, typename T>
+__global__ void __launch_bounds__(kWarps * 32)
+router_topk_kernel(const T* __restrict__ logits, int n_tok, int E, int K, int scoring,
+                   int renormalize, float scale, int32_t* __restrict__ expert_ids,
+                   float* __restrict__ probs, int32_t* status) {
+  const int lane = threadIdx.x & 31;
+  const int t = blockIdx.x * kWarps + (threadIdx.x >> 5);
+  if (t >= n_tok) return;
+  const T* row = logits + (size_t)t * E;
+  float v[NPL];
+  bool nan = false;
+  load_row<T, NPL, kVec>(row, E, lane, v, nan);
+  if (nan) set_status(status, MOE_ERR_INVALID_ARG);
+  uint32_t pk[NPL];
+#pragma unroll
+  for (int i = 0; i < NPL; ++i) {
+    const int j = index_of<T, NPL, kVec>(i, lane);
+    pk[i] = j < E ? (key_of(v[i]) & ~1023u) | (uint32_t)(1023 - j) : 0u;
+  }
+  float row_sum = 0.f;
+  if (scoring == MOE_SCORE_SOFTMAX && !renormalize) {
+    float m = v[0];
+#pragma unroll
+    for (int i = 1; i < NPL; ++i) m = fmaxf(m, v[i]);
+    m = value_of(__reduce_max_sync(kAll, key_of(m)));
+    if (m > -INFINITY) {
+#pragma unroll
+      for (int i = 0; i < NPL; ++i) row_sum += __expf(v[i] - m);
+      row_sum = warp_sum(row_sum);
+    }
+  }
+  sort_desc(pk);
+  const int rounds = min(K + 1, E);
+  uint32_t mine = 0u;  // lane k: the k-th of the packed logits
+  for (int k = 0; k < rounds; ++k) {
+    const uint32_t best = __reduce_max_sync(kAll, pk[0]);
+    const bool won = pk[0] == best;
+#pragma unroll
+    for (int i = 0; i + 1 < NPL; ++i) pk[i] = won ? pk[i + 1] : pk[i];
+    if (won) pk[NPL - 1] = 0u;
+    if (lane == k) mine = best;
+  }
+  int sel_id = 1023 - (int)(mine & 1023u);
+  const bool on = lane < rounds;
+  float sel = on ? to_f32(row[sel_id]) : 0.f;
+  sel = fminf(fmaxf(sel, -INFINITY), 3.402823466e+38f) + 0.f;
+  if constexpr (sizeof(T) == 4) {
+    // equal 22 bits of different logits, or at the edge of the selection
+    // (where further logits may share them): again, with full keys
+    const uint32_t next = __shfl_down_sync(kAll, mine, 1);
+    const float next_sel = __shfl_down_sync(kAll, sel, 1);
+    const bool again = lane + 1 < rounds && (mine >> 10) == (next >> 10) &&
+                       (sel != next_sel || lane == K - 1);
+    if (__any_sync(kAll, again)) {
+      sel_id = select_exact<NPL>(row, E, K, lane);
+      sel = lane < K ? to_f32(row[sel_id]) : 0.f;
+      sel = fminf(fmaxf(sel, -INFINITY), 3.402823466e+38f) + 0.f;
     }
   }
   const float q = selected_weight(sel, lane, K, scoring, renormalize != 0, row_sum);
@@ -128,7 +227,24 @@ router_topk_kernel(const T* __restrict__ logits, int n_tok, int E, int K, int sc
   }
 }
 
-template <int NPL, typename T>
+// The dense part of a gradient row: -c v[i], or zeros.
+template <typename T, int NPL, bool kVec>
+__device__ __forceinline__ void store_row(T* row, int E, int lane, const float (&v)[NPL]) {
+  constexpr int V = VecTraits<T>::kElems;
+  if constexpr (kVec) {
+#pragma unroll
+    for (int i = 0; i < NPL; i += V) {
+      const int j = index_of<T, NPL, kVec>(i, lane);
+      if (j < E) st_v4(row + j, VecTraits<T>::pack(v + i));
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < NPL; ++i)
+      if (lane + 32 * i < E) put(row + lane + 32 * i, v[i]);
+  }
+}
+
+template <int NPL, bool kVec, typename T>
 __global__ void __launch_bounds__(kWarps * 32)
 router_grad_kernel(const float* __restrict__ grad_probs, const T* __restrict__ logits,
                    const int32_t* __restrict__ expert_ids, int n_tok, int E, int K, int scoring,
@@ -143,55 +259,59 @@ router_grad_kernel(const float* __restrict__ grad_probs, const T* __restrict__ l
   float g = 0.f, sel = -INFINITY;
   if (lane < K) {
     id = expert_ids[(size_t)t * K + lane];
+    g = scale * grad_probs[(size_t)t * K + lane];
+  }
+  const bool full_row = scoring == MOE_SCORE_SOFTMAX && !renormalize;
+  float v[NPL];
+  if (full_row) load_row<T, NPL, kVec>(row, E, lane, v, nan);
+  if (lane < K) {
     if (id < 0 || id >= E) {
       set_status(status, MOE_ERR_BAD_ID);
       id = -1;
+      g = 0.f;
     } else {
-      g = scale * grad_probs[(size_t)t * K + lane];
       sel = clean_logit(to_f32(row[id]), nan);
     }
   }
-  // the largest selected logit, whatever the order of the ids
-  const float m_sel = value_of(__reduce_max_sync(kAll, key_of(sel)));
-  float d = 0.f;
-  if (scoring == MOE_SCORE_SOFTMAX && !renormalize) {
-    float v[NPL], m = -INFINITY;
-#pragma unroll
-    for (int i = 0; i < NPL; ++i) {
-      const int j = lane + 32 * i;
-      v[i] = j < E ? clean_logit(to_f32(row[j]), nan) : -INFINITY;
-      m = fmaxf(m, v[i]);
+  // an id named twice collects both gradients
+  const unsigned same = __match_any_sync(kAll, lane < K ? id : -1 - lane);
+  const bool twice = __any_sync(kAll, lane < K && id >= 0 && (same & (same - 1)) != 0u);
+  auto collect = [&](float x) {
+    if (!twice) return x;
+    float s = 0.f;
+    for (int k = 0; k < K; ++k) {
+      const int ik = __shfl_sync(kAll, id, k);
+      const float xk = __shfl_sync(kAll, x, k);
+      if (ik == id) s += xk;
     }
+    return s;
+  };
+  const bool on = sel > -INFINITY;
+  float d = 0.f;
+  if (full_row) {
+    float m = v[0];
+#pragma unroll
+    for (int i = 1; i < NPL; ++i) m = fmaxf(m, v[i]);
     m = value_of(__reduce_max_sync(kAll, key_of(m)));
     float s = 0.f;
 #pragma unroll
     for (int i = 0; i < NPL; ++i) {
-      v[i] = v[i] > -INFINITY ? expf(v[i] - m) : 0.f;
+      v[i] = v[i] > -INFINITY ? __expf(v[i] - m) : 0.f;
       s += v[i];
     }
     s = warp_sum(s);
     const float inv = s > 0.f ? 1.f / s : 0.f;
-    const float q = sel > -INFINITY ? expf(sel - m) * inv : 0.f;
-    const float D = warp_sum(q > 0.f ? g * q : 0.f);
+    const float q = on ? __expf(sel - m) * inv : 0.f;
+    const float D = warp_sum(on ? g * q : 0.f), c = inv * D;
 #pragma unroll
-    for (int i = 0; i < NPL; ++i) {
-      const int j = lane + 32 * i;
-      if (j < E) put(drow + j, v[i] > 0.f ? -(v[i] * inv) * D : 0.f);
-    }
-    float gs = 0.f;  // an id named twice collects both gradients
-    for (int k = 0; k < K; ++k) {
-      const int ik = __shfl_sync(kAll, id, k);
-      const float gk = __shfl_sync(kAll, g, k);
-      if (ik == id) gs += gk;
-    }
-    d = q > 0.f ? q * (gs - D) : 0.f;
+    for (int i = 0; i < NPL; ++i) v[i] = v[i] > 0.f ? -v[i] * c : 0.f;
+    const float both = collect(g);
+    d = on ? q * (both - D) : 0.f;
   } else {
 #pragma unroll
-    for (int i = 0; i < NPL; ++i) {
-      const int j = lane + 32 * i;
-      if (j < E) put(drow + j, 0.f);
-    }
-    const bool on = sel > -INFINITY;
+    for (int i = 0; i < NPL; ++i) v[i] = 0.f;
+    // the largest selected logit, whatever the order of the ids
+    const float m_sel = value_of(__reduce_max_sync(kAll, key_of(sel)));
     float q = 0.f, mine;
     if (scoring == MOE_SCORE_SOFTMAX) {
       q = on ? expf(sel - m_sel) : 0.f;
@@ -208,12 +328,9 @@ router_grad_kernel(const float* __restrict__ grad_probs, const T* __restrict__ l
     }
     // 1 - sigmoid(l) = 1 / (1 + e^l)
     if (scoring == MOE_SCORE_SIGMOID && on) mine *= 1.f / (1.f + expf(sel));
-    for (int k = 0; k < K; ++k) {
-      const int ik = __shfl_sync(kAll, id, k);
-      const float mk = __shfl_sync(kAll, mine, k);
-      if (ik == id) d += mk;
-    }
+    d = collect(mine);
   }
+  store_row<T, NPL, kVec>(drow, E, lane, v);
   if (nan) set_status(status, MOE_ERR_INVALID_ARG);
   __syncwarp();  // the row's values are in place before the selected ones replace theirs
   if (lane < K && id >= 0) put(drow + id, d);
@@ -229,14 +346,24 @@ int check_router(const void* logits, int dtype, int T, int E, int K, int scoring
   return MOE_OK;
 }
 
+// f(logits per lane, 16-byte vectors) for rows of E logits.  Vectors need rows
+// of whole vectors and a lane that holds whole ones.
 template <typename T, typename F>
 void by_width(int E, F&& f) {
-  if (E <= 32) f(std::integral_constant<int, 1>{});
-  else if (E <= 64) f(std::integral_constant<int, 2>{});
-  else if (E <= 128) f(std::integral_constant<int, 4>{});
-  else if (E <= 256) f(std::integral_constant<int, 8>{});
-  else if (E <= 512) f(std::integral_constant<int, 16>{});
-  else f(std::integral_constant<int, 32>{});
+  constexpr int V = VecTraits<T>::kElems;
+  const bool vec = E % V == 0;
+  auto go = [&](auto n) {
+    if constexpr (decltype(n)::value >= V) {
+      if (vec) return f(n, std::true_type{});
+    }
+    f(n, std::false_type{});
+  };
+  if (E <= 32) go(std::integral_constant<int, 1>{});
+  else if (E <= 64) go(std::integral_constant<int, 2>{});
+  else if (E <= 128) go(std::integral_constant<int, 4>{});
+  else if (E <= 256) go(std::integral_constant<int, 8>{});
+  else if (E <= 512) go(std::integral_constant<int, 16>{});
+  else go(std::integral_constant<int, 32>{});
 }
 
 }  // namespace
@@ -253,9 +380,9 @@ extern "C" int moe_router_topk(const void* logits, int dtype, int T, int E, int 
     return MOE_ERR_INVALID_ARG;
   const int grid = (T + kWarps - 1) / kWarps;
   auto go = [&](auto* x) {
-    using D = std::remove_pointer_t<decltype(x)>;
-    by_width<D>(E, [&](auto n) {
-      router_topk_kernel<decltype(n)::value, std::remove_const_t<D>><<<grid, kWarps * 32, 0, stream>>>(
+    using D = std::remove_const_t<std::remove_pointer_t<decltype(x)>>;
+    by_width<D>(E, [&](auto n, auto vec) {
+      router_topk_kernel<decltype(n)::value, decltype(vec)::value, D><<<grid, kWarps * 32, 0, stream>>>(
           x, T, E, K, scoring, renormalize, scale, expert_ids, probs, dev_status);
     });
   };
@@ -278,8 +405,8 @@ extern "C" int moe_router_topk_grad(const float* grad_probs, const void* logits,
   const int grid = (T + kWarps - 1) / kWarps;
   auto go = [&](auto* x, auto* d) {
     using D = std::remove_pointer_t<decltype(d)>;
-    by_width<D>(E, [&](auto n) {
-      router_grad_kernel<decltype(n)::value, D><<<grid, kWarps * 32, 0, stream>>>(
+    by_width<D>(E, [&](auto n, auto vec) {
+      router_grad_kernel<decltype(n)::value, decltype(vec)::value, D><<<grid, kWarps * 32, 0, stream>>>(
           grad_probs, x, expert_ids, T, E, K, scoring, renormalize, scale, d, dev_status);
     });
   };

@@ -138,6 +138,14 @@ def _stream() -> int:
     return torch.cuda.current_stream().cuda_stream
 
 
+# The raw handle of the same stream without building a Stream object (1 us a
+# call), where torch has it.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+if _raw_stream is not None:
+    def _stream() -> int:  # noqa: F811
+        return _raw_stream(torch.cuda.current_device())
+
+
 def _ptr(t: Optional[torch.Tensor]):
     if t is None:
         return None
@@ -561,7 +569,7 @@ def _scoring(name: str) -> int:
 
 
 def _shape(t: Optional[torch.Tensor], shape: tuple, name: str):
-    if t is not None and tuple(t.shape) != shape:
+    if t is not None and t.shape != shape:
         raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
 
 
@@ -571,9 +579,9 @@ def moe_router_topk(logits, K: int, *, scoring: str = "softmax", renormalize: bo
     (float32 or bfloat16): (expert_ids [T, K] int32, probs [T, K] float32)."""
     T, E = logits.shape
     if expert_ids is None:
-        expert_ids = torch.empty((T, K), dtype=torch.int32, device=logits.device)
+        expert_ids = logits.new_empty((T, K), dtype=torch.int32)
     if probs is None:
-        probs = torch.empty((T, K), dtype=torch.float32, device=logits.device)
+        probs = logits.new_empty((T, K), dtype=torch.float32)
     _check(expert_ids, torch.int32, "expert_ids")
     _check(probs, torch.float32, "probs")
     _shape(expert_ids, (T, K), "expert_ids")
@@ -617,9 +625,9 @@ def moe_quantize_rows(x, *, row_map=None, K: int = 1, N: Optional[int] = None, q
     if N is None:
         N = T * K if row_map is not None else T
     if q is None:
-        q = torch.empty((N, H), dtype=torch.int8, device=x.device)
+        q = x.new_empty((N, H), dtype=torch.int8)
     if scale is None:
-        scale = torch.empty(N, dtype=torch.float32, device=x.device)
+        scale = x.new_empty(N, dtype=torch.float32)
     _check(q, torch.int8, "q")
     _check(scale, torch.float32, "scale")
     _shape(q, (N, H), "q")
@@ -702,18 +710,26 @@ def moe_layer_few_tokens(tokens, expert_ids, probs, W_gate, W_up, W_down, *, sca
     if workspace is None:
         ws = moe_layer_few_tokens_workspace_size(T, K, H, I, E)
         workspace = torch.empty(max(ws, 16), dtype=torch.uint8, device=tokens.device)
-    for t, dt, shape, n in ((tokens, torch.bfloat16, (T, H), "tokens"),
-                            (expert_ids, torch.int32, (T, K), "expert_ids"),
-                            (probs, torch.float32, (T, K), "probs"),
-                            (W_gate, wdt, (E, I, H), "W_gate"), (W_up, wdt, (E, I, H), "W_up"),
-                            (W_down, wdt, (E, H, I), "W_down"),
-                            (gs, torch.float32, (E, I), "gate scale"),
-                            (us, torch.float32, (E, I), "up scale"),
-                            (ds, torch.float32, (E, H), "down scale"),
-                            (shared_x, torch.bfloat16, (T, H), "shared_x"),
-                            (out, torch.bfloat16, (T, H), "out")):
-        _check(t, dt, n)
-        _shape(t, shape, n)
+    bf16, f32 = torch.bfloat16, torch.float32
+    if not (tokens.dtype is bf16 and out.dtype is bf16 and expert_ids.dtype is torch.int32
+            and probs.dtype is f32 and W_gate.dtype is wdt and W_up.dtype is wdt
+            and W_down.dtype is wdt and expert_ids.shape[0] == T and probs.shape == expert_ids.shape
+            and tokens.shape == out.shape and W_gate.shape == (E, I, H)
+            and W_up.shape == (E, I, H) and W_down.shape == (E, H, I)
+            and (scales is None or (gs.dtype is f32 and us.dtype is f32 and ds.dtype is f32
+                                    and gs.shape == (E, I) and us.shape == (E, I)
+                                    and ds.shape == (E, H)))
+            and (shared_x is None or (shared_x.dtype is bf16 and shared_x.shape == tokens.shape))):
+        for t, dt, shape, n in ((tokens, bf16, (T, H), "tokens"),
+                                (expert_ids, torch.int32, (T, K), "expert_ids"),
+                                (probs, f32, (T, K), "probs"),
+                                (W_gate, wdt, (E, I, H), "W_gate"), (W_up, wdt, (E, I, H), "W_up"),
+                                (W_down, wdt, (E, H, I), "W_down"),
+                                (gs, f32, (E, I), "gate scale"), (us, f32, (E, I), "up scale"),
+                                (ds, f32, (E, H), "down scale"),
+                                (shared_x, bf16, (T, H), "shared_x"), (out, bf16, (T, H), "out")):
+            _check(t, dt, n)
+            _shape(t, shape, n)
     mask = _mask(active_mask, T, K) if active_mask is not None else None
     _call("moe_layer_few_tokens", _ptr(tokens), _ptr(expert_ids), _ptr(probs), T, H, K, I, E,
           num_special, _ptr(mask), mask.dim() if mask is not None else 0,

@@ -11,7 +11,7 @@
 // rounding decision is that of exact arithmetic (127 x / top is a quotient of
 // a 15-bit and an 8-bit integer: a tie exactly, or further from one than the
 // division's error), so x * (127 / top) decides all but the elements within
-// 2^-12 of a tie, and for those the exact residual 127 x - q top (one fma)
+// 2^-15 of a tie, and for those the exact residual 127 x - q top (one fma)
 // does.  fp32 rows divide: their quotients can lie closer to a tie.
 #include <math.h>
 
@@ -46,32 +46,39 @@ struct Rounding {
   float mul, div, k;  // q = rint(x * mul / div), k = mul / div
 };
 
-template <bool kExactQuotient>
-__device__ __forceinline__ uint32_t round_bits(float x, const Rounding& r) {
-  if constexpr (!kExactQuotient) return __float_as_uint(__fdiv_rn(x * r.mul, r.div) + kMagic);
-  const float y = x * r.k;
-  const float z = y + kMagic, d = y - (z - kMagic);
-  uint32_t bits = __float_as_uint(z);
-  if (fabsf(fabsf(d) - 0.5f) < 0x1p-12f) {
-    const float q = z - kMagic, e = fmaf(-q, r.div, x * r.mul);  // exact
-    const float two = 2.f * fabsf(e);
-    if (two > r.div || (two == r.div && (bits & 1u))) bits += e > 0.f ? 1u : 0xffffffffu;
-  }
-  return bits;
-}
-
+// 16 elements in 8 bits.
 template <typename T>
 __device__ __forceinline__ uint4 round16(const Chunk<T>& c, const Rounding& r) {
   float f[16];
   c.get(f);
+  uint32_t b[16];
+  if constexpr (sizeof(T) == 4) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) b[i] = __float_as_uint(__fdiv_rn(f[i] * r.mul, r.div) + kMagic);
+  } else {
+    // x k is within 128 * 2^-23 < 2^-15 of the quotient: only nearer to a tie
+    // than that can its rounding differ
+    bool near = false;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const float y = f[i] * r.k, z = y + kMagic;
+      near |= fabsf(y - (z - kMagic)) > 0.5f - 0x1p-15f;
+      b[i] = __float_as_uint(z);
+    }
+    if (near) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const float q = __uint_as_float(b[i]) - kMagic, e = fmaf(-q, r.div, f[i] * r.mul);  // exact
+        const float two = 2.f * fabsf(e);
+        if (two > r.div || (two == r.div && (b[i] & 1u))) b[i] += e > 0.f ? 1u : 0xffffffffu;
+      }
+    }
+  }
   uint32_t w[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    uint32_t b[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) b[j] = round_bits<sizeof(T) == 2>(f[4 * i + j], r);
-    w[i] = __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410);
-  }
+  for (int i = 0; i < 4; ++i)
+    w[i] = __byte_perm(__byte_perm(b[4 * i], b[4 * i + 1], 0x0040),
+                       __byte_perm(b[4 * i + 2], b[4 * i + 3], 0x0040), 0x5410);
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
@@ -86,12 +93,25 @@ quantize_rows_kernel(const T* __restrict__ x, const int32_t* __restrict__ row_ma
   const int i = threadIdx.x % TPR, lane = threadIdx.x & 31;
   const bool live = t < n_tok;
   const T* row = x + (size_t)t * H;
+  // largest magnitude: of fp32 the bits' maximum; of bf16 two at a time (the
+  // maximum that keeps a NaN)
   uint32_t top = 0;
   auto widen = [&](const Chunk<T>& c) {
-    float f[16];
-    c.get(f);
 #pragma unroll
-    for (int j = 0; j < 16; ++j) top = max(top, __float_as_uint(f[j]) & 0x7fffffffu);
+    for (int j = 0; j < Chunk<T>::n; ++j) {
+      const uint32_t w[4] = {c.v[j].x, c.v[j].y, c.v[j].z, c.v[j].w};
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        if constexpr (sizeof(T) == 4) {
+          top = max(top, w[q] & 0x7fffffffu);
+        } else {
+          const uint32_t a = w[q] & 0x7fff7fffu;
+          const __nv_bfloat162 h = __hmax2_nan(*reinterpret_cast<const __nv_bfloat162*>(&a),
+                                               *reinterpret_cast<const __nv_bfloat162*>(&top));
+          top = *reinterpret_cast<const uint32_t*>(&h);
+        }
+      }
+    }
   };
   Chunk<T> c[NV > 0 ? NV : 1];
   if constexpr (NV > 0) {
@@ -115,6 +135,7 @@ quantize_rows_kernel(const T* __restrict__ x, const int32_t* __restrict__ row_ma
     dest = row_map != nullptr ? row_map[(size_t)t * K + lane] : t;
     if (dest >= N) dest = -1;
   }
+  if constexpr (sizeof(T) == 2) top = max(top & 0xffff0000u, top << 16);  // as fp32
   top = __reduce_max_sync(0xffffffffu, top);
   if constexpr (TPR > 32) {
     if (lane == 0) part[threadIdx.x >> 5] = top;

@@ -13,17 +13,16 @@
 //   * the weights are the A operand (M = channels): they go from the 8-bit
 //     tile through registers into tensor memory, never back to shared memory;
 //   * the rows are the B operand (N = rows), so a tile takes as many rows as
-//     an expert has, in steps of 16 up to 192: 25 rows cost 32 columns, not
-//     128 rows;
+//     an expert has, in steps of 16 up to 320 (two accumulators of 160): 25
+//     rows cost 32 columns, not 128 rows, and the weights of an expert of up
+//     to 320 rows are loaded and expanded once;
 //   * CTA pairs (cta_group::2): 256 channels per MMA, each CTA expands its
-//     own 128 channels and half of the rows.  Per 64-deep step a CTA moves
-//     14 KB (TMA) + 14 KB (read) + 12 KB (fp16 rows) + 12 KB (MMA reads) in
-//     the 384 cycles of its MMAs at 192 rows.
+//     own 128 channels and half of the rows.
 //
 // Warps: 1 TMA producer, 1 MMA issuer (in the leading CTA), 8 epilogue (two
-// per tensor-memory lane quarter), two groups of 4 + 3 that expand A and B of
+// per tensor-memory lane quarter), two groups of 4 + 5 that expand A and B of
 // alternate 128-deep stages, 32 operand rows a warp.  Tensor memory: two
-// 192-column accumulators and two 64-column A buffers.
+// 160-column accumulators and two 64-column A buffers.
 //
 // The expanding warps of both CTAs arrive on the leader's barrier with the
 // default (CTA-scope) release: what they wrote, tensor memory and shared
@@ -44,15 +43,17 @@ namespace moe {
 namespace tc {
 namespace {
 
-constexpr int kRowTile = 192;                  // B rows (N) of a tile, at most
-constexpr int kStages = 5;                     // 8-bit stages, 128 deep
+constexpr int kSub = 160;                      // B rows (N) of one accumulator, at most
+constexpr int kRowTile = 2 * kSub;             // B rows of a tile
+constexpr int kStages = 3;                     // 8-bit stages, 128 deep
 constexpr int kBufs = 2;                       // expanded stages
 constexpr uint32_t kA8 = 128 * 128;            // 8-bit A bytes of a stage
 constexpr uint32_t kB8 = kRowTile / 2 * 128;   // 8-bit B bytes of a stage
 constexpr uint32_t kB16 = kRowTile / 2 * 256;  // fp16 B bytes of a stage, two 64-deep halves
-constexpr uint32_t kAccCols = kRowTile, kACol = 2 * kAccCols;
+constexpr uint32_t kAccCols = kSub, kACol = 2 * kAccCols;
 constexpr int kTmaWarp = 0, kMmaWarp = 1, kEpiWarp = 2, kAWarp = 10, kBWarp = 18;
-constexpr int kThreadsI8 = 24 * 32;
+constexpr int kBGroup = kRowTile / 64;         // warps that expand B, per group
+constexpr int kThreadsI8 = (18 + 2 * kBGroup) * 32;
 constexpr int kBars = 2 * kStages + 2 * kBufs + 4 + 1;
 constexpr uint32_t kStageWarp = 2048 + 128;  // epilogue staging of a warp: rows, then row scales
 constexpr uint32_t kStage = kStages * (kA8 + kB8) + kBufs * kB16;
@@ -70,17 +71,19 @@ struct I8Params {
   int32_t* status;
   int N, E, Kd, Nout;
   int ch_tiles;  // channel tiles per expert: of 256 (128 for gate/up)
-  int row_tile;  // rows of a tile, at most
 };
 
 struct I8Tile {
-  int e, row0, hi;  // expert, first row, end of the expert's rows
-  int n;            // MMA N: rows of the tile, a multiple of 16, at least 32
+  int e, row0, hi;  // expert, first row, end of the tile's rows
+  int subs;         // accumulators the rows take: 1 or 2
+  int n;            // MMA N of each: a multiple of 16, at least 32
   int ch0;          // first channel of this CTA
+  __device__ __forceinline__ int b_rows() const { return subs * n / 2; }  // of this CTA
 };
 
 // Tile t is channel tile (t mod ch_tiles) of row tile t / ch_tiles; the rows
-// of an expert are split evenly over its ceil(rows / row_tile) row tiles.
+// of an expert are split evenly over its ceil(rows / 320) row tiles, the rows
+// of a row tile evenly over its accumulators.
 template <bool kSwiglu>
 __device__ __forceinline__ I8Tile i8_tile(int t, const I8Params& p, const int32_t* prefix,
                                           const int32_t* offs, int rank) {
@@ -89,10 +92,11 @@ __device__ __forceinline__ I8Tile i8_tile(int t, const I8Params& p, const int32_
   x.e = find_expert(prefix, p.E, g);
   const ExpertRows r = expert_rows(offs, x.e, p.N);
   const int parts = prefix[x.e + 1] - prefix[x.e], i = g - prefix[x.e];
-  const int per = ((r.hi - r.lo + parts - 1) / parts + 15) & ~15;
+  const int per = (r.hi - r.lo + parts - 1) / parts;
   x.row0 = r.lo + i * per;
   x.hi = min(r.hi, x.row0 + per);
-  x.n = max(32, per);
+  x.subs = per > kSub ? 2 : 1;
+  x.n = max(32, ((per + x.subs - 1) / x.subs + 15) & ~15);
   x.ch0 = (t - g * p.ch_tiles) * (kSwiglu ? 128 : 256) + rank * (kSwiglu ? 64 : 128);
   return x;
 }
@@ -153,10 +157,10 @@ gmm_i8_kernel(const __grid_constant__ CUtensorMap mapW0, const __grid_constant__
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
       mbar_init(q_full(s), 1);
-      mbar_init(q_empty(s), 7);  // an expanding group
+      mbar_init(q_empty(s), 4 + kBGroup);  // an expanding group
     }
     for (int b = 0; b < kBufs; ++b) {
-      mbar_init(c_full(b), 14);  // the leader's: an expanding group of both CTAs
+      mbar_init(c_full(b), 2 * (4 + kBGroup));  // the leader's: a group of both CTAs
       mbar_init(c_empty(b), 1);
     }
     for (int a = 0; a < 2; ++a) {
@@ -178,7 +182,7 @@ gmm_i8_kernel(const __grid_constant__ CUtensorMap mapW0, const __grid_constant__
     tmem_relinquish_pair();
   }
   stage_offsets(p.off, p.E, p.N, offs, scratch);
-  build_tile_prefix(offs, p.E, p.N, p.row_tile, prefix, scratch);  // ends with __syncthreads
+  build_tile_prefix(offs, p.E, p.N, kRowTile, prefix, scratch);  // ends with __syncthreads
   const int total = prefix[p.E] * p.ch_tiles;
   tc_fence_before();
   __syncthreads();
@@ -189,36 +193,40 @@ gmm_i8_kernel(const __grid_constant__ CUtensorMap mapW0, const __grid_constant__
   const int t0 = (int)cluster_id_x(), dt = (int)cluster_count_x();
   const int stages = (p.Kd + 127) / 128;
 
-  if (warp == kTmaWarp) {
-    if (lane == 0) {
-      int s = 0, n = 0;
-      uint32_t ph = 0;
-      bool run = true;
-      for (int t = t0; run && t < total; t += dt) {
-        const I8Tile x = i8_tile<kSwiglu>(t, p, prefix, offs, rank);
-        const int nb = x.n / 2, r0 = x.row0 + rank * nb;
-        const uint32_t tx = kA8 + (uint32_t)nb * 128u;
-        for (int k = 0; k < stages; ++k) {
-          if (!mbar_wait(q_empty(s), ph ^ 1u, abort_flag, p.status)) {
-            run = false;
-            break;
-          }
-          mbar_arrive_expect_tx(q_full(s), tx);
-          const uint32_t a = sA8 + s * kA8, b = sB8 + s * kB8;
-          tma_load_3d(a, &mapW0, q_full(s), k * 128, x.ch0, x.e);
-          if constexpr (kSwiglu) tma_load_3d(a + kA8 / 2, &mapW1, q_full(s), k * 128, x.ch0, x.e);
+  if (warp == kTmaWarp) {  // the whole warp, one lane elected for each copy
+    const uint32_t ub = uniform(base);
+    int s = 0, n = 0;
+    uint32_t ph = 0;
+    bool run = true;
+    for (int t = t0; run && t < total; t += dt) {
+      const I8Tile x = i8_tile<kSwiglu>(t, p, prefix, offs, rank);
+      const int nh = (int)uniform(x.n) / 2, subs = (int)uniform(x.subs), e = (int)uniform(x.e);
+      const int ch0 = (int)uniform(x.ch0), r0 = (int)uniform(x.row0) + rank * nh;
+      const uint32_t tx = kA8 + (uint32_t)(subs * nh) * 128u;
+      for (int k = 0; k < stages; ++k) {
+        run = mbar_wait_warp(q_empty(s), ph ^ 1u, abort_flag, p.status);
+        if (!run) break;
+        mbar_arrive_expect_tx_warp(q_full(s), tx);
+        const uint32_t a = ub + s * kA8;
+        uint32_t b = ub + kStages * kA8 + s * kB8;
+        tma_load_3d_warp(a, &mapW0, q_full(s), k * 128, ch0, e);
+        if constexpr (kSwiglu) tma_load_3d_warp(a + kA8 / 2, &mapW1, q_full(s), k * 128, ch0, e);
+        // this CTA's half of each accumulator's rows, one after the other
+        for (int j = 0; j < subs; ++j) {
           int r = 0;
-          for (; r + 32 <= nb; r += 32) tma_load_2d(b + r * 128, &mapX32, q_full(s), k * 128, r0 + r);
-          for (; r < nb; r += 8) tma_load_2d(b + r * 128, &mapX8, q_full(s), k * 128, r0 + r);
-          ++n;
-          if (++s == kStages) s = 0, ph ^= 1u;
+          for (; r + 32 <= nh; r += 32, b += 4096)
+            tma_load_2d_warp(b, &mapX32, q_full(s), k * 128, r0 + j * 2 * nh + r);
+          for (; r < nh; r += 8, b += 1024)
+            tma_load_2d_warp(b, &mapX8, q_full(s), k * 128, r0 + j * 2 * nh + r);
         }
+        ++n;
+        if (++s == kStages) s = 0, ph ^= 1u;
       }
-      // every copy has landed before the CTA may exit
-      for (int st = 0; st < kStages && st < n; ++st) {
-        const int last = st + (n - 1 - st) / kStages * kStages;
-        mbar_wait(q_full(st), (uint32_t)(last / kStages) & 1u, abort_flag, p.status, false);
-      }
+    }
+    // every copy has landed before the CTA may exit
+    for (int st = 0; st < kStages && st < n; ++st) {
+      const int last = st + (n - 1 - st) / kStages * kStages;
+      mbar_wait_warp(q_full(st), (uint32_t)(last / kStages) & 1u, abort_flag, p.status, false);
     }
   } else if (warp == kMmaWarp) {
     if (rank == 0) {  // the whole warp, one lane elected for each MMA
@@ -227,13 +235,18 @@ gmm_i8_kernel(const __grid_constant__ CUtensorMap mapW0, const __grid_constant__
       int b = 0, it = 0;
       uint32_t ph = 0;
       bool run = true;
-      for (int t = t0; run && t < total; t += dt, ++it) {
-        const uint32_t idesc = uniform(idesc_f16_f32(256, i8_tile<kSwiglu>(t, p, prefix, offs, rank).n));
-        const int acc = it & 1;
-        run = __all_sync(0xffffffffu, mbar_wait<true>(t_empty(acc), ((it >> 1) & 1) ^ 1u, abort_flag, p.status));
+      for (int t = t0; run && t < total; t += dt) {
+        const I8Tile x = i8_tile<kSwiglu>(t, p, prefix, offs, rank);
+        const int n = (int)uniform(x.n), subs = (int)uniform(x.subs);
+        const uint32_t idesc = idesc_f16_f32(256, n);
+        // accumulators it, it + 1 (mod 2), as they become free
+        for (int j = 0; run && j < subs; ++j)
+          run = __all_sync(0xffffffffu, mbar_wait<true>(t_empty((it + j) & 1), (((it + j) >> 1) & 1) ^ 1u,
+                                                        abort_flag, p.status));
         if (!run) break;
         tc_fence_after();
-        const uint32_t d = tm + acc * kAccCols;
+        const uint32_t d0 = tm + (it & 1) * kAccCols, d1 = tm + ((it + 1) & 1) * kAccCols;
+        const uint32_t sub1 = (uint32_t)n * 64u >> 4;  // the second's rows in shared memory
         uint32_t accum = 0u;
         for (int k = 0; k < stages; ++k) {
           run = mbar_wait_warp(c_full(b), ph, abort_flag, p.status);
@@ -244,7 +257,9 @@ gmm_i8_kernel(const __grid_constant__ CUtensorMap mapW0, const __grid_constant__
           // (past the end of Kd both operands are zeros)
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk) {
-            umma_f16_ta_warp<true>(d, a + kk * 8, bd + (kk >> 2) * (kB16 >> 5) + (kk & 3) * 2, idesc, accum);
+            const uint64_t bk = bd + (kk >> 2) * (kB16 >> 5) + (kk & 3) * 2;
+            umma_f16_ta_warp<true>(d0, a + kk * 8, bk, idesc, accum);
+            if (subs > 1) umma_f16_ta_warp<true>(d1, a + kk * 8, bk + sub1, idesc, accum);
             accum = 1u;
           }
           umma_commit_pair_warp(c_empty(b), 3);
@@ -252,7 +267,8 @@ gmm_i8_kernel(const __grid_constant__ CUtensorMap mapW0, const __grid_constant__
           if (b == 0) ph ^= 1u;
         }
         if (!run) break;
-        umma_commit_pair_warp(t_full(acc), 3);
+        for (int j = 0; j < subs; ++j) umma_commit_pair_warp(t_full((it + j) & 1), 3);
+        it += subs;
       }
       umma_commit_pair_warp(drain, 1);
       mbar_wait_warp(drain, 0, abort_flag, p.status, false);
@@ -260,9 +276,9 @@ gmm_i8_kernel(const __grid_constant__ CUtensorMap mapW0, const __grid_constant__
   } else if (warp >= kAWarp) {
     // ---- expand: a lane takes one 128-byte row of the stage ----
     const bool is_a = warp < kBWarp;
-    const int grp = is_a ? (warp - kAWarp) >> 2 : (warp - kBWarp) / 3;
+    const int grp = is_a ? (warp - kAWarp) >> 2 : (warp - kBWarp) / kBGroup;
     const int quarter = warp & 3;                              // A: tensor-memory lanes
-    const int rg = is_a ? 0 : (warp - kBWarp) - 3 * grp;        // B: rows 32 rg + lane
+    const int rg = is_a ? 0 : (warp - kBWarp) - kBGroup * grp;  // B: rows 32 rg + lane
     // A row of this lane: gate/up stages hold 64 gate rows, then 64 up rows; a
     // warp takes 16 of each, so that gate and up of a channel meet in lanes i
     // and i + 16 of one epilogue warp.
@@ -282,7 +298,7 @@ gmm_i8_kernel(const __grid_constant__ CUtensorMap mapW0, const __grid_constant__
     bool run = true;
     for (int t = t0; run && t < total; t += dt) {
       // B rows past the tile's own are not expanded (the MMA does not read them)
-      const bool any = is_a || rg * 32 < i8_tile<kSwiglu>(t, p, prefix, offs, rank).n / 2;
+      const bool any = is_a || rg * 32 < i8_tile<kSwiglu>(t, p, prefix, offs, rank).b_rows();
       for (int k = (n0 ^ grp) & 1; k < stages; k += 2) {
         run = mbar_wait_warp(q_full(s), ph, abort_flag, p.status);
         if (!run) break;
@@ -297,6 +313,7 @@ gmm_i8_kernel(const __grid_constant__ CUtensorMap mapW0, const __grid_constant__
 #pragma unroll
           for (int j = 0; j < 4; ++j) v[j] = ld_shared_v4(src ^ ((j + 4) << 4));
         }
+        mbar_arrive_warp(q_empty(s));  // all of the rows are read
         run = mbar_wait_warp(c_empty(grp), bph ^ 1u, abort_flag, p.status);
         if (!run) break;
         if (is_a) {
@@ -319,7 +336,6 @@ gmm_i8_kernel(const __grid_constant__ CUtensorMap mapW0, const __grid_constant__
           fence_proxy_async_smem();
         }
         mbar_arrive_cluster_warp(full_of_leader);
-        mbar_arrive_warp(q_empty(s));
         bph ^= 1u;
         s += 2;
         if (s >= kStages) s -= kStages, ph ^= 1u;
@@ -339,15 +355,18 @@ gmm_i8_kernel(const __grid_constant__ CUtensorMap mapW0, const __grid_constant__
     float* scale = reinterpret_cast<float*>(g + kStage + (warp - kEpiWarp) * kStageWarp + 2048);
     const int ch_l = kSwiglu ? quarter * 16 + (lane & 15) : quarter * 32 + lane;
     int it = 0;
-    for (int t = t0; t < total; t += dt, ++it) {
-      const I8Tile x = i8_tile<kSwiglu>(t, p, prefix, offs, rank);
-      const int acc = it & 1;
-      const int ch = x.ch0 + ch_l;
-      const float cs = ch >= p.Nout ? 0.f
-                                    : ((kSwiglu && lane >= 16) ? p.s1 : p.s0)[(size_t)x.e * p.Nout + ch];
-      const int rows = x.hi - x.row0;
-      float rs = part * 32 + lane < rows ? p.rs[x.row0 + part * 32 + lane] : 0.f;
-      if (!mbar_wait_warp(t_full(acc), (it >> 1) & 1, abort_flag, p.status)) break;
+    bool run = true;
+    for (int t = t0; run && t < total; t += dt) {
+     const I8Tile x = i8_tile<kSwiglu>(t, p, prefix, offs, rank);
+     const int ch = x.ch0 + ch_l;
+     const float cs = ch >= p.Nout ? 0.f
+                                   : ((kSwiglu && lane >= 16) ? p.s1 : p.s0)[(size_t)x.e * p.Nout + ch];
+     for (int sub = 0; sub < x.subs; ++sub, ++it) {
+      const int acc = it & 1, row0 = x.row0 + sub * x.n;
+      const int rows = min(x.hi - row0, x.n);
+      float rs = part * 32 + lane < rows ? p.rs[row0 + part * 32 + lane] : 0.f;
+      run = mbar_wait_warp(t_full(acc), (it >> 1) & 1, abort_flag, p.status);
+      if (!run) break;
       tc_fence_after();
       const uint32_t d = tmem + acc * kAccCols + ((uint32_t)(quarter * 32) << 16);
       // 16-byte chunk of the staging rows that this lane copies out, and the
@@ -355,12 +374,12 @@ gmm_i8_kernel(const __grid_constant__ CUtensorMap mapW0, const __grid_constant__
       const int wr = lane / kV, wc = lane % kV;
       const int wch = x.ch0 + quarter * kCh + wc * (16 / (int)sizeof(O));
       const size_t ld = (size_t)p.Nout * sizeof(O);
-      uint8_t* dst = static_cast<uint8_t*>(p.out) + (size_t)(x.row0 + wr) * ld + (size_t)wch * sizeof(O);
+      uint8_t* dst = static_cast<uint8_t*>(p.out) + (size_t)(row0 + wr) * ld + (size_t)wch * sizeof(O);
       for (int c0 = part * 32; c0 < rows; c0 += 64) {
         uint32_t v[32];
         tmem_ld_32x32b_x32(d + c0, v);
         scale[lane] = rs;
-        rs = c0 + 64 + lane < rows ? p.rs[x.row0 + c0 + 64 + lane] : 0.f;
+        rs = c0 + 64 + lane < rows ? p.rs[row0 + c0 + 64 + lane] : 0.f;
         __syncwarp();
         tmem_ld_wait();
 #pragma unroll
@@ -370,25 +389,40 @@ gmm_i8_kernel(const __grid_constant__ CUtensorMap mapW0, const __grid_constant__
             // half takes the even rows, the upper half the odd ones
             const bool up = lane >= 16;
             const uint32_t st = stage_u + (lane & 15) * 2 + (up ? kRowB : 0);
+            // (values first, stores after: the exchanges and the exponentials
+            // of the rows overlap)
 #pragma unroll
-            for (int j = 0; j < 32; j += 2) {
-              const float2 r = *reinterpret_cast<const float2*>(scale + j);
-              const float y0 = __uint_as_float(v[j]) * cs * r.x, y1 = __uint_as_float(v[j + 1]) * cs * r.y;
-              const float got = __shfl_xor_sync(0xffffffffu, up ? y0 : y1, 16);
-              const float gate = up ? got : y0, u = up ? y1 : got;
-              st_shared_b16(st + j * kRowB, __fdividef(gate, 1.f + __expf(-gate)) * u);
+            for (int h = 0; h < 32; h += 16) {
+              float y[8];
+#pragma unroll
+              for (int j = 0; j < 16; j += 2) {
+                const float2 r = *reinterpret_cast<const float2*>(scale + h + j);
+                const float y0 = __uint_as_float(v[h + j]) * cs * r.x;
+                const float y1 = __uint_as_float(v[h + j + 1]) * cs * r.y;
+                const float got = __shfl_xor_sync(0xffffffffu, up ? y0 : y1, 16);
+                const float gate = up ? got : y0, u = up ? y1 : got;
+                y[j / 2] = __fdividef(gate, 1.f + __expf(-gate)) * u;
+              }
+#pragma unroll
+              for (int j = 0; j < 16; j += 2) st_shared_b16(st + (h + j) * kRowB, y[j / 2]);
             }
           } else {
             const uint32_t st = stage_u + lane * (uint32_t)sizeof(O);
 #pragma unroll
-            for (int j = 0; j < kPass; j += 4) {
-              const float4 r = *reinterpret_cast<const float4*>(scale + p0 + j);
-              const float f[4] = {r.x, r.y, r.z, r.w};
+            for (int h = 0; h < kPass; h += 16) {
+              float y[16];
 #pragma unroll
-              for (int q = 0; q < 4; ++q) {
-                const float y = __uint_as_float(v[p0 + j + q]) * cs * f[q];
-                if constexpr (sizeof(O) == 2) st_shared_b16(st + (j + q) * kRowB, y);
-                else st_shared_f32(st + (j + q) * kRowB, y);
+              for (int j = 0; j < 16; j += 4) {
+                const float4 r = *reinterpret_cast<const float4*>(scale + p0 + h + j);
+                y[j] = __uint_as_float(v[p0 + h + j]) * cs * r.x;
+                y[j + 1] = __uint_as_float(v[p0 + h + j + 1]) * cs * r.y;
+                y[j + 2] = __uint_as_float(v[p0 + h + j + 2]) * cs * r.z;
+                y[j + 3] = __uint_as_float(v[p0 + h + j + 3]) * cs * r.w;
+              }
+#pragma unroll
+              for (int j = 0; j < 16; ++j) {
+                if constexpr (sizeof(O) == 2) st_shared_b16(st + (h + j) * kRowB, y[j]);
+                else st_shared_f32(st + (h + j) * kRowB, y[j]);
               }
             }
           }
@@ -405,6 +439,7 @@ gmm_i8_kernel(const __grid_constant__ CUtensorMap mapW0, const __grid_constant__
       }
       tc_fence_before();
       mbar_arrive_cluster_warp(mapa_shared(t_empty(acc), 0));
+     }
     }
   }
   tc_fence_before();
@@ -446,7 +481,7 @@ int launch_i8(const int8_t* A, const float* rs, const int8_t* B0, const float* s
   });
   if (attr != cudaSuccess) return MOE_ERR_CUDA;
   const int per = kSwiglu ? 128 : 256;
-  const I8Params p{off, rs, s0, s1, out, status, N, E, Kd, Nout, (Nout + per - 1) / per, kRowTile};
+  const I8Params p{off, rs, s0, s1, out, status, N, E, Kd, Nout, (Nout + per - 1) / per};
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeClusterDimension;

@@ -120,13 +120,21 @@ __device__ __forceinline__ void expand16(uint4 v, uint32_t* r) {
   expand4(v.w, r[6], r[7]);
 }
 
-__device__ __forceinline__ void st_shared_b16(uint32_t addr, float v) {
-  const __nv_bfloat16 h = __float2bfloat16_rn(v);
-  asm volatile("st.shared.u16 [%0], %1;" ::"r"(addr), "h"(*reinterpret_cast<const unsigned short*>(&h))
-               : "memory");
+__device__ __forceinline__ void st_shared_u32(uint32_t addr, uint32_t v) {
+  asm volatile("st.shared.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
-__device__ __forceinline__ void st_shared_f32(uint32_t addr, float v) {
-  asm volatile("st.shared.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+
+// Two products at once.
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 r;
+  asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "mul.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return r;
+}
+__device__ __forceinline__ float2 mul2(uint32_t x, uint32_t y, float s, float t) {
+  return mul2(make_float2(__uint_as_float(x), __uint_as_float(y)), make_float2(s, t));
 }
 
 template <bool kSwiglu, typename O>
@@ -345,12 +353,11 @@ gmm_i8_kernel(const __grid_constant__ CUtensorMap mapW0, const __grid_constant__
   } else {
     // ---- epilogue: lanes are channels, accumulator columns are rows ----
     // The two warps of a quarter take alternate pieces of 32 columns.  A piece
-    // is scaled, turned through the warp's staging rows (one row of 32
-    // channels, or 16 for gate/up, per column) and written in 16-byte chunks.
+    // is scaled, turned through the warp's staging rows and written in 16-byte
+    // chunks of 8 channels.
     const int quarter = warp & 3, part = (warp - kEpiWarp) >> 2;
-    constexpr int kCh = kSwiglu ? 16 : 32;                        // channels per warp
-    constexpr int kRowB = kCh * (int)sizeof(O), kV = kRowB / 16;  // staging row, its chunks
-    constexpr int kPass = kRowB > 64 ? 16 : 32;                   // columns staged at a time
+    constexpr int kCh = kSwiglu ? 16 : 32;  // channels per warp
+    O* out = static_cast<O*>(p.out);
     const uint32_t stage_u = base + kStage + (uint32_t)(warp - kEpiWarp) * kStageWarp;
     float* scale = reinterpret_cast<float*>(g + kStage + (warp - kEpiWarp) * kStageWarp + 2048);
     const int ch_l = kSwiglu ? quarter * 16 + (lane & 15) : quarter * 32 + lane;
@@ -369,12 +376,6 @@ gmm_i8_kernel(const __grid_constant__ CUtensorMap mapW0, const __grid_constant__
       if (!run) break;
       tc_fence_after();
       const uint32_t d = tmem + acc * kAccCols + ((uint32_t)(quarter * 32) << 16);
-      // 16-byte chunk of the staging rows that this lane copies out, and the
-      // channels it holds; Nout is a multiple of 16, so a chunk is whole
-      const int wr = lane / kV, wc = lane % kV;
-      const int wch = x.ch0 + quarter * kCh + wc * (16 / (int)sizeof(O));
-      const size_t ld = (size_t)p.Nout * sizeof(O);
-      uint8_t* dst = static_cast<uint8_t*>(p.out) + (size_t)(row0 + wr) * ld + (size_t)wch * sizeof(O);
       for (int c0 = part * 32; c0 < rows; c0 += 64) {
         uint32_t v[32];
         tmem_ld_32x32b_x32(d + c0, v);
@@ -382,56 +383,79 @@ gmm_i8_kernel(const __grid_constant__ CUtensorMap mapW0, const __grid_constant__
         rs = c0 + 64 + lane < rows ? p.rs[row0 + c0 + 64 + lane] : 0.f;
         __syncwarp();
         tmem_ld_wait();
+        if constexpr (sizeof(O) == 4) {
+          // fp32: staging rows of 32 channels, 16 columns at a time
 #pragma unroll
-        for (int p0 = 0; p0 < 32; p0 += kPass) {
+          for (int p0 = 0; p0 < 32; p0 += 16) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+              st_shared_u32(stage_u + lane * 4 + j * 128,
+                            __float_as_uint(__uint_as_float(v[p0 + j]) * cs * scale[p0 + j]));
+            __syncwarp();
+            const int wr = lane >> 3, wch = x.ch0 + quarter * kCh + (lane & 7) * 4;
+            if (wch < p.Nout) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const int r = c0 + p0 + wr + i * 4;
+                if (r < rows)
+                  st_v4(out + (size_t)(row0 + r) * p.Nout + wch, ld_shared_v4(stage_u + lane * 16 + i * 512));
+              }
+            }
+            __syncwarp();
+          }
+        } else {
+          // bf16: words of two rows of a channel; [pair][channel]
+          uint32_t w[kSwiglu ? 8 : 16];
           if constexpr (kSwiglu) {
             // lanes 0-15 hold gate, 16-31 up of the same channels: the lower
             // half takes the even rows, the upper half the odd ones
             const bool up = lane >= 16;
-            const uint32_t st = stage_u + (lane & 15) * 2 + (up ? kRowB : 0);
-            // (values first, stores after: the exchanges and the exponentials
-            // of the rows overlap)
+            float y[16];
 #pragma unroll
-            for (int h = 0; h < 32; h += 16) {
-              float y[8];
-#pragma unroll
-              for (int j = 0; j < 16; j += 2) {
-                const float2 r = *reinterpret_cast<const float2*>(scale + h + j);
-                const float y0 = __uint_as_float(v[h + j]) * cs * r.x;
-                const float y1 = __uint_as_float(v[h + j + 1]) * cs * r.y;
-                const float got = __shfl_xor_sync(0xffffffffu, up ? y0 : y1, 16);
-                const float gate = up ? got : y0, u = up ? y1 : got;
-                y[j / 2] = __fdividef(gate, 1.f + __expf(-gate)) * u;
-              }
-#pragma unroll
-              for (int j = 0; j < 16; j += 2) st_shared_b16(st + (h + j) * kRowB, y[j / 2]);
+            for (int j = 0; j < 32; j += 2) {
+              const float2 f = mul2(mul2(v[j], v[j + 1], cs, cs), *reinterpret_cast<const float2*>(scale + j));
+              const float got = __shfl_xor_sync(0xffffffffu, up ? f.x : f.y, 16);
+              const float gate = up ? got : f.x, u = up ? f.y : got;
+              y[j / 2] = __fdividef(gate, 1.f + __expf(-gate)) * u;
             }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) w[j] = VecTraits<__nv_bfloat16>::pack2(y[2 * j], y[2 * j + 1]);
+            // word row 2j + up: rows 4j + up and 4j + up + 2
+            const uint32_t st = stage_u + (lane & 15) * 4 + (up ? 64 : 0);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) st_shared_u32(st + j * 128, w[j]);
           } else {
-            const uint32_t st = stage_u + lane * (uint32_t)sizeof(O);
 #pragma unroll
-            for (int h = 0; h < kPass; h += 16) {
-              float y[16];
-#pragma unroll
-              for (int j = 0; j < 16; j += 4) {
-                const float4 r = *reinterpret_cast<const float4*>(scale + p0 + h + j);
-                y[j] = __uint_as_float(v[p0 + h + j]) * cs * r.x;
-                y[j + 1] = __uint_as_float(v[p0 + h + j + 1]) * cs * r.y;
-                y[j + 2] = __uint_as_float(v[p0 + h + j + 2]) * cs * r.z;
-                y[j + 3] = __uint_as_float(v[p0 + h + j + 3]) * cs * r.w;
-              }
-#pragma unroll
-              for (int j = 0; j < 16; ++j) {
-                if constexpr (sizeof(O) == 2) st_shared_b16(st + (h + j) * kRowB, y[j]);
-                else st_shared_f32(st + (h + j) * kRowB, y[j]);
-              }
+            for (int j = 0; j < 16; ++j) {
+              const float2 f =
+                  mul2(mul2(v[2 * j], v[2 * j + 1], cs, cs), *reinterpret_cast<const float2*>(scale + 2 * j));
+              w[j] = VecTraits<__nv_bfloat16>::pack2(f.x, f.y);
             }
+#pragma unroll
+            for (int j = 0; j < 16; ++j) st_shared_u32(stage_u + lane * 4 + j * 128, w[j]);
           }
           __syncwarp();
-          if (wch < p.Nout) {
+          // a lane takes 8 channels of a pair of rows: 32 bytes of words (the
+          // halves in an order that keeps 8 lanes on distinct banks)
+          constexpr int G = kCh / 8, kWordRow = kCh * 4;
 #pragma unroll
-            for (int i = 0; i < kPass * kRowB / 512; ++i) {
-              const int r = c0 + p0 + wr + i * (32 / kV);
-              if (r < rows) st_v4(dst + (size_t)(r - wr) * ld, ld_shared_v4(stage_u + lane * 16 + i * 512));
+          for (int i = 0; i < 16 * G / 32; ++i) {
+            const int pr = (lane + 32 * i) / G, gch = (lane + 32 * i) % G;
+            const uint32_t src = stage_u + pr * kWordRow + gch * 32;
+            const uint32_t first = kSwiglu ? ((pr >> 1) & 1) * 16 : (pr & 1) * 16;
+            const uint4 m0 = ld_shared_v4(src + first), m1 = ld_shared_v4(src + (first ^ 16));
+            const uint4 a = first ? m1 : m0, b = first ? m0 : m1;
+            const uint4 lo = make_uint4(__byte_perm(a.x, a.y, 0x5410), __byte_perm(a.z, a.w, 0x5410),
+                                        __byte_perm(b.x, b.y, 0x5410), __byte_perm(b.z, b.w, 0x5410));
+            const uint4 hi = make_uint4(__byte_perm(a.x, a.y, 0x7632), __byte_perm(a.z, a.w, 0x7632),
+                                        __byte_perm(b.x, b.y, 0x7632), __byte_perm(b.z, b.w, 0x7632));
+            const int r = c0 + (kSwiglu ? (pr >> 1) * 4 + (pr & 1) : 2 * pr);
+            constexpr int dr = kSwiglu ? 2 : 1;
+            const int wch = x.ch0 + quarter * kCh + gch * 8;
+            if (wch < p.Nout) {
+              O* dst = out + (size_t)(row0 + r) * p.Nout + wch;
+              if (r < rows) st_v4(dst, lo);
+              if (r + dr < rows) st_v4(dst + (size_t)dr * p.Nout, hi);
             }
           }
           __syncwarp();

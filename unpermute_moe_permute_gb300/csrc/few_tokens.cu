@@ -444,22 +444,19 @@ few_tokens_kernel(const __grid_constant__ CUtensorMap mapG, const __grid_constan
         if constexpr (I8) {
           const uint32_t a = tmem + 256 + c * 128;
 #pragma unroll
-          for (int kk = 0; kk < 8; ++kk) {
-            const uint64_t b = bd + (kk >> 2) * (TR::b_box >> 4) + (kk & 3) * 2;
-            umma_f16_ta_warp<false>(d, a + kk * 8, b, idesc, accum);
-            umma_f16_ta_warp<false>(d + NP, a + 64 + kk * 8, b, idesc, accum);
+          for (int h = 0; h < 2; ++h) {
+            const uint64_t b = bd + h * (TR::b_box >> 4);
+            umma_f16_ta_k64_warp<false>(d, a + h * 32, b, idesc, accum);
+            umma_f16_ta_k64_warp<false>(d + NP, a + 64 + h * 32, b, idesc, accum);
             accum = 1u;
           }
           umma_commit_warp(c_empty(c));
           c ^= 1;
           if (c == 0) cph ^= 1u;
         } else {
-#pragma unroll
-          for (int kk = 0; kk < 4; ++kk) {
-            umma_f16_warp<false>(d, ad + kk * 2, bd + kk * 2, idesc, accum);
-            umma_f16_warp<false>(d + NP, ad + (kBox16 >> 4) + kk * 2, bd + kk * 2, idesc, accum);
-            accum = 1u;
-          }
+          umma_f16_k64_warp(d, ad, bd, idesc, accum);
+          umma_f16_k64_warp(d + NP, ad + (kBox16 >> 4), bd, idesc, accum);
+          accum = 1u;
         }
         umma_commit_warp(empty(s));
         if (++s == S) s = 0, ph ^= 1u;

@@ -19,10 +19,9 @@
 //   * CTA pairs (cta_group::2): 256 channels per MMA, each CTA expands its
 //     own 128 channels and half of the rows.
 //
-// Warps: 1 TMA producer, 1 MMA issuer (in the leading CTA), 8 epilogue (two
-// per tensor-memory lane quarter), two groups of 4 + 5 that expand A and B of
-// alternate 128-deep stages, 32 operand rows a warp.  Tensor memory: two
-// 160-column accumulators and two 64-column A buffers.
+// Warps: 1 TMA producer, 1 MMA issuer (in the leading CTA), epilogue warps (one
+// or two per tensor-memory lane quarter), groups that expand A and B of the
+// 128-deep stages in turn, 32 operand rows a warp (I8Cfg).
 //
 // The expanding warps of both CTAs arrive on the leader's barrier with the
 // default (CTA-scope) release: what they wrote, tensor memory and shared
@@ -43,26 +42,38 @@ namespace moe {
 namespace tc {
 namespace {
 
-constexpr int kSub = 160;                      // B rows (N) of one accumulator, at most
-constexpr int kRowTile = 2 * kSub;             // B rows of a tile
-constexpr int kStages = 3;                     // 8-bit stages, 128 deep
-constexpr int kBufs = 2;                       // expanded stages
-constexpr uint32_t kA8 = 128 * 128;            // 8-bit A bytes of a stage
-constexpr uint32_t kB8 = kRowTile / 2 * 128;   // 8-bit B bytes of a stage
-constexpr uint32_t kB16 = kRowTile / 2 * 256;  // fp16 B bytes of a stage, two 64-deep halves
-constexpr uint32_t kAccCols = kSub, kACol = 2 * kAccCols;
-constexpr int kTmaWarp = 0, kMmaWarp = 1, kEpiWarp = 2, kAWarp = 10, kBWarp = 18;
-constexpr int kBGroup = kRowTile / 64;         // warps that expand B, per group
-constexpr int kThreadsI8 = (18 + 2 * kBGroup) * 32;
-constexpr int kBars = 2 * kStages + 2 * kBufs + 4 + 1;
-constexpr uint32_t kStageWarp = 2048 + 128;  // epilogue staging of a warp: rows, then row scales
-constexpr uint32_t kStage = kStages * (kA8 + kB8) + kBufs * kB16;
-constexpr uint32_t kCtrl = kStage + 8 * kStageWarp;
-constexpr uint32_t kHolder = kCtrl + 8 * kBars;
-constexpr uint32_t kTable = kHolder + 8;       // prefix, offsets, scan scratch
-constexpr uint32_t kSmem = kTable + 2 * (kMaxExperts + 1) * 4 + 32 * 4 + 1024;
-static_assert(kSmem <= 232448, "more shared memory than one CTA may use");
-static_assert(kACol + kBufs * 64 <= 512, "more tensor memory than there is");
+// kSub: B rows (N) of one accumulator, at most; a tile has up to two.
+// kGroups: expanding groups, which take the 128-deep stages in turn, with an
+// expanded buffer each.  kEpi: epilogue warps.  kStages: 8-bit stages.
+template <int SUB, int GROUPS, int EPI, int STAGES>
+struct I8Cfg {
+  static constexpr int kSub = SUB, kGroups = GROUPS, kEpi = EPI, kStages = STAGES;
+  static constexpr int kRowTile = 2 * kSub;             // B rows of a tile
+  static constexpr uint32_t kA8 = 128 * 128;            // 8-bit A bytes of a stage
+  static constexpr uint32_t kB8 = kRowTile / 2 * 128;   // 8-bit B bytes of a stage
+  static constexpr uint32_t kB16 = kRowTile / 2 * 256;  // fp16 B bytes, two 64-deep halves
+  static constexpr uint32_t kACol = 2 * kSub;           // tensor memory: accumulators, A buffers
+  static constexpr int kBGroup = (kRowTile + 63) / 64;  // warps that expand B, per group
+  static constexpr int kAWarp = 2 + kEpi, kBWarp = kAWarp + 4 * kGroups;
+  static constexpr int kThreads = (kBWarp + kGroups * kBGroup) * 32;
+  static constexpr int kBars = 2 * kStages + 2 * kGroups + 4 + 1;
+  static constexpr uint32_t kStageWarp = 2048 + 128;  // epilogue staging of a warp: rows, row scales
+  static constexpr uint32_t kStage = kStages * (kA8 + kB8) + kGroups * kB16;
+  static constexpr uint32_t kCtrl = kStage + kEpi * kStageWarp;
+  static constexpr uint32_t kHolder = kCtrl + 8 * kBars;
+  static constexpr uint32_t kTable = kHolder + 8;  // prefix, offsets, scan scratch
+  static constexpr uint32_t kSmem = kTable + 2 * (kMaxExperts + 1) * 4 + 32 * 4 + 1024;
+  static_assert(kSmem <= 232448, "more shared memory than one CTA may use");
+  static_assert(kACol + kGroups * 64 <= 512, "more tensor memory than there is");
+  static_assert(kGroups <= kStages && kRowTile % 64 == 0, "geometry");
+};
+
+// Experts with rows: two accumulators of 160 columns.  Experts with few rows
+// each: the stream of weights bounds it, so the room goes to a deeper ring and
+// to more warps that expand weights.
+using I8Many = I8Cfg<160, 2, 8, 3>;
+using I8Few = I8Cfg<32, 4, 4, 8>;
+constexpr int kTmaWarp = 0, kMmaWarp = 1, kEpiWarp = 2;
 
 struct I8Params {
   const int32_t* off;
@@ -82,9 +93,9 @@ struct I8Tile {
 };
 
 // Tile t is channel tile (t mod ch_tiles) of row tile t / ch_tiles; the rows
-// of an expert are split evenly over its ceil(rows / 320) row tiles, the rows
+// of an expert are split evenly over its ceil(rows / (2 kSub)) row tiles, the rows
 // of a row tile evenly over its accumulators.
-template <bool kSwiglu>
+template <bool kSwiglu, int kSub>
 __device__ __forceinline__ I8Tile i8_tile(int t, const I8Params& p, const int32_t* prefix,
                                           const int32_t* offs, int rank) {
   I8Tile x;
@@ -137,27 +148,30 @@ __device__ __forceinline__ float2 mul2(uint32_t x, uint32_t y, float s, float t)
   return mul2(make_float2(__uint_as_float(x), __uint_as_float(y)), make_float2(s, t));
 }
 
-template <bool kSwiglu, typename O>
-__global__ void __launch_bounds__(kThreadsI8, 1)
+template <typename C, bool kSwiglu, typename O>
+__global__ void __launch_bounds__(C::kThreads, 1)
 gmm_i8_kernel(const __grid_constant__ CUtensorMap mapW0, const __grid_constant__ CUtensorMap mapW1,
               const __grid_constant__ CUtensorMap mapX32, const __grid_constant__ CUtensorMap mapX8,
               const I8Params p) {
+  constexpr int kSub = C::kSub, kGroups = C::kGroups, kStages = C::kStages, kBGroup = C::kBGroup;
+  constexpr int kAWarp = C::kAWarp, kBWarp = C::kBWarp, kEpi = C::kEpi;
+  constexpr uint32_t kA8 = C::kA8, kB8 = C::kB8, kB16 = C::kB16, kACol = C::kACol;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
   uint8_t* g = smem_raw + (base - raw);
   const uint32_t sA8 = base, sB8 = base + kStages * kA8, sB16 = sB8 + kStages * kB8;
-  const uint32_t bars = base + kCtrl;
+  const uint32_t bars = base + C::kCtrl;
   auto q_full = [&](int s) { return bars + 8u * s; };
   auto q_empty = [&](int s) { return bars + 8u * (kStages + s); };
   auto c_full = [&](int b) { return bars + 8u * (2 * kStages + b); };
-  auto c_empty = [&](int b) { return bars + 8u * (2 * kStages + kBufs + b); };
-  auto t_full = [&](int a) { return bars + 8u * (2 * kStages + 2 * kBufs + a); };
-  auto t_empty = [&](int a) { return bars + 8u * (2 * kStages + 2 * kBufs + 2 + a); };
-  const uint32_t drain = bars + 8u * (2 * kStages + 2 * kBufs + 4);
-  uint32_t* holder = reinterpret_cast<uint32_t*>(g + kHolder);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(g + kHolder + 4);
-  int32_t* prefix = reinterpret_cast<int32_t*>(g + kTable);
+  auto c_empty = [&](int b) { return bars + 8u * (2 * kStages + kGroups + b); };
+  auto t_full = [&](int a) { return bars + 8u * (2 * kStages + 2 * kGroups + a); };
+  auto t_empty = [&](int a) { return bars + 8u * (2 * kStages + 2 * kGroups + 2 + a); };
+  const uint32_t drain = bars + 8u * (2 * kStages + 2 * kGroups + 4);
+  uint32_t* holder = reinterpret_cast<uint32_t*>(g + C::kHolder);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(g + C::kHolder + 4);
+  int32_t* prefix = reinterpret_cast<int32_t*>(g + C::kTable);
   int32_t* offs = prefix + (kMaxExperts + 1);
   int32_t* scratch = offs + (kMaxExperts + 1);
   const int warp = (int)uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
@@ -167,13 +181,13 @@ gmm_i8_kernel(const __grid_constant__ CUtensorMap mapW0, const __grid_constant__
       mbar_init(q_full(s), 1);
       mbar_init(q_empty(s), 4 + kBGroup);  // an expanding group
     }
-    for (int b = 0; b < kBufs; ++b) {
+    for (int b = 0; b < kGroups; ++b) {
       mbar_init(c_full(b), 2 * (4 + kBGroup));  // the leader's: a group of both CTAs
       mbar_init(c_empty(b), 1);
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(t_full(a), 1);
-      mbar_init(t_empty(a), 16);  // 8 epilogue warps of both CTAs
+      mbar_init(t_empty(a), 2 * kEpi);  // the epilogue warps of both CTAs
     }
     mbar_init(drain, 1);
     *abort_flag = 0;
@@ -190,7 +204,7 @@ gmm_i8_kernel(const __grid_constant__ CUtensorMap mapW0, const __grid_constant__
     tmem_relinquish_pair();
   }
   stage_offsets(p.off, p.E, p.N, offs, scratch);
-  build_tile_prefix(offs, p.E, p.N, kRowTile, prefix, scratch);  // ends with __syncthreads
+  build_tile_prefix(offs, p.E, p.N, C::kRowTile, prefix, scratch);  // ends with __syncthreads
   const int total = prefix[p.E] * p.ch_tiles;
   tc_fence_before();
   __syncthreads();
@@ -207,7 +221,7 @@ gmm_i8_kernel(const __grid_constant__ CUtensorMap mapW0, const __grid_constant__
     uint32_t ph = 0;
     bool run = true;
     for (int t = t0; run && t < total; t += dt) {
-      const I8Tile x = i8_tile<kSwiglu>(t, p, prefix, offs, rank);
+      const I8Tile x = i8_tile<kSwiglu, kSub>(t, p, prefix, offs, rank);
       const int nh = (int)uniform(x.n) / 2, subs = (int)uniform(x.subs), e = (int)uniform(x.e);
       const int ch0 = (int)uniform(x.ch0), r0 = (int)uniform(x.row0) + rank * nh;
       const uint32_t tx = kA8 + (uint32_t)(subs * nh) * 128u;
@@ -244,7 +258,7 @@ gmm_i8_kernel(const __grid_constant__ CUtensorMap mapW0, const __grid_constant__
       uint32_t ph = 0;
       bool run = true;
       for (int t = t0; run && t < total; t += dt) {
-        const I8Tile x = i8_tile<kSwiglu>(t, p, prefix, offs, rank);
+        const I8Tile x = i8_tile<kSwiglu, kSub>(t, p, prefix, offs, rank);
         const int n = (int)uniform(x.n), subs = (int)uniform(x.subs);
         const uint32_t idesc = idesc_f16_f32(256, n);
         // accumulators it, it + 1 (mod 2), as they become free
@@ -253,7 +267,7 @@ gmm_i8_kernel(const __grid_constant__ CUtensorMap mapW0, const __grid_constant__
                                                         abort_flag, p.status));
         if (!run) break;
         tc_fence_after();
-        const uint32_t d0 = tm + (it & 1) * kAccCols, d1 = tm + ((it + 1) & 1) * kAccCols;
+        const uint32_t d0 = tm + (it & 1) * kSub, d1 = tm + ((it + 1) & 1) * kSub;
         const uint32_t sub1 = (uint32_t)n * 64u >> 4;  // the second's rows in shared memory
         uint32_t accum = 0u;
         for (int k = 0; k < stages; ++k) {
@@ -264,15 +278,14 @@ gmm_i8_kernel(const __grid_constant__ CUtensorMap mapW0, const __grid_constant__
           const uint32_t a = tm + kACol + b * 64;
           // (past the end of Kd both operands are zeros)
 #pragma unroll
-          for (int kk = 0; kk < 8; ++kk) {
-            const uint64_t bk = bd + (kk >> 2) * (kB16 >> 5) + (kk & 3) * 2;
-            umma_f16_ta_warp<true>(d0, a + kk * 8, bk, idesc, accum);
-            if (subs > 1) umma_f16_ta_warp<true>(d1, a + kk * 8, bk + sub1, idesc, accum);
+          for (int h = 0; h < 2; ++h) {
+            const uint64_t bh = bd + h * (kB16 >> 5);
+            umma_f16_ta_k64_warp<true>(d0, a + h * 32, bh, idesc, accum);
+            if (subs > 1) umma_f16_ta_k64_warp<true>(d1, a + h * 32, bh + sub1, idesc, accum);
             accum = 1u;
           }
           umma_commit_pair_warp(c_empty(b), 3);
-          b ^= 1;
-          if (b == 0) ph ^= 1u;
+          if (++b == kGroups) b = 0, ph ^= 1u;
         }
         if (!run) break;
         for (int j = 0; j < subs; ++j) umma_commit_pair_warp(t_full((it + j) & 1), 3);
@@ -301,13 +314,13 @@ gmm_i8_kernel(const __grid_constant__ CUtensorMap mapW0, const __grid_constant__
     const uint32_t b_dst = sB16 + grp * kB16 + row * 128 + ((row & 7) << 4);
     const uint32_t step = is_a ? kA8 : kB8;
     const uint32_t full_of_leader = mapa_shared(c_full(grp), 0);
-    int s = grp, n0 = 0;  // ring stage; stages before this tile
+    int s = grp, n0 = 0;  // ring stage; stages before this tile (mod kGroups)
     uint32_t ph = 0, bph = 0;
     bool run = true;
     for (int t = t0; run && t < total; t += dt) {
       // B rows past the tile's own are not expanded (the MMA does not read them)
-      const bool any = is_a || rg * 32 < i8_tile<kSwiglu>(t, p, prefix, offs, rank).b_rows();
-      for (int k = (n0 ^ grp) & 1; k < stages; k += 2) {
+      const bool any = is_a || rg * 32 < i8_tile<kSwiglu, kSub>(t, p, prefix, offs, rank).b_rows();
+      for (int k = (grp - n0 + kGroups) % kGroups; k < stages; k += kGroups) {
         run = mbar_wait_warp(q_full(s), ph, abort_flag, p.status);
         if (!run) break;
         uint4 v[4];
@@ -345,26 +358,26 @@ gmm_i8_kernel(const __grid_constant__ CUtensorMap mapW0, const __grid_constant__
         }
         mbar_arrive_cluster_warp(full_of_leader);
         bph ^= 1u;
-        s += 2;
+        s += kGroups;
         if (s >= kStages) s -= kStages, ph ^= 1u;
       }
-      n0 += stages;
+      n0 = (n0 + stages) % kGroups;
     }
   } else {
     // ---- epilogue: lanes are channels, accumulator columns are rows ----
-    // The two warps of a quarter take alternate pieces of 32 columns.  A piece
+    // The warps of a quarter take pieces of 32 columns in turn.  A piece
     // is scaled, turned through the warp's staging rows and written in 16-byte
     // chunks of 8 channels.
     const int quarter = warp & 3, part = (warp - kEpiWarp) >> 2;
     constexpr int kCh = kSwiglu ? 16 : 32;  // channels per warp
     O* out = static_cast<O*>(p.out);
-    const uint32_t stage_u = base + kStage + (uint32_t)(warp - kEpiWarp) * kStageWarp;
-    float* scale = reinterpret_cast<float*>(g + kStage + (warp - kEpiWarp) * kStageWarp + 2048);
+    const uint32_t stage_u = base + C::kStage + (uint32_t)(warp - kEpiWarp) * C::kStageWarp;
+    float* scale = reinterpret_cast<float*>(g + C::kStage + (warp - kEpiWarp) * C::kStageWarp + 2048);
     const int ch_l = kSwiglu ? quarter * 16 + (lane & 15) : quarter * 32 + lane;
     int it = 0;
     bool run = true;
     for (int t = t0; run && t < total; t += dt) {
-     const I8Tile x = i8_tile<kSwiglu>(t, p, prefix, offs, rank);
+     const I8Tile x = i8_tile<kSwiglu, kSub>(t, p, prefix, offs, rank);
      const int ch = x.ch0 + ch_l;
      const float cs = ch >= p.Nout ? 0.f
                                    : ((kSwiglu && lane >= 16) ? p.s1 : p.s0)[(size_t)x.e * p.Nout + ch];
@@ -375,12 +388,12 @@ gmm_i8_kernel(const __grid_constant__ CUtensorMap mapW0, const __grid_constant__
       run = mbar_wait_warp(t_full(acc), (it >> 1) & 1, abort_flag, p.status);
       if (!run) break;
       tc_fence_after();
-      const uint32_t d = tmem + acc * kAccCols + ((uint32_t)(quarter * 32) << 16);
-      for (int c0 = part * 32; c0 < rows; c0 += 64) {
+      const uint32_t d = tmem + acc * kSub + ((uint32_t)(quarter * 32) << 16);
+      for (int c0 = part * 32; c0 < rows; c0 += 8 * kEpi) {
         uint32_t v[32];
         tmem_ld_32x32b_x32(d + c0, v);
         scale[lane] = rs;
-        rs = c0 + 64 + lane < rows ? p.rs[row0 + c0 + 64 + lane] : 0.f;
+        rs = c0 + 8 * kEpi + lane < rows ? p.rs[row0 + c0 + 8 * kEpi + lane] : 0.f;
         __syncwarp();
         tmem_ld_wait();
         if constexpr (sizeof(O) == 4) {
@@ -484,6 +497,52 @@ int check_i8(const void* A, const float* rs, const int32_t* off, int N, int H, i
   return MOE_OK;
 }
 
+template <typename C, bool kSwiglu, typename O>
+int launch_cfg(const CUtensorMap& w0, const CUtensorMap& w1, const CUtensorMap& x32,
+               const CUtensorMap& x8, const I8Params& p, cudaStream_t s) {
+  static std::once_flag once;
+  static cudaError_t attr = cudaSuccess;
+  std::call_once(once, [] {
+    attr = cudaFuncSetAttribute(gmm_i8_kernel<C, kSwiglu, O>,
+                                cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem);
+  });
+  if (attr != cudaSuccess) return MOE_ERR_CUDA;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = 2;
+  at[0].val.clusterDim.y = 1;
+  at[0].val.clusterDim.z = 1;
+  // one persistent CTA per SM, as many whole pairs as can be resident
+  cfg.gridDim = dim3(sm_count() / 2 * 2, 1, 1);
+  cfg.blockDim = dim3(C::kThreads, 1, 1);
+  cfg.dynamicSmemBytes = C::kSmem;
+  cfg.stream = s;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  static int resident = -1;
+  if (resident < 0) {
+    int n = 0;
+    resident = (cudaOccupancyMaxActiveClusters(&n, gmm_i8_kernel<C, kSwiglu, O>, &cfg) == cudaSuccess && n > 0)
+                   ? n
+                   : 0;
+    (void)cudaGetLastError();
+  }
+  if (resident > 0 && 2 * resident < (int)cfg.gridDim.x) cfg.gridDim.x = 2 * resident;
+  if (cudaLaunchKernelEx(&cfg, gmm_i8_kernel<C, kSwiglu, O>, w0, w1, x32, x8, p) != cudaSuccess) {
+    (void)cudaGetLastError();
+    return MOE_ERR_CUDA;
+  }
+  count_launches(1);
+  return MOE_OK;
+}
+
+#ifndef I8_FEW_ROWS
+#define I8_FEW_ROWS 48
+#endif
+// Rows per expert, on average, up to which the few-rows form runs.
+constexpr long long kFewRows = I8_FEW_ROWS;
+
 template <bool kSwiglu, typename O>
 int launch_i8(const int8_t* A, const float* rs, const int8_t* B0, const float* s0, const int8_t* B1,
               const float* s1, const int32_t* off, int N, int Kd, int Nout, int E, O* out,
@@ -497,43 +556,10 @@ int launch_i8(const int8_t* A, const float* rs, const int8_t* B0, const float* s
   if (!make_map_sw128(&w0, B0, 1, 3, dw, bw) || !make_map_sw128(&w1, B1 ? B1 : B0, 1, 3, dw, bw) ||
       !make_map_sw128(&x32, A, 1, 2, dx, b32) || !make_map_sw128(&x8, A, 1, 2, dx, b8))
     return MOE_ERR_CUDA;
-  static std::once_flag once;
-  static cudaError_t attr = cudaSuccess;
-  std::call_once(once, [] {
-    attr = cudaFuncSetAttribute(gmm_i8_kernel<kSwiglu, O>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                (int)kSmem);
-  });
-  if (attr != cudaSuccess) return MOE_ERR_CUDA;
   const int per = kSwiglu ? 128 : 256;
   const I8Params p{off, rs, s0, s1, out, status, N, E, Kd, Nout, (Nout + per - 1) / per};
-  cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = 2;
-  at[0].val.clusterDim.y = 1;
-  at[0].val.clusterDim.z = 1;
-  // one persistent CTA per SM, as many whole pairs as can be resident
-  cfg.gridDim = dim3(sm_count() / 2 * 2, 1, 1);
-  cfg.blockDim = dim3(kThreadsI8, 1, 1);
-  cfg.dynamicSmemBytes = kSmem;
-  cfg.stream = s;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  static int resident = -1;
-  if (resident < 0) {
-    int n = 0;
-    resident = (cudaOccupancyMaxActiveClusters(&n, gmm_i8_kernel<kSwiglu, O>, &cfg) == cudaSuccess && n > 0)
-                   ? n
-                   : 0;
-    (void)cudaGetLastError();
-  }
-  if (resident > 0 && 2 * resident < (int)cfg.gridDim.x) cfg.gridDim.x = 2 * resident;
-  if (cudaLaunchKernelEx(&cfg, gmm_i8_kernel<kSwiglu, O>, w0, w1, x32, x8, p) != cudaSuccess) {
-    (void)cudaGetLastError();
-    return MOE_ERR_CUDA;
-  }
-  count_launches(1);
-  return MOE_OK;
+  return (long long)N <= kFewRows * E ? launch_cfg<I8Few, kSwiglu, O>(w0, w1, x32, x8, p, s)
+                                      : launch_cfg<I8Many, kSwiglu, O>(w0, w1, x32, x8, p, s);
 }
 
 }  // namespace

@@ -579,9 +579,9 @@ def moe_router_topk(logits, K: int, *, scoring: str = "softmax", renormalize: bo
     (float32 or bfloat16): (expert_ids [T, K] int32, probs [T, K] float32)."""
     T, E = logits.shape
     if expert_ids is None:
-        expert_ids = logits.new_empty((T, K), dtype=torch.int32)
+        expert_ids = torch.empty((T, K), dtype=torch.int32, device=logits.device)
     if probs is None:
-        probs = logits.new_empty((T, K), dtype=torch.float32)
+        probs = torch.empty((T, K), dtype=torch.float32, device=logits.device)
     _check(expert_ids, torch.int32, "expert_ids")
     _check(probs, torch.float32, "probs")
     _shape(expert_ids, (T, K), "expert_ids")
@@ -625,9 +625,9 @@ def moe_quantize_rows(x, *, row_map=None, K: int = 1, N: Optional[int] = None, q
     if N is None:
         N = T * K if row_map is not None else T
     if q is None:
-        q = x.new_empty((N, H), dtype=torch.int8)
+        q = torch.empty((N, H), dtype=torch.int8, device=x.device)
     if scale is None:
-        scale = x.new_empty(N, dtype=torch.float32)
+        scale = torch.empty(N, dtype=torch.float32, device=x.device)
     _check(q, torch.int8, "q")
     _check(scale, torch.float32, "scale")
     _shape(q, (N, H), "q")

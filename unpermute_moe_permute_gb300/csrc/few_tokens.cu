@@ -70,7 +70,8 @@ template <int NP, bool I8>
 struct FewTraits {
   static constexpr int k = I8 ? 128 : 64;                // k of a unit
   static constexpr uint32_t b_box = NP * 128;            // 64 k of the tokens
-  static constexpr uint32_t stage = 2 * kBox16 + (I8 ? 2 : 1) * b_box;
+  static constexpr bool can_narrow = NP == 16 && !I8;    // (see narrow below)
+  static constexpr uint32_t stage = 2 * kBox16 + (I8 || can_narrow ? 2 : 1) * b_box;
   static constexpr int stages = (int)(212992 / stage) < 6 ? (int)(212992 / stage) : 6;
   static constexpr int threads = (I8 ? 20 : 12) * 32;
   static constexpr int bars = 2 * stages + 4 + 4 + 2;
@@ -80,7 +81,8 @@ struct FewTraits {
   static constexpr uint32_t list = bitmap + 256;           // active experts
   static constexpr uint32_t slot = list + 2 * kMaxSlots;   // expert of each slot
   static constexpr uint32_t prob = slot + 2 * kMaxSlots;
-  static constexpr uint32_t smem = prob + 4 * kMaxSlots + 1024;
+  static constexpr uint32_t cross = prob + 4 * kMaxSlots;  // up values of a narrow tile [16][64]
+  static constexpr uint32_t smem = cross + (can_narrow ? 4096 : 0) + 1024;
   static_assert(smem <= 232448, "more shared memory than one CTA may use");
 };
 
@@ -199,6 +201,7 @@ __device__ __forceinline__ float swiglu(float g, float u) { return __fdividef(g,
 template <int NP, bool I8>
 __global__ void __launch_bounds__(FewTraits<NP, I8>::threads, 1)
 few_tokens_kernel(const __grid_constant__ CUtensorMap mapG, const __grid_constant__ CUtensorMap mapU,
+                  const __grid_constant__ CUtensorMap mapG64, const __grid_constant__ CUtensorMap mapU64,
                   const __grid_constant__ CUtensorMap mapD, const __grid_constant__ CUtensorMap mapX,
                   const __grid_constant__ CUtensorMap mapAct, const FewParams p) {
   using TR = FewTraits<NP, I8>;
@@ -222,6 +225,7 @@ few_tokens_kernel(const __grid_constant__ CUtensorMap mapG, const __grid_constan
   int16_t* list = reinterpret_cast<int16_t*>(g + TR::list);
   int16_t* slot = reinterpret_cast<int16_t*>(g + TR::slot);
   float* prob = reinterpret_cast<float*>(g + TR::prob);
+  float* cross = reinterpret_cast<float*>(g + TR::cross);
   const int warp = (int)uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
   const int TK = p.T * p.K, G = (int)gridDim.x, cta = (int)blockIdx.x;
 
@@ -242,6 +246,10 @@ few_tokens_kernel(const __grid_constant__ CUtensorMap mapG, const __grid_constan
     mbar_fence_init();
     tma_prefetch_desc(&mapG);
     tma_prefetch_desc(&mapU);
+    if (TR::can_narrow) {
+      tma_prefetch_desc(&mapG64);
+      tma_prefetch_desc(&mapU64);
+    }
     tma_prefetch_desc(&mapD);
     tma_prefetch_desc(&mapX);
     tma_prefetch_desc(&mapAct);
@@ -296,16 +304,29 @@ few_tokens_kernel(const __grid_constant__ CUtensorMap mapG, const __grid_constan
   tc_fence_after();
   const uint32_t tmem = uniform(holder[0]);
   const int A = (int)uniform(holder[3]);
-  const int nt1 = (p.I + 127) / 128, nt2 = (p.H + 255) / 256;
-  const int KB1 = (p.H + TR::k - 1) / TR::k, KB2 = (p.I + TR::k - 1) / TR::k;
+  // Phase 1, when a CTA has at most one tile: whole tiles, one CTA each, need no
+  // partial sums (8 us of stores, counts and loads at the end of the phase),
+  // but only as many CTAs stream as there are tiles, each at up to 60 GB/s
+  // against 6.7 TB/s for all.  For N = 16 also in tiles of 64 columns (gate and
+  // up rows together one A operand of 128).  T=1 H=2048 E=128 K=8 I=768: 96
+  // whole narrow tiles NARROW us, 48 tiles in 152 equal runs SPLIT us.
+  const int wide1 = (p.I + 127) / 128, bytes1 = 256 * p.H * (I8 ? 1 : 2);  // of a wide tile
+  const int t_split = A * wide1 * (bytes1 / 1024) / 6550 + 8;              // us
+  const int t_whole = A * wide1 <= G ? bytes1 / 60000 : t_split + 1;
+  const int t_narrow = TR::can_narrow && A * (p.I / 64) <= G ? bytes1 / 120000 : t_split + 1;
+  const bool narrow = t_narrow <= t_split && t_narrow < t_whole;
+  const int rows1 = narrow ? 64 : 128;
+  const int nt1 = (p.I + rows1 - 1) / rows1, nt2 = (p.H + 255) / 256;
+  const int k1 = narrow ? 2 * TR::k : TR::k;  // k of a unit of phase 1
+  const int KB1 = (p.H + k1 - 1) / k1, KB2 = (p.I + TR::k - 1) / TR::k;
   const int U1 = A * nt1 * KB1, U2 = nt2 * A * KB2;
-  const int G1 = min(G, U1), G2 = min(G, U2);
+  const int G1 = narrow || t_whole <= t_split ? A * nt1 : min(G, U1), G2 = min(G, U2);
   const int lo1 = cta < G1 ? first_unit(U1, cta, G1) : 0, hi1 = cta < G1 ? first_unit(U1, cta + 1, G1) : 0;
   const int lo2 = cta < G2 ? first_unit(U2, cta, G2) : 0, hi2 = cta < G2 ? first_unit(U2, cta + 1, G2) : 0;
   const Segments seg1(lo1, hi1, KB1);
   uint32_t* ready = p.count;
   uint32_t* cnt1 = ready + p.A_max;
-  uint32_t* cnt2 = cnt1 + (size_t)p.A_max * nt1;
+  uint32_t* cnt2 = cnt1 + (size_t)p.A_max * wide1;
   unsigned long long* flags = p.epoch + 1;
 
   // One warp waits until every CTA's counters are clear (and every CTA has read
@@ -333,47 +354,55 @@ few_tokens_kernel(const __grid_constant__ CUtensorMap mapG, const __grid_constan
   }
 
   if (warp == 0) {
-    // ---------------- weights ----------------
-    if (lane == 0) {
-      int s = 0, n = 0;
-      uint32_t ph = 0;
-      auto slot_free = [&]() { return mbar_wait(empty(s), ph ^ 1u, abort_flag, p.status); };
-      auto next = [&]() {
-        ++n;
-        if (++s == S) s = 0, ph ^= 1u;
-      };
-      bool run = true;
-      for (int i = 0; run && i < seg1.count; ++i) {
-        int tile, u, len;
-        seg1.get(i, tile, u, len);
-        const int kb = u - tile * KB1, e = list[tile / nt1], i0 = (tile % nt1) * 128;
-        for (int k = kb; k < kb + len; ++k) {
-          if (!(run = slot_free())) break;
-          const uint32_t a = base + s * TR::stage;
-          mbar_arrive_expect_tx(full(s), 2 * kBox16);
-          tma_load_3d(a, &mapG, full(s), k * TR::k, i0, e);
-          tma_load_3d(a + kBox16, &mapU, full(s), k * TR::k, i0, e);
-          next();
+    // ---------------- weights: the whole warp, one lane elected for each copy ----------------
+    int s = 0, n = 0;
+    uint32_t ph = 0;
+    bool run = true;
+    auto next = [&]() {
+      ++n;
+      if (++s == S) s = 0, ph ^= 1u;
+    };
+    for (int i = 0; run && i < seg1.count; ++i) {
+      int tile, u, len;
+      seg1.get(i, tile, u, len);
+      const int kb = u - tile * KB1, e = (int)uniform(list[tile / nt1]);
+      const int i0 = (tile % nt1) * rows1;
+      for (int k = kb; k < kb + len; ++k) {
+        run = mbar_wait_warp(empty(s), ph ^ 1u, abort_flag, p.status);
+        if (!run) break;
+        const uint32_t a = base + s * TR::stage;
+        mbar_arrive_expect_tx_warp(full(s), 2 * kBox16);
+        if (narrow) {  // 64 rows of each, two k blocks
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            tma_load_3d_warp(a + h * kBox16, &mapG64, full(s), k * k1 + h * TR::k, i0, e);
+            tma_load_3d_warp(a + h * kBox16 + kBox16 / 2, &mapU64, full(s), k * k1 + h * TR::k, i0, e);
+          }
+        } else {
+          tma_load_3d_warp(a, &mapG, full(s), k * TR::k, i0, e);
+          tma_load_3d_warp(a + kBox16, &mapU, full(s), k * TR::k, i0, e);
         }
+        next();
       }
-      for (int u = lo2; run && u < hi2;) {
-        const int ta = u / KB2, kb = u - ta * KB2, len = min(KB2 - kb, hi2 - u);
-        const int e = list[ta % A], h0 = (ta / A) * 256;
-        for (int k = kb; k < kb + len; ++k) {
-          if (!(run = slot_free())) break;
-          const uint32_t a = base + s * TR::stage;
-          mbar_arrive_expect_tx(full(s), 2 * kBox16);
-          tma_load_3d(a, &mapD, full(s), k * TR::k, h0, e);
-          tma_load_3d(a + kBox16, &mapD, full(s), k * TR::k, h0 + 128, e);
-          next();
-        }
-        u += len;
+    }
+    for (int u = lo2; run && u < hi2;) {
+      const int ta = u / KB2, kb = u - ta * KB2, len = min(KB2 - kb, hi2 - u);
+      const int e = (int)uniform(list[ta % A]), h0 = (ta / A) * 256;
+      for (int k = kb; k < kb + len; ++k) {
+        run = mbar_wait_warp(empty(s), ph ^ 1u, abort_flag, p.status);
+        if (!run) break;
+        const uint32_t a = base + s * TR::stage;
+        mbar_arrive_expect_tx_warp(full(s), 2 * kBox16);
+        tma_load_3d_warp(a, &mapD, full(s), k * TR::k, h0, e);
+        tma_load_3d_warp(a + kBox16, &mapD, full(s), k * TR::k, h0 + 128, e);
+        next();
       }
-      // every copy has landed before the CTA may exit
-      for (int st = 0; st < S && st < n; ++st) {
-        const int last = st + (n - 1 - st) / S * S;
-        mbar_wait(full(st), (uint32_t)(last / S) & 1u, abort_flag, p.status, false);
-      }
+      u += len;
+    }
+    // every copy has landed before the CTA may exit
+    for (int st = 0; st < S && st < n; ++st) {
+      const int last = st + (n - 1 - st) / S * S;
+      mbar_wait_warp(full(st), (uint32_t)(last / S) & 1u, abort_flag, p.status, false);
     }
   } else if (warp == 10) {
     // ---------------- tokens, activations ----------------
@@ -385,13 +414,11 @@ few_tokens_kernel(const __grid_constant__ CUtensorMap mapG, const __grid_constan
      seg1.get(i, tile, u, len);
      for (int k = u - tile * KB1; len > 0; ++k, --len) {
       if (!(run = mbar_wait_warp(empty(s), ph ^ 1u, abort_flag, p.status))) break;
-      if (lane == 0) {
-        const uint32_t b = base + s * TR::stage + 2 * kBox16;
-        mbar_arrive_expect_tx(full(s), I8 ? 2 * TR::b_box : TR::b_box);
-        tma_load_2d(b, &mapX, full(s), k * TR::k, 0);
-        if constexpr (I8) tma_load_2d(b + TR::b_box, &mapX, full(s), k * TR::k + 64, 0);
-      }
-      __syncwarp();
+      const uint32_t b = base + s * TR::stage + 2 * kBox16;
+      const bool both = I8 || narrow;  // 128 k
+      mbar_arrive_expect_tx_warp(full(s), both ? 2 * TR::b_box : TR::b_box);
+      tma_load_2d_warp(b, &mapX, full(s), k * k1, 0);
+      if (both) tma_load_2d_warp(b + TR::b_box, &mapX, full(s), k * k1 + 64, 0);
       if (++s == S) s = 0, ph ^= 1u;
      }
     }
@@ -402,18 +429,15 @@ few_tokens_kernel(const __grid_constant__ CUtensorMap mapG, const __grid_constan
       if (a != seen && checked < A) {  // (the experts come round in order)
         run = poll_warp([&]() { return ld_relaxed(ready + a) == (uint32_t)nt1; }, abort_flag, p.status);
         if (!run) break;
+        asm volatile("fence.proxy.async.global;" ::: "memory");  // (before the copies read them)
         seen = a;
         ++checked;
       }
       if (!(run = mbar_wait_warp(empty(s), ph ^ 1u, abort_flag, p.status))) break;
-      if (lane == 0) {
-        asm volatile("fence.proxy.async.global;" ::: "memory");
-        const uint32_t b = base + s * TR::stage + 2 * kBox16;
-        mbar_arrive_expect_tx(full(s), I8 ? 2 * TR::b_box : TR::b_box);
-        tma_load_3d(b, &mapAct, full(s), k * TR::k, 0, a);
-        if constexpr (I8) tma_load_3d(b + TR::b_box, &mapAct, full(s), k * TR::k + 64, 0, a);
-      }
-      __syncwarp();
+      const uint32_t b = base + s * TR::stage + 2 * kBox16;
+      mbar_arrive_expect_tx_warp(full(s), I8 ? 2 * TR::b_box : TR::b_box);
+      tma_load_3d_warp(b, &mapAct, full(s), k * TR::k, 0, a);
+      if constexpr (I8) tma_load_3d_warp(b + TR::b_box, &mapAct, full(s), k * TR::k + 64, 0, a);
       if (++s == S) s = 0, ph ^= 1u;
     }
   } else if (warp == 1) {
@@ -424,7 +448,7 @@ few_tokens_kernel(const __grid_constant__ CUtensorMap mapG, const __grid_constan
     uint32_t ph = 0, cph = 0;
     bool run = true;
     // one segment: len units of one tile (phase 1) or one tile and expert (phase 2)
-    auto segment = [&](int len) {
+    auto segment = [&](int len, bool two) {
       const int acc = it & 1;
       run = mbar_wait_warp(t_empty(acc), ((it >> 1) & 1) ^ 1u, abort_flag, p.status);
       if (!run) return;
@@ -455,7 +479,8 @@ few_tokens_kernel(const __grid_constant__ CUtensorMap mapG, const __grid_constan
           if (c == 0) cph ^= 1u;
         } else {
           umma_f16_k64_warp(d, ad, bd, idesc, accum);
-          umma_f16_k64_warp(d + NP, ad + (kBox16 >> 4), bd, idesc, accum);
+          if (two) umma_f16_k64_warp(d + NP, ad + (kBox16 >> 4), bd, idesc, accum);
+          else umma_f16_k64_warp(d, ad + (kBox16 >> 4), bd + (TR::b_box >> 4), idesc, 1u);
           accum = 1u;
         }
         umma_commit_warp(empty(s));
@@ -467,11 +492,11 @@ few_tokens_kernel(const __grid_constant__ CUtensorMap mapG, const __grid_constan
     for (int i = 0; run && i < seg1.count; ++i) {
       int tile, u, len;
       seg1.get(i, tile, u, len);
-      segment(len);
+      segment(len, !narrow);
     }
     for (int u = lo2; run && u < hi2;) {
       const int len = min(KB2 - u % KB2, hi2 - u);
-      segment(len);
+      segment(len, true);
       u += len;
     }
     umma_commit_warp(drain);
@@ -500,7 +525,7 @@ few_tokens_kernel(const __grid_constant__ CUtensorMap mapG, const __grid_constan
     for (; run && it < seg1.count; ++it) {
       int tile, u, len;
       seg1.get(it, tile, u, len);
-      const int a = tile / nt1, e = list[a], i = (tile % nt1) * 128 + r;
+      const int a = tile / nt1, e = list[a], i = (tile % nt1) * rows1 + (r & (rows1 - 1));
       const bool in = i < p.I;
       const int acc = it & 1;
       float gsc = 1.f, usc = 1.f;
@@ -514,9 +539,25 @@ few_tokens_kernel(const __grid_constant__ CUtensorMap mapG, const __grid_constan
       const size_t pstride = (size_t)p.T * 256;  // floats of a partial
       float* part = p.part1 + (size_t)col0 * 256 + r;
       float* mine = part + ((size_t)cta * 2 + (u == lo1 ? 0 : 1)) * pstride;
+      if constexpr (TR::can_narrow) {
+        if (narrow) {  // lanes 0-63 hold gate, 64-127 up: up crosses through shared memory
+          uint32_t v[8];
+          tmem_ld_32x32b_x8(d, v);
+          tmem_ld_wait();
+          float* x = cross + (size_t)col0 * 64 + (r & 63);
+          if (r >= 64)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) x[j * 64] = __uint_as_float(v[j]);
+          epi_sync();
+          if (r < 64)
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              if (j < T) act[(size_t)j * p.I] = __float2bfloat16_rn(swiglu(__uint_as_float(v[j]), x[j * 64]));
+        }
+      }
 #pragma unroll
       for (int c0 = 0; c0 < NC; c0 += CH) {
-        if (c0 >= T) break;
+        if (c0 >= T || narrow) break;
         uint32_t gv[CH], uv[CH];
         if constexpr (CH == 16) {
           tmem_ld_32x32b_x16(d + c0, gv);
@@ -762,14 +803,15 @@ int launch_few(FewParams p, const void* x, const void* Wg, const void* Wu, const
                cudaStream_t s) {
   using TR = FewTraits<NP, I8>;
   constexpr int esz = I8 ? 1 : 2;
-  CUtensorMap mg, mu, md, mx, ma;
+  CUtensorMap mg, mu, mg64, mu64, md, mx, ma;
   const uint64_t d1[3] = {(uint64_t)p.H, (uint64_t)p.I, (uint64_t)p.E};
   const uint64_t d2[3] = {(uint64_t)p.I, (uint64_t)p.H, (uint64_t)p.E};
-  const uint32_t bw[3] = {128 / esz, 128, 1};
+  const uint32_t bw[3] = {128 / esz, 128, 1}, bw64[3] = {128 / esz, 64, 1};
   const uint64_t dx[2] = {(uint64_t)p.H, (uint64_t)p.T};
   const uint64_t da[3] = {(uint64_t)p.I, (uint64_t)p.T, (uint64_t)p.A_max};
   const uint32_t bx[3] = {64, NP, 1};
   if (!make_map_sw128(&mg, Wg, esz, 3, d1, bw) || !make_map_sw128(&mu, Wu, esz, 3, d1, bw) ||
+      !make_map_sw128(&mg64, Wg, esz, 3, d1, bw64) || !make_map_sw128(&mu64, Wu, esz, 3, d1, bw64) ||
       !make_map_sw128(&md, Wd, esz, 3, d2, bw) || !make_map_sw128(&mx, x, 2, 2, dx, bx) ||
       !make_map_sw128(&ma, p.act, 2, 3, da, bx))
     return MOE_ERR_CUDA;
@@ -790,7 +832,7 @@ int launch_few(FewParams p, const void* x, const void* Wg, const void* Wu, const
   cfg.stream = s;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, few_tokens_kernel<NP, I8>, mg, mu, md, mx, ma, p) != cudaSuccess) {
+  if (cudaLaunchKernelEx(&cfg, few_tokens_kernel<NP, I8>, mg, mu, mg64, mu64, md, mx, ma, p) != cudaSuccess) {
     (void)cudaGetLastError();
     return MOE_ERR_CUDA;
   }

@@ -28,14 +28,15 @@
 // memory of their own SM, is read by that SM's tensor core alone, and is
 // ordered by tcgen05.wait::st and the async-proxy fence before the arrival.
 // A cluster-scope release there, by one forwarding thread, cost 1100 cycles a
-// step (398 us instead of LATER us for 8192 x 4096 x 4096).
+// step (8192 x 4096 x 4096: 399 us against 262 us, the rest being as it was).
+#include <cuda_fp16.h>
 #include <math.h>
 
 #include <mutex>
 
 #include "common.cuh"
 #include "sched.cuh"
-#include "tc_ptx.cuh"
+#include "tc_warp.cuh"
 #include "tma_host.cuh"
 
 namespace moe {
@@ -537,11 +538,13 @@ int launch_cfg(const CUtensorMap& w0, const CUtensorMap& w1, const CUtensorMap& 
   return MOE_OK;
 }
 
-#ifndef I8_FEW_ROWS
-#define I8_FEW_ROWS 48
-#endif
-// Rows per expert, on average, up to which the few-rows form runs.
-constexpr long long kFewRows = I8_FEW_ROWS;
+// Rows per expert, on average, up to which the few-rows form runs (the routing
+// itself is not known on the host).  GB300, E=64 H=2048, us, few / many:
+//   rows  I=512 gate/up    down        I=768 gate/up    down
+//     25  42.6 / 49.2   28.7 / 32.8    55.4 / 65.5   34.8 / 41.0
+//     48  45.1 / 49.9   32.8 / 32.9    61.4 / 65.5   36.9 / 41.2
+//     64  49.2 / 53.2   38.9 / 34.8    77.8 / 69.2   49.2 / 43.3
+constexpr long long kFewRows = 48;
 
 template <bool kSwiglu, typename O>
 int launch_i8(const int8_t* A, const float* rs, const int8_t* B0, const float* s0, const int8_t* B1,

@@ -208,3 +208,31 @@ def test_int8_layer_of_a_prompt(lib):
     want = torch.einsum("tk,tkhi,tki->th", probs.double(), Wd.double()[i], torch.nn.functional.silu(h[0]) * h[1])
     rel = float((out.double() - want).norm() / want.norm())
     assert rel < 0.03
+
+
+@pytest.mark.parametrize("per", [96, 8])
+def test_products_repeat(lib, per):
+    """A late copy in one launch of thousands must not let a stage through early:
+    many launches over more tiles than CTAs, in both forms (96 rows an expert, 8
+    rows), give the same bytes and no error."""
+    E, H, I = 64, 1024, 768
+    g = torch.Generator(device=DEV).manual_seed(per)
+
+    def ints(*shape):
+        return torch.randint(-127, 128, shape, device=DEV, generator=g, dtype=torch.int8)
+
+    off = torch.arange(0, E + 1, dtype=torch.int32, device=DEV) * per
+    N = E * per
+    x, wg, wu = ints(N, H), ints(E, I, H), ints(E, I, H)
+    rs = torch.full((N,), 1e-3, device=DEV)
+    cs = torch.full((E, I), 1e-3, device=DEV)
+    st = lib.new_status()
+    up = lib.moe_gate_up_swiglu_int8(x, rs, off, wg, cs, wu, cs, dev_status=st).clone()
+    down = lib.moe_down_proj_int8(x, rs, off, wg, cs, dev_status=st).clone()
+    differ = torch.zeros((), dtype=torch.int64, device=DEV)
+    for i in range(3000):
+        u = lib.moe_gate_up_swiglu_int8(x, rs, off, wg, cs, wu, cs, dev_status=st)
+        d = lib.moe_down_proj_int8(x, rs, off, wg, cs, dev_status=st)
+        if i % 20 == 0:
+            differ += (u != up).sum() + (d != down).sum()
+    assert int(differ) == 0 and int(st) == 0

@@ -13,7 +13,7 @@
 //   * the weights are the A operand (M = channels): they go from the 8-bit
 //     tile through registers into tensor memory, never back to shared memory;
 //   * the rows are the B operand (N = rows), so a tile takes as many rows as
-//     an expert has, in steps of 16 up to 320 (two accumulators of 160): 25
+//     an expert has, in steps of 32 up to 320 (two accumulators of 160): 25
 //     rows cost 32 columns, not 128 rows, and the weights of an expert of up
 //     to 320 rows are loaded and expanded once;
 //   * CTA pairs (cta_group::2): 256 channels per MMA, each CTA expands its
@@ -57,7 +57,18 @@ struct I8Cfg {
   static constexpr int kBGroup = (kRowTile + 63) / 64;  // warps that expand B, per group
   static constexpr int kAWarp = 2 + kEpi, kBWarp = kAWarp + 4 * kGroups;
   static constexpr int kThreads = (kBWarp + kGroups * kBGroup) * 32;
-  static constexpr int kBars = 2 * kStages + 2 * kGroups + 4 + 1;
+  // A group handles every kGroups-th stage, so it would meet a slot's "loaded"
+  // barrier only at every second use (3 slots, 2 groups), where the phase
+  // parity of the use it waits for and of the one two before are the same: a
+  // late load in between would let it through early.  So each (slot, group)
+  // has a barrier of its own: stage i signals number i mod lcm(slots, groups).
+  static constexpr int lcm(int a, int b) {
+    int m = a;
+    while (m % b) m += a;
+    return m;
+  }
+  static constexpr int kFulls = lcm(kStages, kGroups);
+  static constexpr int kBars = kFulls + kStages + 2 * kGroups + 4 + 1;
   static constexpr uint32_t kStageWarp = 2048 + 128;  // epilogue staging of a warp: rows, row scales
   static constexpr uint32_t kStage = kStages * (kA8 + kB8) + kGroups * kB16;
   static constexpr uint32_t kCtrl = kStage + kEpi * kStageWarp;
@@ -66,7 +77,7 @@ struct I8Cfg {
   static constexpr uint32_t kSmem = kTable + 2 * (kMaxExperts + 1) * 4 + 32 * 4 + 1024;
   static_assert(kSmem <= 232448, "more shared memory than one CTA may use");
   static_assert(kACol + kGroups * 64 <= 512, "more tensor memory than there is");
-  static_assert(kGroups <= kStages && kRowTile % 64 == 0, "geometry");
+  static_assert(kGroups <= kStages && kSub % 32 == 0 && kFulls % kGroups == 0, "geometry");
 };
 
 // Experts with rows: two accumulators of 160 columns.  Experts with few rows
@@ -88,7 +99,7 @@ struct I8Params {
 struct I8Tile {
   int e, row0, hi;  // expert, first row, end of the tile's rows
   int subs;         // accumulators the rows take: 1 or 2
-  int n;            // MMA N of each: a multiple of 16, at least 32
+  int n;            // MMA N of each: a multiple of 32
   int ch0;          // first channel of this CTA
   __device__ __forceinline__ int b_rows() const { return subs * n / 2; }  // of this CTA
 };
@@ -108,7 +119,7 @@ __device__ __forceinline__ I8Tile i8_tile(int t, const I8Params& p, const int32_
   x.row0 = r.lo + i * per;
   x.hi = min(r.hi, x.row0 + per);
   x.subs = per > kSub ? 2 : 1;
-  x.n = max(32, ((per + x.subs - 1) / x.subs + 15) & ~15);
+  x.n = ((per + x.subs - 1) / x.subs + 31) & ~31;  // (pairs take N in steps of 32)
   x.ch0 = (t - g * p.ch_tiles) * (kSwiglu ? 128 : 256) + rank * (kSwiglu ? 64 : 128);
   return x;
 }
@@ -152,10 +163,10 @@ __device__ __forceinline__ float2 mul2(uint32_t x, uint32_t y, float s, float t)
 template <typename C, bool kSwiglu, typename O>
 __global__ void __launch_bounds__(C::kThreads, 1)
 gmm_i8_kernel(const __grid_constant__ CUtensorMap mapW0, const __grid_constant__ CUtensorMap mapW1,
-              const __grid_constant__ CUtensorMap mapX32, const __grid_constant__ CUtensorMap mapX8,
+              const __grid_constant__ CUtensorMap mapX32, const __grid_constant__ CUtensorMap mapX16,
               const I8Params p) {
   constexpr int kSub = C::kSub, kGroups = C::kGroups, kStages = C::kStages, kBGroup = C::kBGroup;
-  constexpr int kAWarp = C::kAWarp, kBWarp = C::kBWarp, kEpi = C::kEpi;
+  constexpr int kAWarp = C::kAWarp, kBWarp = C::kBWarp, kEpi = C::kEpi, kFulls = C::kFulls;
   constexpr uint32_t kA8 = C::kA8, kB8 = C::kB8, kB16 = C::kB16, kACol = C::kACol;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
@@ -163,13 +174,14 @@ gmm_i8_kernel(const __grid_constant__ CUtensorMap mapW0, const __grid_constant__
   uint8_t* g = smem_raw + (base - raw);
   const uint32_t sA8 = base, sB8 = base + kStages * kA8, sB16 = sB8 + kStages * kB8;
   const uint32_t bars = base + C::kCtrl;
-  auto q_full = [&](int s) { return bars + 8u * s; };
-  auto q_empty = [&](int s) { return bars + 8u * (kStages + s); };
-  auto c_full = [&](int b) { return bars + 8u * (2 * kStages + b); };
-  auto c_empty = [&](int b) { return bars + 8u * (2 * kStages + kGroups + b); };
-  auto t_full = [&](int a) { return bars + 8u * (2 * kStages + 2 * kGroups + a); };
-  auto t_empty = [&](int a) { return bars + 8u * (2 * kStages + 2 * kGroups + 2 + a); };
-  const uint32_t drain = bars + 8u * (2 * kStages + 2 * kGroups + 4);
+  auto q_full = [&](int i) { return bars + 8u * i; };  // i: stage mod kFulls
+  auto q_empty = [&](int s) { return bars + 8u * (kFulls + s); };
+  const uint32_t bars2 = bars + 8u * (kFulls + kStages);
+  auto c_full = [&](int b) { return bars2 + 8u * b; };
+  auto c_empty = [&](int b) { return bars2 + 8u * (kGroups + b); };
+  auto t_full = [&](int a) { return bars2 + 8u * (2 * kGroups + a); };
+  auto t_empty = [&](int a) { return bars2 + 8u * (2 * kGroups + 2 + a); };
+  const uint32_t drain = bars2 + 8u * (2 * kGroups + 4);
   uint32_t* holder = reinterpret_cast<uint32_t*>(g + C::kHolder);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(g + C::kHolder + 4);
   int32_t* prefix = reinterpret_cast<int32_t*>(g + C::kTable);
@@ -178,8 +190,8 @@ gmm_i8_kernel(const __grid_constant__ CUtensorMap mapW0, const __grid_constant__
   const int warp = (int)uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
+    for (int i = 0; i < kFulls; ++i) mbar_init(q_full(i), 1);
     for (int s = 0; s < kStages; ++s) {
-      mbar_init(q_full(s), 1);
       mbar_init(q_empty(s), 4 + kBGroup);  // an expanding group
     }
     for (int b = 0; b < kGroups; ++b) {
@@ -198,8 +210,11 @@ gmm_i8_kernel(const __grid_constant__ CUtensorMap mapW0, const __grid_constant__
     tma_prefetch_desc(&mapW0);
     if constexpr (kSwiglu) tma_prefetch_desc(&mapW1);
     tma_prefetch_desc(&mapX32);
-    tma_prefetch_desc(&mapX8);
+    tma_prefetch_desc(&mapX16);
   }
+  // Both CTAs are present and their barriers initialised before either uses
+  // the other's (the pair's tensor-memory allocation included).
+  cluster_sync_all();
   if (warp == kMmaWarp) {
     tmem_alloc_pair(smem_u32(holder), 512);
     tmem_relinquish_pair();
@@ -211,14 +226,13 @@ gmm_i8_kernel(const __grid_constant__ CUtensorMap mapW0, const __grid_constant__
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *holder;
-  cluster_sync_all();  // both CTAs' barriers are initialised
   const int rank = (int)cluster_ctarank();
   const int t0 = (int)cluster_id_x(), dt = (int)cluster_count_x();
   const int stages = (p.Kd + 127) / 128;
 
   if (warp == kTmaWarp) {  // the whole warp, one lane elected for each copy
     const uint32_t ub = uniform(base);
-    int s = 0, n = 0;
+    int s = 0, f = 0, n = 0;  // slot, its barrier, stages so far
     uint32_t ph = 0;
     bool run = true;
     for (int t = t0; run && t < total; t += dt) {
@@ -229,28 +243,29 @@ gmm_i8_kernel(const __grid_constant__ CUtensorMap mapW0, const __grid_constant__
       for (int k = 0; k < stages; ++k) {
         run = mbar_wait_warp(q_empty(s), ph ^ 1u, abort_flag, p.status);
         if (!run) break;
-        mbar_arrive_expect_tx_warp(q_full(s), tx);
+        mbar_arrive_expect_tx_warp(q_full(f), tx);
         const uint32_t a = ub + s * kA8;
         uint32_t b = ub + kStages * kA8 + s * kB8;
-        tma_load_3d_warp(a, &mapW0, q_full(s), k * 128, ch0, e);
-        if constexpr (kSwiglu) tma_load_3d_warp(a + kA8 / 2, &mapW1, q_full(s), k * 128, ch0, e);
+        tma_load_3d_warp(a, &mapW0, q_full(f), k * 128, ch0, e);
+        if constexpr (kSwiglu) tma_load_3d_warp(a + kA8 / 2, &mapW1, q_full(f), k * 128, ch0, e);
         // this CTA's half of each accumulator's rows, one after the other
         for (int j = 0; j < subs; ++j) {
           int r = 0;
           for (; r + 32 <= nh; r += 32, b += 4096)
-            tma_load_2d_warp(b, &mapX32, q_full(s), k * 128, r0 + j * 2 * nh + r);
-          for (; r < nh; r += 8, b += 1024)
-            tma_load_2d_warp(b, &mapX8, q_full(s), k * 128, r0 + j * 2 * nh + r);
+            tma_load_2d_warp(b, &mapX32, q_full(f), k * 128, r0 + j * 2 * nh + r);
+          if (r < nh) {
+            tma_load_2d_warp(b, &mapX16, q_full(f), k * 128, r0 + j * 2 * nh + r);
+            b += 2048;
+          }
         }
         ++n;
         if (++s == kStages) s = 0, ph ^= 1u;
+        if (++f == kFulls) f = 0;
       }
     }
     // every copy has landed before the CTA may exit
-    for (int st = 0; st < kStages && st < n; ++st) {
-      const int last = st + (n - 1 - st) / kStages * kStages;
-      mbar_wait_warp(q_full(st), (uint32_t)(last / kStages) & 1u, abort_flag, p.status, false);
-    }
+    for (int i = max(0, n - kStages); i < n; ++i)
+      mbar_wait_warp(q_full(i % kFulls), (uint32_t)(i / kFulls) & 1u, abort_flag, p.status, false);
   } else if (warp == kMmaWarp) {
     if (rank == 0) {  // the whole warp, one lane elected for each MMA
       const uint64_t bdesc0 = desc_sw128(uniform(sB16), 16, 1024);
@@ -315,14 +330,14 @@ gmm_i8_kernel(const __grid_constant__ CUtensorMap mapW0, const __grid_constant__
     const uint32_t b_dst = sB16 + grp * kB16 + row * 128 + ((row & 7) << 4);
     const uint32_t step = is_a ? kA8 : kB8;
     const uint32_t full_of_leader = mapa_shared(c_full(grp), 0);
-    int s = grp, n0 = 0;  // ring stage; stages before this tile (mod kGroups)
+    int s = grp, f = grp, n0 = 0;  // slot, its barrier; stages before this tile (mod kGroups)
     uint32_t ph = 0, bph = 0;
     bool run = true;
     for (int t = t0; run && t < total; t += dt) {
       // B rows past the tile's own are not expanded (the MMA does not read them)
       const bool any = is_a || rg * 32 < i8_tile<kSwiglu, kSub>(t, p, prefix, offs, rank).b_rows();
       for (int k = (grp - n0 + kGroups) % kGroups; k < stages; k += kGroups) {
-        run = mbar_wait_warp(q_full(s), ph, abort_flag, p.status);
+        run = mbar_wait_warp(q_full(f), ph, abort_flag, p.status);
         if (!run) break;
         uint4 v[4];
         uint32_t r[32];
@@ -360,10 +375,14 @@ gmm_i8_kernel(const __grid_constant__ CUtensorMap mapW0, const __grid_constant__
         mbar_arrive_cluster_warp(full_of_leader);
         bph ^= 1u;
         s += kGroups;
-        if (s >= kStages) s -= kStages, ph ^= 1u;
+        if (s >= kStages) s -= kStages;
+        f += kGroups;
+        if (f >= kFulls) f -= kFulls, ph ^= 1u;
       }
       n0 = (n0 + stages) % kGroups;
     }
+    // the last of the leader's signals to this CTA's barriers has arrived
+    if (run) mbar_wait_warp(c_empty(grp), bph ^ 1u, abort_flag, p.status);
   } else {
     // ---- epilogue: lanes are channels, accumulator columns are rows ----
     // The warps of a quarter take pieces of 32 columns in turn.  A piece
@@ -500,7 +519,7 @@ int check_i8(const void* A, const float* rs, const int32_t* off, int N, int H, i
 
 template <typename C, bool kSwiglu, typename O>
 int launch_cfg(const CUtensorMap& w0, const CUtensorMap& w1, const CUtensorMap& x32,
-               const CUtensorMap& x8, const I8Params& p, cudaStream_t s) {
+               const CUtensorMap& x16, const I8Params& p, cudaStream_t s) {
   static std::once_flag once;
   static cudaError_t attr = cudaSuccess;
   std::call_once(once, [] {
@@ -530,7 +549,7 @@ int launch_cfg(const CUtensorMap& w0, const CUtensorMap& w1, const CUtensorMap& 
     (void)cudaGetLastError();
   }
   if (resident > 0 && 2 * resident < (int)cfg.gridDim.x) cfg.gridDim.x = 2 * resident;
-  if (cudaLaunchKernelEx(&cfg, gmm_i8_kernel<C, kSwiglu, O>, w0, w1, x32, x8, p) != cudaSuccess) {
+  if (cudaLaunchKernelEx(&cfg, gmm_i8_kernel<C, kSwiglu, O>, w0, w1, x32, x16, p) != cudaSuccess) {
     (void)cudaGetLastError();
     return MOE_ERR_CUDA;
   }
@@ -551,18 +570,18 @@ int launch_i8(const int8_t* A, const float* rs, const int8_t* B0, const float* s
               const float* s1, const int32_t* off, int N, int Kd, int Nout, int E, O* out,
               int32_t* status, cudaStream_t s) {
   if (int rc = device_ok()) return rc;
-  CUtensorMap w0, w1, x32, x8;
+  CUtensorMap w0, w1, x32, x16;
   const uint64_t dw[3] = {(uint64_t)Kd, (uint64_t)Nout, (uint64_t)E};
   const uint32_t bw[3] = {128, kSwiglu ? 64u : 128u, 1};
   const uint64_t dx[2] = {(uint64_t)Kd, (uint64_t)N};
-  const uint32_t b32[2] = {128, 32}, b8[2] = {128, 8};
+  const uint32_t b32[2] = {128, 32}, b16[2] = {128, 16};
   if (!make_map_sw128(&w0, B0, 1, 3, dw, bw) || !make_map_sw128(&w1, B1 ? B1 : B0, 1, 3, dw, bw) ||
-      !make_map_sw128(&x32, A, 1, 2, dx, b32) || !make_map_sw128(&x8, A, 1, 2, dx, b8))
+      !make_map_sw128(&x32, A, 1, 2, dx, b32) || !make_map_sw128(&x16, A, 1, 2, dx, b16))
     return MOE_ERR_CUDA;
   const int per = kSwiglu ? 128 : 256;
   const I8Params p{off, rs, s0, s1, out, status, N, E, Kd, Nout, (Nout + per - 1) / per};
-  return (long long)N <= kFewRows * E ? launch_cfg<I8Few, kSwiglu, O>(w0, w1, x32, x8, p, s)
-                                      : launch_cfg<I8Many, kSwiglu, O>(w0, w1, x32, x8, p, s);
+  return (long long)N <= kFewRows * E ? launch_cfg<I8Few, kSwiglu, O>(w0, w1, x32, x16, p, s)
+                                      : launch_cfg<I8Many, kSwiglu, O>(w0, w1, x32, x16, p, s);
 }
 
 }  // namespace

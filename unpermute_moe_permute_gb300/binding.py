@@ -128,7 +128,7 @@ def load_library(path: Optional[str] = None):
 
 
 def _call(name: str, *args):
-    lib = load_library()
+    lib = _lib or load_library()
     rc = getattr(lib, name)(*args)
     if rc != MOE_OK:
         raise MoeError(name, rc, lib.moe_status_string(rc).decode())
@@ -139,11 +139,35 @@ def _stream() -> int:
 
 
 # The raw handle of the same stream without building a Stream object (1 us a
-# call), where torch has it.
+# call), where torch has it; the arguments before it are on the device, so torch
+# has been set up.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-if _raw_stream is not None:
+_get_device = getattr(torch._C, "_cuda_getDevice", None)
+if _raw_stream is not None and _get_device is not None:
     def _stream() -> int:  # noqa: F811
-        return _raw_stream(torch.cuda.current_device())
+        return _raw_stream(_get_device())
+
+
+# Outputs of the calls of a few microseconds.  Beside a launch, torch.empty
+# costs 4.6 us for the first tensor and 2.1 for the second (1.5 alone); torch's
+# direct allocation of a strided tensor, where it is there, half of that.
+try:
+    _empty_strided = torch._C._dynamo.guards._empty_strided_cuda
+except AttributeError:
+    _empty_strided = None
+
+
+def _empty1(n: int, dtype, like: torch.Tensor) -> torch.Tensor:
+    if _empty_strided is not None and like.is_cuda and like.get_device() == _get_device():
+        return _empty_strided((n,), (1,), dtype)
+    return torch.empty(n, dtype=dtype, device=like.device)
+
+
+def _empty2(n: int, m: int, dtype, like: torch.Tensor) -> torch.Tensor:
+    """An uninitialised [n, m] on the device of `like`."""
+    if _empty_strided is not None and like.is_cuda and like.get_device() == _get_device():
+        return _empty_strided((n, m), (m, 1), dtype)
+    return torch.empty((n, m), dtype=dtype, device=like.device)
 
 
 def _ptr(t: Optional[torch.Tensor]):
@@ -579,13 +603,15 @@ def moe_router_topk(logits, K: int, *, scoring: str = "softmax", renormalize: bo
     (float32 or bfloat16): (expert_ids [T, K] int32, probs [T, K] float32)."""
     T, E = logits.shape
     if expert_ids is None:
-        expert_ids = torch.empty((T, K), dtype=torch.int32, device=logits.device)
+        expert_ids = _empty2(T, K, torch.int32, logits)
+    else:
+        _check(expert_ids, torch.int32, "expert_ids")
+        _shape(expert_ids, (T, K), "expert_ids")
     if probs is None:
-        probs = torch.empty((T, K), dtype=torch.float32, device=logits.device)
-    _check(expert_ids, torch.int32, "expert_ids")
-    _check(probs, torch.float32, "probs")
-    _shape(expert_ids, (T, K), "expert_ids")
-    _shape(probs, (T, K), "probs")
+        probs = _empty2(T, K, torch.float32, logits)
+    else:
+        _check(probs, torch.float32, "probs")
+        _shape(probs, (T, K), "probs")
     _call("moe_router_topk", _ptr(logits), _dtype(logits), T, E, K, _scoring(scoring),
           int(renormalize), scale, _ptr(expert_ids), _ptr(probs), _ptr(dev_status), _stream())
     return expert_ids, probs
@@ -598,13 +624,14 @@ def moe_router_topk_grad(grad_probs, logits, expert_ids, *, scoring: str = "soft
     T, E = logits.shape
     K = expert_ids.shape[1]
     if grad_logits is None:
-        grad_logits = torch.empty_like(logits)
+        grad_logits = _empty2(T, E, logits.dtype, logits)
+    else:
+        _check(grad_logits, logits.dtype, "grad_logits")
+        _shape(grad_logits, (T, E), "grad_logits")
     _check(grad_probs, torch.float32, "grad_probs")
     _check(expert_ids, torch.int32, "expert_ids")
-    _check(grad_logits, logits.dtype, "grad_logits")
     _shape(grad_probs, (T, K), "grad_probs")
     _shape(expert_ids, (T, K), "expert_ids")
-    _shape(grad_logits, (T, E), "grad_logits")
     _call("moe_router_topk_grad", _ptr(grad_probs), _ptr(logits), _dtype(logits),
           _ptr(expert_ids), T, E, K, _scoring(scoring), int(renormalize), scale,
           _ptr(grad_logits), _ptr(dev_status), _stream())
@@ -625,13 +652,15 @@ def moe_quantize_rows(x, *, row_map=None, K: int = 1, N: Optional[int] = None, q
     if N is None:
         N = T * K if row_map is not None else T
     if q is None:
-        q = torch.empty((N, H), dtype=torch.int8, device=x.device)
+        q = _empty2(N, H, torch.int8, x)
+    else:
+        _check(q, torch.int8, "q")
+        _shape(q, (N, H), "q")
     if scale is None:
-        scale = torch.empty(N, dtype=torch.float32, device=x.device)
-    _check(q, torch.int8, "q")
-    _check(scale, torch.float32, "scale")
-    _shape(q, (N, H), "q")
-    _shape(scale, (N,), "scale")
+        scale = _empty1(N, torch.float32, x)
+    else:
+        _check(scale, torch.float32, "scale")
+        _shape(scale, (N,), "scale")
     _call("moe_quantize_rows", _ptr(x), _dtype(x), _ptr(row_map), T, H, K, N, _ptr(q),
           _ptr(scale), _stream())
     return q, scale
@@ -644,19 +673,23 @@ def moe_gate_up_swiglu_int8(permuted_q, row_scale, expert_offsets, W_gate_q, gat
     N, H = permuted_q.shape
     E, I, _ = W_gate_q.shape
     if act is None:
-        act = torch.empty((N, I), dtype=torch.bfloat16, device=permuted_q.device)
-    for t, n in ((permuted_q, "permuted_q"), (W_gate_q, "W_gate_q"), (W_up_q, "W_up_q")):
-        _check(t, torch.int8, n)
-    for t, n in ((row_scale, "row_scale"), (gate_scale, "gate_scale"), (up_scale, "up_scale")):
-        _check(t, torch.float32, n)
+        act = _empty2(N, I, torch.bfloat16, permuted_q)
+    i8, f32 = torch.int8, torch.float32
+    if not (permuted_q.dtype is i8 and W_gate_q.dtype is i8 and W_up_q.dtype is i8
+            and row_scale.dtype is f32 and gate_scale.dtype is f32 and up_scale.dtype is f32
+            and act.dtype is torch.bfloat16 and row_scale.shape == (N,)
+            and W_gate_q.shape == W_up_q.shape == (E, I, H)
+            and gate_scale.shape == up_scale.shape == (E, I) and act.shape == (N, I)):
+        for t, dt, shape, n in ((permuted_q, i8, (N, H), "permuted_q"),
+                                (W_gate_q, i8, (E, I, H), "W_gate_q"),
+                                (W_up_q, i8, (E, I, H), "W_up_q"),
+                                (row_scale, f32, (N,), "row_scale"),
+                                (gate_scale, f32, (E, I), "gate_scale"),
+                                (up_scale, f32, (E, I), "up_scale"),
+                                (act, torch.bfloat16, (N, I), "act")):
+            _check(t, dt, n)
+            _shape(t, shape, n)
     _check(expert_offsets, torch.int32, "expert_offsets")
-    _check(act, torch.bfloat16, "act")
-    _shape(row_scale, (N,), "row_scale")
-    _shape(W_gate_q, (E, I, H), "W_gate_q")
-    _shape(W_up_q, (E, I, H), "W_up_q")
-    _shape(gate_scale, (E, I), "gate_scale")
-    _shape(up_scale, (E, I), "up_scale")
-    _shape(act, (N, I), "act")
     _call("moe_gate_up_swiglu_int8", _ptr(permuted_q), _ptr(row_scale), _ptr(expert_offsets), N,
           H, I, E, _ptr(W_gate_q), _ptr(gate_scale), _ptr(W_up_q), _ptr(up_scale), _ptr(act),
           _ptr(dev_status), _stream())
@@ -671,16 +704,19 @@ def moe_down_proj_int8(act_q, row_scale, expert_offsets, W_down_q, down_scale, *
     N, I = act_q.shape
     E, H, _ = W_down_q.shape
     if expanded is None:
-        expanded = torch.empty((N, H), dtype=out_dtype, device=act_q.device)
-    for t, n in ((act_q, "act_q"), (W_down_q, "W_down_q")):
-        _check(t, torch.int8, n)
-    for t, n in ((row_scale, "row_scale"), (down_scale, "down_scale")):
-        _check(t, torch.float32, n)
+        expanded = _empty2(N, H, out_dtype, act_q)
+    else:
+        _shape(expanded, (N, H), "expanded")
+    i8, f32 = torch.int8, torch.float32
+    if not (act_q.dtype is i8 and W_down_q.dtype is i8 and row_scale.dtype is f32
+            and down_scale.dtype is f32 and row_scale.shape == (N,)
+            and W_down_q.shape == (E, H, I) and down_scale.shape == (E, H)):
+        for t, dt, shape, n in ((act_q, i8, (N, I), "act_q"), (W_down_q, i8, (E, H, I), "W_down_q"),
+                                (row_scale, f32, (N,), "row_scale"),
+                                (down_scale, f32, (E, H), "down_scale")):
+            _check(t, dt, n)
+            _shape(t, shape, n)
     _check(expert_offsets, torch.int32, "expert_offsets")
-    _shape(row_scale, (N,), "row_scale")
-    _shape(W_down_q, (E, H, I), "W_down_q")
-    _shape(down_scale, (E, H), "down_scale")
-    _shape(expanded, (N, H), "expanded")
     _call("moe_down_proj_int8", _ptr(act_q), _ptr(row_scale), _ptr(expert_offsets), N, H, I, E,
           _ptr(W_down_q), _ptr(down_scale), _ptr(expanded), _dtype(expanded), _ptr(dev_status),
           _stream())
@@ -706,10 +742,10 @@ def moe_layer_few_tokens(tokens, expert_ids, probs, W_gate, W_up, W_down, *, sca
     wdt = torch.bfloat16 if scales is None else torch.int8
     gs, us, ds = scales if scales is not None else (None, None, None)
     if out is None:
-        out = torch.empty((T, H), dtype=torch.bfloat16, device=tokens.device)
+        out = _empty2(T, H, torch.bfloat16, tokens)
     if workspace is None:
         ws = moe_layer_few_tokens_workspace_size(T, K, H, I, E)
-        workspace = torch.empty(max(ws, 16), dtype=torch.uint8, device=tokens.device)
+        workspace = _empty1(max(ws, 16), torch.uint8, tokens)
     bf16, f32 = torch.bfloat16, torch.float32
     if not (tokens.dtype is bf16 and out.dtype is bf16 and expert_ids.dtype is torch.int32
             and probs.dtype is f32 and W_gate.dtype is wdt and W_up.dtype is wdt

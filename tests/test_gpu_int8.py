@@ -56,6 +56,18 @@ def test_quantize_rows_not_finite_and_tiny(lib):
     assert (q[4, 0::2] == 127).all() and (q[4, 1::2] == -42).all()
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("size", [1e-40, 3e-38, 2e-37, 1e-36, 1e-30, 1e37, 3e38])
+def test_quantize_rows_of_every_magnitude(lib, dtype, size):
+    """127 / top is out of fp32's range below 2^-121."""
+    g = np.random.default_rng(5)
+    x = torch.from_numpy(np.clip(g.standard_normal((9, 400)), -1, 1) * size).to(dtype)
+    q, s = lib.moe_quantize_rows(x.to(DEV))
+    w_q, w_s = S.quantize_rows(np64(x))
+    assert np.array_equal(np64(q), w_q)
+    assert np.array_equal(s.cpu().numpy(), w_s)
+
+
 @pytest.mark.parametrize("T,H,E,K,special", [(40, 64, 8, 4, 3), (1, 2048, 16, 8, 0), (257, 208, 24, 5, 2)])
 def test_quantize_rows_into_expert_major_order(lib, T, H, E, K, special):
     g = np.random.default_rng(T)

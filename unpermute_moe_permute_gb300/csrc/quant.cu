@@ -2,17 +2,15 @@
 // row map, to the K expert-major rows of the token (each token is read and
 // rounded once).
 //
-// Bound by memory: TPR threads (32 to 256) hold a row in registers, 16
-// elements a chunk, find its largest magnitude (the bits of |x| order like
-// |x|, and a NaN's are the largest of all, so an integer maximum finds both)
-// and round it without reading it again.
+// Memory bounds it if the instructions are few: TPR threads (32 to 256) hold a
+// row in registers, 8 elements a chunk, find its largest magnitude (a NaN
+// stays one) and round it without reading it again.
 //
-// q = rint(127 x / top), the division rounded to fp32.  For bf16 rows the
-// rounding decision is that of exact arithmetic (127 x / top is a quotient of
-// a 15-bit and an 8-bit integer: a tie exactly, or further from one than the
-// division's error), so x * (127 / top) decides all but the elements within
-// 2^-15 of a tie, and for those the exact residual 127 x - q top (one fma)
-// does.  fp32 rows divide: their quotients can lie closer to a tie.
+// q = rint(127 x / top), the division rounded to fp32.  With k near 127 / top,
+// x k (1 + 2^-20) and x k (1 - 2^-20) round to the same integer unless the
+// quotient is that near to a tie; they enclose it whatever the roundings of k
+// (an approximate division, 2^-22), 127 x and the division (2^-24 each).  The
+// chunks where they differ (one in 60 of a warp) divide.
 #include <math.h>
 
 #include <type_traits>
@@ -25,14 +23,14 @@ namespace {
 constexpr int kThreads = 256;
 
 template <typename T>
-struct Chunk {  // 16 elements as loaded
-  static constexpr int n = 16 / VecTraits<T>::kElems;
+struct Chunk {  // 8 elements as loaded
+  static constexpr int n = 8 / VecTraits<T>::kElems;
   uint4 v[n];
   __device__ __forceinline__ void load(const T* p) {
 #pragma unroll
     for (int i = 0; i < n; ++i) v[i] = ld_nc_v4(p + i * VecTraits<T>::kElems);
   }
-  __device__ __forceinline__ void get(float (&f)[16]) const {
+  __device__ __forceinline__ void get(float (&f)[8]) const {
 #pragma unroll
     for (int i = 0; i < n; ++i) VecTraits<T>::unpack(v[i], f + i * VecTraits<T>::kElems);
   }
@@ -42,44 +40,66 @@ struct Chunk {  // 16 elements as loaded
 // sum's bits is the integer's low byte.
 constexpr float kMagic = 12582912.f;
 
+// Two fused multiply-adds at once.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 r;
+  asm("{\n\t.reg .b64 a, b, c, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "mov.b64 c, {%6, %7};\n\tfma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return r;
+}
+
+// The larger magnitudes of two pairs of bf16, a NaN if one is; the signs are of no meaning.
+__device__ __forceinline__ uint32_t max_abs_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.NaN.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
 struct Rounding {
-  float mul, div, k;  // q = rint(x * mul / div), k = mul / div
+  float mul, div;    // q = rint(x * mul / div)
+  float above, below;  // mul / div, a little more and a little less
 };
 
-// 16 elements in 8 bits.
-template <typename T>
-__device__ __forceinline__ uint4 round16(const Chunk<T>& c, const Rounding& r) {
-  float f[16];
-  c.get(f);
-  uint32_t b[16];
-  if constexpr (sizeof(T) == 4) {
+// Low bytes of 8 words.
+__device__ __forceinline__ uint2 low_bytes(const uint32_t (&b)[8]) {
+  uint32_t w[2];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) b[i] = __float_as_uint(__fdiv_rn(f[i] * r.mul, r.div) + kMagic);
-  } else {
-    // x k is within 128 * 2^-23 < 2^-15 of the quotient: only nearer to a tie
-    // than that can its rounding differ
-    bool near = false;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const float y = f[i] * r.k, z = y + kMagic;
-      near |= fabsf(y - (z - kMagic)) > 0.5f - 0x1p-15f;
-      b[i] = __float_as_uint(z);
-    }
-    if (near) {
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const float q = __uint_as_float(b[i]) - kMagic, e = fmaf(-q, r.div, f[i] * r.mul);  // exact
-        const float two = 2.f * fabsf(e);
-        if (two > r.div || (two == r.div && (b[i] & 1u))) b[i] += e > 0.f ? 1u : 0xffffffffu;
-      }
-    }
-  }
-  uint32_t w[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
+  for (int i = 0; i < 2; ++i)
     w[i] = __byte_perm(__byte_perm(b[4 * i], b[4 * i + 1], 0x0040),
                        __byte_perm(b[4 * i + 2], b[4 * i + 3], 0x0040), 0x5410);
-  return make_uint4(w[0], w[1], w[2], w[3]);
+  return make_uint2(w[0], w[1]);
+}
+
+template <typename T>
+__device__ __noinline__ uint2 round8_divide(Chunk<T> c, float mul, float div) {
+  float f[8];
+  c.get(f);
+  uint32_t b[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) b[i] = __float_as_uint(__fdiv_rn(f[i] * mul, div) + kMagic);
+  return low_bytes(b);
+}
+
+// 8 elements in 8 bits.
+template <typename T>
+__device__ __forceinline__ uint2 round8(const Chunk<T>& c, const Rounding& r) {
+  float f[8];
+  c.get(f);
+  uint32_t b[8], differ = 0u;
+  const float2 magic = make_float2(kMagic, kMagic);
+#pragma unroll
+  for (int i = 0; i < 8; i += 2) {
+    const float2 x = make_float2(f[i], f[i + 1]);
+    const float2 z = fma2(x, make_float2(r.above, r.above), magic);
+    const float2 y = fma2(x, make_float2(r.below, r.below), magic);
+    b[i] = __float_as_uint(z.x), b[i + 1] = __float_as_uint(z.y);
+    differ |= b[i] ^ __float_as_uint(y.x);
+    differ |= b[i + 1] ^ __float_as_uint(y.y);
+  }
+  if (differ) return round8_divide<T>(c, r.mul, r.div);
+  return low_bytes(b);
 }
 
 // TPR threads per row, NV chunks each in registers; NV = 0: rows of any
@@ -102,14 +122,8 @@ quantize_rows_kernel(const T* __restrict__ x, const int32_t* __restrict__ row_ma
       const uint32_t w[4] = {c.v[j].x, c.v[j].y, c.v[j].z, c.v[j].w};
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        if constexpr (sizeof(T) == 4) {
-          top = max(top, w[q] & 0x7fffffffu);
-        } else {
-          const uint32_t a = w[q] & 0x7fff7fffu;
-          const __nv_bfloat162 h = __hmax2_nan(*reinterpret_cast<const __nv_bfloat162*>(&a),
-                                               *reinterpret_cast<const __nv_bfloat162*>(&top));
-          top = *reinterpret_cast<const uint32_t*>(&h);
-        }
+        if constexpr (sizeof(T) == 4) top = max(top, w[q] & 0x7fffffffu);
+        else top = max_abs_bf16x2(top, w[q]);
       }
     }
   };
@@ -117,14 +131,14 @@ quantize_rows_kernel(const T* __restrict__ x, const int32_t* __restrict__ row_ma
   if constexpr (NV > 0) {
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
-      const int h = (v * TPR + i) * 16;
+      const int h = (v * TPR + i) * 8;
       if (live && h < H) c[v].load(row + h);
     }
 #pragma unroll
     for (int v = 0; v < NV; ++v)
-      if (live && (v * TPR + i) * 16 < H) widen(c[v]);
+      if (live && (v * TPR + i) * 8 < H) widen(c[v]);
   } else {
-    for (int h = i * 16; live && h < H; h += TPR * 16) {
+    for (int h = i * 8; live && h < H; h += TPR * 8) {
       c[0].load(row + h);
       widen(c[0]);
     }
@@ -135,7 +149,7 @@ quantize_rows_kernel(const T* __restrict__ x, const int32_t* __restrict__ row_ma
     dest = row_map != nullptr ? row_map[(size_t)t * K + lane] : t;
     if (dest >= N) dest = -1;
   }
-  if constexpr (sizeof(T) == 2) top = max(top & 0xffff0000u, top << 16);  // as fp32
+  if constexpr (sizeof(T) == 2) top = max(top & 0x7fff0000u, (top & 0x7fffu) << 16);  // as fp32
   top = __reduce_max_sync(0xffffffffu, top);
   if constexpr (TPR > 32) {
     if (lane == 0) part[threadIdx.x >> 5] = top;
@@ -147,28 +161,41 @@ quantize_rows_kernel(const T* __restrict__ x, const int32_t* __restrict__ row_ma
   const float m = __uint_as_float(top);
   const bool zero = !finite || top == 0u;
   // 127 x would pass the range of fp32 from 2^121 on, and 127 / top below
-  // 2^-119: such rows are scaled by a power of two, which changes no quotient
+  // 2^-119: such rows are scaled by a power of two, which changes no quotient,
+  // and divide every element (NaN and 0 differ)
   const float by = m >= 0x1p119f ? 0x1p-10f : m < 0x1p-100f ? 0x1p60f : 1.f;
   Rounding r;
   r.mul = zero ? 0.f : 127.f * by;
   r.div = zero ? 1.f : m * by;
-  r.k = r.mul / r.div;
+  const float k = __fdividef(r.mul, r.div);
+  r.above = by != 1.f && !zero ? __int_as_float(0x7fffffff) : k * (1.f + 0x1p-20f);
+  r.below = k * (1.f - 0x1p-20f);
   if (i < K && live && dest >= 0) scale[dest] = finite ? m / 127.f : __int_as_float(0x7fffffff);
-  auto put = [&](const Chunk<T>& ch, int h) {
-    const uint4 w = zero ? make_uint4(0u, 0u, 0u, 0u) : round16(ch, r);
+  // the rows of the K slots in turn, a row's chunks together
+  constexpr int kW = NV > 0 ? NV : 1;
+  uint2 w[kW];
+  auto put = [&](int h0) {
     for (int k = 0; k < K; ++k) {
       const int d = __shfl_sync(0xffffffffu, dest, k);
-      if (d >= 0 && h < H) st_v4(q + (size_t)d * H + h, w);
+      if (d < 0) continue;
+      int8_t* to = q + (size_t)d * H;
+#pragma unroll
+      for (int v = 0; v < kW; ++v) {
+        const int h = h0 + (v * TPR + i) * 8;
+        if (h < H) *reinterpret_cast<uint2*>(to + h) = w[v];
+      }
     }
   };
   if constexpr (NV > 0) {
 #pragma unroll
-    for (int v = 0; v < NV; ++v) put(c[v], (v * TPR + i) * 16);
+    for (int v = 0; v < NV; ++v) w[v] = zero ? make_uint2(0u, 0u) : round8(c[v], r);
+    put(0);
   } else {
-    for (int h0 = 0; h0 < H; h0 += TPR * 16) {
-      const int h = h0 + i * 16;
+    for (int h0 = 0; h0 < H; h0 += TPR * 8) {
+      const int h = h0 + i * 8;
       if (live && h < H) c[0].load(row + h);
-      put(c[0], h);
+      w[0] = zero ? make_uint2(0u, 0u) : round8(c[0], r);
+      put(h0);
     }
   }
 }
@@ -182,13 +209,19 @@ void launch_quantize(const T* x, const int32_t* row_map, int n_tok, int H, int K
         <<<(n_tok + R - 1) / R, kThreads, 0, s>>>(x, row_map, n_tok, H, K, N, q, scale);
   };
   using std::integral_constant;
-  // at most four chunks (32 or 64 registers) a thread
-  if (H <= 512) go(integral_constant<int, 32>{}, integral_constant<int, 1>{});
-  else if (H <= 1024) go(integral_constant<int, 32>{}, integral_constant<int, 2>{});
-  else if (H <= 2048) go(integral_constant<int, 32>{}, integral_constant<int, 4>{});
-  else if (H <= 4096) go(integral_constant<int, 64>{}, integral_constant<int, 4>{});
-  else if (H <= 8192) go(integral_constant<int, 128>{}, integral_constant<int, 4>{});
-  else if (H <= 16384) go(integral_constant<int, 256>{}, integral_constant<int, 4>{});
+  // at most four chunks a thread up to 8192 elements: twice as many chunks in
+  // half as many threads keep fewer rows in flight (16384 x 2048: 25.0 us
+  // against 30.7; 8192 x 4096: 24.8 against 31.5), half as many pay for the
+  // barrier (28.7 and 28.7)
+  if (H <= 256) go(integral_constant<int, 32>{}, integral_constant<int, 1>{});
+  else if (H <= 512) go(integral_constant<int, 32>{}, integral_constant<int, 2>{});
+  else if (H <= 768) go(integral_constant<int, 32>{}, integral_constant<int, 3>{});
+  else if (H <= 1024) go(integral_constant<int, 32>{}, integral_constant<int, 4>{});
+  else if (H <= 1536) go(integral_constant<int, 64>{}, integral_constant<int, 3>{});
+  else if (H <= 2048) go(integral_constant<int, 64>{}, integral_constant<int, 4>{});
+  else if (H <= 4096) go(integral_constant<int, 128>{}, integral_constant<int, 4>{});
+  else if (H <= 8192) go(integral_constant<int, 256>{}, integral_constant<int, 4>{});
+  else if (H <= 16384) go(integral_constant<int, 256>{}, integral_constant<int, 8>{});
   else go(integral_constant<int, 256>{}, integral_constant<int, 0>{});
 }
 

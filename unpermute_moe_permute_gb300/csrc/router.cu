@@ -56,6 +56,15 @@ __device__ __forceinline__ float warp_sum(float v) {
   return v;
 }
 
+// e^x, x <= 0, with what is below 2^-126 flushed to 0: a term of a sum that is
+// at least 1, or of a gradient.  (__expf keeps subnormals, at three more
+// instructions each.)
+__device__ __forceinline__ float exp_flush(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x * 1.4426950408889634f));
+  return r;
+}
+
 // sigmoid(l) / sigmoid(l0) for l <= l0, without overflow:
 // sigmoid(l) = e^min(l, 0) / (1 + e^-|l|).
 __device__ __forceinline__ float sigmoid_ratio(float l, float l0) {
@@ -90,46 +99,82 @@ __device__ __forceinline__ int index_of(int i, int lane) {
 }
 
 // The row's logits as the definition takes them, -inf past its end; nan: one
-// of them was a NaN.
+// of them was a NaN.  Lanes whose logits are all finite, as nearly always, skip
+// the clamps: 0 v summed is NaN as soon as one is not (two multiply-adds an
+// element, on the pipe that the selection leaves idle).
 template <typename T, int NPL, bool kVec>
 __device__ __forceinline__ void load_row(const T* row, int E, int lane, float (&v)[NPL], bool& nan) {
   constexpr int V = VecTraits<T>::kElems;
+  float check = 0.f;
   if constexpr (kVec) {
 #pragma unroll
     for (int i = 0; i < NPL; i += V) {
       const int j = index_of<T, NPL, kVec>(i, lane);
-      if (j < E) VecTraits<T>::unpack(ld_v4(row + j), v + i);
-      else
+      if (j < E) {
+        VecTraits<T>::unpack(ld_v4(row + j), v + i);
+#pragma unroll
+        for (int k = 0; k < V; ++k) check = fmaf(v[i + k], 0.f, check);
+      } else {
 #pragma unroll
         for (int k = 0; k < V; ++k) v[i + k] = -INFINITY;
+      }
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < NPL; ++i) v[i] = lane + 32 * i < E ? to_f32(row[lane + 32 * i]) : -INFINITY;
+    for (int i = 0; i < NPL; ++i) {
+      const bool in = lane + 32 * i < E;
+      v[i] = in ? to_f32(row[lane + 32 * i]) : -INFINITY;
+      check = fmaf(in ? v[i] : 0.f, 0.f, check);
+    }
+  }
+  if (check != check) {
+#pragma unroll
+    for (int i = 0; i < NPL; ++i) {
+      nan |= v[i] != v[i];
+      v[i] = fminf(fmaxf(v[i], -INFINITY), 3.402823466e+38f);  // NaN: -inf
+    }
   }
 #pragma unroll
-  for (int i = 0; i < NPL; ++i) {
-    nan |= v[i] != v[i];
-    v[i] = fminf(fmaxf(v[i], -INFINITY), 3.402823466e+38f) + 0.f;  // NaN: -inf; -0: +0
-  }
+  for (int i = 0; i < NPL; ++i) v[i] += 0.f;  // -0: +0
 }
 
-// Descending order by a merging network (Batcher's odd-even merge sort).
 template <int N>
-__device__ __forceinline__ void sort_desc(uint32_t (&a)[N]) {
+__device__ __forceinline__ void order(uint32_t (&a)[N], int i, int j) {
+  const uint32_t x = a[i], y = a[j];
+  a[i] = max(x, y);
+  a[j] = min(x, y);
+}
+
+// a[0..D) in descending order becomes the D largest of a, D a power of two:
+// each D elements by a merging network (Batcher's odd-even merge sort), then
+// group by group the larger of a[i] and b[D-1-i], a bitonic sequence of the D
+// largest of both, put in order.
+template <int D, int N>
+__device__ __forceinline__ void top_desc(uint32_t (&a)[N]) {
 #pragma unroll
-  for (int p = 1; p < N; p <<= 1)
+  for (int g = 0; g < N; g += D) {
 #pragma unroll
-    for (int k = p; k >= 1; k >>= 1)
+    for (int p = 1; p < D; p <<= 1)
 #pragma unroll
-      for (int j = k % p; j + k < N; j += 2 * k)
+      for (int k = p; k >= 1; k >>= 1)
 #pragma unroll
-        for (int i = 0; i < k; ++i)
-          if (i + j + k < N && (i + j) / (2 * p) == (i + j + k) / (2 * p)) {
-            const uint32_t x = a[i + j], y = a[i + j + k];
-            a[i + j] = max(x, y);
-            a[i + j + k] = min(x, y);
-          }
+        for (int j = k % p; j + k < D; j += 2 * k)
+#pragma unroll
+          for (int i = 0; i < k; ++i)
+            if (i + j + k < D && (i + j) / (2 * p) == (i + j + k) / (2 * p)) order(a, g + i + j, g + i + j + k);
+  }
+#pragma unroll
+  for (int w = D; w < N; w <<= 1)
+#pragma unroll
+    for (int g = 0; g < N; g += 2 * w) {
+#pragma unroll
+      for (int i = 0; i < D; ++i) a[g + i] = max(a[g + i], a[g + w + D - 1 - i]);
+#pragma unroll
+      for (int k = D / 2; k >= 1; k >>= 1)
+#pragma unroll
+        for (int i = 0; i < D; ++i)
+          if (!(i & k)) order(a, g + i, g + i + k);
+    }
 }
 
 // The selection by full keys; lane k < K gets the k-th id.
@@ -161,11 +206,15 @@ __device__ __noinline__ int select_exact(const T* row, int E, int K, int lane) {
   return sel_id;
 }
 
-template <int NPL, bool kVec, typename T>
+// D: how many of its logits a lane keeps in order.  A lane whose D all win (4
+// of the first 9: about one row in 250 when the order is random) does the row
+// again with full keys.
+template <int NPL, int D, bool kVec, typename T>
 __global__ void __launch_bounds__(kWarps * 32)
 router_topk_kernel(const T* __restrict__ logits, int n_tok, int E, int K, int scoring,
                    int renormalize, float scale, int32_t* __restrict__ expert_ids,
                    float* __restrict__ probs, int32_t* status) {
+  constexpr uint32_t kIndex = 32 * NPL - 1;  // the bits of an index
   const int lane = threadIdx.x & 31;
   const int t = blockIdx.x * kWarps + (threadIdx.x >> 5);
   if (t >= n_tok) return;
@@ -178,46 +227,45 @@ router_topk_kernel(const T* __restrict__ logits, int n_tok, int E, int K, int sc
 #pragma unroll
   for (int i = 0; i < NPL; ++i) {
     const int j = index_of<T, NPL, kVec>(i, lane);
-    pk[i] = j < E ? (key_of(v[i]) & ~1023u) | (uint32_t)(1023 - j) : 0u;
+    pk[i] = j < E ? (key_of(v[i]) & ~kIndex) | (kIndex - j) : 0u;
   }
-  float row_sum = 0.f;
-  if (scoring == MOE_SCORE_SOFTMAX && !renormalize) {
-    float m = v[0];
-#pragma unroll
-    for (int i = 1; i < NPL; ++i) m = fmaxf(m, v[i]);
-    m = value_of(__reduce_max_sync(kAll, key_of(m)));
-    if (m > -INFINITY) {
-#pragma unroll
-      for (int i = 0; i < NPL; ++i) row_sum += __expf(v[i] - m);
-      row_sum = warp_sum(row_sum);
-    }
-  }
-  sort_desc(pk);
+  top_desc<D>(pk);
+  const bool more = D < NPL && pk[D - 1] != 0u;  // the lane may hold others
   const int rounds = min(K + 1, E);
   uint32_t mine = 0u;  // lane k: the k-th of the packed logits
+#pragma unroll 3
   for (int k = 0; k < rounds; ++k) {
     const uint32_t best = __reduce_max_sync(kAll, pk[0]);
     const bool won = pk[0] == best;
 #pragma unroll
-    for (int i = 0; i + 1 < NPL; ++i) pk[i] = won ? pk[i + 1] : pk[i];
-    if (won) pk[NPL - 1] = 0u;
+    for (int i = 0; i + 1 < D; ++i) pk[i] = won ? pk[i + 1] : pk[i];
+    if (won) pk[D - 1] = 0u;
     if (lane == k) mine = best;
   }
-  int sel_id = 1023 - (int)(mine & 1023u);
+  int sel_id = (int)(kIndex - (mine & kIndex));
   const bool on = lane < rounds;
   float sel = on ? to_f32(row[sel_id]) : 0.f;
   sel = fminf(fmaxf(sel, -INFINITY), 3.402823466e+38f) + 0.f;
+  bool again = more && pk[0] == 0u;
   if constexpr (sizeof(T) == 4) {
-    // equal 22 bits of different logits, or at the edge of the selection
-    // (where further logits may share them): again, with full keys
+    // equal leading bits of different logits, or at the edge of the selection
+    // (where further logits may share them)
     const uint32_t next = __shfl_down_sync(kAll, mine, 1);
     const float next_sel = __shfl_down_sync(kAll, sel, 1);
-    const bool again = lane + 1 < rounds && (mine >> 10) == (next >> 10) &&
-                       (sel != next_sel || lane == K - 1);
-    if (__any_sync(kAll, again)) {
-      sel_id = select_exact<NPL>(row, E, K, lane);
-      sel = lane < K ? to_f32(row[sel_id]) : 0.f;
-      sel = fminf(fmaxf(sel, -INFINITY), 3.402823466e+38f) + 0.f;
+    again |= lane + 1 < rounds && ((mine ^ next) & ~kIndex) == 0u && (sel != next_sel || lane == K - 1);
+  }
+  if (__any_sync(kAll, again)) {
+    sel_id = select_exact<NPL>(row, E, K, lane);
+    sel = lane < K ? to_f32(row[sel_id]) : 0.f;
+    sel = fminf(fmaxf(sel, -INFINITY), 3.402823466e+38f) + 0.f;
+  }
+  float row_sum = 0.f;
+  if (scoring == MOE_SCORE_SOFTMAX && !renormalize) {
+    const float m = __shfl_sync(kAll, sel, 0);  // the row's largest
+    if (m > -INFINITY) {
+#pragma unroll
+      for (int i = 0; i < NPL; ++i) row_sum += exp_flush(v[i] - m);
+      row_sum = warp_sum(row_sum);
     }
   }
   const float q = selected_weight(sel, lane, K, scoring, renormalize != 0, row_sum);
@@ -274,8 +322,13 @@ router_grad_kernel(const float* __restrict__ grad_probs, const T* __restrict__ l
     }
   }
   // an id named twice collects both gradients
-  const unsigned same = __match_any_sync(kAll, lane < K ? id : -1 - lane);
-  const bool twice = __any_sync(kAll, lane < K && id >= 0 && (same & (same - 1)) != 0u);
+  bool same = false;
+  for (int d = 1; 2 * d <= K; ++d) {
+    const int other = lane + d < K ? lane + d : lane + d - K;  // lanes < K: the d-th next, in a ring
+    const int ik = __shfl_sync(kAll, id, other & 31);
+    same |= lane < K && id >= 0 && ik == id;
+  }
+  const bool twice = __any_sync(kAll, same);
   auto collect = [&](float x) {
     if (!twice) return x;
     float s = 0.f;
@@ -292,19 +345,25 @@ router_grad_kernel(const float* __restrict__ grad_probs, const T* __restrict__ l
     float m = v[0];
 #pragma unroll
     for (int i = 1; i < NPL; ++i) m = fmaxf(m, v[i]);
-    m = value_of(__reduce_max_sync(kAll, key_of(m)));
+    // (a row of -inf alone: every term and the sum are 0)
+    m = fmaxf(value_of(__reduce_max_sync(kAll, key_of(m))), -3.402823466e+38f);
     float s = 0.f;
 #pragma unroll
     for (int i = 0; i < NPL; ++i) {
-      v[i] = v[i] > -INFINITY ? __expf(v[i] - m) : 0.f;
+      v[i] = exp_flush(v[i] - m);
       s += v[i];
     }
     s = warp_sum(s);
     const float inv = s > 0.f ? 1.f / s : 0.f;
-    const float q = on ? __expf(sel - m) * inv : 0.f;
+    const float q = on ? exp_flush(sel - m) * inv : 0.f;
     const float D = warp_sum(on ? g * q : 0.f), c = inv * D;
+    if (fabsf(c) <= 3.402823466e+38f) {
 #pragma unroll
-    for (int i = 0; i < NPL; ++i) v[i] = v[i] > 0.f ? -v[i] * c : 0.f;
+      for (int i = 0; i < NPL; ++i) v[i] = fmaf(-v[i], c, 0.f);
+    } else {  // an infinite or NaN gradient leaves the masked logits' at 0
+#pragma unroll
+      for (int i = 0; i < NPL; ++i) v[i] = v[i] > 0.f ? -v[i] * c : 0.f;
+    }
     const float both = collect(g);
     d = on ? q * (both - D) : 0.f;
   } else {
@@ -382,8 +441,11 @@ extern "C" int moe_router_topk(const void* logits, int dtype, int T, int E, int 
   auto go = [&](auto* x) {
     using D = std::remove_const_t<std::remove_pointer_t<decltype(x)>>;
     by_width<D>(E, [&](auto n, auto vec) {
-      router_topk_kernel<decltype(n)::value, decltype(vec)::value, D><<<grid, kWarps * 32, 0, stream>>>(
-          x, T, E, K, scoring, renormalize, scale, expert_ids, probs, dev_status);
+      constexpr int N = decltype(n)::value;
+      auto* kernel = K <= 8 ? router_topk_kernel<N, N < 4 ? N : 4, decltype(vec)::value, D>
+                            : router_topk_kernel<N, N < 8 ? N : 8, decltype(vec)::value, D>;
+      kernel<<<grid, kWarps * 32, 0, stream>>>(x, T, E, K, scoring, renormalize, scale, expert_ids, probs,
+                                               dev_status);
     });
   };
   if (dtype == MOE_F32) go(static_cast<const float*>(logits));

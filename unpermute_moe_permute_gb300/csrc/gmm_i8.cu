@@ -99,14 +99,14 @@ struct I8Params {
 struct I8Tile {
   int e, row0, hi;  // expert, first row, end of the tile's rows
   int subs;         // accumulators the rows take: 1 or 2
-  int n;            // MMA N of each: a multiple of 32
+  int n, n1;        // MMA N of the first and of the second: multiples of 32
   int ch0;          // first channel of this CTA
-  __device__ __forceinline__ int b_rows() const { return subs * n / 2; }  // of this CTA
+  __device__ __forceinline__ int b_rows() const { return (n + n1) / 2; }  // of this CTA
 };
 
 // Tile t is channel tile (t mod ch_tiles) of row tile t / ch_tiles; the rows
 // of an expert are split evenly over its ceil(rows / (2 kSub)) row tiles, the rows
-// of a row tile evenly over its accumulators.
+// of a row tile over its accumulators in steps of 32.
 template <bool kSwiglu, int kSub>
 __device__ __forceinline__ I8Tile i8_tile(int t, const I8Params& p, const int32_t* prefix,
                                           const int32_t* offs, int rank) {
@@ -119,7 +119,9 @@ __device__ __forceinline__ I8Tile i8_tile(int t, const I8Params& p, const int32_
   x.row0 = r.lo + i * per;
   x.hi = min(r.hi, x.row0 + per);
   x.subs = per > kSub ? 2 : 1;
-  x.n = ((per + x.subs - 1) / x.subs + 31) & ~31;  // (pairs take N in steps of 32)
+  const int steps = (per + 31) >> 5;  // (pairs take N in steps of 32)
+  x.n = x.subs == 2 ? ((steps + 1) >> 1) * 32 : steps * 32;
+  x.n1 = steps * 32 - x.n;
   x.ch0 = (t - g * p.ch_tiles) * (kSwiglu ? 128 : 256) + rank * (kSwiglu ? 64 : 128);
   return x;
 }
@@ -237,9 +239,9 @@ gmm_i8_kernel(const __grid_constant__ CUtensorMap mapW0, const __grid_constant__
     bool run = true;
     for (int t = t0; run && t < total; t += dt) {
       const I8Tile x = i8_tile<kSwiglu, kSub>(t, p, prefix, offs, rank);
-      const int nh = (int)uniform(x.n) / 2, subs = (int)uniform(x.subs), e = (int)uniform(x.e);
-      const int ch0 = (int)uniform(x.ch0), r0 = (int)uniform(x.row0) + rank * nh;
-      const uint32_t tx = kA8 + (uint32_t)(subs * nh) * 128u;
+      const int nh0 = (int)uniform(x.n) / 2, nh1 = (int)uniform(x.n1) / 2, e = (int)uniform(x.e);
+      const int ch0 = (int)uniform(x.ch0), r0 = (int)uniform(x.row0);
+      const uint32_t tx = kA8 + (uint32_t)(nh0 + nh1) * 128u;
       for (int k = 0; k < stages; ++k) {
         run = mbar_wait_warp(q_empty(s), ph ^ 1u, abort_flag, p.status);
         if (!run) break;
@@ -249,12 +251,13 @@ gmm_i8_kernel(const __grid_constant__ CUtensorMap mapW0, const __grid_constant__
         tma_load_3d_warp(a, &mapW0, q_full(f), k * 128, ch0, e);
         if constexpr (kSwiglu) tma_load_3d_warp(a + kA8 / 2, &mapW1, q_full(f), k * 128, ch0, e);
         // this CTA's half of each accumulator's rows, one after the other
-        for (int j = 0; j < subs; ++j) {
+        for (int j = 0; j < 2; ++j) {
+          const int nh = j ? nh1 : nh0, rj = r0 + (j ? 2 * nh0 : 0) + rank * nh;
           int r = 0;
           for (; r + 32 <= nh; r += 32, b += 4096)
-            tma_load_2d_warp(b, &mapX32, q_full(f), k * 128, r0 + j * 2 * nh + r);
+            tma_load_2d_warp(b, &mapX32, q_full(f), k * 128, rj + r);
           if (r < nh) {
-            tma_load_2d_warp(b, &mapX16, q_full(f), k * 128, r0 + j * 2 * nh + r);
+            tma_load_2d_warp(b, &mapX16, q_full(f), k * 128, rj + r);
             b += 2048;
           }
         }
@@ -276,7 +279,7 @@ gmm_i8_kernel(const __grid_constant__ CUtensorMap mapW0, const __grid_constant__
       for (int t = t0; run && t < total; t += dt) {
         const I8Tile x = i8_tile<kSwiglu, kSub>(t, p, prefix, offs, rank);
         const int n = (int)uniform(x.n), subs = (int)uniform(x.subs);
-        const uint32_t idesc = idesc_f16_f32(256, n);
+        const uint32_t idesc = idesc_f16_f32(256, n), idesc1 = idesc_f16_f32(256, (int)uniform(x.n1));
         // accumulators it, it + 1 (mod 2), as they become free
         for (int j = 0; run && j < subs; ++j)
           run = __all_sync(0xffffffffu, mbar_wait<true>(t_empty((it + j) & 1), (((it + j) >> 1) & 1) ^ 1u,
@@ -297,7 +300,7 @@ gmm_i8_kernel(const __grid_constant__ CUtensorMap mapW0, const __grid_constant__
           for (int h = 0; h < 2; ++h) {
             const uint64_t bh = bd + h * (kB16 >> 5);
             umma_f16_ta_k64_warp<true>(d0, a + h * 32, bh, idesc, accum);
-            if (subs > 1) umma_f16_ta_k64_warp<true>(d1, a + h * 32, bh + sub1, idesc, accum);
+            if (subs > 1) umma_f16_ta_k64_warp<true>(d1, a + h * 32, bh + sub1, idesc1, accum);
             accum = 1u;
           }
           umma_commit_pair_warp(c_empty(b), 3);
@@ -403,7 +406,7 @@ gmm_i8_kernel(const __grid_constant__ CUtensorMap mapW0, const __grid_constant__
                                    : ((kSwiglu && lane >= 16) ? p.s1 : p.s0)[(size_t)x.e * p.Nout + ch];
      for (int sub = 0; sub < x.subs; ++sub, ++it) {
       const int acc = it & 1, row0 = x.row0 + sub * x.n;
-      const int rows = min(x.hi - row0, x.n);
+      const int rows = min(x.hi - row0, sub ? x.n1 : x.n);
       float rs = part * 32 + lane < rows ? p.rs[row0 + part * 32 + lane] : 0.f;
       run = mbar_wait_warp(t_full(acc), (it >> 1) & 1, abort_flag, p.status);
       if (!run) break;

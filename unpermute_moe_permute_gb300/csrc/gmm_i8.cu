@@ -162,6 +162,15 @@ __device__ __forceinline__ float2 mul2(uint32_t x, uint32_t y, float s, float t)
   return mul2(make_float2(__uint_as_float(x), __uint_as_float(y)), make_float2(s, t));
 }
 
+// x / (1 + e^-x): the approximate exponential and reciprocal in the forms that
+// flush what is below 2^-126 (half the instructions of those that keep it).
+__device__ __forceinline__ float silu(float x) {
+  float e, r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(x * -1.4426950408889634f));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
+  return x * r;
+}
+
 template <typename C, bool kSwiglu, typename O>
 __global__ void __launch_bounds__(C::kThreads, 1)
 gmm_i8_kernel(const __grid_constant__ CUtensorMap mapW0, const __grid_constant__ CUtensorMap mapW1,
@@ -416,6 +425,10 @@ gmm_i8_kernel(const __grid_constant__ CUtensorMap mapW0, const __grid_constant__
       if (!run) break;
       tc_fence_after();
       const uint32_t d = tmem + acc * kSub + ((uint32_t)(quarter * 32) << 16);
+      auto give_back = [&]() {
+        tc_fence_before();
+        mbar_arrive_cluster_warp(mapa_shared(t_empty(acc), 0));
+      };
       for (int c0 = part * 32; c0 < rows; c0 += 8 * kEpi) {
         uint32_t v[32];
         tmem_ld_32x32b_x32(d + c0, v);
@@ -423,6 +436,7 @@ gmm_i8_kernel(const __grid_constant__ CUtensorMap mapW0, const __grid_constant__
         rs = c0 + 8 * kEpi + lane < rows ? p.rs[row0 + c0 + 8 * kEpi + lane] : 0.f;
         __syncwarp();
         tmem_ld_wait();
+        if (c0 + 8 * kEpi >= rows) give_back();  // the warp's last piece is in registers
         if constexpr (sizeof(O) == 4) {
           // fp32: staging rows of 32 channels, 16 columns at a time
 #pragma unroll
@@ -456,7 +470,7 @@ gmm_i8_kernel(const __grid_constant__ CUtensorMap mapW0, const __grid_constant__
               const float2 f = mul2(mul2(v[j], v[j + 1], cs, cs), *reinterpret_cast<const float2*>(scale + j));
               const float got = __shfl_xor_sync(0xffffffffu, up ? f.x : f.y, 16);
               const float gate = up ? got : f.x, u = up ? f.y : got;
-              y[j / 2] = __fdividef(gate, 1.f + __expf(-gate)) * u;
+              y[j / 2] = silu(gate) * u;
             }
 #pragma unroll
             for (int j = 0; j < 8; ++j) w[j] = VecTraits<__nv_bfloat16>::pack2(y[2 * j], y[2 * j + 1]);
@@ -501,8 +515,7 @@ gmm_i8_kernel(const __grid_constant__ CUtensorMap mapW0, const __grid_constant__
           __syncwarp();
         }
       }
-      tc_fence_before();
-      mbar_arrive_cluster_warp(mapa_shared(t_empty(acc), 0));
+      if (part * 32 >= rows) give_back();  // (it had none)
      }
     }
   }

@@ -417,10 +417,15 @@ gmm_i8_kernel(const __grid_constant__ CUtensorMap mapW0, const __grid_constant__
      const int ch = x.ch0 + ch_l;
      const float cs = ch >= p.Nout ? 0.f
                                    : ((kSwiglu && lane >= 16) ? p.s1 : p.s0)[(size_t)x.e * p.Nout + ch];
+     // row scales of the first pieces (the second accumulator's ahead of its
+     // wait, which is short)
+     const int r_first = x.row0 + part * 32 + lane, r_second = r_first + x.n;
+     const float rs_first = part * 32 + lane < min(x.hi - x.row0, x.n) ? p.rs[r_first] : 0.f;
+     const float rs_second = x.subs > 1 && r_second < x.hi ? p.rs[r_second] : 0.f;
      for (int sub = 0; sub < x.subs; ++sub, ++it) {
       const int acc = it & 1, row0 = x.row0 + sub * x.n;
       const int rows = min(x.hi - row0, sub ? x.n1 : x.n);
-      float rs = part * 32 + lane < rows ? p.rs[row0 + part * 32 + lane] : 0.f;
+      float rs = sub ? rs_second : rs_first;
       run = mbar_wait_warp(t_full(acc), (it >> 1) & 1, abort_flag, p.status);
       if (!run) break;
       tc_fence_after();

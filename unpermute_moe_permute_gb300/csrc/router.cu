@@ -3,17 +3,20 @@
 //
 // One warp per token, the row in registers (E <= 1024: at most 32 logits a
 // lane).  Both scores grow with the logit, so no rounded score enters the
-// selection.  Memory asks for 5 us at 16384 x 256 forward and backward
-// together; what bounds the kernels is the instructions of the selection:
-//   * a logit is packed into 32 bits as the upper 22 bits of a key that orders
-//     like the float, and its index counted down: one warp-wide maximum
-//     (redux) gives the largest and, among equals, the lowest index.  bf16
-//     logits fit the 22 bits;
-//   * each lane sorts its packed logits once (a merging network of min / max
-//     pairs) and gives up its head when it wins;
-//   * for fp32 logits, rows where two of the first K + 1 share their 22 bits
-//     without being equal are done again with full keys (two reductions and a
-//     scan a round): about one row in a hundred for normal logits.
+// selection.  Memory asks for 5.2 us at 16384 x 256 fp32 forward and backward
+// together; what bounds the kernels is the instructions of the selection and
+// of the row's exponentials (issue slots 65-70 % busy; 14.8 us and 12.3 us):
+//   * a logit is packed into 32 bits as the upper bits of a key that orders
+//     like the float, and its index (5 to 10 bits) counted down: one warp-wide
+//     maximum (redux) gives the largest and, among equals, the lowest index.
+//     bf16 logits fit the 22 bits that are left at least;
+//   * each lane puts the largest 4 of its packed logits (8 for K > 8) in order
+//     (networks of min / max pairs) and gives up its head when it wins.  In
+//     order as a whole (8 of 8) the same kernel took 16.4 us;
+//   * rows where a lane has given up all of those, and for fp32 logits rows
+//     where two of the first K + 1 share their upper bits without being equal,
+//     are done again with full keys (two reductions and a scan a round): under
+//     one row in a hundred for normal logits.
 #include <math.h>
 
 #include <type_traits>

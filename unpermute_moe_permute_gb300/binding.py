@@ -130,7 +130,7 @@ def load_library(path: Optional[str] = None):
 def _call(name: str, *args):
     lib = _lib or load_library()
     rc = getattr(lib, name)(*args)
-    if rc != MOE_OK:
+    if rc:
         raise MoeError(name, rc, lib.moe_status_string(rc).decode())
 
 
@@ -173,11 +173,11 @@ def _empty2(n: int, m: int, dtype, like: torch.Tensor) -> torch.Tensor:
 def _ptr(t: Optional[torch.Tensor]):
     if t is None:
         return None
+    if t.is_cuda and t.is_contiguous():
+        return t.data_ptr()
     if not t.is_cuda:
         raise ValueError("tensor must be on a CUDA device (no CPU path)")
-    if not t.is_contiguous():
-        raise ValueError("tensor must be contiguous")
-    return t.data_ptr()
+    raise ValueError("tensor must be contiguous")
 
 
 def _dtype(t: torch.Tensor) -> int:

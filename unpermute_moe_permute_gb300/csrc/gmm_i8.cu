@@ -608,9 +608,10 @@ int launch_i8(const int8_t* A, const float* rs, const int8_t* B0, const float* s
   const uint32_t bw[3] = {128, kSwiglu ? 64u : 128u, 1};
   const uint64_t dx[2] = {(uint64_t)Kd, (uint64_t)N};
   const uint32_t b32[2] = {128, 32}, b16[2] = {128, 16};
-  if (!make_map_sw128(&w0, B0, 1, 3, dw, bw) || !make_map_sw128(&w1, B1 ? B1 : B0, 1, 3, dw, bw) ||
+  if (!make_map_sw128(&w0, B0, 1, 3, dw, bw) || (kSwiglu && !make_map_sw128(&w1, B1, 1, 3, dw, bw)) ||
       !make_map_sw128(&x32, A, 1, 2, dx, b32) || !make_map_sw128(&x16, A, 1, 2, dx, b16))
     return MOE_ERR_CUDA;
+  if (!kSwiglu) w1 = w0;
   const int per = kSwiglu ? 128 : 256;
   const I8Params p{off, rs, s0, s1, out, status, N, E, Kd, Nout, (Nout + per - 1) / per};
   return (long long)N <= kFewRows * E ? launch_cfg<I8Few, kSwiglu, O>(w0, w1, x32, x16, p, s)

@@ -68,6 +68,24 @@ def test_quantize_rows_of_every_magnitude(lib, dtype, size):
     assert np.array_equal(s.cpu().numpy(), w_s)
 
 
+def test_quantize_rows_every_bf16_quotient(lib):
+    """Every mantissa of a row's largest magnitude against every bf16 value of the
+    nine binades below it, both signs: all the quotients there are."""
+    m = np.arange(128, 256, dtype=np.float64)
+    low = (m[None, :] * 2.0 ** -np.arange(1, 10)[:, None]).reshape(-1)
+    rows = []
+    for M in range(128, 256):
+        r = np.concatenate([[M], np.minimum(m, M), low, -np.minimum(m, M), -low])
+        rows.append(np.pad(r, (0, -len(r) % 16)))
+    x = torch.from_numpy(np.stack(rows)).bfloat16()
+    assert np.array_equal(np64(x), np.stack(rows))
+    for scale in (1.0, 2.0 ** -9, 2.0 ** 100):
+        q, s = lib.moe_quantize_rows((x * scale).to(DEV))
+        exact = 127 * np64(x) / np64(x).max(1, keepdims=True)      # ties are exact in float64
+        assert np.array_equal(np64(q), np.rint(exact))
+        assert np.array_equal(np64(q), S.quantize_rows(np64(x * scale))[0])
+
+
 @pytest.mark.parametrize("T,H,E,K,special", [(40, 64, 8, 4, 3), (1, 2048, 16, 8, 0), (257, 208, 24, 5, 2)])
 def test_quantize_rows_into_expert_major_order(lib, T, H, E, K, special):
     g = np.random.default_rng(T)

@@ -4,16 +4,23 @@
 //
 // Memory bounds it if the instructions are few: TPR threads (32 to 256) hold a
 // row in registers, 8 elements a chunk, find its largest magnitude (a NaN
-// stays one) and round it without reading it again.  32768 x 768 18.7 us (75 MB:
-// 11 us at the copy rate), 8192 x 4096 24.8 us (100 MB: 15), 4096 x 2048 to 8
-// rows each 20.6 us (84 MB: 12); issue slots are 65 % busy in the first two, the
-// third waits for its stores.
+// stays one) and round it without reading it again.  32768 x 768 18 us (75 MB:
+// 11 us at the copy rate), 8192 x 4096 20.6 us (100 MB: 15), 4096 x 2048 to 8
+// rows each 19.4 us (84 MB: 12, the stores).  Deciding near ties by a second
+// product and a division took 24.6 us at 8192 x 4096: x = top / 2 is a tie and
+// so common a value that a third of the warps' chunks divided.
 //
-// q = rint(127 x / top), the division rounded to fp32.  With k near 127 / top,
-// x k (1 + 2^-20) and x k (1 - 2^-20) round to the same integer unless the
-// quotient is that near to a tie; they enclose it whatever the roundings of k
-// (an approximate division, 2^-22), 127 x and the division (2^-24 each).  The
-// chunks where they differ (one in 60 of a warp) divide.
+// q = rint(127 x / top), the division rounded to fp32.
+//
+// bf16: a quotient 127 x / top = 127 m / (M 2^j), m and M of 8 bits, is a tie or
+// at least 2^-16 of itself away from one.  So with k = 127 / top to 2^-21 of
+// itself and never below, x k rounds as the quotient does, and a tie upwards.
+// The ties are 127 / 2 (x = top / 2, a common value: to 64, upwards), and any
+// n + 1/2 when 127 divides M, M = 254: there k is a power of two and exact.
+//
+// fp32: x k (1 + 2^-20) and x k (1 - 2^-20) enclose the quotient whatever the
+// roundings of k (2^-22), 127 x and the division (2^-24 each); the chunks where
+// they round to different integers (one in 60 of a warp) divide.
 #include <math.h>
 
 #include <type_traits>
@@ -61,8 +68,9 @@ __device__ __forceinline__ uint32_t max_abs_bf16x2(uint32_t a, uint32_t b) {
 }
 
 struct Rounding {
-  float mul, div;    // q = rint(x * mul / div)
+  float mul, div;      // q = rint(x * mul / div)
   float above, below;  // mul / div, a little more and a little less
+  bool divide;         // that is out of range: every element is divided
 };
 
 // Low bytes of 8 words.
@@ -96,12 +104,14 @@ __device__ __forceinline__ uint2 round8(const Chunk<T>& c, const Rounding& r) {
   for (int i = 0; i < 8; i += 2) {
     const float2 x = make_float2(f[i], f[i + 1]);
     const float2 z = fma2(x, make_float2(r.above, r.above), magic);
-    const float2 y = fma2(x, make_float2(r.below, r.below), magic);
     b[i] = __float_as_uint(z.x), b[i + 1] = __float_as_uint(z.y);
-    differ |= b[i] ^ __float_as_uint(y.x);
-    differ |= b[i + 1] ^ __float_as_uint(y.y);
+    if constexpr (sizeof(T) == 4) {
+      const float2 y = fma2(x, make_float2(r.below, r.below), magic);
+      differ |= b[i] ^ __float_as_uint(y.x);
+      differ |= b[i + 1] ^ __float_as_uint(y.y);
+    }
   }
-  if (differ) return round8_divide<T>(c, r.mul, r.div);
+  if (differ || r.divide) return round8_divide<T>(c, r.mul, r.div);
   return low_bytes(b);
 }
 
@@ -164,15 +174,19 @@ quantize_rows_kernel(const T* __restrict__ x, const int32_t* __restrict__ row_ma
   const float m = __uint_as_float(top);
   const bool zero = !finite || top == 0u;
   // 127 x would pass the range of fp32 from 2^121 on, and 127 / top below
-  // 2^-119: such rows are scaled by a power of two, which changes no quotient,
-  // and divide every element (NaN and 0 differ)
+  // 2^-119: such rows are scaled by a power of two, which changes no quotient
   const float by = m >= 0x1p119f ? 0x1p-10f : m < 0x1p-100f ? 0x1p60f : 1.f;
   Rounding r;
   r.mul = zero ? 0.f : 127.f * by;
   r.div = zero ? 1.f : m * by;
+  r.divide = !zero && by != 1.f;
   const float k = __fdividef(r.mul, r.div);
-  r.above = by != 1.f && !zero ? __int_as_float(0x7fffffff) : k * (1.f + 0x1p-20f);
-  r.below = k * (1.f - 0x1p-20f);
+  if constexpr (sizeof(T) == 4) {
+    r.above = k * (1.f + 0x1p-20f), r.below = k * (1.f - 0x1p-20f);
+  } else {
+    r.above = k * (1.f + 0x1p-21f);
+    if ((top & 0x7f0000u) == 0x7e0000u) r.above = __fdiv_rn(r.mul, r.div);  // M = 254
+  }
   if (i < K && live && dest >= 0) scale[dest] = finite ? m / 127.f : __int_as_float(0x7fffffff);
   // the rows of the K slots in turn, a row's chunks together
   constexpr int kW = NV > 0 ? NV : 1;
@@ -212,10 +226,9 @@ void launch_quantize(const T* x, const int32_t* row_map, int n_tok, int H, int K
         <<<(n_tok + R - 1) / R, kThreads, 0, s>>>(x, row_map, n_tok, H, K, N, q, scale);
   };
   using std::integral_constant;
-  // at most four chunks a thread up to 8192 elements: twice as many chunks in
-  // half as many threads keep fewer rows in flight (16384 x 2048: 25.0 us
-  // against 30.7; 8192 x 4096: 24.8 against 31.5), half as many pay for the
-  // barrier (28.7 and 28.7)
+  // at most four chunks a thread up to 8192 elements: eight in half as many
+  // threads took 22.6 us against 20.9 at 16384 x 2048 (8192 x 4096: 21.2 and
+  // 21.4), two in twice as many 24.5 (and 23.0)
   if (H <= 256) go(integral_constant<int, 32>{}, integral_constant<int, 1>{});
   else if (H <= 512) go(integral_constant<int, 32>{}, integral_constant<int, 2>{});
   else if (H <= 768) go(integral_constant<int, 32>{}, integral_constant<int, 3>{});

@@ -238,6 +238,9 @@ gmm_i8_kernel(const __grid_constant__ CUtensorMap mapW0, const __grid_constant__
     tmem_alloc_pair(smem_u32(holder), 512);
     tmem_relinquish_pair();
   }
+  // From here on what earlier kernels of the stream wrote is read: the part
+  // above may overlap the end of the one before (as the rows' rounding lets it).
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   stage_offsets(p.off, p.E, p.N, offs, scratch);
   build_tile_prefix(offs, p.E, p.N, C::kRowTile, prefix, scratch);  // ends with __syncthreads
   const int total = prefix[p.E] * p.ch_tiles;
@@ -561,7 +564,7 @@ int launch_cfg(const CUtensorMap& w0, const CUtensorMap& w1, const CUtensorMap& 
   });
   if (attr != cudaSuccess) return MOE_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute at[1];
+  cudaLaunchAttribute at[2];
   at[0].id = cudaLaunchAttributeClusterDimension;
   at[0].val.clusterDim.x = 2;
   at[0].val.clusterDim.y = 1;
@@ -571,8 +574,10 @@ int launch_cfg(const CUtensorMap& w0, const CUtensorMap& w1, const CUtensorMap& 
   cfg.blockDim = dim3(C::kThreads, 1, 1);
   cfg.dynamicSmemBytes = C::kSmem;
   cfg.stream = s;
+  at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 2;
   static int resident = -1;
   if (resident < 0) {
     int n = 0;

@@ -13,8 +13,8 @@
 // q = rint(127 x / top), the division rounded to fp32.
 //
 // bf16: a quotient 127 x / top = 127 m / (M 2^j), m and M of 8 bits, is a tie or
-// at least 2^-16 of itself away from one.  So with k = 127 / top to 2^-21 of
-// itself and never below, x k rounds as the quotient does, and a tie upwards.
+// at least 2^-16 of itself away from one.  So with k above 127 / top by 2^-20 of
+// itself at most, x k rounds as the quotient does, and a tie upwards.
 // The ties are 127 / 2 (x = top / 2, a common value: to 64, upwards), and any
 // n + 1/2 when 127 divides M, M = 254: there k is a power of two and exact.
 //
@@ -122,6 +122,9 @@ __global__ void __launch_bounds__(kThreads)
 quantize_rows_kernel(const T* __restrict__ x, const int32_t* __restrict__ row_map, int n_tok,
                      int H, int K, int N, int8_t* __restrict__ q, float* __restrict__ scale) {
   __shared__ uint32_t part[kThreads / 32];
+  // The next kernel's CTAs may be set up once all of this grid's have begun (a
+  // kernel that asks for it waits for this one's end before it reads).
+  asm volatile("griddepcontrol.launch_dependents;");
   const int t = blockIdx.x * (kThreads / TPR) + threadIdx.x / TPR;
   const int i = threadIdx.x % TPR, lane = threadIdx.x & 31;
   const bool live = t < n_tok;

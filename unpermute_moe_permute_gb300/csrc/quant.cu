@@ -122,8 +122,10 @@ __global__ void __launch_bounds__(kThreads)
 quantize_rows_kernel(const T* __restrict__ x, const int32_t* __restrict__ row_map, int n_tok,
                      int H, int K, int N, int8_t* __restrict__ q, float* __restrict__ scale) {
   __shared__ uint32_t part[kThreads / 32];
-  // The next kernel's CTAs may be set up once all of this grid's have begun (a
-  // kernel that asks for it waits for this one's end before it reads).
+  // The launch overlaps the end of the kernel before, and the next kernel's CTAs
+  // may be set up once all of this grid's have come here (one that asks for it
+  // waits for this one's end before it reads).
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;");
   const int t = blockIdx.x * (kThreads / TPR) + threadIdx.x / TPR;
   const int i = threadIdx.x % TPR, lane = threadIdx.x & 31;
@@ -225,8 +227,17 @@ void launch_quantize(const T* x, const int32_t* row_map, int n_tok, int H, int K
                      float* scale, cudaStream_t s) {
   auto go = [&](auto tpr, auto nv) {
     constexpr int R = kThreads / decltype(tpr)::value;
-    quantize_rows_kernel<T, decltype(tpr)::value, decltype(nv)::value>
-        <<<(n_tok + R - 1) / R, kThreads, 0, s>>>(x, row_map, n_tok, H, K, N, q, scale);
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = dim3((n_tok + R - 1) / R);
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = s;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    (void)cudaLaunchKernelEx(&cfg, quantize_rows_kernel<T, decltype(tpr)::value, decltype(nv)::value>, x,
+                             row_map, n_tok, H, K, N, q, scale);
   };
   using std::integral_constant;
   // at most four chunks a thread up to 8192 elements: eight in half as many

@@ -93,6 +93,13 @@ __device__ __forceinline__ float selected_weight(float sel, int lane, int K, int
   return on ? w / s : 0.f;
 }
 
+// The launch overlaps the end of the kernel before, and the next one's may
+// overlap the end of this.
+__device__ __forceinline__ void begin_dependent() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;");
+}
+
 // Element i of a lane: 16-byte vectors when kVec (16-byte rows, and a lane
 // holds whole vectors), else every 32nd.
 template <typename T, int NPL, bool kVec>
@@ -220,6 +227,7 @@ router_topk_kernel(const T* __restrict__ logits, int n_tok, int E, int K, int sc
   constexpr uint32_t kIndex = 32 * NPL - 1;  // the bits of an index
   const int lane = threadIdx.x & 31;
   const int t = blockIdx.x * kWarps + (threadIdx.x >> 5);
+  begin_dependent();
   if (t >= n_tok) return;
   const T* row = logits + (size_t)t * E;
   float v[NPL];
@@ -302,6 +310,7 @@ router_grad_kernel(const float* __restrict__ grad_probs, const T* __restrict__ l
                    int renormalize, float scale, T* __restrict__ grad_logits, int32_t* status) {
   const int lane = threadIdx.x & 31;
   const int t = blockIdx.x * kWarps + (threadIdx.x >> 5);
+  begin_dependent();
   if (t >= n_tok) return;
   const T* row = logits + (size_t)t * E;
   T* drow = grad_logits + (size_t)t * E;
@@ -398,6 +407,20 @@ router_grad_kernel(const float* __restrict__ grad_probs, const T* __restrict__ l
   if (lane < K && id >= 0) put(drow + id, d);
 }
 
+template <typename F, typename... A>
+void launch_pdl(F* kernel, int grid, cudaStream_t stream, A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(kWarps * 32);
+  cfg.stream = stream;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  (void)cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 int check_router(const void* logits, int dtype, int T, int E, int K, int scoring) {
   if (T < 0 || E <= 0 || K <= 0) return MOE_ERR_INVALID_ARG;
   if (dtype != MOE_F32 && dtype != MOE_BF16) return MOE_ERR_INVALID_ARG;
@@ -447,8 +470,7 @@ extern "C" int moe_router_topk(const void* logits, int dtype, int T, int E, int 
       constexpr int N = decltype(n)::value;
       auto* kernel = K <= 8 ? router_topk_kernel<N, N < 4 ? N : 4, decltype(vec)::value, D>
                             : router_topk_kernel<N, N < 8 ? N : 8, decltype(vec)::value, D>;
-      kernel<<<grid, kWarps * 32, 0, stream>>>(x, T, E, K, scoring, renormalize, scale, expert_ids, probs,
-                                               dev_status);
+      launch_pdl(kernel, grid, stream, x, T, E, K, scoring, renormalize, scale, expert_ids, probs, dev_status);
     });
   };
   if (dtype == MOE_F32) go(static_cast<const float*>(logits));
@@ -471,8 +493,8 @@ extern "C" int moe_router_topk_grad(const float* grad_probs, const void* logits,
   auto go = [&](auto* x, auto* d) {
     using D = std::remove_pointer_t<decltype(d)>;
     by_width<D>(E, [&](auto n, auto vec) {
-      router_grad_kernel<decltype(n)::value, decltype(vec)::value, D><<<grid, kWarps * 32, 0, stream>>>(
-          grad_probs, x, expert_ids, T, E, K, scoring, renormalize, scale, d, dev_status);
+      launch_pdl(router_grad_kernel<decltype(n)::value, decltype(vec)::value, D>, grid, stream, grad_probs, x,
+                 expert_ids, T, E, K, scoring, renormalize, scale, d, dev_status);
     });
   };
   if (dtype == MOE_F32) go(static_cast<const float*>(logits), static_cast<float*>(grad_logits));

@@ -598,10 +598,11 @@ int launch_cfg(const CUtensorMap& w0, const CUtensorMap& w1, const CUtensorMap& 
 // Rows per expert, on average, up to which the few-rows form runs (the routing
 // itself is not known on the host).  GB300, E=64 H=2048, us, few / many:
 //   rows  I=512 gate/up    down        I=768 gate/up    down
-//     25  42.6 / 49.2   28.7 / 32.8    55.4 / 65.5   34.8 / 41.0
-//     48  45.1 / 49.9   32.8 / 32.9    61.4 / 65.5   36.9 / 41.2
-//     64  49.2 / 53.2   38.9 / 34.8    77.8 / 69.2   49.2 / 43.3
-constexpr long long kFewRows = 48;
+//     25  42.0 / 49.4   28.7 / 33.0    53.9 / 66.3   33.8 / 41.0
+//     48  43.4 / 50.1   32.3 / 33.7    57.3 / 67.6   36.9 / 41.0
+//     64  45.1 / 53.5   37.1 / 35.6    67.6 / 69.9   45.1 / 43.0
+//     80  57.3 / 53.5   45.6 / 36.9    75.8 / 71.7   51.2 / 43.7
+constexpr long long few_rows(bool swiglu) { return swiglu ? 64 : 48; }
 
 template <bool kSwiglu, typename O>
 int launch_i8(const int8_t* A, const float* rs, const int8_t* B0, const float* s0, const int8_t* B1,
@@ -619,8 +620,9 @@ int launch_i8(const int8_t* A, const float* rs, const int8_t* B0, const float* s
   if (!kSwiglu) w1 = w0;
   const int per = kSwiglu ? 128 : 256;
   const I8Params p{off, rs, s0, s1, out, status, N, E, Kd, Nout, (Nout + per - 1) / per};
-  return (long long)N <= kFewRows * E ? launch_cfg<I8Few, kSwiglu, O>(w0, w1, x32, x16, p, s)
-                                      : launch_cfg<I8Many, kSwiglu, O>(w0, w1, x32, x16, p, s);
+  return (long long)N <= few_rows(kSwiglu) * E
+             ? launch_cfg<I8Few, kSwiglu, O>(w0, w1, x32, x16, p, s)
+             : launch_cfg<I8Many, kSwiglu, O>(w0, w1, x32, x16, p, s);
 }
 
 }  // namespace

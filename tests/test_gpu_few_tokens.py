@@ -177,3 +177,61 @@ def test_few_tokens_matches_the_prompt_path(lib):
     _, y, _ = lib.moe_expert_mlp(r.permuted, r.expert_offsets, d["W_gate"], d["W_up"], d["W_down"])
     ref = lib.moe_combine(y, r.row_map, d["expert_ids"], d["probs"], 24, shared_x=d["shared_x"])
     assert float((out.float() - ref.float()).abs().max()) <= 1e-2 * float(ref.float().abs().max())
+
+
+@pytest.mark.parametrize("weights", ["bf16", "int8"])
+def test_few_tokens_leave_no_flags_behind(lib, weights):
+    """Whatever a call sets to show that its counters are clear, it takes back:
+    the flags (64 bits a CTA, after the epoch's word) end as zeros, and the epoch
+    has moved on."""
+    d = _dev(_data(11, 20, 256, 16, 4, 128, weights))
+    n = lib.moe_layer_few_tokens_workspace_size(20, 4, 256, 128, 16)
+    for fill in (0, 255):
+        ws = torch.full((n,), fill, dtype=torch.uint8, device=DEV)
+        before = int(ws[:8].view(torch.int64))
+        for call in range(1, 4):
+            lib.moe_layer_few_tokens(**d, workspace=ws)
+            words = ws[:8 * 161].view(torch.int64)
+            ctas = torch.cuda.get_device_properties(0).multi_processor_count
+            assert int(words[0]) == before + call and (words[1:1 + min(ctas, 160)] == 0).all()
+
+
+@pytest.mark.parametrize("weights", ["bf16", "int8"])
+@pytest.mark.parametrize("T", [1, 31])
+def test_few_tokens_with_the_workspace_words_written_back(lib, T, weights):
+    """A small tensor that takes the workspace's memory between two calls writes
+    its first bytes (here: back to what they were) and leaves the rest."""
+    a, b = (_dev(_data(s, T, 512, 40, 6, 256, weights)) for s in (12, 13))
+    want = [lib.moe_layer_few_tokens(**d) for d in (a, b)]
+    ws = torch.zeros(lib.moe_layer_few_tokens_workspace_size(T, 6, 512, 256, 40), dtype=torch.uint8, device=DEV)
+    st = lib.new_status()
+    differ = torch.zeros((), dtype=torch.int64, device=DEV)
+    for n in (4, 8, 64, 128):
+        first = ws[:n].clone()
+        for i in range(100):
+            ws[:n].copy_(first)
+            out = lib.moe_layer_few_tokens(**(a, b)[i % 2], workspace=ws, dev_status=st)
+            differ += (out != want[i % 2]).sum()
+    assert int(differ) == 0 and int(st) == 0
+
+
+@pytest.mark.parametrize("weights", ["bf16", "int8"])
+def test_few_tokens_in_a_graph_beside_a_small_tensor(lib, weights):
+    """The same inside a graph, whose addresses repeat with every replay."""
+    d = _dev(_data(14, 5, 512, 40, 6, 256, weights))
+    other = _dev(_data(15, 5, 512, 40, 6, 256, weights))
+    inputs = [{k: v[k].clone() for k in ("tokens", "expert_ids", "probs")} for v in (d, other)]
+    want = [lib.moe_layer_few_tokens(**dict(d, **i)) for i in inputs]
+    ws = torch.zeros(lib.moe_layer_few_tokens_workspace_size(5, 6, 512, 256, 40), dtype=torch.uint8, device=DEV)
+    st = lib.new_status()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        ws[:8].zero_()
+        out = lib._m.moe_layer_few_tokens(**d, workspace=ws, dev_status=st)
+    differ = torch.zeros((), dtype=torch.int64, device=DEV)
+    for i in range(50):
+        for k, v in inputs[i % 2].items():
+            d[k].copy_(v)
+        graph.replay()
+        differ += (out != want[i % 2]).sum()
+    assert int(differ) == 0 and int(st) == 0

@@ -30,11 +30,16 @@
 // CTAs wait for one another, so the launch is cooperative (all of it
 // resident); every wait is bounded.  The counters are zeroed by the kernel
 // itself: each CTA clears its share and then sets its flag to a tag made from
-// the workspace's epoch word; a CTA counts only after it has seen all flags,
-// and CTA 0 then opens the next epoch.  So nothing has to be cleared, neither
-// before the first call nor between the replays of a graph.  (Counters that
-// carried the tag themselves, changed by compare-and-swap, need no flags, but
-// 152 CTAs retrying on one word cost 75 us.)
+// the workspace's epoch word; a CTA counts only after it has seen all flags.
+// The last CTA to have seen them zeroes the flags and opens the next epoch, so
+// a call leaves no tag behind: whatever else uses the workspace's memory
+// between two calls, and whichever words of it that changes, the next call
+// finds flags that match its tag only when its own CTAs set them.  Nothing has
+// to be cleared, neither before the first call nor between the replays of a
+// graph.  (Flags left in place would match as soon as something wrote the epoch
+// word back, a small tensor in the same memory for one.  Counters that carried
+// the tag themselves, changed by compare-and-swap, need no flags, but 152 CTAs
+// retrying on one word cost 75 us.)
 #include <math.h>
 
 #include <mutex>
@@ -61,7 +66,7 @@ struct FewParams {
   __nv_bfloat16* act;          // [A, T, I]
   float *part1, *part2;        // [CTA][2][T][2][128], [CTA][2][T][256]
   unsigned long long* epoch;   // epoch, flag of each CTA
-  uint32_t* count;             // ready[A], tiles of phase 1, tiles of phase 2
+  uint32_t* count;             // ready[A], tiles of phase 1, tiles of phase 2, seen
   int32_t* status;
   int mask_dims, T, H, K, I, E, E_all, A_max;
 };
@@ -260,7 +265,7 @@ few_tokens_kernel(const __grid_constant__ CUtensorMap mapG, const __grid_constan
   }
   // this CTA's share of the counters, then its flag
   const unsigned long long epoch = *p.epoch, tag = tag_of(epoch);
-  const int n_count = p.A_max + p.A_max * ((p.I + 127) / 128) + (p.H + 255) / 256;
+  const int n_count = p.A_max + p.A_max * ((p.I + 127) / 128) + (p.H + 255) / 256 + 1;
   for (int i = cta * TR::threads + threadIdx.x; i < n_count; i += G * TR::threads) p.count[i] = 0u;
   // the slots' experts, and the experts that some slot chose, in order
   if (threadIdx.x < 32) bitmap[threadIdx.x] = 0u;
@@ -327,10 +332,12 @@ few_tokens_kernel(const __grid_constant__ CUtensorMap mapG, const __grid_constan
   uint32_t* ready = p.count;
   uint32_t* cnt1 = ready + p.A_max;
   uint32_t* cnt2 = cnt1 + (size_t)p.A_max * wide1;
+  uint32_t* seen = p.count + n_count - 1;
   unsigned long long* flags = p.epoch + 1;
 
   // One warp waits until every CTA's counters are clear (and every CTA has read
-  // the epoch), while the first weights are under way.
+  // the epoch), while the first weights are under way.  Then it counts itself
+  // among those that need the flags no more.
   if (warp == 11) {
     const bool ok = poll_warp([&]() {
       unsigned long long w[(kMaxCtas + 31) / 32];
@@ -343,8 +350,14 @@ few_tokens_kernel(const __grid_constant__ CUtensorMap mapG, const __grid_constan
       return all;
     }, abort_flag, p.status);
     if (ok) {
-      if (cta == 0 && lane == 0) *p.epoch = epoch + 1;
       mbar_arrive_warp(clear);
+      const uint32_t before = uniform(lane == 0 ? add_acq_rel(seen) : 0u);
+      if (before == (uint32_t)G - 1) {
+        for (int i = lane; i < G; i += 32) flags[i] = 0ull;
+        if (lane == 0) *p.epoch = epoch + 1;
+      }
+    } else if (lane == 0) {  // (flags of a call that ran out stay, under an epoch that is over)
+      *p.epoch = epoch + 1;
     }
   }
 
@@ -790,7 +803,7 @@ FewLayout few_layout(int T, int K, int H, int I, int E) {
   auto up = [](size_t v) { return (v + 255) & ~(size_t)255; };
   FewLayout l;
   l.words = up(8 * (1 + kMaxCtas));
-  l.counts = up(4 * (A + A * ((I + 127) / 128) + (H + 255) / 256));
+  l.counts = up(4 * (A + A * ((I + 127) / 128) + (H + 255) / 256 + 1));
   l.part1 = (size_t)kMaxCtas * 2 * T * 256 * 4;
   l.part2 = (size_t)kMaxCtas * 2 * T * 256 * 4;
   l.act = up(A * T * I * 2);

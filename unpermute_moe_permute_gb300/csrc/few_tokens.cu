@@ -82,8 +82,9 @@ struct FewTraits {
   static constexpr int bars = 2 * stages + 4 + 4 + 2;
   static constexpr uint32_t ctrl = stages * stage;
   static constexpr uint32_t holder = ctrl + 8 * bars;     // tensor memory, abort, flag, A
-  static constexpr uint32_t bitmap = holder + 16;          // 32 words, then 32 prefixes
-  static constexpr uint32_t list = bitmap + 256;           // active experts
+  static constexpr uint32_t bitmap = holder + 16;          // 32 words
+  static constexpr uint32_t issued = bitmap + 128;        // stages filled by warps 0 and 10
+  static constexpr uint32_t list = issued + 16;            // active experts
   static constexpr uint32_t slot = list + 2 * kMaxSlots;   // expert of each slot
   static constexpr uint32_t prob = slot + 2 * kMaxSlots;
   static constexpr uint32_t cross = prob + 4 * kMaxSlots;  // up values of a narrow tile [16][64]
@@ -231,6 +232,7 @@ few_tokens_kernel(const __grid_constant__ CUtensorMap mapG, const __grid_constan
   int16_t* slot = reinterpret_cast<int16_t*>(g + TR::slot);
   float* prob = reinterpret_cast<float*>(g + TR::prob);
   float* cross = reinterpret_cast<float*>(g + TR::cross);
+  int* issued = reinterpret_cast<int*>(g + TR::issued);
   const int warp = (int)uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
   const int TK = p.T * p.K, G = (int)gridDim.x, cta = (int)blockIdx.x;
 
@@ -366,6 +368,19 @@ few_tokens_kernel(const __grid_constant__ CUtensorMap mapG, const __grid_constan
       p.out[i] = p.shared_x ? p.shared_x[i] : __float2bfloat16_rn(0.f);
   }
 
+  // The end of the two loading warps (w: 0 weights, 1 tokens; n stages filled):
+  // every copy has landed before the CTA may exit.  When a wait ran out they
+  // may have stopped at different stages; each arrives for those that only the
+  // other filled, so that their barriers complete.
+  auto drain_ring = [&](int w, int n) {
+    if (lane == 0) issued[w] = n;
+    asm volatile("bar.sync 2, 64;" ::: "memory");
+    const int other = issued[w ^ 1], all = max(n, other);
+    for (int i = n; i < other; ++i) mbar_arrive_warp(full(i % S));
+    for (int i = max(0, all - S); i < all; ++i)
+      mbar_wait_warp(full(i % S), (uint32_t)(i / S) & 1u, abort_flag, p.status, false);
+  };
+
   if (warp == 0) {
     // ---------------- weights: the whole warp, one lane elected for each copy ----------------
     int s = 0, n = 0;
@@ -412,16 +427,16 @@ few_tokens_kernel(const __grid_constant__ CUtensorMap mapG, const __grid_constan
       }
       u += len;
     }
-    // every copy has landed before the CTA may exit
-    for (int st = 0; st < S && st < n; ++st) {
-      const int last = st + (n - 1 - st) / S * S;
-      mbar_wait_warp(full(st), (uint32_t)(last / S) & 1u, abort_flag, p.status, false);
-    }
+    drain_ring(0, n);
   } else if (warp == 10) {
     // ---------------- tokens, activations ----------------
-    int s = 0;
+    int s = 0, n = 0;
     uint32_t ph = 0;
     bool run = true;
+    auto next = [&]() {
+      ++n;
+      if (++s == S) s = 0, ph ^= 1u;
+    };
     for (int i = 0; run && i < seg1.count; ++i) {
      int tile, u, len;
      seg1.get(i, tile, u, len);
@@ -432,7 +447,7 @@ few_tokens_kernel(const __grid_constant__ CUtensorMap mapG, const __grid_constan
       mbar_arrive_expect_tx_warp(full(s), both ? 2 * TR::b_box : TR::b_box);
       tma_load_2d_warp(b, &mapX, full(s), k * k1, 0);
       if (both) tma_load_2d_warp(b + TR::b_box, &mapX, full(s), k * k1 + 64, 0);
-      if (++s == S) s = 0, ph ^= 1u;
+      next();
      }
     }
     if (run) run = mbar_wait_warp(clear, 0, abort_flag, p.status);
@@ -451,8 +466,9 @@ few_tokens_kernel(const __grid_constant__ CUtensorMap mapG, const __grid_constan
       mbar_arrive_expect_tx_warp(full(s), I8 ? 2 * TR::b_box : TR::b_box);
       tma_load_3d_warp(b, &mapAct, full(s), k * TR::k, 0, a);
       if constexpr (I8) tma_load_3d_warp(b + TR::b_box, &mapAct, full(s), k * TR::k + 64, 0, a);
-      if (++s == S) s = 0, ph ^= 1u;
+      next();
     }
+    drain_ring(1, n);
   } else if (warp == 1) {
     // ---------------- MMA: the whole warp, one lane elected for each ----------------
     constexpr uint32_t idesc = idesc_bf16_f32(128, NP, false, false);

@@ -235,3 +235,24 @@ def test_few_tokens_in_a_graph_beside_a_small_tensor(lib, weights):
         graph.replay()
         differ += (out != want[i % 2]).sum()
     assert int(differ) == 0 and int(st) == 0
+
+
+def test_few_tokens_over_memory_of_other_uses(lib):
+    """The workspace's memory as other tensors leave it: small integers, row maps
+    with minus ones, zeros under any epoch."""
+    d = _dev(_data(16, 12, 512, 40, 6, 256, "bf16"))
+    n = lib.moe_layer_few_tokens_workspace_size(12, 6, 512, 256, 40) // 8 * 8
+    want = lib.moe_layer_few_tokens(**d)
+    fills = [torch.arange(n // 8, device=DEV), torch.arange(n // 8, device=DEV) - 1,
+             torch.arange(n // 4, dtype=torch.int32, device=DEV), torch.full((n // 8,), -1, device=DEV)]
+    for first in (-161, -2, -1, 1, 2**62):                  # zeros after another epoch
+        z = torch.zeros(n // 8, dtype=torch.int64, device=DEV)
+        z[0] = first
+        fills.append(z)
+    z = torch.full((n // 8,), -1, device=DEV)
+    z[0] = 0
+    fills.append(z)
+    for f in fills:
+        ws = torch.cat([f.view(torch.uint8), torch.zeros(64, dtype=torch.uint8, device=DEV)])
+        for _ in range(3):
+            assert torch.equal(lib.moe_layer_few_tokens(**d, workspace=ws), want)

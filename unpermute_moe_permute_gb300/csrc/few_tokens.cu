@@ -119,13 +119,12 @@ struct Segments {
   }
 };
 
-// Tag of an epoch (a mixing function, so that a workspace filled with one
-// byte does not look like its own tag).
-__device__ __forceinline__ unsigned long long tag_of(unsigned long long e) {
-  e += 0x9e3779b97f4a7c15ull;
-  e = (e ^ (e >> 30)) * 0xbf58476d1ce4e5b9ull;
-  e = (e ^ (e >> 27)) * 0x94d049bb133111ebull;
-  return e ^ (e >> 31);
+// Tag that CTA c sets in an epoch: a multiple of 2^64 / golden ratio, which
+// spreads neighbouring numbers over all 64 bits, made odd.  Zeros are no tag,
+// every CTA has another, and memory that holds something else (one byte
+// repeated, small integers, minus ones) holds none.
+__device__ __forceinline__ unsigned long long tag_of(unsigned long long e, int c) {
+  return (e + (unsigned long long)c + 1) * 0x9e3779b97f4a7c15ull | 1ull;
 }
 
 // Wait by a whole warp until ok() holds in every lane; false when the limit
@@ -266,7 +265,7 @@ few_tokens_kernel(const __grid_constant__ CUtensorMap mapG, const __grid_constan
     tmem_relinquish();
   }
   // this CTA's share of the counters, then its flag
-  const unsigned long long epoch = *p.epoch, tag = tag_of(epoch);
+  const unsigned long long epoch = *p.epoch;
   const int n_count = p.A_max + p.A_max * ((p.I + 127) / 128) + (p.H + 255) / 256 + 1;
   for (int i = cta * TR::threads + threadIdx.x; i < n_count; i += G * TR::threads) p.count[i] = 0u;
   // the slots' experts, and the experts that some slot chose, in order
@@ -293,7 +292,8 @@ few_tokens_kernel(const __grid_constant__ CUtensorMap mapG, const __grid_constan
   fence_proxy_async_smem();  // (before TMA writes where the ids were)
   __syncthreads();
   if (threadIdx.x == 32)
-    asm volatile("st.release.gpu.global.u64 [%0], %1;" ::"l"(p.epoch + 1 + cta), "l"(tag) : "memory");
+    asm volatile("st.release.gpu.global.u64 [%0], %1;" ::"l"(p.epoch + 1 + cta), "l"(tag_of(epoch, cta))
+                 : "memory");
   if (warp == 0) {
     const int n = __popc(bitmap[lane]);
     int incl = n;
@@ -345,10 +345,11 @@ few_tokens_kernel(const __grid_constant__ CUtensorMap mapG, const __grid_constan
       unsigned long long w[(kMaxCtas + 31) / 32];
 #pragma unroll
       for (int i = 0; i < (kMaxCtas + 31) / 32; ++i)
-        w[i] = lane + 32 * i < G ? ld_relaxed(flags + lane + 32 * i) : tag;
+        w[i] = lane + 32 * i < G ? ld_relaxed(flags + lane + 32 * i) : 0ull;
       bool all = true;
 #pragma unroll
-      for (int i = 0; i < (kMaxCtas + 31) / 32; ++i) all &= w[i] == tag;
+      for (int i = 0; i < (kMaxCtas + 31) / 32; ++i)
+        all &= lane + 32 * i >= G || w[i] == tag_of(epoch, lane + 32 * i);
       return all;
     }, abort_flag, p.status);
     if (ok) {

@@ -266,3 +266,31 @@ def test_products_repeat(lib, per):
         if i % 20 == 0:
             differ += (u != up).sum() + (d != down).sum()
     assert int(differ) == 0 and int(st) == 0
+
+
+def test_new_outputs_are_filled_where_torch_fills_them(lib):
+    """Under deterministic algorithms torch fills new memory (NaN, the largest
+    integer): the rows that no call writes too, the bytes of any other memory not."""
+    T, K, H, E, I = 24, 4, 64, 6, 32
+    g = torch.Generator(device=DEV).manual_seed(8)
+    ids = torch.rand(T, E + 4, generator=g, device=DEV).topk(K, dim=1).indices.int()
+    x = torch.randn(T, H, generator=g, device=DEV).bfloat16()
+    w = torch.randint(-127, 128, (E, I, H), generator=g, device=DEV, dtype=torch.int8)
+    cs = torch.full((E, I), 1e-3, device=DEV)
+    r = lib.moe_permute(None, ids, E, 4)
+    n = int(r.expert_offsets[-1])
+    assert 0 < n < T * K
+    junk = [torch.full((T * K, m), 3, dtype=d, device=DEV)
+            for m, d in ((H, torch.int8), (1, torch.float32), (I, torch.bfloat16))]
+    del junk                                                        # (back to the allocator)
+    before = torch.are_deterministic_algorithms_enabled()
+    torch.use_deterministic_algorithms(True)
+    try:
+        q, s = lib.moe_quantize_rows(x, row_map=r.row_map, K=K)
+        act = lib.moe_gate_up_swiglu_int8(q, s, r.expert_offsets, w, cs, w, cs)
+        y = lib.moe_down_proj_int8(q, s, r.expert_offsets, w, cs, out_dtype=torch.float32)
+    finally:
+        torch.use_deterministic_algorithms(before)
+    assert (q[n:] == 127).all()
+    for t in (s, act, y):
+        assert torch.isnan(t[n:]).all() and torch.isfinite(t[:n]).all()

@@ -155,17 +155,27 @@ try:
     _empty_strided = torch._C._dynamo.guards._empty_strided_cuda
 except AttributeError:
     _empty_strided = None
+if _get_device is None:
+    _empty_strided = None
+
+
+def _direct(like: torch.Tensor) -> bool:
+    """Whether the direct allocation gives what torch.empty would: on the current
+    device, and not where torch fills new memory (deterministic algorithms), which
+    the direct allocation does not."""
+    return (_empty_strided is not None and like.is_cuda and like.get_device() == _get_device()
+            and not torch.are_deterministic_algorithms_enabled())
 
 
 def _empty1(n: int, dtype, like: torch.Tensor) -> torch.Tensor:
-    if _empty_strided is not None and like.is_cuda and like.get_device() == _get_device():
+    if _direct(like):
         return _empty_strided((n,), (1,), dtype)
     return torch.empty(n, dtype=dtype, device=like.device)
 
 
 def _empty2(n: int, m: int, dtype, like: torch.Tensor) -> torch.Tensor:
     """An uninitialised [n, m] on the device of `like`."""
-    if _empty_strided is not None and like.is_cuda and like.get_device() == _get_device():
+    if _direct(like):
         return _empty_strided((n, m), (m, 1), dtype)
     return torch.empty((n, m), dtype=dtype, device=like.device)
 

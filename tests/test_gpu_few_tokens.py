@@ -256,3 +256,86 @@ def test_few_tokens_over_memory_of_other_uses(lib):
         ws = torch.cat([f.view(torch.uint8), torch.zeros(64, dtype=torch.uint8, device=DEV)])
         for _ in range(3):
             assert torch.equal(lib.moe_layer_few_tokens(**d, workspace=ws), want)
+
+
+# Phase 1 over equal runs of units, a tile shared by the CTAs whose runs meet in
+# it ("split"): taken when there are more tiles of 128 columns than CTAs, or few
+# and long ones.  Columns of an accumulator (16, 32, 64) and, on 152 CTAs, tiles,
+# shared tiles (bf16 / int8) and CTAs of a shared tile.
+SPLIT = [  # T, H, E, K, I
+    (16, 512, 100, 8, 320),    # 16: 219 tiles, 133 / 114 shared, 2 CTAs
+    (17, 320, 100, 8, 320),    # 32: 213 tiles, 121 / 101 shared, 2 CTAs
+    (32, 1088, 100, 8, 256),   # 32, all in use: 186 tiles, 142 / 134 shared, 2 CTAs
+    (33, 320, 100, 8, 256),    # 64, the second half of the warps with one token: 186 tiles, 120 / 100 shared, 2 CTAs
+    (64, 1088, 100, 8, 256),   # 64, all in use: 200 tiles, 136 / 128 shared, 2 CTAs
+    (24, 4096, 6, 2, 128),     # 32: 6 tiles of 26 CTAs each
+    (50, 4096, 6, 2, 192),     # 64, half of a tile past the end: 12 tiles of 13 or 14 CTAs each
+]
+
+
+@pytest.mark.parametrize("weights", ["bf16", "int8"])
+@pytest.mark.parametrize("T,H,E,K,I", SPLIT)
+def test_few_tokens_with_shared_tiles(lib, T, H, E, K, I, weights):
+    d = _data(T + H + E, T, H, E, K, I, weights, shared=T % 2 == 1)
+    _check(lib.moe_layer_few_tokens(**_dev(d)), d)
+
+
+@pytest.mark.parametrize("weights", ["bf16", "int8"])
+@pytest.mark.parametrize("T,H,E,K,I", [(31, 512, 100, 6, 320), (64, 512, 100, 8, 256)])
+def test_few_tokens_with_shared_tiles_repeats_bit_for_bit(lib, T, H, E, K, I, weights):
+    """A dirty workspace, the last call's own words, and first words written back."""
+    d, e = (_dev(_data(s, T, H, E, K, I, weights, shared=True)) for s in (17, 18))
+    want = [lib.moe_layer_few_tokens(**v) for v in (d, e)]
+    n = lib.moe_layer_few_tokens_workspace_size(T, K, H, I, E)
+    st = lib.new_status()
+    differ = torch.zeros((), dtype=torch.int64, device=DEV)
+    for fill in (0, 255, 85):
+        ws = torch.full((n,), fill, dtype=torch.uint8, device=DEV)
+        first = ws[:8].clone()
+        for i in range(40):
+            if i % 4 == 3:
+                ws[:8].copy_(first)
+            out = lib.moe_layer_few_tokens(**(d, e)[i % 2], workspace=ws, dev_status=st)
+            differ += (out != want[i % 2]).sum()
+    assert int(differ) == 0 and int(st) == 0
+
+
+def test_few_tokens_with_shared_tiles_on_two_streams_and_in_a_graph(lib):
+    a = _dev(_data(19, 20, 512, 100, 8, 320, "bf16"))
+    b = _dev(_data(20, 64, 512, 100, 8, 256, "int8"))
+    want = lib.moe_layer_few_tokens(**a), lib.moe_layer_few_tokens(**b)
+    streams = torch.cuda.Stream(), torch.cuda.Stream()
+    got = [[], []]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for i, d in enumerate((a, b)):
+            with torch.cuda.stream(streams[i]):
+                got[i].append(lib._m.moe_layer_few_tokens(**d))
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(torch.equal(o, want[i]) for o in got[i])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = lib._m.moe_layer_few_tokens(**b)
+    c = _dev(_data(21, 64, 512, 100, 8, 256, "int8"))
+    for k in ("tokens", "expert_ids", "probs"):
+        b[k].copy_(c[k])
+    for _ in range(3):
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, lib.moe_layer_few_tokens(**b))
+
+
+def test_few_tokens_with_shared_tiles_keep_to_their_own_rows(lib):
+    """Values of one token reach no other; ids of inactive slots change at most
+    the order of the sums."""
+    d = _data(22, 40, 512, 100, 8, 320, "bf16")
+    clean = lib.moe_layer_few_tokens(**_dev(d)).cpu()
+    d["tokens"][3], d["tokens"][39, 5] = float("nan"), float("inf")
+    out = lib.moe_layer_few_tokens(**_dev(d)).cpu()
+    keep = [t for t in range(40) if t not in (3, 39)]
+    assert torch.isnan(out[3]).all() and torch.equal(out[keep], clean[keep])
+    mask = torch.ones(40, dtype=torch.uint8)
+    mask[::3] = 0
+    d = _data(22, 40, 512, 100, 8, 320, "bf16")
+    _check(lib.moe_layer_few_tokens(**_dev(d), active_mask=mask.to(DEV)), d, mask)

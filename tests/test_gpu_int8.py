@@ -294,3 +294,33 @@ def test_new_outputs_are_filled_where_torch_fills_them(lib):
     assert (q[n:] == 127).all()
     for t in (s, act, y):
         assert torch.isnan(t[n:]).all() and torch.isfinite(t[:n]).all()
+
+
+# Row lengths of every form: 1 to 4 chunks a thread at 32, 64, 128 and 256 threads
+# a row, 8 chunks, and rows read twice (past 16384).
+LENGTHS = [16, 256, 272, 512, 528, 768, 784, 1024, 1040, 1536, 1552, 2048, 2064, 4096, 4112, 8192, 8208, 16384,
+           16400, 40000]
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("H", LENGTHS)
+def test_quantize_rows_of_every_length(lib, H, dtype):
+    T, K, E = 11, 3, 5
+    g = np.random.default_rng(H)
+    x = _rows(H + 1, T, H, dtype)
+    x[4, -1], x[5, 0], x[6, H // 2 + 1] = 50.0, -60.0, 70.0             # the largest at a row's ends
+    x[7, -3] = float("nan")
+    w_q, w_s = S.quantize_rows(np64(x))
+    q, s = lib.moe_quantize_rows(x.to(DEV))
+    assert np.array_equal(np64(q), w_q)
+    assert np.array_equal(s.cpu().numpy(), w_s, equal_nan=True)
+    ids = torch.from_numpy(np.argsort(g.random((T, E + 1)), axis=1)[:, :K].astype(np.int32))
+    r = lib.moe_permute(None, ids.to(DEV), E, 1)                         # (one special id: rows that stay)
+    q = torch.full((T * K, H), 99, dtype=torch.int8, device=DEV)
+    s = torch.full((T * K,), 99.0, device=DEV)
+    lib.moe_quantize_rows(x.to(DEV), row_map=r.row_map, K=K, q=q, scale=s)
+    si, _, _, off = O.permute_routing(ids.numpy(), E, 1)
+    n = int(off[-1])
+    assert np.array_equal(np64(q)[:n], w_q[si[:n] // K])
+    assert np.array_equal(s.cpu().numpy()[:n], w_s[si[:n] // K], equal_nan=True)
+    assert (q[n:] == 99).all() and (s[n:] == 99).all()

@@ -127,3 +127,43 @@ def test_router_large_batch_and_second_stream(lib):
     assert torch.equal(ids, ids2) and torch.equal(p, p2)
     want = torch.sort(l, dim=1, descending=True, stable=True).indices[:, :8]
     assert torch.equal(ids.long(), want)
+
+
+# ids of a row whose K slots name an expert more than once: neighbours, the first
+# and the last, half of the slots apart, three times, all the same
+REPEATED = [
+    [3, 3], [5, 5, 5], [7, 1, 7], [2, 9, 9, 4], [8, 1, 2, 8], [6, 0, 6, 0], [4, 11, 13, 4, 11, 13],
+    [1, 2, 3, 4, 1, 6, 7, 8], [10, 0, 10, 3, 10, 5, 6, 7], [12] * 8, [0, 1, 2, 3, 4, 5, 6, 7, 8, 9, 10, 11, 12, 13, 14, 0],
+    [0, 1, 2, 3, 4, 5, 6, 7, 0, 1, 2, 3, 4, 5, 6, 7],
+]
+
+
+@pytest.mark.parametrize("scoring,renorm", MODES)
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("E", [16, 40, 257])
+def test_router_grad_of_repeated_ids(lib, E, dtype, scoring, renorm):
+    """An expert that several slots name collects their gradients, whatever their
+    places and whatever order the slots are in: the Jacobian of each slot's
+    weight, in 64 bits.  The bound is the one above, for K slots."""
+    g = np.random.default_rng(E)
+    for row in REPEATED:
+        K = len(row)
+        ids = np.array([row, row[::-1], np.roll(row, 1), g.permutation(row)], dtype=np.int32)
+        logits = torch.from_numpy(g.standard_normal((4, E)) * 2).to(dtype)
+        logits[3, row[0]] = -np.inf                                     # a masked one among them
+        l, gp = np64(logits), g.standard_normal((4, K)).astype(np.float32)
+        d = lib.moe_router_topk_grad(torch.from_numpy(gp).to(DEV), logits.to(DEV), torch.from_numpy(ids).to(DEV),
+                                     scoring=scoring, renormalize=renorm, scale=2.0)
+        want = S.router_topk_grad(gp, l, ids, scoring, renorm, 2.0)
+        mag = np.zeros_like(l)
+        for t in range(4):
+            q = np.abs(S._selected(S._clean(l)[t], ids[t], scoring, renorm))
+            gk = np.abs(2.0 * gp[t].astype(np.float64))
+            D = (gk * q).sum()
+            if scoring == "softmax" and not renorm:
+                mag[t] += S._scores(S._clean(l)[t], scoring) * D
+            np.add.at(mag[t], ids[t], q * (gk + (D if scoring == "softmax" or renorm else 0)))
+        bound = (_rel(l, E) + K * 2.0 ** -23) * mag + 1e-37
+        if dtype == torch.bfloat16:
+            bound = bound + ulp(np.maximum(np.abs(np64(d)), np.abs(want)), "bf16")
+        assert np.all(np.abs(np64(d) - want) <= bound)

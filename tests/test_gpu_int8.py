@@ -324,3 +324,25 @@ def test_quantize_rows_of_every_length(lib, H, dtype):
     assert np.array_equal(np64(q)[:n], w_q[si[:n] // K])
     assert np.array_equal(s.cpu().numpy()[:n], w_s[si[:n] // K], equal_nan=True)
     assert (q[n:] == 99).all() and (s[n:] == 99).all()
+
+
+@pytest.mark.parametrize("per", [96, 8])
+def test_products_repeat_in_every_launch(lib, per):
+    """Every one of thousands of launches of both products in both forms is
+    compared, on the device."""
+    E, H, I = 64, 1024, 768
+    g = torch.Generator(device=DEV).manual_seed(per + 1)
+    off = torch.arange(0, E + 1, dtype=torch.int32, device=DEV) * per
+    N = E * per
+    x = torch.randint(-127, 128, (N, H), device=DEV, generator=g, dtype=torch.int8)
+    wg, wu = (torch.randint(-127, 128, (E, I, H), device=DEV, generator=g, dtype=torch.int8) for _ in range(2))
+    rs, cs = torch.full((N,), 1e-3, device=DEV), torch.full((E, I), 1e-3, device=DEV)
+    st = lib.new_status()
+    up = lib.moe_gate_up_swiglu_int8(x, rs, off, wg, cs, wu, cs, dev_status=st).clone()
+    down = lib.moe_down_proj_int8(x, rs, off, wg, cs, dev_status=st).clone()
+    differ = torch.zeros((), dtype=torch.bool, device=DEV)
+    for _ in range(3000):
+        u = lib.moe_gate_up_swiglu_int8(x, rs, off, wg, cs, wu, cs, dev_status=st)
+        d = lib.moe_down_proj_int8(x, rs, off, wg, cs, dev_status=st)
+        differ |= (u != up).any() | (d != down).any()
+    assert not bool(differ) and int(st) == 0

@@ -42,9 +42,8 @@
 // retrying on one word cost 75 us.)
 #include <math.h>
 
-#include <mutex>
-
 #include "common.cuh"
+#include "per_device.h"
 #include "tc_warp.cuh"
 #include "tma_host.cuh"
 
@@ -845,13 +844,14 @@ int launch_few(FewParams p, const void* x, const void* Wg, const void* Wu, const
       !make_map_sw128(&md, Wd, esz, 3, d2, bw) || !make_map_sw128(&mx, x, 2, 2, dx, bx) ||
       !make_map_sw128(&ma, p.act, 2, 3, da, bx))
     return MOE_ERR_CUDA;
-  static std::once_flag once;
-  static cudaError_t attr = cudaSuccess;
-  std::call_once(once, [] {
-    attr = cudaFuncSetAttribute(few_tokens_kernel<NP, I8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                (int)TR::smem);
+  static PerDevice smem_allowed;
+  int dev = -1;
+  if (cudaGetDevice(&dev) != cudaSuccess) return MOE_ERR_CUDA;
+  const int allowed = smem_allowed.get(dev, [] {
+    return cudaFuncSetAttribute(few_tokens_kernel<NP, I8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                (int)TR::smem) == cudaSuccess;
   });
-  if (attr != cudaSuccess) return MOE_ERR_CUDA;
+  if (!allowed) return MOE_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeCooperative;

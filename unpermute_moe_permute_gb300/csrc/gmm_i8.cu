@@ -38,11 +38,11 @@
 // A cluster-scope release there, by one forwarding thread, cost 1100 cycles a
 // step (8192 x 4096 x 4096: 399 us against 262 us, the rest being as it was).
 #include <cuda_fp16.h>
+#include <limits.h>
 #include <math.h>
 
-#include <mutex>
-
 #include "common.cuh"
+#include "per_device.h"
 #include "sched.cuh"
 #include "tc_warp.cuh"
 #include "tma_host.cuh"
@@ -556,13 +556,14 @@ int check_i8(const void* A, const float* rs, const int32_t* off, int N, int H, i
 template <typename C, bool kSwiglu, typename O>
 int launch_cfg(const CUtensorMap& w0, const CUtensorMap& w1, const CUtensorMap& x32,
                const CUtensorMap& x16, const I8Params& p, cudaStream_t s) {
-  static std::once_flag once;
-  static cudaError_t attr = cudaSuccess;
-  std::call_once(once, [] {
-    attr = cudaFuncSetAttribute(gmm_i8_kernel<C, kSwiglu, O>,
-                                cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem);
+  static PerDevice smem_allowed, resident_pairs;
+  int dev = -1;
+  if (cudaGetDevice(&dev) != cudaSuccess) return MOE_ERR_CUDA;
+  const int allowed = smem_allowed.get(dev, [] {
+    return cudaFuncSetAttribute(gmm_i8_kernel<C, kSwiglu, O>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                (int)C::kSmem) == cudaSuccess;
   });
-  if (attr != cudaSuccess) return MOE_ERR_CUDA;
+  if (!allowed) return MOE_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute at[2];
   at[0].id = cudaLaunchAttributeClusterDimension;
@@ -578,15 +579,13 @@ int launch_cfg(const CUtensorMap& w0, const CUtensorMap& w1, const CUtensorMap& 
   at[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 2;
-  static int resident = -1;
-  if (resident < 0) {
+  const int pairs = resident_pairs.get(dev, [&] {
     int n = 0;
-    resident = (cudaOccupancyMaxActiveClusters(&n, gmm_i8_kernel<C, kSwiglu, O>, &cfg) == cudaSuccess && n > 0)
-                   ? n
-                   : 0;
+    const bool known = cudaOccupancyMaxActiveClusters(&n, gmm_i8_kernel<C, kSwiglu, O>, &cfg) == cudaSuccess;
     (void)cudaGetLastError();
-  }
-  if (resident > 0 && 2 * resident < (int)cfg.gridDim.x) cfg.gridDim.x = 2 * resident;
+    return known && n > 0 ? n : INT_MAX;
+  });
+  if (pairs < (int)cfg.gridDim.x / 2) cfg.gridDim.x = 2 * pairs;
   if (cudaLaunchKernelEx(&cfg, gmm_i8_kernel<C, kSwiglu, O>, w0, w1, x32, x16, p) != cudaSuccess) {
     (void)cudaGetLastError();
     return MOE_ERR_CUDA;

@@ -231,7 +231,7 @@ void launch_quantize(const T* x, const int32_t* row_map, int n_tok, int H, int K
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.gridDim = dim3((n_tok + R - 1) / R);
+    cfg.gridDim = dim3((n_tok - 1) / R + 1);  // (n_tok + R - 1 may pass 31 bits)
     cfg.blockDim = dim3(kThreads);
     cfg.stream = s;
     cfg.attrs = at;

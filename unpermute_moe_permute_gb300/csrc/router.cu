@@ -463,7 +463,7 @@ extern "C" int moe_router_topk(const void* logits, int dtype, int T, int E, int 
   if (T == 0) return MOE_OK;
   if (!expert_ids || !probs || !aligned16(expert_ids) || !aligned16(probs))
     return MOE_ERR_INVALID_ARG;
-  const int grid = (T + kWarps - 1) / kWarps;
+  const int grid = (T - 1) / kWarps + 1;  // (T + kWarps - 1 may pass 31 bits)
   auto go = [&](auto* x) {
     using D = std::remove_const_t<std::remove_pointer_t<decltype(x)>>;
     by_width<D>(E, [&](auto n, auto vec) {
@@ -489,7 +489,7 @@ extern "C" int moe_router_topk_grad(const float* grad_probs, const void* logits,
   if (!grad_probs || !expert_ids || !grad_logits || !aligned16(grad_probs) ||
       !aligned16(expert_ids) || !aligned16(grad_logits))
     return MOE_ERR_INVALID_ARG;
-  const int grid = (T + kWarps - 1) / kWarps;
+  const int grid = (T - 1) / kWarps + 1;  // (T + kWarps - 1 may pass 31 bits)
   auto go = [&](auto* x, auto* d) {
     using D = std::remove_pointer_t<decltype(d)>;
     by_width<D>(E, [&](auto n, auto vec) {

@@ -487,7 +487,9 @@ int moe_router_topk_grad(const float* grad_probs, const void* logits, int dtype,
  * The integers are multiplied exactly and summed in 32 bits (fp32: exact
  * while the partial sums stay under 2^24, else each addition rounds to 24
  * bits); one rounding to the output's dtype.  H and I multiples of 16, at
- * most 131072; rows >= expert_offsets[E] are not touched. */
+ * most 131072; N at most MOE_INT8_MAX_ROWS; rows >= expert_offsets[E] are not
+ * touched. */
+#define MOE_INT8_MAX_ROWS 0x7f000000
 int moe_quantize_rows(const void* x, int dtype, const int32_t* row_map, int T, int H, int K, int N,
                       int8_t* q, float* scale, cudaStream_t stream);
 int moe_gate_up_swiglu_int8(const int8_t* permuted_q, const float* row_scale,

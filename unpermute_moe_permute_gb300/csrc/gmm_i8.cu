@@ -549,6 +549,7 @@ int check_i8(const void* A, const float* rs, const int32_t* off, int N, int H, i
   if (E > kMaxExperts) return MOE_ERR_SHAPE;
   if (off == nullptr && E != 1) return MOE_ERR_INVALID_ARG;
   if (H % 16 || I % 16 || H > 131072 || I > 131072) return MOE_ERR_SHAPE;
+  if (N > MOE_INT8_MAX_ROWS) return MOE_ERR_SHAPE;  // (rows and row tiles added up stay within 31 bits)
   if (N > 0 && (!A || !rs || !aligned16(A))) return MOE_ERR_INVALID_ARG;
   return MOE_OK;
 }

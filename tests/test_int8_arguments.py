@@ -4,6 +4,7 @@ import os
 import shutil
 
 import pytest
+import torch
 
 LIMIT = 0x7f000000
 
@@ -29,3 +30,18 @@ def test_rows(lib, N, what):
                                        None) == want
     assert lib.moe_down_proj_int8(None, None, None, N, 64, 64, 1, None, None, None, binding.MOE_BF16, None,
                                   None) == want
+
+
+def test_offsets_for_every_expert(lib):
+    """The kernels read E + 1 offsets."""
+    from unpermute_moe_permute_gb300 import binding as b
+    q, rs = torch.zeros(4, 128, dtype=torch.int8), torch.zeros(4)
+    w, cs = torch.zeros(8, 64, 128, dtype=torch.int8), torch.zeros(8, 64)
+    for n in (0, 1, 8):
+        off = torch.zeros(n, dtype=torch.int32)
+        with pytest.raises(ValueError, match="expert_offsets must have"):
+            b.moe_gate_up_swiglu_int8(q, rs, off, w, cs, w, cs, act=torch.zeros(4, 64, dtype=torch.bfloat16))
+        with pytest.raises(ValueError, match="expert_offsets must have"):
+            b.moe_down_proj_int8(q, rs, off, w, cs, expanded=torch.zeros(4, 64))
+    with pytest.raises(ValueError, match="CUDA"):                    # enough of them: the next check
+        b.moe_down_proj_int8(q, rs, torch.zeros(9, dtype=torch.int32), w, cs, expanded=torch.zeros(4, 64))

@@ -676,6 +676,12 @@ def moe_quantize_rows(x, *, row_map=None, K: int = 1, N: Optional[int] = None, q
     return q, scale
 
 
+def _offsets(expert_offsets: Optional[torch.Tensor], E: int):
+    _check(expert_offsets, torch.int32, "expert_offsets")
+    if expert_offsets is not None and expert_offsets.numel() < E + 1:
+        raise ValueError(f"expert_offsets must have E+1 = {E + 1} entries, got {expert_offsets.numel()}")
+
+
 def moe_gate_up_swiglu_int8(permuted_q, row_scale, expert_offsets, W_gate_q, gate_scale, W_up_q,
                             up_scale, *, act=None, dev_status=None):
     """act [N, I] bf16 = silu(g) * u, g and u the 8-bit products of the
@@ -699,7 +705,7 @@ def moe_gate_up_swiglu_int8(permuted_q, row_scale, expert_offsets, W_gate_q, gat
                                 (act, torch.bfloat16, (N, I), "act")):
             _check(t, dt, n)
             _shape(t, shape, n)
-    _check(expert_offsets, torch.int32, "expert_offsets")
+    _offsets(expert_offsets, E)
     _call("moe_gate_up_swiglu_int8", _ptr(permuted_q), _ptr(row_scale), _ptr(expert_offsets), N,
           H, I, E, _ptr(W_gate_q), _ptr(gate_scale), _ptr(W_up_q), _ptr(up_scale), _ptr(act),
           _ptr(dev_status), _stream())
@@ -726,7 +732,7 @@ def moe_down_proj_int8(act_q, row_scale, expert_offsets, W_down_q, down_scale, *
                                 (down_scale, f32, (E, H), "down_scale")):
             _check(t, dt, n)
             _shape(t, shape, n)
-    _check(expert_offsets, torch.int32, "expert_offsets")
+    _offsets(expert_offsets, E)
     _call("moe_down_proj_int8", _ptr(act_q), _ptr(row_scale), _ptr(expert_offsets), N, H, I, E,
           _ptr(W_down_q), _ptr(down_scale), _ptr(expanded), _dtype(expanded), _ptr(dev_status),
           _stream())

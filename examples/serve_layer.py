@@ -129,7 +129,9 @@ def main(argv=None):
                   f"off the bf16 layer by {off(y, want[:t]):.4f}")
     print(f"training {a.tokens:5d} tokens  "
           f"{_time(lambda: layer.backward(want, layer.forward(x)[1]), 5):8.1f} us forward and backward")
-    lib.moe_check_status(layer.status)
+    status = lib.moe_check_status(layer.status)
+    if status != lib.MOE_OK:
+        raise SystemExit(lib.status_name(status))
 
 
 if __name__ == "__main__":

@@ -96,3 +96,10 @@ def test_command(example, capsys):
     example.main(["--tokens", "70", "--hidden", "256", "--inter", "128", "--experts", "8", "--topk", "2"])
     text = capsys.readouterr().out
     assert "prompt" in text and "decode      64" in text and "training" in text
+
+
+def test_command_says_when_a_kernel_failed(example, monkeypatch):
+    """The device status word ends the command with its name."""
+    monkeypatch.setattr(example.lib, "moe_check_status", lambda status: example.lib.MOE_ERR_BAD_ID)
+    with pytest.raises(SystemExit, match=example.lib.status_name(example.lib.MOE_ERR_BAD_ID)):
+        example.main(["--tokens", "70", "--hidden", "256", "--inter", "128", "--experts", "8", "--topk", "2"])

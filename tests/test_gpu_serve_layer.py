@@ -103,3 +103,35 @@ def test_command_says_when_a_kernel_failed(example, monkeypatch):
     monkeypatch.setattr(example.lib, "moe_check_status", lambda status: example.lib.MOE_ERR_BAD_ID)
     with pytest.raises(SystemExit, match=example.lib.status_name(example.lib.MOE_ERR_BAD_ID)):
         example.main(["--tokens", "70", "--hidden", "256", "--inter", "128", "--experts", "8", "--topk", "2"])
+
+
+@pytest.mark.parametrize("T", [9, 700])
+def test_prompt_and_training_in_a_graph(example, T):
+    """Router, rows, products and the router's gradient, whose launches overlap the
+    end of the kernel before, captured once (few and many rows an expert) and
+    replayed with new tokens."""
+    layer = example.Layer(256, 128, 8, 2, renormalize=False)
+    x, grad = (torch.zeros(T, 256, device="cuda", dtype=torch.bfloat16) for _ in range(2))
+
+    def step():
+        out, saved = layer.forward(x)
+        dx, dl, (dg, du, dd) = layer.backward(grad, saved)
+        return layer.prompt(x), out, dx, dl, dg, du, dd
+
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        step()
+    s.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        got = step()
+    for seed in range(3):
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        for t in (x, grad):
+            t.copy_(torch.randn(T, 256, device="cuda", generator=g))
+        graph.replay()
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(got, step()):
+            assert torch.equal(a, b)
+    assert int(layer.status) == 0

@@ -432,7 +432,9 @@ int moe_gate_up_wgrad(const void* dgu, const void* permuted, int dtype,
  *   probs[t, k]    = scale * p_id(k),                    renormalize == 0
  *                  = scale * p_id(k) / sum_k' p_id(k'),  renormalize != 0
  * in fp32 whatever the logits' dtype (both scores grow with the logit, so
- * the selection compares the logits themselves, without rounding).
+ * the selection compares the logits themselves, without rounding).  A
+ * selection by anything else (a score plus a bias, groups of experts first) is
+ * not made here; experts that such a step rules out are masked.
  *   -inf masks an expert: its weight is 0 (it is selected, lowest index
  *   first, only when fewer than K logits are above -inf; a row of -inf alone
  *   gets ids 0..K-1 and weights 0).  +inf counts as the largest finite
@@ -507,8 +509,9 @@ int moe_down_proj_int8(const int8_t* act_q, const float* row_scale, const int32_
  *   act[t, k] = silu(W_gate[e] x_t) * (W_up[e] x_t),       e = expert_ids[t, k]
  *   out[t]    = shared_x[t] + sum_k probs[t, k] W_down[e] act[t, k]
  * for 0 <= T <= MOE_FEW_TOKENS tokens in bf16: what moe_permute, moe_expert_mlp
- * and moe_combine give, without their buffers, reading each weight of an
- * expert that some token chose once.
+ * and moe_unpermute give (with shared_x as in moe_combine, whose copy and const
+ * experts are not made here: every special id adds nothing), without their
+ * buffers, reading each weight of an expert that some token chose once.
  *   tokens, out     [T, H] bf16; shared_x [T, H] bf16 or NULL
  *   weight_dtype    MOE_BF16: W_gate, W_up [E, I, H], W_down [E, H, I] bf16
  *                   (the scale pointers are NULL); MOE_INT8: the same in int8
@@ -521,12 +524,15 @@ int moe_down_proj_int8(const int8_t* act_q, const float* row_scale, const int32_
  *                   [0, E + num_special) or repeated within a row sets
  *                   MOE_ERR_BAD_ID and adds nothing.
  *   workspace       moe_layer_few_tokens_workspace_size(T, K, H, I, E) bytes,
- *                   16-byte aligned, needs no clearing; calls that can
- *                   overlap on the GPU need one each
+ *                   16-byte aligned, needs no clearing, and may be used for
+ *                   anything else between two calls; calls that can overlap
+ *                   on the GPU need one each
  * A token without an active slot gets shared_x[t], or zeros.  H and I are
- * multiples of 64.  Sums are fp32 in an order that depends on the sizes and
- * the ids alone; act is rounded to bf16 once.  A token's result depends on
- * its own row and its own experts' weights only. */
+ * multiples of 64.  Sums are fp32 in an order that depends on the sizes, the
+ * ids, the mask and the number of SMs alone; act is rounded to bf16 once, as
+ * moe_expert_mlp rounds it.  A token's result depends on its own row and its
+ * own experts' weights only, but for the order of the sums: other tokens' ids
+ * can change its last bits, their values cannot. */
 #define MOE_FEW_TOKENS 64
 size_t moe_layer_few_tokens_workspace_size(int T, int K, int H, int I, int E);
 int moe_layer_few_tokens(const void* tokens, const int32_t* expert_ids, const float* probs, int T,

@@ -15,10 +15,10 @@
 //     tile when all have finished;
 //   * the weights are the A operand (M = 128 of their rows), the tokens the B
 //     operand (N = 16, 32 or 64): every active expert is multiplied with all
-//     tokens, which the tensor cores have time for (at N = 64 under a fifth of
-//     the stream's time), and a (token, expert) pair that was not chosen is
-//     left out when the result is read;
-//   * one warp streams weights through a ring of 4 to 6 stages (TMA) without
+//     tokens, which the tensor cores have time for (at N = 64 they are busy 16 %
+//     of the time with bf16 weights, 24 % with 8-bit ones), and a (token,
+//     expert) pair that was not chosen is left out when the result is read;
+//   * one warp streams weights through a ring of 4 or 5 stages (TMA) without
 //     ever waiting for results: at the turn from phase 1 to phase 2 it fills
 //     the ring with down weights while the last activations are still being
 //     made.  Another warp loads the tokens' and activations' tiles and alone
@@ -76,7 +76,7 @@ struct FewTraits {
   static constexpr uint32_t b_box = NP * 128;            // 64 k of the tokens
   static constexpr bool can_narrow = NP == 16 && !I8;    // (see narrow below)
   static constexpr uint32_t stage = 2 * kBox16 + (I8 || can_narrow ? 2 : 1) * b_box;
-  static constexpr int stages = (int)(212992 / stage) < 6 ? (int)(212992 / stage) : 6;
+  static constexpr int stages = (int)(212992 / stage);   // 5; 4 for N = 64 with 8-bit weights
   static constexpr int threads = (I8 ? 20 : 12) * 32;
   static constexpr int bars = 2 * stages + 4 + 4 + 2;
   static constexpr uint32_t ctrl = stages * stage;
@@ -200,6 +200,17 @@ __device__ __forceinline__ void expand16_bf16(uint4 v, uint32_t* r) {
   r[6] = bytes_to_bf16(v.w, 0x4140), r[7] = bytes_to_bf16(v.w, 0x4342);
 }
 
+// act in fp32, rounded to bf16 once where it is stored: the second product's
+// tensor instruction takes both operands in one 16-bit type, and its weights
+// are bf16 (8-bit ones are exact in it).  fp16 would be finer, but act has the
+// range of a product of two sums and bf16 weights are not exact in fp16; the
+// layer's other path rounds act to bf16 as well.  It is the only rounding to
+// fewer than 32 bits before the output's own: it moves the output by 0.0026 of
+// its norm (T=64 H=2048 E=128 K=8 I=768; the output's own rounding is 0.0017),
+// and from the same formula with that rounding the kernel is 0.0005 off, the
+// roundings that fall the other way.  The exponential and the quotient are the
+// approximate ones, off by 2 + 1.16 |g| units of the 24th bit: under 2^-17 of
+// act for |g| < 88.
 __device__ __forceinline__ float swiglu(float g, float u) { return __fdividef(g, 1.f + __expf(-g)) * u; }
 
 template <int NP, bool I8>

@@ -596,7 +596,9 @@ int launch_cfg(const CUtensorMap& w0, const CUtensorMap& w1, const CUtensorMap& 
 }
 
 // Rows per expert, on average, up to which the few-rows form runs (the routing
-// itself is not known on the host).  GB300, E=64 H=2048, us, few / many:
+// itself is not known on the host; where it is skewed, an expert of many rows
+// reads its weights once for every 64 of them, which was not measured).  GB300,
+// E=64 H=2048, as many rows for every expert, us, few / many:
 //   rows  I=512 gate/up    down        I=768 gate/up    down
 //     25  42.0 / 49.4   28.7 / 33.0    53.9 / 66.3   33.8 / 41.0
 //     48  43.4 / 50.1   32.3 / 33.7    57.3 / 67.6   36.9 / 41.0

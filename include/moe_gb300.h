@@ -474,8 +474,8 @@ int moe_router_topk_grad(const float* grad_probs, const void* logits, int dtype,
  *                     copy of moe_permute_rows with the rounding fused in.
  *                     Entries outside [0, N) are skipped; rows that no entry
  *                     names are not written.
- * x [T, H] MOE_F32 or MOE_BF16, q [N, H] int8, scale [N]; H % 16 == 0.  For
- * weights, call it on [E * rows, H]: the scale of a row is then the scale of
+ * x [T, H] MOE_F32 or MOE_BF16, q [N, H] int8, scale [N]; H % 16 == 0, at most
+ * MOE_QUANTIZE_MAX_LENGTH.  For weights, call it on [E * rows, H]: the scale of a row is then the scale of
  * an output channel.
  *
  * The products, for the rows of expert e (expert_offsets as above;
@@ -492,6 +492,7 @@ int moe_router_topk_grad(const float* grad_probs, const void* logits, int dtype,
  * most 131072; N at most MOE_INT8_MAX_ROWS; rows >= expert_offsets[E] are not
  * touched. */
 #define MOE_INT8_MAX_ROWS 0x7f000000
+#define MOE_QUANTIZE_MAX_LENGTH 0x40000000
 int moe_quantize_rows(const void* x, int dtype, const int32_t* row_map, int T, int H, int K, int N,
                       int8_t* q, float* scale, cudaStream_t stream);
 int moe_gate_up_swiglu_int8(const int8_t* permuted_q, const float* row_scale,

@@ -1,4 +1,4 @@
-"""Arguments of the 8-bit products that the host refuses before any CUDA call."""
+"""Arguments of the 8-bit rows and products that are refused before any CUDA call."""
 
 import os
 import shutil
@@ -45,3 +45,13 @@ def test_offsets_for_every_expert(lib):
             b.moe_down_proj_int8(q, rs, off, w, cs, expanded=torch.zeros(4, 64))
     with pytest.raises(ValueError, match="CUDA"):                    # enough of them: the next check
         b.moe_down_proj_int8(q, rs, torch.zeros(9, dtype=torch.int32), w, cs, expanded=torch.zeros(4, 64))
+
+
+@pytest.mark.parametrize("H,what", [(0x40000000, "MOE_ERR_INVALID_ARG"), (0x40000010, "MOE_ERR_SHAPE"),
+                                    (2**31 - 16, "MOE_ERR_SHAPE")])
+def test_length_of_a_row(lib, H, what):
+    """Rows whose last step would pass 31 bits; up to the limit the missing output
+    is what is refused."""
+    from unpermute_moe_permute_gb300 import binding
+    for dtype in (binding.MOE_F32, binding.MOE_BF16):
+        assert lib.moe_quantize_rows(0x10000, dtype, None, 1, H, 1, 1, None, None, None) == getattr(binding, what)

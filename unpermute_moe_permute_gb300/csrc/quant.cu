@@ -265,6 +265,7 @@ extern "C" int moe_quantize_rows(const void* x, int dtype, const int32_t* row_ma
   if (T < 0 || H <= 0 || K <= 0 || N < 0) return MOE_ERR_INVALID_ARG;
   if (dtype != MOE_F32 && dtype != MOE_BF16) return MOE_ERR_INVALID_ARG;
   if (H % 16 || K > kMaxK || (long long)T * K > 0x7fffffffLL) return MOE_ERR_SHAPE;
+  if (H > MOE_QUANTIZE_MAX_LENGTH) return MOE_ERR_SHAPE;  // (a step past a row's end stays within 31 bits)
   if (row_map == nullptr && (K != 1 || N < T)) return MOE_ERR_SHAPE;
   if (T == 0 || N == 0) return MOE_OK;
   if (!x || !q || !scale || !aligned16(x) || !aligned16(q)) return MOE_ERR_INVALID_ARG;

@@ -475,8 +475,8 @@ int moe_router_topk_grad(const float* grad_probs, const void* logits, int dtype,
  *                     Entries outside [0, N) are skipped; rows that no entry
  *                     names are not written.
  * x [T, H] MOE_F32 or MOE_BF16, q [N, H] int8, scale [N]; H % 16 == 0, at most
- * MOE_QUANTIZE_MAX_LENGTH.  For weights, call it on [E * rows, H]: the scale of a row is then the scale of
- * an output channel.
+ * MOE_QUANTIZE_MAX_LENGTH.  For weights, call it on [E * rows, H]: the scale of
+ * a row is then the scale of an output channel.
  *
  * The products, for the rows of expert e (expert_offsets as above;
  * expert_offsets NULL with E = 1: one matrix for all N rows):
@@ -529,12 +529,13 @@ int moe_down_proj_int8(const int8_t* act_q, const float* row_scale, const int32_
  *                   anything else between two calls; calls that can overlap
  *                   on the GPU need one each
  * A token without an active slot gets shared_x[t], or zeros.  H and I are
- * multiples of 64.  Sums are fp32 in an order that depends on the sizes, the
+ * multiples of 64, at most MOE_FEW_MAX_SIZE.  Sums are fp32 in an order that depends on the sizes, the
  * ids, the mask and the number of SMs alone; act is rounded to bf16 once, as
  * moe_expert_mlp rounds it.  A token's result depends on its own row and its
  * own experts' weights only, but for the order of the sums: other tokens' ids
  * can change its last bits, their values cannot. */
 #define MOE_FEW_TOKENS 64
+#define MOE_FEW_MAX_SIZE 0x100000
 size_t moe_layer_few_tokens_workspace_size(int T, int K, int H, int I, int E);
 int moe_layer_few_tokens(const void* tokens, const int32_t* expert_ids, const float* probs, int T,
                          int H, int K, int I, int E, int num_special, const uint8_t* active_mask,

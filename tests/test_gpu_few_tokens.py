@@ -339,3 +339,18 @@ def test_few_tokens_with_shared_tiles_keep_to_their_own_rows(lib):
     mask[::3] = 0
     d = _data(22, 40, 512, 100, 8, 320, "bf16")
     _check(lib.moe_layer_few_tokens(**_dev(d), active_mask=mask.to(DEV)), d, mask)
+
+
+def test_few_tokens_of_long_rows(lib):
+    """H and I at the limit, one expert each (the sums by torch in 64 bits)."""
+    g = torch.Generator(device=DEV).manual_seed(23)
+    for H, I in ((2**20, 64), (64, 2**20)):
+        x, wg, wu, wd = (torch.randn(*s, generator=g, device=DEV, dtype=torch.bfloat16) * s[-1] ** -0.5
+                         for s in ((3, H), (1, I, H), (1, I, H), (1, H, I)))
+        x *= H ** 0.5
+        ids, p = torch.zeros(3, 1, dtype=torch.int32, device=DEV), torch.rand(3, 1, generator=g, device=DEV)
+        out = lib.moe_layer_few_tokens(x, ids, p, wg, wu, wd)
+        a, b = x.double() @ wg[0].double().t(), x.double() @ wu[0].double().t()
+        want = p.double() * ((torch.nn.functional.silu(a) * b) @ wd[0].double().t())
+        # two roundings to bf16 (act's, the output's), 2^-9 of a value at most each, and fp32 sums
+        assert float((out.double() - want).norm() / want.norm()) < 2 * 2.0 ** -9

@@ -890,6 +890,7 @@ using namespace moe::tc;
 
 extern "C" size_t moe_layer_few_tokens_workspace_size(int T, int K, int H, int I, int E) {
   if (T <= 0 || K <= 0 || H <= 0 || I <= 0 || E <= 0 || T > MOE_FEW_TOKENS || K > kMaxK) return 0;
+  if (H > MOE_FEW_MAX_SIZE || I > MOE_FEW_MAX_SIZE) return 0;
   return few_layout(T, K, H, I, E).total;
 }
 
@@ -909,6 +910,7 @@ extern "C" int moe_layer_few_tokens(const void* tokens, const int32_t* expert_id
   if ((long long)E + num_special > 0x7fffffffLL || (long long)K > (long long)E + num_special)
     return MOE_ERR_SHAPE;
   if (H % 64 || I % 64) return MOE_ERR_SHAPE;
+  if (H > MOE_FEW_MAX_SIZE || I > MOE_FEW_MAX_SIZE) return MOE_ERR_SHAPE;  // (T H, a tile's bytes: 31 bits)
   if (T == 0) return MOE_OK;
   if (!tokens || !expert_ids || !probs || !W_gate || !W_up || !W_down || !out || !workspace)
     return MOE_ERR_INVALID_ARG;

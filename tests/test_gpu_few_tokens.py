@@ -354,3 +354,34 @@ def test_few_tokens_of_long_rows(lib):
         want = p.double() * ((torch.nn.functional.silu(a) * b) @ wd[0].double().t())
         # two roundings to bf16 (act's, the output's), 2^-9 of a value at most each, and fp32 sums
         assert float((out.double() - want).norm() / want.norm()) < 2 * 2.0 ** -9
+
+
+@pytest.mark.parametrize("weights", ["bf16", "int8"])
+@pytest.mark.parametrize("T", [3, 20, 64])
+def test_few_tokens_saturated_gates(lib, T, weights):
+    """Gates far below and above the range of e^g, each alone in a column of act
+    and carried to one output.  act and out round to bf16 (2^-9 each), the
+    quotient is 0 where 1 + e^-g is past 2^126: 88 u 2^-126 at most is lost."""
+    H = I = 64
+    gate = torch.tensor([0.0, -0.0, 1, -1, 20, -20, 60, -60, 80, -80, 86, -86, 88, -88, 90, -90, 120, -120, 1000, -1000,
+                         3e4, -3e4, 127, -127] + [float(i) for i in range(-20, 20)])
+    u = torch.where(torch.arange(64) % 3 == 0, -3.0, 2.0)
+    x = torch.zeros(T, H, dtype=torch.bfloat16)
+    x[:, 0], x[:, 1] = 1, 1
+    if weights == "bf16":
+        wg, wu, wd = torch.zeros(1, I, H), torch.zeros(1, I, H), torch.eye(64)[None]
+        wg[0, :, 0], wu[0, :, 1] = gate, u
+        w, scales = [v.bfloat16() for v in (wg, wu, wd)], None
+        g64 = w[0][0, :, 0].double()
+    else:
+        w = [torch.zeros(1, 64, 64, dtype=torch.int8) for _ in range(3)]
+        w[0][0, :, 0], w[1][0, :, 1] = 1, 1
+        w[2][0] = torch.eye(64).to(torch.int8)
+        scales = tuple(v[None].to(DEV) for v in (gate, u, torch.ones(64)))
+        g64 = gate.double()
+    out = lib.moe_layer_few_tokens(x.to(DEV), torch.zeros(T, 1, dtype=torch.int32, device=DEV),
+                                   torch.ones(T, 1, device=DEV), *(v.to(DEV) for v in w),
+                                   scales=scales).cpu().double()
+    want = (torch.nn.functional.silu(g64) * u.double()).expand(T, -1)
+    assert torch.isfinite(out).all()
+    assert bool(((out - want).abs() <= want.abs() * (2 ** -8 + 2 ** -16) + 88 * 3 * 2.0 ** -126).all())

@@ -330,7 +330,7 @@ gmm_i8_kernel(const __grid_constant__ CUtensorMap mapW0, const __grid_constant__
         for (int j = 0; j < subs; ++j) umma_commit_pair_warp(t_full((it + j) & 1), 3);
         it += subs;
       }
-      umma_commit_pair_warp(drain, 1);
+      umma_commit_pair_warp(drain, 3);  // the last signal to either CTA
       mbar_wait_warp(drain, 0, abort_flag, p.status, false);
     }
   } else if (warp >= kAWarp) {
@@ -534,6 +534,8 @@ gmm_i8_kernel(const __grid_constant__ CUtensorMap mapW0, const __grid_constant__
       if (part * 32 >= rows) give_back();  // (it had none)
      }
     }
+    // the peer too ends after the leader's last signal, when a wait ran out as well
+    if (rank != 0 && warp == kEpiWarp) mbar_wait_warp(drain, 0, abort_flag, p.status, false);
   }
   tc_fence_before();
   __syncthreads();

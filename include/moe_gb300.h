@@ -433,8 +433,8 @@ int moe_gate_up_wgrad(const void* dgu, const void* permuted, int dtype,
  *                  = scale * p_id(k) / sum_k' p_id(k'),  renormalize != 0
  * in fp32 whatever the logits' dtype (both scores grow with the logit, so
  * the selection compares the logits themselves, without rounding).  A
- * selection by anything else (a score plus a bias, groups of experts first) is
- * not made here; experts that such a step rules out are masked.
+ * selection by a score plus a bias, or among the best groups of experts, is
+ * moe_router_topk_grouped's; experts that any other step rules out are masked.
  *   -inf masks an expert: its weight is 0 (it is selected, lowest index
  *   first, only when fewer than K logits are above -inf; a row of -inf alone
  *   gets ids 0..K-1 and weights 0).  +inf counts as the largest finite
@@ -461,6 +461,35 @@ int moe_router_topk_grad(const float* grad_probs, const void* logits, int dtype,
                          const int32_t* expert_ids, int T, int E, int K, int scoring,
                          int renormalize, float scale, void* grad_logits, int32_t* dev_status,
                          cudaStream_t stream);
+
+/* moe_router_topk_grouped: the selection with a bias for each expert (as
+ * balancing without a loss keeps it) and among the best groups of experts:
+ *   s_j = p_j above (softmax over all E, or sigmoid)
+ *   c_j = s_j + bias[j]                   bias [E] float32, or NULL: zeros
+ *   v_g = the sum of the group_top (1 or 2) largest c_j of group g, the experts
+ *         [g E / num_groups, (g + 1) E / num_groups)
+ *   the top_groups groups of largest v_g are kept (ties to the lowest group)
+ *   expert_ids[t]  = the K largest c_j of the kept groups in descending order,
+ *                    ties to the lowest index
+ *   probs[t, k]    = scale * s_id(k), or scale * s_id(k) / sum_k' s_id(k'):
+ *                    weights know the bias only through the selection
+ * The selection is that of c in 64 bits (fp32 decides where it can); with no
+ * bias, and group_top 1 or all groups kept, it compares the logits.
+ *   A logit of -inf takes its expert out, and so does a bias of -inf: among
+ *   groups, one with fewer experts left (of group_top) comes after those with
+ *   more, and an expert that is out is selected, lowest index first, only when
+ *   the kept groups have fewer than K others.  Its weight is 0 where the logit
+ *   is -inf.  +inf and NaN logits as above; a bias that is +inf or NaN counts
+ *   as -inf and sets MOE_ERR_INVALID_ARG in dev_status.
+ * 1 <= K <= 16, E <= 1024, num_groups <= 32 divides E, group_top <= E / num_groups,
+ * K <= top_groups * E / num_groups; a group has at most 32 experts for each of
+ * the 32 / P lanes that hold it, P = num_groups rounded up to a power of two.
+ * The gradient of the logits is moe_router_topk_grad's, from the same logits
+ * and expert_ids; the selection, and with it the bias, has none. */
+int moe_router_topk_grouped(const void* logits, int dtype, const float* bias, int T, int E, int K,
+                            int num_groups, int top_groups, int group_top, int scoring,
+                            int renormalize, float scale, int32_t* expert_ids, float* probs,
+                            int32_t* dev_status, cudaStream_t stream);
 
 /* ---- 8-bit rows and products ----------------------------------------------
  *

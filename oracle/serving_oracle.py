@@ -11,7 +11,7 @@ from __future__ import annotations
 
 import numpy as np
 
-__all__ = ["router_topk", "router_topk_grad", "quantize_rows", "linear_int8",
+__all__ = ["router_topk", "router_topk_grouped", "router_topk_grad", "quantize_rows", "linear_int8",
            "gate_up_swiglu_int8", "layer_few_tokens"]
 
 F32_MAX = float(np.finfo(np.float32).max)
@@ -70,6 +70,33 @@ def router_topk(logits, K: int, scoring: str, renormalize: bool, scale: float):
     probs = np.zeros((T, K))
     for t in range(T):
         ids[t] = np.argsort(-l[t], kind="stable")[:K]
+        probs[t] = scale * _selected(l[t], ids[t], scoring, renormalize)
+    return ids, probs
+
+
+def router_topk_grouped(logits, bias, K: int, groups: int, top_groups: int, group_top: int,
+                        scoring: str, renormalize: bool, scale: float):
+    """(expert_ids, probs): the K largest scores plus bias of the top_groups best
+    groups, weights from the scores alone.  With no bias, and no sums of two that
+    matter, the logits are compared."""
+    l = _clean(logits)
+    T, E = l.shape
+    size = E // groups
+    b = np.zeros(E) if bias is None else np.asarray(bias, dtype=np.float64)
+    b = np.where(b < np.inf, b, -np.inf)  # +inf, NaN: out
+    plain = bias is None and (group_top == 1 or top_groups == groups)
+    ids = np.zeros((T, K), dtype=np.int64)
+    probs = np.zeros((T, K))
+    for t in range(T):
+        c = l[t] if plain else np.where(np.isneginf(l[t]), -np.inf, _scores(l[t], scoring) + b)
+        value = []
+        for g in range(groups):
+            best = np.sort(c[g * size:(g + 1) * size])[::-1][:group_top]
+            left = best[~np.isneginf(best)]
+            value.append((-len(left), -left.sum() if len(left) else 0.0, g))
+        kept = [g for _, _, g in sorted(value)[:top_groups]]
+        among = sorted((-c[j], j) for g in kept for j in range(g * size, (g + 1) * size))
+        ids[t] = [j for _, j in among[:K]]
         probs[t] = scale * _selected(l[t], ids[t], scoring, renormalize)
     return ids, probs
 

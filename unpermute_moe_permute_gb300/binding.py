@@ -91,6 +91,7 @@ _SIGNATURES = {
     "moe_gate_up_wgrad_gather": ([_P, _P, _I, _P, _I, _P, _I, _I, _I, _I, _P, _P, _P, _P], _I),
     "moe_router_topk": ([_P, _I, _I, _I, _I, _I, _I, _F, _P, _P, _P, _P], _I),
     "moe_router_topk_grad": ([_P, _P, _I, _P, _I, _I, _I, _I, _I, _F, _P, _P, _P], _I),
+    "moe_router_topk_grouped": ([_P, _I, _P, _I, _I, _I, _I, _I, _I, _I, _I, _F, _P, _P, _P, _P], _I),
     "moe_quantize_rows": ([_P, _I, _P, _I, _I, _I, _I, _P, _P, _P], _I),
     "moe_gate_up_swiglu_int8": ([_P, _P, _P, _I, _I, _I, _I, _P, _P, _P, _P, _P, _P, _P], _I),
     "moe_down_proj_int8": ([_P, _P, _P, _I, _I, _I, _I, _P, _P, _P, _I, _P, _P], _I),
@@ -624,6 +625,33 @@ def moe_router_topk(logits, K: int, *, scoring: str = "softmax", renormalize: bo
         _shape(probs, (T, K), "probs")
     _call("moe_router_topk", _ptr(logits), _dtype(logits), T, E, K, _scoring(scoring),
           int(renormalize), scale, _ptr(expert_ids), _ptr(probs), _ptr(dev_status), _stream())
+    return expert_ids, probs
+
+
+def moe_router_topk_grouped(logits, K: int, *, bias=None, num_groups: int = 1, top_groups: int = 1,
+                            group_top: int = 1, scoring: str = "sigmoid", renormalize: bool = True,
+                            scale: float = 1.0, expert_ids=None, probs=None, dev_status=None):
+    """moe_router_topk with a bias [E] float32 added to the scores that select,
+    among the top_groups best of num_groups groups of experts (a group's value
+    is the sum of its group_top largest).  The gradient of the logits is
+    moe_router_topk_grad's."""
+    T, E = logits.shape
+    if bias is not None:
+        _check(bias, torch.float32, "bias")
+        _shape(bias, (E,), "bias")
+    if expert_ids is None:
+        expert_ids = _empty2(T, K, torch.int32, logits)
+    else:
+        _check(expert_ids, torch.int32, "expert_ids")
+        _shape(expert_ids, (T, K), "expert_ids")
+    if probs is None:
+        probs = _empty2(T, K, torch.float32, logits)
+    else:
+        _check(probs, torch.float32, "probs")
+        _shape(probs, (T, K), "probs")
+    _call("moe_router_topk_grouped", _ptr(logits), _dtype(logits), _ptr(bias), T, E, K, num_groups,
+          top_groups, group_top, _scoring(scoring), int(renormalize), scale, _ptr(expert_ids),
+          _ptr(probs), _ptr(dev_status), _stream())
     return expert_ids, probs
 
 

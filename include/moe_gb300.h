@@ -534,6 +534,56 @@ int moe_down_proj_int8(const int8_t* act_q, const float* row_scale, const int32_
                        const float* down_scale, void* expanded, int out_dtype,
                        int32_t* dev_status, cudaStream_t stream);
 
+/* ---- 4-bit weights --------------------------------------------------------
+ *
+ * A weight matrix [rows, cols] (cols: inputs) in 4 bits with a scale for each
+ * `group` (32, 64 or 128) inputs of a row:
+ *   w[n, k] = q[n, k] * scale[k / group, n],      q in [-8, 7]
+ *   W_q    [rows, cols / 2] bytes, q as two's complement.  Eight consecutive
+ *          inputs make four bytes: (0, 2), (4, 6), (1, 3), (5, 7), the first of
+ *          each in the lower four bits.  (As a little-endian word: inputs 0, 2, 4,
+ *          6, 1, 3, 5, 7 from the lowest bits up.)
+ *   scale  [cols / group, rows] bf16
+ * with E of them one after the other.  cols a multiple of 64 and of group, rows
+ * and cols at most MOE_INT4_MAX_SIZE, E at most 65535.
+ *
+ * moe_quantize_weights_int4: W [E, rows, cols] MOE_F32 or MOE_BF16;
+ *   scale = max |w| of the group times 1 / 7 in fp32, rounded to five
+ *           significant bits (ties to even; under 2^-126 to a multiple of 2^-130)
+ *   q     = the fp32 quotient w / scale, rounded to nearest even (and into
+ *           [-8, 7], which only scales under 2^-126 need)
+ * Five bits of scale leave q * scale a bf16 value.  A group of zeros (or whose
+ * scale rounds to 0): scale 0, q 0; a group that holds a NaN or an infinity:
+ * scale NaN, q 0, so that every product with it is NaN.
+ * moe_dequantize_weights_int4: W [E, rows, cols] bf16 = q * scale, rounded to
+ *   nearest even: the weights that the products below multiply with.
+ *
+ * The products, for the rows of expert e (expert_offsets as above;
+ * expert_offsets NULL with E = 1: one matrix for all N rows):
+ *   y[i, n] = sum_k x[i, k] * bf16(q[e, n, k] * scale[e, k / group, n])
+ * (exact for scales of at most five significant bits; others are multiplied by
+ * weights rounded to bf16, 2^-9 of themselves at most).
+ * moe_gate_up_swiglu_int4: act [N, I] bf16 = silu(g) * u with g, u such
+ *   products of permuted [N, H] bf16, W_gate_q and W_up_q [E, I, H / 2],
+ *   gate_scale and up_scale [E, H / group, I].
+ * moe_down_proj_int4: expanded [N, H] MOE_BF16 or MOE_F32 (out_dtype) from act
+ *   [N, I] bf16, W_down_q [E, H, I / 2], down_scale [E, I / group, H].
+ * fp32 sums, one rounding to the output's dtype.  H and I multiples of 64, at
+ * most MOE_INT4_MAX_SIZE; N at most MOE_INT8_MAX_ROWS; rows >= expert_offsets[E]
+ * are not touched.  Every pointer is 16-byte aligned. */
+#define MOE_INT4_MAX_SIZE 0x100000
+int moe_quantize_weights_int4(const void* W, int dtype, int E, int rows, int cols, int group,
+                              uint8_t* W_q, void* scale, cudaStream_t stream);
+int moe_dequantize_weights_int4(const uint8_t* W_q, const void* scale, int E, int rows, int cols,
+                                int group, void* W, cudaStream_t stream);
+int moe_gate_up_swiglu_int4(const void* permuted, const int32_t* expert_offsets, int N, int H, int I,
+                            int E, int group, const uint8_t* W_gate_q, const void* gate_scale,
+                            const uint8_t* W_up_q, const void* up_scale, void* act,
+                            int32_t* dev_status, cudaStream_t stream);
+int moe_down_proj_int4(const void* act, const int32_t* expert_offsets, int N, int H, int I, int E,
+                       int group, const uint8_t* W_down_q, const void* down_scale, void* expanded,
+                       int out_dtype, int32_t* dev_status, cudaStream_t stream);
+
 /* ---- the whole layer for a few tokens --------------------------------------
  *
  *   act[t, k] = silu(W_gate[e] x_t) * (W_up[e] x_t),       e = expert_ids[t, k]

@@ -11,8 +11,11 @@ from __future__ import annotations
 
 import numpy as np
 
+from .moe_oracle import round_to_bf16
+
 __all__ = ["router_topk", "router_topk_grouped", "router_topk_grad", "quantize_rows", "linear_int8",
-           "gate_up_swiglu_int8", "layer_few_tokens"]
+           "gate_up_swiglu_int8", "quantize_weights_int4", "pack_int4", "unpack_int4", "weights_int4",
+           "linear_float", "layer_few_tokens"]
 
 F32_MAX = float(np.finfo(np.float32).max)
 
@@ -169,6 +172,66 @@ def gate_up_swiglu_int8(q, row_scale, offsets, Wg_q, gs, Wu_q, us):
     g = linear_int8(q, row_scale, offsets, Wg_q, gs)
     u = linear_int8(q, row_scale, offsets, Wu_q, us)
     return _silu(g) * u, g, u
+
+
+# The inputs of eight whose values a byte holds: (lower, upper four bits).
+_BYTES = ((0, 2), (4, 6), (1, 3), (5, 7))
+
+
+def pack_int4(q):
+    """Whole numbers [..., k] in [-8, 7] as bytes [..., k / 2]."""
+    q = np.asarray(q) & 15
+    p = np.zeros(q.shape[:-1] + (q.shape[-1] // 2,), dtype=np.uint8)
+    for i, (a, b) in enumerate(_BYTES):
+        p[..., i::4] = q[..., a::8] | q[..., b::8] << 4
+    return p
+
+
+def unpack_int4(p):
+    """The whole numbers of pack_int4's bytes."""
+    p = np.asarray(p).astype(np.int64)
+    q = np.zeros(p.shape[:-1] + (p.shape[-1] * 2,), dtype=np.int64)
+    for i, (a, b) in enumerate(_BYTES):
+        q[..., a::8], q[..., b::8] = p[..., i::4] & 15, p[..., i::4] >> 4
+    return np.where(q > 7, q - 16, q)
+
+
+def quantize_weights_int4(W, group: int):
+    """(q [E, n, k] whole numbers, scale [E, k / group, n] float32) of weights
+    [E, n, k] in float32 arithmetic, as the format defines it."""
+    W = np.asarray(W, dtype=np.float32)
+    w = W.reshape(W.shape[:2] + (-1, group))
+    top = np.max(np.abs(w), axis=-1)
+    bad = ~np.all(np.isfinite(w), axis=-1)
+    top = np.where(bad, np.float32(0), top)
+    t = top * np.float32(1.0 / 7.0)
+    # five significant bits, ties to even, and at least 2^-130
+    step = np.ldexp(1.0, np.maximum(np.frexp(t.astype(np.float64))[1] - 5, -130))
+    scale = (np.rint(t.astype(np.float64) / step) * step).astype(np.float32)
+    s = np.where(scale > 0, scale, np.float32(1))[..., None]
+    with np.errstate(invalid="ignore", over="ignore"):
+        q = np.clip(np.rint((w / s).astype(np.float32)), -8, 7)
+    q = np.where((scale > 0)[..., None], q, 0).astype(np.int64)
+    scale = np.where(bad, np.float32(np.nan), scale)
+    return q.reshape(W.shape), np.swapaxes(scale, 1, 2)
+
+
+def weights_int4(W_q, scale):
+    """The weights [E, n, k] that bytes and scales [E, k / group, n] stand for:
+    q * scale rounded to bf16."""
+    q = unpack_int4(W_q)
+    s = np.swapaxes(np.asarray(scale, dtype=np.float64), 1, 2)
+    return round_to_bf16(q * np.repeat(s, q.shape[2] // s.shape[2], axis=2))
+
+
+def linear_float(x, offsets, W):
+    """y[i] = W[e] x[i] for the rows i of expert e."""
+    x = np.asarray(x, dtype=np.float64)
+    y = np.zeros((x.shape[0], W.shape[1]))
+    for e in range(W.shape[0]):
+        lo, hi = int(offsets[e]), int(offsets[e + 1])
+        y[lo:hi] = x[lo:hi] @ np.asarray(W[e], dtype=np.float64).T
+    return y
 
 
 def layer_few_tokens(x, ids, probs, Wg, Wu, Wd, E: int, num_special: int = 0, mask=None,

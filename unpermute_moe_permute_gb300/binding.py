@@ -95,6 +95,10 @@ _SIGNATURES = {
     "moe_quantize_rows": ([_P, _I, _P, _I, _I, _I, _I, _P, _P, _P], _I),
     "moe_gate_up_swiglu_int8": ([_P, _P, _P, _I, _I, _I, _I, _P, _P, _P, _P, _P, _P, _P], _I),
     "moe_down_proj_int8": ([_P, _P, _P, _I, _I, _I, _I, _P, _P, _P, _I, _P, _P], _I),
+    "moe_quantize_weights_int4": ([_P, _I, _I, _I, _I, _I, _P, _P, _P], _I),
+    "moe_dequantize_weights_int4": ([_P, _P, _I, _I, _I, _I, _P, _P], _I),
+    "moe_gate_up_swiglu_int4": ([_P, _P, _I, _I, _I, _I, _I, _P, _P, _P, _P, _P, _P, _P], _I),
+    "moe_down_proj_int4": ([_P, _P, _I, _I, _I, _I, _I, _P, _P, _P, _I, _P, _P], _I),
     "moe_layer_few_tokens_workspace_size": ([_I, _I, _I, _I, _I], _SZ),
     "moe_layer_few_tokens": ([_P, _P, _P, _I, _I, _I, _I, _I, _I, _P, _I, _I, _P, _P, _P, _P, _P,
                               _P, _P, _P, _P, _SZ, _P, _P], _I),
@@ -764,6 +768,123 @@ def moe_down_proj_int8(act_q, row_scale, expert_offsets, W_down_q, down_scale, *
     _call("moe_down_proj_int8", _ptr(act_q), _ptr(row_scale), _ptr(expert_offsets), N, H, I, E,
           _ptr(W_down_q), _ptr(down_scale), _ptr(expanded), _dtype(expanded), _ptr(dev_status),
           _stream())
+    return expanded
+
+
+# ---------------------------------------------------------------- 4-bit weights
+
+_INT4_GROUPS = (32, 64, 128)
+
+
+def _int4_group(scale: torch.Tensor, cols: int, name: str) -> int:
+    """The group that a scale [..., cols / group, rows] is for."""
+    groups = scale.shape[-2] if scale.dim() > 1 else 0
+    if groups == 0 or cols % groups or cols // groups not in _INT4_GROUPS:
+        raise ValueError(f"{name} must have {' or '.join(f'{cols} / {g}' for g in _INT4_GROUPS)} groups, "
+                         f"got {groups}")
+    return cols // groups
+
+
+def moe_quantize_weights_int4(W, group: int = 128, *, W_q=None, scale=None):
+    """Weights W [E, rows, cols] or [rows, cols] (float32 or bfloat16) in 4 bits
+    with a scale for each group (32, 64 or 128) of a row's inputs: (W_q [...,
+    rows, cols / 2] uint8, scale [..., cols / group, rows] bfloat16)."""
+    if W.dim() not in (2, 3):
+        raise ValueError(f"W must have two or three dimensions, got {W.dim()}")
+    if group not in _INT4_GROUPS:
+        raise ValueError(f"group must be one of {_INT4_GROUPS}, got {group}")
+    rows, cols = W.shape[-2:]
+    if cols % 64 or cols % group:
+        raise ValueError(f"the inputs of a row ({cols}) must be a multiple of 64 and of the group ({group})")
+    lead = tuple(W.shape[:-2])
+    if W_q is None:
+        W_q = torch.empty(lead + (rows, cols // 2), dtype=torch.uint8, device=W.device)
+    else:
+        _check(W_q, torch.uint8, "W_q")
+        _shape(W_q, lead + (rows, cols // 2), "W_q")
+    if scale is None:
+        scale = torch.empty(lead + (cols // group, rows), dtype=torch.bfloat16, device=W.device)
+    else:
+        _check(scale, torch.bfloat16, "scale")
+        _shape(scale, lead + (cols // group, rows), "scale")
+    _call("moe_quantize_weights_int4", _ptr(W), _dtype(W), lead[0] if lead else 1, rows, cols, group,
+          _ptr(W_q), _ptr(scale), _stream())
+    return W_q, scale
+
+
+def moe_dequantize_weights_int4(W_q, scale, *, W=None):
+    """The bfloat16 weights that W_q and scale of moe_quantize_weights_int4
+    stand for."""
+    if W_q.dim() not in (2, 3):
+        raise ValueError(f"W_q must have two or three dimensions, got {W_q.dim()}")
+    rows, cols = W_q.shape[-2], 2 * W_q.shape[-1]
+    lead = tuple(W_q.shape[:-2])
+    group = _int4_group(scale, cols, "scale")
+    _check(W_q, torch.uint8, "W_q")
+    _check(scale, torch.bfloat16, "scale")
+    _shape(scale, lead + (cols // group, rows), "scale")
+    if W is None:
+        W = torch.empty(lead + (rows, cols), dtype=torch.bfloat16, device=W_q.device)
+    else:
+        _check(W, torch.bfloat16, "W")
+        _shape(W, lead + (rows, cols), "W")
+    _call("moe_dequantize_weights_int4", _ptr(W_q), _ptr(scale), lead[0] if lead else 1, rows, cols,
+          group, _ptr(W), _stream())
+    return W
+
+
+def moe_gate_up_swiglu_int4(permuted, expert_offsets, W_gate_q, gate_scale, W_up_q, up_scale, *,
+                            act=None, dev_status=None):
+    """act [N, I] bf16 = silu(g) * u, g and u the products of the expert-major
+    rows permuted [N, H] (bf16) with 4-bit weights [E, I, H / 2] (uint8, scales
+    [E, H / group, I] bf16)."""
+    N, H = permuted.shape
+    E, I, _ = W_gate_q.shape
+    if act is None:
+        act = _empty2(N, I, torch.bfloat16, permuted)
+    u8, bf16 = torch.uint8, torch.bfloat16
+    group = _int4_group(gate_scale, H, "gate_scale")
+    if not (permuted.dtype is bf16 and W_gate_q.dtype is u8 and W_up_q.dtype is u8
+            and gate_scale.dtype is bf16 and up_scale.dtype is bf16 and act.dtype is bf16
+            and W_gate_q.shape == W_up_q.shape == (E, I, H // 2)
+            and gate_scale.shape == up_scale.shape == (E, H // group, I) and act.shape == (N, I)):
+        for t, dt, shape, n in ((permuted, bf16, (N, H), "permuted"),
+                                (W_gate_q, u8, (E, I, H // 2), "W_gate_q"),
+                                (W_up_q, u8, (E, I, H // 2), "W_up_q"),
+                                (gate_scale, bf16, (E, H // group, I), "gate_scale"),
+                                (up_scale, bf16, (E, H // group, I), "up_scale"),
+                                (act, bf16, (N, I), "act")):
+            _check(t, dt, n)
+            _shape(t, shape, n)
+    _offsets(expert_offsets, E)
+    _call("moe_gate_up_swiglu_int4", _ptr(permuted), _ptr(expert_offsets), N, H, I, E, group,
+          _ptr(W_gate_q), _ptr(gate_scale), _ptr(W_up_q), _ptr(up_scale), _ptr(act),
+          _ptr(dev_status), _stream())
+    return act
+
+
+def moe_down_proj_int4(act, expert_offsets, W_down_q, down_scale, *, expanded=None,
+                       out_dtype=torch.bfloat16, dev_status=None):
+    """expanded [N, H] (bfloat16 or float32) = the product of act [N, I] (bf16)
+    with each expert's 4-bit W_down_q [E, H, I / 2] (scale [E, I / group, H]).
+    expert_offsets None: one matrix (E = 1) for all rows."""
+    N, I = act.shape
+    E, H, _ = W_down_q.shape
+    if expanded is None:
+        expanded = _empty2(N, H, out_dtype, act)
+    else:
+        _shape(expanded, (N, H), "expanded")
+    u8, bf16 = torch.uint8, torch.bfloat16
+    group = _int4_group(down_scale, I, "down_scale")
+    if not (act.dtype is bf16 and W_down_q.dtype is u8 and down_scale.dtype is bf16
+            and W_down_q.shape == (E, H, I // 2) and down_scale.shape == (E, I // group, H)):
+        for t, dt, shape, n in ((act, bf16, (N, I), "act"), (W_down_q, u8, (E, H, I // 2), "W_down_q"),
+                                (down_scale, bf16, (E, I // group, H), "down_scale")):
+            _check(t, dt, n)
+            _shape(t, shape, n)
+    _offsets(expert_offsets, E)
+    _call("moe_down_proj_int4", _ptr(act), _ptr(expert_offsets), N, H, I, E, group, _ptr(W_down_q),
+          _ptr(down_scale), _ptr(expanded), _dtype(expanded), _ptr(dev_status), _stream())
     return expanded
 
 

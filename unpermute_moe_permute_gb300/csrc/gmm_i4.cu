@@ -1,0 +1,450 @@
+// Grouped products of bf16 rows and 4-bit expert weights with a scale for each
+// group of inputs, on tcgen05 tensor cores (sm_103a).
+//
+//   y[i, n] = sum_k x[i, k] bf16(q[e, n, k] s[e, k / group, n])
+//
+// The weights are expanded to bf16 on chip (exact for scales of five
+// significant bits) and multiplied by kind::f16 with fp32 sums.  DRAM and L2 see
+// half a byte a weight.  What bounds it is the tensor pipe when experts have rows
+// enough, else the stream of weights and the integer pipe that expands them:
+//
+//   * the weights are the A operand (M = channels): 64 bytes of a row, 128 of
+//     its inputs, go through registers into tensor memory;
+//   * the rows are the B operand (N = rows), as they come by TMA: up to 320 of an
+//     expert in two accumulators of 160, so the weights of an expert of up to 320
+//     rows are loaded and expanded once;
+//   * CTA pairs (cta_group::2): 256 channels per MMA, each CTA expands its own
+//     128 channels and holds half of the rows;
+//   * the scales come by TMA beside the weights they belong to, a column of 128
+//     channels for each group (zeros past the ends, as the weights).
+//
+// Warps: 1 TMA producer, 1 MMA issuer (in the leading CTA), epilogue warps, and
+// groups of four warps that expand the 128-deep stages in turn.  The barrier of a
+// loaded stage is waited for by the expanding group alone: what its arrival tells
+// the MMA issuer about tensor memory holds for the rows of the stage too, which
+// had landed before.
+#include <limits.h>
+
+#include "common.cuh"
+#include "int4.cuh"
+#include "pair_tile.cuh"
+#include "per_device.h"
+#include "tma_host.cuh"
+
+namespace moe {
+namespace tc {
+namespace {
+
+template <int SUB, int GROUPS, int EPI, int STAGES>
+struct I4Cfg {
+  static constexpr int kSub = SUB, kGroups = GROUPS, kEpi = EPI, kStages = STAGES;
+  static constexpr int kRowTile = 2 * kSub;             // B rows of a tile
+  static constexpr uint32_t kB = kRowTile / 2 * 256;    // B bytes of a stage: two 64-deep halves
+  static constexpr uint32_t kA = 128 * 64;              // 4-bit A bytes of a stage
+  static constexpr uint32_t kS = 4 * 128 * 2;           // scales of a stage, at most
+  static constexpr uint32_t kACol = 2 * kSub;           // tensor memory: accumulators, A buffers
+  static constexpr int kAWarp = 2 + kEpi;
+  static constexpr int kThreads = (kAWarp + 4 * kGroups) * 32;
+  // (A barrier for each slot and group, so that a group meets every phase of its
+  // barriers: with 3 groups and 4 slots it would else see every third.)
+  static constexpr int lcm(int a, int b) {
+    int m = a;
+    while (m % b) m += a;
+    return m;
+  }
+  static constexpr int kFulls = lcm(kStages, kGroups);
+  static constexpr int kBars = kFulls + kStages + 2 * kGroups + 4 + 1;
+  static constexpr uint32_t kStageWarp = 2048;  // epilogue staging of a warp
+  static constexpr uint32_t kStage = kStages * (kB + kA + kS);
+  static constexpr uint32_t kCtrl = kStage + kEpi * kStageWarp;
+  static constexpr uint32_t kHolder = kCtrl + 8 * kBars;
+  static constexpr uint32_t kTable = kHolder + 8;  // prefix, offsets, scan scratch
+  static constexpr uint32_t kSmem = kTable + 2 * (kMaxExperts + 1) * 4 + 32 * 4 + 1024;
+  static_assert(kSmem <= 232448, "more shared memory than one CTA may use");
+  static_assert(kACol + kGroups * 64 <= 512, "more tensor memory than there is");
+  static_assert(kGroups <= kStages && kSub % 32 == 0 && kFulls % kGroups == 0, "geometry");
+};
+
+using I4Many = I4Cfg<160, 3, 8, 4>;
+using I4Few = I4Cfg<32, 4, 4, 10>;
+
+struct I4Params {
+  const int32_t* off;
+  void* out;
+  int32_t* status;
+  int N, E, Kd, Nout;
+  int ch_tiles;    // channel tiles per expert: of 256 (128 for gate/up)
+  int per;         // scale groups of a 128-deep stage: 4, 2, 1
+};
+
+template <typename C, bool kSwiglu, typename O>
+__global__ void __launch_bounds__(C::kThreads, 1)
+gmm_i4_kernel(const __grid_constant__ CUtensorMap mapW0, const __grid_constant__ CUtensorMap mapW1,
+              const __grid_constant__ CUtensorMap mapS0, const __grid_constant__ CUtensorMap mapS1,
+              const __grid_constant__ CUtensorMap mapX32, const __grid_constant__ CUtensorMap mapX16,
+              const I4Params p) {
+  constexpr int kSub = C::kSub, kGroups = C::kGroups, kStages = C::kStages, kEpi = C::kEpi;
+  constexpr int kAWarp = C::kAWarp, kFulls = C::kFulls;
+  constexpr uint32_t kA = C::kA, kB = C::kB, kS = C::kS, kACol = C::kACol;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  uint8_t* g = smem_raw + (base - raw);
+  const uint32_t sB = base, sA = sB + kStages * kB, sS = sA + kStages * kA;
+  const uint32_t bars = base + C::kCtrl;
+  auto q_full = [&](int i) { return bars + 8u * i; };  // i: stage mod kFulls
+  auto q_empty = [&](int s) { return bars + 8u * (kFulls + s); };
+  const uint32_t bars2 = bars + 8u * (kFulls + kStages);
+  auto c_full = [&](int b) { return bars2 + 8u * b; };
+  auto c_empty = [&](int b) { return bars2 + 8u * (kGroups + b); };
+  auto t_full = [&](int a) { return bars2 + 8u * (2 * kGroups + a); };
+  auto t_empty = [&](int a) { return bars2 + 8u * (2 * kGroups + 2 + a); };
+  const uint32_t drain = bars2 + 8u * (2 * kGroups + 4);
+  uint32_t* holder = reinterpret_cast<uint32_t*>(g + C::kHolder);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(g + C::kHolder + 4);
+  int32_t* prefix = reinterpret_cast<int32_t*>(g + C::kTable);
+  int32_t* offs = prefix + (kMaxExperts + 1);
+  int32_t* scratch = offs + (kMaxExperts + 1);
+  const int warp = (int)uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kFulls; ++i) mbar_init(q_full(i), 1);
+    for (int s = 0; s < kStages; ++s) mbar_init(q_empty(s), 4 + 1);  // an expanding group, the MMAs
+    for (int b = 0; b < kGroups; ++b) {
+      mbar_init(c_full(b), 2 * 4);  // the leader's: a group of both CTAs
+      mbar_init(c_empty(b), 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(t_full(a), 1);
+      mbar_init(t_empty(a), 2 * kEpi);  // the epilogue warps of both CTAs
+    }
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    mbar_fence_init();
+  }
+  if (warp == kTmaWarp && lane == 0) {
+    tma_prefetch_desc(&mapW0);
+    tma_prefetch_desc(&mapS0);
+    if constexpr (kSwiglu) {
+      tma_prefetch_desc(&mapW1);
+      tma_prefetch_desc(&mapS1);
+    }
+    tma_prefetch_desc(&mapX32);
+    tma_prefetch_desc(&mapX16);
+  }
+  // Both CTAs are present and their barriers initialised before either uses
+  // the other's (the pair's tensor-memory allocation included).
+  cluster_sync_all();
+  if (warp == kMmaWarp) {
+    tmem_alloc_pair(smem_u32(holder), 512);
+    tmem_relinquish_pair();
+  }
+  // From here on what earlier kernels of the stream wrote is read: the part
+  // above may overlap the end of the one before.
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  stage_offsets(p.off, p.E, p.N, offs, scratch);
+  build_tile_prefix(offs, p.E, p.N, C::kRowTile, prefix, scratch);  // ends with __syncthreads
+  const int total = prefix[p.E] * p.ch_tiles;
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *holder;
+  const int rank = (int)cluster_ctarank();
+  const int t0 = (int)cluster_id_x(), dt = (int)cluster_count_x();
+  const int stages = (p.Kd + 127) / 128;
+
+  if (warp == kTmaWarp) {  // the whole warp, one lane elected for each copy
+    const uint32_t ub = uniform(base);
+    const int per = (int)uniform(p.per);
+    int s = 0, f = 0, n = 0;  // slot, its barrier, stages so far
+    uint32_t ph = 0;
+    bool run = true;
+    for (int t = t0; run && t < total; t += dt) {
+      const PairTile x = pair_tile<kSwiglu, kSub>(t, p, prefix, offs, rank);
+      const int nh0 = (int)uniform(x.n) / 2, nh1 = (int)uniform(x.n1) / 2, e = (int)uniform(x.e);
+      const int ch0 = (int)uniform(x.ch0), r0 = (int)uniform(x.row0);
+      const uint32_t tx = kA + (uint32_t)per * 256u + (uint32_t)(nh0 + nh1) * 256u;
+      for (int k = 0; k < stages; ++k) {
+        run = mbar_wait_warp(q_empty(s), ph ^ 1u, abort_flag, p.status);
+        if (!run) break;
+        mbar_arrive_expect_tx_warp(q_full(f), tx);
+        const uint32_t a = ub + kStages * kB + s * kA, sc = ub + kStages * (kB + kA) + s * kS;
+        tma_load_3d_warp(a, &mapW0, q_full(f), k * 64, ch0, e);
+        tma_load_3d_warp(sc, &mapS0, q_full(f), ch0, k * per, e);
+        if constexpr (kSwiglu) {
+          tma_load_3d_warp(a + kA / 2, &mapW1, q_full(f), k * 64, ch0, e);
+          tma_load_3d_warp(sc + per * 128, &mapS1, q_full(f), ch0, k * per, e);
+        }
+        // this CTA's half of each accumulator's rows, one after the other
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint32_t b = ub + s * kB + h * (kB / 2);
+          for (int j = 0; j < 2; ++j) {
+            const int nh = j ? nh1 : nh0, rj = r0 + (j ? 2 * nh0 : 0) + rank * nh;
+            int r = 0;
+            for (; r + 32 <= nh; r += 32, b += 4096)
+              tma_load_2d_warp(b, &mapX32, q_full(f), k * 128 + h * 64, rj + r);
+            if (r < nh) {
+              tma_load_2d_warp(b, &mapX16, q_full(f), k * 128 + h * 64, rj + r);
+              b += 2048;
+            }
+          }
+        }
+        ++n;
+        if (++s == kStages) s = 0, ph ^= 1u;
+        if (++f == kFulls) f = 0;
+      }
+    }
+    // every copy has landed, and the leader's signals to the slots have come,
+    // before the CTA may exit
+    for (int i = max(0, n - kStages); i < n; ++i) {
+      mbar_wait_warp(q_full(i % kFulls), (uint32_t)(i / kFulls) & 1u, abort_flag, p.status, false);
+      if (run) run = mbar_wait_warp(q_empty(i % kStages), (uint32_t)(i / kStages) & 1u, abort_flag, p.status);
+    }
+  } else if (warp == kMmaWarp) {
+    if (rank == 0) {  // the whole warp, one lane elected for each MMA
+      const uint64_t bdesc0 = desc_sw128(uniform(sB), 16, 1024);
+      const uint32_t tm = uniform(tmem);
+      int b = 0, s = 0, it = 0;
+      uint32_t ph = 0;
+      bool run = true;
+      for (int t = t0; run && t < total; t += dt) {
+        const PairTile x = pair_tile<kSwiglu, kSub>(t, p, prefix, offs, rank);
+        const int n = (int)uniform(x.n), subs = (int)uniform(x.subs);
+        const uint32_t idesc = idesc_bf16_f32(256, n, false, false);
+        const uint32_t idesc1 = idesc_bf16_f32(256, (int)uniform(x.n1), false, false);
+        // accumulators it, it + 1 (mod 2), as they become free
+        for (int j = 0; run && j < subs; ++j)
+          run = __all_sync(0xffffffffu, mbar_wait<true>(t_empty((it + j) & 1), (((it + j) >> 1) & 1) ^ 1u,
+                                                        abort_flag, p.status));
+        if (!run) break;
+        tc_fence_after();
+        const uint32_t d0 = tm + (it & 1) * kSub, d1 = tm + ((it + 1) & 1) * kSub;
+        const uint32_t sub1 = (uint32_t)n * 64u >> 4;  // the second's rows in shared memory
+        uint32_t accum = 0u;
+        for (int k = 0; k < stages; ++k) {
+          run = mbar_wait_warp(c_full(b), ph, abort_flag, p.status);
+          if (!run) break;
+          tc_fence_after();
+          const uint64_t bd = bdesc0 + (uint64_t)s * (kB >> 4);
+          const uint32_t a = tm + kACol + b * 64;
+          // (past the end of Kd both operands are zeros)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const uint64_t bh = bd + h * (kB >> 5);
+            umma_f16_ta_k64_warp<true>(d0, a + h * 32, bh, idesc, accum);
+            if (subs > 1) umma_f16_ta_k64_warp<true>(d1, a + h * 32, bh + sub1, idesc1, accum);
+            accum = 1u;
+          }
+          umma_commit_pair_warp(c_empty(b), 3);
+          umma_commit_pair_warp(q_empty(s), 3);
+          if (++b == kGroups) b = 0, ph ^= 1u;
+          if (++s == kStages) s = 0;
+        }
+        if (!run) break;
+        for (int j = 0; j < subs; ++j) umma_commit_pair_warp(t_full((it + j) & 1), 3);
+        it += subs;
+      }
+      umma_commit_pair_warp(drain, 3);  // the last signal to either CTA
+      mbar_wait_warp(drain, 0, abort_flag, p.status, false);
+    }
+  } else if (warp >= kAWarp) {
+    // ---- expand: a lane takes one 64-byte row of the stage ----
+    const int grp = (warp - kAWarp) >> 2, quarter = warp & 3;  // quarter: tensor-memory lanes
+    // Row of this lane: gate/up stages hold 64 gate rows, then 64 up rows; a warp
+    // takes 16 of each, so that gate and up of a channel meet in lanes i and
+    // i + 16 of one epilogue warp.
+    const int row = kSwiglu ? (lane < 16 ? quarter * 16 + lane : 48 + quarter * 16 + lane) : quarter * 32 + lane;
+    // Chunk c of row r sits at chunk c ^ (r / 2 & 3) (64-byte swizzle).
+    const uint32_t src0 = sA + row * 64 + (((row >> 1) & 3) << 4);
+    // its scales: 64 (128) channels of the first group, of the second, ...
+    const int up = kSwiglu && row >= 64;
+    const uint32_t sc0 = sS + (up ? p.per * 128 : 0) + (row - (up ? 64 : 0)) * 2;
+    constexpr uint32_t kScaleRow = kSwiglu ? 128 : 256;
+    const int shift = p.per == 4 ? 0 : p.per == 2 ? 1 : 2;  // chunks of 32 inputs to groups
+    const uint32_t dst = tmem + kACol + grp * 64 + ((uint32_t)(quarter * 32) << 16);
+    const uint32_t full_of_leader = mapa_shared(c_full(grp), 0);
+    int s = grp, f = grp, n0 = 0;  // slot, its barrier; stages before this tile (mod kGroups)
+    uint32_t ph = 0, bph = 0;
+    bool run = true;
+    for (int t = t0; run && t < total; t += dt) {
+      for (int k = (grp - n0 + kGroups) % kGroups; k < stages; k += kGroups) {
+        run = mbar_wait_warp(q_full(f), ph, abort_flag, p.status);
+        if (!run) break;
+        uint4 v[4];
+        uint32_t sc[4], r[32];
+        const uint32_t src = src0 + s * kA, scs = sc0 + s * kS;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          v[j] = ld_shared_v4(src ^ (j << 4));
+          sc[j] = ld_shared_u16(scs + (j >> shift) * kScaleRow) * 0x10001u;
+        }
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          expand_int4(v[j].x, sc[j], r + 16 * j);
+          expand_int4(v[j].y, sc[j], r + 16 * j + 4);
+          expand_int4(v[j].z, sc[j], r + 16 * j + 8);
+          expand_int4(v[j].w, sc[j], r + 16 * j + 12);
+        }
+        // The row and its scales are read: the fence orders these reads before
+        // the copy that refills the slot.
+        fence_proxy_async_smem();
+        mbar_arrive_warp(q_empty(s));
+        run = mbar_wait_warp(c_empty(grp), bph ^ 1u, abort_flag, p.status);
+        if (!run) break;
+        tc_fence_after();
+        tmem_st_32x32b_x32(dst, r);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          expand_int4(v[j + 2].x, sc[j + 2], r + 16 * j);
+          expand_int4(v[j + 2].y, sc[j + 2], r + 16 * j + 4);
+          expand_int4(v[j + 2].z, sc[j + 2], r + 16 * j + 8);
+          expand_int4(v[j + 2].w, sc[j + 2], r + 16 * j + 12);
+        }
+        tmem_st_32x32b_x32(dst + 32, r);
+        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive_cluster_warp(full_of_leader);
+        bph ^= 1u;
+        s += kGroups;
+        if (s >= kStages) s -= kStages;
+        f += kGroups;
+        if (f >= kFulls) f -= kFulls, ph ^= 1u;
+      }
+      n0 = (n0 + stages) % kGroups;
+    }
+    // the last of the leader's signals to this CTA's barriers has arrived
+    if (run) mbar_wait_warp(c_empty(grp), bph ^ 1u, abort_flag, p.status);
+  } else {
+    pair_epilogue<C, kSwiglu, false, O>(p, base, g, tmem, warp, lane, rank, t0, dt, total, t_full(0), t_empty(0),
+                                        abort_flag, prefix, offs);
+    // the peer too ends after the leader's last signal, when a wait ran out as well
+    if (rank != 0 && warp == kEpiWarp) mbar_wait_warp(drain, 0, abort_flag, p.status, false);
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync_all();  // no CTA leaves while its peer may still signal its barriers
+  if (warp == kMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem, 512);
+  }
+}
+
+template <typename C, bool kSwiglu, typename O>
+int launch_cfg(const CUtensorMap (&m)[6], const I4Params& p, cudaStream_t s) {
+  static PerDevice smem_allowed, resident_pairs;
+  int dev = -1;
+  if (cudaGetDevice(&dev) != cudaSuccess) return MOE_ERR_CUDA;
+  const int allowed = smem_allowed.get(dev, [] {
+    return cudaFuncSetAttribute(gmm_i4_kernel<C, kSwiglu, O>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                (int)C::kSmem) == cudaSuccess;
+  });
+  if (!allowed) return MOE_ERR_CUDA;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = 2;
+  at[0].val.clusterDim.y = 1;
+  at[0].val.clusterDim.z = 1;
+  // one persistent CTA per SM, as many whole pairs as can be resident
+  cfg.gridDim = dim3(sm_count() / 2 * 2, 1, 1);
+  cfg.blockDim = dim3(C::kThreads, 1, 1);
+  cfg.dynamicSmemBytes = C::kSmem;
+  cfg.stream = s;
+  at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 2;
+  const int pairs = resident_pairs.get(dev, [&] {
+    int n = 0;
+    const bool known = cudaOccupancyMaxActiveClusters(&n, gmm_i4_kernel<C, kSwiglu, O>, &cfg) == cudaSuccess;
+    (void)cudaGetLastError();
+    return known && n > 0 ? n : INT_MAX;
+  });
+  if (pairs < (int)cfg.gridDim.x / 2) cfg.gridDim.x = 2 * pairs;
+  if (cudaLaunchKernelEx(&cfg, gmm_i4_kernel<C, kSwiglu, O>, m[0], m[1], m[2], m[3], m[4], m[5], p) != cudaSuccess) {
+    (void)cudaGetLastError();
+    return MOE_ERR_CUDA;
+  }
+  count_launches(1);
+  return MOE_OK;
+}
+
+// Rows per expert, on average, up to which the few-rows form runs (the routing
+// itself is not known on the host).
+constexpr long long few_rows(bool swiglu) { return swiglu ? 64 : 48; }
+
+template <bool kSwiglu, typename O>
+int launch_i4(const void* x, const uint8_t* W0, const void* s0, const uint8_t* W1, const void* s1,
+              const int32_t* off, int N, int Kd, int Nout, int E, int group, O* out, int32_t* status,
+              cudaStream_t s) {
+  if (int rc = device_ok()) return rc;
+  CUtensorMap m[6];
+  const int per = 128 / group;
+  const uint32_t ch = kSwiglu ? 64 : 128;
+  const uint64_t dw[3] = {(uint64_t)Kd / 2, (uint64_t)Nout, (uint64_t)E};
+  const uint32_t bw[3] = {64, ch, 1};
+  const uint64_t ds[3] = {(uint64_t)Nout, (uint64_t)(Kd / group), (uint64_t)E};
+  const uint32_t bs[3] = {ch, (uint32_t)per, 1};
+  const uint64_t dx[2] = {(uint64_t)Kd, (uint64_t)N};
+  const uint32_t b32[2] = {64, 32}, b16[2] = {64, 16};
+  if (!make_map(&m[0], W0, 1, 3, dw, bw, CU_TENSOR_MAP_SWIZZLE_64B) ||
+      !make_map(&m[1], kSwiglu ? W1 : W0, 1, 3, dw, bw, CU_TENSOR_MAP_SWIZZLE_64B) ||
+      !make_map(&m[2], s0, 2, 3, ds, bs, CU_TENSOR_MAP_SWIZZLE_NONE) ||
+      !make_map(&m[3], kSwiglu ? s1 : s0, 2, 3, ds, bs, CU_TENSOR_MAP_SWIZZLE_NONE) ||
+      !make_map_sw128(&m[4], x, 2, 2, dx, b32) || !make_map_sw128(&m[5], x, 2, 2, dx, b16))
+    return MOE_ERR_CUDA;
+  const int chs = kSwiglu ? 128 : 256;
+  const I4Params p{off, out, status, N, E, Kd, Nout, (Nout + chs - 1) / chs, per};
+  return (long long)N <= few_rows(kSwiglu) * E ? launch_cfg<I4Few, kSwiglu, O>(m, p, s)
+                                               : launch_cfg<I4Many, kSwiglu, O>(m, p, s);
+}
+
+int check_i4(const void* x, const int32_t* off, int N, int H, int I, int E, int Kd, int group) {
+  if (N < 0 || H <= 0 || I <= 0 || E <= 0) return MOE_ERR_INVALID_ARG;
+  if (group != 32 && group != 64 && group != 128) return MOE_ERR_INVALID_ARG;
+  if (E > kMaxExperts) return MOE_ERR_SHAPE;
+  if (off == nullptr && E != 1) return MOE_ERR_INVALID_ARG;
+  if (H % 64 || I % 64 || Kd % group || H > MOE_INT4_MAX_SIZE || I > MOE_INT4_MAX_SIZE) return MOE_ERR_SHAPE;
+  if (N > MOE_INT8_MAX_ROWS) return MOE_ERR_SHAPE;  // (rows and row tiles added up stay within 31 bits)
+  if (N > 0 && (!x || !aligned16(x))) return MOE_ERR_INVALID_ARG;
+  return MOE_OK;
+}
+
+}  // namespace
+}  // namespace tc
+}  // namespace moe
+
+using namespace moe;
+using namespace moe::tc;
+
+extern "C" int moe_gate_up_swiglu_int4(const void* permuted, const int32_t* expert_offsets, int N, int H,
+                                       int I, int E, int group, const uint8_t* W_gate_q,
+                                       const void* gate_scale, const uint8_t* W_up_q,
+                                       const void* up_scale, void* act, int32_t* dev_status,
+                                       cudaStream_t stream) {
+  if (int rc = check_i4(permuted, expert_offsets, N, H, I, E, H, group)) return rc;
+  if (N == 0) return MOE_OK;
+  const void* ptrs[] = {W_gate_q, gate_scale, W_up_q, up_scale, act};
+  for (const void* p : ptrs)
+    if (!p || !aligned16(p)) return MOE_ERR_INVALID_ARG;
+  return launch_i4<true>(permuted, W_gate_q, gate_scale, W_up_q, up_scale, expert_offsets, N, H, I, E, group,
+                         static_cast<__nv_bfloat16*>(act), dev_status, stream);
+}
+
+extern "C" int moe_down_proj_int4(const void* act, const int32_t* expert_offsets, int N, int H, int I,
+                                  int E, int group, const uint8_t* W_down_q, const void* down_scale,
+                                  void* expanded, int out_dtype, int32_t* dev_status,
+                                  cudaStream_t stream) {
+  if (int rc = check_i4(act, expert_offsets, N, H, I, E, I, group)) return rc;
+  if (out_dtype != MOE_F32 && out_dtype != MOE_BF16) return MOE_ERR_INVALID_ARG;
+  if (N == 0) return MOE_OK;
+  const void* ptrs[] = {W_down_q, down_scale, expanded};
+  for (const void* p : ptrs)
+    if (!p || !aligned16(p)) return MOE_ERR_INVALID_ARG;
+  if (out_dtype == MOE_F32)
+    return launch_i4<false>(act, W_down_q, down_scale, nullptr, nullptr, expert_offsets, N, I, H, E, group,
+                            static_cast<float*>(expanded), dev_status, stream);
+  return launch_i4<false>(act, W_down_q, down_scale, nullptr, nullptr, expert_offsets, N, I, H, E, group,
+                          static_cast<__nv_bfloat16*>(expanded), dev_status, stream);
+}

@@ -43,8 +43,7 @@
 
 #include "common.cuh"
 #include "per_device.h"
-#include "sched.cuh"
-#include "tc_warp.cuh"
+#include "pair_tile.cuh"
 #include "tma_host.cuh"
 
 namespace moe {
@@ -93,7 +92,6 @@ struct I8Cfg {
 // to more warps that expand weights.
 using I8Many = I8Cfg<160, 2, 8, 3>;
 using I8Few = I8Cfg<32, 4, 4, 8>;
-constexpr int kTmaWarp = 0, kMmaWarp = 1, kEpiWarp = 2;
 
 struct I8Params {
   const int32_t* off;
@@ -103,36 +101,6 @@ struct I8Params {
   int N, E, Kd, Nout;
   int ch_tiles;  // channel tiles per expert: of 256 (128 for gate/up)
 };
-
-struct I8Tile {
-  int e, row0, hi;  // expert, first row, end of the tile's rows
-  int subs;         // accumulators the rows take: 1 or 2
-  int n, n1;        // MMA N of the first and of the second: multiples of 32
-  int ch0;          // first channel of this CTA
-  __device__ __forceinline__ int b_rows() const { return (n + n1) / 2; }  // of this CTA
-};
-
-// Tile t is channel tile (t mod ch_tiles) of row tile t / ch_tiles; the rows
-// of an expert are split evenly over its ceil(rows / (2 kSub)) row tiles, the rows
-// of a row tile over its accumulators in steps of 32.
-template <bool kSwiglu, int kSub>
-__device__ __forceinline__ I8Tile i8_tile(int t, const I8Params& p, const int32_t* prefix,
-                                          const int32_t* offs, int rank) {
-  I8Tile x;
-  const int g = t / p.ch_tiles;
-  x.e = find_expert(prefix, p.E, g);
-  const ExpertRows r = expert_rows(offs, x.e, p.N);
-  const int parts = prefix[x.e + 1] - prefix[x.e], i = g - prefix[x.e];
-  const int per = (r.hi - r.lo + parts - 1) / parts;
-  x.row0 = r.lo + i * per;
-  x.hi = min(r.hi, x.row0 + per);
-  x.subs = per > kSub ? 2 : 1;
-  const int steps = (per + 31) >> 5;  // (pairs take N in steps of 32)
-  x.n = x.subs == 2 ? ((steps + 1) >> 1) * 32 : steps * 32;
-  x.n1 = steps * 32 - x.n;
-  x.ch0 = (t - g * p.ch_tiles) * (kSwiglu ? 128 : 256) + rank * (kSwiglu ? 64 : 128);
-  return x;
-}
 
 // Four signed bytes as fp16: 0x64uu is 1024 + u with u = byte + 128, less
 // 1152.  The pairs are bytes (0, 2) and (1, 3): both operands are expanded
@@ -151,32 +119,6 @@ __device__ __forceinline__ void expand16(uint4 v, uint32_t* r) {
   expand4(v.y, r[2], r[3]);
   expand4(v.z, r[4], r[5]);
   expand4(v.w, r[6], r[7]);
-}
-
-__device__ __forceinline__ void st_shared_u32(uint32_t addr, uint32_t v) {
-  asm volatile("st.shared.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
-}
-
-// Two products at once.
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-  float2 r;
-  asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
-      "mul.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
-      : "=f"(r.x), "=f"(r.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-  return r;
-}
-__device__ __forceinline__ float2 mul2(uint32_t x, uint32_t y, float s, float t) {
-  return mul2(make_float2(__uint_as_float(x), __uint_as_float(y)), make_float2(s, t));
-}
-
-// x / (1 + e^-x): the approximate exponential and reciprocal in the forms that
-// flush what is below 2^-126 (half the instructions of those that keep it).
-__device__ __forceinline__ float silu(float x) {
-  float e, r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(x * -1.4426950408889634f));
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
-  return x * r;
 }
 
 template <typename C, bool kSwiglu, typename O>
@@ -258,7 +200,7 @@ gmm_i8_kernel(const __grid_constant__ CUtensorMap mapW0, const __grid_constant__
     uint32_t ph = 0;
     bool run = true;
     for (int t = t0; run && t < total; t += dt) {
-      const I8Tile x = i8_tile<kSwiglu, kSub>(t, p, prefix, offs, rank);
+      const PairTile x = pair_tile<kSwiglu, kSub>(t, p, prefix, offs, rank);
       const int nh0 = (int)uniform(x.n) / 2, nh1 = (int)uniform(x.n1) / 2, e = (int)uniform(x.e);
       const int ch0 = (int)uniform(x.ch0), r0 = (int)uniform(x.row0);
       const uint32_t tx = kA8 + (uint32_t)(nh0 + nh1) * 128u;
@@ -297,7 +239,7 @@ gmm_i8_kernel(const __grid_constant__ CUtensorMap mapW0, const __grid_constant__
       uint32_t ph = 0;
       bool run = true;
       for (int t = t0; run && t < total; t += dt) {
-        const I8Tile x = i8_tile<kSwiglu, kSub>(t, p, prefix, offs, rank);
+        const PairTile x = pair_tile<kSwiglu, kSub>(t, p, prefix, offs, rank);
         const int n = (int)uniform(x.n), subs = (int)uniform(x.subs);
         const uint32_t idesc = idesc_f16_f32(256, n), idesc1 = idesc_f16_f32(256, (int)uniform(x.n1));
         // accumulators it, it + 1 (mod 2), as they become free
@@ -358,7 +300,7 @@ gmm_i8_kernel(const __grid_constant__ CUtensorMap mapW0, const __grid_constant__
     bool run = true;
     for (int t = t0; run && t < total; t += dt) {
       // B rows past the tile's own are not expanded (the MMA does not read them)
-      const bool any = is_a || rg * 32 < i8_tile<kSwiglu, kSub>(t, p, prefix, offs, rank).b_rows();
+      const bool any = is_a || rg * 32 < pair_tile<kSwiglu, kSub>(t, p, prefix, offs, rank).b_rows();
       for (int k = (grp - n0 + kGroups) % kGroups; k < stages; k += kGroups) {
         run = mbar_wait_warp(q_full(f), ph, abort_flag, p.status);
         if (!run) break;
@@ -411,129 +353,8 @@ gmm_i8_kernel(const __grid_constant__ CUtensorMap mapW0, const __grid_constant__
     // the last of the leader's signals to this CTA's barriers has arrived
     if (run) mbar_wait_warp(c_empty(grp), bph ^ 1u, abort_flag, p.status);
   } else {
-    // ---- epilogue: lanes are channels, accumulator columns are rows ----
-    // The warps of a quarter take pieces of 32 columns in turn.  A piece
-    // is scaled, turned through the warp's staging rows and written in 16-byte
-    // chunks of 8 channels.
-    const int quarter = warp & 3, part = (warp - kEpiWarp) >> 2;
-    constexpr int kCh = kSwiglu ? 16 : 32;  // channels per warp
-    O* out = static_cast<O*>(p.out);
-    const uint32_t stage_u = base + C::kStage + (uint32_t)(warp - kEpiWarp) * C::kStageWarp;
-    float* scale = reinterpret_cast<float*>(g + C::kStage + (warp - kEpiWarp) * C::kStageWarp + 2048);
-    const int ch_l = kSwiglu ? quarter * 16 + (lane & 15) : quarter * 32 + lane;
-    int it = 0;
-    bool run = true;
-    for (int t = t0; run && t < total; t += dt) {
-     const I8Tile x = i8_tile<kSwiglu, kSub>(t, p, prefix, offs, rank);
-     const int ch = x.ch0 + ch_l;
-     const float cs = ch >= p.Nout ? 0.f
-                                   : ((kSwiglu && lane >= 16) ? p.s1 : p.s0)[(size_t)x.e * p.Nout + ch];
-     // row scales of the first pieces (the second accumulator's ahead of its
-     // wait, which is short)
-     const int r_first = x.row0 + part * 32 + lane, r_second = r_first + x.n;
-     const float rs_first = part * 32 + lane < min(x.hi - x.row0, x.n) ? p.rs[r_first] : 0.f;
-     const float rs_second = x.subs > 1 && r_second < x.hi ? p.rs[r_second] : 0.f;
-     for (int sub = 0; sub < x.subs; ++sub, ++it) {
-      const int acc = it & 1, row0 = x.row0 + sub * x.n;
-      const int rows = min(x.hi - row0, sub ? x.n1 : x.n);
-      float rs = sub ? rs_second : rs_first;
-      run = mbar_wait_warp(t_full(acc), (it >> 1) & 1, abort_flag, p.status);
-      if (!run) break;
-      tc_fence_after();
-      const uint32_t d = tmem + acc * kSub + ((uint32_t)(quarter * 32) << 16);
-      auto give_back = [&]() {
-        tc_fence_before();
-        mbar_arrive_cluster_warp(mapa_shared(t_empty(acc), 0));
-      };
-      for (int c0 = part * 32; c0 < rows; c0 += 8 * kEpi) {
-        uint32_t v[32];
-        tmem_ld_32x32b_x32(d + c0, v);
-        scale[lane] = rs;
-        rs = c0 + 8 * kEpi + lane < rows ? p.rs[row0 + c0 + 8 * kEpi + lane] : 0.f;
-        __syncwarp();
-        tmem_ld_wait();
-        if (c0 + 8 * kEpi >= rows) give_back();  // the warp's last piece is in registers
-        if constexpr (sizeof(O) == 4) {
-          // fp32: staging rows of 32 channels, 16 columns at a time
-#pragma unroll
-          for (int p0 = 0; p0 < 32; p0 += 16) {
-#pragma unroll
-            for (int j = 0; j < 16; ++j)
-              st_shared_u32(stage_u + lane * 4 + j * 128,
-                            __float_as_uint(__uint_as_float(v[p0 + j]) * cs * scale[p0 + j]));
-            __syncwarp();
-            const int wr = lane >> 3, wch = x.ch0 + quarter * kCh + (lane & 7) * 4;
-            if (wch < p.Nout) {
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const int r = c0 + p0 + wr + i * 4;
-                if (r < rows)
-                  st_v4(out + (size_t)(row0 + r) * p.Nout + wch, ld_shared_v4(stage_u + lane * 16 + i * 512));
-              }
-            }
-            __syncwarp();
-          }
-        } else {
-          // bf16: words of two rows of a channel; [pair][channel]
-          uint32_t w[kSwiglu ? 8 : 16];
-          if constexpr (kSwiglu) {
-            // lanes 0-15 hold gate, 16-31 up of the same channels: the lower
-            // half takes the even rows, the upper half the odd ones
-            const bool up = lane >= 16;
-            float y[16];
-#pragma unroll
-            for (int j = 0; j < 32; j += 2) {
-              const float2 f = mul2(mul2(v[j], v[j + 1], cs, cs), *reinterpret_cast<const float2*>(scale + j));
-              const float got = __shfl_xor_sync(0xffffffffu, up ? f.x : f.y, 16);
-              const float gate = up ? got : f.x, u = up ? f.y : got;
-              y[j / 2] = silu(gate) * u;
-            }
-#pragma unroll
-            for (int j = 0; j < 8; ++j) w[j] = VecTraits<__nv_bfloat16>::pack2(y[2 * j], y[2 * j + 1]);
-            // word row 2j + up: rows 4j + up and 4j + up + 2
-            const uint32_t st = stage_u + (lane & 15) * 4 + (up ? 64 : 0);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) st_shared_u32(st + j * 128, w[j]);
-          } else {
-#pragma unroll
-            for (int j = 0; j < 16; ++j) {
-              const float2 f =
-                  mul2(mul2(v[2 * j], v[2 * j + 1], cs, cs), *reinterpret_cast<const float2*>(scale + 2 * j));
-              w[j] = VecTraits<__nv_bfloat16>::pack2(f.x, f.y);
-            }
-#pragma unroll
-            for (int j = 0; j < 16; ++j) st_shared_u32(stage_u + lane * 4 + j * 128, w[j]);
-          }
-          __syncwarp();
-          // a lane takes 8 channels of a pair of rows: 32 bytes of words (the
-          // halves in an order that keeps 8 lanes on distinct banks)
-          constexpr int G = kCh / 8, kWordRow = kCh * 4;
-#pragma unroll
-          for (int i = 0; i < 16 * G / 32; ++i) {
-            const int pr = (lane + 32 * i) / G, gch = (lane + 32 * i) % G;
-            const uint32_t src = stage_u + pr * kWordRow + gch * 32;
-            const uint32_t first = kSwiglu ? ((pr >> 1) & 1) * 16 : (pr & 1) * 16;
-            const uint4 m0 = ld_shared_v4(src + first), m1 = ld_shared_v4(src + (first ^ 16));
-            const uint4 a = first ? m1 : m0, b = first ? m0 : m1;
-            const uint4 lo = make_uint4(__byte_perm(a.x, a.y, 0x5410), __byte_perm(a.z, a.w, 0x5410),
-                                        __byte_perm(b.x, b.y, 0x5410), __byte_perm(b.z, b.w, 0x5410));
-            const uint4 hi = make_uint4(__byte_perm(a.x, a.y, 0x7632), __byte_perm(a.z, a.w, 0x7632),
-                                        __byte_perm(b.x, b.y, 0x7632), __byte_perm(b.z, b.w, 0x7632));
-            const int r = c0 + (kSwiglu ? (pr >> 1) * 4 + (pr & 1) : 2 * pr);
-            constexpr int dr = kSwiglu ? 2 : 1;
-            const int wch = x.ch0 + quarter * kCh + gch * 8;
-            if (wch < p.Nout) {
-              O* dst = out + (size_t)(row0 + r) * p.Nout + wch;
-              if (r < rows) st_v4(dst, lo);
-              if (r + dr < rows) st_v4(dst + (size_t)dr * p.Nout, hi);
-            }
-          }
-          __syncwarp();
-        }
-      }
-      if (part * 32 >= rows) give_back();  // (it had none)
-     }
-    }
+    pair_epilogue<C, kSwiglu, true, O>(p, base, g, tmem, warp, lane, rank, t0, dt, total, t_full(0), t_empty(0),
+                                       abort_flag, prefix, offs);
     // the peer too ends after the leader's last signal, when a wait ran out as well
     if (rank != 0 && warp == kEpiWarp) mbar_wait_warp(drain, 0, abort_flag, p.status, false);
   }

@@ -624,6 +624,20 @@ int moe_layer_few_tokens(const void* tokens, const int32_t* expert_ids, const fl
                          void* workspace, size_t workspace_bytes, int32_t* dev_status,
                          cudaStream_t stream);
 
+/* moe_layer_few_tokens over 4-bit weights: W_gate_q, W_up_q [E, I, H / 2] with
+ * gate_scale, up_scale [E, H / group, I], W_down_q [E, H, I / 2] with down_scale
+ * [E, I / down_group, H] (bf16), the weights being bf16(q * scale) as in the
+ * products above.  H a multiple of group, I of down_group; the scales 16-byte
+ * aligned.  All else as there, the workspace's size too. */
+int moe_layer_few_tokens_int4(const void* tokens, const int32_t* expert_ids, const float* probs,
+                              int T, int H, int K, int I, int E, int num_special,
+                              const uint8_t* active_mask, int mask_dims, int group, int down_group,
+                              const uint8_t* W_gate_q, const void* gate_scale,
+                              const uint8_t* W_up_q, const void* up_scale, const uint8_t* W_down_q,
+                              const void* down_scale, const void* shared_x, void* out,
+                              void* workspace, size_t workspace_bytes, int32_t* dev_status,
+                              cudaStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

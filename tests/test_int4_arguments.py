@@ -133,3 +133,52 @@ def test_binding_refuses_wrong_tensors(built_lib):  # noqa: F811
         b.moe_dequantize_weights_int4(w, s[:, :3])
     with pytest.raises(ValueError, match="scale must be"):
         b.moe_dequantize_weights_int4(w, s.float())
+
+
+FEW = [
+    # tokens, ids, probs, T, H, K, I, E, specials, mask, mask_dims, group, down_group, Wg, gs, Wu, us, Wd, ds, shared,
+    # out, workspace, bytes, status, stream
+    ((P, P, P, 4, 128, 2, 64, 8, 0, None, 0, 16, 64, P, P, P, P, P, P, None, P, P, 1 << 30, None, None), INV),
+    ((P, P, P, 4, 128, 2, 64, 8, 0, None, 0, 64, 0, P, P, P, P, P, P, None, P, P, 1 << 30, None, None), INV),
+    ((P, P, P, 4, 192, 2, 64, 8, 0, None, 0, 128, 64, P, P, P, P, P, P, None, P, P, 1 << 30, None, None), SHAPE),
+    ((P, P, P, 4, 128, 2, 64, 8, 0, None, 0, 64, 128, P, P, P, P, P, P, None, P, P, 1 << 30, None, None), SHAPE),
+    ((P, P, P, 65, 128, 2, 64, 8, 0, None, 0, 64, 64, P, P, P, P, P, P, None, P, P, 1 << 30, None, None), SHAPE),
+    ((P, P, P, 4, 96, 2, 64, 8, 0, None, 0, 32, 64, P, P, P, P, P, P, None, P, P, 1 << 30, None, None), SHAPE),
+    ((P, P, P, 4, 0x100040, 2, 64, 8, 0, None, 0, 64, 64, P, P, P, P, P, P, None, P, P, 1 << 30, None, None), SHAPE),
+    ((P, P, P, 4, 128, 17, 64, 64, 0, None, 0, 64, 64, P, P, P, P, P, P, None, P, P, 1 << 30, None, None), SHAPE),
+    ((P, P, P, 4, 128, 2, 64, 8, 0, P, 3, 64, 64, P, P, P, P, P, P, None, P, P, 1 << 30, None, None), INV),
+    ((P, P, P, 4, 128, 2, 64, 8, 0, None, 0, 64, 64, P, None, P, P, P, P, None, P, P, 1 << 30, None, None), INV),
+    ((P, P, P, 4, 128, 2, 64, 8, 0, None, 0, 64, 64, P, P, P, U, P, P, None, P, P, 1 << 30, None, None), INV),
+    ((P, P, P, 4, 128, 2, 64, 8, 0, None, 0, 64, 64, P, P, P, P, U, P, None, P, P, 1 << 30, None, None), INV),
+    ((P, P, P, 4, 128, 2, 64, 8, 0, None, 0, 64, 64, P, P, P, P, P, P, U, P, P, 1 << 30, None, None), INV),
+    ((P, P, P, 4, 128, 2, 64, 8, 0, None, 0, 64, 64, P, P, P, P, P, P, None, P, P, 100, None, None), INV),
+    ((P, None, P, 4, 128, 2, 64, 8, 0, None, 0, 64, 64, P, P, P, P, P, P, None, P, P, 1 << 30, None, None), INV),
+]
+
+
+@pytest.mark.parametrize("args,status", FEW)
+def test_few_tokens_refused_on_the_host(built_lib, args, status):  # noqa: F811
+    from unpermute_moe_permute_gb300 import binding
+    assert binding.load_library(built_lib).moe_layer_few_tokens_int4(*args) == status
+
+
+def test_few_tokens_binding_refuses_wrong_tensors(built_lib):  # noqa: F811
+    from unpermute_moe_permute_gb300 import binding as b
+    bf16, u8 = torch.bfloat16, torch.uint8
+    x, ids, p = torch.zeros(3, 128, dtype=bf16), torch.zeros(3, 2, dtype=torch.int32), torch.zeros(3, 2)
+    w1, s1 = torch.zeros(4, 64, 64, dtype=u8), torch.zeros(4, 2, 64, dtype=bf16)
+    w2, s2 = torch.zeros(4, 128, 32, dtype=u8), torch.zeros(4, 2, 128, dtype=bf16)
+    ws = torch.zeros(1 << 20, dtype=u8)
+    call = lambda *a, **k: b.moe_layer_few_tokens_int4(*a, out=x, workspace=ws, **k)  # noqa: E731
+    for args, what in (((x, ids, p, w1, s1, w1, s1, w2, s2), "CUDA"),
+                       ((x.float(), ids, p, w1, s1, w1, s1, w2, s2), "tokens must be"),
+                       ((x, ids.long(), p, w1, s1, w1, s1, w2, s2), "expert_ids must be"),
+                       ((x, ids, p[:2], w1, s1, w1, s1, w2, s2), "probs must have shape"),
+                       ((x, ids, p, w1, s1, w1, s1[:, :1], w2, s2), "up_scale must have shape"),
+                       ((x, ids, p, w1, s1[:, :0], w1, s1, w2, s2), "gate_scale must have"),
+                       ((x, ids, p, w1, s1, w1, s1, w2[:, :64], s2), "W_down_q must have shape"),
+                       ((x, ids, p, w1, s1, w1, s1, w2, s2.float()), "down_scale must be")):
+        with pytest.raises(ValueError, match=what):
+            call(*args)
+    with pytest.raises(ValueError, match="shared_x must have shape"):
+        call(x, ids, p, w1, s1, w1, s1, w2, s2, shared_x=x[:2])

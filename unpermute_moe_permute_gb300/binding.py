@@ -102,6 +102,8 @@ _SIGNATURES = {
     "moe_layer_few_tokens_workspace_size": ([_I, _I, _I, _I, _I], _SZ),
     "moe_layer_few_tokens": ([_P, _P, _P, _I, _I, _I, _I, _I, _I, _P, _I, _I, _P, _P, _P, _P, _P,
                               _P, _P, _P, _P, _SZ, _P, _P], _I),
+    "moe_layer_few_tokens_int4": ([_P, _P, _P, _I, _I, _I, _I, _I, _I, _P, _I, _I, _I, _P, _P, _P,
+                                   _P, _P, _P, _P, _P, _P, _SZ, _P, _P], _I),
 }
 
 
@@ -936,5 +938,52 @@ def moe_layer_few_tokens(tokens, expert_ids, probs, W_gate, W_up, W_down, *, sca
           num_special, _ptr(mask), mask.dim() if mask is not None else 0,
           MOE_BF16 if scales is None else MOE_INT8, _ptr(W_gate), _ptr(W_up), _ptr(W_down),
           _ptr(gs), _ptr(us), _ptr(ds), _ptr(shared_x), _ptr(out), _ptr(workspace),
+          workspace.numel() * workspace.element_size(), _ptr(dev_status), _stream())
+    return out
+
+
+def moe_layer_few_tokens_int4(tokens, expert_ids, probs, W_gate_q, gate_scale, W_up_q, up_scale,
+                              W_down_q, down_scale, *, num_special: int = 0, active_mask=None,
+                              shared_x=None, out=None, workspace=None, dev_status=None):
+    """moe_layer_few_tokens over 4-bit weights: W_gate_q, W_up_q [E, I, H / 2] and
+    W_down_q [E, H, I / 2] uint8 with bf16 scales [E, H / group, I] and
+    [E, I / group, H], as moe_quantize_weights_int4 makes them."""
+    T, H = tokens.shape
+    K = expert_ids.shape[1]
+    E, I, _ = W_gate_q.shape
+    if out is None:
+        out = _empty2(T, H, torch.bfloat16, tokens)
+    if workspace is None:
+        ws = moe_layer_few_tokens_workspace_size(T, K, H, I, E)
+        workspace = _empty1(max(ws, 16), torch.uint8, tokens)
+    bf16, f32, u8 = torch.bfloat16, torch.float32, torch.uint8
+    group = _int4_group(gate_scale, H, "gate_scale")
+    down_group = _int4_group(down_scale, I, "down_scale")
+    if not (tokens.dtype is bf16 and out.dtype is bf16 and expert_ids.dtype is torch.int32
+            and probs.dtype is f32 and W_gate_q.dtype is u8 and W_up_q.dtype is u8
+            and W_down_q.dtype is u8 and gate_scale.dtype is bf16 and up_scale.dtype is bf16
+            and down_scale.dtype is bf16 and expert_ids.shape[0] == T
+            and probs.shape == expert_ids.shape and tokens.shape == out.shape
+            and W_gate_q.shape == W_up_q.shape == (E, I, H // 2) and W_down_q.shape == (E, H, I // 2)
+            and gate_scale.shape == up_scale.shape == (E, H // group, I)
+            and down_scale.shape == (E, I // down_group, H)
+            and (shared_x is None or (shared_x.dtype is bf16 and shared_x.shape == tokens.shape))):
+        for t, dt, shape, n in ((tokens, bf16, (T, H), "tokens"),
+                                (expert_ids, torch.int32, (T, K), "expert_ids"),
+                                (probs, f32, (T, K), "probs"),
+                                (W_gate_q, u8, (E, I, H // 2), "W_gate_q"),
+                                (W_up_q, u8, (E, I, H // 2), "W_up_q"),
+                                (W_down_q, u8, (E, H, I // 2), "W_down_q"),
+                                (gate_scale, bf16, (E, H // group, I), "gate_scale"),
+                                (up_scale, bf16, (E, H // group, I), "up_scale"),
+                                (down_scale, bf16, (E, I // down_group, H), "down_scale"),
+                                (shared_x, bf16, (T, H), "shared_x"), (out, bf16, (T, H), "out")):
+            _check(t, dt, n)
+            _shape(t, shape, n)
+    mask = _mask(active_mask, T, K) if active_mask is not None else None
+    _call("moe_layer_few_tokens_int4", _ptr(tokens), _ptr(expert_ids), _ptr(probs), T, H, K, I, E,
+          num_special, _ptr(mask), mask.dim() if mask is not None else 0, group, down_group,
+          _ptr(W_gate_q), _ptr(gate_scale), _ptr(W_up_q), _ptr(up_scale), _ptr(W_down_q),
+          _ptr(down_scale), _ptr(shared_x), _ptr(out), _ptr(workspace),
           workspace.numel() * workspace.element_size(), _ptr(dev_status), _stream())
     return out

@@ -25,7 +25,10 @@
 //     waits for an expert's activations to be complete.
 //   * 8-bit weights go from the ring through registers to tensor memory as
 //     bf16 (exact) and are the A operand there; the scale of a channel is a
-//     lane's own factor in the epilogue.
+//     lane's own factor in the epilogue;
+//   * 4-bit weights go the same way, 256 of k in a unit of the same bytes, each
+//     multiplied by its group's scale as it is expanded (exact for scales of five
+//     significant bits).  The scales come by TMA beside their weights.
 //
 // CTAs wait for one another, so the launch is cooperative (all of it
 // resident); every wait is bounded.  The counters are zeroed by the kernel
@@ -43,6 +46,7 @@
 #include <math.h>
 
 #include "common.cuh"
+#include "int4.cuh"
 #include "per_device.h"
 #include "tc_warp.cuh"
 #include "tma_host.cuh"
@@ -68,16 +72,22 @@ struct FewParams {
   uint32_t* count;             // ready[A], tiles of phase 1, tiles of phase 2, seen
   int32_t* status;
   int mask_dims, T, H, K, I, E, E_all, A_max;
+  int per1, per2;  // 4-bit weights: scale groups of a unit in each phase, 8, 4, 2
 };
 
-template <int NP, bool I8>
+template <int NP, int BITS>
 struct FewTraits {
-  static constexpr int k = I8 ? 128 : 64;                // k of a unit
+  static constexpr int k = 1024 / BITS;                  // k of a unit
   static constexpr uint32_t b_box = NP * 128;            // 64 k of the tokens
-  static constexpr bool can_narrow = NP == 16 && !I8;    // (see narrow below)
-  static constexpr uint32_t stage = 2 * kBox16 + (I8 || can_narrow ? 2 : 1) * b_box;
-  static constexpr int stages = (int)(212992 / stage);   // 5; 4 for N = 64 with 8-bit weights
-  static constexpr int threads = (I8 ? 20 : 12) * 32;
+  static constexpr bool can_narrow = NP == 16 && BITS == 16;  // (see narrow below)
+  static constexpr int b_boxes = can_narrow ? 2 : k / 64;
+  static constexpr uint32_t scales = 2 * kBox16 + b_boxes * b_box;  // 4-bit: two tiles' scales
+  static constexpr uint32_t stage = scales + (BITS == 4 ? 2 * 8 * 256 : 0);
+  static constexpr int stages = (int)(212992 / stage);   // 5; 4 for N = 64 with 8-bit weights; 4, 4, 3 with 4-bit
+  // Groups of eight warps that expand: with 4-bit weights two, which take the
+  // halves of a unit, where the registers allow it.
+  static constexpr int groups = BITS == 16 ? 0 : BITS == 4 && NP <= 32 ? 2 : 1;
+  static constexpr int threads = (12 + 8 * groups) * 32;
   static constexpr int bars = 2 * stages + 4 + 4 + 2;
   static constexpr uint32_t ctrl = stages * stage;
   static constexpr uint32_t holder = ctrl + 8 * bars;     // tensor memory, abort, flag, A
@@ -213,14 +223,18 @@ __device__ __forceinline__ void expand16_bf16(uint4 v, uint32_t* r) {
 // act for |g| < 88.
 __device__ __forceinline__ float swiglu(float g, float u) { return __fdividef(g, 1.f + __expf(-g)) * u; }
 
-template <int NP, bool I8>
-__global__ void __launch_bounds__(FewTraits<NP, I8>::threads, 1)
+template <int NP, int BITS>
+__global__ void __launch_bounds__(FewTraits<NP, BITS>::threads, 1)
 few_tokens_kernel(const __grid_constant__ CUtensorMap mapG, const __grid_constant__ CUtensorMap mapU,
                   const __grid_constant__ CUtensorMap mapG64, const __grid_constant__ CUtensorMap mapU64,
                   const __grid_constant__ CUtensorMap mapD, const __grid_constant__ CUtensorMap mapX,
-                  const __grid_constant__ CUtensorMap mapAct, const FewParams p) {
-  using TR = FewTraits<NP, I8>;
+                  const __grid_constant__ CUtensorMap mapAct, const __grid_constant__ CUtensorMap mapGS,
+                  const __grid_constant__ CUtensorMap mapUS, const __grid_constant__ CUtensorMap mapDS,
+                  const FewParams p) {
+  using TR = FewTraits<NP, BITS>;
+  constexpr bool I8 = BITS == 8, I4 = BITS == 4;
   constexpr int S = TR::stages;
+  constexpr int kWide = BITS == 16 ? 64 : 128;  // a unit's width in the weights' maps: 128 bytes
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = uniform((raw + 1023u) & ~1023u);
@@ -248,7 +262,7 @@ few_tokens_kernel(const __grid_constant__ CUtensorMap mapG, const __grid_constan
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
       mbar_init(full(s), 2);               // weights, tokens
-      mbar_init(empty(s), I8 ? 9 : 1);     // MMAs (and the expanding warps)
+      mbar_init(empty(s), 1 + 8 * TR::groups);  // MMAs (and the expanding warps)
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(t_full(a), 1);
@@ -269,6 +283,11 @@ few_tokens_kernel(const __grid_constant__ CUtensorMap mapG, const __grid_constan
     tma_prefetch_desc(&mapD);
     tma_prefetch_desc(&mapX);
     tma_prefetch_desc(&mapAct);
+    if (I4) {
+      tma_prefetch_desc(&mapGS);
+      tma_prefetch_desc(&mapUS);
+      tma_prefetch_desc(&mapDS);
+    }
   }
   if (warp == 1) {
     tmem_alloc(smem_u32(holder), 512);
@@ -327,7 +346,7 @@ few_tokens_kernel(const __grid_constant__ CUtensorMap mapG, const __grid_constan
   // against 6.7 TB/s for all.  For N = 16 also in tiles of 64 columns (gate and
   // up rows together one A operand of 128).  T=1 H=2048 E=128 K=8 I=768: 96
   // whole narrow tiles 32.8 us, 48 tiles in 152 equal runs 35.8 us (from cold).
-  const int wide1 = (p.I + 127) / 128, bytes1 = 256 * p.H * (I8 ? 1 : 2);  // of a wide tile
+  const int wide1 = (p.I + 127) / 128, bytes1 = 32 * p.H * BITS;  // of a wide tile
   const int t_split = A * wide1 * (bytes1 / 1024) / 6550 + 8;              // us
   const int t_whole = A * wide1 <= G ? bytes1 / 60000 : t_split + 1;
   const int t_narrow = TR::can_narrow && A * (p.I / 64) <= G ? bytes1 / 120000 : t_split + 1;
@@ -410,7 +429,11 @@ few_tokens_kernel(const __grid_constant__ CUtensorMap mapG, const __grid_constan
         run = mbar_wait_warp(empty(s), ph ^ 1u, abort_flag, p.status);
         if (!run) break;
         const uint32_t a = base + s * TR::stage;
-        mbar_arrive_expect_tx_warp(full(s), 2 * kBox16);
+        mbar_arrive_expect_tx_warp(full(s), 2 * kBox16 + (I4 ? 512u * p.per1 : 0u));
+        if constexpr (I4) {
+          tma_load_3d_warp(a + TR::scales, &mapGS, full(s), i0, k * p.per1, e);
+          tma_load_3d_warp(a + TR::scales + 256 * p.per1, &mapUS, full(s), i0, k * p.per1, e);
+        }
         if (narrow) {  // 64 rows of each, two k blocks
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
@@ -418,8 +441,8 @@ few_tokens_kernel(const __grid_constant__ CUtensorMap mapG, const __grid_constan
             tma_load_3d_warp(a + h * kBox16 + kBox16 / 2, &mapU64, full(s), k * k1 + h * TR::k, i0, e);
           }
         } else {
-          tma_load_3d_warp(a, &mapG, full(s), k * TR::k, i0, e);
-          tma_load_3d_warp(a + kBox16, &mapU, full(s), k * TR::k, i0, e);
+          tma_load_3d_warp(a, &mapG, full(s), k * kWide, i0, e);
+          tma_load_3d_warp(a + kBox16, &mapU, full(s), k * kWide, i0, e);
         }
         next();
       }
@@ -431,9 +454,13 @@ few_tokens_kernel(const __grid_constant__ CUtensorMap mapG, const __grid_constan
         run = mbar_wait_warp(empty(s), ph ^ 1u, abort_flag, p.status);
         if (!run) break;
         const uint32_t a = base + s * TR::stage;
-        mbar_arrive_expect_tx_warp(full(s), 2 * kBox16);
-        tma_load_3d_warp(a, &mapD, full(s), k * TR::k, h0, e);
-        tma_load_3d_warp(a + kBox16, &mapD, full(s), k * TR::k, h0 + 128, e);
+        mbar_arrive_expect_tx_warp(full(s), 2 * kBox16 + (I4 ? 512u * p.per2 : 0u));
+        if constexpr (I4) {
+          tma_load_3d_warp(a + TR::scales, &mapDS, full(s), h0, k * p.per2, e);
+          tma_load_3d_warp(a + TR::scales + 256 * p.per2, &mapDS, full(s), h0 + 128, k * p.per2, e);
+        }
+        tma_load_3d_warp(a, &mapD, full(s), k * kWide, h0, e);
+        tma_load_3d_warp(a + kBox16, &mapD, full(s), k * kWide, h0 + 128, e);
         next();
       }
       u += len;
@@ -454,10 +481,9 @@ few_tokens_kernel(const __grid_constant__ CUtensorMap mapG, const __grid_constan
      for (int k = u - tile * KB1; len > 0; ++k, --len) {
       if (!(run = mbar_wait_warp(empty(s), ph ^ 1u, abort_flag, p.status))) break;
       const uint32_t b = base + s * TR::stage + 2 * kBox16;
-      const bool both = I8 || narrow;  // 128 k
-      mbar_arrive_expect_tx_warp(full(s), both ? 2 * TR::b_box : TR::b_box);
-      tma_load_2d_warp(b, &mapX, full(s), k * k1, 0);
-      if (both) tma_load_2d_warp(b + TR::b_box, &mapX, full(s), k * k1 + 64, 0);
+      const int boxes = k1 / 64;
+      mbar_arrive_expect_tx_warp(full(s), boxes * TR::b_box);
+      for (int q = 0; q < boxes; ++q) tma_load_2d_warp(b + q * TR::b_box, &mapX, full(s), k * k1 + q * 64, 0);
       next();
      }
     }
@@ -474,9 +500,10 @@ few_tokens_kernel(const __grid_constant__ CUtensorMap mapG, const __grid_constan
       }
       if (!(run = mbar_wait_warp(empty(s), ph ^ 1u, abort_flag, p.status))) break;
       const uint32_t b = base + s * TR::stage + 2 * kBox16;
-      mbar_arrive_expect_tx_warp(full(s), I8 ? 2 * TR::b_box : TR::b_box);
-      tma_load_3d_warp(b, &mapAct, full(s), k * TR::k, 0, a);
-      if constexpr (I8) tma_load_3d_warp(b + TR::b_box, &mapAct, full(s), k * TR::k + 64, 0, a);
+      mbar_arrive_expect_tx_warp(full(s), TR::k / 64 * TR::b_box);
+#pragma unroll
+      for (int q = 0; q < TR::k / 64; ++q)
+        tma_load_3d_warp(b + q * TR::b_box, &mapAct, full(s), k * TR::k + q * 64, 0, a);
       next();
     }
     drain_ring(1, n);
@@ -498,25 +525,27 @@ few_tokens_kernel(const __grid_constant__ CUtensorMap mapG, const __grid_constan
       for (int k = 0; k < len; ++k) {
         run = mbar_wait_warp(full(s), ph, abort_flag, p.status);
         if (!run) return;
-        if constexpr (I8) {
-          run = mbar_wait_warp(c_full(c), cph, abort_flag, p.status);
-          if (!run) return;
-        }
         tc_fence_after();
         const uint64_t ad = d0 + (uint64_t)s * (TR::stage >> 4);
         const uint64_t bd = ad + (2 * kBox16 >> 4);
-        if constexpr (I8) {
-          const uint32_t a = tmem + 256 + c * 128;
+        if constexpr (BITS < 16) {
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const uint64_t b = bd + h * (TR::b_box >> 4);
-            umma_f16_ta_k64_warp<false>(d, a + h * 32, b, idesc, accum);
-            umma_f16_ta_k64_warp<false>(d + NP, a + 64 + h * 32, b, idesc, accum);
-            accum = 1u;
+          for (int half = 0; half < TR::k / 128; ++half) {  // expanded 128 of k at a time
+            run = mbar_wait_warp(c_full(c), cph, abort_flag, p.status);
+            if (!run) return;
+            tc_fence_after();
+            const uint32_t a = tmem + 256 + c * 128;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const uint64_t b = bd + (2 * half + h) * (TR::b_box >> 4);
+              umma_f16_ta_k64_warp<false>(d, a + h * 32, b, idesc, accum);
+              umma_f16_ta_k64_warp<false>(d + NP, a + 64 + h * 32, b, idesc, accum);
+              accum = 1u;
+            }
+            umma_commit_warp(c_empty(c));
+            c ^= 1;
+            if (c == 0) cph ^= 1u;
           }
-          umma_commit_warp(c_empty(c));
-          c ^= 1;
-          if (c == 0) cph ^= 1u;
         } else {
           umma_f16_k64_warp(d, ad, bd, idesc, accum);
           if (two) umma_f16_k64_warp(d + NP, ad + (kBox16 >> 4), bd, idesc, accum);
@@ -812,6 +841,55 @@ few_tokens_kernel(const __grid_constant__ CUtensorMap mapG, const __grid_constan
       if (c == 0) cph ^= 1u;
       if (++s == S) s = 0, ph ^= 1u;
     }
+  } else if (I4 && warp >= 12) {
+    // ---------------- expand: 4-bit rows to bf16 in tensor memory ----------------
+    // A lane takes one row of one of the unit's two boxes, 128 of its k at a time;
+    // two groups take one half of a unit each.
+    const int quarter = warp & 3, j = ((warp - 12) >> 2) & 1, grp = (warp - 12) >> 3, r = quarter * 32 + lane;
+    const uint32_t row = base + j * kBox16 + r * 128 + ((r & 7) << 4);
+    const uint32_t dst = tmem + 256 + j * 64 + ((uint32_t)(quarter * 32) << 16);
+    const int n1 = hi1 - lo1, n = n1 + hi2 - lo2;
+    int s = 0;
+    uint32_t ph = 0, cph = 0;
+    bool run = true;
+    for (int i = 0; i < n; ++i) {
+      if (!mbar_wait_warp(full(s), ph, abort_flag, p.status)) break;
+      const int per = i < n1 ? p.per1 : p.per2;
+      const int shift = per == 8 ? 0 : per == 4 ? 1 : 2;  // chunks of 32 k to groups
+      const uint32_t sc0 = base + s * TR::stage + TR::scales + j * per * 256 + r * 2;
+      const uint32_t src = row + s * TR::stage;
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        if (TR::groups == 2 && half != grp) continue;
+        const uint32_t a = dst + half * 128;
+        uint32_t f[32];
+        auto expand = [&](int q) {  // two chunks: 64 of k
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const uint4 v = ld_shared_v4(src ^ ((q + h) << 4));
+            const uint32_t sc = ld_shared_u16(sc0 + ((q + h) >> shift) * 256) * 0x10001u;
+            expand_int4(v.x, sc, f + 16 * h);
+            expand_int4(v.y, sc, f + 16 * h + 4);
+            expand_int4(v.z, sc, f + 16 * h + 8);
+            expand_int4(v.w, sc, f + 16 * h + 12);
+          }
+        };
+        expand(4 * half);
+        run = mbar_wait_warp(c_empty(half), cph ^ 1u, abort_flag, p.status);
+        if (!run) break;
+        tc_fence_after();
+        tmem_st_32x32b_x32(a, f);
+        expand(4 * half + 2);
+        tmem_st_32x32b_x32(a + 32, f);
+        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive_warp(c_full(half));
+      }
+      if (!run) break;
+      mbar_arrive_warp(empty(s));
+      cph ^= 1u;
+      if (++s == S) s = 0, ph ^= 1u;
+    }
   }
   tc_fence_before();
   __syncthreads();
@@ -838,14 +916,20 @@ FewLayout few_layout(int T, int K, int H, int I, int E) {
   return l;
 }
 
-template <int NP, bool I8>
-int launch_few(FewParams p, const void* x, const void* Wg, const void* Wu, const void* Wd,
-               cudaStream_t s) {
-  using TR = FewTraits<NP, I8>;
-  constexpr int esz = I8 ? 1 : 2;
-  CUtensorMap mg, mu, mg64, mu64, md, mx, ma;
-  const uint64_t d1[3] = {(uint64_t)p.H, (uint64_t)p.I, (uint64_t)p.E};
-  const uint64_t d2[3] = {(uint64_t)p.I, (uint64_t)p.H, (uint64_t)p.E};
+// What the weights and their scales are: of 4-bit weights the bf16 scales (the
+// others' float32 ones are in FewParams).
+struct FewWeights {
+  const void *gate, *up, *down, *gs, *us, *ds;
+};
+
+template <int NP, int BITS>
+int launch_few(FewParams p, const void* x, const FewWeights& w, cudaStream_t s) {
+  using TR = FewTraits<NP, BITS>;
+  constexpr int esz = BITS == 16 ? 2 : 1, pack = BITS == 4 ? 2 : 1;
+  const void *Wg = w.gate, *Wu = w.up, *Wd = w.down;
+  CUtensorMap mg, mu, mg64, mu64, md, mx, ma, mgs = {}, mus = {}, mds = {};
+  const uint64_t d1[3] = {(uint64_t)p.H / pack, (uint64_t)p.I, (uint64_t)p.E};
+  const uint64_t d2[3] = {(uint64_t)p.I / pack, (uint64_t)p.H, (uint64_t)p.E};
   const uint32_t bw[3] = {128 / esz, 128, 1}, bw64[3] = {128 / esz, 64, 1};
   const uint64_t dx[2] = {(uint64_t)p.H, (uint64_t)p.T};
   const uint64_t da[3] = {(uint64_t)p.I, (uint64_t)p.T, (uint64_t)p.A_max};
@@ -855,11 +939,20 @@ int launch_few(FewParams p, const void* x, const void* Wg, const void* Wu, const
       !make_map_sw128(&md, Wd, esz, 3, d2, bw) || !make_map_sw128(&mx, x, 2, 2, dx, bx) ||
       !make_map_sw128(&ma, p.act, 2, 3, da, bx))
     return MOE_ERR_CUDA;
+  if constexpr (BITS == 4) {
+    const uint64_t s1[3] = {(uint64_t)p.I, (uint64_t)p.H * p.per1 / 256, (uint64_t)p.E};
+    const uint64_t s2[3] = {(uint64_t)p.H, (uint64_t)p.I * p.per2 / 256, (uint64_t)p.E};
+    const uint32_t b1[3] = {128, (uint32_t)p.per1, 1}, b2[3] = {128, (uint32_t)p.per2, 1};
+    if (!make_map(&mgs, w.gs, 2, 3, s1, b1, CU_TENSOR_MAP_SWIZZLE_NONE) ||
+        !make_map(&mus, w.us, 2, 3, s1, b1, CU_TENSOR_MAP_SWIZZLE_NONE) ||
+        !make_map(&mds, w.ds, 2, 3, s2, b2, CU_TENSOR_MAP_SWIZZLE_NONE))
+      return MOE_ERR_CUDA;
+  }
   static PerDevice smem_allowed;
   int dev = -1;
   if (cudaGetDevice(&dev) != cudaSuccess) return MOE_ERR_CUDA;
   const int allowed = smem_allowed.get(dev, [] {
-    return cudaFuncSetAttribute(few_tokens_kernel<NP, I8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    return cudaFuncSetAttribute(few_tokens_kernel<NP, BITS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                 (int)TR::smem) == cudaSuccess;
   });
   if (!allowed) return MOE_ERR_CUDA;
@@ -873,7 +966,7 @@ int launch_few(FewParams p, const void* x, const void* Wg, const void* Wu, const
   cfg.stream = s;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, few_tokens_kernel<NP, I8>, mg, mu, mg64, mu64, md, mx, ma, p) != cudaSuccess) {
+  if (cudaLaunchKernelEx(&cfg, few_tokens_kernel<NP, BITS>, mg, mu, mg64, mu64, md, mx, ma, mgs, mus, mds, p) != cudaSuccess) {
     (void)cudaGetLastError();
     return MOE_ERR_CUDA;
   }
@@ -894,32 +987,37 @@ extern "C" size_t moe_layer_few_tokens_workspace_size(int T, int K, int H, int I
   return few_layout(T, K, H, I, E).total;
 }
 
-extern "C" int moe_layer_few_tokens(const void* tokens, const int32_t* expert_ids,
-                                    const float* probs, int T, int H, int K, int I, int E,
-                                    int num_special, const uint8_t* active_mask, int mask_dims,
-                                    int weight_dtype, const void* W_gate, const void* W_up,
-                                    const void* W_down, const float* gate_scale,
-                                    const float* up_scale, const float* down_scale,
-                                    const void* shared_x, void* out, void* workspace,
-                                    size_t workspace_bytes, int32_t* dev_status,
-                                    cudaStream_t stream) {
+namespace moe {
+namespace tc {
+namespace {
+
+// bits: 16, 8, 4.
+int few_tokens(int bits, const void* tokens, const int32_t* expert_ids, const float* probs, int T, int H, int K,
+               int I, int E, int num_special, const uint8_t* active_mask, int mask_dims, int group1, int group2,
+               const FewWeights& w, const void* shared_x, void* out, void* workspace, size_t workspace_bytes,
+               int32_t* dev_status, cudaStream_t stream) {
   if (T < 0 || H <= 0 || K <= 0 || I <= 0 || E <= 0 || num_special < 0) return MOE_ERR_INVALID_ARG;
-  if (weight_dtype != MOE_BF16 && weight_dtype != MOE_INT8) return MOE_ERR_INVALID_ARG;
   if (active_mask != nullptr && mask_dims != 1 && mask_dims != 2) return MOE_ERR_INVALID_ARG;
   if (T > MOE_FEW_TOKENS || K > kMaxK || E > kMaxExperts) return MOE_ERR_SHAPE;
   if ((long long)E + num_special > 0x7fffffffLL || (long long)K > (long long)E + num_special)
     return MOE_ERR_SHAPE;
   if (H % 64 || I % 64) return MOE_ERR_SHAPE;
   if (H > MOE_FEW_MAX_SIZE || I > MOE_FEW_MAX_SIZE) return MOE_ERR_SHAPE;  // (T H, a tile's bytes: 31 bits)
+  if (bits == 4) {
+    for (int g : {group1, group2})
+      if (g != 32 && g != 64 && g != 128) return MOE_ERR_INVALID_ARG;
+    if (H % group1 || I % group2) return MOE_ERR_SHAPE;
+  }
   if (T == 0) return MOE_OK;
-  if (!tokens || !expert_ids || !probs || !W_gate || !W_up || !W_down || !out || !workspace)
+  if (!tokens || !expert_ids || !probs || !w.gate || !w.up || !w.down || !out || !workspace)
     return MOE_ERR_INVALID_ARG;
-  const bool i8 = weight_dtype == MOE_INT8;
-  if (i8 != (gate_scale != nullptr) || i8 != (up_scale != nullptr) || i8 != (down_scale != nullptr))
+  const bool scaled = bits < 16;
+  if (scaled != (w.gs != nullptr) || scaled != (w.us != nullptr) || scaled != (w.ds != nullptr))
     return MOE_ERR_INVALID_ARG;
-  const void* ptrs[] = {tokens, W_gate, W_up, W_down, shared_x, out, workspace};
+  const void* ptrs[] = {tokens, w.gate, w.up, w.down, shared_x, out, workspace};
   for (const void* p : ptrs)
     if (p && !aligned16(p)) return MOE_ERR_INVALID_ARG;
+  if (bits == 4 && (!aligned16(w.gs) || !aligned16(w.us) || !aligned16(w.ds))) return MOE_ERR_INVALID_ARG;
   if (workspace_bytes < moe_layer_few_tokens_workspace_size(T, K, H, I, E))
     return MOE_ERR_INVALID_ARG;
   if (int rc = device_ok()) return rc;
@@ -929,9 +1027,15 @@ extern "C" int moe_layer_few_tokens(const void* tokens, const int32_t* expert_id
   p.ids = expert_ids;
   p.probs = probs;
   p.mask = active_mask;
-  p.gs = gate_scale;
-  p.us = up_scale;
-  p.ds = down_scale;
+  if (bits == 8) {
+    p.gs = static_cast<const float*>(w.gs);
+    p.us = static_cast<const float*>(w.us);
+    p.ds = static_cast<const float*>(w.ds);
+  }
+  if (bits == 4) {
+    p.per1 = 256 / group1;
+    p.per2 = 256 / group2;
+  }
   p.shared_x = static_cast<const __nv_bfloat16*>(shared_x);
   p.out = static_cast<__nv_bfloat16*>(out);
   p.epoch = reinterpret_cast<unsigned long long*>(ws);
@@ -948,11 +1052,47 @@ extern "C" int moe_layer_few_tokens(const void* tokens, const int32_t* expert_id
   p.E = E;
   p.E_all = E + num_special;
   p.A_max = T * K < E ? T * K : E;
-  auto go = [&](auto i8) {
-    constexpr bool I8 = decltype(i8)::value;
-    if (T <= 16) return launch_few<16, I8>(p, tokens, W_gate, W_up, W_down, stream);
-    if (T <= 32) return launch_few<32, I8>(p, tokens, W_gate, W_up, W_down, stream);
-    return launch_few<64, I8>(p, tokens, W_gate, W_up, W_down, stream);
+  auto go = [&](auto b) {
+    constexpr int B = decltype(b)::value;
+    if (T <= 16) return launch_few<16, B>(p, tokens, w, stream);
+    if (T <= 32) return launch_few<32, B>(p, tokens, w, stream);
+    return launch_few<64, B>(p, tokens, w, stream);
   };
-  return weight_dtype == MOE_INT8 ? go(std::true_type{}) : go(std::false_type{});
+  if (bits == 4) return go(std::integral_constant<int, 4>{});
+  if (bits == 8) return go(std::integral_constant<int, 8>{});
+  return go(std::integral_constant<int, 16>{});
+}
+
+}  // namespace
+}  // namespace tc
+}  // namespace moe
+
+extern "C" int moe_layer_few_tokens(const void* tokens, const int32_t* expert_ids,
+                                    const float* probs, int T, int H, int K, int I, int E,
+                                    int num_special, const uint8_t* active_mask, int mask_dims,
+                                    int weight_dtype, const void* W_gate, const void* W_up,
+                                    const void* W_down, const float* gate_scale,
+                                    const float* up_scale, const float* down_scale,
+                                    const void* shared_x, void* out, void* workspace,
+                                    size_t workspace_bytes, int32_t* dev_status,
+                                    cudaStream_t stream) {
+  if (weight_dtype != MOE_BF16 && weight_dtype != MOE_INT8) return MOE_ERR_INVALID_ARG;
+  return few_tokens(weight_dtype == MOE_INT8 ? 8 : 16, tokens, expert_ids, probs, T, H, K, I, E, num_special,
+                    active_mask, mask_dims, 0, 0,
+                    FewWeights{W_gate, W_up, W_down, gate_scale, up_scale, down_scale}, shared_x, out, workspace,
+                    workspace_bytes, dev_status, stream);
+}
+
+extern "C" int moe_layer_few_tokens_int4(const void* tokens, const int32_t* expert_ids,
+                                         const float* probs, int T, int H, int K, int I, int E,
+                                         int num_special, const uint8_t* active_mask, int mask_dims,
+                                         int group, int down_group, const uint8_t* W_gate_q,
+                                         const void* gate_scale, const uint8_t* W_up_q,
+                                         const void* up_scale, const uint8_t* W_down_q,
+                                         const void* down_scale, const void* shared_x, void* out,
+                                         void* workspace, size_t workspace_bytes,
+                                         int32_t* dev_status, cudaStream_t stream) {
+  return few_tokens(4, tokens, expert_ids, probs, T, H, K, I, E, num_special, active_mask, mask_dims, group,
+                    down_group, FewWeights{W_gate_q, W_up_q, W_down_q, gate_scale, up_scale, down_scale}, shared_x,
+                    out, workspace, workspace_bytes, dev_status, stream);
 }

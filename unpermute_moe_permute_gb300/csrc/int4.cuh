@@ -24,8 +24,8 @@ __device__ __forceinline__ uint32_t as_u32(__nv_bfloat162 v) { return *reinterpr
 __device__ __forceinline__ void expand_int4(uint32_t w, uint32_t scale2, uint32_t* r) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    // (one three-input operation: and, then exclusive or)
-    const uint32_t t = ((w >> (4 * i)) & kInt4Mask) ^ kInt4Magic;
+    uint32_t t;  // (shifted & mask) ^ magic in one operation: left to the compiler it takes two
+    asm("lop3.b32 %0, %1, %2, %3, 0x6a;" : "=r"(t) : "r"(w >> (4 * i)), "r"(kInt4Mask), "r"(kInt4Magic));
     r[i] = as_u32(__hmul2(__hsub2(as_bf162(t), as_bf162(kInt4Zero)), as_bf162(scale2)));
   }
 }

@@ -48,6 +48,8 @@
 
 #include <math.h>
 
+#include <type_traits>
+
 #include "common.cuh"
 #include "int4.cuh"
 #include "per_device.h"
@@ -90,9 +92,11 @@ struct FewTraits {
   // Warps that expand, and the buffers of 128 expanded k (128 columns of tensor
   // memory) that they fill in turn.  4-bit weights: twice the warps and a third
   // buffer where registers and tensor memory have room.
-  static constexpr int expand = BITS == 16 ? 0 : BITS == 4 && NP <= 32 ? 16 : 8;
+  static constexpr int expand = BITS == 4 && NP <= 32 ? 16 : 8;
   static constexpr int bufs = BITS == 4 && NP <= 32 ? 3 : 2;
-  static constexpr int threads = (12 + expand) * 32;
+  static constexpr int threads = (12 + (BITS == 16 ? 0 : expand)) * 32;
+  // Warps that issue MMAs: with 4-bit weights one for each of a unit's two boxes.
+  static constexpr int issuers = BITS == 4 ? 2 : 1;
   static constexpr int bars = 2 * stages + 4 + 2 * bufs + 2;
   static constexpr uint32_t ctrl = stages * stage;
   static constexpr uint32_t holder = ctrl + 8 * bars;     // tensor memory, abort, flag, A
@@ -267,17 +271,17 @@ few_tokens_kernel(const __grid_constant__ CUtensorMap mapG, const __grid_constan
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
       mbar_init(full(s), 2);               // weights, tokens
-      mbar_init(empty(s), 1 + TR::expand);  // MMAs (and the expanding warps)
+      mbar_init(empty(s), TR::issuers + (BITS == 16 ? 0 : TR::expand));  // MMAs, expanding warps
     }
     for (int a = 0; a < 2; ++a) {
-      mbar_init(t_full(a), 1);
+      mbar_init(t_full(a), TR::issuers);
       mbar_init(t_empty(a), 8);  // the epilogue warps
     }
-    for (int b = 0; TR::expand > 0 && b < TR::bufs; ++b) {
-      mbar_init(c_full(b), TR::expand > 0 ? TR::expand : 1);
-      mbar_init(c_empty(b), 1);
+    for (int b = 0; b < TR::bufs; ++b) {
+      mbar_init(c_full(b), TR::expand);
+      mbar_init(c_empty(b), TR::issuers);
     }
-    mbar_init(drain, 1);
+    mbar_init(drain, TR::issuers);
     mbar_init(clear, 1);
     *abort_flag = 0;
     mbar_fence_init();
@@ -514,8 +518,10 @@ few_tokens_kernel(const __grid_constant__ CUtensorMap mapG, const __grid_constan
       next();
     }
     drain_ring(1, n);
-  } else if (warp == 1) {
+  } else if (warp == 1 || (I4 && warp == 11)) {
     // ---------------- MMA: the whole warp, one lane elected for each ----------------
+    // (4-bit: the unit's first box, or its second)
+    const uint32_t box = warp == 1 ? 0u : 1u;
     constexpr uint32_t idesc = idesc_bf16_f32(128, NP, false, false);
     const uint64_t d0 = desc_sw128(base, 16, 1024);
     int s = 0, c = 0, it = 0;
@@ -537,16 +543,20 @@ few_tokens_kernel(const __grid_constant__ CUtensorMap mapG, const __grid_constan
         const uint64_t bd = ad + (2 * kBox16 >> 4);
         if constexpr (BITS < 16) {
 #pragma unroll
-          for (int half = 0; half < TR::k / 128; ++half) {  // expanded 128 of k at a time
+          for (int q = 0; q < TR::k / 128; ++q) {  // expanded 128 of k at a time
             run = mbar_wait_warp(c_full(c), cph, abort_flag, p.status);
             if (!run) return;
             tc_fence_after();
             const uint32_t a = tmem + 512 - 128 * TR::bufs + c * 128;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-              const uint64_t b = bd + (2 * half + h) * (TR::b_box >> 4);
-              umma_f16_ta_k64_warp<false>(d, a + h * 32, b, idesc, accum);
-              umma_f16_ta_k64_warp<false>(d + NP, a + 64 + h * 32, b, idesc, accum);
+              const uint64_t b = bd + (2 * q + h) * (TR::b_box >> 4);
+              if constexpr (I4) {
+                umma_f16_ta_k64_warp<false>(d + box * NP, a + box * 64 + h * 32, b, idesc, accum);
+              } else {
+                umma_f16_ta_k64_warp<false>(d, a + h * 32, b, idesc, accum);
+                umma_f16_ta_k64_warp<false>(d + NP, a + 64 + h * 32, b, idesc, accum);
+              }
               accum = 1u;
             }
             umma_commit_warp(c_empty(c));
@@ -854,46 +864,48 @@ few_tokens_kernel(const __grid_constant__ CUtensorMap mapG, const __grid_constan
     constexpr int kParts = TR::expand == 16 ? 1 : 2;
     const int quarter = warp & 3, j = ((warp - 12) >> 2) & 1, r = quarter * 32 + lane;
     const int part = kParts == 1 ? (warp - 12) >> 3 : 0;
-    const uint32_t row = base + j * kBox16 + r * 128 + ((r & 7) << 4);
+    const uint32_t row = base + j * kBox16 + r * 128 + (((r & 7) ^ (2 * part)) << 4);
     const uint32_t dst = tmem + 512 - 128 * TR::bufs + j * 64 + part * 32 + ((uint32_t)(quarter * 32) << 16);
     const int n1 = hi1 - lo1, n = n1 + hi2 - lo2;
     int s = 0, c = 0;
     uint32_t ph = 0, cph = 0;
+    const uint32_t mask = int4_mask();
+    uint32_t sc_at = 0, sc_off[2][2 * kParts];  // where a lane's scales are in a stage
     bool run = true;
     for (int i = 0; run && i < n; ++i) {
+      if (i == 0 || i == n1) {  // (a phase begins)
+        const int per = i < n1 ? p.per1 : p.per2;
+        const int shift = per == 8 ? 0 : per == 4 ? 1 : 2;  // chunks of 32 k to groups
+        sc_at = base + TR::scales + j * per * 256 + r * 2;
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int q = 0; q < 2 * kParts; ++q) sc_off[h][q] = ((4 * h + 2 * part + q) >> shift) << 8;
+      }
       run = mbar_wait_warp(full(s), ph, abort_flag, p.status);
       if (!run) break;
-      const int per = i < n1 ? p.per1 : p.per2;
-      const int shift = per == 8 ? 0 : per == 4 ? 1 : 2;  // chunks of 32 k to groups
-      const uint32_t sc0 = base + s * TR::stage + TR::scales + j * per * 256 + r * 2;
-      const uint32_t src = row + s * TR::stage;
-      for (int half = 0; run && half < 2; ++half) {
-        uint32_t f[32];
-        auto expand = [&](int chunk) {  // two chunks: 64 of k
+      const uint32_t src = row + s * TR::stage, scs = sc_at + s * TR::stage;
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const uint4 v = ld_shared_v4(src ^ ((chunk + h) << 4));
-            const uint32_t sc = ld_shared_u16(sc0 + ((chunk + h) >> shift) * 256) * 0x10001u;
-            expand_int4(v.x, sc, f + 16 * h);
-            expand_int4(v.y, sc, f + 16 * h + 4);
-            expand_int4(v.z, sc, f + 16 * h + 8);
-            expand_int4(v.w, sc, f + 16 * h + 12);
-          }
+      for (int h = 0; h < 2; ++h) {
+        uint32_t f[32];
+        auto expand = [&](int q) {  // two chunks: 64 of k
+          const uint32_t at = src ^ (h << 6) ^ (q << 4);
+          expand_int4_row(ld_shared_v4(at), ld_shared_u16(scs + sc_off[h][q]), mask, f);
+          expand_int4_row(ld_shared_v4(at ^ 16), ld_shared_u16(scs + sc_off[h][q + 1]), mask, f + 16);
         };
-        expand(4 * half + 2 * part);
+        expand(0);
         run = mbar_wait_warp(c_empty(c), cph ^ 1u, abort_flag, p.status);
-        if (run) {
-          tc_fence_after();
-          tmem_st_32x32b_x32(dst + c * 128, f);
-          if constexpr (kParts == 2) {
-            expand(4 * half + 2);
-            tmem_st_32x32b_x32(dst + c * 128 + 32, f);
-          }
-          tmem_st_wait();
-          tc_fence_before();
-          mbar_arrive_warp(c_full(c));
-          if (++c == TR::bufs) c = 0, cph ^= 1u;
+        if (!run) break;
+        tc_fence_after();
+        tmem_st_32x32b_x32(dst + c * 128, f);
+        if constexpr (kParts == 2) {
+          expand(2);
+          tmem_st_32x32b_x32(dst + c * 128 + 32, f);
         }
+        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive_warp(c_full(c));
+        if (++c == TR::bufs) c = 0, cph ^= 1u;
       }
       if (!run) break;
       mbar_arrive_warp(empty(s));

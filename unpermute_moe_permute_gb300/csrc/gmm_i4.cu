@@ -264,6 +264,7 @@ gmm_i4_kernel(const __grid_constant__ CUtensorMap mapW0, const __grid_constant__
     const int shift = p.per == 4 ? 0 : p.per == 2 ? 1 : 2;  // chunks of 32 inputs to groups
     const uint32_t dst = tmem + kACol + grp * 64 + ((uint32_t)(quarter * 32) << 16);
     const uint32_t full_of_leader = mapa_shared(c_full(grp), 0);
+    const uint32_t mask = int4_mask();
     int s = grp, f = grp, n0 = 0;  // slot, its barrier; stages before this tile (mod kGroups)
     uint32_t ph = 0, bph = 0;
     bool run = true;
@@ -277,15 +278,10 @@ gmm_i4_kernel(const __grid_constant__ CUtensorMap mapW0, const __grid_constant__
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           v[j] = ld_shared_v4(src ^ (j << 4));
-          sc[j] = ld_shared_u16(scs + (j >> shift) * kScaleRow) * 0x10001u;
+          sc[j] = ld_shared_u16(scs + (j >> shift) * kScaleRow);
         }
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          expand_int4(v[j].x, sc[j], r + 16 * j);
-          expand_int4(v[j].y, sc[j], r + 16 * j + 4);
-          expand_int4(v[j].z, sc[j], r + 16 * j + 8);
-          expand_int4(v[j].w, sc[j], r + 16 * j + 12);
-        }
+        expand_int4_row(v[0], sc[0], mask, r);
+        expand_int4_row(v[1], sc[1], mask, r + 16);
         // The row and its scales are read: the fence orders these reads before
         // the copy that refills the slot.
         fence_proxy_async_smem();
@@ -294,13 +290,8 @@ gmm_i4_kernel(const __grid_constant__ CUtensorMap mapW0, const __grid_constant__
         if (!run) break;
         tc_fence_after();
         tmem_st_32x32b_x32(dst, r);
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          expand_int4(v[j + 2].x, sc[j + 2], r + 16 * j);
-          expand_int4(v[j + 2].y, sc[j + 2], r + 16 * j + 4);
-          expand_int4(v[j + 2].z, sc[j + 2], r + 16 * j + 8);
-          expand_int4(v[j + 2].w, sc[j + 2], r + 16 * j + 12);
-        }
+        expand_int4_row(v[2], sc[2], mask, r);
+        expand_int4_row(v[3], sc[3], mask, r + 16);
         tmem_st_32x32b_x32(dst + 32, r);
         tmem_st_wait();
         tc_fence_before();

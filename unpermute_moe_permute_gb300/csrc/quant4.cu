@@ -112,6 +112,7 @@ dequantize_int4_kernel(const uint32_t* __restrict__ q, const uint16_t* __restric
   const int groups = cols / (8 * lanes), c = c0 + 8 * lane;
   const size_t e = blockIdx.y;
   const int g0 = c0 / (8 * lanes), n = min(32 / lanes, groups - g0);
+  const uint32_t mask = int4_mask();
   uint32_t v[kPerWarp];
 #pragma unroll
   for (int i = 0; i < kPerWarp; ++i) {
@@ -129,7 +130,7 @@ dequantize_int4_kernel(const uint32_t* __restrict__ q, const uint16_t* __restric
     if (r < rows && c < cols) {
       const uint32_t s = tile[lane / lanes][warp * kPerWarp + i] * 0x10001u;
       uint32_t x[4];
-      expand_int4(v[i], s, x);
+      expand_int4(v[i], s, mask, x);
       st_cs_v4(w + (e * rows + r) * cols + c, make_uint4(x[0], x[1], x[2], x[3]));
     }
   }

@@ -12,12 +12,16 @@
 // The selection is that of exact scores.  c is computed in fp32 and carried as
 // a 32-bit key whose lowest bits (3 for 8 scores a lane) say which of the lane's
 // scores it is; one warp-wide maximum a round finds the next.  What lies closer
-// together than fp32's error and the missing bits, at the border between kept
-// and dropped groups or anywhere among the first K + 1, is decided again in 64
-// bits (select_exact).  Of normal logits at E = 256 in 8 groups K = 8 that is
-// one row in 200.  Where no score is needed (no bias, and no sum of two) the
-// logits themselves are compared and their keys hold the whole index, as in the
-// plain router.
+// together than fp32's error, at the border between kept and dropped groups or
+// anywhere among the first K + 1, is decided again in 64 bits, a lane for each
+// score in question (exact_groups, exact_among); rows that those cannot take
+// (more than 32 scores in question, groups or rows with too few experts left) by
+// the whole row in 64 bits (select_exact).  Of normal logits at E = 256 in 8 groups
+// K = 8 two rows in a thousand need it.  The whole row takes a warp 7 us of the slow
+// 64-bit pipe, which at first was half of the launch, its tail (16384 rows 38 us,
+// now 21; softmax, whose sum takes the row's exponentials in 64 bits, 38 and 26).  Where no score is needed (no bias, and no
+// sum of two) the logits themselves are compared and their keys hold the whole
+// index, as in the plain router.
 #include <type_traits>
 
 #include "router.cuh"
@@ -46,6 +50,157 @@ __device__ __forceinline__ float clean_bias(float b, bool& bad) {
   if (b < INFINITY) return b;
   bad = true;
   return -INFINITY;
+}
+
+// Error of c in fp32 for sigmoid, and of a difference of two: z = -l log2(e) is
+// off by 1.5 |z| 2^-24 and its exponential by 2^-22, of which s (1 - s) <= 1/4
+// (times |l|: 0.224) reaches s; 1 + e^-l rounds, the reciprocal is off by 2^-23:
+// together under 2^-21.9.  For softmax 2^-22 and the sum's rounding, 37 additions
+// at most: under p 2^-18.
+__device__ __forceinline__ float margin_of(float x, float y, float eps) {
+  return eps + 0x1p-23f * (fabsf(x) + fabsf(y));  // (the sums with the biases round)
+}
+constexpr float kSigmoidEps = 0x1p-20f;
+
+__device__ __forceinline__ float sigmoid_fast(float l) {
+  float s;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(l * -1.4426950408889634f));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(1.f + s));
+  return s;
+}
+
+__device__ __forceinline__ double sigmoid_exact(double l) {
+  const double e = exp(-fabs(l));
+  return (l < 0.0 ? e : 1.0) / (1.0 + e);
+}
+
+// Unsigned keys in the order of the doubles (compared as integers: the 64-bit
+// float pipe is slow).
+__device__ __forceinline__ unsigned long long key64(double v) {
+  const long long b = __double_as_longlong(v + 0.0);
+  return (unsigned long long)(b < 0 ? ~b : b ^ (long long)0x8000000000000000ull);
+}
+
+// How a row's scores come from its logits: in fp32, and in 64 bits.
+struct Scores {
+  bool soft;
+  float m, inv, eps;  // softmax: the largest logit, 1 / the sum; the error (margin_of)
+  __device__ __forceinline__ float fast(float l) const { return soft ? exp_flush(l - m) * inv : sigmoid_fast(l); }
+  __device__ __forceinline__ double exact(double l, double sum) const {
+    return soft ? exp(l - m) / sum : sigmoid_exact(l);
+  }
+};
+
+// The sum of e^(l - m) over the row, in every lane.
+template <int NPL, typename T>
+__device__ __forceinline__ double exact_sum(const T* row, const GroupParams& p, float m, int lane) {
+  const int g = lane >> p.lg, r = lane & ((1 << p.lg) - 1);
+  bool flag = false;
+  double s = 0.0;
+#pragma unroll 1
+  for (int i = 0; i < NPL; ++i) {
+    const int o = place<T, false>(i, r, p.lg);
+    if (g < p.G && o < p.size) s += exp((double)clean_logit(to_f32(row[g * p.size + o]), flag) - m);
+  }
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(kAll, s, d);
+  return s;
+}
+
+// Whether the group of this lane is kept, by the exact sums of its
+// `each` largest; fail where it is not those that fp32 names without doubt.
+// list: 32 words of the warp's own.
+template <int NPL, typename T>
+__device__ __noinline__ bool exact_groups(const T* row, const GroupParams& p, const Scores& f, int lane, int* list, bool& fail) {
+  const int g = lane >> p.lg, r = lane & ((1 << p.lg) - 1);
+  float c[NPL], a1 = -INFINITY, a2 = -INFINITY;
+  bool flag = false;
+#pragma unroll
+  for (int i = 0; i < NPL; ++i) {
+    const int o = place<T, false>(i, r, p.lg), j = g * p.size + o;
+    const bool in = g < p.G && o < p.size;
+    const float l = in ? clean_logit(to_f32(row[j]), flag) : -INFINITY;
+    const float b = in && p.bias ? clean_bias(p.bias[j], flag) : 0.f;
+    c[i] = l > -INFINITY ? f.fast(l) + b : -INFINITY;
+    a2 = fmaxf(a2, fminf(a1, c[i]));
+    a1 = fmaxf(a1, c[i]);
+  }
+  for (int d = 1; d < 1 << p.lg; d <<= 1) {
+    const float b1 = __shfl_xor_sync(kAll, a1, d), b2 = __shfl_xor_sync(kAll, a2, d);
+    a2 = fmaxf(fminf(a1, b1), fmaxf(a2, b2));
+    a1 = fmaxf(a1, b1);
+  }
+  const float last = p.each > 1 ? a2 : a1, cut = last - margin_of(last, last, f.eps);
+  const unsigned mine = (p.lg == 5 ? kAll : (1u << (1 << p.lg)) - 1u) << (g << p.lg);  // the group's lanes
+  int n = 0;
+#pragma unroll
+  for (int i = 0; i < NPL; ++i) {
+    const bool on = c[i] > -INFINITY && c[i] >= cut;
+    const unsigned m = __ballot_sync(kAll, on) & mine;
+    const int at = n + __popc(m & lanemask_lt());
+    if (on && at < p.each) list[g * p.each + at] = g * p.size + place<T, false>(i, r, p.lg);
+    n += __popc(m);
+  }
+  fail = !__all_sync(kAll, g >= p.G || n == p.each);
+  if (fail) return false;
+  __syncwarp();
+  const double sum = f.soft ? exact_sum<NPL>(row, p, f.m, lane) : 0.0;
+  double v = 0.0;
+  if (lane < p.G * p.each) {
+    const int j = list[lane];
+    v = f.exact(clean_logit(to_f32(row[j]), flag), sum) + (p.bias ? (double)p.bias[j] : 0.0);
+  }
+  if (p.each > 1) v += __shfl_xor_sync(kAll, v, 1);
+  const unsigned long long key = __shfl_sync(kAll, key64(v), (g * p.each) & 31);
+  int rank = 0;
+  for (int h = 0; h < p.G; ++h) {
+    const unsigned long long other = __shfl_sync(kAll, key, h << p.lg);
+    rank += other > key || (other == key && h < g);
+  }
+  __syncwarp();
+  return g < p.G && rank < p.top;
+}
+
+// The selection among the scores (by_logit: logits) of kept groups that are at
+// least cut; lane k < K gets the k-th id.  fail: more than 32 of them.
+template <int NPL, typename T>
+__device__ __noinline__ int exact_among(const T* row, const GroupParams& p, const Scores& f, bool by_logit, bool keep,
+                                        float cut, int lane, int* list, bool& fail) {
+  const int g = lane >> p.lg, r = lane & ((1 << p.lg) - 1);
+  bool flag = false;
+  int n = 0;
+#pragma unroll
+  for (int i = 0; i < NPL; ++i) {
+    const int o = place<T, false>(i, r, p.lg), j = g * p.size + o;
+    const bool in = keep && o < p.size;
+    float c = in ? clean_logit(to_f32(row[j]), flag) : -INFINITY;
+    if (!by_logit && c > -INFINITY) c = f.fast(c) + (p.bias ? clean_bias(p.bias[j], flag) : 0.f);
+    const bool on = c > -INFINITY && c >= cut;
+    const unsigned m = __ballot_sync(kAll, on);
+    const int at = n + __popc(m & lanemask_lt());
+    if (on && at < 32) list[at] = j;
+    n += __popc(m);
+  }
+  fail = n > 32 || n < p.K;
+  if (fail) return 0;
+  __syncwarp();
+  const double sum = f.soft && !by_logit ? exact_sum<NPL>(row, p, f.m, lane) : 0.0;
+  int id = 0;
+  unsigned long long key = 0;
+  if (lane < n) {
+    id = list[lane];
+    const double l = clean_logit(to_f32(row[id]), flag);
+    key = key64(by_logit ? l : f.exact(l, sum) + (p.bias ? (double)p.bias[id] : 0.0));
+  }
+  int rank = 0;
+  for (int i = 0; i < n; ++i) {
+    const unsigned long long other = __shfl_sync(kAll, key, i);
+    const int oid = __shfl_sync(kAll, id, i);
+    rank += other > key || (other == key && oid < id);
+  }
+  if (lane < n && rank < p.K) list[rank] = id;
+  __syncwarp();
+  return lane < p.K ? list[lane] : 0;
 }
 
 // The selection in 64 bits; lane k < K gets the k-th id.  by_logit: c is the
@@ -81,13 +236,7 @@ __device__ __noinline__ int select_exact(const T* row, const GroupParams& p, boo
       const bool in = g < p.G && o < p.size;
       const float l = in ? clean_logit(to_f32(row[g * p.size + o]), flag) : -INFINITY;
       const float b = in && p.bias ? clean_bias(p.bias[g * p.size + o], flag) : 0.f;
-      double s;
-      if (p.scoring == MOE_SCORE_SOFTMAX) {
-        s = c[i] / inv;
-      } else {
-        const double e = exp(-fabs(c[i]));
-        s = (c[i] < 0.0 ? e : 1.0) / (1.0 + e);
-      }
+      const double s = p.scoring == MOE_SCORE_SOFTMAX ? c[i] / inv : sigmoid_exact(c[i]);
       c[i] = l > -INFINITY ? s + b : -INFINITY;
     }
   }
@@ -193,14 +342,9 @@ router_grouped_kernel(const T* __restrict__ logits, const __grid_constant__ Grou
     for (int i = 0; i < NPL; ++i) row_sum += exp_flush(c[i] - m);
     row_sum = fmaxf(warp_sum(row_sum), 1e-30f);  // (a row of -inf alone: every term is 0)
   }
-  // Error of a difference of two c: the approximate exponential and reciprocal
-  // are off by 2^-22 each, s (1 - s) |l| < 0.23 takes the rounding of the
-  // exponential's argument, so s is off by less than 2^-22; for softmax also the
-  // sum's rounding, 37 additions at most: p 2^-18.
-  float eps = 0.f;
+  const float inv = 1.f / row_sum;
+  const Scores f{soft, m, inv, soft ? 0x1p-20f + inv * 0x1p-17f : kSigmoidEps};
   if constexpr (!kByLogit) {
-    const float inv = 1.f / row_sum;
-    eps = soft ? inv * 0x1p-17f : 0x1p-20f;
     float bcheck = 0.f, b[NPL];
 #pragma unroll
     for (int i = 0; i < NPL; ++i) b[i] = 0.f;
@@ -226,18 +370,13 @@ router_grouped_kernel(const T* __restrict__ logits, const __grid_constant__ Grou
     }
 #pragma unroll
     for (int i = 0; i < NPL; ++i) {
-      float s;
-      if (soft) {
-        s = exp_flush(c[i] - m) * inv;
-      } else {
-        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(c[i] * -1.4426950408889634f));
-        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(1.f + s));
-      }
-      c[i] = c[i] > -INFINITY ? s + b[i] : -INFINITY;
+      c[i] = c[i] > -INFINITY ? f.fast(c[i]) + b[i] : -INFINITY;
     }
   }
   if (flag) set_status(status, MOE_ERR_INVALID_ARG);
-  bool again = false, keep = g < p.G;
+  bool again = false, keep = g < p.G;  // again: by the whole row
+  __shared__ int lists[kWarps][32];
+  int* list = lists[threadIdx.x >> 5];
   if (p.top < p.G) {
     float a1 = c[0], a2 = -INFINITY;
 #pragma unroll
@@ -262,7 +401,12 @@ router_grouped_kernel(const T* __restrict__ logits, const __grid_constant__ Grou
     if constexpr (!kByLogit) {  // the border between kept and dropped groups
       const float lo = value_of(__reduce_min_sync(kAll, keep ? key_of(v) : 0xffffffffu));
       const float hi = value_of(__reduce_max_sync(kAll, !keep && g < p.G ? key_of(v) : 0u));
-      again |= lo - hi <= 2.f * eps + 0x1p-21f * (fabsf(lo) + fabsf(hi));
+      // (dropped groups without experts are no question, nor are kept ones)
+      if (hi > -INFINITY && lo > -INFINITY && lo - hi <= 2.f * margin_of(lo, hi, f.eps) + 0x1p-22f * (fabsf(lo) + fabsf(hi))) {  // (sums of two)
+        bool fail = __any_sync(kAll, again) || p.G * p.each > 32;
+        if (!fail) keep = exact_groups<NPL>(row, p, f, lane, list, fail);
+        again |= fail;
+      }
     }
   }
   uint32_t pk[NPL];
@@ -291,21 +435,33 @@ router_grouped_kernel(const T* __restrict__ logits, const __grid_constant__ Grou
   } else {
     sel_id = (from >> p.lg) * p.size + place<T, kVec>((int)(kLow - (mine & kLow)), from & ((1 << p.lg) - 1), p.lg);
   }
-  float sel = lane < p.K && mine != 0u ? to_f32(row[sel_id]) : -INFINITY;
+  float sel = lane <= p.K && mine != 0u ? to_f32(row[sel_id]) : -INFINITY;
   sel = fminf(sel, 3.402823466e+38f) + 0.f;
   again |= (more && pk[0] == 0u) || (lane < p.K && mine == 0u);
+  // Two neighbours of the first K + 1 that are too close.  Below the last of the K
+  // may be any score with the upper bits of the next key.
   const uint32_t next = __shfl_down_sync(kAll, mine, 1);
+  const bool pair = lane < p.K && next != 0u, edge = lane == p.K - 1;
+  bool close = false;
   if constexpr (!kByLogit) {
-    const float x = value_of(mine & ~kLow), y = value_of(next & ~kLow);
-    again |= lane < p.K && next != 0u && x - y <= eps + (0x1p-23f * NPL + 0x1p-22f) * (fabsf(x) + fabsf(y));
+    const float bias = p.bias && lane <= p.K && mine != 0u ? p.bias[sel_id] : 0.f;
+    const float own = f.fast(sel) + bias;
+    float below = __shfl_down_sync(kAll, own, 1);
+    if (edge) below = value_of(next | kLow);
+    close = pair && own - below <= margin_of(own, below, f.eps);
   } else if constexpr (sizeof(T) == 4) {
-    // equal leading bits of different logits, or at the edge of the selection
-    // (where further logits may share them)
-    const float next_sel = __shfl_down_sync(kAll, sel, 1);
-    again |= lane < p.K && next != 0u && ((mine ^ next) & ~kLow) == 0u && (sel != next_sel || lane == p.K - 1);
+    const float below = __shfl_down_sync(kAll, sel, 1);
+    close = pair && ((mine ^ next) & ~kLow) == 0u && (sel != below || edge);
   }
-  if (__any_sync(kAll, again)) {
-    sel_id = select_exact<NPL>(row, p, kByLogit, lane);
+  if (__any_sync(kAll, again || close)) {
+    bool whole = __any_sync(kAll, again);
+    if (!whole) {
+      // none of the K is below this, and none of the exact K below it less the margin
+      const float low = value_of(__shfl_sync(kAll, mine, p.K - 1) & ~kLow);
+      const float cut = kByLogit ? low : low - margin_of(low, low, f.eps);
+      sel_id = exact_among<NPL>(row, p, f, kByLogit, keep, cut, lane, list, whole);
+    }
+    if (whole) sel_id = select_exact<NPL>(row, p, kByLogit, lane);
     sel = lane < p.K ? to_f32(row[sel_id]) : -INFINITY;
     sel = fminf(fmaxf(sel, -INFINITY), 3.402823466e+38f) + 0.f;
   }

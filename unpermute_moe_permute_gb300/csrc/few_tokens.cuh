@@ -84,8 +84,8 @@ template <int NP, int BITS>
 struct FewTraits {
   static constexpr int k = 1024 / BITS;                  // k of a unit
   static constexpr uint32_t b_box = NP * 128;            // 64 k of the tokens
-  static constexpr bool can_narrow = NP == 16 && BITS == 16;  // (see narrow below)
-  static constexpr int b_boxes = can_narrow ? 2 : k / 64;
+  static constexpr bool can_narrow = NP == 16 && BITS != 8;  // (see narrow below)
+  static constexpr int b_boxes = (can_narrow ? 2 : 1) * k / 64;
   static constexpr uint32_t scales = 2 * kBox16 + b_boxes * b_box;  // 4-bit: two tiles' scales
   static constexpr uint32_t stage = scales + (BITS == 4 ? 2 * 8 * 256 : 0);
   static constexpr int stages = (int)(212992 / stage);   // 5; 4 for N = 64 with 8-bit weights; 4, 4, 3 with 4-bit
@@ -238,7 +238,8 @@ few_tokens_kernel(const __grid_constant__ CUtensorMap mapG, const __grid_constan
                   const __grid_constant__ CUtensorMap mapG64, const __grid_constant__ CUtensorMap mapU64,
                   const __grid_constant__ CUtensorMap mapD, const __grid_constant__ CUtensorMap mapX,
                   const __grid_constant__ CUtensorMap mapAct, const __grid_constant__ CUtensorMap mapGS,
-                  const __grid_constant__ CUtensorMap mapUS, const __grid_constant__ CUtensorMap mapDS,
+                  const __grid_constant__ CUtensorMap mapUS, const __grid_constant__ CUtensorMap mapGS64,
+                  const __grid_constant__ CUtensorMap mapUS64, const __grid_constant__ CUtensorMap mapDS,
                   const FewParams p) {
   using TR = FewTraits<NP, BITS>;
   constexpr bool I8 = BITS == 8, I4 = BITS == 4;
@@ -298,6 +299,10 @@ few_tokens_kernel(const __grid_constant__ CUtensorMap mapG, const __grid_constan
       tma_prefetch_desc(&mapGS);
       tma_prefetch_desc(&mapUS);
       tma_prefetch_desc(&mapDS);
+      if (TR::can_narrow) {
+        tma_prefetch_desc(&mapGS64);
+        tma_prefetch_desc(&mapUS64);
+      }
     }
   }
   if (warp == 1) {
@@ -358,9 +363,11 @@ few_tokens_kernel(const __grid_constant__ CUtensorMap mapG, const __grid_constan
   // up rows together one A operand of 128).  T=1 H=2048 E=128 K=8 I=768: 96
   // whole narrow tiles 32.8 us, 48 tiles in 152 equal runs 35.8 us (from cold).
   const int wide1 = (p.I + 127) / 128, bytes1 = 32 * p.H * BITS;  // of a wide tile
-  const int t_split = A * wide1 * (bytes1 / 1024) / 6550 + 8;              // us
-  const int t_whole = A * wide1 <= G ? bytes1 / 60000 : t_split + 1;
-  const int t_narrow = TR::can_narrow && A * (p.I / 64) <= G ? bytes1 / 120000 : t_split + 1;
+  // (4-bit weights: 30 GB/s of a CTA and 4.1 TB/s of all, the rate of their expansion)
+  constexpr int r_all = I4 ? 4100 : 6550, r_one = I4 ? 30000 : 60000;
+  const int t_split = A * wide1 * (bytes1 / 1024) / r_all + 8;             // us
+  const int t_whole = A * wide1 <= G ? bytes1 / r_one : t_split + 1;
+  const int t_narrow = TR::can_narrow && A * (p.I / 64) <= G ? bytes1 / (2 * r_one) : t_split + 1;
   const bool narrow = t_narrow <= t_split && t_narrow < t_whole;
   const int rows1 = narrow ? 64 : 128;
   const int nt1 = (p.I + rows1 - 1) / rows1, nt2 = (p.H + 255) / 256;
@@ -441,15 +448,22 @@ few_tokens_kernel(const __grid_constant__ CUtensorMap mapG, const __grid_constan
         if (!run) break;
         const uint32_t a = base + s * TR::stage;
         mbar_arrive_expect_tx_warp(full(s), 2 * kBox16 + (I4 ? 512u * p.per1 : 0u));
-        if constexpr (I4) {
+        if (I4 && narrow) {  // of each k block: 64 gate channels, 64 up channels
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t sc = a + TR::scales + 256 * p.per1 * h;
+            tma_load_3d_warp(sc, &mapGS64, full(s), i0, (2 * k + h) * p.per1, e);
+            tma_load_3d_warp(sc + 128 * p.per1, &mapUS64, full(s), i0, (2 * k + h) * p.per1, e);
+          }
+        } else if (I4) {
           tma_load_3d_warp(a + TR::scales, &mapGS, full(s), i0, k * p.per1, e);
           tma_load_3d_warp(a + TR::scales + 256 * p.per1, &mapUS, full(s), i0, k * p.per1, e);
         }
         if (narrow) {  // 64 rows of each, two k blocks
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            tma_load_3d_warp(a + h * kBox16, &mapG64, full(s), k * k1 + h * TR::k, i0, e);
-            tma_load_3d_warp(a + h * kBox16 + kBox16 / 2, &mapU64, full(s), k * k1 + h * TR::k, i0, e);
+            tma_load_3d_warp(a + h * kBox16, &mapG64, full(s), (2 * k + h) * kWide, i0, e);
+            tma_load_3d_warp(a + h * kBox16 + kBox16 / 2, &mapU64, full(s), (2 * k + h) * kWide, i0, e);
           }
         } else {
           tma_load_3d_warp(a, &mapG, full(s), k * kWide, i0, e);
@@ -550,7 +564,8 @@ few_tokens_kernel(const __grid_constant__ CUtensorMap mapG, const __grid_constan
             const uint32_t a = tmem + 512 - 128 * TR::bufs + c * 128;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-              const uint64_t b = bd + (2 * q + h) * (TR::b_box >> 4);
+              // (a narrow tile's boxes are two k blocks, summed in an accumulator each)
+              const uint64_t b = bd + (2 * q + h + (I4 && !two ? 4 * box : 0u)) * (TR::b_box >> 4);
               if constexpr (I4) {
                 umma_f16_ta_k64_warp<false>(d + box * NP, a + box * 64 + h * 32, b, idesc, accum);
               } else {
@@ -628,6 +643,13 @@ few_tokens_kernel(const __grid_constant__ CUtensorMap mapG, const __grid_constan
         if (narrow) {  // lanes 0-63 hold gate, 64-127 up: up crosses through shared memory
           uint32_t v[8];
           tmem_ld_32x32b_x8(d, v);
+          if constexpr (I4) {  // the other k block's sums
+            uint32_t w[8];
+            tmem_ld_32x32b_x8(d + NP, w);
+            tmem_ld_wait();
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = __float_as_uint(__uint_as_float(v[j]) + __uint_as_float(w[j]));
+          }
           tmem_ld_wait();
           float* x = cross + (size_t)col0 * 64 + (r & 63);
           if (r >= 64)
@@ -876,11 +898,12 @@ few_tokens_kernel(const __grid_constant__ CUtensorMap mapG, const __grid_constan
       if (i == 0 || i == n1) {  // (a phase begins)
         const int per = i < n1 ? p.per1 : p.per2;
         const int shift = per == 8 ? 0 : per == 4 ? 1 : 2;  // chunks of 32 k to groups
-        sc_at = base + TR::scales + j * per * 256 + r * 2;
+        const bool half = narrow && i < n1;  // rows of 64 channels: gate's, up's
+        sc_at = base + TR::scales + j * per * 256 + (half && r >= 64 ? per * 128 + (r - 64) * 2 : r * 2);
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
-          for (int q = 0; q < 2 * kParts; ++q) sc_off[h][q] = ((4 * h + 2 * part + q) >> shift) << 8;
+          for (int q = 0; q < 2 * kParts; ++q) sc_off[h][q] = ((4 * h + 2 * part + q) >> shift) << (half ? 7 : 8);
       }
       run = mbar_wait_warp(full(s), ph, abort_flag, p.status);
       if (!run) break;
@@ -948,7 +971,7 @@ int launch_few(FewParams p, const void* x, const FewWeights& w, cudaStream_t s) 
   using TR = FewTraits<NP, BITS>;
   constexpr int esz = BITS == 16 ? 2 : 1, pack = BITS == 4 ? 2 : 1;
   const void *Wg = w.gate, *Wu = w.up, *Wd = w.down;
-  CUtensorMap mg, mu, mg64, mu64, md, mx, ma, mgs = {}, mus = {}, mds = {};
+  CUtensorMap mg, mu, mg64, mu64, md, mx, ma, mgs = {}, mus = {}, mgs64 = {}, mus64 = {}, mds = {};
   const uint64_t d1[3] = {(uint64_t)p.H / pack, (uint64_t)p.I, (uint64_t)p.E};
   const uint64_t d2[3] = {(uint64_t)p.I / pack, (uint64_t)p.H, (uint64_t)p.E};
   const uint32_t bw[3] = {128 / esz, 128, 1}, bw64[3] = {128 / esz, 64, 1};
@@ -964,8 +987,11 @@ int launch_few(FewParams p, const void* x, const FewWeights& w, cudaStream_t s) 
     const uint64_t s1[3] = {(uint64_t)p.I, (uint64_t)p.H * p.per1 / 256, (uint64_t)p.E};
     const uint64_t s2[3] = {(uint64_t)p.H, (uint64_t)p.I * p.per2 / 256, (uint64_t)p.E};
     const uint32_t b1[3] = {128, (uint32_t)p.per1, 1}, b2[3] = {128, (uint32_t)p.per2, 1};
+    const uint32_t b64[3] = {64, (uint32_t)p.per1, 1};
     if (!make_map(&mgs, w.gs, 2, 3, s1, b1, CU_TENSOR_MAP_SWIZZLE_NONE) ||
         !make_map(&mus, w.us, 2, 3, s1, b1, CU_TENSOR_MAP_SWIZZLE_NONE) ||
+        !make_map(&mgs64, w.gs, 2, 3, s1, b64, CU_TENSOR_MAP_SWIZZLE_NONE) ||
+        !make_map(&mus64, w.us, 2, 3, s1, b64, CU_TENSOR_MAP_SWIZZLE_NONE) ||
         !make_map(&mds, w.ds, 2, 3, s2, b2, CU_TENSOR_MAP_SWIZZLE_NONE))
       return MOE_ERR_CUDA;
   }
@@ -987,7 +1013,7 @@ int launch_few(FewParams p, const void* x, const FewWeights& w, cudaStream_t s) 
   cfg.stream = s;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, few_tokens_kernel<NP, BITS>, mg, mu, mg64, mu64, md, mx, ma, mgs, mus, mds, p) != cudaSuccess) {
+  if (cudaLaunchKernelEx(&cfg, few_tokens_kernel<NP, BITS>, mg, mu, mg64, mu64, md, mx, ma, mgs, mus, mgs64, mus64, mds, p) != cudaSuccess) {
     (void)cudaGetLastError();
     return MOE_ERR_CUDA;
   }

@@ -18,6 +18,11 @@
 //   * the scales come by TMA beside the weights they belong to, a column of 128
 //     channels for each group (zeros past the ends, as the weights).
 //
+// Where there are too few tiles for the SMs (a dense layer of a few rows), the
+// pairs of a cluster share a tile's inputs: pair s of S takes the s-th part of k,
+// and pair 0 adds the others' sums, which they write into its shared memory, to
+// its own, in their order.
+//
 // Warps: 1 TMA producer, 1 MMA issuer (in the leading CTA), epilogue warps, and
 // groups of four warps that expand the 128-deep stages in turn.  The barrier of a
 // loaded stage is waited for by the expanding group alone: what its arrival tells
@@ -35,9 +40,10 @@ namespace moe {
 namespace tc {
 namespace {
 
-template <int SUB, int GROUPS, int EPI, int STAGES>
+// SPLIT: pairs that share a tile.
+template <int SUB, int GROUPS, int EPI, int STAGES, int SPLIT = 1>
 struct I4Cfg {
-  static constexpr int kSub = SUB, kGroups = GROUPS, kEpi = EPI, kStages = STAGES;
+  static constexpr int kSub = SUB, kGroups = GROUPS, kEpi = EPI, kStages = STAGES, kSplit = SPLIT;
   static constexpr int kRowTile = 2 * kSub;             // B rows of a tile
   static constexpr uint32_t kB = kRowTile / 2 * 256;    // B bytes of a stage: two 64-deep halves
   static constexpr uint32_t kA = 128 * 64;              // 4-bit A bytes of a stage
@@ -53,9 +59,11 @@ struct I4Cfg {
     return m;
   }
   static constexpr int kFulls = lcm(kStages, kGroups);
-  static constexpr int kBars = kFulls + kStages + 2 * kGroups + 4 + 1;
+  static constexpr int kBars = kFulls + kStages + 2 * kGroups + 4 + 1 + 2;
   static constexpr uint32_t kStageWarp = 2048;  // epilogue staging of a warp
-  static constexpr uint32_t kStage = kStages * (kB + kA + kS);
+  static constexpr uint32_t kPart = kRowTile * 128 * 4;  // sums of another pair: [row][channel]
+  static constexpr uint32_t kParts = kStages * (kB + kA + kS);
+  static constexpr uint32_t kStage = kParts + (kSplit - 1) * kPart;
   static constexpr uint32_t kCtrl = kStage + kEpi * kStageWarp;
   static constexpr uint32_t kHolder = kCtrl + 8 * kBars;
   static constexpr uint32_t kTable = kHolder + 8;  // prefix, offsets, scan scratch
@@ -67,6 +75,8 @@ struct I4Cfg {
 
 using I4Many = I4Cfg<160, 3, 8, 4>;
 using I4Few = I4Cfg<32, 4, 4, 10>;
+using I4Split2 = I4Cfg<32, 4, 4, 8, 2>;
+using I4Split4 = I4Cfg<32, 4, 4, 5, 4>;
 
 struct I4Params {
   const int32_t* off;
@@ -75,6 +85,60 @@ struct I4Params {
   int N, E, Kd, Nout;
   int ch_tiles;    // channel tiles per expert: of 256 (128 for gate/up)
   int per;         // scale groups of a 128-deep stage: 4, 2, 1
+};
+
+// The pairs of a cluster that share a tile: what pair 0 needs to add the others'
+// sums, and they to hand theirs over.
+template <typename C>
+struct SplitTile {
+  uint32_t parts, full, empty;  // shared memory: sums; pair 0's barrier, the others' barrier
+  int pair, rank, lane, quarter;
+  volatile int* abort_flag;
+  int32_t* status;
+  uint32_t tile = 0;  // tiles so far
+  __device__ __forceinline__ uint32_t at(int s, int c) const {
+    return parts + s * C::kPart + (uint32_t)c * 512u + (uint32_t)(quarter * 32 + lane) * 4u;
+  }
+  __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity) const {
+    return __all_sync(0xffffffffu, mbar_wait<true>(bar, parity, abort_flag, status));
+  }
+  __device__ __forceinline__ static void arrive(uint32_t cluster_addr) {
+    __syncwarp();
+    asm volatile(
+        "{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\t"
+        "@q mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];\n\t}" ::"r"(cluster_addr)
+        : "memory");
+  }
+  // the last tile's sums have been read
+  __device__ __forceinline__ bool begin() { return pair == 0 || wait(empty, (tile & 1u) ^ 1u); }
+  __device__ __forceinline__ bool piece(uint32_t (&v)[32], int c) {
+    if (pair != 0) {
+      const uint32_t dst = mapa_shared(at(pair - 1, c), rank);
+#pragma unroll
+      for (int j = 0; j < 32; ++j)
+        asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(dst + j * 512), "r"(v[j]) : "memory");
+      return false;
+    }
+    if (!wait(full, tile & 1u)) return false;
+#pragma unroll
+    for (int s = 0; s < C::kSplit - 1; ++s)
+#pragma unroll
+      for (int j = 0; j < 32; ++j) {
+        float f;
+        asm volatile("ld.shared.f32 %0, [%1];" : "=f"(f) : "r"(at(s, c + j)));
+        v[j] = __float_as_uint(__uint_as_float(v[j]) + f);
+      }
+    return true;
+  }
+  __device__ __forceinline__ void end() {
+    if (pair != 0) {
+      arrive(mapa_shared(full, rank));
+    } else {
+#pragma unroll
+      for (int s = 1; s < C::kSplit; ++s) arrive(mapa_shared(empty, 2 * s + rank));
+    }
+    ++tile;
+  }
 };
 
 template <typename C, bool kSwiglu, typename O>
@@ -99,7 +163,7 @@ gmm_i4_kernel(const __grid_constant__ CUtensorMap mapW0, const __grid_constant__
   auto c_empty = [&](int b) { return bars2 + 8u * (kGroups + b); };
   auto t_full = [&](int a) { return bars2 + 8u * (2 * kGroups + a); };
   auto t_empty = [&](int a) { return bars2 + 8u * (2 * kGroups + 2 + a); };
-  const uint32_t drain = bars2 + 8u * (2 * kGroups + 4);
+  const uint32_t drain = bars2 + 8u * (2 * kGroups + 4), part_full = drain + 8u, part_empty = drain + 16u;
   uint32_t* holder = reinterpret_cast<uint32_t*>(g + C::kHolder);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(g + C::kHolder + 4);
   int32_t* prefix = reinterpret_cast<int32_t*>(g + C::kTable);
@@ -119,6 +183,8 @@ gmm_i4_kernel(const __grid_constant__ CUtensorMap mapW0, const __grid_constant__
       mbar_init(t_empty(a), 2 * kEpi);  // the epilogue warps of both CTAs
     }
     mbar_init(drain, 1);
+    mbar_init(part_full, C::kSplit > 1 ? (C::kSplit - 1) * kEpi : 1);
+    mbar_init(part_empty, kEpi);
     *abort_flag = 0;
     mbar_fence_init();
   }
@@ -149,9 +215,12 @@ gmm_i4_kernel(const __grid_constant__ CUtensorMap mapW0, const __grid_constant__
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *holder;
-  const int rank = (int)cluster_ctarank();
+  // the CTA in its pair, the pair in its cluster and the part of k that it takes
+  const int crank = (int)cluster_ctarank(), rank = crank & 1, leader = crank & ~1, pair = crank >> 1;
+  const uint16_t both = (uint16_t)(3 << leader);
   const int t0 = (int)cluster_id_x(), dt = (int)cluster_count_x();
-  const int stages = (p.Kd + 127) / 128;
+  const int all = (p.Kd + 127) / 128, k_lo = all * pair / C::kSplit;
+  const int stages = all * (pair + 1) / C::kSplit - k_lo;
 
   if (warp == kTmaWarp) {  // the whole warp, one lane elected for each copy
     const uint32_t ub = uniform(base);
@@ -169,11 +238,11 @@ gmm_i4_kernel(const __grid_constant__ CUtensorMap mapW0, const __grid_constant__
         if (!run) break;
         mbar_arrive_expect_tx_warp(q_full(f), tx);
         const uint32_t a = ub + kStages * kB + s * kA, sc = ub + kStages * (kB + kA) + s * kS;
-        tma_load_3d_warp(a, &mapW0, q_full(f), k * 64, ch0, e);
-        tma_load_3d_warp(sc, &mapS0, q_full(f), ch0, k * per, e);
+        tma_load_3d_warp(a, &mapW0, q_full(f), (k_lo + k) * 64, ch0, e);
+        tma_load_3d_warp(sc, &mapS0, q_full(f), ch0, (k_lo + k) * per, e);
         if constexpr (kSwiglu) {
-          tma_load_3d_warp(a + kA / 2, &mapW1, q_full(f), k * 64, ch0, e);
-          tma_load_3d_warp(sc + per * 128, &mapS1, q_full(f), ch0, k * per, e);
+          tma_load_3d_warp(a + kA / 2, &mapW1, q_full(f), (k_lo + k) * 64, ch0, e);
+          tma_load_3d_warp(sc + per * 128, &mapS1, q_full(f), ch0, (k_lo + k) * per, e);
         }
         // this CTA's half of each accumulator's rows, one after the other
 #pragma unroll
@@ -183,9 +252,9 @@ gmm_i4_kernel(const __grid_constant__ CUtensorMap mapW0, const __grid_constant__
             const int nh = j ? nh1 : nh0, rj = r0 + (j ? 2 * nh0 : 0) + rank * nh;
             int r = 0;
             for (; r + 32 <= nh; r += 32, b += 4096)
-              tma_load_2d_warp(b, &mapX32, q_full(f), k * 128 + h * 64, rj + r);
+              tma_load_2d_warp(b, &mapX32, q_full(f), (k_lo + k) * 128 + h * 64, rj + r);
             if (r < nh) {
-              tma_load_2d_warp(b, &mapX16, q_full(f), k * 128 + h * 64, rj + r);
+              tma_load_2d_warp(b, &mapX16, q_full(f), (k_lo + k) * 128 + h * 64, rj + r);
               b += 2048;
             }
           }
@@ -236,16 +305,16 @@ gmm_i4_kernel(const __grid_constant__ CUtensorMap mapW0, const __grid_constant__
             if (subs > 1) umma_f16_ta_k64_warp<true>(d1, a + h * 32, bh + sub1, idesc1, accum);
             accum = 1u;
           }
-          umma_commit_pair_warp(c_empty(b), 3);
-          umma_commit_pair_warp(q_empty(s), 3);
+          umma_commit_pair_warp(c_empty(b), both);
+          umma_commit_pair_warp(q_empty(s), both);
           if (++b == kGroups) b = 0, ph ^= 1u;
           if (++s == kStages) s = 0;
         }
         if (!run) break;
-        for (int j = 0; j < subs; ++j) umma_commit_pair_warp(t_full((it + j) & 1), 3);
+        for (int j = 0; j < subs; ++j) umma_commit_pair_warp(t_full((it + j) & 1), both);
         it += subs;
       }
-      umma_commit_pair_warp(drain, 3);  // the last signal to either CTA
+      umma_commit_pair_warp(drain, both);  // the last signal to either CTA
       mbar_wait_warp(drain, 0, abort_flag, p.status, false);
     }
   } else if (warp >= kAWarp) {
@@ -263,7 +332,7 @@ gmm_i4_kernel(const __grid_constant__ CUtensorMap mapW0, const __grid_constant__
     constexpr uint32_t kScaleRow = kSwiglu ? 128 : 256;
     const int shift = p.per == 4 ? 0 : p.per == 2 ? 1 : 2;  // chunks of 32 inputs to groups
     const uint32_t dst = tmem + kACol + grp * 64 + ((uint32_t)(quarter * 32) << 16);
-    const uint32_t full_of_leader = mapa_shared(c_full(grp), 0);
+    const uint32_t full_of_leader = mapa_shared(c_full(grp), leader);
     const uint32_t mask = int4_mask();
     int s = grp, f = grp, n0 = 0;  // slot, its barrier; stages before this tile (mod kGroups)
     uint32_t ph = 0, bph = 0;
@@ -307,8 +376,14 @@ gmm_i4_kernel(const __grid_constant__ CUtensorMap mapW0, const __grid_constant__
     // the last of the leader's signals to this CTA's barriers has arrived
     if (run) mbar_wait_warp(c_empty(grp), bph ^ 1u, abort_flag, p.status);
   } else {
-    pair_epilogue<C, kSwiglu, false, O>(p, base, g, tmem, warp, lane, rank, t0, dt, total, t_full(0), t_empty(0),
-                                        abort_flag, prefix, offs);
+    auto go = [&](auto&& split) {
+      pair_epilogue<C, kSwiglu, false, O>(p, base, g, tmem, warp, lane, rank, leader, t0, dt, total, t_full(0),
+                                          t_empty(0), abort_flag, prefix, offs, split);
+    };
+    if constexpr (C::kSplit > 1)
+      go(SplitTile<C>{base + C::kParts, part_full, part_empty, pair, rank, lane, warp & 3, abort_flag, p.status});
+    else
+      go(WholeTile());
     // the peer too ends after the leader's last signal, when a wait ran out as well
     if (rank != 0 && warp == kEpiWarp) mbar_wait_warp(drain, 0, abort_flag, p.status, false);
   }
@@ -321,9 +396,11 @@ gmm_i4_kernel(const __grid_constant__ CUtensorMap mapW0, const __grid_constant__
   }
 }
 
+constexpr int kNoRoom = -1;  // more tiles than clusters that can be resident
+
 template <typename C, bool kSwiglu, typename O>
-int launch_cfg(const CUtensorMap (&m)[6], const I4Params& p, cudaStream_t s) {
-  static PerDevice smem_allowed, resident_pairs;
+int launch_cfg(const CUtensorMap (&m)[6], const I4Params& p, long long tiles, cudaStream_t s) {
+  static PerDevice smem_allowed, resident;
   int dev = -1;
   if (cudaGetDevice(&dev) != cudaSuccess) return MOE_ERR_CUDA;
   const int allowed = smem_allowed.get(dev, [] {
@@ -334,11 +411,12 @@ int launch_cfg(const CUtensorMap (&m)[6], const I4Params& p, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute at[2];
   at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = 2;
+  at[0].val.clusterDim.x = 2 * C::kSplit;
   at[0].val.clusterDim.y = 1;
   at[0].val.clusterDim.z = 1;
-  // one persistent CTA per SM, as many whole pairs as can be resident
-  cfg.gridDim = dim3(sm_count() / 2 * 2, 1, 1);
+  // one persistent CTA per SM, as many whole clusters as can be resident
+  constexpr int kCluster = 2 * C::kSplit;
+  cfg.gridDim = dim3(sm_count() / kCluster * kCluster, 1, 1);
   cfg.blockDim = dim3(C::kThreads, 1, 1);
   cfg.dynamicSmemBytes = C::kSmem;
   cfg.stream = s;
@@ -346,13 +424,15 @@ int launch_cfg(const CUtensorMap (&m)[6], const I4Params& p, cudaStream_t s) {
   at[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 2;
-  const int pairs = resident_pairs.get(dev, [&] {
+  const int clusters = resident.get(dev, [&] {
     int n = 0;
     const bool known = cudaOccupancyMaxActiveClusters(&n, gmm_i4_kernel<C, kSwiglu, O>, &cfg) == cudaSuccess;
     (void)cudaGetLastError();
     return known && n > 0 ? n : INT_MAX;
   });
-  if (pairs < (int)cfg.gridDim.x / 2) cfg.gridDim.x = 2 * pairs;
+  if (clusters < (int)cfg.gridDim.x / kCluster) cfg.gridDim.x = kCluster * clusters;
+  // tiles: at most that many, or not known
+  if (C::kSplit > 1 && tiles > (int)cfg.gridDim.x / kCluster) return kNoRoom;
   if (cudaLaunchKernelEx(&cfg, gmm_i4_kernel<C, kSwiglu, O>, m[0], m[1], m[2], m[3], m[4], m[5], p) != cudaSuccess) {
     (void)cudaGetLastError();
     return MOE_ERR_CUDA;
@@ -362,8 +442,13 @@ int launch_cfg(const CUtensorMap (&m)[6], const I4Params& p, cudaStream_t s) {
 }
 
 // Rows per expert, on average, up to which the few-rows form runs (the routing
-// itself is not known on the host).
-constexpr long long few_rows(bool swiglu) { return swiglu ? 64 : 48; }
+// itself is not known on the host).  GB300, E=64 H=2048, random routing, us, few / many:
+//   rows  I=512 gate/up    down        I=768 gate/up    down
+//     24  29.7 / 30.1   18.7 / 19.0    40.7 / 47.7   22.7 / 23.3
+//     48  31.4 / 33.5   19.9 / 20.5    43.4 / 51.3   24.0 / 25.3
+//     64  37.5 / 35.1   25.7 / 21.3    56.3 / 53.4   31.6 / 26.6
+// (at 64 half of the experts have more rows than one tile takes).
+constexpr long long kFewRows = 48;
 
 template <bool kSwiglu, typename O>
 int launch_i4(const void* x, const uint8_t* W0, const void* s0, const uint8_t* W1, const void* s1,
@@ -387,8 +472,15 @@ int launch_i4(const void* x, const uint8_t* W0, const void* s0, const uint8_t* W
     return MOE_ERR_CUDA;
   const int chs = kSwiglu ? 128 : 256;
   const I4Params p{off, out, status, N, E, Kd, Nout, (Nout + chs - 1) / chs, per};
-  return (long long)N <= few_rows(kSwiglu) * E ? launch_cfg<I4Few, kSwiglu, O>(m, p, s)
-                                               : launch_cfg<I4Many, kSwiglu, O>(m, p, s);
+  if ((long long)N > kFewRows * E) return launch_cfg<I4Many, kSwiglu, O>(m, p, 0, s);
+  // Pairs share tiles where all tiles there can be (one for every 64 rows and one
+  // more for every expert with rows) have a cluster of their own, and each pair
+  // two stages at least.
+  const long long tiles = (E == 1 ? (N + 63) / 64 : (long long)(N < E ? N : E) + N / 64) * p.ch_tiles;
+  int rc = kNoRoom;
+  if (Kd >= 1024) rc = launch_cfg<I4Split4, kSwiglu, O>(m, p, tiles, s);
+  if (rc == kNoRoom && Kd >= 512) rc = launch_cfg<I4Split2, kSwiglu, O>(m, p, tiles, s);
+  return rc == kNoRoom ? launch_cfg<I4Few, kSwiglu, O>(m, p, tiles, s) : rc;
 }
 
 int check_i4(const void* x, const int32_t* off, int N, int H, int I, int E, int Kd, int group) {

@@ -353,8 +353,8 @@ gmm_i8_kernel(const __grid_constant__ CUtensorMap mapW0, const __grid_constant__
     // the last of the leader's signals to this CTA's barriers has arrived
     if (run) mbar_wait_warp(c_empty(grp), bph ^ 1u, abort_flag, p.status);
   } else {
-    pair_epilogue<C, kSwiglu, true, O>(p, base, g, tmem, warp, lane, rank, t0, dt, total, t_full(0), t_empty(0),
-                                       abort_flag, prefix, offs);
+    pair_epilogue<C, kSwiglu, true, O>(p, base, g, tmem, warp, lane, rank, 0, t0, dt, total, t_full(0), t_empty(0),
+                                       abort_flag, prefix, offs, WholeTile());
     // the peer too ends after the leader's last signal, when a wait ran out as well
     if (rank != 0 && warp == kEpiWarp) mbar_wait_warp(drain, 0, abort_flag, p.status, false);
   }

@@ -67,15 +67,26 @@ __device__ __forceinline__ float silu(float x) {
   return x * r;
 }
 
+// A tile that one pair of CTAs sums alone.
+struct WholeTile {
+  __device__ __forceinline__ bool begin() { return true; }
+  // v: 32 accumulator columns from column c of the tile on.  Whether this CTA
+  // goes on to write them.
+  __device__ __forceinline__ bool piece(uint32_t (&)[32], int) { return true; }
+  __device__ __forceinline__ void end() {}
+};
+
 // The epilogue warps' part of a kernel: every tile's accumulators to rows of
 // p.out, with SwiGLU where a tile holds gate and up channels.  kScaled: a scale
-// for each channel (p.s0, p.s1) and each row (p.rs).
-template <typename C, bool kSwiglu, bool kScaled, typename O, typename P>
+// for each channel (p.s0, p.s1) and each row (p.rs).  rank: of the CTA in its
+// pair; leader: of the pair's leading CTA in the cluster.  split: how a tile's
+// sums are put together (WholeTile, or pairs that share its inputs).
+template <typename C, bool kSwiglu, bool kScaled, typename O, typename P, typename S>
 __device__ __forceinline__ void pair_epilogue(const P& p, uint32_t base, uint8_t* g, uint32_t tmem, int warp,
-                                              int lane, int rank, int t0, int dt, int total,
+                                              int lane, int rank, int leader, int t0, int dt, int total,
                                               uint32_t t_full, uint32_t t_empty,
                                               volatile int* abort_flag, const int32_t* prefix,
-                                              const int32_t* offs) {
+                                              const int32_t* offs, S&& split) {
   constexpr int kSub = C::kSub, kEpi = C::kEpi;
   // Lanes are channels, accumulator columns are rows; the warps of a quarter take
   // pieces of 32 columns in turn.  A piece is scaled, turned through the warp's
@@ -107,7 +118,8 @@ __device__ __forceinline__ void pair_epilogue(const P& p, uint32_t base, uint8_t
      rs_first = part * 32 + lane < min(x.hi - x.row0, x.n) ? p.rs[r_first] : 0.f;
      rs_second = x.subs > 1 && r_second < x.hi ? p.rs[r_second] : 0.f;
    }
-   for (int sub = 0; sub < x.subs; ++sub, ++it) {
+   run = split.begin();
+   for (int sub = 0; run && sub < x.subs; ++sub, ++it) {
     const int acc = it & 1, row0 = x.row0 + sub * x.n;
     const int rows = min(x.hi - row0, sub ? x.n1 : x.n);
     float rs = sub ? rs_second : rs_first;
@@ -117,7 +129,7 @@ __device__ __forceinline__ void pair_epilogue(const P& p, uint32_t base, uint8_t
     const uint32_t d = tmem + acc * kSub + ((uint32_t)(quarter * 32) << 16);
     auto give_back = [&]() {
       tc_fence_before();
-      mbar_arrive_cluster_warp(mapa_shared(t_empty + 8u * acc, 0));
+      mbar_arrive_cluster_warp(mapa_shared(t_empty + 8u * acc, leader));
     };
     for (int c0 = part * 32; c0 < rows; c0 += 8 * kEpi) {
       uint32_t v[32];
@@ -129,6 +141,7 @@ __device__ __forceinline__ void pair_epilogue(const P& p, uint32_t base, uint8_t
       }
       tmem_ld_wait();
       if (c0 + 8 * kEpi >= rows) give_back();  // the warp's last piece is in registers
+      if (!split.piece(v, sub * x.n + c0)) continue;
       if constexpr (sizeof(O) == 4) {
         // fp32: staging rows of 32 channels, 16 columns at a time
 #pragma unroll
@@ -208,6 +221,7 @@ __device__ __forceinline__ void pair_epilogue(const P& p, uint32_t base, uint8_t
     }
     if (part * 32 >= rows) give_back();  // (it had none)
    }
+   if (run) split.end();
   }
 }
 

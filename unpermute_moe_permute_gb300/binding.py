@@ -187,6 +187,15 @@ def _empty2(n: int, m: int, dtype, like: torch.Tensor) -> torch.Tensor:
     return torch.empty((n, m), dtype=dtype, device=like.device)
 
 
+def _empty_matrices(lead: tuple, n: int, m: int, dtype, like: torch.Tensor) -> torch.Tensor:
+    """An uninitialised [n, m], or [E, n, m] with lead = (E,)."""
+    if not lead:
+        return _empty2(n, m, dtype, like)
+    if _direct(like):
+        return _empty_strided((lead[0], n, m), (n * m, m, 1), dtype)
+    return torch.empty((lead[0], n, m), dtype=dtype, device=like.device)
+
+
 def _ptr(t: Optional[torch.Tensor]):
     if t is None:
         return None
@@ -642,7 +651,7 @@ def moe_router_topk_grouped(logits, K: int, *, bias=None, num_groups: int = 1, t
     is the sum of its group_top largest).  The gradient of the logits is
     moe_router_topk_grad's."""
     T, E = logits.shape
-    if bias is not None:
+    if bias is not None and not (bias.dtype is torch.float32 and bias.shape == (E,)):
         _check(bias, torch.float32, "bias")
         _shape(bias, (E,), "bias")
     if expert_ids is None:
@@ -800,12 +809,12 @@ def moe_quantize_weights_int4(W, group: int = 128, *, W_q=None, scale=None):
         raise ValueError(f"the inputs of a row ({cols}) must be a multiple of 64 and of the group ({group})")
     lead = tuple(W.shape[:-2])
     if W_q is None:
-        W_q = torch.empty(lead + (rows, cols // 2), dtype=torch.uint8, device=W.device)
+        W_q = _empty_matrices(lead, rows, cols // 2, torch.uint8, W)
     else:
         _check(W_q, torch.uint8, "W_q")
         _shape(W_q, lead + (rows, cols // 2), "W_q")
     if scale is None:
-        scale = torch.empty(lead + (cols // group, rows), dtype=torch.bfloat16, device=W.device)
+        scale = _empty_matrices(lead, cols // group, rows, torch.bfloat16, W)
     else:
         _check(scale, torch.bfloat16, "scale")
         _shape(scale, lead + (cols // group, rows), "scale")
@@ -826,7 +835,7 @@ def moe_dequantize_weights_int4(W_q, scale, *, W=None):
     _check(scale, torch.bfloat16, "scale")
     _shape(scale, lead + (cols // group, rows), "scale")
     if W is None:
-        W = torch.empty(lead + (rows, cols), dtype=torch.bfloat16, device=W_q.device)
+        W = _empty_matrices(lead, rows, cols, torch.bfloat16, W_q)
     else:
         _check(W, torch.bfloat16, "W")
         _shape(W, lead + (rows, cols), "W")

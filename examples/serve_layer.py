@@ -1,17 +1,19 @@
 """One MoE layer served and trained through the library's calls.
 
   python examples/serve_layer.py [--tokens 512] [--hidden 2048] [--inter 768]
-                                 [--experts 128] [--topk 8] [--bf16]
+                                 [--experts 128] [--topk 8] [--bf16] [--int4]
+                                 [--groups 8 --top-groups 4]
 
-Layer holds the weights (bf16, and the same in int8 with a scale per channel)
-and runs
+Layer holds the weights (bf16, and the same in int8 with a scale per channel, or
+in 4 bits with a scale for each group of inputs) and runs
   prompts   router -> routing -> rows in int8 -> int8 gate/up + SwiGLU ->
-            rows in int8 -> int8 down -> weighted sum of the K slots
+            rows in int8 -> int8 down -> weighted sum of the K slots; with 4-bit
+            weights bf16 rows -> gate/up + SwiGLU -> down -> weighted sum
   decoding  router -> the whole layer in one launch, for up to 64 tokens, over
-            the int8 or the bf16 weights
+            the int8, the 4-bit or the bf16 weights
   training  router -> bf16 layer forward and backward -> gradient of the
-            router's logits
-The command prints each path's time and how far the int8 paths are from bf16.
+            router's logits; with groups also a step of the experts' biases
+The command prints each path's time and how far the serving paths are from bf16.
 """
 
 import argparse
@@ -26,7 +28,10 @@ from unpermute_moe_permute_gb300 import binding as lib  # noqa: E402
 
 class Layer:
     def __init__(self, H, I, E, K, scoring="softmax", renormalize=True, scale=1.0, seed=0,
-                 device="cuda"):
+                 device="cuda", int4_group=None, groups=None):
+        """int4_group: the inputs that share a scale of the 4-bit weights (None:
+        none are made).  groups: (number, kept, experts that speak for a group)
+        of the router, which then has a bias for each expert."""
         g = torch.Generator(device=device).manual_seed(seed)
 
         def weights(*shape):
@@ -42,17 +47,41 @@ class Layer:
         for w in (self.gate, self.up, self.down):
             q, s = lib.moe_quantize_rows(w.view(-1, w.shape[2]))
             self.int8.append((q.view(w.shape), s.view(w.shape[:2])))
+        self.int4 = None
+        if int4_group is not None:
+            self.int4 = [lib.moe_quantize_weights_int4(w, int4_group)
+                         for w in (self.gate, self.up, self.down)]
+        self.groups = groups
+        self.bias = torch.zeros(E, device=device) if groups is not None else None
         self.status = lib.new_status(device)
 
     def route(self, x):
         """The experts and weights of each token, and the logits."""
         logits = (x @ self.router.t()).float()
-        ids, probs = lib.moe_router_topk(logits, self.K, dev_status=self.status, **self.how)
+        if self.groups is not None:
+            number, kept, each = self.groups
+            ids, probs = lib.moe_router_topk_grouped(
+                logits, self.K, bias=self.bias, num_groups=number, top_groups=kept, group_top=each,
+                dev_status=self.status, **self.how)
+        else:
+            ids, probs = lib.moe_router_topk(logits, self.K, dev_status=self.status, **self.how)
         return ids, probs, logits
 
-    def prompt(self, x):
-        """Any number of tokens [T, H], int8 weights."""
+    def balance(self, tokens_per_expert, rate=1e-3):
+        """A step of the biases: up for experts with fewer tokens than the mean."""
+        n = tokens_per_expert.float()
+        self.bias += rate * torch.sign(n.mean() - n)
+
+    def prompt(self, x, int4=False):
+        """Any number of tokens [T, H], int8 or 4-bit weights."""
         ids, probs, _ = self.route(x)
+        if int4:
+            r = lib.moe_permute(x, ids, self.E, dev_status=self.status)
+            gate, up, down = self.int4
+            act = lib.moe_gate_up_swiglu_int4(r.permuted, r.expert_offsets, *gate, *up,
+                                              dev_status=self.status)
+            y = lib.moe_down_proj_int4(act, r.expert_offsets, *down, dev_status=self.status)
+            return lib.moe_unpermute(y, r.row_map, probs, x.shape[0], self.K)
         r = lib.moe_permute(None, ids, self.E, dev_status=self.status)
         (wg, gs), (wu, us), (wd, ds) = self.int8
         q, s = lib.moe_quantize_rows(x, row_map=r.row_map, K=self.K)
@@ -62,9 +91,13 @@ class Layer:
         y = lib.moe_down_proj_int8(q, s, r.expert_offsets, wd, ds, dev_status=self.status)
         return lib.moe_unpermute(y, r.row_map, probs, x.shape[0], self.K)
 
-    def decode(self, x, int8=True, workspace=None):
+    def decode(self, x, int8=True, workspace=None, int4=False):
         """Up to MOE_FEW_TOKENS tokens [T, H]; the workspace may be kept between calls."""
         ids, probs, _ = self.route(x)
+        if int4:
+            gate, up, down = self.int4
+            return lib.moe_layer_few_tokens_int4(x, ids, probs, *gate, *up, *down,
+                                                 workspace=workspace, dev_status=self.status)
         (wg, gs), (wu, us), (wd, ds) = self.int8
         w = (wg, wu, wd) if int8 else (self.gate, self.up, self.down)
         return lib.moe_layer_few_tokens(x, ids, probs, *w, scales=(gs, us, ds) if int8 else None,
@@ -112,20 +145,28 @@ def main(argv=None):
     p.add_argument("--experts", type=int, default=128)
     p.add_argument("--topk", type=int, default=8)
     p.add_argument("--bf16", action="store_true", help="decode over the bf16 weights")
+    p.add_argument("--int4", action="store_true", help="prompts and decoding over 4-bit weights")
+    p.add_argument("--groups", type=int, default=1, help="groups of experts, by sigmoid scores")
+    p.add_argument("--top-groups", type=int, default=1)
     a = p.parse_args(argv)
-    layer = Layer(a.hidden, a.inter, a.experts, a.topk)
+    size = a.experts // max(a.groups, 1)
+    layer = Layer(a.hidden, a.inter, a.experts, a.topk,
+                  scoring="sigmoid" if a.groups > 1 else "softmax",
+                  int4_group=64 if a.int4 else None,
+                  groups=(a.groups, a.top_groups, min(2, size)) if a.groups > 1 else None)
     x = torch.randn(a.tokens, a.hidden, device="cuda", dtype=torch.bfloat16)
     want, saved = layer.forward(x)
 
     def off(y, ref):
         return float((y.float() - ref.float()).norm() / ref.float().norm())
 
-    print(f"prompt   {a.tokens:5d} tokens  {_time(lambda: layer.prompt(x)):8.1f} us  "
-          f"int8 off bf16 by {off(layer.prompt(x), want):.4f}")
+    print(f"prompt   {a.tokens:5d} tokens  {_time(lambda: layer.prompt(x, int4=a.int4)):8.1f} us  "
+          f"{'4-bit' if a.int4 else 'int8'} off bf16 by {off(layer.prompt(x, int4=a.int4), want):.4f}")
+    how = dict(int8=not a.bf16, int4=a.int4)
     for t in (1, 8, 64):
         if t <= a.tokens:
-            y = layer.decode(x[:t], int8=not a.bf16)
-            print(f"decode   {t:5d} tokens  {_time(lambda: layer.decode(x[:t], int8=not a.bf16)):8.1f} us  "
+            y = layer.decode(x[:t], **how)
+            print(f"decode   {t:5d} tokens  {_time(lambda: layer.decode(x[:t], **how)):8.1f} us  "
                   f"off the bf16 layer by {off(y, want[:t]):.4f}")
     print(f"training {a.tokens:5d} tokens  "
           f"{_time(lambda: layer.backward(want, layer.forward(x)[1]), 5):8.1f} us forward and backward")

@@ -206,6 +206,16 @@ def _ptr(t: Optional[torch.Tensor]):
     raise ValueError("tensor must be contiguous")
 
 
+def _on_current_device(*tensors):
+    """The kernels run on the current device: tensors of another one are refused
+    (CPU tensors are _ptr's to refuse)."""
+    current = _get_device() if _get_device is not None and torch.cuda.is_initialized() else None
+    for t in tensors:
+        if t is not None and t.is_cuda and current is not None and t.get_device() != current:
+            raise ValueError(f"tensor on cuda:{t.get_device()}, but the current device is cuda:{current} "
+                             "(use torch.cuda.device)")
+
+
 def _dtype(t: torch.Tensor) -> int:
     try:
         return _DTYPES[t.dtype]
@@ -664,6 +674,7 @@ def moe_router_topk_grouped(logits, K: int, *, bias=None, num_groups: int = 1, t
     else:
         _check(probs, torch.float32, "probs")
         _shape(probs, (T, K), "probs")
+    _on_current_device(logits, bias, expert_ids, probs, dev_status)
     _call("moe_router_topk_grouped", _ptr(logits), _dtype(logits), _ptr(bias), T, E, K, num_groups,
           top_groups, group_top, _scoring(scoring), int(renormalize), scale, _ptr(expert_ids),
           _ptr(probs), _ptr(dev_status), _stream())
@@ -818,6 +829,7 @@ def moe_quantize_weights_int4(W, group: int = 128, *, W_q=None, scale=None):
     else:
         _check(scale, torch.bfloat16, "scale")
         _shape(scale, lead + (cols // group, rows), "scale")
+    _on_current_device(W, W_q, scale)
     _call("moe_quantize_weights_int4", _ptr(W), _dtype(W), lead[0] if lead else 1, rows, cols, group,
           _ptr(W_q), _ptr(scale), _stream())
     return W_q, scale
@@ -839,6 +851,7 @@ def moe_dequantize_weights_int4(W_q, scale, *, W=None):
     else:
         _check(W, torch.bfloat16, "W")
         _shape(W, lead + (rows, cols), "W")
+    _on_current_device(W_q, scale, W)
     _call("moe_dequantize_weights_int4", _ptr(W_q), _ptr(scale), lead[0] if lead else 1, rows, cols,
           group, _ptr(W), _stream())
     return W
@@ -868,6 +881,7 @@ def moe_gate_up_swiglu_int4(permuted, expert_offsets, W_gate_q, gate_scale, W_up
             _check(t, dt, n)
             _shape(t, shape, n)
     _offsets(expert_offsets, E)
+    _on_current_device(permuted, expert_offsets, W_gate_q, gate_scale, W_up_q, up_scale, act, dev_status)
     _call("moe_gate_up_swiglu_int4", _ptr(permuted), _ptr(expert_offsets), N, H, I, E, group,
           _ptr(W_gate_q), _ptr(gate_scale), _ptr(W_up_q), _ptr(up_scale), _ptr(act),
           _ptr(dev_status), _stream())
@@ -894,6 +908,7 @@ def moe_down_proj_int4(act, expert_offsets, W_down_q, down_scale, *, expanded=No
             _check(t, dt, n)
             _shape(t, shape, n)
     _offsets(expert_offsets, E)
+    _on_current_device(act, expert_offsets, W_down_q, down_scale, expanded, dev_status)
     _call("moe_down_proj_int4", _ptr(act), _ptr(expert_offsets), N, H, I, E, group, _ptr(W_down_q),
           _ptr(down_scale), _ptr(expanded), _dtype(expanded), _ptr(dev_status), _stream())
     return expanded
@@ -990,6 +1005,8 @@ def moe_layer_few_tokens_int4(tokens, expert_ids, probs, W_gate_q, gate_scale, W
             _check(t, dt, n)
             _shape(t, shape, n)
     mask = _mask(active_mask, T, K) if active_mask is not None else None
+    _on_current_device(tokens, expert_ids, probs, W_gate_q, gate_scale, W_up_q, up_scale, W_down_q,
+                       down_scale, mask, shared_x, out, workspace, dev_status)
     _call("moe_layer_few_tokens_int4", _ptr(tokens), _ptr(expert_ids), _ptr(probs), T, H, K, I, E,
           num_special, _ptr(mask), mask.dim() if mask is not None else 0, group, down_group,
           _ptr(W_gate_q), _ptr(gate_scale), _ptr(W_up_q), _ptr(up_scale), _ptr(W_down_q),

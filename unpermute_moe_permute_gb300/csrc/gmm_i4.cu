@@ -9,7 +9,7 @@
 // enough, else the stream of weights and the integer pipe that expands them:
 //
 //   * the weights are the A operand (M = channels): 64 bytes of a row, 128 of
-//     its inputs, go through registers into tensor memory;
+//     its inputs, go through registers into tensor memory at a time;
 //   * the rows are the B operand (N = rows), as they come by TMA: up to 320 of an
 //     expert in two accumulators of 160, so the weights of an expert of up to 320
 //     rows are loaded and expanded once;
@@ -24,10 +24,14 @@
 // its own, in their order.
 //
 // Warps: 1 TMA producer, 1 MMA issuer (in the leading CTA), epilogue warps, and
-// groups of four warps that expand the 128-deep stages in turn.  The barrier of a
-// loaded stage is waited for by the expanding group alone: what its arrival tells
-// the MMA issuer about tensor memory holds for the rows of the stage too, which
-// had landed before.
+// groups of four warps that expand 128 of k in turn.  The barrier of a loaded stage
+// is waited for by the expanding groups alone: what their arrival tells the MMA
+// issuer about tensor memory holds for the rows of the stage too, which had landed
+// before.
+//
+// Few rows: stages are 256 deep, because the copies' 128-byte rows take the TMA unit
+// half the time of 64-byte ones.  (With 128-deep stages 203 tokens of 64 experts,
+// H=2048 I=512, took 29.5 us, now 26.9.)
 #include <limits.h>
 
 #include "common.cuh"
@@ -40,25 +44,28 @@ namespace moe {
 namespace tc {
 namespace {
 
-// SPLIT: pairs that share a tile.
-template <int SUB, int GROUPS, int EPI, int STAGES, int SPLIT = 1>
+// DEEP: k of a stage.  SPLIT: pairs that share a tile.
+template <int SUB, int GROUPS, int EPI, int DEEP, int STAGES, int SPLIT = 1>
 struct I4Cfg {
-  static constexpr int kSub = SUB, kGroups = GROUPS, kEpi = EPI, kStages = STAGES, kSplit = SPLIT;
+  static constexpr int kSub = SUB, kGroups = GROUPS, kEpi = EPI, kDeep = DEEP, kStages = STAGES, kSplit = SPLIT;
+  // The parts of 128 k of a stage go to the groups of a team, the stages to the
+  // teams in turn.
+  static constexpr int kPer = DEEP / 128, kTeams = GROUPS / kPer;
   static constexpr int kRowTile = 2 * kSub;             // B rows of a tile
-  static constexpr uint32_t kB = kRowTile / 2 * 256;    // B bytes of a stage: two 64-deep halves
-  static constexpr uint32_t kA = 128 * 64;              // 4-bit A bytes of a stage
-  static constexpr uint32_t kS = 4 * 128 * 2;           // scales of a stage, at most
+  static constexpr uint32_t kB = kRowTile / 2 * DEEP * 2;  // B bytes of a stage: 64-deep pieces
+  static constexpr uint32_t kA = 128 * DEEP / 2;        // 4-bit A bytes of a stage
+  static constexpr uint32_t kS = DEEP / 32 * 128 * 2;   // scales of a stage, at most
   static constexpr uint32_t kACol = 2 * kSub;           // tensor memory: accumulators, A buffers
   static constexpr int kAWarp = 2 + kEpi;
   static constexpr int kThreads = (kAWarp + 4 * kGroups) * 32;
-  // (A barrier for each slot and group, so that a group meets every phase of its
-  // barriers: with 3 groups and 4 slots it would else see every third.)
+  // (A barrier for each slot and team, so that a team meets every phase of its
+  // barriers: with 3 teams and 4 slots it would else see every third.)
   static constexpr int lcm(int a, int b) {
     int m = a;
     while (m % b) m += a;
     return m;
   }
-  static constexpr int kFulls = lcm(kStages, kGroups);
+  static constexpr int kFulls = lcm(kStages, kTeams);
   static constexpr int kBars = kFulls + kStages + 2 * kGroups + 4 + 1 + 2;
   static constexpr uint32_t kStageWarp = 2048;  // epilogue staging of a warp
   static constexpr uint32_t kPart = kRowTile * 128 * 4;  // sums of another pair: [row][channel]
@@ -70,13 +77,13 @@ struct I4Cfg {
   static constexpr uint32_t kSmem = kTable + 2 * (kMaxExperts + 1) * 4 + 32 * 4 + 1024;
   static_assert(kSmem <= 232448, "more shared memory than one CTA may use");
   static_assert(kACol + kGroups * 64 <= 512, "more tensor memory than there is");
-  static_assert(kGroups <= kStages && kSub % 32 == 0 && kFulls % kGroups == 0, "geometry");
+  static_assert(kTeams <= kStages && kSub % 32 == 0 && kGroups % kPer == 0, "geometry");
 };
 
-using I4Many = I4Cfg<160, 3, 8, 4>;
-using I4Few = I4Cfg<32, 4, 4, 10>;
-using I4Split2 = I4Cfg<32, 4, 4, 8, 2>;
-using I4Split4 = I4Cfg<32, 4, 4, 5, 4>;
+using I4Many = I4Cfg<160, 3, 8, 128, 4>;
+using I4Few = I4Cfg<32, 4, 4, 256, 6>;
+using I4Split2 = I4Cfg<32, 4, 4, 256, 5, 2>;
+using I4Split4 = I4Cfg<32, 4, 4, 256, 3, 4>;
 
 struct I4Params {
   const int32_t* off;
@@ -84,7 +91,7 @@ struct I4Params {
   int32_t* status;
   int N, E, Kd, Nout;
   int ch_tiles;    // channel tiles per expert: of 256 (128 for gate/up)
-  int per;         // scale groups of a 128-deep stage: 4, 2, 1
+  int group;       // inputs of a scale
 };
 
 // The pairs of a cluster that share a tile: what pair 0 needs to add the others'
@@ -148,7 +155,7 @@ gmm_i4_kernel(const __grid_constant__ CUtensorMap mapW0, const __grid_constant__
               const __grid_constant__ CUtensorMap mapX32, const __grid_constant__ CUtensorMap mapX16,
               const I4Params p) {
   constexpr int kSub = C::kSub, kGroups = C::kGroups, kStages = C::kStages, kEpi = C::kEpi;
-  constexpr int kAWarp = C::kAWarp, kFulls = C::kFulls;
+  constexpr int kAWarp = C::kAWarp, kFulls = C::kFulls, kDeep = C::kDeep, kPer = C::kPer, kTeams = C::kTeams;
   constexpr uint32_t kA = C::kA, kB = C::kB, kS = C::kS, kACol = C::kACol;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
@@ -173,7 +180,7 @@ gmm_i4_kernel(const __grid_constant__ CUtensorMap mapW0, const __grid_constant__
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kFulls; ++i) mbar_init(q_full(i), 1);
-    for (int s = 0; s < kStages; ++s) mbar_init(q_empty(s), 4 + 1);  // an expanding group, the MMAs
+    for (int s = 0; s < kStages; ++s) mbar_init(q_empty(s), 4 * kPer + 1);  // a team, the MMAs
     for (int b = 0; b < kGroups; ++b) {
       mbar_init(c_full(b), 2 * 4);  // the leader's: a group of both CTAs
       mbar_init(c_empty(b), 1);
@@ -219,12 +226,12 @@ gmm_i4_kernel(const __grid_constant__ CUtensorMap mapW0, const __grid_constant__
   const int crank = (int)cluster_ctarank(), rank = crank & 1, leader = crank & ~1, pair = crank >> 1;
   const uint16_t both = (uint16_t)(3 << leader);
   const int t0 = (int)cluster_id_x(), dt = (int)cluster_count_x();
-  const int all = (p.Kd + 127) / 128, k_lo = all * pair / C::kSplit;
+  const int all = (p.Kd + kDeep - 1) / kDeep, k_lo = all * pair / C::kSplit;
   const int stages = all * (pair + 1) / C::kSplit - k_lo;
 
   if (warp == kTmaWarp) {  // the whole warp, one lane elected for each copy
     const uint32_t ub = uniform(base);
-    const int per = (int)uniform(p.per);
+    const int per = kDeep / (int)uniform(p.group);
     int s = 0, f = 0, n = 0;  // slot, its barrier, stages so far
     uint32_t ph = 0;
     bool run = true;
@@ -232,29 +239,29 @@ gmm_i4_kernel(const __grid_constant__ CUtensorMap mapW0, const __grid_constant__
       const PairTile x = pair_tile<kSwiglu, kSub>(t, p, prefix, offs, rank);
       const int nh0 = (int)uniform(x.n) / 2, nh1 = (int)uniform(x.n1) / 2, e = (int)uniform(x.e);
       const int ch0 = (int)uniform(x.ch0), r0 = (int)uniform(x.row0);
-      const uint32_t tx = kA + (uint32_t)per * 256u + (uint32_t)(nh0 + nh1) * 256u;
+      const uint32_t tx = kA + (uint32_t)per * 256u + (uint32_t)(nh0 + nh1) * (2u * kDeep);
       for (int k = 0; k < stages; ++k) {
         run = mbar_wait_warp(q_empty(s), ph ^ 1u, abort_flag, p.status);
         if (!run) break;
         mbar_arrive_expect_tx_warp(q_full(f), tx);
         const uint32_t a = ub + kStages * kB + s * kA, sc = ub + kStages * (kB + kA) + s * kS;
-        tma_load_3d_warp(a, &mapW0, q_full(f), (k_lo + k) * 64, ch0, e);
+        tma_load_3d_warp(a, &mapW0, q_full(f), (k_lo + k) * (kDeep / 2), ch0, e);
         tma_load_3d_warp(sc, &mapS0, q_full(f), ch0, (k_lo + k) * per, e);
         if constexpr (kSwiglu) {
-          tma_load_3d_warp(a + kA / 2, &mapW1, q_full(f), (k_lo + k) * 64, ch0, e);
+          tma_load_3d_warp(a + kA / 2, &mapW1, q_full(f), (k_lo + k) * (kDeep / 2), ch0, e);
           tma_load_3d_warp(sc + per * 128, &mapS1, q_full(f), ch0, (k_lo + k) * per, e);
         }
         // this CTA's half of each accumulator's rows, one after the other
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint32_t b = ub + s * kB + h * (kB / 2);
+        for (int h = 0; h < kDeep / 64; ++h) {
+          uint32_t b = ub + s * kB + h * (kB / (kDeep / 64));
           for (int j = 0; j < 2; ++j) {
             const int nh = j ? nh1 : nh0, rj = r0 + (j ? 2 * nh0 : 0) + rank * nh;
             int r = 0;
             for (; r + 32 <= nh; r += 32, b += 4096)
-              tma_load_2d_warp(b, &mapX32, q_full(f), (k_lo + k) * 128 + h * 64, rj + r);
+              tma_load_2d_warp(b, &mapX32, q_full(f), (k_lo + k) * kDeep + h * 64, rj + r);
             if (r < nh) {
-              tma_load_2d_warp(b, &mapX16, q_full(f), (k_lo + k) * 128 + h * 64, rj + r);
+              tma_load_2d_warp(b, &mapX16, q_full(f), (k_lo + k) * kDeep + h * 64, rj + r);
               b += 2048;
             }
           }
@@ -292,22 +299,25 @@ gmm_i4_kernel(const __grid_constant__ CUtensorMap mapW0, const __grid_constant__
         const uint32_t sub1 = (uint32_t)n * 64u >> 4;  // the second's rows in shared memory
         uint32_t accum = 0u;
         for (int k = 0; k < stages; ++k) {
-          run = mbar_wait_warp(c_full(b), ph, abort_flag, p.status);
-          if (!run) break;
-          tc_fence_after();
           const uint64_t bd = bdesc0 + (uint64_t)s * (kB >> 4);
-          const uint32_t a = tm + kACol + b * 64;
-          // (past the end of Kd both operands are zeros)
+          for (int q = 0; run && q < kPer; ++q) {
+            run = mbar_wait_warp(c_full(b), ph, abort_flag, p.status);
+            if (!run) break;
+            tc_fence_after();
+            const uint32_t a = tm + kACol + b * 64;
+            // (past the end of Kd both operands are zeros)
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const uint64_t bh = bd + h * (kB >> 5);
-            umma_f16_ta_k64_warp<true>(d0, a + h * 32, bh, idesc, accum);
-            if (subs > 1) umma_f16_ta_k64_warp<true>(d1, a + h * 32, bh + sub1, idesc1, accum);
-            accum = 1u;
+            for (int h = 0; h < 2; ++h) {
+              const uint64_t bh = bd + (uint64_t)(2 * q + h) * (kB / (kDeep / 64) >> 4);
+              umma_f16_ta_k64_warp<true>(d0, a + h * 32, bh, idesc, accum);
+              if (subs > 1) umma_f16_ta_k64_warp<true>(d1, a + h * 32, bh + sub1, idesc1, accum);
+              accum = 1u;
+            }
+            umma_commit_pair_warp(c_empty(b), both);
+            if (++b == kGroups) b = 0, ph ^= 1u;
           }
-          umma_commit_pair_warp(c_empty(b), both);
+          if (!run) break;
           umma_commit_pair_warp(q_empty(s), both);
-          if (++b == kGroups) b = 0, ph ^= 1u;
           if (++s == kStages) s = 0;
         }
         if (!run) break;
@@ -318,27 +328,29 @@ gmm_i4_kernel(const __grid_constant__ CUtensorMap mapW0, const __grid_constant__
       mbar_wait_warp(drain, 0, abort_flag, p.status, false);
     }
   } else if (warp >= kAWarp) {
-    // ---- expand: a lane takes one 64-byte row of the stage ----
+    // ---- expand: a lane takes 64 bytes of a row of the stage ----
     const int grp = (warp - kAWarp) >> 2, quarter = warp & 3;  // quarter: tensor-memory lanes
+    const int team = grp / kPer, part = grp % kPer;
     // Row of this lane: gate/up stages hold 64 gate rows, then 64 up rows; a warp
     // takes 16 of each, so that gate and up of a channel meet in lanes i and
     // i + 16 of one epilogue warp.
     const int row = kSwiglu ? (lane < 16 ? quarter * 16 + lane : 48 + quarter * 16 + lane) : quarter * 32 + lane;
-    // Chunk c of row r sits at chunk c ^ (r / 2 & 3) (64-byte swizzle).
-    const uint32_t src0 = sA + row * 64 + (((row >> 1) & 3) << 4);
+    // Chunk c of row r sits at chunk c ^ (r / 2 & 3) (64-byte swizzle) or c ^ (r & 7).
+    const uint32_t src0 = sA + row * (kDeep / 2) +
+                          (kDeep == 128 ? ((row >> 1) & 3) << 4 : ((row & 7) ^ (4 * part)) << 4);
     // its scales: 64 (128) channels of the first group, of the second, ...
     const int up = kSwiglu && row >= 64;
-    const uint32_t sc0 = sS + (up ? p.per * 128 : 0) + (row - (up ? 64 : 0)) * 2;
     constexpr uint32_t kScaleRow = kSwiglu ? 128 : 256;
-    const int shift = p.per == 4 ? 0 : p.per == 2 ? 1 : 2;  // chunks of 32 inputs to groups
+    const int shift = p.group == 32 ? 0 : p.group == 64 ? 1 : 2;  // chunks of 32 inputs to groups
+    const uint32_t sc0 = sS + (up ? kDeep / p.group * 128 : 0) + (row - (up ? 64 : 0)) * 2;
     const uint32_t dst = tmem + kACol + grp * 64 + ((uint32_t)(quarter * 32) << 16);
     const uint32_t full_of_leader = mapa_shared(c_full(grp), leader);
     const uint32_t mask = int4_mask();
-    int s = grp, f = grp, n0 = 0;  // slot, its barrier; stages before this tile (mod kGroups)
+    int s = team, f = team, n0 = 0;  // slot, its barrier; stages before this tile (mod kTeams)
     uint32_t ph = 0, bph = 0;
     bool run = true;
     for (int t = t0; run && t < total; t += dt) {
-      for (int k = (grp - n0 + kGroups) % kGroups; k < stages; k += kGroups) {
+      for (int k = (team - n0 + kTeams) % kTeams; k < stages; k += kTeams) {
         run = mbar_wait_warp(q_full(f), ph, abort_flag, p.status);
         if (!run) break;
         uint4 v[4];
@@ -347,7 +359,7 @@ gmm_i4_kernel(const __grid_constant__ CUtensorMap mapW0, const __grid_constant__
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           v[j] = ld_shared_v4(src ^ (j << 4));
-          sc[j] = ld_shared_u16(scs + (j >> shift) * kScaleRow);
+          sc[j] = ld_shared_u16(scs + ((4 * part + j) >> shift) * kScaleRow);
         }
         expand_int4_row(v[0], sc[0], mask, r);
         expand_int4_row(v[1], sc[1], mask, r + 16);
@@ -366,12 +378,12 @@ gmm_i4_kernel(const __grid_constant__ CUtensorMap mapW0, const __grid_constant__
         tc_fence_before();
         mbar_arrive_cluster_warp(full_of_leader);
         bph ^= 1u;
-        s += kGroups;
+        s += kTeams;
         if (s >= kStages) s -= kStages;
-        f += kGroups;
+        f += kTeams;
         if (f >= kFulls) f -= kFulls, ph ^= 1u;
       }
-      n0 = (n0 + stages) % kGroups;
+      n0 = (n0 + stages) % kTeams;
     }
     // the last of the leader's signals to this CTA's barriers has arrived
     if (run) mbar_wait_warp(c_empty(grp), bph ^ 1u, abort_flag, p.status);
@@ -450,37 +462,48 @@ int launch_cfg(const CUtensorMap (&m)[6], const I4Params& p, long long tiles, cu
 // (at 64 half of the experts have more rows than one tile takes).
 constexpr long long kFewRows = 48;
 
+struct I4Call {
+  const void *x, *W0, *s0, *W1, *s1;
+  int group;
+};
+
+template <typename C, bool kSwiglu, typename O>
+int launch_maps(const I4Call& c, I4Params p, long long tiles, cudaStream_t s) {
+  CUtensorMap m[6];
+  const uint32_t ch = kSwiglu ? 64 : 128;
+  const uint64_t dw[3] = {(uint64_t)p.Kd / 2, (uint64_t)p.Nout, (uint64_t)p.E};
+  const uint32_t bw[3] = {C::kDeep / 2, ch, 1};
+  const uint64_t ds[3] = {(uint64_t)p.Nout, (uint64_t)(p.Kd / c.group), (uint64_t)p.E};
+  const uint32_t bs[3] = {ch, (uint32_t)(C::kDeep / c.group), 1};
+  const uint64_t dx[2] = {(uint64_t)p.Kd, (uint64_t)p.N};
+  const uint32_t b32[2] = {64, 32}, b16[2] = {64, 16};
+  const CUtensorMapSwizzle swizzle = C::kDeep == 128 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B;
+  if (!make_map(&m[0], c.W0, 1, 3, dw, bw, swizzle) ||
+      !make_map(&m[1], kSwiglu ? c.W1 : c.W0, 1, 3, dw, bw, swizzle) ||
+      !make_map(&m[2], c.s0, 2, 3, ds, bs, CU_TENSOR_MAP_SWIZZLE_NONE) ||
+      !make_map(&m[3], kSwiglu ? c.s1 : c.s0, 2, 3, ds, bs, CU_TENSOR_MAP_SWIZZLE_NONE) ||
+      !make_map_sw128(&m[4], c.x, 2, 2, dx, b32) || !make_map_sw128(&m[5], c.x, 2, 2, dx, b16))
+    return MOE_ERR_CUDA;
+  return launch_cfg<C, kSwiglu, O>(m, p, tiles, s);
+}
+
 template <bool kSwiglu, typename O>
 int launch_i4(const void* x, const uint8_t* W0, const void* s0, const uint8_t* W1, const void* s1,
               const int32_t* off, int N, int Kd, int Nout, int E, int group, O* out, int32_t* status,
               cudaStream_t s) {
   if (int rc = device_ok()) return rc;
-  CUtensorMap m[6];
-  const int per = 128 / group;
-  const uint32_t ch = kSwiglu ? 64 : 128;
-  const uint64_t dw[3] = {(uint64_t)Kd / 2, (uint64_t)Nout, (uint64_t)E};
-  const uint32_t bw[3] = {64, ch, 1};
-  const uint64_t ds[3] = {(uint64_t)Nout, (uint64_t)(Kd / group), (uint64_t)E};
-  const uint32_t bs[3] = {ch, (uint32_t)per, 1};
-  const uint64_t dx[2] = {(uint64_t)Kd, (uint64_t)N};
-  const uint32_t b32[2] = {64, 32}, b16[2] = {64, 16};
-  if (!make_map(&m[0], W0, 1, 3, dw, bw, CU_TENSOR_MAP_SWIZZLE_64B) ||
-      !make_map(&m[1], kSwiglu ? W1 : W0, 1, 3, dw, bw, CU_TENSOR_MAP_SWIZZLE_64B) ||
-      !make_map(&m[2], s0, 2, 3, ds, bs, CU_TENSOR_MAP_SWIZZLE_NONE) ||
-      !make_map(&m[3], kSwiglu ? s1 : s0, 2, 3, ds, bs, CU_TENSOR_MAP_SWIZZLE_NONE) ||
-      !make_map_sw128(&m[4], x, 2, 2, dx, b32) || !make_map_sw128(&m[5], x, 2, 2, dx, b16))
-    return MOE_ERR_CUDA;
   const int chs = kSwiglu ? 128 : 256;
-  const I4Params p{off, out, status, N, E, Kd, Nout, (Nout + chs - 1) / chs, per};
-  if ((long long)N > kFewRows * E) return launch_cfg<I4Many, kSwiglu, O>(m, p, 0, s);
+  const I4Params p{off, out, status, N, E, Kd, Nout, (Nout + chs - 1) / chs, group};
+  const I4Call c{x, W0, s0, W1, s1, group};
+  if ((long long)N > kFewRows * E) return launch_maps<I4Many, kSwiglu, O>(c, p, 0, s);
   // Pairs share tiles where all tiles there can be (one for every 64 rows and one
   // more for every expert with rows) have a cluster of their own, and each pair
-  // two stages at least.
+  // a stage at least.
   const long long tiles = (E == 1 ? (N + 63) / 64 : (long long)(N < E ? N : E) + N / 64) * p.ch_tiles;
   int rc = kNoRoom;
-  if (Kd >= 1024) rc = launch_cfg<I4Split4, kSwiglu, O>(m, p, tiles, s);
-  if (rc == kNoRoom && Kd >= 512) rc = launch_cfg<I4Split2, kSwiglu, O>(m, p, tiles, s);
-  return rc == kNoRoom ? launch_cfg<I4Few, kSwiglu, O>(m, p, tiles, s) : rc;
+  if (Kd >= 1024 && tiles <= sm_count() / 8) rc = launch_maps<I4Split4, kSwiglu, O>(c, p, tiles, s);
+  if (rc == kNoRoom && Kd >= 512 && tiles <= sm_count() / 4) rc = launch_maps<I4Split2, kSwiglu, O>(c, p, tiles, s);
+  return rc == kNoRoom ? launch_maps<I4Few, kSwiglu, O>(c, p, tiles, s) : rc;
 }
 
 int check_i4(const void* x, const int32_t* off, int N, int H, int I, int E, int Kd, int group) {

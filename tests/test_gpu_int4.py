@@ -262,3 +262,49 @@ def test_prompt_path_in_4_bits_captured(lib):
         # act, the expert's row and the result are rounded to bf16: 2^-9 / sqrt(3) rms each
         assert float((out.double() - want).norm() / want.norm()) < 0.005
     assert int(st) == 0
+
+
+# Where a form begins or ends: rows of one tile and one more, tiles of 64 rows that
+# all have a pair of their own, two pairs to a tile (2048 inputs and more, uneven
+# halves of 9 and of 17 stages), with and without offsets.
+FORMS = [(64, 2048, 1024), (65, 2048, 1024), (200, 1024, 2048), (320, 2304, 1088), (48, 4352, 256), (1, 2048, 64),
+         (33, 2112, 4096), (500, 512, 512)]
+
+
+@pytest.mark.parametrize("N,Kd,Nout", FORMS)
+def test_dense_forms(lib, N, Kd, Nout):
+    x, off, q, s = _case(N + Kd, [N], Kd, Nout, 64, five=False)
+    W = S.weights_int4(q.numpy(), np64(s))
+    want = S.linear_float(np64(x), off.numpy(), W)
+    mag = S.linear_float(np.abs(np64(x)), off.numpy(), np.abs(W))
+    for o in (None, off.to(DEV)):
+        out = lib.moe_down_proj_int4(x.to(DEV), o, q.to(DEV), s.to(DEV), out_dtype=torch.float32)
+        assert_elementwise(np64(out), want, mag, Kd + 2, "f32", "dense")
+
+
+@pytest.mark.parametrize("counts,Kd,Nout", [([3, 0, 60, 1], 2048, 256), ([20, 64, 0, 33, 1, 0, 0, 9], 2304, 320)])
+def test_two_pairs_to_a_tile_of_gate_up(lib, counts, Kd, Nout):
+    x, off, qg, sg = _case(Kd + 1, counts, Kd, Nout, 64)
+    _, _, qu, su = _case(Kd + 2, counts, Kd, Nout, 64)
+    act = lib.moe_gate_up_swiglu_int4(x.to(DEV), off.to(DEV), qg.to(DEV), sg.to(DEV), qu.to(DEV), su.to(DEV))
+    Wg, Wu = S.weights_int4(qg.numpy(), np64(sg)), S.weights_int4(qu.numpy(), np64(su))
+    g, u = S.linear_float(np64(x), off.numpy(), Wg), S.linear_float(np64(x), off.numpy(), Wu)
+    want, ax = S._silu(g) * u, np.abs(np64(x))
+    dg = (Kd + 4) * U32 * S.linear_float(ax, off.numpy(), np.abs(Wg))
+    du = (Kd + 4) * U32 * S.linear_float(ax, off.numpy(), np.abs(Wu))
+    bound = 1.1 * np.abs(u) * dg + np.abs(S._silu(g)) * du + (np.abs(g) + 16) * 2 * U32 * np.abs(want)
+    assert np.all(np.abs(np64(act) - want) <= bound + ulp(np.maximum(np.abs(np64(act)), np.abs(want)), "bf16"))
+
+
+def test_two_pairs_to_a_tile_repeat_in_every_launch(lib):
+    """Sums that one pair writes into another's shared memory, thousands of times."""
+    g = torch.Generator(device=DEV).manual_seed(6)
+    x = torch.randn(19, 2048, device=DEV, generator=g).bfloat16()
+    q = torch.randint(0, 256, (1, 4096, 1024), device=DEV, generator=g, dtype=torch.uint8)
+    s = (torch.rand(1, 32, 4096, device=DEV, generator=g) * 1e-2).bfloat16()
+    st = lib.new_status()
+    want = lib.moe_down_proj_int4(x, None, q, s, dev_status=st).clone()
+    differ = torch.zeros((), dtype=torch.bool, device=DEV)
+    for _ in range(3000):
+        differ |= (lib.moe_down_proj_int4(x, None, q, s, dev_status=st) != want).any()
+    assert not bool(differ) and int(st) == 0

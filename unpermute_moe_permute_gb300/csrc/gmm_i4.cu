@@ -83,7 +83,6 @@ struct I4Cfg {
 using I4Many = I4Cfg<160, 3, 8, 128, 4>;
 using I4Few = I4Cfg<32, 4, 4, 256, 6>;
 using I4Split2 = I4Cfg<32, 4, 4, 256, 5, 2>;
-using I4Split4 = I4Cfg<32, 4, 4, 256, 3, 4>;
 
 struct I4Params {
   const int32_t* off;
@@ -456,9 +455,9 @@ int launch_cfg(const CUtensorMap (&m)[6], const I4Params& p, long long tiles, cu
 // Rows per expert, on average, up to which the few-rows form runs (the routing
 // itself is not known on the host).  GB300, E=64 H=2048, random routing, us, few / many:
 //   rows  I=512 gate/up    down        I=768 gate/up    down
-//     24  29.7 / 30.1   18.7 / 19.0    40.7 / 47.7   22.7 / 23.3
-//     48  31.4 / 33.5   19.9 / 20.5    43.4 / 51.3   24.0 / 25.3
-//     64  37.5 / 35.1   25.7 / 21.3    56.3 / 53.4   31.6 / 26.6
+//     24  26.6 / 29.4   19.6 / 19.3    36.8 / 48.0   22.9 / 23.8
+//     40  29.1 / 32.8   21.3 / 20.9    40.4 / 51.2   25.2 / 26.0
+//     64  35.5 / 34.7   27.7 / 21.7    52.0 / 53.6   33.4 / 27.3
 // (at 64 half of the experts have more rows than one tile takes).
 constexpr long long kFewRows = 48;
 
@@ -495,14 +494,18 @@ int launch_i4(const void* x, const uint8_t* W0, const void* s0, const uint8_t* W
   const int chs = kSwiglu ? 128 : 256;
   const I4Params p{off, out, status, N, E, Kd, Nout, (Nout + chs - 1) / chs, group};
   const I4Call c{x, W0, s0, W1, s1, group};
-  if ((long long)N > kFewRows * E) return launch_maps<I4Many, kSwiglu, O>(c, p, 0, s);
-  // Pairs share tiles where all tiles there can be (one for every 64 rows and one
-  // more for every expert with rows) have a cluster of their own, and each pair
-  // a stage at least.
-  const long long tiles = (E == 1 ? (N + 63) / 64 : (long long)(N < E ? N : E) + N / 64) * p.ch_tiles;
+  // The tiles of 64 rows that there can be: one for every 64 rows, and one more for
+  // every expert with rows.
+  const long long tiles = (E == 1 ? (N - 1) / 64 + 1 : (long long)(N < E ? N : E) + N / 64) * p.ch_tiles;
+  // The few-rows form too where each of its tiles has a pair of its own: smaller
+  // tiles are more SMs then (256 rows, 2048 inputs, 4096 channels 16.2 -> 11.7 us).
+  if (N > kFewRows * E && tiles > sm_count() / 2) return launch_maps<I4Many, kSwiglu, O>(c, p, 0, s);
+  // Two pairs share a tile where all of them have a cluster of their own: 19 rows,
+  // 4096 channels, with 4096 inputs 14.4 -> 11.7 us, 2048 10.2 -> 9.6, 1024 8.2 -> 8.6.
+  // (Four pairs: 10.5 us for 1024 channels, 11.6 with two; of their clusters fewer than 16
+  // can be resident.)
   int rc = kNoRoom;
-  if (Kd >= 1024 && tiles <= sm_count() / 8) rc = launch_maps<I4Split4, kSwiglu, O>(c, p, tiles, s);
-  if (rc == kNoRoom && Kd >= 512 && tiles <= sm_count() / 4) rc = launch_maps<I4Split2, kSwiglu, O>(c, p, tiles, s);
+  if (Kd >= 2048 && tiles <= sm_count() / 4) rc = launch_maps<I4Split2, kSwiglu, O>(c, p, tiles, s);
   return rc == kNoRoom ? launch_maps<I4Few, kSwiglu, O>(c, p, tiles, s) : rc;
 }
 

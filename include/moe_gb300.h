@@ -569,8 +569,9 @@ int moe_down_proj_int8(const int8_t* act_q, const float* row_scale, const int32_
  * moe_down_proj_int4: expanded [N, H] MOE_BF16 or MOE_F32 (out_dtype) from act
  *   [N, I] bf16, W_down_q [E, H, I / 2], down_scale [E, I / group, H].
  * fp32 sums in an order that depends on the sizes and the number of SMs alone, one
- * rounding to the output's dtype.  H and I multiples of 64, at most MOE_INT4_MAX_SIZE; N at most MOE_INT8_MAX_ROWS; rows >= expert_offsets[E]
- * are not touched.  Every pointer is 16-byte aligned. */
+ * rounding to the output's dtype.  H and I multiples of 64, at most
+ * MOE_INT4_MAX_SIZE; N at most MOE_INT8_MAX_ROWS; rows >= expert_offsets[E] are not
+ * touched.  Every pointer is 16-byte aligned. */
 #define MOE_INT4_MAX_SIZE 0x100000
 int moe_quantize_weights_int4(const void* W, int dtype, int E, int rows, int cols, int group,
                               uint8_t* W_q, void* scale, cudaStream_t stream);

@@ -209,11 +209,16 @@ def _ptr(t: Optional[torch.Tensor]):
 def _on_current_device(*tensors):
     """The kernels run on the current device: tensors of another one are refused
     (CPU tensors are _ptr's to refuse)."""
-    current = _get_device() if _get_device is not None and torch.cuda.is_initialized() else None
+    if _get_device is None:
+        return
+    current = None
     for t in tensors:
-        if t is not None and t.is_cuda and current is not None and t.get_device() != current:
-            raise ValueError(f"tensor on cuda:{t.get_device()}, but the current device is cuda:{current} "
-                             "(use torch.cuda.device)")
+        if t is not None and t.is_cuda:
+            if current is None:
+                current = _get_device()
+            if t.get_device() != current:
+                raise ValueError(f"tensor on cuda:{t.get_device()}, but the current device is cuda:{current} "
+                                 "(use torch.cuda.device)")
 
 
 def _dtype(t: torch.Tensor) -> int:
@@ -807,18 +812,25 @@ def _int4_group(scale: torch.Tensor, cols: int, name: str) -> int:
     return cols // groups
 
 
+def _matrices(t: torch.Tensor, name: str):
+    """((E,) or (), rows, columns) of [E, rows, columns] or [rows, columns]."""
+    shape = t.shape
+    if len(shape) == 3:
+        return (shape[0],), shape[1], shape[2]
+    if len(shape) == 2:
+        return (), shape[0], shape[1]
+    raise ValueError(f"{name} must have two or three dimensions, got {len(shape)}")
+
+
 def moe_quantize_weights_int4(W, group: int = 128, *, W_q=None, scale=None):
     """Weights W [E, rows, cols] or [rows, cols] (float32 or bfloat16) in 4 bits
     with a scale for each group (32, 64 or 128) of a row's inputs: (W_q [...,
     rows, cols / 2] uint8, scale [..., cols / group, rows] bfloat16)."""
-    if W.dim() not in (2, 3):
-        raise ValueError(f"W must have two or three dimensions, got {W.dim()}")
+    lead, rows, cols = _matrices(W, "W")
     if group not in _INT4_GROUPS:
         raise ValueError(f"group must be one of {_INT4_GROUPS}, got {group}")
-    rows, cols = W.shape[-2:]
     if cols % 64 or cols % group:
         raise ValueError(f"the inputs of a row ({cols}) must be a multiple of 64 and of the group ({group})")
-    lead = tuple(W.shape[:-2])
     if W_q is None:
         W_q = _empty_matrices(lead, rows, cols // 2, torch.uint8, W)
     else:
@@ -838,10 +850,8 @@ def moe_quantize_weights_int4(W, group: int = 128, *, W_q=None, scale=None):
 def moe_dequantize_weights_int4(W_q, scale, *, W=None):
     """The bfloat16 weights that W_q and scale of moe_quantize_weights_int4
     stand for."""
-    if W_q.dim() not in (2, 3):
-        raise ValueError(f"W_q must have two or three dimensions, got {W_q.dim()}")
-    rows, cols = W_q.shape[-2], 2 * W_q.shape[-1]
-    lead = tuple(W_q.shape[:-2])
+    lead, rows, cols = _matrices(W_q, "W_q")
+    cols *= 2
     group = _int4_group(scale, cols, "scale")
     _check(W_q, torch.uint8, "W_q")
     _check(scale, torch.bfloat16, "scale")

@@ -1037,7 +1037,8 @@ int launch_few(FewParams p, const void* x, const FewWeights& w, cudaStream_t s) 
   cfg.stream = s;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, few_tokens_kernel<NP, BITS, split_act>, mg, mu, mg64, mu64, md, mx, ma, mgs, mus, mgs64, mus64, mds, p) != cudaSuccess) {
+  if (cudaLaunchKernelEx(&cfg, few_tokens_kernel<NP, BITS, split_act>, mg, mu, mg64, mu64, md, mx, ma, mgs,
+                         mus, mgs64, mus64, mds, p) != cudaSuccess) {
     (void)cudaGetLastError();
     return MOE_ERR_CUDA;
   }

@@ -97,6 +97,30 @@ def test_scores_that_32_bits_cannot_tell_apart(lib, scoring):
                    grad=False)
 
 
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("size", [64.0, 1e3, 3e4])
+def test_biases_that_cancel_in_a_group(lib, scoring, size):
+    """A group's two largest are s + size and s' - size: their sum is of the size
+    of a score, its error in fp32 of the biases'."""
+    g = np.random.default_rng(int(size))
+    T, E, G = 400, 64, 8
+    logits = torch.from_numpy(g.standard_normal((T, E))).float().to(DEV)
+    bias = torch.full((E,), -size)
+    bias[::E // G] = size
+    _check(lib, logits, bias.to(DEV), 4, G, 3, 2, scoring, True, grad=False)
+
+
+def test_biases_whose_sums_pass_the_range(lib):
+    """Sums of two beyond fp32's largest, of either sign, beside a group without experts."""
+    of = [2e38, 3e38, 2.5e38, 0.0, -2e38, -3e38, -2.5e38, -float("inf")]
+    bias = torch.tensor(of, dtype=torch.float32, device=DEV).repeat_interleave(4)
+    logits = torch.from_numpy(np.random.default_rng(8).standard_normal((5, 32))).float().to(DEV)
+    for top in range(1, 8):
+        for order in (list(range(32)), list(range(31, -1, -1))):
+            _check(lib, logits, bias[order], 4, 8, top, 2, "sigmoid", True, grad=False)
+            _check(lib, logits, bias[order], min(16, 4 * top), 8, top, 2, "softmax", True, grad=False)
+
+
 def test_many_rows_in_order(lib):
     """A training step's rows: each row's selection against a 64-bit sort."""
     T, E, K, G, top = 16384, 256, 8, 8, 4

@@ -391,7 +391,10 @@ router_grouped_kernel(const T* __restrict__ logits, const __grid_constant__ Grou
     }
     // (a group with one expert of two ranks between those with two and none)
     again = keep && p.each > 1 && a1 > -INFINITY && a2 == -INFINITY;
-    const float v = p.each > 1 ? a1 + a2 : a1;
+    // (a sum past fp32's range is still a sum, and more than none)
+    constexpr float kMost = 3.402823466e+38f;
+    float v = a1;
+    if (p.each > 1) v = a2 > -INFINITY ? fminf(fmaxf(a1 + a2, -kMost), kMost) : -INFINITY;
     int rank = 0;
     for (int h = 0; h < p.G; ++h) {
       const float vh = __shfl_sync(kAll, v, h << p.lg);
@@ -399,10 +402,13 @@ router_grouped_kernel(const T* __restrict__ logits, const __grid_constant__ Grou
     }
     keep = keep && rank < p.top;
     if constexpr (!kByLogit) {  // the border between kept and dropped groups
-      const float lo = value_of(__reduce_min_sync(kAll, keep ? key_of(v) : 0xffffffffu));
-      const float hi = value_of(__reduce_max_sync(kAll, !keep && g < p.G ? key_of(v) : 0u));
+      // A sum's error is that of its scores, the half steps of both with their
+      // biases (which may cancel in the sum) and its own: 3 2^-24 of the two.
+      const float err = f.eps + 0x1p-22f * fabsf(a1) + (p.each > 1 ? 0x1p-22f * fabsf(a2) : 0.f);
+      const float lo = value_of(__reduce_min_sync(kAll, keep ? key_of(v - err) : 0xffffffffu));
+      const float hi = value_of(__reduce_max_sync(kAll, !keep && v > -INFINITY && g < p.G ? key_of(v + err) : 0u));
       // (dropped groups without experts are no question, nor are kept ones)
-      if (hi > -INFINITY && lo > -INFINITY && lo - hi <= 2.f * margin_of(lo, hi, f.eps) + 0x1p-22f * (fabsf(lo) + fabsf(hi))) {  // (sums of two)
+      if (hi > -INFINITY && lo > -INFINITY && lo <= hi) {
         bool fail = __any_sync(kAll, again) || p.G * p.each > 32;
         if (!fail) keep = exact_groups<NPL>(row, p, f, lane, list, fail);
         again |= fail;

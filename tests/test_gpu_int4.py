@@ -199,9 +199,9 @@ def test_corrupt_offsets_stay_inside(lib):
         assert (out[n:] == 3.0).all()
 
 
-@pytest.mark.parametrize("per", [96, 8])
+@pytest.mark.parametrize("per", [160, 96, 64, 8])
 def test_products_repeat_in_every_launch(lib, per):
-    """Every one of thousands of launches of both products in both forms is compared,
+    """Every one of thousands of launches of both products in all forms is compared,
     on the device."""
     E, H, I = 64, 1024, 768
     g = torch.Generator(device=DEV).manual_seed(per + 1)
@@ -294,6 +294,35 @@ def test_two_pairs_to_a_tile_of_gate_up(lib, counts, Kd, Nout):
     du = (Kd + 4) * U32 * S.linear_float(ax, off.numpy(), np.abs(Wu))
     bound = 1.1 * np.abs(u) * dg + np.abs(S._silu(g)) * du + (np.abs(g) + 16) * 2 * U32 * np.abs(want)
     assert np.all(np.abs(np64(act) - want) <= bound + ulp(np.maximum(np.abs(np64(act)), np.abs(want)), "bf16"))
+
+
+# Tiles of one accumulator: up to 80 and up to 128 rows per expert on average, with
+# experts of none, of more than one tile takes and of more than two, and with more
+# tiles than pairs.
+ONE = [([70, 0, 129, 1, 33, 64, 150, 0, 40, 80], 320, 64), ([128] * 3 + [0, 0, 16], 640, 128),
+       ([70, 0, 129, 1, 160, 64, 257, 0], 320, 32), ([161, 0, 320, 31], 64, 64), ([128, 128, 128], 512, 128)]
+
+
+@pytest.mark.parametrize("counts,Kd,group", ONE)
+def test_one_accumulator_to_a_tile(lib, counts, Kd, group):
+    Nout, n = 5248, 2624
+    x, off, q, s = _case(Kd, counts, Kd, Nout, group, five=False)
+    ax = np.abs(np64(x))
+    W = S.weights_int4(q.numpy(), np64(s))
+    want, mag = S.linear_float(np64(x), off.numpy(), W), S.linear_float(ax, off.numpy(), np.abs(W))
+    q, s = q.to(DEV), s.to(DEV)
+    for dt, name in ((torch.float32, "f32"), (torch.bfloat16, "bf16")):
+        out = lib.moe_down_proj_int4(x.to(DEV), off.to(DEV), q, s, out_dtype=dt)
+        assert_elementwise(np64(out), want, mag, Kd + 2, name, "rows")
+    gate, up = slice(0, n), slice(n, 2 * n)
+    part = [t for c in (gate, up) for t in (q[:, c].contiguous(), s[:, :, c].contiguous())]
+    act = lib.moe_gate_up_swiglu_int4(x.to(DEV), off.to(DEV), *part)
+    g, u = want[:, gate], want[:, up]
+    dg, du = (Kd + 4) * U32 * mag[:, gate], (Kd + 4) * U32 * mag[:, up]
+    act_want = S._silu(g) * u
+    bound = 1.1 * np.abs(u) * dg + np.abs(S._silu(g)) * du + (np.abs(g) + 16) * 2 * U32 * np.abs(act_want)
+    bound = bound + ulp(np.maximum(np.abs(np64(act)), np.abs(act_want)), "bf16")
+    assert np.all(np.abs(np64(act) - act_want) <= bound)
 
 
 def test_two_pairs_to_a_tile_repeat_in_every_launch(lib):

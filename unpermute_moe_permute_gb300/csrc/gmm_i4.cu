@@ -12,7 +12,8 @@
 //     its inputs, go through registers into tensor memory at a time;
 //   * the rows are the B operand (N = rows), as they come by TMA: up to 320 of an
 //     expert in two accumulators of 160, so the weights of an expert of up to 320
-//     rows are loaded and expanded once;
+//     rows are loaded and expanded once (fewer rows: one accumulator of 128 or 160,
+//     the other is the next tile's);
 //   * CTA pairs (cta_group::2): 256 channels per MMA, each CTA expands its own
 //     128 channels and holds half of the rows;
 //   * the scales come by TMA beside the weights they belong to, a column of 128
@@ -44,18 +45,18 @@ namespace moe {
 namespace tc {
 namespace {
 
-// DEEP: k of a stage.  SPLIT: pairs that share a tile.
-template <int SUB, int GROUPS, int EPI, int DEEP, int STAGES, int SPLIT = 1>
+// DEEP: k of a stage.  SUBS: accumulators of a tile.  SPLIT: pairs that share a tile.
+template <int SUB, int GROUPS, int EPI, int DEEP, int STAGES, int SUBS = 2, int SPLIT = 1>
 struct I4Cfg {
   static constexpr int kSub = SUB, kGroups = GROUPS, kEpi = EPI, kDeep = DEEP, kStages = STAGES, kSplit = SPLIT;
   // The parts of 128 k of a stage go to the groups of a team, the stages to the
   // teams in turn.
   static constexpr int kPer = DEEP / 128, kTeams = GROUPS / kPer;
-  static constexpr int kRowTile = 2 * kSub;             // B rows of a tile
+  static constexpr int kRowTile = SUBS * kSub;          // B rows of a tile
   static constexpr uint32_t kB = kRowTile / 2 * DEEP * 2;  // B bytes of a stage: 64-deep pieces
   static constexpr uint32_t kA = 128 * DEEP / 2;        // 4-bit A bytes of a stage
   static constexpr uint32_t kS = DEEP / 32 * 128 * 2;   // scales of a stage, at most
-  static constexpr uint32_t kACol = 2 * kSub;           // tensor memory: accumulators, A buffers
+  static constexpr uint32_t kACol = 2 * kSub;           // tensor memory: two accumulators, A buffers
   static constexpr int kAWarp = 2 + kEpi;
   static constexpr int kThreads = (kAWarp + 4 * kGroups) * 32;
   // (A barrier for each slot and team, so that a team meets every phase of its
@@ -82,7 +83,9 @@ struct I4Cfg {
 
 using I4Many = I4Cfg<160, 3, 8, 128, 4>;
 using I4Few = I4Cfg<32, 4, 4, 256, 6>;
-using I4Split2 = I4Cfg<32, 4, 4, 256, 5, 2>;
+using I4Split2 = I4Cfg<32, 4, 4, 256, 5, 2, 2>;
+using I4To80 = I4Cfg<128, 4, 4, 256, 4, 1>;
+using I4To128 = I4Cfg<160, 3, 8, 128, 6, 1>;
 
 struct I4Params {
   const int32_t* off;
@@ -452,14 +455,25 @@ int launch_cfg(const CUtensorMap (&m)[6], const I4Params& p, long long tiles, cu
   return MOE_OK;
 }
 
-// Rows per expert, on average, up to which the few-rows form runs (the routing
-// itself is not known on the host).  GB300, E=64 H=2048, random routing, us, few / many:
-//   rows  I=512 gate/up    down        I=768 gate/up    down
-//     24  26.6 / 29.4   19.6 / 19.3    36.8 / 48.0   22.9 / 23.8
-//     40  29.1 / 32.8   21.3 / 20.9    40.4 / 51.2   25.2 / 26.0
-//     64  35.5 / 34.7   27.7 / 21.7    52.0 / 53.6   33.4 / 27.3
-// (at 64 half of the experts have more rows than one tile takes).
-constexpr long long kFewRows = 48;
+// Rows per expert, on average, up to which a form runs (the routing itself is not
+// known on the host).  Tiles of one accumulator hold few enough rows that a slot
+// has room for more or longer stages, and the epilogue overlaps the next tile;
+// experts of more rows than it takes have their weights expanded again for each
+// tile.  GB300, random routing, gate/up and down, us, I4Few, I4To80, I4To128, I4Many:
+//   rows  E=128 H=2048 I=768                    E=128 H=4096 I=1536
+//     24  63+41  --     71+41   85+51          209+113  --       242+131  301+159
+//     40  69+45  71+45  77+45   89+53          223+125  242+132  264+140  311+164
+//     64  --     75+47  81+48   93+56            --     251+137  277+145  323+169
+//     96  --     81+49  85+50   97+60            --     269+146  291+154  339+176
+//    128  --    108+66  92+53  102+62            --     387+216  312+171  351+185
+//    160  --     --    118+70  111+69            --      --      455+241  391+212
+// and with experts' shares as 1 / sqrt(rank), E=128 H=2048 I=768:
+//     48  77+51  --     79+46   92+55      (40: 73+48  72+45  77+45  91+54)
+//     64  --     77+49  82+49   95+57
+//     96  --     91+57  92+55  101+61
+//    128  --    104+64 103+60  109+67
+//    160  --     --    112+68  111+73
+constexpr long long kFewRows = 40, kRowsTo80 = 80, kRowsTo128 = 128;
 
 struct I4Call {
   const void *x, *W0, *s0, *W1, *s1;
@@ -499,7 +513,11 @@ int launch_i4(const void* x, const uint8_t* W0, const void* s0, const uint8_t* W
   const long long tiles = (E == 1 ? (N - 1) / 64 + 1 : (long long)(N < E ? N : E) + N / 64) * p.ch_tiles;
   // The few-rows form too where each of its tiles has a pair of its own: smaller
   // tiles are more SMs then (256 rows, 2048 inputs, 4096 channels 16.2 -> 11.7 us).
-  if (N > kFewRows * E && tiles > sm_count() / 2) return launch_maps<I4Many, kSwiglu, O>(c, p, 0, s);
+  if (N > kFewRows * E && tiles > sm_count() / 2) {
+    if (N > kRowsTo128 * E) return launch_maps<I4Many, kSwiglu, O>(c, p, 0, s);
+    if (N > kRowsTo80 * E) return launch_maps<I4To128, kSwiglu, O>(c, p, 0, s);
+    return launch_maps<I4To80, kSwiglu, O>(c, p, 0, s);
+  }
   // Two pairs share a tile where all of them have a cluster of their own: 19 rows,
   // 4096 channels, with 4096 inputs 14.4 -> 11.7 us, 2048 10.2 -> 9.6, 1024 8.2 -> 8.6.
   // (Four pairs: 10.5 us for 1024 channels, 11.6 with two; of their clusters fewer than 16

@@ -52,6 +52,13 @@ struct I4Cfg {
   // The parts of 128 k of a stage go to the groups of a team, the stages to the
   // teams in turn.
   static constexpr int kPer = DEEP / 128, kTeams = GROUPS / kPer;
+  // The first accumulator's products go ahead of the second's: two parts (128 k) at
+  // a tile's beginning, while the second's last sums are still being read, three at
+  // its end, so that the first's can be.  (256 rows of each of 128 experts, H=2048
+  // I=768: gate/up 143 -> 133 us, down 90 -> 82; with two and two 135 and 80, three
+  // and two 135 and 85.  The forms for few rows take 3 to 20 % longer with that loop.)
+  static constexpr bool kAhead = SUBS == 2 && kPer == 1;
+  static constexpr int kHead = 2, kTail = 3;
   static constexpr int kRowTile = SUBS * kSub;          // B rows of a tile
   static constexpr uint32_t kB = kRowTile / 2 * DEEP * 2;  // B bytes of a stage: 64-deep pieces
   static constexpr uint32_t kA = 128 * DEEP / 2;        // 4-bit A bytes of a stage
@@ -78,6 +85,7 @@ struct I4Cfg {
   static constexpr uint32_t kSmem = kTable + 2 * (kMaxExperts + 1) * 4 + 32 * 4 + 1024;
   static_assert(kSmem <= 232448, "more shared memory than one CTA may use");
   static_assert(kACol + kGroups * 64 <= 512, "more tensor memory than there is");
+  static_assert(!kAhead || (kHead <= kGroups && kTail <= kGroups && kGroups <= kStages), "parts ahead");
   static_assert(kTeams <= kStages && kSub % 32 == 0 && kGroups % kPer == 0, "geometry");
 };
 
@@ -283,6 +291,7 @@ gmm_i4_kernel(const __grid_constant__ CUtensorMap mapW0, const __grid_constant__
     if (rank == 0) {  // the whole warp, one lane elected for each MMA
       const uint64_t bdesc0 = desc_sw128(uniform(sB), 16, 1024);
       const uint32_t tm = uniform(tmem);
+      constexpr uint64_t kPiece = kB / (kDeep / 64) >> 4;  // 64 of k of a stage's rows
       int b = 0, s = 0, it = 0;
       uint32_t ph = 0;
       bool run = true;
@@ -291,39 +300,81 @@ gmm_i4_kernel(const __grid_constant__ CUtensorMap mapW0, const __grid_constant__
         const int n = (int)uniform(x.n), subs = (int)uniform(x.subs);
         const uint32_t idesc = idesc_bf16_f32(256, n, false, false);
         const uint32_t idesc1 = idesc_bf16_f32(256, (int)uniform(x.n1), false, false);
-        // accumulators it, it + 1 (mod 2), as they become free
-        for (int j = 0; run && j < subs; ++j)
+        // accumulator it + j (mod 2) is free
+        auto acc_wait = [&](int j) {
           run = __all_sync(0xffffffffu, mbar_wait<true>(t_empty((it + j) & 1), (((it + j) >> 1) & 1) ^ 1u,
                                                         abort_flag, p.status));
-        if (!run) break;
-        tc_fence_after();
+          tc_fence_after();
+          return run;
+        };
+        if (!acc_wait(0)) break;
         const uint32_t d0 = tm + (it & 1) * kSub, d1 = tm + ((it + 1) & 1) * kSub;
         const uint32_t sub1 = (uint32_t)n * 64u >> 4;  // the second's rows in shared memory
-        uint32_t accum = 0u;
-        for (int k = 0; k < stages; ++k) {
-          const uint64_t bd = bdesc0 + (uint64_t)s * (kB >> 4);
-          for (int q = 0; run && q < kPer; ++q) {
-            run = mbar_wait_warp(c_full(b), ph, abort_flag, p.status);
-            if (!run) break;
-            tc_fence_after();
-            const uint32_t a = tm + kACol + b * 64;
-            // (past the end of Kd both operands are zeros)
+        if constexpr (C::kAhead) {
+          for (int k = 0; k < stages;) {
+            const int left = stages - k;
+            const int ahead = subs == 1 ? 1 : k == 0 ? min(C::kHead, left) : left <= C::kTail ? left : 1;
+            int b1 = b, s1 = s;
+            for (int i = 0; i < ahead; ++i) {
+              run = mbar_wait_warp(c_full(b1), b1 < b ? ph ^ 1u : ph, abort_flag, p.status);
+              if (!run) break;
+              tc_fence_after();
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const uint64_t bh = bd + (uint64_t)(2 * q + h) * (kB / (kDeep / 64) >> 4);
-              umma_f16_ta_k64_warp<true>(d0, a + h * 32, bh, idesc, accum);
-              if (subs > 1) umma_f16_ta_k64_warp<true>(d1, a + h * 32, bh + sub1, idesc1, accum);
-              accum = 1u;
+              for (int h = 0; h < 2; ++h)
+                umma_f16_ta_k64_warp<true>(d0, tm + kACol + b1 * 64 + h * 32, bdesc0 + (uint64_t)s1 * (kB >> 4) + h * kPiece,
+                                           idesc, (uint32_t)(k + i + h > 0));
+              if (++b1 == kGroups) b1 = 0;
+              if (++s1 == kStages) s1 = 0;
             }
-            umma_commit_pair_warp(c_empty(b), both);
-            if (++b == kGroups) b = 0, ph ^= 1u;
+            if (!run) break;
+            if (subs > 1) {
+              if (k == 0 && !acc_wait(1)) break;
+              if (ahead == left) umma_commit_pair_warp(t_full(it & 1), both);
+            }
+            for (int i = 0; i < ahead; ++i, ++k) {
+              if (subs > 1) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                  umma_f16_ta_k64_warp<true>(d1, tm + kACol + b * 64 + h * 32,
+                                             bdesc0 + (uint64_t)s * (kB >> 4) + h * kPiece + sub1, idesc1,
+                                             (uint32_t)(k + h > 0));
+              }
+              umma_commit_pair_warp(c_empty(b), both);
+              if (++b == kGroups) b = 0, ph ^= 1u;
+              umma_commit_pair_warp(q_empty(s), both);
+              if (++s == kStages) s = 0;
+            }
           }
           if (!run) break;
-          umma_commit_pair_warp(q_empty(s), both);
-          if (++s == kStages) s = 0;
+        } else {
+          if (subs > 1 && !acc_wait(1)) break;
+          uint32_t accum = 0u;
+          for (int k = 0; k < stages; ++k) {
+            const uint64_t bd = bdesc0 + (uint64_t)s * (kB >> 4);
+            for (int q = 0; run && q < kPer; ++q) {
+              run = mbar_wait_warp(c_full(b), ph, abort_flag, p.status);
+              if (!run) break;
+              tc_fence_after();
+              const uint32_t a = tm + kACol + b * 64;
+              // (past the end of Kd both operands are zeros)
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                const uint64_t bh = bd + (uint64_t)(2 * q + h) * kPiece;
+                umma_f16_ta_k64_warp<true>(d0, a + h * 32, bh, idesc, accum);
+                if (subs > 1) umma_f16_ta_k64_warp<true>(d1, a + h * 32, bh + sub1, idesc1, accum);
+                accum = 1u;
+              }
+              umma_commit_pair_warp(c_empty(b), both);
+              if (++b == kGroups) b = 0, ph ^= 1u;
+            }
+            if (!run) break;
+            umma_commit_pair_warp(q_empty(s), both);
+            if (++s == kStages) s = 0;
+          }
+          if (!run) break;
+          if (subs > 1) umma_commit_pair_warp(t_full(it & 1), both);
         }
-        if (!run) break;
-        for (int j = 0; j < subs; ++j) umma_commit_pair_warp(t_full((it + j) & 1), both);
+        umma_commit_pair_warp(t_full((it + subs - 1) & 1), both);
         it += subs;
       }
       umma_commit_pair_warp(drain, both);  // the last signal to either CTA
@@ -466,7 +517,7 @@ int launch_cfg(const CUtensorMap (&m)[6], const I4Params& p, long long tiles, cu
 //     64  --     75+47  81+48   93+56            --     251+137  277+145  323+169
 //     96  --     81+49  85+50   97+60            --     269+146  291+154  339+176
 //    128  --    108+66  92+53  102+62            --     387+216  312+171  351+185
-//    160  --     --    118+70  111+69            --      --      455+241  391+212
+//    160  --     --    118+70  110+68            --      --      455+241  391+212
 // and with experts' shares as 1 / sqrt(rank), E=128 H=2048 I=768:
 //     48  77+51  --     79+46   92+55      (40: 73+48  72+45  77+45  91+54)
 //     64  --     77+49  82+49   95+57

@@ -121,6 +121,25 @@ def test_biases_whose_sums_pass_the_range(lib):
             _check(lib, logits, bias[order], min(16, 4 * top), 8, top, 2, "softmax", True, grad=False)
 
 
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("E,K,G,top,each", [(256, 8, 8, 4, 2), (512, 16, 4, 2, 1), (96, 9, 1, 1, 1), (40, 3, 10, 3, 2)])
+def test_rows_of_one_logit(lib, E, K, G, top, each, dtype, scoring):
+    """Padding rows: every logit and every bias the same, all but one of them, all but
+    the first, and all masked."""
+    l = torch.zeros(7, E)
+    l[1] = 2.5
+    l[2, E - 1] = 2.0 ** -7
+    l[3, 0] = -1.0
+    l[4] = -float("inf")
+    l[5] = float("inf")
+    l[6, E // 2] = -float("inf")
+    flat, last = torch.full((E,), 0.125), torch.full((E,), 0.125)
+    last[E - 1] = 0.25
+    for b in (None, torch.zeros(E), flat, last, torch.full((E,), -float("inf"))):
+        _check(lib, l.to(dtype).to(DEV), None if b is None else b.to(DEV), K, G, top, each, scoring, True, grad=False)
+
+
 def test_many_rows_in_order(lib):
     """A training step's rows: each row's selection against a 64-bit sort."""
     T, E, K, G, top = 16384, 256, 8, 8, 4

@@ -19,7 +19,9 @@
 // the whole row in 64 bits (select_exact).  Of normal logits at E = 256 in 8 groups
 // K = 8 two rows in a thousand need it.  The whole row takes a warp 7 us of the slow
 // 64-bit pipe, which at first was half of the launch, its tail (16384 rows 38 us,
-// now 21; softmax, whose sum takes the row's exponentials in 64 bits, 38 and 26).  Where no score is needed (no bias, and no
+// now 21; softmax, whose sum takes the row's exponentials in 64 bits, 38 and 26).
+// Rows of one logit and one bias, as padding gives them, are in the order of the
+// index and need neither (16384 of them 413 us by the whole row, now 22).  Where no score is needed (no bias, and no
 // sum of two) the logits themselves are compared and their keys hold the whole
 // index, as in the plain router.
 #include <type_traits>
@@ -105,6 +107,16 @@ __device__ __forceinline__ double exact_sum(const T* row, const GroupParams& p, 
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(kAll, s, d);
   return s;
+}
+
+// Whether all of the row's experts have one logit and one bias (padding rows of
+// zeros): their order is that of the index.
+template <typename T>
+__device__ __noinline__ bool all_the_same(const T* row, const GroupParams& p, int lane) {
+  const float l = to_f32(row[0]), b = p.bias ? p.bias[0] : 0.f;
+  bool same = l > -INFINITY && b > -INFINITY && b < INFINITY;
+  for (int j = lane; same && j < p.E; j += 32) same = to_f32(row[j]) == l && (!p.bias || p.bias[j] == b);
+  return __all_sync(kAll, same);
 }
 
 // Whether the group of this lane is kept, by the exact sums of its
@@ -409,7 +421,7 @@ router_grouped_kernel(const T* __restrict__ logits, const __grid_constant__ Grou
       const float hi = value_of(__reduce_max_sync(kAll, !keep && v > -INFINITY && g < p.G ? key_of(v + err) : 0u));
       // (dropped groups without experts are no question, nor are kept ones)
       if (hi > -INFINITY && lo > -INFINITY && lo <= hi) {
-        bool fail = __any_sync(kAll, again) || p.G * p.each > 32;
+        bool fail = all_the_same(row, p, lane) || __any_sync(kAll, again) || p.G * p.each > 32;
         if (!fail) keep = exact_groups<NPL>(row, p, f, lane, list, fail);
         again |= fail;
       }
@@ -461,7 +473,10 @@ router_grouped_kernel(const T* __restrict__ logits, const __grid_constant__ Grou
   }
   if (__any_sync(kAll, again || close)) {
     bool whole = __any_sync(kAll, again);
-    if (!whole) {
+    if (all_the_same(row, p, lane)) {
+      sel_id = lane;
+      whole = false;
+    } else if (!whole) {
       // none of the K is below this, and none of the exact K below it less the margin
       const float low = value_of(__shfl_sync(kAll, mine, p.K - 1) & ~kLow);
       const float cut = kByLogit ? low : low - margin_of(low, low, f.eps);

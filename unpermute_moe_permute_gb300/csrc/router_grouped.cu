@@ -21,9 +21,9 @@
 // 64-bit pipe, which at first was half of the launch, its tail (16384 rows 38 us,
 // now 21; softmax, whose sum takes the row's exponentials in 64 bits, 38 and 26).
 // Rows of one logit and one bias, as padding gives them, are in the order of the
-// index and need neither (16384 of them 413 us by the whole row, now 22).  Where no score is needed (no bias, and no
-// sum of two) the logits themselves are compared and their keys hold the whole
-// index, as in the plain router.
+// index and need neither (16384 of them 413 us by the whole row, now 22).
+// Where no score is needed (no bias, and no sum of two) the logits themselves are
+// compared and their keys hold the whole index, as in the plain router.
 #include <type_traits>
 
 #include "router.cuh"

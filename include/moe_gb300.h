@@ -629,7 +629,7 @@ int moe_layer_few_tokens(const void* tokens, const int32_t* expert_ids, const fl
  * gate_scale, up_scale [E, H / group, I], W_down_q [E, H, I / 2] with down_scale
  * [E, I / down_group, H] (bf16), the weights being bf16(q * scale) as in the
  * products above.  H a multiple of group, I of down_group; the scales 16-byte
- * aligned.  Up to 8 tokens act keeps 16 significant bits.  All else as there, the
+ * aligned.  act keeps 16 significant bits (two bf16).  All else as there, the
  * workspace's size too. */
 int moe_layer_few_tokens_int4(const void* tokens, const int32_t* expert_ids, const float* probs,
                               int T, int H, int K, int I, int E, int num_special,

@@ -235,13 +235,17 @@ def linear_float(x, offsets, W):
 
 
 def layer_few_tokens(x, ids, probs, Wg, Wu, Wd, E: int, num_special: int = 0, mask=None,
-                     shared=None, gs=None, us=None, ds=None):
-    """(out [T, H], bound [T, H]).  bound: what fp32 sums in any order and one
-    rounding of act to bfloat16 can add up to, without the rounding of out:
-      dg  = (H + 4) 2^-24 sum |w x|,  du alike  (the scale's product included)
-      dact <= |silu'(g) u| dg + |silu(g)| du + dg du + (2^-9 + 2^-20) |act|
+                     shared=None, gs=None, us=None, ds=None, act_rounding=2.0 ** -9, exact_sums=False):
+    """(out [T, H], bound [T, H]).  bound: what fp32 sums in any order and act's
+    rounding add up to, without the rounding of out:
+      dg  = (H + 4) 2^-24 sum |w x|,  du alike  (the scale's product included);
+            0 with exact_sums, for data whose sums are exact in fp32
+      dact <= |silu'(g) u| dg + |silu(g)| du + dg du + (act_rounding + 2^-20) |act|
               (silu' is in [-0.1, 1.1])
       dout <= sum_k |p| (|Wd| dact + (I + 2 K + 8) 2^-24 |Wd| |act|)
+    act_rounding: 2^-9 for act in one bfloat16, half of what a single rounding can
+    reach and more than a sum of I of them does; 2^-16 for act as a bfloat16 and
+    the bfloat16 of what that leaves, each off by 2^-8 of its value at most.
     """
     x = np.asarray(x, dtype=np.float64)
     T, H = x.shape
@@ -269,10 +273,10 @@ def layer_few_tokens(x, ids, probs, Wg, Wu, Wd, E: int, num_special: int = 0, ma
             act = _silu(g) * u
             p = float(probs[t, k])
             out[t] += p * (wd @ act)
-            dg = (H + 4) * u32 * (np.abs(wg) @ np.abs(x[t]))
-            du = (H + 4) * u32 * (np.abs(wu) @ np.abs(x[t]))
+            dg = (0 if exact_sums else H + 4) * u32 * (np.abs(wg) @ np.abs(x[t]))
+            du = (0 if exact_sums else H + 4) * u32 * (np.abs(wu) @ np.abs(x[t]))
             dact = 1.1 * np.abs(u) * dg + np.abs(_silu(g)) * du + 1.1 * dg * du \
-                + (2.0 ** -9 + 2.0 ** -20) * np.abs(act)
+                + (act_rounding + 2.0 ** -20) * np.abs(act)
             bound[t] += abs(p) * (np.abs(wd) @ (dact * (1 + 2.0 ** -10))
                                   + (I + 2 * K + 8) * u32 * (np.abs(wd) @ np.abs(act)))
     return out, bound

@@ -19,17 +19,21 @@
 //     tokens, which the tensor cores have time for (at N = 64 they are busy 16 %
 //     of the time with bf16 weights, 24 % with 8-bit ones), and a (token,
 //     expert) pair that was not chosen is left out when the result is read;
-//   * one warp streams weights through a ring of 4 or 5 stages (TMA) without
+//   * one warp streams weights through a ring of 3 to 5 stages (TMA) without
 //     ever waiting for results: at the turn from phase 1 to phase 2 it fills
 //     the ring with down weights while the last activations are still being
 //     made.  Another warp loads the tokens' and activations' tiles and alone
-//     waits for an expert's activations to be complete.
+//     waits for an expert's activations to be complete.  For up to 16 tokens and
+//     16- or 4-bit weights phase 1 may take narrow tiles: 64 gate and 64 up rows
+//     in each of two k blocks;
 //   * 8-bit weights go from the ring through registers to tensor memory as
 //     bf16 (exact) and are the A operand there; the scale of a channel is a
 //     lane's own factor in the epilogue;
 //   * 4-bit weights go the same way, 256 of k in a unit of the same bytes, each
 //     multiplied by its group's scale as it is expanded (exact for scales of five
-//     significant bits).  The scales come by TMA beside their weights.
+//     significant bits).  The scales come by TMA beside their weights.  The tokens'
+//     tiles have a ring of their own, 128 of k in a slot, so that a stage is free as
+//     soon as it is expanded.
 //
 // CTAs wait for one another, so the launch is cooperative (all of it
 // resident); every wait is bounded.  The counters are zeroed by the kernel
@@ -69,7 +73,7 @@ struct FewParams {
   const float *gs, *us, *ds;
   const __nv_bfloat16* shared_x;
   __nv_bfloat16* out;
-  __nv_bfloat16* act;          // [A, T, I]; split_act: [A, 2, T, I]
+  __nv_bfloat16* act;          // [A, T, I]; 4-bit weights: [A, 2, T, I]
   float *part1, *part2;        // [CTA][2][T][2][128], [CTA][2][T][256]
   unsigned long long* epoch;   // epoch, flag of each CTA
   uint32_t* count;             // ready[A], tiles of phase 1, tiles of phase 2, seen
@@ -84,25 +88,35 @@ struct FewTraits {
   static constexpr uint32_t b_box = NP * 128;            // 64 k of the tokens
   static constexpr bool can_narrow = NP == 16 && BITS != 8;  // (see narrow below)
   static constexpr int b_boxes = (can_narrow ? 2 : 1) * k / 64;
-  static constexpr uint32_t scales = 2 * kBox16 + b_boxes * b_box;  // 4-bit: two tiles' scales
-  static constexpr uint32_t stage = scales + (BITS == 4 ? 2 * 8 * 256 : 0);
-  static constexpr int stages = (int)(212992 / stage);   // 5; 4 for N = 64 with 8-bit weights; 4, 4, 3 with 4-bit
+  // A stage: a unit's weights, and the tokens' rows or (4-bit) two tiles' scales.
+  static constexpr uint32_t scales = 2 * kBox16;
+  static constexpr uint32_t stage = scales + (BITS == 4 ? 2 * 8 * 256 : b_boxes * b_box);
+  // 4-bit weights, the tokens' ring: a slot holds the rows for 128 of expanded k, two
+  // boxes, each twice (a narrow tile's two k blocks, the activations' two halves).
+  static constexpr uint32_t slot = 4 * b_box;
+  static constexpr int slots = BITS != 4 ? 0 : NP == 64 ? 3 : NP == 32 ? 4 : 5;
+  static constexpr int stages = (int)((212992 - slots * slot) / stage);  // 5; 4 for N = 64 with 8-bit weights; 4, 4, 3 with 4-bit
   // Warps that expand, and the buffers of 128 expanded k (128 columns of tensor
-  // memory) that they fill in turn.  4-bit weights: twice the warps and a third
-  // buffer where registers and tensor memory have room.
+  // memory) that they fill in turn.  4-bit weights: twice the warps where registers
+  // have room, a third buffer where tensor memory has it (17 to 32 tokens give it to
+  // the halves side by side: 32 tokens 85 us, one after the other 87).
   static constexpr int expand = BITS == 4 && NP <= 32 ? 16 : 8;
-  static constexpr int bufs = BITS == 4 && NP <= 32 ? 3 : 2;
+  static constexpr int bufs = BITS == 4 && NP <= 16 ? 3 : 2;
   static constexpr int threads = (12 + (BITS == 16 ? 0 : expand)) * 32;
   // Warps that issue MMAs: with 4-bit weights one for each of a unit's two boxes.
   static constexpr int issuers = BITS == 4 ? 2 : 1;
-  static constexpr int bars = 2 * stages + 4 + 2 * bufs + 2;
-  static constexpr uint32_t ctrl = stages * stage;
+  // The activations' two halves as one B operand, their sums in columns of their own.
+  static constexpr bool side = BITS == 4 && NP <= 32;
+  static constexpr int dn = side ? 2 * NP : NP;            // columns of a box's sums
+  static constexpr int bars = 2 * stages + 4 + 2 * bufs + 2 + 2 * slots;
+  static constexpr uint32_t ring2 = stages * stage;       // 4-bit: the tokens' slots
+  static constexpr uint32_t ctrl = ring2 + slots * slot;
   static constexpr uint32_t holder = ctrl + 8 * bars;     // tensor memory, abort, flag, A
   static constexpr uint32_t bitmap = holder + 16;          // 32 words
   static constexpr uint32_t issued = bitmap + 128;        // stages filled by warps 0 and 10
   static constexpr uint32_t list = issued + 16;            // active experts
-  static constexpr uint32_t slot = list + 2 * kMaxSlots;   // expert of each slot
-  static constexpr uint32_t prob = slot + 2 * kMaxSlots;
+  static constexpr uint32_t expert = list + 2 * kMaxSlots;  // of each (token, slot)
+  static constexpr uint32_t prob = expert + 2 * kMaxSlots;
   static constexpr uint32_t cross = prob + 4 * kMaxSlots;  // up values of a narrow tile [16][64]
   static constexpr uint32_t smem = cross + (can_narrow ? 4096 : 0) + 1024;
   static_assert(smem <= 232448, "more shared memory than one CTA may use");
@@ -217,25 +231,25 @@ __device__ __forceinline__ void expand16_bf16(uint4 v, uint32_t* r) {
   r[6] = bytes_to_bf16(v.w, 0x4140), r[7] = bytes_to_bf16(v.w, 0x4342);
 }
 
-// act in fp32, rounded to bf16 once where it is stored: the second product's
-// tensor instruction takes both operands in one 16-bit type, and its weights
-// are bf16 (8-bit ones are exact in it).  fp16 would be finer, but act has the
-// range of a product of two sums and bf16 weights are not exact in fp16; the
-// layer's other path rounds act to bf16 as well.  It is the only rounding to
-// fewer than 32 bits before the output's own: it moves the output by 0.0026 of
-// its norm (T=64 H=2048 E=128 K=8 I=768; the output's own rounding is 0.0017),
-// and from the same formula with that rounding the kernel is 0.0005 off, the
-// roundings that fall the other way.  With 4-bit weights and up to 8 tokens the
-// instruction's 16 columns hold act as two bf16 (16 bits of it), and the output is
-// as near to the formula's as its own rounding allows (one token 22.7 -> 23.5 us); 16
-// tokens in 32 columns would take 3 to 7 % longer.  The exponential and the quotient are the
-// approximate ones, off by 2 + 1.16 |g| units of the 24th bit: under 2^-17 of act
-// for |g| < 88.
+// act in fp32.  16- and 8-bit weights: rounded to bf16 once where it is stored, as
+// the layer's other path rounds it; the second product's tensor instruction takes
+// both operands in one 16-bit type, and its weights are bf16 (8-bit ones are exact
+// in it).  fp16 would be finer, but act has the range of a product of two sums and
+// bf16 weights are not exact in fp16.  It is the only rounding to fewer than 32 bits
+// before the output's own: it moves the output by 0.0026 of its norm (T=64 H=2048
+// E=128 K=8 I=768; the output's own rounding is 0.0017), and from the same formula
+// with that rounding the kernel is 0.0005 off, the roundings that fall the other way.
+// 4-bit weights: two bf16, the nearest and the nearest to what it leaves, 16 bits of
+// it, and the expanded weights are multiplied with both: side by side in one
+// instruction where tensor memory has the columns (up to 32 tokens), else one after
+// the other.  The output is then as near to the formula's as its own rounding allows
+// for any number of tokens (the same case 0.0017, with one bf16 0.0023), and costs 2
+// to 4 % from 9 tokens on (16 tokens H=7168 146 us against 141, 45 tokens 109 against
+// 107).  The exponential and the quotient are the approximate ones, off by
+// 2 + 1.16 |g| units of the 24th bit: under 2^-17 of act for |g| < 88.
 __device__ __forceinline__ float swiglu(float g, float u) { return __fdividef(g, 1.f + __expf(-g)) * u; }
 
-// split_act (4-bit weights, up to 8 tokens): act as a bf16 and the bf16 of what
-// that leaves, in the second half of the 16 columns (see swiglu).
-template <int NP, int BITS, bool split_act>
+template <int NP, int BITS>
 __global__ void __launch_bounds__(FewTraits<NP, BITS>::threads, 1)
 few_tokens_kernel(const __grid_constant__ CUtensorMap mapG, const __grid_constant__ CUtensorMap mapU,
                   const __grid_constant__ CUtensorMap mapG64, const __grid_constant__ CUtensorMap mapU64,
@@ -260,12 +274,14 @@ few_tokens_kernel(const __grid_constant__ CUtensorMap mapG, const __grid_constan
   auto c_full = [&](int b) { return bars + 8u * (2 * S + 4 + b); };
   auto c_empty = [&](int b) { return bars + 8u * (2 * S + 4 + TR::bufs + b); };
   const uint32_t drain = bars + 8u * (2 * S + 4 + 2 * TR::bufs), clear = drain + 8u;
+  auto b_full = [&](int b) { return clear + 8u + 8u * b; };
+  auto b_empty = [&](int b) { return clear + 8u + 8u * (TR::slots + b); };
   uint32_t* holder = reinterpret_cast<uint32_t*>(g + TR::holder);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(holder + 1);
   volatile int* flag = reinterpret_cast<volatile int*>(holder + 2);
   uint32_t* bitmap = reinterpret_cast<uint32_t*>(g + TR::bitmap);
   int16_t* list = reinterpret_cast<int16_t*>(g + TR::list);
-  int16_t* slot = reinterpret_cast<int16_t*>(g + TR::slot);
+  int16_t* slot = reinterpret_cast<int16_t*>(g + TR::expert);
   float* prob = reinterpret_cast<float*>(g + TR::prob);
   float* cross = reinterpret_cast<float*>(g + TR::cross);
   int* issued = reinterpret_cast<int*>(g + TR::issued);
@@ -274,8 +290,12 @@ few_tokens_kernel(const __grid_constant__ CUtensorMap mapG, const __grid_constan
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
-      mbar_init(full(s), 2);               // weights, tokens
-      mbar_init(empty(s), TR::issuers + (BITS == 16 ? 0 : TR::expand));  // MMAs, expanding warps
+      mbar_init(full(s), I4 ? 1 : 2);      // weights, tokens
+      mbar_init(empty(s), (I4 ? 0 : 1) + (BITS == 16 ? 0 : TR::expand));  // MMAs, expanding warps
+    }
+    for (int b = 0; b < TR::slots; ++b) {
+      mbar_init(b_full(b), 1);
+      mbar_init(b_empty(b), TR::issuers);
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(t_full(a), TR::issuers);
@@ -424,6 +444,12 @@ few_tokens_kernel(const __grid_constant__ CUtensorMap mapG, const __grid_constan
   // may have stopped at different stages; each arrives for those that only the
   // other filled, so that their barriers complete.
   auto drain_ring = [&](int w, int n) {
+    if constexpr (I4) {  // (each has a ring of its own)
+      const int size = w == 0 ? S : TR::slots;
+      for (int i = max(0, n - size); i < n; ++i)
+        mbar_wait_warp(w == 0 ? full(i % size) : b_full(i % size), (uint32_t)(i / size) & 1u, abort_flag, p.status, false);
+      return;
+    }
     if (lane == 0) issued[w] = n;
     asm volatile("bar.sync 2, 64;" ::: "memory");
     const int other = issued[w ^ 1], all = max(n, other);
@@ -501,12 +527,27 @@ few_tokens_kernel(const __grid_constant__ CUtensorMap mapG, const __grid_constan
     bool run = true;
     auto next = [&]() {
       ++n;
-      if (++s == S) s = 0, ph ^= 1u;
+      if (++s == (I4 ? TR::slots : S)) s = 0, ph ^= 1u;
     };
     for (int i = 0; run && i < seg1.count; ++i) {
      int tile, u, len;
      seg1.get(i, tile, u, len);
      for (int k = u - tile * KB1; len > 0; ++k, --len) {
+      if constexpr (I4) {  // (of a narrow tile's k blocks the same 128 k in turn)
+        const int k0 = k * k1, boxes = narrow ? 2 : 1;
+#pragma unroll
+        for (int q = 0; q < 2 && run; ++q) {
+          if (!(run = mbar_wait_warp(b_empty(s), ph ^ 1u, abort_flag, p.status))) break;
+          const uint32_t b = base + TR::ring2 + s * TR::slot;
+          mbar_arrive_expect_tx_warp(b_full(s), 2 * boxes * TR::b_box);
+          for (int h = 0; h < 2 * boxes; ++h)
+            tma_load_2d_warp(b + (2 * (h & 1) + (h >> 1)) * TR::b_box, &mapX, b_full(s),
+                             k0 + (h >> 1) * TR::k + q * 128 + (h & 1) * 64, 0);
+          next();
+        }
+        if (!run) break;
+        continue;
+      }
       if (!(run = mbar_wait_warp(empty(s), ph ^ 1u, abort_flag, p.status))) break;
       const uint32_t b = base + s * TR::stage + 2 * kBox16;
       const int boxes = k1 / 64;
@@ -526,19 +567,26 @@ few_tokens_kernel(const __grid_constant__ CUtensorMap mapG, const __grid_constan
         seen = a;
         ++checked;
       }
+      if constexpr (I4) {  // 128 k of either half
+#pragma unroll
+        for (int q = 0; q < 2 && run; ++q) {
+          if (!(run = mbar_wait_warp(b_empty(s), ph ^ 1u, abort_flag, p.status))) break;
+          const uint32_t b = base + TR::ring2 + s * TR::slot;
+          mbar_arrive_expect_tx_warp(b_full(s), 4 * TR::b_box);
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            tma_load_3d_warp(b + 2 * h * TR::b_box, &mapAct, b_full(s), k * TR::k + q * 128 + h * 64, 0, 2 * a);
+          next();
+        }
+        if (!run) break;
+        continue;
+      }
       if (!(run = mbar_wait_warp(empty(s), ph ^ 1u, abort_flag, p.status))) break;
       const uint32_t b = base + s * TR::stage + 2 * kBox16;
       mbar_arrive_expect_tx_warp(full(s), TR::k / 64 * TR::b_box);
 #pragma unroll
-      for (int q = 0; q < TR::k / 64; ++q) {
-        const uint32_t dst = b + q * TR::b_box;
-        if constexpr (split_act) {  // 8 rows of either
-          tma_load_3d_warp(dst, &mapAct, full(s), k * TR::k + q * 64, 0, 2 * a);
-          tma_load_3d_warp(dst + 1024, &mapAct, full(s), k * TR::k + q * 64, 0, 2 * a + 1);
-        } else {
-          tma_load_3d_warp(dst, &mapAct, full(s), k * TR::k + q * 64, 0, a);
-        }
-      }
+      for (int q = 0; q < TR::k / 64; ++q)
+        tma_load_3d_warp(b + q * TR::b_box, &mapAct, full(s), k * TR::k + q * 64, 0, a);
       next();
     }
     drain_ring(1, n);
@@ -546,49 +594,67 @@ few_tokens_kernel(const __grid_constant__ CUtensorMap mapG, const __grid_constan
     // ---------------- MMA: the whole warp, one lane elected for each ----------------
     // (4-bit: the unit's first box, or its second)
     const uint32_t box = warp == 1 ? 0u : 1u;
-    constexpr uint32_t idesc = idesc_bf16_f32(128, NP, false, false);
+    constexpr uint32_t idesc = idesc_bf16_f32(128, NP, false, false), idesc2 = idesc_bf16_f32(128, TR::dn, false, false);
     const uint64_t d0 = desc_sw128(base, 16, 1024);
     int s = 0, c = 0, it = 0;
     uint32_t ph = 0, cph = 0;
     bool run = true;
     // one segment: len units of one tile (phase 1) or one tile and expert (phase 2)
-    // (two: boxes of different rows; the first product's narrow tiles have k blocks)
-    auto segment = [&](int len, bool two) {
-
+    // (two: boxes of different rows; the first product's narrow tiles have k blocks;
+    // halves: of the activations, multiplied with the same expanded weights)
+    auto segment = [&](int len, bool two, bool halves) {
       const int acc = it & 1;
       run = mbar_wait_warp(t_empty(acc), ((it >> 1) & 1) ^ 1u, abort_flag, p.status);
       if (!run) return;
       tc_fence_after();
-      const uint32_t d = tmem + acc * 2 * NP;
+      const uint32_t d = tmem + acc * 2 * TR::dn;
       uint32_t accum = 0u;
+      if constexpr (I4) {
+        for (int k = 0; k < 2 * len; ++k) {  // expanded 128 of k at a time
+          run = mbar_wait_warp(b_full(s), ph, abort_flag, p.status) &&
+                mbar_wait_warp(c_full(c), cph, abort_flag, p.status);
+          if (!run) return;
+          tc_fence_after();
+          const uint32_t a = tmem + 512 - 128 * TR::bufs + c * 128 + box * 64;
+          // (a narrow tile's boxes are two k blocks, summed in an accumulator each)
+          const uint64_t b = d0 + (TR::ring2 >> 4) + (uint64_t)s * (TR::slot >> 4) + (two ? 0u : box) * (TR::b_box >> 4);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const uint64_t bh = b + 2 * h * (TR::b_box >> 4);
+            umma_f16_ta_k64_warp<false>(d + box * TR::dn, a + h * 32, bh, TR::side && halves ? idesc2 : idesc, accum);
+            if (!TR::side && halves)
+              umma_f16_ta_k64_warp<false>(d + box * TR::dn, a + h * 32, bh + (TR::b_box >> 4), idesc, 1u);
+            accum = 1u;
+          }
+          umma_commit_warp(c_empty(c));
+          if (++c == TR::bufs) c = 0, cph ^= 1u;
+          umma_commit_warp(b_empty(s));
+          if (++s == TR::slots) s = 0, ph ^= 1u;
+        }
+        umma_commit_warp(t_full(acc));
+        ++it;
+        return;
+      }
       for (int k = 0; k < len; ++k) {
         run = mbar_wait_warp(full(s), ph, abort_flag, p.status);
         if (!run) return;
         tc_fence_after();
         const uint64_t ad = d0 + (uint64_t)s * (TR::stage >> 4);
         const uint64_t bd = ad + (2 * kBox16 >> 4);
-        if constexpr (BITS < 16) {
+        if constexpr (I8) {
+          run = mbar_wait_warp(c_full(c), cph, abort_flag, p.status);
+          if (!run) return;
+          tc_fence_after();
+          const uint32_t a = tmem + 512 - 128 * TR::bufs + c * 128;
 #pragma unroll
-          for (int q = 0; q < TR::k / 128; ++q) {  // expanded 128 of k at a time
-            run = mbar_wait_warp(c_full(c), cph, abort_flag, p.status);
-            if (!run) return;
-            tc_fence_after();
-            const uint32_t a = tmem + 512 - 128 * TR::bufs + c * 128;
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              // (a narrow tile's boxes are two k blocks, summed in an accumulator each)
-              const uint64_t b = bd + (2 * q + h + (I4 && !two ? 4 * box : 0u)) * (TR::b_box >> 4);
-              if constexpr (I4) {
-                umma_f16_ta_k64_warp<false>(d + box * NP, a + box * 64 + h * 32, b, idesc, accum);
-              } else {
-                umma_f16_ta_k64_warp<false>(d, a + h * 32, b, idesc, accum);
-                umma_f16_ta_k64_warp<false>(d + NP, a + 64 + h * 32, b, idesc, accum);
-              }
-              accum = 1u;
-            }
-            umma_commit_warp(c_empty(c));
-            if (++c == TR::bufs) c = 0, cph ^= 1u;
+          for (int h = 0; h < 2; ++h) {
+            const uint64_t b = bd + h * (TR::b_box >> 4);
+            umma_f16_ta_k64_warp<false>(d, a + h * 32, b, idesc, accum);
+            umma_f16_ta_k64_warp<false>(d + NP, a + 64 + h * 32, b, idesc, accum);
+            accum = 1u;
           }
+          umma_commit_warp(c_empty(c));
+          if (++c == TR::bufs) c = 0, cph ^= 1u;
         } else {
           umma_f16_k64_warp(d, ad, bd, idesc, accum);
           if (two) umma_f16_k64_warp(d + NP, ad + (kBox16 >> 4), bd, idesc, accum);
@@ -604,11 +670,11 @@ few_tokens_kernel(const __grid_constant__ CUtensorMap mapG, const __grid_constan
     for (int i = 0; run && i < seg1.count; ++i) {
       int tile, u, len;
       seg1.get(i, tile, u, len);
-      segment(len, !narrow);
+      segment(len, !narrow, false);
     }
     for (int u = lo2; run && u < hi2;) {
       const int len = min(KB2 - u % KB2, hi2 - u);
-      segment(len, true);
+      segment(len, true, true);
       u += len;
     }
     umma_commit_warp(drain);
@@ -645,15 +711,31 @@ few_tokens_kernel(const __grid_constant__ CUtensorMap mapG, const __grid_constan
       run = epi_all(mbar_wait_warp(t_full(acc), (it >> 1) & 1, abort_flag, p.status));
       if (!run) break;
       tc_fence_after();
-      const uint32_t d = tq + acc * 2 * NP;
+      const uint32_t d = tq + acc * 2 * TR::dn;
       const bool whole = len == KB1;
-      __nv_bfloat16* act = p.act + ((size_t)a * (split_act ? 2 : 1) * p.T + col0) * p.I + i;
-      auto put_act = [&](int t, float v) {
-        const __nv_bfloat16 hi = __float2bfloat16_rn(v);
-        act[(size_t)t * p.I] = hi;
-        if constexpr (split_act) {
-          const float h = __bfloat162float(hi);  // (infinite and NaN values leave nothing)
-          act[(size_t)(p.T + t) * p.I] = __float2bfloat16_rn(fabsf(h) <= 3.402823466e+38f ? v - h : 0.f);
+      __nv_bfloat16* act = p.act + ((size_t)a * (I4 ? 2 : 1) * p.T + col0) * p.I + i;
+      // act of tokens t and t + 1 (if there is one), by whole warps.  4-bit weights: a
+      // bf16 and, T rows on, the bf16 of what that leaves.  Neighbouring lanes turn two
+      // tokens of a channel into two channels of a token, which halves the stores
+      // (45 tokens: they would add 10 us).
+      auto put_act = [&](int t, float v, float w) {
+        if constexpr (I4) {
+          auto halves = [](float x) {
+            const __nv_bfloat16 hi = __float2bfloat16_rn(x);
+            const float h = __bfloat162float(hi);  // (infinite and NaN values leave nothing)
+            return VecTraits<__nv_bfloat16>::pack2(h, fabsf(h) <= 3.402823466e+38f ? x - h : 0.f);
+          };
+          const uint32_t a = halves(v), b = halves(w);
+          const bool odd = lane & 1;
+          const uint32_t got = __shfl_xor_sync(0xffffffffu, odd ? a : b, 1);
+          const uint32_t x = odd ? got : a, y = odd ? b : got;
+          if (odd && t + 1 >= T) return;
+          uint32_t* dst = reinterpret_cast<uint32_t*>(act + (size_t)(t + odd) * p.I - odd);
+          dst[0] = __byte_perm(x, y, 0x5410);
+          dst[(size_t)p.T * p.I / 2] = __byte_perm(x, y, 0x7632);
+        } else {
+          act[(size_t)t * p.I] = __float2bfloat16_rn(v);
+          if (t + 1 < T) act[(size_t)(t + 1) * p.I] = __float2bfloat16_rn(w);
         }
       };
       const size_t pstride = (size_t)p.T * 256;  // floats of a partial
@@ -665,7 +747,7 @@ few_tokens_kernel(const __grid_constant__ CUtensorMap mapG, const __grid_constan
           tmem_ld_32x32b_x8(d, v);
           if constexpr (I4) {  // the other k block's sums
             uint32_t w[8];
-            tmem_ld_32x32b_x8(d + NP, w);
+            tmem_ld_32x32b_x8(d + TR::dn, w);
             tmem_ld_wait();
 #pragma unroll
             for (int j = 0; j < 8; ++j) v[j] = __float_as_uint(__uint_as_float(v[j]) + __uint_as_float(w[j]));
@@ -678,8 +760,9 @@ few_tokens_kernel(const __grid_constant__ CUtensorMap mapG, const __grid_constan
           epi_sync();
           if (r < 64)
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-              if (j < T) put_act(j, swiglu(__uint_as_float(v[j]), x[j * 64]));
+            for (int j = 0; j < 8; j += 2)
+              if (j < T)
+                put_act(j, swiglu(__uint_as_float(v[j]), x[j * 64]), swiglu(__uint_as_float(v[j + 1]), x[j * 64 + 64]));
         }
       }
 #pragma unroll
@@ -688,22 +771,27 @@ few_tokens_kernel(const __grid_constant__ CUtensorMap mapG, const __grid_constan
         uint32_t gv[CH], uv[CH];
         if constexpr (CH == 16) {
           tmem_ld_32x32b_x16(d + c0, gv);
-          tmem_ld_32x32b_x16(d + NP + c0, uv);
+          tmem_ld_32x32b_x16(d + TR::dn + c0, uv);
         } else {
           tmem_ld_32x32b_x8(d + c0, gv);
-          tmem_ld_32x32b_x8(d + NP + c0, uv);
+          tmem_ld_32x32b_x8(d + TR::dn + c0, uv);
         }
         tmem_ld_wait();
 #pragma unroll
-        for (int j = 0; j < CH; ++j) {
+        for (int j = 0; j < CH; j += 2) {
           const int t = c0 + j;
           if (t < T) {
             const float gg = __uint_as_float(gv[j]) * gsc, uu = __uint_as_float(uv[j]) * usc;
+            const float g2 = __uint_as_float(gv[j + 1]) * gsc, u2 = __uint_as_float(uv[j + 1]) * usc;
             if (whole) {
-              if (in) put_act(t, swiglu(gg, uu));
+              if (in) put_act(t, swiglu(gg, uu), swiglu(g2, u2));
             } else {
               mine[t * 256] = gg;
               mine[t * 256 + 128] = uu;
+              if (t + 1 < T) {
+                mine[t * 256 + 256] = g2;
+                mine[t * 256 + 384] = u2;
+              }
             }
           }
         }
@@ -746,8 +834,8 @@ few_tokens_kernel(const __grid_constant__ CUtensorMap mapG, const __grid_constan
                 for (int j = 0; j < 8; ++j) gg[j] += g2[k][j], uu[j] += u2[k][j];
             }
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-              if (t + j < T) put_act(t + j, swiglu(gg[j], uu[j]));
+            for (int j = 0; j < 8; j += 2)
+              if (t + j < T) put_act(t + j, swiglu(gg[j], uu[j]), swiglu(gg[j + 1], uu[j + 1]));
           }
         }
       }
@@ -761,7 +849,7 @@ few_tokens_kernel(const __grid_constant__ CUtensorMap mapG, const __grid_constan
     // and all columns.
     constexpr int CP = 16;  // columns read at a time
     const int rset = (warp - 2) >> 2, r2 = rset * 128 + r;
-    const uint32_t tq2 = tmem + ((uint32_t)(quarter * 32) << 16) + rset * NP;
+    const uint32_t tq2 = tmem + ((uint32_t)(quarter * 32) << 16) + rset * TR::dn;
     const size_t pstride = (size_t)p.T * 256;  // floats of a partial
     const int n = A * KB2;                      // units of a tile
     auto put = [&](int t, int h, float y) {
@@ -790,18 +878,24 @@ few_tokens_kernel(const __grid_constant__ CUtensorMap mapG, const __grid_constan
       // (a warp whose wait ran out still comes to the tile's barrier)
       run = run && mbar_wait_warp(t_full(acc), (it >> 1) & 1, abort_flag, p.status);
       tc_fence_after();
-      const uint32_t d = tq2 + acc * 2 * NP;
+      const uint32_t d = tq2 + acc * 2 * TR::dn;
 #pragma unroll
       for (int c0 = 0; c0 < NP; c0 += CP) {
         const uint32_t bits = ((c0 < 32 ? b0 : b1) >> (c0 & 31)) & ((1u << CP) - 1u);
         if (bits == 0u) continue;
         uint32_t v[CP];
         tmem_ld_32x32b_x16(d + c0, v);
-        tmem_ld_wait();
-        if constexpr (split_act) {
+        if constexpr (TR::side) {
 #pragma unroll
-          for (int j = 0; j < 8; ++j) v[j] = __float_as_uint(__uint_as_float(v[j]) + __uint_as_float(v[j + 8]));
+          for (int q = 0; q < CP; q += 8) {
+            uint32_t low[8];
+            tmem_ld_32x32b_x8(d + NP + c0 + q, low);
+            tmem_ld_wait();
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[q + j] = __float_as_uint(__uint_as_float(v[q + j]) + __uint_as_float(low[j]));
+          }
         }
+        tmem_ld_wait();
 #pragma unroll
         for (int j = 0; j < CP; ++j) {
           const float w = __shfl_sync(0xffffffffu, c0 < 32 ? w0 : w1, (c0 + j) & 31);
@@ -979,7 +1073,7 @@ FewLayout few_layout(int T, int K, int H, int I, int E) {
   l.counts = up(4 * (A + A * ((I + 127) / 128) + (H + 255) / 256 + 1));
   l.part1 = (size_t)kMaxCtas * 2 * T * 256 * 4;
   l.part2 = (size_t)kMaxCtas * 2 * T * 256 * 4;
-  l.act = up(A * T * I * 2 * (T <= 8 ? 2 : 1));  // (split_act)
+  l.act = up(A * T * I * 2 * 2);  // (4-bit weights: two bf16)
   l.total = l.words + l.counts + l.part1 + l.part2 + l.act;
   return l;
 }
@@ -990,7 +1084,7 @@ struct FewWeights {
   const void *gate, *up, *down, *gs, *us, *ds;
 };
 
-template <int NP, int BITS, bool split_act = false>
+template <int NP, int BITS>
 int launch_few(FewParams p, const void* x, const FewWeights& w, cudaStream_t s) {
   using TR = FewTraits<NP, BITS>;
   constexpr int esz = BITS == 16 ? 2 : 1, pack = BITS == 4 ? 2 : 1;
@@ -1000,12 +1094,12 @@ int launch_few(FewParams p, const void* x, const FewWeights& w, cudaStream_t s) 
   const uint64_t d2[3] = {(uint64_t)p.I / pack, (uint64_t)p.H, (uint64_t)p.E};
   const uint32_t bw[3] = {128 / esz, 128, 1}, bw64[3] = {128 / esz, 64, 1};
   const uint64_t dx[2] = {(uint64_t)p.H, (uint64_t)p.T};
-  const uint64_t da[3] = {(uint64_t)p.I, (uint64_t)p.T, (uint64_t)p.A_max * (split_act ? 2 : 1)};
-  const uint32_t bx[3] = {64, NP, 1}, bx8[3] = {64, 8, 1};
+  const uint64_t da[3] = {(uint64_t)p.I, (uint64_t)p.T, (uint64_t)p.A_max * (BITS == 4 ? 2 : 1)};
+  const uint32_t bx[3] = {64, NP, 1}, bx2[3] = {64, NP, 2};  // (4-bit: both halves)
   if (!make_map_sw128(&mg, Wg, esz, 3, d1, bw) || !make_map_sw128(&mu, Wu, esz, 3, d1, bw) ||
       !make_map_sw128(&mg64, Wg, esz, 3, d1, bw64) || !make_map_sw128(&mu64, Wu, esz, 3, d1, bw64) ||
       !make_map_sw128(&md, Wd, esz, 3, d2, bw) || !make_map_sw128(&mx, x, 2, 2, dx, bx) ||
-      !make_map_sw128(&ma, p.act, 2, 3, da, split_act ? bx8 : bx))
+      !make_map_sw128(&ma, p.act, 2, 3, da, BITS == 4 ? bx2 : bx))
     return MOE_ERR_CUDA;
   if constexpr (BITS == 4) {
     const uint64_t s1[3] = {(uint64_t)p.I, (uint64_t)p.H * p.per1 / 256, (uint64_t)p.E};
@@ -1023,7 +1117,7 @@ int launch_few(FewParams p, const void* x, const FewWeights& w, cudaStream_t s) 
   int dev = -1;
   if (cudaGetDevice(&dev) != cudaSuccess) return MOE_ERR_CUDA;
   const int allowed = smem_allowed.get(dev, [] {
-    return cudaFuncSetAttribute(few_tokens_kernel<NP, BITS, split_act>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    return cudaFuncSetAttribute(few_tokens_kernel<NP, BITS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                 (int)TR::smem) == cudaSuccess;
   });
   if (!allowed) return MOE_ERR_CUDA;
@@ -1037,7 +1131,7 @@ int launch_few(FewParams p, const void* x, const FewWeights& w, cudaStream_t s) 
   cfg.stream = s;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, few_tokens_kernel<NP, BITS, split_act>, mg, mu, mg64, mu64, md, mx, ma, mgs,
+  if (cudaLaunchKernelEx(&cfg, few_tokens_kernel<NP, BITS>, mg, mu, mg64, mu64, md, mx, ma, mgs,
                          mus, mgs64, mus64, mds, p) != cudaSuccess) {
     (void)cudaGetLastError();
     return MOE_ERR_CUDA;
@@ -1108,8 +1202,6 @@ int few_tokens(const void* tokens, const int32_t* expert_ids, const float* probs
   p.E = E;
   p.E_all = E + num_special;
   p.A_max = T * K < E ? T * K : E;
-  if constexpr (BITS == 4)
-    if (T <= 8) return launch_few<16, BITS, true>(p, tokens, w, stream);
   if (T <= 16) return launch_few<16, BITS>(p, tokens, w, stream);
   if (T <= 32) return launch_few<32, BITS>(p, tokens, w, stream);
   return launch_few<64, BITS>(p, tokens, w, stream);

@@ -607,7 +607,10 @@ int moe_down_proj_int4(const void* act, const int32_t* expert_offsets, int N, in
  *   workspace       moe_layer_few_tokens_workspace_size(T, K, H, I, E) bytes,
  *                   16-byte aligned, needs no clearing, and may be used for
  *                   anything else between two calls; calls that can overlap
- *                   on the GPU need one each
+ *                   on the GPU need one each.  The size does not fall when T, K,
+ *                   H, I or E grows, so one workspace serves every smaller call,
+ *                   and it is that of 4-bit weights: these here need (and are
+ *                   refused without) 2 min(T K, E) T I bytes less
  * A token without an active slot gets shared_x[t], or zeros.  H and I are
  * multiples of 64, at most MOE_FEW_MAX_SIZE.  Sums are fp32 in an order that depends on the sizes, the
  * ids, the mask and the number of SMs alone; act is rounded to bf16 once, as

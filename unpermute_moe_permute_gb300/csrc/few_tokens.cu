@@ -1065,7 +1065,9 @@ struct FewLayout {
   size_t words, counts, part1, part2, act, total;
 };
 
-FewLayout few_layout(int T, int K, int H, int I, int E) {
+// bits: of a weight.  act comes last, so that other weights' calls find everything
+// else where 4-bit ones, which keep act in two bf16, have it.
+FewLayout few_layout(int T, int K, int H, int I, int E, int bits) {
   const size_t A = (size_t)(T * K < E ? T * K : E);
   auto up = [](size_t v) { return (v + 255) & ~(size_t)255; };
   FewLayout l;
@@ -1073,7 +1075,7 @@ FewLayout few_layout(int T, int K, int H, int I, int E) {
   l.counts = up(4 * (A + A * ((I + 127) / 128) + (H + 255) / 256 + 1));
   l.part1 = (size_t)kMaxCtas * 2 * T * 256 * 4;
   l.part2 = (size_t)kMaxCtas * 2 * T * 256 * 4;
-  l.act = up(A * T * I * 2 * 2);  // (4-bit weights: two bf16)
+  l.act = up(A * T * I * (bits == 4 ? 4 : 2));
   l.total = l.words + l.counts + l.part1 + l.part2 + l.act;
   return l;
 }
@@ -1168,10 +1170,9 @@ int few_tokens(const void* tokens, const int32_t* expert_ids, const float* probs
   for (const void* p : ptrs)
     if (p && !aligned16(p)) return MOE_ERR_INVALID_ARG;
   if (BITS == 4 && (!aligned16(w.gs) || !aligned16(w.us) || !aligned16(w.ds))) return MOE_ERR_INVALID_ARG;
-  if (workspace_bytes < moe_layer_few_tokens_workspace_size(T, K, H, I, E))
-    return MOE_ERR_INVALID_ARG;
+  const FewLayout l = few_layout(T, K, H, I, E, BITS);
+  if (workspace_bytes < l.total) return MOE_ERR_INVALID_ARG;  // (what these weights use)
   if (int rc = device_ok()) return rc;
-  const FewLayout l = few_layout(T, K, H, I, E);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   FewParams p{};
   p.ids = expert_ids;
@@ -1217,7 +1218,7 @@ using namespace moe::tc;
 extern "C" size_t moe_layer_few_tokens_workspace_size(int T, int K, int H, int I, int E) {
   if (T <= 0 || K <= 0 || H <= 0 || I <= 0 || E <= 0 || T > MOE_FEW_TOKENS || K > kMaxK) return 0;
   if (H > MOE_FEW_MAX_SIZE || I > MOE_FEW_MAX_SIZE) return 0;
-  return few_layout(T, K, H, I, E).total;
+  return few_layout(T, K, H, I, E, 4).total;  // (any weights)
 }
 
 extern "C" int moe_layer_few_tokens(const void* tokens, const int32_t* expert_ids,

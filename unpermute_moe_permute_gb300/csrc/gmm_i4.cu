@@ -25,10 +25,13 @@
 // its own, in their order.
 //
 // Warps: 1 TMA producer, 1 MMA issuer (in the leading CTA), epilogue warps, and
-// groups of four warps that expand 128 of k in turn.  The barrier of a loaded stage
-// is waited for by the expanding groups alone: what their arrival tells the MMA
-// issuer about tensor memory holds for the rows of the stage too, which had landed
-// before.
+// groups of four warps that expand 128 of k in turn.  A stage has two barriers: the
+// expanding groups wait for its weights and scales, each CTA's on its own; the MMA
+// issuer for its rows, both CTAs' on the leader's.  Its instructions read the peer's
+// shared memory, and the copies into it signal the leader themselves: an arrival of
+// the peer's warps after they have seen a copy land says so only with release and
+// acquire at cluster scope (gate/up of 256 rows an expert 176 us, not 132).  The issuer
+// tries both barriers of a part at once (one after the other: few rows 62 -> 66 us).
 //
 // Few rows: stages are 256 deep, because the copies' 128-byte rows take the TMA unit
 // half the time of 64-byte ones.  (With 128-deep stages 203 tokens of 64 experts,
@@ -74,14 +77,14 @@ struct I4Cfg {
     return m;
   }
   static constexpr int kFulls = lcm(kStages, kTeams);
-  static constexpr int kBars = kFulls + kStages + 2 * kGroups + 4 + 1 + 2;
+  static constexpr int kBars = kFulls + 2 * kStages + 2 * kGroups + 4 + 1 + 2 + 1;
   static constexpr uint32_t kStageWarp = 2048;  // epilogue staging of a warp
   static constexpr uint32_t kPart = kRowTile * 128 * 4;  // sums of another pair: [row][channel]
   static constexpr uint32_t kParts = kStages * (kB + kA + kS);
   static constexpr uint32_t kStage = kParts + (kSplit - 1) * kPart;
   static constexpr uint32_t kCtrl = kStage + kEpi * kStageWarp;
   static constexpr uint32_t kHolder = kCtrl + 8 * kBars;
-  static constexpr uint32_t kTable = kHolder + 8;  // prefix, offsets, scan scratch
+  static constexpr uint32_t kTable = kHolder + 16;  // prefix, offsets, scan scratch
   static constexpr uint32_t kSmem = kTable + 2 * (kMaxExperts + 1) * 4 + 32 * 4 + 1024;
   static_assert(kSmem <= 232448, "more shared memory than one CTA may use");
   static_assert(kACol + kGroups * 64 <= 512, "more tensor memory than there is");
@@ -119,13 +122,6 @@ struct SplitTile {
   __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity) const {
     return __all_sync(0xffffffffu, mbar_wait<true>(bar, parity, abort_flag, status));
   }
-  __device__ __forceinline__ static void arrive(uint32_t cluster_addr) {
-    __syncwarp();
-    asm volatile(
-        "{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\t"
-        "@q mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];\n\t}" ::"r"(cluster_addr)
-        : "memory");
-  }
   // the last tile's sums have been read
   __device__ __forceinline__ bool begin() { return pair == 0 || wait(empty, (tile & 1u) ^ 1u); }
   __device__ __forceinline__ bool piece(uint32_t (&v)[32], int c) {
@@ -149,10 +145,10 @@ struct SplitTile {
   }
   __device__ __forceinline__ void end() {
     if (pair != 0) {
-      arrive(mapa_shared(full, rank));
+      mbar_arrive_release_cluster_warp(mapa_shared(full, rank));
     } else {
 #pragma unroll
-      for (int s = 1; s < C::kSplit; ++s) arrive(mapa_shared(empty, 2 * s + rank));
+      for (int s = 1; s < C::kSplit; ++s) mbar_arrive_release_cluster_warp(mapa_shared(empty, 2 * s + rank));
     }
     ++tile;
   }
@@ -181,8 +177,11 @@ gmm_i4_kernel(const __grid_constant__ CUtensorMap mapW0, const __grid_constant__
   auto t_full = [&](int a) { return bars2 + 8u * (2 * kGroups + a); };
   auto t_empty = [&](int a) { return bars2 + 8u * (2 * kGroups + 2 + a); };
   const uint32_t drain = bars2 + 8u * (2 * kGroups + 4), part_full = drain + 8u, part_empty = drain + 16u;
+  const uint32_t counted = drain + 24u;
+  auto rows_full = [&](int s) { return drain + 32u + 8u * s; };
   uint32_t* holder = reinterpret_cast<uint32_t*>(g + C::kHolder);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(g + C::kHolder + 4);
+  volatile int* peer_stages = reinterpret_cast<volatile int*>(g + C::kHolder + 8);
   int32_t* prefix = reinterpret_cast<int32_t*>(g + C::kTable);
   int32_t* offs = prefix + (kMaxExperts + 1);
   int32_t* scratch = offs + (kMaxExperts + 1);
@@ -190,7 +189,10 @@ gmm_i4_kernel(const __grid_constant__ CUtensorMap mapW0, const __grid_constant__
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kFulls; ++i) mbar_init(q_full(i), 1);
-    for (int s = 0; s < kStages; ++s) mbar_init(q_empty(s), 4 * kPer + 1);  // a team, the MMAs
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(q_empty(s), 4 * kPer + 1);  // a team, the MMAs
+      mbar_init(rows_full(s), 2);           // the leader's: both CTAs' copies
+    }
     for (int b = 0; b < kGroups; ++b) {
       mbar_init(c_full(b), 2 * 4);  // the leader's: a group of both CTAs
       mbar_init(c_empty(b), 1);
@@ -200,6 +202,7 @@ gmm_i4_kernel(const __grid_constant__ CUtensorMap mapW0, const __grid_constant__
       mbar_init(t_empty(a), 2 * kEpi);  // the epilogue warps of both CTAs
     }
     mbar_init(drain, 1);
+    mbar_init(counted, 1);
     mbar_init(part_full, C::kSplit > 1 ? (C::kSplit - 1) * kEpi : 1);
     mbar_init(part_empty, kEpi);
     *abort_flag = 0;
@@ -242,6 +245,7 @@ gmm_i4_kernel(const __grid_constant__ CUtensorMap mapW0, const __grid_constant__
   if (warp == kTmaWarp) {  // the whole warp, one lane elected for each copy
     const uint32_t ub = uniform(base);
     const int per = kDeep / (int)uniform(p.group);
+    const uint32_t rows_of_leader = uniform(mapa_shared(rows_full(0), leader));
     int s = 0, f = 0, n = 0;  // slot, its barrier, stages so far
     uint32_t ph = 0;
     bool run = true;
@@ -249,7 +253,7 @@ gmm_i4_kernel(const __grid_constant__ CUtensorMap mapW0, const __grid_constant__
       const PairTile x = pair_tile<kSwiglu, kSub>(t, p, prefix, offs, rank);
       const int nh0 = (int)uniform(x.n) / 2, nh1 = (int)uniform(x.n1) / 2, e = (int)uniform(x.e);
       const int ch0 = (int)uniform(x.ch0), r0 = (int)uniform(x.row0);
-      const uint32_t tx = kA + (uint32_t)per * 256u + (uint32_t)(nh0 + nh1) * (2u * kDeep);
+      const uint32_t tx = kA + (uint32_t)per * 256u, tx_rows = (uint32_t)(nh0 + nh1) * (2u * kDeep);
       for (int k = 0; k < stages; ++k) {
         run = mbar_wait_warp(q_empty(s), ph ^ 1u, abort_flag, p.status);
         if (!run) break;
@@ -262,6 +266,8 @@ gmm_i4_kernel(const __grid_constant__ CUtensorMap mapW0, const __grid_constant__
           tma_load_3d_warp(sc + per * 128, &mapS1, q_full(f), ch0, (k_lo + k) * per, e);
         }
         // this CTA's half of each accumulator's rows, one after the other
+        const uint32_t rows = rows_of_leader + 8u * s;
+        mbar_arrive_expect_tx_cluster_warp(rows, tx_rows);
 #pragma unroll
         for (int h = 0; h < kDeep / 64; ++h) {
           uint32_t b = ub + s * kB + h * (kB / (kDeep / 64));
@@ -269,9 +275,9 @@ gmm_i4_kernel(const __grid_constant__ CUtensorMap mapW0, const __grid_constant__
             const int nh = j ? nh1 : nh0, rj = r0 + (j ? 2 * nh0 : 0) + rank * nh;
             int r = 0;
             for (; r + 32 <= nh; r += 32, b += 4096)
-              tma_load_2d_warp(b, &mapX32, q_full(f), (k_lo + k) * kDeep + h * 64, rj + r);
+              tma_load_2d_pair_warp(b, &mapX32, rows, (k_lo + k) * kDeep + h * 64, rj + r);
             if (r < nh) {
-              tma_load_2d_warp(b, &mapX16, q_full(f), (k_lo + k) * kDeep + h * 64, rj + r);
+              tma_load_2d_pair_warp(b, &mapX16, rows, (k_lo + k) * kDeep + h * 64, rj + r);
               b += 2048;
             }
           }
@@ -281,8 +287,23 @@ gmm_i4_kernel(const __grid_constant__ CUtensorMap mapW0, const __grid_constant__
         if (++f == kFulls) f = 0;
       }
     }
-    // every copy has landed, and the leader's signals to the slots have come,
-    // before the CTA may exit
+    // Every copy has landed, and the leader's signals to the slots have come,
+    // before the CTA may exit.  The leader waits for both CTAs' rows (the peer stays
+    // until the closing cluster barrier).  When its wait ran out the two may have
+    // stopped at different stages: it arrives for the one that did not come so far
+    // (kStages apart at most: the slots are freed in both together).
+    if (rank != 0) {
+      asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(mapa_shared(smem_u32(holder) + 8u, leader)), "r"(n) : "memory");
+      mbar_arrive_release_cluster_warp(mapa_shared(counted, leader));
+    } else {
+      int m = n;  // the peer's stages
+      if (!run && __all_sync(0xffffffffu, mbar_wait<true>(counted, 0, abort_flag, p.status, false)))
+        m = (int)uniform(*peer_stages);
+      const int most = max(n, m);
+      for (int i = min(n, m); i < most; ++i) mbar_arrive_warp(rows_full(i % kStages));
+      for (int i = max(0, most - kStages); i < most; ++i)
+        mbar_wait_warp(rows_full(i % kStages), (uint32_t)(i / kStages) & 1u, abort_flag, p.status, false);
+    }
     for (int i = max(0, n - kStages); i < n; ++i) {
       mbar_wait_warp(q_full(i % kFulls), (uint32_t)(i / kFulls) & 1u, abort_flag, p.status, false);
       if (run) run = mbar_wait_warp(q_empty(i % kStages), (uint32_t)(i / kStages) & 1u, abort_flag, p.status);
@@ -293,7 +314,7 @@ gmm_i4_kernel(const __grid_constant__ CUtensorMap mapW0, const __grid_constant__
       const uint32_t tm = uniform(tmem);
       constexpr uint64_t kPiece = kB / (kDeep / 64) >> 4;  // 64 of k of a stage's rows
       int b = 0, s = 0, it = 0;
-      uint32_t ph = 0;
+      uint32_t ph = 0, sph = 0;
       bool run = true;
       for (int t = t0; run && t < total; t += dt) {
         const PairTile x = pair_tile<kSwiglu, kSub>(t, p, prefix, offs, rank);
@@ -316,7 +337,8 @@ gmm_i4_kernel(const __grid_constant__ CUtensorMap mapW0, const __grid_constant__
             const int ahead = subs == 1 ? 1 : k == 0 ? min(C::kHead, left) : left <= C::kTail ? left : 1;
             int b1 = b, s1 = s;
             for (int i = 0; i < ahead; ++i) {
-              run = mbar_wait_warp(c_full(b1), b1 < b ? ph ^ 1u : ph, abort_flag, p.status);
+              run = mbar_wait2_warp(rows_full(s1), s1 < s ? sph ^ 1u : sph, c_full(b1), b1 < b ? ph ^ 1u : ph, abort_flag,
+                                    p.status);
               if (!run) break;
               tc_fence_after();
 #pragma unroll
@@ -342,7 +364,7 @@ gmm_i4_kernel(const __grid_constant__ CUtensorMap mapW0, const __grid_constant__
               umma_commit_pair_warp(c_empty(b), both);
               if (++b == kGroups) b = 0, ph ^= 1u;
               umma_commit_pair_warp(q_empty(s), both);
-              if (++s == kStages) s = 0;
+              if (++s == kStages) s = 0, sph ^= 1u;
             }
           }
           if (!run) break;
@@ -351,8 +373,10 @@ gmm_i4_kernel(const __grid_constant__ CUtensorMap mapW0, const __grid_constant__
           uint32_t accum = 0u;
           for (int k = 0; k < stages; ++k) {
             const uint64_t bd = bdesc0 + (uint64_t)s * (kB >> 4);
-            for (int q = 0; run && q < kPer; ++q) {
-              run = mbar_wait_warp(c_full(b), ph, abort_flag, p.status);
+#pragma unroll
+            for (int q = 0; q < kPer; ++q) {
+              run = q == 0 ? mbar_wait2_warp(rows_full(s), sph, c_full(b), ph, abort_flag, p.status)
+                           : mbar_wait_warp(c_full(b), ph, abort_flag, p.status);
               if (!run) break;
               tc_fence_after();
               const uint32_t a = tm + kACol + b * 64;
@@ -369,7 +393,7 @@ gmm_i4_kernel(const __grid_constant__ CUtensorMap mapW0, const __grid_constant__
             }
             if (!run) break;
             umma_commit_pair_warp(q_empty(s), both);
-            if (++s == kStages) s = 0;
+            if (++s == kStages) s = 0, sph ^= 1u;
           }
           if (!run) break;
           if (subs > 1) umma_commit_pair_warp(t_full(it & 1), both);

@@ -287,7 +287,9 @@ __device__ __forceinline__ uint32_t mapa_shared(uint32_t addr, uint32_t rank) {
 // use it to hand an accumulator back to the leader's MMA warp once their
 // tcgen05.ld have completed (tcgen05.wait::ld, then
 // tcgen05.fence::before_thread_sync): no generic-proxy memory operation has
-// to be ordered before it.  A release at cluster scope there measured as a
+// to be ordered before it.  (Shared memory of the peer that the leader's MMAs read:
+// TMA loads into it signal the leader's barrier themselves, see tma_load_2d_pair.)
+// A release at cluster scope there measured as a
 // memory-barrier stall per tile in every epilogue warp (the paired gate/up
 // wgrad took 267 instead of 193 us).
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {

@@ -16,20 +16,25 @@ namespace tc {
 // already complete.
 constexpr uint32_t kSuspendNs = 20000;
 
-__device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity,
-                                               volatile int* abort_flag, int32_t* status,
-                                               bool honor_abort = true) {
+__device__ __forceinline__ bool mbar_try_wait_warp(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity), "r"(kSuspendNs)
+      : "memory");
+  return ok != 0;
+}
+
+// attempt(): whether this lane's barriers have completed their phases.
+template <typename F>
+__device__ __forceinline__ bool attempt_warp(F&& attempt, volatile int* abort_flag, int32_t* status,
+                                             bool honor_abort) {
   unsigned long long t0 = 0;
   for (uint32_t i = 0;; ++i) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity), "r"(kSuspendNs)
-        : "memory");
-    if (__all_sync(0xffffffffu, ok != 0)) return true;
+    if (__all_sync(0xffffffffu, attempt())) return true;
     if ((i & 15u) == 15u) {
       if (__any_sync(0xffffffffu, honor_abort && *abort_flag)) return false;
       const unsigned long long now = globaltimer();
@@ -41,6 +46,23 @@ __device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity,
       }
     }
   }
+}
+
+__device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity,
+                                               volatile int* abort_flag, int32_t* status,
+                                               bool honor_abort = true) {
+  return attempt_warp([&]() { return mbar_try_wait_warp(bar, parity); }, abort_flag, status, honor_abort);
+}
+
+// Two barriers in one attempt, their latencies and the vote shared.
+__device__ __forceinline__ bool mbar_wait2_warp(uint32_t bar, uint32_t parity, uint32_t bar2, uint32_t parity2,
+                                                volatile int* abort_flag, int32_t* status) {
+  return attempt_warp(
+      [&]() {
+        const bool first = mbar_try_wait_warp(bar, parity), second = mbar_try_wait_warp(bar2, parity2);
+        return first && second;
+      },
+      abort_flag, status, true);
 }
 
 // One arrival of the warp, after all its lanes' work so far.
@@ -56,6 +78,15 @@ __device__ __forceinline__ void mbar_arrive_cluster_warp(uint32_t cluster_addr) 
   asm volatile(
       "{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\t"
       "@q mbarrier.arrive.shared::cluster.b64 _, [%0];\n\t}" ::"r"(cluster_addr)
+      : "memory");
+}
+// The same with release at cluster scope: for what another CTA of the cluster reads
+// once it has waited at that scope.
+__device__ __forceinline__ void mbar_arrive_release_cluster_warp(uint32_t cluster_addr) {
+  __syncwarp();
+  asm volatile(
+      "{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\t"
+      "@q mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];\n\t}" ::"r"(cluster_addr)
       : "memory");
 }
 
@@ -183,6 +214,26 @@ __device__ __forceinline__ void tma_load_3d_warp(uint32_t dst, const CUtensorMap
       "@q cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
       " [%0], [%1, {%3, %4, %5}], [%2];\n\t}" ::"r"(dst),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z)
+      : "memory");
+}
+
+// For copies whose byte count goes to the barrier of either CTA of a pair (`bar`: a
+// shared::cluster address): that CTA's arrival, and the loads into this CTA's own
+// shared memory.
+__device__ __forceinline__ void mbar_arrive_expect_tx_cluster_warp(uint32_t bar, uint32_t bytes) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\t"
+      "@q mbarrier.arrive.expect_tx.shared::cluster.b64 _, [%0], %1;\n\t}" ::"r"(bar), "r"(bytes)
+      : "memory");
+}
+
+__device__ __forceinline__ void tma_load_2d_pair_warp(uint32_t dst, const CUtensorMap* map, uint32_t bar,
+                                                      int x, int y) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\t"
+      "@q cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4}], [%2];\n\t}" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y)
       : "memory");
 }
 

@@ -20,8 +20,11 @@
 // K = 8 two rows in a thousand need it.  The whole row takes a warp 7 us of the slow
 // 64-bit pipe, which at first was half of the launch, its tail (16384 rows 38 us,
 // now 21; softmax, whose sum takes the row's exponentials in 64 bits, 38 and 26).
-// Rows of one logit and one bias, as padding gives them, are in the order of the
-// index and need neither (16384 of them 413 us by the whole row, now 22).
+// Rows of one logit, as padding gives them, need neither: with one bias (or none) they
+// are in the order of the index (16384 of them 23 us, by the whole row 413), and where
+// balancing has moved the biases, in multiples of its step, so that many scores tie,
+// in the order of the biases (select_by_bias: 55 us; before, one step of 1e-3 from
+// zeros took 424, a hundred steps 45 with sigmoid scores and 187 with softmax).
 // Where no score is needed (no bias, and no sum of two) the logits themselves are
 // compared and their keys hold the whole index, as in the plain router.
 #include <type_traits>
@@ -37,6 +40,7 @@ struct GroupParams {
   int lg;                               // log2 of the lanes of a group
   int scoring, renormalize;
   float scale;
+  double even;                          // 1 / E: the softmax score in a row of one logit
 };
 
 // Element i of a lane inside its group.
@@ -82,6 +86,9 @@ __device__ __forceinline__ unsigned long long key64(double v) {
   const long long b = __double_as_longlong(v + 0.0);
   return (unsigned long long)(b < 0 ? ~b : b ^ (long long)0x8000000000000000ull);
 }
+__device__ __forceinline__ double value64(unsigned long long k) {
+  return __longlong_as_double((long long)(k >> 63 ? k ^ 0x8000000000000000ull : ~k));
+}
 
 // How a row's scores come from its logits: in fp32, and in 64 bits.
 struct Scores {
@@ -109,14 +116,19 @@ __device__ __forceinline__ double exact_sum(const T* row, const GroupParams& p, 
   return s;
 }
 
-// Whether all of the row's experts have one logit and one bias (padding rows of
-// zeros): their order is that of the index.
+// Whether all of the row's experts have one logit (padding rows of zeros), which
+// leaves the order to the biases; and one bias, which leaves it to the index.
+enum Row { kNotKnown, kDiffers, kOneLogit, kAllTheSame };
 template <typename T>
-__device__ __noinline__ bool all_the_same(const T* row, const GroupParams& p, int lane) {
+__device__ __noinline__ Row row_of(const T* row, const GroupParams& p, int lane) {
   const float l = to_f32(row[0]), b = p.bias ? p.bias[0] : 0.f;
-  bool same = l > -INFINITY && b > -INFINITY && b < INFINITY;
-  for (int j = lane; same && j < p.E; j += 32) same = to_f32(row[j]) == l && (!p.bias || p.bias[j] == b);
-  return __all_sync(kAll, same);
+  bool one = l > -INFINITY, same = b > -INFINITY && b < INFINITY;
+  for (int j = lane; one && j < p.E; j += 32) {
+    one = to_f32(row[j]) == l;
+    same = same && (!p.bias || p.bias[j] == b);
+  }
+  if (!__all_sync(kAll, one)) return kDiffers;
+  return __all_sync(kAll, same) ? kAllTheSame : kOneLogit;
 }
 
 // Whether the group of this lane is kept, by the exact sums of its
@@ -215,87 +227,169 @@ __device__ __noinline__ int exact_among(const T* row, const GroupParams& p, cons
   return lane < p.K ? list[lane] : 0;
 }
 
-// The selection in 64 bits; lane k < K gets the k-th id.  by_logit: c is the
-// logit.  Groups with fewer experts above -inf (of `each`) come last; when the
-// kept groups have fewer than K of those, their others follow in order.
-template <int NPL, typename T>
-__device__ __noinline__ int select_exact(const T* row, const GroupParams& p, bool by_logit, int lane) {
+// The score of every expert in a row of one logit.  (The 64-bit pipe is slow, and
+// padding's logits are zeros.)
+__device__ __forceinline__ double score_of_all(float l, const GroupParams& p) {
+  return p.scoring == MOE_SCORE_SOFTMAX ? p.even : l == 0.f ? 0.5 : sigmoid_exact(l);
+}
+
+// The selection in a row of one logit with the score s; lane k < K gets the k-th
+// id.  s + b is in the order of b, and no two biases share a sum, where all are
+// multiples of 2^-50 (all from 2^-27 up are): two of them are 2^-50 apart then, at
+// least, and a sum under 2 rounds by 2^-53 (larger biases are further apart).  fail:
+// one is not, or the kept groups have fewer than K experts left.
+template <int NPL>
+__device__ __noinline__ int select_by_bias(const GroupParams& p, double s, int lane, bool& fail) {
   const int g = lane >> p.lg, r = lane & ((1 << p.lg) - 1);
-  double c[NPL];
-  bool flag = false;
-  float m = -INFINITY;
+  uint32_t key[NPL], a1 = 0u, a2 = 0u;  // 0: out
+  bool small = false, flag = false;
 #pragma unroll
   for (int i = 0; i < NPL; ++i) {
-    const int o = place<T, false>(i, r, p.lg);
-    const float l = g < p.G && o < p.size ? clean_logit(to_f32(row[g * p.size + o]), flag) : -INFINITY;
-    c[i] = l;
-    m = fmaxf(m, l);
+    const int o = place<float, false>(i, r, p.lg);
+    const float b = g < p.G && o < p.size ? clean_bias(p.bias[g * p.size + o], flag) + 0.f : -INFINITY;
+    small |= fabsf(b) < 0x1p-27f && b * 0x1p50f != rintf(b * 0x1p50f);
+    key[i] = b > -INFINITY ? key_of(b) : 0u;
+    a2 = max(a2, min(a1, key[i]));
+    a1 = max(a1, key[i]);
   }
-  if (!by_logit) {
-    double inv = 0.0;
-    if (p.scoring == MOE_SCORE_SOFTMAX) {
-      m = fmaxf(value_of(__reduce_max_sync(kAll, key_of(m))), -3.402823466e+38f);
-      double s = 0.0;
-#pragma unroll
-      for (int i = 0; i < NPL; ++i) s += c[i] = exp(c[i] - m);
-#pragma unroll
-      for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(kAll, s, d);
-      inv = s;
+  bool keep = g < p.G;
+  if (p.top < p.G) {
+    for (int d = 1; d < 1 << p.lg; d <<= 1) {
+      const uint32_t b1 = __shfl_xor_sync(kAll, a1, d), b2 = __shfl_xor_sync(kAll, a2, d);
+      a2 = max(min(a1, b1), max(a2, b2));
+      a1 = max(a1, b1);
     }
+    const int live = (a1 != 0u) + (p.each > 1 && a2 != 0u);
+    unsigned long long v = a1;
+    if (p.each > 1) {
+      const unsigned long long sum = key64((s + value_of(a1)) + (s + value_of(a2)));
+      if (live > 1) v = sum;
+    }
+    int rank = 0;
+    for (int h = 0; h < p.G; ++h) {
+      const unsigned long long vh = __shfl_sync(kAll, v, h << p.lg);
+      const int lh = __shfl_sync(kAll, live, h << p.lg);
+      rank += lh > live || (lh == live && (vh > v || (vh == v && h < g)));
+    }
+    keep = keep && rank < p.top;
+  }
+  int left = 0;
+#pragma unroll
+  for (int i = 0; i < NPL; ++i) {
+    if (!keep) key[i] = 0u;
+    left += key[i] != 0u;
+  }
+  fail = __any_sync(kAll, small) || (int)__reduce_add_sync(kAll, (unsigned)left) < p.K;
+  if (fail) return 0;
+  int sel_id = 0;
+  for (int k = 0; k < p.K; ++k) {
+    uint32_t top = 0u;
+#pragma unroll
+    for (int i = 0; i < NPL; ++i) top = max(top, key[i]);
+    const uint32_t best = __reduce_max_sync(kAll, top);
+    uint32_t at = 0xffffffffu;
+#pragma unroll
+    for (int i = NPL - 1; i >= 0; --i)
+      if (key[i] == best) at = g * p.size + place<float, false>(i, r, p.lg);
+    const uint32_t id = __reduce_min_sync(kAll, at);
+#pragma unroll
+    for (int i = 0; i < NPL; ++i)
+      if (at == id && id == (uint32_t)(g * p.size + place<float, false>(i, r, p.lg))) key[i] = 0u;
+    if (lane == k) sel_id = (int)id;
+  }
+  return sel_id;
+}
+
+// The selection in 64 bits; lane k < K gets the k-th id.  by_logit: c is the
+// logit; one_logit: all of them are the same, one score to compute.  Groups with
+// fewer experts above -inf (of `each`) come last; when the kept groups have fewer
+// than K of those, their others follow in order.
+template <int NPL, typename T>
+__device__ __noinline__ int select_exact(const T* row, const GroupParams& p, bool by_logit, bool one_logit, int lane) {
+  const int g = lane >> p.lg, r = lane & ((1 << p.lg) - 1);
+  const bool soft = p.scoring == MOE_SCORE_SOFTMAX;
+  double c[NPL];
+  bool flag = false;
+  if (one_logit && !by_logit) {
+    const double s = score_of_all(clean_logit(to_f32(row[0]), flag), p);
 #pragma unroll
     for (int i = 0; i < NPL; ++i) {
       const int o = place<T, false>(i, r, p.lg);
-      const bool in = g < p.G && o < p.size;
-      const float l = in ? clean_logit(to_f32(row[g * p.size + o]), flag) : -INFINITY;
-      const float b = in && p.bias ? clean_bias(p.bias[g * p.size + o], flag) : 0.f;
-      const double s = p.scoring == MOE_SCORE_SOFTMAX ? c[i] / inv : sigmoid_exact(c[i]);
-      c[i] = l > -INFINITY ? s + b : -INFINITY;
+      c[i] = g < p.G && o < p.size ? s + (p.bias ? clean_bias(p.bias[g * p.size + o], flag) : 0.f) : -INFINITY;
+    }
+  } else {
+    float m = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < NPL; ++i) {
+      const int o = place<T, false>(i, r, p.lg);
+      const float l = g < p.G && o < p.size ? clean_logit(to_f32(row[g * p.size + o]), flag) : -INFINITY;
+      c[i] = l;
+      m = fmaxf(m, l);
+    }
+    if (!by_logit) {
+      double sum = 0.0;
+      if (soft) {
+        m = fmaxf(value_of(__reduce_max_sync(kAll, key_of(m))), -3.402823466e+38f);
+#pragma unroll
+        for (int i = 0; i < NPL; ++i) sum += c[i] = exp(c[i] - m);
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(kAll, sum, d);
+      }
+#pragma unroll
+      for (int i = 0; i < NPL; ++i) {
+        const int o = place<T, false>(i, r, p.lg);
+        const bool in = g < p.G && o < p.size;
+        const float l = in ? clean_logit(to_f32(row[g * p.size + o]), flag) : -INFINITY;
+        const float b = in && p.bias ? clean_bias(p.bias[g * p.size + o], flag) : 0.f;
+        const double s = soft ? c[i] / sum : sigmoid_exact(c[i]);
+        c[i] = l > -INFINITY ? s + b : -INFINITY;
+      }
     }
   }
-  // the two largest of the group
-  double a1 = -INFINITY, a2 = -INFINITY;
+  // keys, 0 for -inf, and the two largest of the group
+  unsigned long long key[NPL], a1 = 0, a2 = 0;
   unsigned long long open = 0;  // elements that may be chosen yet
 #pragma unroll
   for (int i = 0; i < NPL; ++i) {
     if (g < p.G && place<T, false>(i, r, p.lg) < p.size) open |= 1ull << i;
-    a2 = fmax(a2, fmin(a1, c[i]));
-    a1 = fmax(a1, c[i]);
+    key[i] = __double_as_longlong(c[i]) == (long long)0xfff0000000000000ull ? 0ull : key64(c[i]);
+    a2 = max(a2, min(a1, key[i]));
+    a1 = max(a1, key[i]);
   }
   for (int d = 1; d < 1 << p.lg; d <<= 1) {
-    const double b1 = __shfl_xor_sync(kAll, a1, d), b2 = __shfl_xor_sync(kAll, a2, d);
-    a2 = fmax(fmin(a1, b1), fmax(a2, b2));
-    a1 = fmax(a1, b1);
+    const unsigned long long b1 = __shfl_xor_sync(kAll, a1, d), b2 = __shfl_xor_sync(kAll, a2, d);
+    a2 = max(min(a1, b1), max(a2, b2));
+    a1 = max(a1, b1);
   }
-  const int live = (a1 > -INFINITY) + (p.each > 1 && a2 > -INFINITY);
-  const double v = live > 1 ? a1 + a2 : a1;
+  const int live = (a1 != 0) + (p.each > 1 && a2 != 0);
+  const unsigned long long v = live > 1 ? key64(value64(a1) + value64(a2)) : a1;
   int rank = 0;
   for (int h = 0; h < p.G; ++h) {
-    const double vh = __shfl_sync(kAll, v, h << p.lg);
+    const unsigned long long vh = __shfl_sync(kAll, v, h << p.lg);
     const int lh = __shfl_sync(kAll, live, h << p.lg);
     rank += lh > live || (lh == live && (vh > v || (vh == v && h < g)));
   }
   if (rank >= p.top) open = 0;
   int sel_id = 0;
   for (int k = 0; k < p.K; ++k) {
-    double best = -INFINITY;
-    int at = 0x7fffffff;
+    unsigned long long best = 0;
+    uint32_t at = 0x7fffffffu;
 #pragma unroll
     for (int i = 0; i < NPL; ++i) {  // (in ascending order of the index)
-      if (((open >> i) & 1) && (at == 0x7fffffff || c[i] > best)) {
-        best = c[i];
+      if (((open >> i) & 1) && (at == 0x7fffffffu || key[i] > best)) {
+        best = key[i];
         at = g * p.size + place<T, false>(i, r, p.lg);
       }
     }
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) {
-      const double ob = __shfl_xor_sync(kAll, best, d);
-      const int oa = __shfl_xor_sync(kAll, at, d);
-      if (oa != 0x7fffffff && (at == 0x7fffffff || ob > best || (ob == best && oa < at))) best = ob, at = oa;
-    }
+    // the largest of the upper halves, of the lower ones among those, the lowest index
+    const uint32_t upper = __reduce_max_sync(kAll, (uint32_t)(best >> 32));
+    const bool first = (uint32_t)(best >> 32) == upper;
+    const uint32_t lower = __reduce_max_sync(kAll, first ? (uint32_t)best : 0u);
+    const uint32_t id = __reduce_min_sync(kAll, first && (uint32_t)best == lower ? at : 0x7fffffffu);
 #pragma unroll
     for (int i = 0; i < NPL; ++i)
-      if (g * p.size + place<T, false>(i, r, p.lg) == at) open &= ~(1ull << i);
-    if (lane == k) sel_id = at;
+      if (at == id && (uint32_t)(g * p.size + place<T, false>(i, r, p.lg)) == id) open &= ~(1ull << i);
+    if (lane == k) sel_id = (int)id;
   }
   return sel_id;
 }
@@ -387,6 +481,7 @@ router_grouped_kernel(const T* __restrict__ logits, const __grid_constant__ Grou
   }
   if (flag) set_status(status, MOE_ERR_INVALID_ARG);
   bool again = false, keep = g < p.G;  // again: by the whole row
+  Row kind = kNotKnown;
   __shared__ int lists[kWarps][32];
   int* list = lists[threadIdx.x >> 5];
   if (p.top < p.G) {
@@ -421,7 +516,8 @@ router_grouped_kernel(const T* __restrict__ logits, const __grid_constant__ Grou
       const float hi = value_of(__reduce_max_sync(kAll, !keep && v > -INFINITY && g < p.G ? key_of(v + err) : 0u));
       // (dropped groups without experts are no question, nor are kept ones)
       if (hi > -INFINITY && lo > -INFINITY && lo <= hi) {
-        bool fail = all_the_same(row, p, lane) || __any_sync(kAll, again) || p.G * p.each > 32;
+        kind = row_of(row, p, lane);
+        bool fail = kind != kDiffers || __any_sync(kAll, again) || p.G * p.each > 32;
         if (!fail) keep = exact_groups<NPL>(row, p, f, lane, list, fail);
         again |= fail;
       }
@@ -473,16 +569,19 @@ router_grouped_kernel(const T* __restrict__ logits, const __grid_constant__ Grou
   }
   if (__any_sync(kAll, again || close)) {
     bool whole = __any_sync(kAll, again);
-    if (all_the_same(row, p, lane)) {
+    if (kind == kNotKnown) kind = row_of(row, p, lane);
+    if (kind == kAllTheSame) {
       sel_id = lane;
       whole = false;
+    } else if (kind == kOneLogit) {
+      sel_id = select_by_bias<NPL>(p, score_of_all(clean_logit(to_f32(row[0]), flag), p), lane, whole);
     } else if (!whole) {
       // none of the K is below this, and none of the exact K below it less the margin
       const float low = value_of(__shfl_sync(kAll, mine, p.K - 1) & ~kLow);
       const float cut = kByLogit ? low : low - margin_of(low, low, f.eps);
       sel_id = exact_among<NPL>(row, p, f, kByLogit, keep, cut, lane, list, whole);
     }
-    if (whole) sel_id = select_exact<NPL>(row, p, kByLogit, lane);
+    if (whole) sel_id = select_exact<NPL>(row, p, kByLogit, kind == kOneLogit, lane);
     sel = lane < p.K ? to_f32(row[sel_id]) : -INFINITY;
     sel = fminf(fmaxf(sel, -INFINITY), 3.402823466e+38f) + 0.f;
   }
@@ -521,7 +620,8 @@ extern "C" int moe_router_topk_grouped(const void* logits, int dtype, const floa
   if (E % num_groups || group_top > E / num_groups) return MOE_ERR_SHAPE;
   if (K > top_groups * (E / num_groups)) return MOE_ERR_SHAPE;
   if ((long long)T * K > 0x7fffffffLL) return MOE_ERR_SHAPE;
-  GroupParams p{bias, T, E, K, num_groups, E / num_groups, top_groups, group_top, 5, scoring, renormalize, scale};
+  GroupParams p{bias, T, E, K, num_groups, E / num_groups, top_groups, group_top, 5, scoring, renormalize, scale,
+                1.0 / E};
   for (int n = 1; n < num_groups; n *= 2) --p.lg;
   const int each = ((p.size - 1) >> p.lg) + 1;  // scores of a lane
   if (each > 32) return MOE_ERR_SHAPE;

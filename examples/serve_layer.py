@@ -13,7 +13,8 @@ in 4 bits with a scale for each group of inputs) and runs
             the int8, the 4-bit or the bf16 weights
   training  router -> bf16 layer forward and backward -> gradient of the
             router's logits; with groups also a step of the experts' biases
-The command prints each path's time and how far the serving paths are from bf16.
+The command prints each path's time and how far the serving paths are from bf16;
+with groups it balances the experts for some steps first.
 """
 
 import argparse
@@ -124,6 +125,14 @@ class Layer:
                                                **self.how)
         return grad_x, grad_logits, (dWg, dWu, dWd)
 
+    def train(self, x, grad_of):
+        """A step: forward, backward from grad_of(out), and the biases'."""
+        out, saved = self.forward(x)
+        grads = self.backward(grad_of(out), saved)
+        if self.groups is not None:
+            self.balance(saved[3].tokens_per_expert)
+        return out, grads
+
 
 def _time(f, n=20):
     for _ in range(3):
@@ -155,7 +164,10 @@ def main(argv=None):
                   int4_group=64 if a.int4 else None,
                   groups=(a.groups, a.top_groups, min(2, size)) if a.groups > 1 else None)
     x = torch.randn(a.tokens, a.hidden, device="cuda", dtype=torch.bfloat16)
-    want, saved = layer.forward(x)
+    if layer.groups is not None:
+        for _ in range(10):
+            layer.balance(layer.forward(x)[1][3].tokens_per_expert)
+    want, _ = layer.forward(x)
 
     def off(y, ref):
         return float((y.float() - ref.float()).norm() / ref.float().norm())
@@ -169,7 +181,8 @@ def main(argv=None):
             print(f"decode   {t:5d} tokens  {_time(lambda: layer.decode(x[:t], **how)):8.1f} us  "
                   f"off the bf16 layer by {off(y, want[:t]):.4f}")
     print(f"training {a.tokens:5d} tokens  "
-          f"{_time(lambda: layer.backward(want, layer.forward(x)[1]), 5):8.1f} us forward and backward")
+          f"{_time(lambda: layer.train(x, lambda out: want), 5):8.1f} us forward and backward"
+          f"{', with the biases' if layer.groups is not None else ''}")
     status = lib.moe_check_status(layer.status)
     if status != lib.MOE_OK:
         raise SystemExit(lib.status_name(status))

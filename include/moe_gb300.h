@@ -562,7 +562,7 @@ int moe_down_proj_int8(const int8_t* act_q, const float* row_scale, const int32_
  * expert_offsets NULL with E = 1: one matrix for all N rows):
  *   y[i, n] = sum_k x[i, k] * bf16(q[e, n, k] * scale[e, k / group, n])
  * (exact for scales of at most five significant bits; others are multiplied by
- * weights rounded to bf16, 2^-9 of themselves at most).
+ * weights rounded to bf16, 2^-8 of themselves at most).
  * moe_gate_up_swiglu_int4: act [N, I] bf16 = silu(g) * u with g, u such
  *   products of permuted [N, H] bf16, W_gate_q and W_up_q [E, I, H / 2],
  *   gate_scale and up_scale [E, H / group, I].
